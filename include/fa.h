@@ -278,6 +278,153 @@ fa_status fa_decode_noalloc(const void* q, const void* k_cache, const void* v_ca
                             float* lse, const int32_t* seqlens_k, int B, int Hq, int Hkv,
                             int Sk_max, int d, float scale, cudaStream_t stream);
 
+/*
+ * Paged 8-bit KV cache
+ * ====================
+ * Serving from a cache of pages: fa_kv_assign hands out pages and slots,
+ * fa_kv_write_fp8 quantises new keys and values into them, fa_select_blocks
+ * picks the blocks a query attends, fa_decode_paged_fp8 is the attention of
+ * the last Sq tokens, and fa_kv_read_fp8 gives cached keys and values back as
+ * packed bf16 for fa_fwd_varlen (a prompt chunk over a cached prefix).
+ *
+ *  * k_cache, v_cache: e4m3 bytes (OCP FP8 E4M3) [num_pages, Hkv, page_size, d],
+ *    16-byte aligned; page_size is 16, 32, 64 or 128, d is 64 or 128.
+ *  * k_scale, v_scale: fp32 [num_pages, Hkv], one per (page, KV head); a cached
+ *    value is code * scale.  Scales are finite and > 0.
+ *  * k_bounds: int8 [num_pages, Hkv, 2, d], 16-byte aligned: per channel the
+ *    largest (row 0) and the smallest (row 1) key code of the page in units of 4
+ *    codes, rounded outwards (up and down).  Only fa_select_blocks reads it.
+ *  * block_table: int32 [B, max_blocks]; entry (b, i) is the page of positions
+ *    [i * page_size, (i + 1) * page_size) of request b.  Entries outside
+ *    [0, num_pages) mark absent pages: their keys are treated as hidden.
+ *    Requests may share pages that nothing writes to.
+ *  * Page and slot offsets are computed in 64 bits; a cache may be larger than
+ *    2^32 bytes.
+ */
+
+/*
+ * Block tables and slot maps from request lengths, in one launch.  Request b
+ * holds seqlens[b] tokens and gets newlens[b] more (negative values count as 0).
+ * With have = ceil(seqlens / page_size) and full = ceil((seqlens + newlens) /
+ * page_size) it takes the next full - have pages of free_pages[0, n_free), in
+ * request order, for its table entries [have, full).
+ *   block_table [B,max_blocks]  entries [have, full) written, the rest kept
+ *   slot_map int64 [total_new]  slot of every packed new token, page * page_size +
+ *                               offset; -1 for a token without one and for the
+ *                               packed rows behind the last request
+ *   cu_new int32 [B+1]          offsets of the requests' packed new tokens
+ *   seqlens_out int32 [B]       lengths after the call
+ *   cu_seqlens_k int32 [B+1]    their prefix sums (fa_fwd_varlen's cu_seqlens_k)
+ *   n_used int32 [1]            pages taken off the front of free_pages
+ * A request is refused, whole, when it would need more than max_blocks blocks,
+ * when its packed tokens end behind total_new, or when its pages end behind
+ * n_free: it takes no page, its slots are -1 and its seqlens_out is seqlens.  The
+ * pages a request without room in the free list asked for count as taken for
+ * the requests after it.  Offsets saturate at 2^31 - 1.
+ * Outputs must not overlap seqlens, newlens or free_pages.  slot_map needs
+ * 8-byte alignment, the others 4-byte; free_pages may be NULL when n_free is 0
+ * and slot_map when total_new is 0.
+ */
+fa_status fa_kv_assign(const int32_t* seqlens, const int32_t* newlens, int B, int page_size,
+                       int32_t* block_table, int max_blocks, const int32_t* free_pages, int n_free,
+                       int64_t* slot_map, int total_new, int32_t* cu_new, int32_t* seqlens_out,
+                       int32_t* cu_seqlens_k, int32_t* n_used, cudaStream_t stream);
+
+/*
+ * Quantising write of n_tokens new keys and values.  k, v: bf16, element (head,
+ * token, channel) at head * stride_h + token * stride_t + channel (strides in
+ * elements, >= 0, multiples of 8; base pointers 16-byte aligned), so packed
+ * [Hkv, n, d] and token-major [n, Hkv, d] inputs are both read in place.
+ * slot_map int64 [n_tokens] as fa_kv_assign writes it; tokens with a slot
+ * outside [0, num_pages * page_size) are skipped.
+ * Consecutive tokens in consecutive slots of one page form a run; the run's
+ * first offset n is the number of tokens the page holds before it.  Per head,
+ * separately for K and V:
+ *   s_tok = 2^e, e the smallest with amax <= 448 * 2^e over the run's finite
+ *           values, e in [-100, 119]
+ *   s     = max(s_old, s_tok) if n > 0 (s_old: the page's scale), else s_tok
+ *   new codes  = x / s (in fp32) rounded to the nearest e4m3 value (ties to even),
+ *                at most +-448; an infinity becomes +-448, a NaN the NaN code
+ *   held codes [0, n) = code * s_old / s, rounded again, if s > s_old
+ *   k_bounds (NULL: not kept) = the run's bounds, merged for n > 0 with the old
+ *                ones times s_old / s, rounded outwards; NaN codes count as 0
+ * A scale only grows within a page until its offset 0 is written again.  With
+ * power-of-two scales a held code changes only where it becomes subnormal.
+ * Codes behind the run are left as they were.  A page must not appear in two
+ * runs of one call (its content is unspecified then); fa_kv_assign never
+ * makes such a slot map.
+ */
+fa_status fa_kv_write_fp8(const void* k, const void* v, long long k_stride_h, long long k_stride_t,
+                          long long v_stride_h, long long v_stride_t, const int64_t* slot_map,
+                          int n_tokens, void* k_cache, void* v_cache, float* k_scale,
+                          float* v_scale, int8_t* k_bounds, int num_pages, int Hkv, int page_size,
+                          int d, cudaStream_t stream);
+
+/*
+ * Dequantising read: packed bf16 k, v [Hkv, total_k, d], where sequence s owns rows
+ * [cu_seqlens_k[s], cu_seqlens_k[s+1]) (device int32[nseq+1], non-decreasing) and
+ * row cu_seqlens_k[s] + i is its position i: code * scale rounded to bf16 (exact
+ * for power-of-two scales within bf16's range).  Positions without a page give
+ * zeros; rows of no sequence are left as they were.
+ */
+fa_status fa_kv_read_fp8(const void* k_cache, const void* v_cache, const float* k_scale,
+                         const float* v_scale, const int32_t* block_table,
+                         const int32_t* cu_seqlens_k, void* k, void* v, int nseq, int max_blocks,
+                         int num_pages, int total_k, int Hkv, int page_size, int d,
+                         cudaStream_t stream);
+
+/* Bytes of device workspace fa_select_blocks needs: a 32-bit key per block. */
+size_t fa_select_blocks_workspace_size(int B, int Hkv, int max_blocks);
+
+/*
+ * Block selection: for each request and KV head the k_blocks blocks with the
+ * largest score, an upper bound of the block's scores for 8-bit queries:
+ *   q8_i = rint(q_i / 2^e), |q8_i| <= 127, e the smallest with amax |q| <= 127 * 2^e,
+ *          e in [-100, 119], for each query row
+ *   score = max over the Hq / Hkv * Sq query rows of the KV head of
+ *           k_scale * 2^(e+2) * sum_i max(q8_i * bounds_i,0 , q8_i * bounds_i,1)
+ * The sum is an exact integer and is multiplied by k_scale, then by 2^(e+2), in
+ * fp32.  The first n_first and last n_last blocks of a request are always taken
+ * (n_first + n_last <= k_blocks).  Equal scores: the lower block.  Blocks without
+ * a page and NaN scores rank last.
+ *   q bf16 [B,Hq,Sq,d]; seqlens_k int32 [B] (clamped to [0, max_blocks*page_size])
+ *   sel int32 [B,Hkv,k_blocks]: block indices, ascending, then -1
+ *   n_sel int32 [B,Hkv]: min(k_blocks, ceil(seqlens_k / page_size))
+ */
+fa_status fa_select_blocks(const void* q, const int8_t* k_bounds, const float* k_scale,
+                           const int32_t* block_table, const int32_t* seqlens_k, int32_t* sel,
+                           int32_t* n_sel, int B, int Hq, int Hkv, int Sq, int num_pages,
+                           int max_blocks, int page_size, int d, int k_blocks, int n_first,
+                           int n_last, void* workspace, size_t workspace_bytes,
+                           cudaStream_t stream);
+
+/* Bytes of device workspace fa_decode_paged_fp8 needs (independent of the
+   lengths and of the cache's size). */
+size_t fa_decode_paged_fp8_workspace_size(int B, int Hq, int Hkv, int Sq, int d);
+
+/*
+ * Attention of the last Sq tokens of each request over the paged cache:
+ * q, o bf16 [B,Hq,Sq,d], lse fp32 [B,Hq,Sq] (NULL when not needed).  Request b has
+ * seqlens_k[b] keys (device int32[B], clamped to [0, max_blocks * page_size]; they
+ * include the Sq tokens), and key j is visible to row i iff
+ *   j <= i + seqlens_k[b] - Sq   (bottom-right causal; Sq = 1: every key)
+ * and, when sel and n_sel are given (both or neither), j's block is one of
+ * sel[b,hk,0 .. n_sel[b,hk]) of its KV head (int32 [B,Hkv,max_sel]; n_sel is
+ * clamped to [0, max_sel]; entries outside the request's blocks are ignored, a
+ * block listed twice counts twice).  Rows that see no key give O = 0, LSE = -inf.
+ * What the pages hold behind a request's last key is never used.  A key that
+ * holds NaN makes the rows that see it NaN, and no others.
+ * Any Sq is accepted; for prompts, fa_kv_read_fp8 with fa_fwd_varlen is the
+ * faster path (the rows of a KV head are served 32 at a time here).
+ */
+fa_status fa_decode_paged_fp8(const void* q, const void* k_cache, const void* v_cache,
+                              const float* k_scale, const float* v_scale,
+                              const int32_t* block_table, const int32_t* seqlens_k,
+                              const int32_t* sel, const int32_t* n_sel, void* o, float* lse, int B,
+                              int Hq, int Hkv, int Sq, int num_pages, int max_blocks, int max_sel,
+                              int page_size, int d, float scale, void* workspace,
+                              size_t workspace_bytes, cudaStream_t stream);
+
 /* Reads the device status words of the current device (this synchronises the
    device).  Returns FA_OK or FA_ERR_TIMEOUT; *code_out (may be NULL) receives
    the raw word (low 16 bits: error code, high 16 bits: wait site).  When

@@ -27,7 +27,9 @@ FA_ERR_TIMEOUT = 5
 EXPORTED = ("fa_fwd", "fa_bwd", "fa_bwd_workspace_size", "fa_decode", "fa_decode_workspace_size",
             "fa_decode_noalloc", "fa_fwd_masked", "fa_bwd_masked", "fa_fwd_varlen",
             "fa_bwd_varlen", "fa_fwd_dropout", "fa_bwd_dropout", "fa_key_mask_words",
-            "fa_pack_key_mask", "fa_fwd_fp8", "fa_device_status", "fa_selftest_wait_timeout",
+            "fa_pack_key_mask", "fa_fwd_fp8", "fa_kv_assign", "fa_kv_write_fp8", "fa_kv_read_fp8",
+            "fa_select_blocks", "fa_select_blocks_workspace_size", "fa_decode_paged_fp8",
+            "fa_decode_paged_fp8_workspace_size", "fa_device_status", "fa_selftest_wait_timeout",
             "fa_profile_next_launch", "fa_status_string", "fa_last_error_detail", "fa_version")
 
 _lib = None
@@ -84,6 +86,20 @@ def load_library(path: str = LIB_PATH):
     lib.fa_selftest_wait_timeout.restype = I
     lib.fa_profile_next_launch.argtypes = [P, P]
     lib.fa_profile_next_launch.restype = I
+    L = ctypes.c_longlong
+    lib.fa_kv_assign.argtypes = [P, P, I, I, P, I, P, I, P, I, P, P, P, P, P]
+    lib.fa_kv_write_fp8.argtypes = [P, P, L, L, L, L, P, I, P, P, P, P, P, I, I, I, I, P]
+    lib.fa_kv_read_fp8.argtypes = [P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, P]
+    lib.fa_select_blocks.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I, I, I, P, Z, P]
+    lib.fa_decode_paged_fp8.argtypes = [P, P, P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, I, I,
+                                        F, P, Z, P]
+    for f in (lib.fa_kv_assign, lib.fa_kv_write_fp8, lib.fa_kv_read_fp8, lib.fa_select_blocks,
+              lib.fa_decode_paged_fp8):
+        f.restype = I
+    lib.fa_select_blocks_workspace_size.argtypes = [I, I, I]
+    lib.fa_select_blocks_workspace_size.restype = Z
+    lib.fa_decode_paged_fp8_workspace_size.argtypes = [I, I, I, I, I]
+    lib.fa_decode_paged_fp8_workspace_size.restype = Z
     lib.fa_status_string.argtypes = [I]
     lib.fa_status_string.restype = ctypes.c_char_p
     lib.fa_last_error_detail.restype = ctypes.c_char_p
@@ -374,6 +390,232 @@ def fa_decode_noalloc(q, k_cache, v_cache, seqlens_k, scale: float, o=None, lse=
                                _ptr(seqlens_k), B, Hq, Hkv, Sk_max, d, float(scale),
                                _stream(stream))
     _check(st, "fa_decode_noalloc")
+    return o, lse
+
+
+# --------------------------------------------------- paged 8-bit KV cache --
+
+
+def _on_current_device(*tensors):
+    """The library launches on the current device: every tensor has to be there."""
+    dev = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.device.index != dev:
+            raise ValueError(f"tensors must be on the current device (cuda:{dev}), got {t.device}")
+
+
+def _new(shape, dtype, like, stream):
+    """An output or workspace for a call on `stream`: memory that this thread's
+    current stream allocates is kept from reuse until `stream` is done with it."""
+    t = torch.empty(shape, dtype=dtype, device=like.device)
+    if stream is not None and stream != torch.cuda.current_stream():
+        t.record_stream(stream)
+    return t
+
+
+def _out(t, name, shape, dtype, like, stream):
+    if t is None:
+        return _new(shape, dtype, like, stream)
+    _need(t, name, dtype, len(shape))
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    return t
+
+
+def _workspace(ws, nbytes, like, stream):
+    if ws is None:
+        return _new((max(nbytes, 16),), torch.uint8, like, stream)
+    if not isinstance(ws, torch.Tensor) or not ws.is_cuda or not ws.is_contiguous():
+        raise TypeError("workspace must be a contiguous CUDA tensor")
+    return ws
+
+
+def _need_cache(k_cache, v_cache, k_scale, v_scale):
+    """Shape (num_pages, Hkv, page_size, d) of a cache, checked."""
+    _need8(k_cache, "k_cache")
+    _need8(v_cache, "v_cache")
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must have the same shape")
+    for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        _need(t, n, torch.float32, 2)
+        if tuple(t.shape) != tuple(k_cache.shape[:2]):
+            raise ValueError(f"{n} must be [num_pages, Hkv] = {tuple(k_cache.shape[:2])}")
+    return k_cache.shape
+
+
+def _need_bounds(k_bounds, num_pages, Hkv, d):
+    _need(k_bounds, "k_bounds", torch.int8, 4)
+    if tuple(k_bounds.shape) != (num_pages, Hkv, 2, d):
+        raise ValueError(f"k_bounds must be [num_pages, Hkv, 2, d] = {(num_pages, Hkv, 2, d)}")
+
+
+def _need_table(block_table, seqlens, name, rows):
+    _need(block_table, "block_table", torch.int32, 2)
+    _need(seqlens, name, torch.int32, 1)
+    if block_table.shape[0] != rows:
+        raise ValueError(f"block_table must have {rows} rows, got {block_table.shape[0]}")
+
+
+def fa_kv_assign(seqlens, newlens, page_size: int, block_table, free_pages, total_new: int,
+                 slot_map=None, cu_new=None, seqlens_out=None, cu_seqlens_k=None, n_used=None,
+                 stream=None):
+    """Pages and slots for newlens[b] new tokens of every request (fa_kv_assign):
+    block_table int32 [B,max_blocks] gets the entries of the new blocks, taken
+    off the front of free_pages int32 [n_free].  Returns (slot_map int64
+    [total_new], cu_new int32 [B+1], seqlens_out int32 [B], cu_seqlens_k int32
+    [B+1], n_used int32 [1])."""
+    lib = load_library()
+    _need(newlens, "newlens", torch.int32, 1)
+    _need(free_pages, "free_pages", torch.int32, 1)
+    B = newlens.numel()
+    _need_table(block_table, seqlens, "seqlens", B)
+    if seqlens.numel() != B:
+        raise ValueError("seqlens and newlens must have the same length")
+    _on_current_device(seqlens, newlens, block_table, free_pages, slot_map, cu_new, seqlens_out,
+                       cu_seqlens_k, n_used)
+    slot_map = _out(slot_map, "slot_map", (int(total_new),), torch.int64, seqlens, stream)
+    cu_new = _out(cu_new, "cu_new", (B + 1,), torch.int32, seqlens, stream)
+    seqlens_out = _out(seqlens_out, "seqlens_out", (B,), torch.int32, seqlens, stream)
+    cu_seqlens_k = _out(cu_seqlens_k, "cu_seqlens_k", (B + 1,), torch.int32, seqlens, stream)
+    n_used = _out(n_used, "n_used", (1,), torch.int32, seqlens, stream)
+    st = lib.fa_kv_assign(_ptr(seqlens), _ptr(newlens), B, int(page_size), _ptr(block_table),
+                          block_table.shape[1], _ptr(free_pages), free_pages.numel(),
+                          _ptr(slot_map), int(total_new), _ptr(cu_new), _ptr(seqlens_out),
+                          _ptr(cu_seqlens_k), _ptr(n_used), _stream(stream))
+    _check(st, "fa_kv_assign")
+    return slot_map, cu_new, seqlens_out, cu_seqlens_k, n_used
+
+
+def fa_kv_write_fp8(k, v, slot_map, k_cache, v_cache, k_scale, v_scale, k_bounds=None,
+                    stream=None):
+    """Quantise new keys and values into the cache, in place (fa_kv_write_fp8).
+    k, v bf16 [Hkv, n, d], or any view of that shape whose channels are
+    contiguous and whose other strides are multiples of 8 (a token-major
+    projection output, transposed); slot_map int64 [n]; k_cache/v_cache e4m3
+    [num_pages,Hkv,page_size,d]; k_scale/v_scale fp32 [num_pages,Hkv]; k_bounds
+    int8 [num_pages,Hkv,2,d] when blocks are to be selected."""
+    lib = load_library()
+    num_pages, Hkv, ps, d = _need_cache(k_cache, v_cache, k_scale, v_scale)
+    _need(slot_map, "slot_map", torch.int64, 1)
+    n = slot_map.numel()
+    for t, name in ((k, "k"), (v, "v")):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name} must be a CUDA tensor")
+        if t.dtype != torch.bfloat16:
+            raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
+        if tuple(t.shape) != (Hkv, n, d):
+            raise ValueError(f"{name} must be [Hkv, n, d] = {(Hkv, n, d)}, got {tuple(t.shape)}")
+        if n > 0 and t.stride(2) != 1:
+            raise ValueError(f"{name} must have contiguous channels")
+    if k_bounds is not None:
+        _need_bounds(k_bounds, num_pages, Hkv, d)
+    _on_current_device(k, v, slot_map, k_cache, v_cache, k_scale, v_scale, k_bounds)
+    # a dimension of one element is never stepped over: its stride does not matter
+    st_h = [t.stride(0) if Hkv > 1 else 0 for t in (k, v)]
+    st_t = [t.stride(1) if n > 1 else 0 for t in (k, v)]
+    st = lib.fa_kv_write_fp8(_ptr(k), _ptr(v), st_h[0], st_t[0], st_h[1], st_t[1], _ptr(slot_map),
+                             n, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+                             _ptr(k_bounds), num_pages, Hkv, ps, d, _stream(stream))
+    _check(st, "fa_kv_write_fp8")
+
+
+def fa_kv_read_fp8(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens_k, total_k: int,
+                   k=None, v=None, stream=None):
+    """Cached keys and values as packed bf16 [Hkv,total_k,d] (fa_kv_read_fp8), the
+    layout of fa_fwd_varlen; cu_seqlens_k int32 [nseq+1].  Rows of no sequence
+    are left as they were (unset in new outputs).  Returns (k, v)."""
+    lib = load_library()
+    num_pages, Hkv, ps, d = _need_cache(k_cache, v_cache, k_scale, v_scale)
+    _need(cu_seqlens_k, "cu_seqlens_k", torch.int32, 1)
+    nseq = cu_seqlens_k.numel() - 1
+    _need_table(block_table, cu_seqlens_k, "cu_seqlens_k", nseq)
+    _on_current_device(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens_k, k, v)
+    shape = (Hkv, int(total_k), d)
+    k = _out(k, "k", shape, torch.bfloat16, k_cache, stream)
+    v = _out(v, "v", shape, torch.bfloat16, k_cache, stream)
+    st = lib.fa_kv_read_fp8(_ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
+                            _ptr(block_table), _ptr(cu_seqlens_k), _ptr(k), _ptr(v), nseq,
+                            block_table.shape[1], num_pages, int(total_k), Hkv, ps, d,
+                            _stream(stream))
+    _check(st, "fa_kv_read_fp8")
+    return k, v
+
+
+def fa_select_blocks_workspace_size(B, Hkv, max_blocks) -> int:
+    return int(load_library().fa_select_blocks_workspace_size(B, Hkv, max_blocks))
+
+
+def fa_select_blocks(q, k_bounds, k_scale, block_table, seqlens_k, page_size: int, k_blocks: int,
+                     n_first: int = 1, n_last: int = 1, sel=None, n_sel=None, workspace=None,
+                     stream=None):
+    """The k_blocks blocks of each request and KV head with the largest bound on
+    their scores (fa_select_blocks), always with the first n_first and last
+    n_last.  q bf16 [B,Hq,Sq,d].  Returns (sel int32 [B,Hkv,k_blocks] ascending,
+    filled up with -1, n_sel int32 [B,Hkv])."""
+    lib = load_library()
+    _need(q, "q", torch.bfloat16, 4)
+    B, Hq, Sq, d = q.shape
+    _need(k_scale, "k_scale", torch.float32, 2)
+    num_pages, Hkv = k_scale.shape
+    _need_bounds(k_bounds, num_pages, Hkv, d)
+    _need_table(block_table, seqlens_k, "seqlens_k", B)
+    if seqlens_k.numel() != B:
+        raise ValueError(f"seqlens_k must be [{B}]")
+    _on_current_device(q, k_bounds, k_scale, block_table, seqlens_k, sel, n_sel, workspace)
+    max_blocks = block_table.shape[1]
+    sel = _out(sel, "sel", (B, Hkv, int(k_blocks)), torch.int32, q, stream)
+    n_sel = _out(n_sel, "n_sel", (B, Hkv), torch.int32, q, stream)
+    workspace = _workspace(workspace, fa_select_blocks_workspace_size(B, Hkv, max_blocks), q,
+                           stream)
+    st = lib.fa_select_blocks(_ptr(q), _ptr(k_bounds), _ptr(k_scale), _ptr(block_table),
+                              _ptr(seqlens_k), _ptr(sel), _ptr(n_sel), B, Hq, Hkv, Sq, num_pages,
+                              max_blocks, int(page_size), d, int(k_blocks), int(n_first),
+                              int(n_last), _ptr(workspace),
+                              workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(st, "fa_select_blocks")
+    return sel, n_sel
+
+
+def fa_decode_paged_fp8_workspace_size(B, Hq, Hkv, Sq, d) -> int:
+    return int(load_library().fa_decode_paged_fp8_workspace_size(B, Hq, Hkv, Sq, d))
+
+
+def fa_decode_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k,
+                        scale: float, sel=None, n_sel=None, o=None, lse=None, workspace=None,
+                        stream=None):
+    """Attention of the last Sq tokens of each request over the paged 8-bit cache
+    (fa_decode_paged_fp8).  q bf16 [B,Hq,Sq,d]; seqlens_k int32 [B] counts the Sq
+    tokens too; sel/n_sel (fa_select_blocks) restrict each KV head to the listed
+    blocks.  Returns (o bf16 [B,Hq,Sq,d], lse fp32 [B,Hq,Sq])."""
+    lib = load_library()
+    _need(q, "q", torch.bfloat16, 4)
+    num_pages, Hkv, ps, d = _need_cache(k_cache, v_cache, k_scale, v_scale)
+    B, Hq, Sq, dq = q.shape
+    if dq != d:
+        raise ValueError(f"q has head dimension {dq}, the cache {d}")
+    _need_table(block_table, seqlens_k, "seqlens_k", B)
+    if seqlens_k.numel() != B:
+        raise ValueError(f"seqlens_k must be [{B}]")
+    if (sel is None) != (n_sel is None):
+        raise ValueError("sel and n_sel are given together or not at all")
+    if sel is not None:
+        _need(sel, "sel", torch.int32, 3)
+        _need(n_sel, "n_sel", torch.int32, 2)
+        if tuple(sel.shape[:2]) != (B, Hkv) or tuple(n_sel.shape) != (B, Hkv):
+            raise ValueError(f"sel must be [{B}, {Hkv}, max_sel] and n_sel [{B}, {Hkv}]")
+    _on_current_device(q, k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k, sel, n_sel,
+                       o, lse, workspace)
+    o = _out(o, "o", q.shape, torch.bfloat16, q, stream)
+    lse = _out(lse, "lse", (B, Hq, Sq), torch.float32, q, stream)
+    workspace = _workspace(workspace, fa_decode_paged_fp8_workspace_size(B, Hq, Hkv, Sq, d), q,
+                           stream)
+    st = lib.fa_decode_paged_fp8(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
+                                 _ptr(v_scale), _ptr(block_table), _ptr(seqlens_k), _ptr(sel),
+                                 _ptr(n_sel), _ptr(o), _ptr(lse), B, Hq, Hkv, Sq, num_pages,
+                                 block_table.shape[1], 0 if sel is None else sel.shape[2], ps, d,
+                                 float(scale), _ptr(workspace),
+                                 workspace.numel() * workspace.element_size(), _stream(stream))
+    _check(st, "fa_decode_paged_fp8")
     return o, lse
 
 

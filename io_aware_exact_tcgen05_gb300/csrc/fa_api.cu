@@ -16,6 +16,7 @@
 
 #include "../../include/fa.h"
 #include "fa_internal.h"
+#include "fa_kv.h"
 
 namespace fa {
 ProfileHook& profile_hook() {
@@ -371,6 +372,19 @@ fa_status bwd_launch(const void* q, const void* k, const void* v, const void* o,
 }
 
 }  // namespace
+
+namespace fa {
+fa_status api_fail(fa_status s, const char* fmt, ...) {
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(g_detail, sizeof g_detail, fmt, ap);
+  va_end(ap);
+  return s;
+}
+fa_status api_ok() { return ok(); }
+fa_status api_check_device() { return check_device(); }
+float api_scale_log2(float scale) { return scale_log2_of(scale); }
+}  // namespace fa
 
 extern "C" {
 
