@@ -175,14 +175,16 @@ def select(q, bounds, k_scale, table, seqlens, ps, k_blocks, n_first, n_last):
 
 
 def attend(q, cache: Cache, table, seqlens, scale, sel=None, n_sel=None):
-    """q [B,Hq,Sq,d] float64.  Returns (o, lse, spread, score_size): spread is
+    """q [B,Hq,Sq,d] float64.  Returns (o, lse, spread, score_size, v_top): spread is
     sum_j w_j |v_j| per output, score_size the largest scale * sum_i |q_i k_i| of a
-    row's visible keys (both enter the rounding bounds of a test)."""
+    row's visible keys, v_top the largest magnitude that the V scales of the row's
+    keys allow (they enter the rounding bounds of a test)."""
     B, Hq, Sq, d = q.shape
     heads, ps = cache.codes[0].shape[1:3]
     room = table.shape[1] * ps
     o, spread = np.zeros(q.shape), np.zeros(q.shape)
     lse, size = np.full(q.shape[:3], -np.inf), np.zeros(q.shape[:3])
+    v_top = np.zeros(q.shape[:3])
     for b in range(B):
         n = min(max(int(seqlens[b]), 0), room)
         for h in range(heads):
@@ -194,6 +196,9 @@ def attend(q, cache: Cache, table, seqlens, scale, sel=None, n_sel=None):
                                 for j in range(ps) if i * ps + j < n], np.int64)
             k, absent = cache.gather(0, table[b], h, pos)
             v, _ = cache.gather(1, table[b], h, pos)
+            used = {int(table[b, j // ps]) for j, a in zip(pos, absent) if not a}
+            top = 448.0 * max((float(cache.scale[1][page, h]) for page in used), default=0.0)
+            v_top[b, h * (Hq // heads):(h + 1) * (Hq // heads)] = top
             for g in range(h * (Hq // heads), (h + 1) * (Hq // heads)):
                 for i in range(Sq):
                     see = ~absent & (pos <= i + n - Sq)
@@ -207,4 +212,4 @@ def attend(q, cache: Cache, table, seqlens, scale, sel=None, n_sel=None):
                     o[b, g, i] = w @ v[see]
                     spread[b, g, i] = w @ np.abs(v[see])
                     size[b, g, i] = (np.abs(k[see]) @ np.abs(q[b, g, i])).max() * scale
-    return o, lse, spread, size
+    return o, lse, spread, size, v_top

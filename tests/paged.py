@@ -58,7 +58,7 @@ def i32(x):
     return torch.tensor(np.asarray(x), dtype=torch.int32, device=DEV)
 
 
-def attention_bounds(ref_o, ref_lse, spread, size, n_keys, d):
+def attention_bounds(ref_o, ref_lse, spread, size, v_top, n_keys, d):
     """Element-wise bounds of O and LSE against the 64-bit values.
 
     A score is a sum of d products in fp32 (each term off by at most (d + 4) *
@@ -66,18 +66,24 @@ def attention_bounds(ref_o, ref_lse, spread, size, n_keys, d):
     relatively.  A weight is rounded to f16 (half a step: 2^-11) and its exponential
     is off by 2^-21.  Sums over the keys run in fp32: n * 2^-24.  O is rounded to bf16
     (half a step: 2^-8).  The LSE sees the score's error, the sum's and its own
-    rounding to fp32."""
+    rounding to fp32.
+
+    A weight is stored in f16 as w * 2^13 * (its page's V scale / the largest one):
+    below f16's normal range its rounding is at most 2^-25 there, 2^-38 of the
+    largest weight and V scale, so each key adds at most 2^-38 * v_top (the
+    normaliser is at least 1: the key that set the running maximum counts 1)."""
     eps = 2.0 ** -24
     score = (d + 4) * eps * size
     rel = 2 * score + 2.0 ** -11 + 2.0 ** -21 + n_keys * eps
-    tol_o = 2.0 ** -8 * np.abs(ref_o) + rel[..., None] * spread * (1 + 2.0 ** -8) + 1e-30
+    tol_o = 2.0 ** -8 * np.abs(ref_o) + rel[..., None] * spread * (1 + 2.0 ** -8) + (
+        n_keys * 2.0 ** -38 * v_top[..., None])
     tol_lse = score + (n_keys + 8) * eps + 2.0 ** -21 + 4 * eps * np.abs(
         np.where(np.isfinite(ref_lse), ref_lse, 0.0))
     return tol_o, tol_lse
 
 
 def check_attention(o, lse, ref, n_keys, d):
-    ref_o, ref_lse, spread, size = ref
+    ref_o, ref_lse, spread, size, v_top = ref
     got_o, got_l = f64(o), f64(lse)
     assert np.array_equal(np.isnan(got_o), np.isnan(ref_o)), "NaN pattern of O"
     assert np.array_equal(np.isnan(got_l), np.isnan(ref_lse)), "NaN pattern of LSE"
@@ -85,7 +91,7 @@ def check_attention(o, lse, ref, n_keys, d):
     assert np.array_equal(got_l == -np.inf, dead), "-inf pattern of LSE"
     assert np.all(got_o[dead] == 0.0)
     live = ~dead & ~np.isnan(ref_lse)
-    tol_o, tol_l = attention_bounds(ref_o, ref_lse, spread, size, n_keys, d)
+    tol_o, tol_l = attention_bounds(ref_o, ref_lse, spread, size, v_top, n_keys, d)
     fine = live[..., None] & ~np.isnan(ref_o)
     if fine.any():
         worst = (np.abs(got_o[fine] - ref_o[fine]) / tol_o[fine]).max()
