@@ -115,12 +115,14 @@ def _check(status: int, where: str):
 
 
 def _ptr(t):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    return None if t is None else t.data_ptr()
 
 
 def _stream(stream):
-    s = stream if stream is not None else torch.cuda.current_stream()
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    # the raw handle: building a torch.cuda.Stream costs some 10 us a call
+    return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
 
 
 def _need(t, name, dtype, ndim=None):
@@ -394,66 +396,87 @@ def fa_decode_noalloc(q, k_cache, v_cache, seqlens_k, scale: float, o=None, lse=
 
 
 # --------------------------------------------------- paged 8-bit KV cache --
+#
+# A decode step calls these with a microsecond or two of kernel time each, so a
+# tensor's checks are one expression; what is wrong is worked out only then.
+
+_BF16, _F32, _I32, _I64, _I8 = (torch.bfloat16, torch.float32, torch.int32, torch.int64,
+                                torch.int8)
+_U8 = torch.uint8
+_F8 = getattr(torch, "float8_e4m3fn", torch.uint8)
 
 
-def _on_current_device(*tensors):
-    """The library launches on the current device: every tensor has to be there."""
-    dev = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.device.index != dev:
-            raise ValueError(f"tensors must be on the current device (cuda:{dev}), got {t.device}")
+def _device():
+    """The current device's index; -2 (no tensor's) where there is no driver."""
+    try:
+        return torch._C._cuda_getDevice()
+    except RuntimeError:
+        return -2
 
 
-def _new(shape, dtype, like, stream):
+def _refuse(t, name, dtype, shape, dev):
+    """Raise for the first thing about t that is not as the call needs it."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.get_device() != dev:
+        raise ValueError(f"tensors must be on the current device (cuda:{dev}), {name} is on "
+                         f"{t.device}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _have(t, name, dtype, shape, dev):
+    """t is a contiguous `dtype` tensor of that shape on the current device."""
+    if not (isinstance(t, torch.Tensor) and t.dtype == dtype and t.get_device() == dev
+            and t.shape == shape and t.is_contiguous()):
+        _refuse(t, name, dtype, shape, dev)
+
+
+def _dims(t, name, ndim):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dims")
+    return t.shape
+
+
+def _new(shape, dtype, dev, stream):
     """An output or workspace for a call on `stream`: memory that this thread's
     current stream allocates is kept from reuse until `stream` is done with it."""
-    t = torch.empty(shape, dtype=dtype, device=like.device)
+    t = torch.empty(shape, dtype=dtype, device=dev)
     if stream is not None and stream != torch.cuda.current_stream():
         t.record_stream(stream)
     return t
 
 
-def _out(t, name, shape, dtype, like, stream):
+def _out(t, name, shape, dtype, dev, stream):
     if t is None:
-        return _new(shape, dtype, like, stream)
-    _need(t, name, dtype, len(shape))
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+        return _new(shape, dtype, dev, stream)
+    _have(t, name, dtype, shape, dev)
     return t
 
 
-def _workspace(ws, nbytes, like, stream):
+def _workspace(ws, nbytes, dev, stream):
     if ws is None:
-        return _new((max(nbytes, 16),), torch.uint8, like, stream)
-    if not isinstance(ws, torch.Tensor) or not ws.is_cuda or not ws.is_contiguous():
-        raise TypeError("workspace must be a contiguous CUDA tensor")
+        return _new((max(nbytes, 16),), _U8, dev, stream)
+    if not (isinstance(ws, torch.Tensor) and ws.get_device() == dev and ws.is_contiguous()):
+        raise TypeError("workspace must be a contiguous CUDA tensor on the current device")
     return ws
 
 
-def _need_cache(k_cache, v_cache, k_scale, v_scale):
+def _need_cache(k_cache, v_cache, k_scale, v_scale, dev):
     """Shape (num_pages, Hkv, page_size, d) of a cache, checked."""
-    _need8(k_cache, "k_cache")
-    _need8(v_cache, "v_cache")
-    if v_cache.shape != k_cache.shape:
-        raise ValueError("k_cache and v_cache must have the same shape")
-    for t, n in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        _need(t, n, torch.float32, 2)
-        if tuple(t.shape) != tuple(k_cache.shape[:2]):
-            raise ValueError(f"{n} must be [num_pages, Hkv] = {tuple(k_cache.shape[:2])}")
-    return k_cache.shape
-
-
-def _need_bounds(k_bounds, num_pages, Hkv, d):
-    _need(k_bounds, "k_bounds", torch.int8, 4)
-    if tuple(k_bounds.shape) != (num_pages, Hkv, 2, d):
-        raise ValueError(f"k_bounds must be [num_pages, Hkv, 2, d] = {(num_pages, Hkv, 2, d)}")
-
-
-def _need_table(block_table, seqlens, name, rows):
-    _need(block_table, "block_table", torch.int32, 2)
-    _need(seqlens, name, torch.int32, 1)
-    if block_table.shape[0] != rows:
-        raise ValueError(f"block_table must have {rows} rows, got {block_table.shape[0]}")
+    shape = _dims(k_cache, "k_cache", 4)
+    for t, n in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if isinstance(t, torch.Tensor) and t.dtype not in (_U8, _F8):
+            raise TypeError(f"{n} must hold e4m3 bytes (float8_e4m3fn or uint8), got {t.dtype}")
+        _have(t, n, getattr(t, "dtype", _U8), shape, dev)
+    _have(k_scale, "k_scale", _F32, shape[:2], dev)
+    _have(v_scale, "v_scale", _F32, shape[:2], dev)
+    return shape
 
 
 def fa_kv_assign(seqlens, newlens, page_size: int, block_table, free_pages, total_new: int,
@@ -464,24 +487,24 @@ def fa_kv_assign(seqlens, newlens, page_size: int, block_table, free_pages, tota
     off the front of free_pages int32 [n_free].  Returns (slot_map int64
     [total_new], cu_new int32 [B+1], seqlens_out int32 [B], cu_seqlens_k int32
     [B+1], n_used int32 [1])."""
-    lib = load_library()
-    _need(newlens, "newlens", torch.int32, 1)
-    _need(free_pages, "free_pages", torch.int32, 1)
-    B = newlens.numel()
-    _need_table(block_table, seqlens, "seqlens", B)
-    if seqlens.numel() != B:
-        raise ValueError("seqlens and newlens must have the same length")
-    _on_current_device(seqlens, newlens, block_table, free_pages, slot_map, cu_new, seqlens_out,
-                       cu_seqlens_k, n_used)
-    slot_map = _out(slot_map, "slot_map", (int(total_new),), torch.int64, seqlens, stream)
-    cu_new = _out(cu_new, "cu_new", (B + 1,), torch.int32, seqlens, stream)
-    seqlens_out = _out(seqlens_out, "seqlens_out", (B,), torch.int32, seqlens, stream)
-    cu_seqlens_k = _out(cu_seqlens_k, "cu_seqlens_k", (B + 1,), torch.int32, seqlens, stream)
-    n_used = _out(n_used, "n_used", (1,), torch.int32, seqlens, stream)
-    st = lib.fa_kv_assign(_ptr(seqlens), _ptr(newlens), B, int(page_size), _ptr(block_table),
-                          block_table.shape[1], _ptr(free_pages), free_pages.numel(),
-                          _ptr(slot_map), int(total_new), _ptr(cu_new), _ptr(seqlens_out),
-                          _ptr(cu_seqlens_k), _ptr(n_used), _stream(stream))
+    lib, dev = load_library(), _device()
+    B, max_blocks = _dims(block_table, "block_table", 2)
+    _have(block_table, "block_table", _I32, (B, max_blocks), dev)
+    _have(seqlens, "seqlens", _I32, (B,), dev)
+    _have(newlens, "newlens", _I32, (B,), dev)
+    n_free, = _dims(free_pages, "free_pages", 1)
+    _have(free_pages, "free_pages", _I32, (n_free,), dev)
+    total_new = int(total_new)
+    slot_map = _out(slot_map, "slot_map", (total_new,), _I64, dev, stream)
+    cu_new = _out(cu_new, "cu_new", (B + 1,), _I32, dev, stream)
+    seqlens_out = _out(seqlens_out, "seqlens_out", (B,), _I32, dev, stream)
+    cu_seqlens_k = _out(cu_seqlens_k, "cu_seqlens_k", (B + 1,), _I32, dev, stream)
+    n_used = _out(n_used, "n_used", (1,), _I32, dev, stream)
+    st = lib.fa_kv_assign(seqlens.data_ptr(), newlens.data_ptr(), B, int(page_size),
+                          block_table.data_ptr(), max_blocks, free_pages.data_ptr(), n_free,
+                          slot_map.data_ptr(), total_new, cu_new.data_ptr(),
+                          seqlens_out.data_ptr(), cu_seqlens_k.data_ptr(), n_used.data_ptr(),
+                          _stream(stream))
     _check(st, "fa_kv_assign")
     return slot_map, cu_new, seqlens_out, cu_seqlens_k, n_used
 
@@ -494,28 +517,26 @@ def fa_kv_write_fp8(k, v, slot_map, k_cache, v_cache, k_scale, v_scale, k_bounds
     projection output, transposed); slot_map int64 [n]; k_cache/v_cache e4m3
     [num_pages,Hkv,page_size,d]; k_scale/v_scale fp32 [num_pages,Hkv]; k_bounds
     int8 [num_pages,Hkv,2,d] when blocks are to be selected."""
-    lib = load_library()
-    num_pages, Hkv, ps, d = _need_cache(k_cache, v_cache, k_scale, v_scale)
-    _need(slot_map, "slot_map", torch.int64, 1)
-    n = slot_map.numel()
+    lib, dev = load_library(), _device()
+    num_pages, Hkv, ps, d = _need_cache(k_cache, v_cache, k_scale, v_scale, dev)
+    n, = _dims(slot_map, "slot_map", 1)
+    _have(slot_map, "slot_map", _I64, (n,), dev)
+    strides = []
     for t, name in ((k, "k"), (v, "v")):
-        if not isinstance(t, torch.Tensor) or not t.is_cuda:
-            raise TypeError(f"{name} must be a CUDA tensor")
-        if t.dtype != torch.bfloat16:
-            raise TypeError(f"{name} must be {torch.bfloat16}, got {t.dtype}")
-        if tuple(t.shape) != (Hkv, n, d):
-            raise ValueError(f"{name} must be [Hkv, n, d] = {(Hkv, n, d)}, got {tuple(t.shape)}")
-        if n > 0 and t.stride(2) != 1:
+        if not (isinstance(t, torch.Tensor) and t.dtype == _BF16 and t.get_device() == dev
+                and t.shape == (Hkv, n, d)):
+            _refuse(t, name, _BF16, (Hkv, n, d), dev)
+        st_h, st_t, st_c = t.stride()
+        if n > 0 and st_c != 1:
             raise ValueError(f"{name} must have contiguous channels")
+        # a dimension of one element is never stepped over: its stride does not matter
+        strides += [st_h if Hkv > 1 else 0, st_t if n > 1 else 0]
     if k_bounds is not None:
-        _need_bounds(k_bounds, num_pages, Hkv, d)
-    _on_current_device(k, v, slot_map, k_cache, v_cache, k_scale, v_scale, k_bounds)
-    # a dimension of one element is never stepped over: its stride does not matter
-    st_h = [t.stride(0) if Hkv > 1 else 0 for t in (k, v)]
-    st_t = [t.stride(1) if n > 1 else 0 for t in (k, v)]
-    st = lib.fa_kv_write_fp8(_ptr(k), _ptr(v), st_h[0], st_t[0], st_h[1], st_t[1], _ptr(slot_map),
-                             n, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-                             _ptr(k_bounds), num_pages, Hkv, ps, d, _stream(stream))
+        _have(k_bounds, "k_bounds", _I8, (num_pages, Hkv, 2, d), dev)
+    st = lib.fa_kv_write_fp8(k.data_ptr(), v.data_ptr(), *strides, slot_map.data_ptr(), n,
+                             k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+                             v_scale.data_ptr(), _ptr(k_bounds), num_pages, Hkv, ps, d,
+                             _stream(stream))
     _check(st, "fa_kv_write_fp8")
 
 
@@ -524,19 +545,18 @@ def fa_kv_read_fp8(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens_k
     """Cached keys and values as packed bf16 [Hkv,total_k,d] (fa_kv_read_fp8), the
     layout of fa_fwd_varlen; cu_seqlens_k int32 [nseq+1].  Rows of no sequence
     are left as they were (unset in new outputs).  Returns (k, v)."""
-    lib = load_library()
-    num_pages, Hkv, ps, d = _need_cache(k_cache, v_cache, k_scale, v_scale)
-    _need(cu_seqlens_k, "cu_seqlens_k", torch.int32, 1)
-    nseq = cu_seqlens_k.numel() - 1
-    _need_table(block_table, cu_seqlens_k, "cu_seqlens_k", nseq)
-    _on_current_device(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens_k, k, v)
-    shape = (Hkv, int(total_k), d)
-    k = _out(k, "k", shape, torch.bfloat16, k_cache, stream)
-    v = _out(v, "v", shape, torch.bfloat16, k_cache, stream)
-    st = lib.fa_kv_read_fp8(_ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale),
-                            _ptr(block_table), _ptr(cu_seqlens_k), _ptr(k), _ptr(v), nseq,
-                            block_table.shape[1], num_pages, int(total_k), Hkv, ps, d,
-                            _stream(stream))
+    lib, dev = load_library(), _device()
+    num_pages, Hkv, ps, d = _need_cache(k_cache, v_cache, k_scale, v_scale, dev)
+    nseq, max_blocks = _dims(block_table, "block_table", 2)
+    _have(block_table, "block_table", _I32, (nseq, max_blocks), dev)
+    _have(cu_seqlens_k, "cu_seqlens_k", _I32, (nseq + 1,), dev)
+    total_k = int(total_k)
+    k = _out(k, "k", (Hkv, total_k, d), _BF16, dev, stream)
+    v = _out(v, "v", (Hkv, total_k, d), _BF16, dev, stream)
+    st = lib.fa_kv_read_fp8(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
+                            v_scale.data_ptr(), block_table.data_ptr(), cu_seqlens_k.data_ptr(),
+                            k.data_ptr(), v.data_ptr(), nseq, max_blocks, num_pages, total_k, Hkv,
+                            ps, d, _stream(stream))
     _check(st, "fa_kv_read_fp8")
     return k, v
 
@@ -552,26 +572,25 @@ def fa_select_blocks(q, k_bounds, k_scale, block_table, seqlens_k, page_size: in
     their scores (fa_select_blocks), always with the first n_first and last
     n_last.  q bf16 [B,Hq,Sq,d].  Returns (sel int32 [B,Hkv,k_blocks] ascending,
     filled up with -1, n_sel int32 [B,Hkv])."""
-    lib = load_library()
-    _need(q, "q", torch.bfloat16, 4)
-    B, Hq, Sq, d = q.shape
-    _need(k_scale, "k_scale", torch.float32, 2)
-    num_pages, Hkv = k_scale.shape
-    _need_bounds(k_bounds, num_pages, Hkv, d)
-    _need_table(block_table, seqlens_k, "seqlens_k", B)
-    if seqlens_k.numel() != B:
-        raise ValueError(f"seqlens_k must be [{B}]")
-    _on_current_device(q, k_bounds, k_scale, block_table, seqlens_k, sel, n_sel, workspace)
-    max_blocks = block_table.shape[1]
-    sel = _out(sel, "sel", (B, Hkv, int(k_blocks)), torch.int32, q, stream)
-    n_sel = _out(n_sel, "n_sel", (B, Hkv), torch.int32, q, stream)
-    workspace = _workspace(workspace, fa_select_blocks_workspace_size(B, Hkv, max_blocks), q,
+    lib, dev = load_library(), _device()
+    B, Hq, Sq, d = _dims(q, "q", 4)
+    num_pages, Hkv = _dims(k_scale, "k_scale", 2)
+    max_blocks = _dims(block_table, "block_table", 2)[1]
+    _have(q, "q", _BF16, (B, Hq, Sq, d), dev)
+    _have(k_scale, "k_scale", _F32, (num_pages, Hkv), dev)
+    _have(k_bounds, "k_bounds", _I8, (num_pages, Hkv, 2, d), dev)
+    _have(block_table, "block_table", _I32, (B, max_blocks), dev)
+    _have(seqlens_k, "seqlens_k", _I32, (B,), dev)
+    k_blocks = int(k_blocks)
+    sel = _out(sel, "sel", (B, Hkv, max(k_blocks, 0)), _I32, dev, stream)
+    n_sel = _out(n_sel, "n_sel", (B, Hkv), _I32, dev, stream)
+    workspace = _workspace(workspace, lib.fa_select_blocks_workspace_size(B, Hkv, max_blocks), dev,
                            stream)
-    st = lib.fa_select_blocks(_ptr(q), _ptr(k_bounds), _ptr(k_scale), _ptr(block_table),
-                              _ptr(seqlens_k), _ptr(sel), _ptr(n_sel), B, Hq, Hkv, Sq, num_pages,
-                              max_blocks, int(page_size), d, int(k_blocks), int(n_first),
-                              int(n_last), _ptr(workspace),
-                              workspace.numel() * workspace.element_size(), _stream(stream))
+    st = lib.fa_select_blocks(q.data_ptr(), k_bounds.data_ptr(), k_scale.data_ptr(),
+                              block_table.data_ptr(), seqlens_k.data_ptr(), sel.data_ptr(),
+                              n_sel.data_ptr(), B, Hq, Hkv, Sq, num_pages, max_blocks,
+                              int(page_size), d, k_blocks, int(n_first), int(n_last),
+                              workspace.data_ptr(), workspace.nbytes, _stream(stream))
     _check(st, "fa_select_blocks")
     return sel, n_sel
 
@@ -587,34 +606,32 @@ def fa_decode_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seql
     (fa_decode_paged_fp8).  q bf16 [B,Hq,Sq,d]; seqlens_k int32 [B] counts the Sq
     tokens too; sel/n_sel (fa_select_blocks) restrict each KV head to the listed
     blocks.  Returns (o bf16 [B,Hq,Sq,d], lse fp32 [B,Hq,Sq])."""
-    lib = load_library()
-    _need(q, "q", torch.bfloat16, 4)
-    num_pages, Hkv, ps, d = _need_cache(k_cache, v_cache, k_scale, v_scale)
-    B, Hq, Sq, dq = q.shape
-    if dq != d:
-        raise ValueError(f"q has head dimension {dq}, the cache {d}")
-    _need_table(block_table, seqlens_k, "seqlens_k", B)
-    if seqlens_k.numel() != B:
-        raise ValueError(f"seqlens_k must be [{B}]")
-    if (sel is None) != (n_sel is None):
+    lib, dev = load_library(), _device()
+    B, Hq, Sq, d = shape = _dims(q, "q", 4)
+    _have(q, "q", _BF16, shape, dev)
+    num_pages, Hkv, ps, dc = _need_cache(k_cache, v_cache, k_scale, v_scale, dev)
+    if dc != d:
+        raise ValueError(f"q has head dimension {d}, the cache {dc}")
+    max_blocks = _dims(block_table, "block_table", 2)[1]
+    _have(block_table, "block_table", _I32, (B, max_blocks), dev)
+    _have(seqlens_k, "seqlens_k", _I32, (B,), dev)
+    max_sel = 0
+    if sel is not None and n_sel is not None:
+        max_sel = _dims(sel, "sel", 3)[2]
+        _have(sel, "sel", _I32, (B, Hkv, max_sel), dev)
+        _have(n_sel, "n_sel", _I32, (B, Hkv), dev)
+    elif sel is not None or n_sel is not None:
         raise ValueError("sel and n_sel are given together or not at all")
-    if sel is not None:
-        _need(sel, "sel", torch.int32, 3)
-        _need(n_sel, "n_sel", torch.int32, 2)
-        if tuple(sel.shape[:2]) != (B, Hkv) or tuple(n_sel.shape) != (B, Hkv):
-            raise ValueError(f"sel must be [{B}, {Hkv}, max_sel] and n_sel [{B}, {Hkv}]")
-    _on_current_device(q, k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k, sel, n_sel,
-                       o, lse, workspace)
-    o = _out(o, "o", q.shape, torch.bfloat16, q, stream)
-    lse = _out(lse, "lse", (B, Hq, Sq), torch.float32, q, stream)
-    workspace = _workspace(workspace, fa_decode_paged_fp8_workspace_size(B, Hq, Hkv, Sq, d), q,
-                           stream)
-    st = lib.fa_decode_paged_fp8(_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(k_scale),
-                                 _ptr(v_scale), _ptr(block_table), _ptr(seqlens_k), _ptr(sel),
-                                 _ptr(n_sel), _ptr(o), _ptr(lse), B, Hq, Hkv, Sq, num_pages,
-                                 block_table.shape[1], 0 if sel is None else sel.shape[2], ps, d,
-                                 float(scale), _ptr(workspace),
-                                 workspace.numel() * workspace.element_size(), _stream(stream))
+    o = _out(o, "o", shape, _BF16, dev, stream)
+    lse = _out(lse, "lse", (B, Hq, Sq), _F32, dev, stream)
+    workspace = _workspace(workspace, lib.fa_decode_paged_fp8_workspace_size(B, Hq, Hkv, Sq, d),
+                           dev, stream)
+    st = lib.fa_decode_paged_fp8(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                                 k_scale.data_ptr(), v_scale.data_ptr(), block_table.data_ptr(),
+                                 seqlens_k.data_ptr(), _ptr(sel), _ptr(n_sel), o.data_ptr(),
+                                 lse.data_ptr(), B, Hq, Hkv, Sq, num_pages, max_blocks, max_sel,
+                                 ps, d, float(scale), workspace.data_ptr(), workspace.nbytes,
+                                 _stream(stream))
     _check(st, "fa_decode_paged_fp8")
     return o, lse
 

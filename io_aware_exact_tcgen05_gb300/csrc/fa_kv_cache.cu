@@ -133,119 +133,191 @@ __global__ void __launch_bounds__(kAssignThreads) fa_kv_assign_kernel(const KvAs
 
 // ------------------------------------------------------------------ write --
 //
-// One CTA per (stretch of kWriteChunk packed tokens, KV head, K or V) serves the
-// runs that start in its stretch.  A run is the new tokens of one page: with
-// n tokens in the page before it,
+// A run is the new tokens of one page.  With n tokens in the page before it,
 //   s_tok = 2^e, e the smallest with amax(new) <= 448 * 2^e (finite values),
 //   s = max(s_old, s_tok) if n > 0, else s_tok,
 //   new code = rn_sat(x / s), held code = rn(code * s_old / s).
 // With power-of-two scales both are exact but for e4m3's own rounding, so a
 // page that is requantised loses nothing above its subnormals.
-// The run's values stay in registers between the maximum and the rounding:
-// each is read once.
-constexpr int kWriteThreads = 128;
+//
+// One CTA per (stretch of packed tokens, KV head, K or V) serves the runs that
+// start in its stretch.  HBM bounds long prompts: every value is read once and
+// stays in registers between the maximum and the rounding; a CTA has as many
+// threads as a full page has 128-byte pieces, so each holds at most 8 16-byte
+// pieces, all of them in flight at once.
+template <int D, int PS>
+struct WriteTile {
+  static constexpr int kCols = D / 8;  // 16-byte pieces of a row
+  static constexpr int kThreads = PS * kCols / 8 < 32 ? 32 : PS * kCols / 8;
+  static constexpr int kRows = kThreads / kCols;  // rows of one pass
+  static constexpr int kPasses = PS / kRows;
+  static constexpr int kWarps = kThreads / 32;
+};
 
-template <int D>
-__global__ void __launch_bounds__(kWriteThreads) fa_kv_write_kernel(const KvWriteParams p,
-                                                                    int chunk) {
-  constexpr int CPR = D / 8;                   // 16-byte chunks per row
-  constexpr int RPP = kWriteThreads / CPR;     // rows per pass
-  constexpr int PASSES = 128 / RPP;            // a run has at most 128 rows
-  __shared__ int s_len, s_max;
-  __shared__ int s_hi[D], s_lo[D];
-  const int tid = threadIdx.x, ps = p.s.page_size;
+template <int D, int PS>
+__global__ void __launch_bounds__(WriteTile<D, PS>::kThreads)
+    fa_kv_write_kernel(const KvWriteParams p, int stretch) {
+  using T = WriteTile<D, PS>;
+  __shared__ uint32_t s_max[2][T::kWarps];
+  __shared__ __half2 s_hi[T::kWarps][D / 2], s_lo[T::kWarps][D / 2];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int h = blockIdx.y;
   const bool is_v = blockIdx.z != 0;
-  const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(is_v ? p.v : p.k);
   const long long st_h = is_v ? p.v_stride_h : p.k_stride_h;
   const long long st_t = is_v ? p.v_stride_t : p.k_stride_t;
+  const int col = tid % T::kCols, row0 = tid / T::kCols;
+  const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(is_v ? p.v : p.k) + h * st_h + col * 8;
   uint8_t* cache = static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache);
   float* scales = is_v ? p.v_scale : p.k_scale;
   int8_t* bounds = is_v ? nullptr : p.k_bounds;
-  const long long n_slots = static_cast<long long>(p.s.num_pages) * ps;
-  const int t0 = blockIdx.x * chunk;
-  const int t1 = min(t0 + chunk, p.n_tokens);
-  const int col = tid % CPR, row0 = tid / CPR;
+  const long long n_slots = static_cast<long long>(p.s.num_pages) * PS;
+  const int t_lo = blockIdx.x * stretch;
+  const int t_hi = min(t_lo + stretch, p.n_tokens);
+  int turn = 0;
 
-  for (int t = t0; t < t1; ++t) {
-    const long long slot = p.slot_map[t];
-    if (slot < 0 || slot >= n_slots) continue;  // uniform over the CTA
-    const int off = static_cast<int>(slot % ps);
-    if (t > 0 && off > 0 && p.slot_map[t - 1] == slot - 1) continue;  // inside a run
-    const int page = static_cast<int>(slot / ps);
-    const int most = min(ps - off, p.n_tokens - t);
-    __syncthreads();
-    if (tid == 0) {
-      s_len = most;
-      s_max = 0;
+  for (int base = t_lo; base < t_hi; base += 32) {
+    // every warp finds the runs that start in these 32 tokens
+    long long slot = -1;
+    bool starts = false;
+    if (base + lane < t_hi) {
+      slot = p.slot_map[base + lane];
+      starts = slot >= 0 && slot < n_slots;
+      if (starts && slot % PS != 0 && base + lane > 0)
+        starts = p.slot_map[base + lane - 1] != slot - 1;
     }
-    for (int c = tid; c < D; c += kWriteThreads) {
-      s_hi[c] = -128;
-      s_lo[c] = 127;
-    }
-    __syncthreads();
-    if (tid > 0 && tid < most && p.slot_map[t + tid] != slot + tid) atomicMin(&s_len, tid);
-    const size_t tile = (static_cast<size_t>(page) * p.s.Hkv + h);
-    float s_old = off > 0 ? scales[tile] : 0.f;
-    if (!(s_old > 0.f && s_old <= 3.4028235e38f)) s_old = 0.f;
-    __syncthreads();
-    const int len = s_len;
-    uint4 x[PASSES];
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < PASSES; ++i) {
-      const int r = row0 + i * RPP;
-      x[i] = make_uint4(0u, 0u, 0u, 0u);
-      if (r < len) {
-        x[i] = *reinterpret_cast<const uint4*>(src + h * st_h + (t + r) * st_t + col * 8);
-        m = __vmaxu2(m, max_finite_bf16x2(x[i]));
+    for (uint32_t todo = __ballot_sync(0xffffffffu, starts); todo; todo &= todo - 1) {
+      const int at = __ffs(todo) - 1;
+      const int t = base + at;
+      const long long first = __shfl_sync(0xffffffffu, slot, at);
+      const int page = static_cast<int>(first / PS), off = static_cast<int>(first % PS);
+      const size_t tile = static_cast<size_t>(page) * p.s.Hkv + h;
+      float s_old = off > 0 ? scales[tile] : 0.f;
+      const int most = min(PS - off, p.n_tokens - t);
+      int len = 1;
+      while (len < most) {  // up to the first token that does not follow
+        const int j = len + lane;
+        const uint32_t stop =
+            __ballot_sync(0xffffffffu, j >= most || p.slot_map[t + j] != first + j);
+        if (stop) {
+          len += __ffs(stop) - 1;
+          break;
+        }
+        len += 32;
       }
-    }
-    const int mine = max(m & 0xffffu, m >> 16);
-    const int top = __reduce_max_sync(0xffffffffu, mine);
-    if ((tid & 31) == 0) atomicMax(&s_max, top);
-    __syncthreads();
-    const float s_tok = block_scale(static_cast<uint32_t>(s_max));
-    const float s = fmaxf(s_old, s_tok);
-    uint8_t* dst = cache + tile * ps * D;
-    const bool grown = off > 0 && s > s_old;
-    const float ratio = off > 0 ? s_old / s : 0.f;
-    if (grown) {
-      for (int i = tid; i < off * CPR; i += kWriteThreads) {
-        uint2* w = reinterpret_cast<uint2*>(dst) + i;
-        *w = rescale_codes(*w, ratio);
+      if (!(s_old > 0.f && s_old <= 3.4028235e38f)) s_old = 0.f;
+
+      uint4 x[T::kPasses];
+      uint32_t m = 0, any = 0;  // largest finite magnitude; largest magnitude bits
+#pragma unroll
+      for (int i = 0; i < T::kPasses; ++i) {
+        const int r = row0 + i * T::kRows;
+        x[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (r < len) x[i] = ld_stream16(src + (t + r) * st_t);
       }
-    }
-    const bool pow2 = (__float_as_uint(s) & 0x7fffffu) == 0;
-    const float inv = 1.f / s;
 #pragma unroll
-    for (int i = 0; i < PASSES; ++i) {
-      const int r = row0 + i * RPP;
-      if (r < len) {
-        const uint2 c = quantise8(x[i], s, inv, pow2);
-        reinterpret_cast<uint2*>(dst)[(off + r) * CPR + col] = c;
-        if (bounds) {
+      for (int i = 0; i < T::kPasses; ++i) {
+        any = __vmaxu2(any, __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
+                                     __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu)));
+      }
+      m = any;
+      const bool odd_values = max(any & 0xffffu, any >> 16) >= 0x7f80u;  // infinities, NaN
+      if (odd_values) {
+        m = 0;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float v = code_value((e < 4 ? c.x : c.y) >> (8 * (e & 3)) & 0xffu);
-            atomicMax(&s_hi[col * 8 + e], static_cast<int>(ceilf(v * 0.25f)));
-            atomicMin(&s_lo[col * 8 + e], static_cast<int>(floorf(v * 0.25f)));
+        for (int i = 0; i < T::kPasses; ++i) m = __vmaxu2(m, max_finite_bf16x2(x[i]));
+      }
+      const uint32_t top = __reduce_max_sync(0xffffffffu, max(m & 0xffffu, m >> 16));
+      if (lane == 0) s_max[turn][warp] = top;
+      // all reads of the page's old scale and bounds come before this barrier,
+      // all writes after it
+      __half2 old_hi, old_lo;
+      if (bounds && off > 0 && tid < D / 2) {
+        const char2 a = reinterpret_cast<const char2*>(bounds + tile * 2 * D)[tid];
+        const char2 b = reinterpret_cast<const char2*>(bounds + tile * 2 * D + D)[tid];
+        old_hi = __floats2half2_rn(a.x, a.y);
+        old_lo = __floats2half2_rn(b.x, b.y);
+      }
+      __syncthreads();
+      uint32_t amax = 0;
+#pragma unroll
+      for (int w = 0; w < T::kWarps; ++w) amax = max(amax, s_max[turn][w]);
+      turn ^= 1;
+      const float s = fmaxf(s_old, block_scale(amax));
+      const float ratio = off > 0 ? s_old / s : 0.f;
+      uint8_t* dst = cache + tile * PS * D;
+      if (off > 0 && s > s_old) {
+        for (int i = tid; i < off * T::kCols; i += T::kThreads) {
+          uint2* w = reinterpret_cast<uint2*>(dst) + i;
+          *w = rescale_codes(*w, ratio);
+        }
+      }
+      const bool pow2 = (__float_as_uint(s) & 0x7fffffu) == 0;
+      const float inv = 1.f / s;
+      __half2 hi[4], lo[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        hi[e] = __float2half2_rn(-65504.f);
+        lo[e] = __float2half2_rn(65504.f);
+      }
+#pragma unroll
+      for (int i = 0; i < T::kPasses; ++i) {
+        const int r = row0 + i * T::kRows;
+        if (r < len) {
+          uint2 c = quantise8(x[i], s, inv, pow2);
+          reinterpret_cast<uint2*>(dst)[(off + r) * T::kCols + col] = c;
+          if (bounds) {
+            if (odd_values) c = zero_nan_codes(c);
+            const uint32_t w[4] = {c.x, c.x >> 16, c.y, c.y >> 16};
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint32_t v = e4m3x2_to_f16x2(w[e]);
+              hi[e] = __hmax2(hi[e], *reinterpret_cast<const __half2*>(&v));
+              lo[e] = __hmin2(lo[e], *reinterpret_cast<const __half2*>(&v));
+            }
           }
         }
       }
-    }
-    __syncthreads();
-    if (tid == 0) scales[tile] = s;
-    if (bounds) {
-      int8_t* bd = bounds + tile * 2 * D;
-      for (int c = tid; c < D; c += kWriteThreads) {
-        int hi = s_hi[c], lo = s_lo[c];
-        if (off > 0) {
-          hi = max(hi, static_cast<int>(ceilf(bd[c] * ratio)));
-          lo = min(lo, static_cast<int>(floorf(bd[D + c] * ratio)));
+      if (tid == 0) scales[tile] = s;
+      if (bounds) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+#pragma unroll
+          for (int o = T::kCols; o < 32; o <<= 1) {
+            hi[e] = __hmax2(hi[e], __shfl_xor_sync(0xffffffffu, hi[e], o));
+            lo[e] = __hmin2(lo[e], __shfl_xor_sync(0xffffffffu, lo[e], o));
+          }
+          if (lane < T::kCols) {
+            s_hi[warp][col * 4 + e] = hi[e];
+            s_lo[warp][col * 4 + e] = lo[e];
+          }
         }
-        bd[c] = static_cast<int8_t>(hi);
-        bd[D + c] = static_cast<int8_t>(lo);
+        __syncthreads();
+        for (int c = tid; c < D / 2; c += T::kThreads) {
+          __half2 a = s_hi[0][c], z = s_lo[0][c];
+#pragma unroll
+          for (int w = 1; w < T::kWarps; ++w) {
+            a = __hmax2(a, s_hi[w][c]);
+            z = __hmin2(z, s_lo[w][c]);
+          }
+          float2 f = __half22float2(a), g = __half22float2(z);
+          f = make_float2(ceilf(f.x * 0.25f), ceilf(f.y * 0.25f));
+          g = make_float2(floorf(g.x * 0.25f), floorf(g.y * 0.25f));
+          if (off > 0) {
+            if (c != tid) {  // fewer threads than channel pairs
+              const char2 u = reinterpret_cast<const char2*>(bounds + tile * 2 * D)[c];
+              const char2 v = reinterpret_cast<const char2*>(bounds + tile * 2 * D + D)[c];
+              old_hi = __floats2half2_rn(u.x, u.y);
+              old_lo = __floats2half2_rn(v.x, v.y);
+            }
+            const float2 u = __half22float2(old_hi), v = __half22float2(old_lo);
+            f = make_float2(fmaxf(f.x, ceilf(u.x * ratio)), fmaxf(f.y, ceilf(u.y * ratio)));
+            g = make_float2(fminf(g.x, floorf(v.x * ratio)), fminf(g.y, floorf(v.y * ratio)));
+          }
+          reinterpret_cast<char2*>(bounds + tile * 2 * D)[c] =
+              make_char2(static_cast<signed char>(f.x), static_cast<signed char>(f.y));
+          reinterpret_cast<char2*>(bounds + tile * 2 * D + D)[c] =
+              make_char2(static_cast<signed char>(g.x), static_cast<signed char>(g.y));
+        }
       }
     }
   }
@@ -305,12 +377,35 @@ cudaError_t launch_kv_assign(const KvAssignParams& p, cudaStream_t stream) {
   return cudaGetLastError();
 }
 
-cudaError_t launch_kv_write(const KvWriteParams& p, cudaStream_t stream) {
-  const int chunk = p.n_tokens <= 1024 ? 1 : 16;
-  const dim3 grid((p.n_tokens + chunk - 1) / chunk, p.s.Hkv, 2);
-  if (p.s.d == 128) fa_kv_write_kernel<128><<<grid, kWriteThreads, 0, stream>>>(p, chunk);
-  else fa_kv_write_kernel<64><<<grid, kWriteThreads, 0, stream>>>(p, chunk);
+namespace {
+
+template <int D, int PS>
+cudaError_t launch_write(const KvWriteParams& p, cudaStream_t stream) {
+  // A stretch of a page's length has about one run in it when prompts come in;
+  // single tokens are a run each, so few tokens are spread over more CTAs: the
+  // longest stretch that still leaves some 16 CTAs for each of 152 SMs.
+  const long long work = 2LL * p.n_tokens * p.s.Hkv;
+  int stretch = 1;
+  while (stretch < PS && work / (2 * stretch) >= 152 * 16) stretch *= 2;
+  const dim3 grid((p.n_tokens + stretch - 1) / stretch, p.s.Hkv, 2);
+  fa_kv_write_kernel<D, PS><<<grid, WriteTile<D, PS>::kThreads, 0, stream>>>(p, stretch);
   return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch_write_d(const KvWriteParams& p, cudaStream_t stream) {
+  switch (p.s.page_size) {
+    case 16: return launch_write<D, 16>(p, stream);
+    case 32: return launch_write<D, 32>(p, stream);
+    case 64: return launch_write<D, 64>(p, stream);
+    default: return launch_write<D, 128>(p, stream);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_kv_write(const KvWriteParams& p, cudaStream_t stream) {
+  return p.s.d == 128 ? launch_write_d<128>(p, stream) : launch_write_d<64>(p, stream);
 }
 
 cudaError_t launch_kv_read(const KvReadParams& p, cudaStream_t stream) {

@@ -50,10 +50,19 @@ __device__ __forceinline__ float2 e4m3x2_to_f32x2(uint32_t w) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
-// One code's value; NaN counts as 0 (the bounds of a page leave NaN out).
-__device__ __forceinline__ float code_value(uint32_t c) {
-  const float v = e4m3x2_to_f32x2(c).x;
-  return (c & 0x7fu) == 0x7fu ? 0.f : v;
+// NaN codes -> 0 (the bounds of a page leave NaN out).
+__device__ __forceinline__ uint2 zero_nan_codes(const uint2& w) {
+  return make_uint2(w.x & ~__vcmpeq4(w.x & 0x7f7f7f7fu, 0x7f7f7f7fu),
+                    w.y & ~__vcmpeq4(w.y & 0x7f7f7f7fu, 0x7f7f7f7fu));
+}
+
+// 16 bytes that are read once: past L1.
+__device__ __forceinline__ uint4 ld_stream16(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "l"(p));
+  return v;
 }
 
 // Eight bf16 values / s -> e4m3 codes.  The reciprocal of a power of two is
