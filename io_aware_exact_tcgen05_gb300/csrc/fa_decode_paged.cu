@@ -11,10 +11,12 @@
 //
 // f16 and its range: a query row is multiplied by the power of two that puts
 // its largest element into [2^14, 2^15), which loses nothing above 2^-38 of it.
-// Weights are taken against a running maximum m that may lag by 2 (log2 units)
-// and are stored as w * 2^13 * v_scale / v_ref <= 2^15 (v_ref: the largest V scale
-// so far), so a weight keeps f16's 11 bits down to 2^-27 of the largest and is
-// rounded by at most 2^-38 of it below.  Sums, maxima and accumulators are fp32.
+// Weights are taken against a running maximum m that may lag by 6 (log2 units)
+// and are stored as w * 2^9 * v_scale / v_ref <= 2^15 (v_ref: the largest V scale
+// so far), so a weight keeps f16's 11 bits down to 2^-23 of the largest and is
+// rounded by at most 2^-34 of it below.  (A lag of 2 kept four bits more and
+// moved the maximum on most steps of 32 rows: REPLACE2.)  Sums, maxima and
+// accumulators are fp32.
 //
 // Operands without shared memory: the contraction index of a product may be
 // permuted freely, so a lane loads 16-byte pieces of whole rows and hands their
@@ -46,21 +48,26 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kBlockKeys = 16;
 constexpr int kSms = 152;
-constexpr int kMinShare = 16;       // 16-key blocks a CTA takes at least
-constexpr float kLag = 2.f;         // how far (log2) a weight may exceed the running maximum
-constexpr float kWeightUnit = 8192.f;
+constexpr int kMinShare = 8;        // 16-key blocks a CTA takes at least
+constexpr float kLag = 6.f;         // how far (log2) a weight may exceed the running maximum
+constexpr float kWeightUnit = 512.f;
 
-// Row tiles of 8 a CTA serves, and CTAs per SM (by registers and shared memory).
+// Row tiles of 8 a CTA serves, and CTAs per SM (by registers).  Up to 8 rows the
+// narrow kernel; more go through the wide one, 32 at a time.
 template <int NT> struct Plan;
 template <> struct Plan<1> { static constexpr int kCtasPerSm = 4; };
-template <> struct Plan<2> { static constexpr int kCtasPerSm = 3; };
-template <> struct Plan<4> { static constexpr int kCtasPerSm = 2; };
+template <> struct Plan<2> { static constexpr int kCtasPerSm = 4; };
+template <> struct Plan<4> { static constexpr int kCtasPerSm = 3; };
 
 int row_tiles(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
 int grid_ctas(int nt) {
   return kSms * (nt == 1 ? Plan<1>::kCtasPerSm : nt == 2 ? Plan<2>::kCtasPerSm
                                                          : Plan<4>::kCtasPerSm);
 }
+
+// Running maximum of a row that has seen no key yet: finite, so that differences
+// with it stay defined, and below every score.
+constexpr float kNoMax = -3.0e38f;
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
 
@@ -132,37 +139,98 @@ __device__ __forceinline__ void make_line(const PagedDecodeParams& p, int row_bl
 }
 
 __device__ __forceinline__ long long share_of(long long total, int ctas) {
-  return max((total + ctas - 1) / ctas, static_cast<long long>(kMinShare));
+  const long long even = (total + ctas - 1) / ctas;
+  if (even <= kMinShare) return kMinShare;
+  // whole multiples of 16 leave fewer stretches that straddle two items
+  return even <= 16 ? even : (even + 15) / 16 * 16;
 }
 
-template <int D, int NT>
-struct DecodeSmem {
-  Line line;
-  float m[kWarps][8 * NT];
-  float l[kWarps][8 * NT];
-  alignas(16) float o[kWarps][8 * NT][D + 4];
-  alignas(16) uint2 q[NT > 1 ? NT * (D / 16) * 32 : 1];  // Q fragments; registers hold them for one tile
-  float c_row[8 * NT];
+// A CTA's place in the line: it walks its stretch segment by segment, a segment
+// being blocks [kb0, kb0 + n_seg) of one item (request, KV head) and row block.
+struct Walk {
+  long long at, end, in_item;
+  int item, row_blocks;
+
+  __device__ __forceinline__ bool begin(const PagedDecodeParams& p, int rbs, const Line& line) {
+    row_blocks = rbs;
+    const int items = p.B * p.s.Hkv;
+    const long long total = line.prefix[kThreads];
+    const long long share = share_of(total, gridDim.x);
+    at = share * blockIdx.x;
+    end = min(at + share, total);
+    if (at >= end) return false;
+    int a = 0, z = kThreads;
+    while (z - a > 1) {
+      const int mid = (a + z) >> 1;
+      if (line.prefix[mid] <= at) a = mid; else z = mid;
+    }
+    item = a * ((items + kThreads - 1) / kThreads);
+    in_item = at - line.prefix[a];
+    while (true) {
+      const long long w = static_cast<long long>(item_blocks(p, item)) * row_blocks;
+      if (in_item < w) break;
+      in_item -= w;
+      ++item;
+    }
+    return true;
+  }
+  __device__ __forceinline__ void next(int n_seg, int n_kb) {
+    at += n_seg;
+    in_item += n_seg;
+    if (in_item >= static_cast<long long>(n_kb) * row_blocks) {
+      ++item;
+      in_item = 0;
+    }
+  }
 };
 
-// What a lane looks up for one of its warp's coming blocks.
+struct Segment {
+  int item, b, hk, len, n_kb, kb0, n_seg, row0, n_rows;
+  const int32_t* table;
+  size_t qrow0;
+
+  __device__ __forceinline__ void set(const PagedDecodeParams& p, const Walk& w, int tile_rows) {
+    item = w.item;
+    n_kb = item_blocks(p, item);
+    kb0 = static_cast<int>(w.in_item % n_kb);
+    n_seg = static_cast<int>(min(static_cast<long long>(n_kb - kb0), w.end - w.at));
+    b = item / p.s.Hkv;
+    hk = item % p.s.Hkv;
+    len = request_len(p, b);
+    row0 = static_cast<int>(w.in_item / n_kb) * tile_rows;
+    n_rows = min(tile_rows, p.rows - row0);
+    table = p.block_table + static_cast<size_t>(b) * p.max_blocks;
+    qrow0 = static_cast<size_t>(item) * p.rows + row0;
+  }
+};
+
+template <int D>
+struct NarrowSmem {
+  Line line;
+  float m[kWarps][8];
+  float l[kWarps][8];
+  alignas(16) float o[kWarps][8][D + 4];
+};
+
+// What a lane looks up for one of its warp's coming blocks (block i of the
+// segment; a hidden one has scales of 0 and points at the cache's start).
 struct BlockInfo {
   long long offset;  // bytes from the start of a cache tensor to the block's first key
   int pos;           // position of the first key; INT_MAX: the block is hidden
   float ks, vs;
 };
 
-__device__ __forceinline__ BlockInfo look_up(const PagedDecodeParams& p, int item, int hk, int len,
-                                             const int32_t* table, int kb, int d) {
+__device__ __forceinline__ BlockInfo look_up(const PagedDecodeParams& p, const Segment& sg, int i) {
   const int ps = p.s.page_size, per_page = ps / kBlockKeys;
-  const int idx = kb / per_page, sub = kb % per_page;
-  const int blk = p.sel ? p.sel[static_cast<size_t>(item) * p.max_sel + idx] : idx;
-  BlockInfo r = {0, 0x7fffffff, 1.f, 1.f};
-  if (blk >= 0 && static_cast<long long>(blk) * ps + sub * kBlockKeys < len) {
-    const int page = table[blk];
+  BlockInfo r = {0, 0x7fffffff, 0.f, 0.f};
+  if (i >= sg.n_seg) return r;
+  const int idx = (sg.kb0 + i) / per_page, sub = (sg.kb0 + i) % per_page;
+  const int blk = p.sel ? p.sel[static_cast<size_t>(sg.item) * p.max_sel + idx] : idx;
+  if (blk >= 0 && static_cast<long long>(blk) * ps + sub * kBlockKeys < sg.len) {
+    const int page = sg.table[blk];
     if (page >= 0 && page < p.s.num_pages) {
-      const size_t tile = static_cast<size_t>(page) * p.s.Hkv + hk;
-      r.offset = (static_cast<long long>(tile) * ps + sub * kBlockKeys) * d;
+      const size_t tile = static_cast<size_t>(page) * p.s.Hkv + sg.hk;
+      r.offset = (static_cast<long long>(tile) * ps + sub * kBlockKeys) * p.s.d;
       r.pos = blk * ps + sub * kBlockKeys;
       r.ks = p.k_scale[tile];
       r.vs = p.v_scale[tile];
@@ -171,145 +239,101 @@ __device__ __forceinline__ BlockInfo look_up(const PagedDecodeParams& p, int ite
   return r;
 }
 
-__device__ __forceinline__ bool has_nan_code(uint32_t w) {
-  return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0;
+// Bytes of w that are NaN codes, as a byte mask.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
+  return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu);
 }
 
-template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, Plan<NT>::kCtasPerSm)
-    fa_decode_paged_kernel(const PagedDecodeParams p, int row_blocks, float* part_o, float2* part_ml) {
+// 32 bytes of a query row (16 channels) as f16 times `up`.
+__device__ __forceinline__ void scale_to_f16(const uint4& w, float up, uint32_t (&h)[4]) {
+  const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int e = 0; e < 4; ++e)
+    h[e] = pack_f16x2(__uint_as_float(x[e] << 16) * up, __uint_as_float(x[e] & 0xffff0000u) * up);
+}
+
+// The B operand of row tile row: lane (g, t) loads its channels of row g, scales
+// them by a power of two and hands k-step ks to put(ks, {b0, b1}).  Returns the
+// factor that turns (product * K scale) into a score in log2 units, for row g.
+template <int D, typename Put>
+__device__ __forceinline__ float load_q(const PagedDecodeParams& p, size_t row, bool live, int t,
+                                        Put put) {
+  constexpr int N = D / 32;
+  uint4 w[N];
+  uint32_t top = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    w[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (live)
+      w[i] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) + row * D +
+                                             (i / 2) * 64 + t * 16 + (i % 2) * 8);
+    top = __vmaxu2(top, __vmaxu2(__vmaxu2(w[i].x & 0x7fff7fffu, w[i].y & 0x7fff7fffu),
+                                 __vmaxu2(w[i].z & 0x7fff7fffu, w[i].w & 0x7fff7fffu)));
+  }
+  top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
+  const int ex = max(static_cast<int>(max(top & 0xffffu, top >> 16) >> 7) - 127, -100);
+  const float up = pow2i(14 - ex);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    uint32_t h[4];
+    scale_to_f16(w[i], up, h);
+    // k-steps (i / 2) * 4 + (i % 2) * 2 + {0, 1}: four channels of the lane each
+    const int ks = (i / 2) * 4 + (i % 2) * 2;
+    put(ks, make_uint2(h[0], h[1]));
+    put(ks + 1, make_uint2(h[2], h[3]));
+  }
+  return p.scale_log2 * pow2i(ex - 14);
+}
+
+// Writes one finished output vector (four channels) or partial state.
+template <int D>
+__device__ __forceinline__ void emit(const PagedDecodeParams& p, const Segment& sg, int tile_rows,
+                                     int row, int c, float M, float L, float4 o, float* part_o,
+                                     float2* part_ml) {
+  if (sg.n_seg == sg.n_kb) {
+    const bool empty = L == 0.f;
+    const float inv = empty ? 0.f : 1.f / L;
+    uint2 w;
+    w.x = pack_bf16x2(o.x * inv, o.y * inv);
+    w.y = pack_bf16x2(o.z * inv, o.w * inv);
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + (sg.qrow0 + row) * D + c) = w;
+    if (p.lse && c == 0)
+      p.lse[sg.qrow0 + row] = empty ? neg_inf() : (M + __log2f(L)) * 0.69314718055994530942f;
+  } else {
+    // a CTA's first segment may begin inside an item, its last may end inside one
+    const size_t at = (2 * static_cast<size_t>(blockIdx.x) + (sg.kb0 == 0 ? 1 : 0)) * tile_rows + row;
+    *reinterpret_cast<float4*>(part_o + at * D + c) = o;
+    if (c == 0) part_ml[at] = make_float2(M, L);
+  }
+}
+
+// Up to 8 query rows: the warps take blocks in turn, each with its own state.
+template <int D>
+__global__ void __launch_bounds__(kThreads, Plan<1>::kCtasPerSm)
+    fa_decode_paged_narrow(const PagedDecodeParams p, int row_blocks, float* part_o,
+                           float2* part_ml) {
   constexpr int KC = D / 64;       // 16-byte pieces of a key row per lane
   constexpr int KS = D / 16;       // k-steps of S
   constexpr int MT = D / 16;       // m-tiles of O^T
   constexpr int VW = D / 32;       // 32-bit words of a value row per lane
-  constexpr int R = 8 * NT;
   extern __shared__ __align__(16) unsigned char smem_raw[];
-  DecodeSmem<D, NT>& s = *reinterpret_cast<DecodeSmem<D, NT>*>(smem_raw);
+  NarrowSmem<D>& s = *reinterpret_cast<NarrowSmem<D>*>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
-  const int items = p.B * p.s.Hkv;
 
   make_line(p, row_blocks, s.line);
-  const long long total = s.line.prefix[kThreads];
-  const long long share = share_of(total, gridDim.x);
-  long long at = share * blockIdx.x;
-  const long long end = min(at + share, total);
-  if (at >= end) {
-    griddep_launch_dependents();
-    return;
-  }
-  // the item that holds position `at`, and the position inside it
-  int item;
-  long long in_item;
-  {
-    int a = 0, z = kThreads;
-    while (z - a > 1) {
-      const int mid = (a + z) >> 1;
-      if (s.line.prefix[mid] <= at) a = mid; else z = mid;
-    }
-    item = a * ((items + kThreads - 1) / kThreads);
-    in_item = at - s.line.prefix[a];
-    while (true) {
-      const long long w = static_cast<long long>(item_blocks(p, item)) * row_blocks;
-      if (in_item < w) break;
-      in_item -= w;
-      ++item;
-    }
-  }
-
-  while (at < end) {
-    const int n_kb = item_blocks(p, item);
-    if (n_kb == 0) {  // an item without keys takes no place in the line
-      ++item;
-      in_item = 0;
+  Walk walk;
+  const bool any_work = walk.begin(p, row_blocks, s.line);
+  while (any_work && walk.at < walk.end) {
+    if (item_blocks(p, walk.item) == 0) {  // takes no place in the line
+      ++walk.item;
       continue;
     }
-    const int rb = static_cast<int>(in_item / n_kb);
-    const int kb0 = static_cast<int>(in_item % n_kb);
-    const int n_seg = static_cast<int>(min(static_cast<long long>(n_kb - kb0), end - at));
-    const int b = item / p.s.Hkv, hk = item % p.s.Hkv;
-    const int len = request_len(p, b);
-    const int row0 = rb * R;
-    const int n_rows = min(R, p.rows - row0);
-    const int32_t* table = p.block_table + static_cast<size_t>(b) * p.max_blocks;
-    const size_t qrow0 = static_cast<size_t>(item) * p.rows + row0;
-
-    // ---- queries: scaled by a power of two per row, as B operands ----
-    uint2 qf[NT == 1 ? KS : 1];
-    float c_row[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      if (NT > 1 && (nt % kWarps) != warp) continue;  // the warps share the work, through s.q
-      const int r = nt * 8 + g;
-      uint4 w[2 * KC];
-      uint32_t top = 0;
-#pragma unroll
-      for (int i = 0; i < 2 * KC; ++i) {
-        w[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (r < n_rows)
-          w[i] = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.q) +
-                                                 (qrow0 + r) * D + (i / 2) * 64 + t * 16 +
-                                                 (i % 2) * 8);
-        const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) top = __vmaxu2(top, x[e] & 0x7fff7fffu);
-      }
-      top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 1));
-      top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, 2));
-      const int ex = max(static_cast<int>(max(top & 0xffffu, top >> 16) >> 7) - 127, -100);
-      const float up = pow2i(14 - ex);
-      const float c = p.scale_log2 * pow2i(ex - 14);
-#pragma unroll
-      for (int i = 0; i < 2 * KC; ++i) {
-        const uint32_t x[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
-        uint32_t h[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          h[e] = pack_f16x2(__uint_as_float(x[e] << 16) * up,
-                            __uint_as_float(x[e] & 0xffff0000u) * up);
-        // k-step (i / 2) * 4 + (i % 2) * 2 + {0, 1}: four channels each
-        const int ks = (i / 2) * 4 + (i % 2) * 2;
-        if (NT == 1) {
-          qf[ks] = make_uint2(h[0], h[1]);
-          qf[ks + 1] = make_uint2(h[2], h[3]);
-        } else {
-          s.q[(nt * KS + ks) * 32 + lane] = make_uint2(h[0], h[1]);
-          s.q[(nt * KS + ks + 1) * 32 + lane] = make_uint2(h[2], h[3]);
-        }
-      }
-      if (NT == 1) {
-        c_row[0][0] = __shfl_sync(0xffffffffu, c, 8 * t);
-        c_row[0][1] = __shfl_sync(0xffffffffu, c, 8 * t + 4);
-      } else if (t == 0) {
-        s.c_row[r] = c;
-      }
-    }
-    if (NT > 1) {
-      __syncthreads();
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        c_row[nt][0] = s.c_row[nt * 8 + 2 * t];
-        c_row[nt][1] = s.c_row[nt * 8 + 2 * t + 1];
-      }
-    }
-
-    float m[NT][2], l[NT][2], acc[NT][MT][4];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      m[nt][0] = m[nt][1] = neg_inf();
-      l[nt][0] = l[nt][1] = 0.f;
-#pragma unroll
-      for (int j = 0; j < MT; ++j)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[nt][j][e] = 0.f;
-    }
-    float v_ref = 0.f, v_mul = 0.f;  // v_mul = 2^13 / v_ref
-
-    const int mine = (n_seg - warp + kWarps - 1) / kWarps;  // blocks kb0 + warp + i * kWarps
-    BlockInfo info = {0, 0x7fffffff, 1.f, 1.f};
+    Segment sg;
+    sg.set(p, walk, 8);
     uint4 kr[2][KC];
     uint32_t vr[4][VW];
-
     auto load_k = [&](long long off) {
       const uint8_t* base = static_cast<const uint8_t*>(p.k_cache) + off + g * D + t * 16;
 #pragma unroll
@@ -332,73 +356,314 @@ __global__ void __launch_bounds__(kThreads, Plan<NT>::kCtasPerSm)
         }
       }
     };
-    // P^T (B operand) times V^T, for the value words as they stand
-    auto add_pv = [&](const uint32_t (&pb)[NT][2]) {
-#pragma unroll
-      for (int j = 0; j < MT; ++j) {
-        const uint32_t sel = (j & 1) ? 0x7362u : 0x5140u;
-        const uint32_t lo = __byte_perm(vr[0][j >> 1], vr[1][j >> 1], sel);
-        const uint32_t hi = __byte_perm(vr[2][j >> 1], vr[3][j >> 1], sel);
-        const uint32_t a0 = e4m3x2_to_f16x2(lo), a1 = e4m3x2_to_f16x2(lo >> 16);
-        const uint32_t a2 = e4m3x2_to_f16x2(hi), a3 = e4m3x2_to_f16x2(hi >> 16);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          mma_f16(acc[nt][j], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+    const int mine = (sg.n_seg - warp + kWarps - 1) / kWarps;  // blocks warp + i * kWarps
+    BlockInfo info = look_up(p, sg, warp + lane * kWarps);
+    {  // the first block is on its way while the queries are prepared
+      const long long off = __shfl_sync(0xffffffffu, info.offset, 0);
+      if (mine > 0) {
+        load_k(off);
+        load_v(off);
       }
-    };
+    }
 
-    // A NaN value must reach the rows that see its key and no others (0 * NaN is
-    // NaN): the product of "code is NaN" and "row sees key" says where it goes, and
-    // the code becomes 0 for the product with the weights.
-    auto mark_nan = [&](uint32_t hidden) {
-      uint32_t see[NT][2];
+    uint2 qf[KS];
+    float c_row[2];
+    {
+      const float c = load_q<D>(p, sg.qrow0 + g, g < sg.n_rows, t,
+                                [&](int ks, uint2 v) { qf[ks] = v; });
+      c_row[0] = __shfl_sync(0xffffffffu, c, 8 * t);  // rows 2t and 2t + 1
+      c_row[1] = __shfl_sync(0xffffffffu, c, 8 * t + 4);
+    }
+    float m[2] = {kNoMax, kNoMax}, l[2] = {0.f, 0.f}, acc[MT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const uint32_t h = hidden >> (nt * 4);
-        see[nt][0] = transpose8x8(((h & 1u) ? 0u : 0x3c00u) | ((h & 2u) ? 0u : 0x3c000000u));
-        see[nt][1] = transpose8x8(((h & 4u) ? 0u : 0x3c00u) | ((h & 8u) ? 0u : 0x3c000000u));
-      }
+    for (int j = 0; j < MT; ++j)
 #pragma unroll
-      for (int j = 0; j < MT; ++j) {
-        const uint32_t sel = (j & 1) ? 0x7362u : 0x5140u;
-        uint32_t n[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r)  // 0x38 is e4m3's 1.0
-          n[r] = __vcmpeq4(vr[r][j >> 1] & 0x7f7f7f7fu, 0x7f7f7f7fu) & 0x38383838u;
-        const uint32_t lo = __byte_perm(n[0], n[1], sel), hi = __byte_perm(n[2], n[3], sel);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float c[4] = {0.f, 0.f, 0.f, 0.f};
-          mma_f16(c, e4m3x2_to_f16x2(lo), e4m3x2_to_f16x2(lo >> 16), e4m3x2_to_f16x2(hi),
-                  e4m3x2_to_f16x2(hi >> 16), see[nt][0], see[nt][1]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (c[e] > 0.f) acc[nt][j][e] = __int_as_float(0x7fffffff);
-        }
-      }
-#pragma unroll
-      for (int r = 0; r < 4; ++r)
-#pragma unroll
-        for (int w = 0; w < VW; ++w)
-          vr[r][w] &= ~__vcmpeq4(vr[r][w] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-    };
+      for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
+    float v_ref = 0.f, v_mul = 0.f;  // v_mul = 2^9 / v_ref
 
     for (int i = 0; i < mine; ++i) {
-      if ((i & 31) == 0) {  // the next 32 blocks of this warp, one per lane
-        const int kb = i + lane < mine ? kb0 + warp + (i + lane) * kWarps : -1;
-        if (kb >= 0) info = look_up(p, item, hk, len, table, kb, D);
+      const int src = i & 31;
+      if (src == 0 && i > 0) {  // the next 32 blocks of this warp, one per lane
+        info = look_up(p, sg, warp + (i + lane) * kWarps);
         const long long off = __shfl_sync(0xffffffffu, info.offset, 0);
         load_k(off);
         load_v(off);
       }
-      const int src = i & 31;
       const int pos = __shfl_sync(0xffffffffu, info.pos, src);
       const float ks = __shfl_sync(0xffffffffu, info.ks, src);
       const float vs = __shfl_sync(0xffffffffu, info.vs, src);
       const bool more = i + 1 < mine && src != 31;
       const long long next = __shfl_sync(0xffffffffu, info.offset, (src + 1) & 31);
 
-      // ---- S^T = K Q^T ----
+      // ---- S^T = K Q^T: {key g, row 2t}, {key g, row 2t+1}, {key g+8, ...} x 2 ----
+      float x[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < KC; ++c) {
+        const uint32_t wa[4] = {kr[0][c].x, kr[0][c].y, kr[0][c].z, kr[0][c].w};
+        const uint32_t wb[4] = {kr[1][c].x, kr[1][c].y, kr[1][c].z, kr[1][c].w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint2 q = qf[c * 4 + e];
+          mma_f16(x, e4m3x2_to_f16x2(wa[e]), e4m3x2_to_f16x2(wb[e]),
+                  e4m3x2_to_f16x2(wa[e] >> 16), e4m3x2_to_f16x2(wb[e] >> 16), q.x, q.y);
+        }
+      }
+      if (more) load_k(next);
+
+      // ---- weights against the running maximum ----
+      const bool edge = static_cast<long long>(pos) + kBlockKeys - 1 > sg.len - p.Sq;
+      float f[2] = {ks * c_row[0], ks * c_row[1]};
+      if (edge) {  // scores that are not seen become -inf
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          f[e & 1] = fmaxf(f[e & 1], 1.1754944e-38f);  // -inf * 0 would be NaN
+          const long long key = static_cast<long long>(pos) + g + (e >> 1) * 8;
+          if (key > sg.len - p.Sq + (sg.row0 + 2 * t + (e & 1)) % p.Sq) x[e] = neg_inf();
+        }
+      }
+      float arg[4];
+      bool over = vs > v_ref;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        arg[e] = fmaf(x[e], f[e & 1], -m[e & 1]);
+        over |= arg[e] > kLag;
+      }
+      if (__any_sync(0xffffffffu, over)) {
+        // exact maximum of the block's rows; the state moves to it
+        float v_down = 1.f;
+        if (vs > v_ref) {
+          v_down = v_ref / vs;  // 0 before the first block
+          v_ref = vs;
+          v_mul = kWeightUnit / vs;
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+          float mx = fmaxf(x[r] * f[r], x[2 + r] * f[r]);
+#pragma unroll
+          for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+          mx = fmaxf(m[r], mx);
+          const float a = ex2_approx(m[r] - mx);
+          m[r] = mx;
+          l[r] *= a;
+#pragma unroll
+          for (int j = 0; j < MT; ++j) {
+            acc[j][r] *= a * v_down;
+            acc[j][2 + r] *= a * v_down;
+          }
+          arg[r] = fmaf(x[r], f[r], -mx);
+          arg[2 + r] = fmaf(x[2 + r], f[r], -mx);
+        }
+      }
+      const float unit = vs * v_mul;
+      float w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        w[e] = ex2_approx(arg[e]);
+        l[e & 1] += w[e];
+        w[e] *= unit;
+      }
+      const uint32_t pb0 = transpose8x8(pack_f16x2(w[0], w[1]));
+      const uint32_t pb1 = transpose8x8(pack_f16x2(w[2], w[3]));
+
+      // ---- O^T += V^T P^T ----
+      if (edge) {
+        bool nan = false;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          const bool dead = static_cast<long long>(pos) + 2 * t + (r & 1) + (r >> 1) * 8 >= sg.len;
+#pragma unroll
+          for (int e = 0; e < VW; ++e) {
+            if (dead) vr[r][e] = 0u;  // what lies behind the last key may be anything
+            nan |= nan_codes(vr[r][e]) != 0;
+          }
+        }
+        if (p.Sq > 1 && __any_sync(0xffffffffu, nan)) {
+          // A NaN value must reach the rows that see its key and no others (0 * NaN is
+          // NaN): the product of "code is NaN" and "row sees key" says where it goes,
+          // and the code becomes 0 for the product with the weights.
+          const int last = sg.len - p.Sq + (sg.row0 + g) % p.Sq - pos - 2 * t;
+          const uint32_t see0 = (last >= 0 ? 0x3c00u : 0u) | (last >= 1 ? 0x3c000000u : 0u);
+          const uint32_t see1 = (last >= 8 ? 0x3c00u : 0u) | (last >= 9 ? 0x3c000000u : 0u);
+#pragma unroll
+          for (int j = 0; j < MT; ++j) {
+            const uint32_t sel = (j & 1) ? 0x7362u : 0x5140u;
+            uint32_t n[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) n[r] = nan_codes(vr[r][j >> 1]) & 0x38383838u;  // 1.0
+            const uint32_t lo = __byte_perm(n[0], n[1], sel), hi = __byte_perm(n[2], n[3], sel);
+            float c[4] = {0.f, 0.f, 0.f, 0.f};
+            mma_f16(c, e4m3x2_to_f16x2(lo), e4m3x2_to_f16x2(lo >> 16), e4m3x2_to_f16x2(hi),
+                    e4m3x2_to_f16x2(hi >> 16), see0, see1);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (c[e] > 0.f) acc[j][e] = __int_as_float(0x7fffffff);
+          }
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int e = 0; e < VW; ++e) vr[r][e] &= ~nan_codes(vr[r][e]);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < MT; ++j) {
+        const uint32_t sel = (j & 1) ? 0x7362u : 0x5140u;
+        const uint32_t lo = __byte_perm(vr[0][j >> 1], vr[1][j >> 1], sel);
+        const uint32_t hi = __byte_perm(vr[2][j >> 1], vr[3][j >> 1], sel);
+        mma_f16(acc[j], e4m3x2_to_f16x2(lo), e4m3x2_to_f16x2(lo >> 16), e4m3x2_to_f16x2(hi),
+                e4m3x2_to_f16x2(hi >> 16), pb0, pb1);
+      }
+      if (more) load_v(next);
+    }
+
+    // ---- merge the warps' states ----
+    const float back = v_ref * (1.f / kWeightUnit);
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      float sum = l[r];
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      const int row = 2 * t + r;
+      if (g == 0) {
+        s.m[warp][row] = m[r];
+        s.l[warp][row] = sum;
+      }
+#pragma unroll
+      for (int j = 0; j < MT; ++j)
+        *reinterpret_cast<float2*>(&s.o[warp][row][g * (D / 8) + 2 * j]) =
+            make_float2(acc[j][r] * back, acc[j][2 + r] * back);
+    }
+    __syncthreads();
+    for (int idx = tid; idx < sg.n_rows * (D / 4); idx += kThreads) {
+      const int row = idx / (D / 4), c = (idx % (D / 4)) * 4;
+      float M = kNoMax;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s.m[w][row]);
+      float L = 0.f;
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float wt = ex2_approx(s.m[w][row] - M);
+        const float4 v = *reinterpret_cast<const float4*>(&s.o[w][row][c]);
+        L = fmaf(wt, s.l[w][row], L);
+        o.x = fmaf(wt, v.x, o.x);
+        o.y = fmaf(wt, v.y, o.y);
+        o.z = fmaf(wt, v.z, o.z);
+        o.w = fmaf(wt, v.w, o.w);
+      }
+      emit<D>(p, sg, 8, row, c, M, L, o, part_o, part_ml);
+    }
+    __syncthreads();
+    walk.next(sg.n_seg, sg.n_kb);
+  }
+  griddep_launch_dependents();
+}
+
+// 9 to 32 query rows: the four warps work on the same four blocks (64 keys).  Each
+// computes the scores of one block for all rows; the weights go through shared
+// memory as B operands, and each warp adds its 32 channels of O^T (at d = 64 two
+// warps share 32 channels and take two of the blocks each).  So the accumulators
+// of a warp are 32 channels x 32 rows, a quarter of what a warp on its own would
+// hold (its 255 registers left 8 warps per SM: 68 us where this takes REPLACE).
+// The running maxima are the CTA's; the vote on moving them is the barrier that
+// hands the weights over.
+template <int D, int NT>
+struct WideSmem {
+  Line line;
+  float c_row[8 * NT];
+  float m[8 * NT];
+  float l[kWarps][8 * NT];
+  float mx[kWarps][8 * NT];
+  float vs[kWarps];
+  alignas(16) uint2 q[NT * (D / 16) * 32];
+  alignas(16) uint2 w[2][kWarps][NT][32];         // P^T of the four blocks, double buffered
+  alignas(16) float o[128 / D][8 * NT][D + 4];
+};
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, Plan<NT>::kCtasPerSm)
+    fa_decode_paged_wide(const PagedDecodeParams p, int row_blocks, float* part_o,
+                         float2* part_ml) {
+  constexpr int KC = D / 64;           // 16-byte pieces of a key row per lane
+  constexpr int KS = D / 16;           // k-steps of S
+  constexpr int DW = D / 32;           // warps side by side over the channels
+  constexpr int VB = DW;               // blocks whose values a warp multiplies
+  constexpr int R = 8 * NT;
+  extern __shared__ __align__(16) unsigned char smem_raw[];
+  WideSmem<D, NT>& s = *reinterpret_cast<WideSmem<D, NT>*>(smem_raw);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const int dw = warp % DW, vb0 = (warp / DW) * VB;  // channels [32 dw, ..), blocks [vb0, ..)
+
+  make_line(p, row_blocks, s.line);
+  Walk walk;
+  const bool any_work = walk.begin(p, row_blocks, s.line);
+  while (any_work && walk.at < walk.end) {
+    if (item_blocks(p, walk.item) == 0) {  // takes no place in the line
+      ++walk.item;
+      continue;
+    }
+    Segment sg;
+    sg.set(p, walk, R);
+    const int steps = (sg.n_seg + kWarps - 1) / kWarps;
+    uint4 kr[2][KC];
+    uint32_t vr[VB][4];
+    auto load_k = [&](long long off) {
+      const uint8_t* base = static_cast<const uint8_t*>(p.k_cache) + off + g * D + t * 16;
+#pragma unroll
+      for (int i = 0; i < KC; ++i) {
+        kr[0][i] = ld_stream16(base + i * 64);
+        kr[1][i] = ld_stream16(base + 8 * D + i * 64);
+      }
+    };
+    auto load_v = [&](int v, long long off) {
+      const uint8_t* base = static_cast<const uint8_t*>(p.v_cache) + off + 2 * t * D + dw * 32 + g * 4;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        vr[v][i] = __ldg(reinterpret_cast<const uint32_t*>(base + ((i & 1) + (i >> 1) * 8) * D));
+    };
+    // lane j of every warp looks block j of the coming 32 up, and of the 32 after them
+    BlockInfo info = look_up(p, sg, lane), ahead = look_up(p, sg, 32 + lane);
+    load_k(__shfl_sync(0xffffffffu, info.offset, warp));
+#pragma unroll
+    for (int v = 0; v < VB; ++v) load_v(v, __shfl_sync(0xffffffffu, info.offset, vb0 + v));
+
+    for (int nt = warp; nt < NT; nt += kWarps) {
+      const int r = nt * 8 + g;
+      const float c = load_q<D>(p, sg.qrow0 + r, r < sg.n_rows, t, [&](int ks, uint2 v) {
+        s.q[(nt * KS + ks) * 32 + lane] = v;
+      });
+      if (t == 0) s.c_row[r] = c;
+    }
+    __syncthreads();
+    float c_row[NT][2], m[NT][2], l[NT][2], acc[2][NT][4];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+      for (int r = 0; r < 2; ++r) {
+        c_row[nt][r] = s.c_row[nt * 8 + 2 * t + r];
+        m[nt][r] = kNoMax;
+        l[nt][r] = 0.f;
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[j][nt][e] = 0.f;
+    }
+    float v_ref = 0.f, v_mul = 0.f;
+
+    for (int i = 0; i < steps; ++i) {
+      const int src = (i & 7) * kWarps;  // this step's blocks are lanes src .. src + 3
+      if (src == 0 && i > 0) {
+        info = ahead;
+        ahead = look_up(p, sg, (i / 8 + 1) * 32 + lane);
+      }
+      const int pos = __shfl_sync(0xffffffffu, info.pos, src + warp);
+      const float ks = __shfl_sync(0xffffffffu, info.ks, src + warp);
+      const float vs = __shfl_sync(0xffffffffu, info.vs, src + warp);
+      const long long next = (i & 7) == 7 ? ahead.offset : info.offset;
+      const int next_src = (src + kWarps) & 31;
+
+      // ---- S^T = K Q^T of this warp's block ----
       float x[NT][4];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -414,105 +679,159 @@ __global__ void __launch_bounds__(kThreads, Plan<NT>::kCtasPerSm)
           const uint32_t a1 = e4m3x2_to_f16x2(wb[e]), a3 = e4m3x2_to_f16x2(wb[e] >> 16);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            const uint2 q = NT == 1 ? qf[NT == 1 ? c * 4 + e : 0] : s.q[(nt * KS + c * 4 + e) * 32 + lane];
+            const uint2 q = s.q[(nt * KS + c * 4 + e) * 32 + lane];
             mma_f16(x[nt], a0, a1, a2, a3, q.x, q.y);
           }
         }
       }
-      if (more) load_k(next);
+      load_k(__shfl_sync(0xffffffffu, next, next_src + warp));  // past the end: the cache's start
 
       // ---- weights against the running maximum ----
-      // x[nt]: {key g, row 2t}, {key g, row 2t+1}, {key g+8, row 2t}, {key g+8, row 2t+1}
-      const bool edge = static_cast<long long>(pos) + kBlockKeys - 1 > len - p.Sq;
-      float arg[NT][4];
-      bool over = vs > v_ref;
-      uint32_t hidden = 0;  // bit nt * 4 + e
-      if (edge) {
+      float f[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        f[nt][0] = ks * c_row[nt][0];
+        f[nt][1] = ks * c_row[nt][1];
+      }
+      if (static_cast<long long>(pos) + kBlockKeys - 1 > sg.len - p.Sq) {  // as in the narrow kernel
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int row = row0 + nt * 8 + 2 * t + (e & 1);
+            f[nt][e & 1] = fmaxf(f[nt][e & 1], 1.1754944e-38f);
             const long long key = static_cast<long long>(pos) + g + (e >> 1) * 8;
-            if (key > len - p.Sq + row % p.Sq) hidden |= 1u << (nt * 4 + e);
+            if (key > sg.len - p.Sq + (sg.row0 + nt * 8 + 2 * t + (e & 1)) % p.Sq)
+              x[nt][e] = neg_inf();
           }
       }
+      float ws[NT][2];
+      auto put_weights = [&] {
+        const float unit = vs * v_mul;
+        bool over = vs > v_ref;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+        for (int nt = 0; nt < NT; ++nt) {
+          float w[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float f = ks * c_row[nt][e & 1];
-          arg[nt][e] = fmaf(x[nt][e], f, -m[nt][e & 1]);
-          if (edge && (hidden >> (nt * 4 + e) & 1u)) arg[nt][e] = neg_inf();
-          over |= arg[nt][e] > kLag;
+          for (int e = 0; e < 4; ++e) {
+            const float arg = fmaf(x[nt][e], f[nt][e & 1], -m[nt][e & 1]);
+            over |= arg > kLag;
+            w[e] = ex2_approx(arg);
+          }
+          s.w[i & 1][warp][nt][lane] =
+              make_uint2(transpose8x8(pack_f16x2(w[0] * unit, w[1] * unit)),
+                         transpose8x8(pack_f16x2(w[2] * unit, w[3] * unit)));
+          ws[nt][0] = w[0] + w[2];
+          ws[nt][1] = w[1] + w[3];
         }
-      if (__any_sync(0xffffffffu, over)) {
-        // exact maximum of the block's rows; the state moves to it
-        float v_down = 1.f;
-        if (vs > v_ref) {
-          v_down = v_ref / vs;  // 0 before the first block
-          v_ref = vs;
-          v_mul = kWeightUnit / vs;
+        return over;
+      };
+      if (__syncthreads_or(put_weights())) {
+        // exact maximum of the four blocks' rows; the CTA's state moves to it
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            float mx = fmaxf(x[nt][r] * f[nt][r], x[nt][2 + r] * f[nt][r]);
+#pragma unroll
+            for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+            if (g == 0) s.mx[warp][nt * 8 + 2 * t + r] = mx;
+          }
+        if (lane == 0) s.vs[warp] = vs;
+        __syncthreads();
+        float top = 0.f, v_down = 1.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s.vs[w]);
+        if (top > v_ref) {
+          v_down = v_ref / top;  // 0 before the first block
+          v_ref = top;
+          v_mul = kWeightUnit / top;
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            const float f = ks * c_row[nt][r];
-            float mx = neg_inf();
-            if (!(hidden >> (nt * 4 + r) & 1u)) mx = x[nt][r] * f;
-            if (!(hidden >> (nt * 4 + 2 + r) & 1u)) mx = fmaxf(mx, x[nt][2 + r] * f);
+            float m_new = m[nt][r];
 #pragma unroll
-            for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            const float m_new = fmaxf(m[nt][r], mx);
-            const float a = m[nt][r] == neg_inf() ? 0.f : ex2_approx(m[nt][r] - m_new);
+            for (int w = 0; w < kWarps; ++w) m_new = fmaxf(m_new, s.mx[w][nt * 8 + 2 * t + r]);
+            const float a = ex2_approx(m[nt][r] - m_new);
             m[nt][r] = m_new;
             l[nt][r] *= a;
 #pragma unroll
-            for (int j = 0; j < MT; ++j) {
-              acc[nt][j][r] *= a * v_down;
-              acc[nt][j][2 + r] *= a * v_down;
+            for (int j = 0; j < 2; ++j) {
+              acc[j][nt][r] *= a * v_down;
+              acc[j][nt][2 + r] *= a * v_down;
             }
-#pragma unroll
-            for (int e = r; e < 4; e += 2)
-              arg[nt][e] = (hidden >> (nt * 4 + e) & 1u) ? neg_inf()
-                                                         : fmaf(x[nt][e], f, -m_new);
           }
+        put_weights();
+        __syncthreads();
       }
-      const float unit = vs * v_mul;
-      uint32_t pb[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float w[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          w[e] = ex2_approx(arg[nt][e]);
-          l[nt][e & 1] += w[e];
-          w[e] *= unit;
-        }
-        pb[nt][0] = transpose8x8(pack_f16x2(w[0], w[1]));
-        pb[nt][1] = transpose8x8(pack_f16x2(w[2], w[3]));
+        l[nt][0] += ws[nt][0];
+        l[nt][1] += ws[nt][1];
       }
 
-      // ---- O^T += V^T P^T ----
-      if (edge) {
-        bool nan = false;
+      // ---- O^T += V^T P^T, this warp's channels and blocks ----
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          const bool dead = static_cast<long long>(pos) + 2 * t + (r & 1) + (r >> 1) * 8 >= len;
+      for (int v = 0; v < VB; ++v) {
+        const int vpos = __shfl_sync(0xffffffffu, info.pos, src + vb0 + v);
+        if (static_cast<long long>(vpos) + kBlockKeys - 1 > sg.len - p.Sq) {
+          bool nan = false;
 #pragma unroll
-          for (int w = 0; w < VW; ++w) {
-            if (dead) vr[r][w] = 0u;  // what lies behind the last key may be anything
-            nan |= has_nan_code(vr[r][w]);
+          for (int r = 0; r < 4; ++r) {
+            // what lies behind the last key may be anything
+            if (static_cast<long long>(vpos) + 2 * t + (r & 1) + (r >> 1) * 8 >= sg.len) vr[v][r] = 0u;
+            nan |= nan_codes(vr[v][r]) != 0;
+          }
+          if (p.Sq > 1 && __any_sync(0xffffffffu, nan)) {
+            // NaN values go to the rows that see their keys, and to no others (as in
+            // the narrow kernel)
+            uint32_t n[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              n[r] = nan_codes(vr[v][r]) & 0x38383838u;
+              vr[v][r] &= ~nan_codes(vr[v][r]);
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const int last = sg.len - p.Sq + (sg.row0 + nt * 8 + g) % p.Sq - vpos - 2 * t;
+              const uint32_t see0 = (last >= 0 ? 0x3c00u : 0u) | (last >= 1 ? 0x3c000000u : 0u);
+              const uint32_t see1 = (last >= 8 ? 0x3c00u : 0u) | (last >= 9 ? 0x3c000000u : 0u);
+#pragma unroll
+              for (int j = 0; j < 2; ++j) {
+                const uint32_t sel = j ? 0x7362u : 0x5140u;
+                const uint32_t lo = __byte_perm(n[0], n[1], sel), hi = __byte_perm(n[2], n[3], sel);
+                float c[4] = {0.f, 0.f, 0.f, 0.f};
+                mma_f16(c, e4m3x2_to_f16x2(lo), e4m3x2_to_f16x2(lo >> 16), e4m3x2_to_f16x2(hi),
+                        e4m3x2_to_f16x2(hi >> 16), see0, see1);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (c[e] > 0.f) acc[j][nt][e] = __int_as_float(0x7fffffff);
+              }
+            }
           }
         }
-        if (p.Sq > 1 && __any_sync(0xffffffffu, nan)) mark_nan(hidden);
+        uint32_t a[2][4];
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint32_t sel = j ? 0x7362u : 0x5140u;
+          const uint32_t lo = __byte_perm(vr[v][0], vr[v][1], sel);
+          const uint32_t hi = __byte_perm(vr[v][2], vr[v][3], sel);
+          a[j][0] = e4m3x2_to_f16x2(lo), a[j][1] = e4m3x2_to_f16x2(lo >> 16);
+          a[j][2] = e4m3x2_to_f16x2(hi), a[j][3] = e4m3x2_to_f16x2(hi >> 16);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const uint2 w = s.w[i & 1][vb0 + v][nt][lane];
+          mma_f16(acc[0][nt], a[0][0], a[0][1], a[0][2], a[0][3], w.x, w.y);
+          mma_f16(acc[1][nt], a[1][0], a[1][1], a[1][2], a[1][3], w.x, w.y);
+        }
+        load_v(v, __shfl_sync(0xffffffffu, next, next_src + vb0 + v));
       }
-      add_pv(pb);
-      if (more) load_v(next);
     }
 
-    // ---- merge the warps' states ----
+    // ---- the CTA's state ----
+    const float back = v_ref * (1.f / kWeightUnit);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -522,57 +841,29 @@ __global__ void __launch_bounds__(kThreads, Plan<NT>::kCtasPerSm)
         for (int o = 4; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
         const int row = nt * 8 + 2 * t + r;
         if (g == 0) {
-          s.m[warp][row] = m[nt][r];
           s.l[warp][row] = sum;
+          if (warp == 0) s.m[row] = m[nt][r];
         }
-        const float back = v_ref * (1.f / kWeightUnit);
 #pragma unroll
-        for (int j = 0; j < MT; ++j)
-          *reinterpret_cast<float2*>(&s.o[warp][row][g * (D / 8) + 2 * j]) =
-              make_float2(acc[nt][j][r] * back, acc[nt][j][2 + r] * back);
+        for (int j = 0; j < 2; ++j)
+          *reinterpret_cast<float2*>(&s.o[warp / DW][row][dw * 32 + g * 4 + 2 * j]) =
+              make_float2(acc[j][nt][r] * back, acc[j][nt][2 + r] * back);
       }
     __syncthreads();
-    const bool whole = n_seg == n_kb;
-    const size_t slot = 2 * static_cast<size_t>(blockIdx.x) + (kb0 == 0 ? 1 : 0);
-    for (int idx = tid; idx < n_rows * (D / 4); idx += kThreads) {
+    for (int idx = tid; idx < sg.n_rows * (D / 4); idx += kThreads) {
       const int row = idx / (D / 4), c = (idx % (D / 4)) * 4;
-      float M = neg_inf();
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s.m[w][row]);
+      float4 o = *reinterpret_cast<const float4*>(&s.o[0][row][c]);
+      if constexpr (D == 64) {
+        const float4 u = *reinterpret_cast<const float4*>(&s.o[1][row][c]);
+        o = make_float4(o.x + u.x, o.y + u.y, o.z + u.z, o.w + u.w);
+      }
       float L = 0.f;
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float wt = s.m[w][row] == neg_inf() ? 0.f : ex2_approx(s.m[w][row] - M);
-        const float4 v = *reinterpret_cast<const float4*>(&s.o[w][row][c]);
-        // a warp without a visible key has l = 0 (or NaN, which has to stay)
-        L += wt == 0.f ? s.l[w][row] * 0.f : wt * s.l[w][row];
-        o.x = fmaf(wt, v.x, o.x);
-        o.y = fmaf(wt, v.y, o.y);
-        o.z = fmaf(wt, v.z, o.z);
-        o.w = fmaf(wt, v.w, o.w);
-      }
-      if (whole) {
-        const bool empty = L == 0.f;
-        const float inv = empty ? 0.f : 1.f / L;
-        uint2 w;
-        w.x = pack_bf16x2(o.x * inv, o.y * inv);
-        w.y = pack_bf16x2(o.z * inv, o.w * inv);
-        *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + (qrow0 + row) * D + c) = w;
-        if (p.lse && c == 0)
-          p.lse[qrow0 + row] = empty ? neg_inf() : (M + __log2f(L)) * 0.69314718055994530942f;
-      } else {
-        *reinterpret_cast<float4*>(part_o + (slot * R + row) * D + c) = o;
-        if (c == 0) part_ml[slot * R + row] = make_float2(M, L);
-      }
+      for (int w = 0; w < kWarps; ++w) L += s.l[w][row];
+      emit<D>(p, sg, R, row, c, s.m[row], L, o, part_o, part_ml);
     }
     __syncthreads();
-    at += n_seg;
-    in_item += n_seg;
-    if (in_item >= static_cast<long long>(n_kb) * row_blocks) {
-      ++item;
-      in_item = 0;
-    }
+    walk.next(sg.n_seg, sg.n_kb);
   }
   griddep_launch_dependents();
 }
@@ -612,17 +903,16 @@ __global__ void __launch_bounds__(kThreads)
   griddep_wait();
   if (c0 == c1) return;  // one CTA finished it
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  float M = neg_inf(), L = 0.f, o[E];
+  float M = kNoMax, L = 0.f, o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
   for (int c = c0 + warp; c <= c1; c += kWarps) {
     const size_t at = (2 * static_cast<size_t>(c) + (c == c0 ? 1 : 0)) * tile_rows + r;
     const float2 ml = part_ml[at];
     const float m_new = fmaxf(M, ml.x);
-    const float a = M == neg_inf() ? 0.f : ex2_approx(M - m_new);
-    const float w = ml.x == neg_inf() ? 0.f : ex2_approx(ml.x - m_new);
+    const float a = ex2_approx(M - m_new), w = ex2_approx(ml.x - m_new);
     M = m_new;
-    L = L * a + (w == 0.f ? ml.y * 0.f : w * ml.y);
+    L = L * a + w * ml.y;
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = fmaf(w, part_o[at * D + lane * E + e], o[e] * a);
   }
@@ -634,12 +924,12 @@ __global__ void __launch_bounds__(kThreads)
   for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = o[e];
   __syncthreads();
   for (int c = threadIdx.x; c < D; c += kThreads) {
-    M = neg_inf();
+    M = kNoMax;
     for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w]);
     float sum = 0.f, v = 0.f;
     for (int w = 0; w < kWarps; ++w) {
-      const float wt = s_m[w] == neg_inf() ? 0.f : ex2_approx(s_m[w] - M);
-      sum += wt == 0.f ? s_l[w] * 0.f : wt * s_l[w];
+      const float wt = ex2_approx(s_m[w] - M);
+      sum = fmaf(wt, s_l[w], sum);
       v = fmaf(wt, s_o[w][c], v);
     }
     const bool empty = sum == 0.f;
@@ -651,11 +941,8 @@ __global__ void __launch_bounds__(kThreads)
 
 template <int D, int NT>
 cudaError_t launch_nt(const PagedDecodeParams& p, cudaStream_t stream) {
-  const size_t smem = sizeof(DecodeSmem<D, NT>);
-  cudaError_t e = cudaFuncSetAttribute(fa_decode_paged_kernel<D, NT>,
-                                       cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
-  if (e != cudaSuccess) return e;
+  constexpr size_t smem = NT == 1 ? sizeof(NarrowSmem<D>) : sizeof(WideSmem<D, NT == 1 ? 2 : NT>);
+  static_assert(smem <= 48 * 1024, "fits without an opt-in");
   const int row_blocks = (p.rows + 8 * NT - 1) / (8 * NT);
   // no more CTAs than there can be shares
   const long long list = p.sel ? p.max_sel : p.max_blocks;
@@ -665,9 +952,12 @@ cudaError_t launch_nt(const PagedDecodeParams& p, cudaStream_t stream) {
   float* part_o = static_cast<float*>(p.workspace);
   float2* part_ml = reinterpret_cast<float2*>(part_o + 2 * static_cast<size_t>(ctas) * 8 * NT * D);
   hook_before(stream);
-  fa_decode_paged_kernel<D, NT><<<ctas, kThreads, smem, stream>>>(p, row_blocks, part_o, part_ml);
+  if constexpr (NT == 1)
+    fa_decode_paged_narrow<D><<<ctas, kThreads, smem, stream>>>(p, row_blocks, part_o, part_ml);
+  else
+    fa_decode_paged_wide<D, NT><<<ctas, kThreads, smem, stream>>>(p, row_blocks, part_o, part_ml);
   hook_after(stream);
-  e = cudaGetLastError();
+  const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   return launch_dependent(fa_decode_paged_merge<D>, dim3(p.rows, p.B * p.s.Hkv), dim3(kThreads), 0,
                           stream, p, row_blocks, 8 * NT, ctas, static_cast<const float*>(part_o),

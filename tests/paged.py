@@ -68,15 +68,15 @@ def attention_bounds(ref_o, ref_lse, spread, size, v_top, n_keys, d):
     (half a step: 2^-8).  The LSE sees the score's error, the sum's and its own
     rounding to fp32.
 
-    A weight is stored in f16 as w * 2^13 * (its page's V scale / the largest one):
-    below f16's normal range its rounding is at most 2^-25 there, 2^-38 of the
-    largest weight and V scale, so each key adds at most 2^-38 * v_top (the
-    normaliser is at least 1: the key that set the running maximum counts 1)."""
+    A weight is stored in f16 as w * 2^9 * (its page's V scale / the largest one): below
+    f16's normal range its rounding is at most 2^-25 there, 2^-34 of the largest
+    weight and V scale, so each key adds at most 2^-34 * v_top (the normaliser is at
+    least 1: the key that set the running maximum counts 1)."""
     eps = 2.0 ** -24
     score = (d + 4) * eps * size
     rel = 2 * score + 2.0 ** -11 + 2.0 ** -21 + n_keys * eps
     tol_o = 2.0 ** -8 * np.abs(ref_o) + rel[..., None] * spread * (1 + 2.0 ** -8) + (
-        n_keys * 2.0 ** -38 * v_top[..., None])
+        n_keys * 2.0 ** -34 * v_top[..., None])
     tol_lse = score + (n_keys + 8) * eps + 2.0 ** -21 + 4 * eps * np.abs(
         np.where(np.isfinite(ref_lse), ref_lse, 0.0))
     return tol_o, tol_lse
