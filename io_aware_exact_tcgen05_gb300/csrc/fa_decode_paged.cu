@@ -138,27 +138,36 @@ __device__ __forceinline__ void make_line(const PagedDecodeParams& p, int row_bl
   __syncthreads();
 }
 
-__device__ __forceinline__ long long share_of(long long total, int ctas) {
+// Blocks per CTA.  At least 8, so that a short request is not cut into pieces
+// that cost more to join than to read, but no more than an item has on average:
+// a segment has a fixed cost of some microseconds, so CTAs should not queue up
+// tiny ones (208 items of one block: REPLACE3).
+__device__ __forceinline__ long long share_of(long long total, int items, int ctas) {
   const long long even = (total + ctas - 1) / ctas;
-  if (even <= kMinShare) return kMinShare;
-  // whole multiples of 16 leave fewer stretches that straddle two items
-  return even <= 16 ? even : (even + 15) / 16 * 16;
+  const long long least = min(static_cast<long long>(kMinShare), max(total / items, 1ll));
+  if (even <= 16) return max(even, least);
+  return (even + 15) / 16 * 16;  // fewer stretches that straddle two items
 }
 
-// A CTA's place in the line: it walks its stretch segment by segment, a segment
-// being blocks [kb0, kb0 + n_seg) of one item (request, KV head) and row block.
-struct Walk {
-  long long at, end, in_item;
-  int item, row_blocks;
+// A CTA walks its stretch of the line segment by segment: blocks [kb0, kb0 + n_seg)
+// of one item (request, KV head) and row block.  One thread keeps the place, in
+// shared memory, so that it takes no registers in the main loop.
+struct Segment {
+  long long at, end, in_item;  // place in the line, the stretch's end, place in the item
+  size_t qrow0;
+  const int32_t* table;
+  int item, hk, len, n_kb, kb0, n_seg, row0, n_rows;
+  bool live;
 
-  __device__ __forceinline__ bool begin(const PagedDecodeParams& p, int rbs, const Line& line) {
-    row_blocks = rbs;
+  __device__ __forceinline__ void begin(const PagedDecodeParams& p, int row_blocks, int tile_rows,
+                                        const Line& line) {
     const int items = p.B * p.s.Hkv;
     const long long total = line.prefix[kThreads];
-    const long long share = share_of(total, gridDim.x);
+    const long long share = share_of(total, items, gridDim.x);
     at = share * blockIdx.x;
     end = min(at + share, total);
-    if (at >= end) return false;
+    live = at < end;
+    if (!live) return;
     int a = 0, z = kThreads;
     while (z - a > 1) {
       const int mid = (a + z) >> 1;
@@ -166,38 +175,27 @@ struct Walk {
     }
     item = a * ((items + kThreads - 1) / kThreads);
     in_item = at - line.prefix[a];
-    while (true) {
-      const long long w = static_cast<long long>(item_blocks(p, item)) * row_blocks;
-      if (in_item < w) break;
-      in_item -= w;
-      ++item;
-    }
-    return true;
+    find(p, row_blocks, tile_rows);
   }
-  __device__ __forceinline__ void next(int n_seg, int n_kb) {
+  __device__ __forceinline__ void next(const PagedDecodeParams& p, int row_blocks, int tile_rows) {
     at += n_seg;
     in_item += n_seg;
-    if (in_item >= static_cast<long long>(n_kb) * row_blocks) {
-      ++item;
-      in_item = 0;
-    }
+    live = at < end;
+    if (live) find(p, row_blocks, tile_rows);
   }
-};
-
-struct Segment {
-  int item, b, hk, len, n_kb, kb0, n_seg, row0, n_rows;
-  const int32_t* table;
-  size_t qrow0;
-
-  __device__ __forceinline__ void set(const PagedDecodeParams& p, const Walk& w, int tile_rows) {
-    item = w.item;
+  // from (item, in_item), which may lie behind the item's end
+  __device__ __forceinline__ void find(const PagedDecodeParams& p, int row_blocks, int tile_rows) {
     n_kb = item_blocks(p, item);
-    kb0 = static_cast<int>(w.in_item % n_kb);
-    n_seg = static_cast<int>(min(static_cast<long long>(n_kb - kb0), w.end - w.at));
-    b = item / p.s.Hkv;
+    while (in_item >= static_cast<long long>(n_kb) * row_blocks) {
+      in_item -= static_cast<long long>(n_kb) * row_blocks;
+      n_kb = item_blocks(p, ++item);
+    }
+    kb0 = static_cast<int>(in_item % n_kb);
+    n_seg = static_cast<int>(min(static_cast<long long>(n_kb - kb0), end - at));
+    const int b = item / p.s.Hkv;
     hk = item % p.s.Hkv;
     len = request_len(p, b);
-    row0 = static_cast<int>(w.in_item / n_kb) * tile_rows;
+    row0 = static_cast<int>(in_item / n_kb) * tile_rows;
     n_rows = min(tile_rows, p.rows - row0);
     table = p.block_table + static_cast<size_t>(b) * p.max_blocks;
     qrow0 = static_cast<size_t>(item) * p.rows + row0;
@@ -207,6 +205,7 @@ struct Segment {
 template <int D>
 struct NarrowSmem {
   Line line;
+  Segment seg;
   float m[kWarps][8];
   float l[kWarps][8];
   alignas(16) float o[kWarps][8][D + 4];
@@ -323,15 +322,10 @@ __global__ void __launch_bounds__(kThreads, Plan<1>::kCtasPerSm)
   const int g = lane >> 2, t = lane & 3;
 
   make_line(p, row_blocks, s.line);
-  Walk walk;
-  const bool any_work = walk.begin(p, row_blocks, s.line);
-  while (any_work && walk.at < walk.end) {
-    if (item_blocks(p, walk.item) == 0) {  // takes no place in the line
-      ++walk.item;
-      continue;
-    }
-    Segment sg;
-    sg.set(p, walk, 8);
+  const Segment& sg = s.seg;
+  if (tid == 0) s.seg.begin(p, row_blocks, 8, s.line);
+  __syncthreads();
+  while (sg.live) {
     uint4 kr[2][KC];
     uint32_t vr[4][VW];
     auto load_k = [&](long long off) {
@@ -405,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, Plan<1>::kCtasPerSm)
         for (int e = 0; e < 4; ++e) {
           const uint2 q = qf[c * 4 + e];
           mma_f16(x, e4m3x2_to_f16x2(wa[e]), e4m3x2_to_f16x2(wb[e]),
-                  e4m3x2_to_f16x2(wa[e] >> 16), e4m3x2_to_f16x2(wb[e] >> 16), q.x, q.y);
+                  e4m3x2_hi_to_f16x2(wa[e]), e4m3x2_hi_to_f16x2(wb[e]), q.x, q.y);
         }
       }
       if (more) load_k(next);
@@ -492,8 +486,8 @@ __global__ void __launch_bounds__(kThreads, Plan<1>::kCtasPerSm)
             for (int r = 0; r < 4; ++r) n[r] = nan_codes(vr[r][j >> 1]) & 0x38383838u;  // 1.0
             const uint32_t lo = __byte_perm(n[0], n[1], sel), hi = __byte_perm(n[2], n[3], sel);
             float c[4] = {0.f, 0.f, 0.f, 0.f};
-            mma_f16(c, e4m3x2_to_f16x2(lo), e4m3x2_to_f16x2(lo >> 16), e4m3x2_to_f16x2(hi),
-                    e4m3x2_to_f16x2(hi >> 16), see0, see1);
+            mma_f16(c, e4m3x2_to_f16x2(lo), e4m3x2_hi_to_f16x2(lo), e4m3x2_to_f16x2(hi),
+                    e4m3x2_hi_to_f16x2(hi), see0, see1);
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               if (c[e] > 0.f) acc[j][e] = __int_as_float(0x7fffffff);
@@ -509,8 +503,8 @@ __global__ void __launch_bounds__(kThreads, Plan<1>::kCtasPerSm)
         const uint32_t sel = (j & 1) ? 0x7362u : 0x5140u;
         const uint32_t lo = __byte_perm(vr[0][j >> 1], vr[1][j >> 1], sel);
         const uint32_t hi = __byte_perm(vr[2][j >> 1], vr[3][j >> 1], sel);
-        mma_f16(acc[j], e4m3x2_to_f16x2(lo), e4m3x2_to_f16x2(lo >> 16), e4m3x2_to_f16x2(hi),
-                e4m3x2_to_f16x2(hi >> 16), pb0, pb1);
+        mma_f16(acc[j], e4m3x2_to_f16x2(lo), e4m3x2_hi_to_f16x2(lo), e4m3x2_to_f16x2(hi),
+                e4m3x2_hi_to_f16x2(hi), pb0, pb1);
       }
       if (more) load_v(next);
     }
@@ -553,7 +547,8 @@ __global__ void __launch_bounds__(kThreads, Plan<1>::kCtasPerSm)
       emit<D>(p, sg, 8, row, c, M, L, o, part_o, part_ml);
     }
     __syncthreads();
-    walk.next(sg.n_seg, sg.n_kb);
+    if (tid == 0) s.seg.next(p, row_blocks, 8);
+    __syncthreads();
   }
   griddep_launch_dependents();
 }
@@ -569,6 +564,7 @@ __global__ void __launch_bounds__(kThreads, Plan<1>::kCtasPerSm)
 template <int D, int NT>
 struct WideSmem {
   Line line;
+  Segment seg;
   float c_row[8 * NT];
   float m[8 * NT];
   float l[kWarps][8 * NT];
@@ -595,15 +591,10 @@ __global__ void __launch_bounds__(kThreads, Plan<NT>::kCtasPerSm)
   const int dw = warp % DW, vb0 = (warp / DW) * VB;  // channels [32 dw, ..), blocks [vb0, ..)
 
   make_line(p, row_blocks, s.line);
-  Walk walk;
-  const bool any_work = walk.begin(p, row_blocks, s.line);
-  while (any_work && walk.at < walk.end) {
-    if (item_blocks(p, walk.item) == 0) {  // takes no place in the line
-      ++walk.item;
-      continue;
-    }
-    Segment sg;
-    sg.set(p, walk, R);
+  const Segment& sg = s.seg;
+  if (tid == 0) s.seg.begin(p, row_blocks, R, s.line);
+  __syncthreads();
+  while (sg.live) {
     const int steps = (sg.n_seg + kWarps - 1) / kWarps;
     uint4 kr[2][KC];
     uint32_t vr[VB][4];
@@ -675,8 +666,8 @@ __global__ void __launch_bounds__(kThreads, Plan<NT>::kCtasPerSm)
         const uint32_t wb[4] = {kr[1][c].x, kr[1][c].y, kr[1][c].z, kr[1][c].w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const uint32_t a0 = e4m3x2_to_f16x2(wa[e]), a2 = e4m3x2_to_f16x2(wa[e] >> 16);
-          const uint32_t a1 = e4m3x2_to_f16x2(wb[e]), a3 = e4m3x2_to_f16x2(wb[e] >> 16);
+          const uint32_t a0 = e4m3x2_to_f16x2(wa[e]), a2 = e4m3x2_hi_to_f16x2(wa[e]);
+          const uint32_t a1 = e4m3x2_to_f16x2(wb[e]), a3 = e4m3x2_hi_to_f16x2(wb[e]);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             const uint2 q = s.q[(nt * KS + c * 4 + e) * 32 + lane];
@@ -802,8 +793,8 @@ __global__ void __launch_bounds__(kThreads, Plan<NT>::kCtasPerSm)
                 const uint32_t sel = j ? 0x7362u : 0x5140u;
                 const uint32_t lo = __byte_perm(n[0], n[1], sel), hi = __byte_perm(n[2], n[3], sel);
                 float c[4] = {0.f, 0.f, 0.f, 0.f};
-                mma_f16(c, e4m3x2_to_f16x2(lo), e4m3x2_to_f16x2(lo >> 16), e4m3x2_to_f16x2(hi),
-                        e4m3x2_to_f16x2(hi >> 16), see0, see1);
+                mma_f16(c, e4m3x2_to_f16x2(lo), e4m3x2_hi_to_f16x2(lo), e4m3x2_to_f16x2(hi),
+                        e4m3x2_hi_to_f16x2(hi), see0, see1);
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                   if (c[e] > 0.f) acc[j][nt][e] = __int_as_float(0x7fffffff);
@@ -817,8 +808,8 @@ __global__ void __launch_bounds__(kThreads, Plan<NT>::kCtasPerSm)
           const uint32_t sel = j ? 0x7362u : 0x5140u;
           const uint32_t lo = __byte_perm(vr[v][0], vr[v][1], sel);
           const uint32_t hi = __byte_perm(vr[v][2], vr[v][3], sel);
-          a[j][0] = e4m3x2_to_f16x2(lo), a[j][1] = e4m3x2_to_f16x2(lo >> 16);
-          a[j][2] = e4m3x2_to_f16x2(hi), a[j][3] = e4m3x2_to_f16x2(hi >> 16);
+          a[j][0] = e4m3x2_to_f16x2(lo), a[j][1] = e4m3x2_hi_to_f16x2(lo);
+          a[j][2] = e4m3x2_to_f16x2(hi), a[j][3] = e4m3x2_hi_to_f16x2(hi);
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -863,7 +854,8 @@ __global__ void __launch_bounds__(kThreads, Plan<NT>::kCtasPerSm)
       emit<D>(p, sg, R, row, c, s.m[row], L, o, part_o, part_ml);
     }
     __syncthreads();
-    walk.next(sg.n_seg, sg.n_kb);
+    if (tid == 0) s.seg.next(p, row_blocks, R);
+    __syncthreads();
   }
   griddep_launch_dependents();
 }
@@ -895,7 +887,7 @@ __global__ void __launch_bounds__(kThreads)
   for (int i = item / per * per; i < item; ++i)
     start += static_cast<long long>(item_blocks(p, i)) * row_blocks;
   start += static_cast<long long>(rb) * n_kb;
-  const long long share = share_of(line.prefix[kThreads], ctas);
+  const long long share = share_of(line.prefix[kThreads], items, ctas);
   const int c0 = static_cast<int>(start / share);
   const int c1 = static_cast<int>((start + n_kb - 1) / share);
   // Every CTA waits, also one with nothing to join: what follows this kernel in
@@ -947,8 +939,7 @@ cudaError_t launch_nt(const PagedDecodeParams& p, cudaStream_t stream) {
   // no more CTAs than there can be shares
   const long long list = p.sel ? p.max_sel : p.max_blocks;
   const long long most = list * (p.s.page_size / kBlockKeys) * p.B * p.s.Hkv * row_blocks;
-  const int ctas = static_cast<int>(min(static_cast<long long>(kSms * Plan<NT>::kCtasPerSm),
-                                        (most + kMinShare - 1) / kMinShare));
+  const int ctas = static_cast<int>(min(static_cast<long long>(kSms * Plan<NT>::kCtasPerSm), most));
   float* part_o = static_cast<float*>(p.workspace);
   float2* part_ml = reinterpret_cast<float2*>(part_o + 2 * static_cast<size_t>(ctas) * 8 * NT * D);
   hook_before(stream);

@@ -11,6 +11,7 @@
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 
+#include "fa_internal.h"
 #include "fa_kv.h"
 #include "fa_kv_device.cuh"
 
@@ -21,6 +22,8 @@ constexpr int kScoreThreads = 256;
 constexpr int kScoreBlocks = 64;  // cache blocks per CTA
 constexpr int kRowTile = 16;      // query rows quantised into shared memory at a time
 constexpr int kSelectThreads = 512;
+constexpr int kSelectWarps = kSelectThreads / 32;
+constexpr int kKeysPerThread = 16;  // up to 8192 blocks live in registers
 
 // Order-preserving map of a score to an unsigned key; NaN ranks lowest.
 __device__ __forceinline__ uint32_t score_key(float s) {
@@ -74,15 +77,31 @@ __global__ void __launch_bounds__(kScoreThreads) fa_block_score_kernel(const Sel
   const int b = item / p.s.Hkv, hk = item % p.s.Hkv;
   const int n = request_blocks(p, b);
   const int first = blockIdx.x * kScoreBlocks;
-  if (first >= n) return;
+  if (first >= n) {
+    griddep_launch_dependents();
+    return;
+  }
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int part = lane % LPB, sub = lane / LPB;
   const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) +
                            static_cast<size_t>(item) * p.rows * D;
   constexpr int PER = kScoreBlocks / (WARPS * BPW);
-  float best[PER];
+  // the bounds of all blocks of this warp are on their way while q is quantised
+  float best[PER], ks[PER];
+  int4 w[PER];
 #pragma unroll
-  for (int i = 0; i < PER; ++i) best[i] = __int_as_float(0xff800000);
+  for (int i = 0; i < PER; ++i) {
+    const int blk = first + (i * WARPS + warp) * BPW + sub;
+    const int page = blk < n ? p.block_table[static_cast<size_t>(b) * p.max_blocks + blk] : -1;
+    best[i] = __int_as_float(0xff800000);
+    ks[i] = -1.f;  // no page
+    w[i] = make_int4(0, 0, 0, 0);
+    if (page >= 0 && page < p.s.num_pages) {
+      const size_t tile = static_cast<size_t>(page) * p.s.Hkv + hk;
+      w[i] = __ldg(reinterpret_cast<const int4*>(p.k_bounds + tile * 2 * D + part * 16));
+      ks[i] = p.k_scale[tile];
+    }
+  }
   for (int r0 = 0; r0 < p.rows; r0 += kRowTile) {
     const int rows = min(kRowTile, p.rows - r0);
     __syncthreads();
@@ -91,25 +110,17 @@ __global__ void __launch_bounds__(kScoreThreads) fa_block_score_kernel(const Sel
       if (lane == 0) s_scale[r] = pow2i(e + 2);
     }
     __syncthreads();
+    for (int r = 0; r < rows; ++r) {
+      const int4 a = *reinterpret_cast<const int4*>(&s_q[r][part * 16]);
+      const float scale = s_scale[r];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) {
-      const int blk = first + (i * WARPS + warp) * BPW + sub;
-      const int page = blk < n ? p.block_table[static_cast<size_t>(b) * p.max_blocks + blk] : -1;
-      const bool ok = page >= 0 && page < p.s.num_pages;
-      int4 w = make_int4(0, 0, 0, 0);
-      float ks = 0.f;
-      if (ok) {
-        const size_t tile = static_cast<size_t>(page) * p.s.Hkv + hk;
-        w = *reinterpret_cast<const int4*>(p.k_bounds + tile * 2 * D + part * 16);
-        ks = p.k_scale[tile];
-      }
-      for (int r = 0; r < rows; ++r) {
-        const int4 a = *reinterpret_cast<const int4*>(&s_q[r][part * 16]);
-        int u = __dp4a(a.x, w.x, __dp4a(a.y, w.y, __dp4a(a.z, w.z, __dp4a(a.w, w.w, 0))));
+      for (int i = 0; i < PER; ++i) {
+        int u = __dp4a(a.x, w[i].x,
+                       __dp4a(a.y, w[i].y, __dp4a(a.z, w[i].z, __dp4a(a.w, w[i].w, 0))));
 #pragma unroll
         for (int o = 1; o < LPB; o <<= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
-        const float s = static_cast<float>(u) * ks * s_scale[r];
-        if (ok && (s > best[i] || s != s)) best[i] = s;
+        const float s = static_cast<float>(u) * ks[i] * scale;
+        if (s > best[i] || s != s) best[i] = s;
       }
     }
   }
@@ -119,77 +130,133 @@ __global__ void __launch_bounds__(kScoreThreads) fa_block_score_kernel(const Sel
     if (part == 0 && blk < n) {
       const bool forced = blk < p.n_first || blk >= n - p.n_last;
       p.keys[static_cast<size_t>(item) * p.max_blocks + blk] =
-          forced ? 0xffffffffu : score_key(best[i]);
+          forced ? 0xffffffffu : ks[i] < 0.f ? score_key(__int_as_float(0xff800000)) : score_key(best[i]);
     }
   }
+  griddep_launch_dependents();
 }
 
 // The k = min(k_blocks, n) blocks with the largest keys of one (request, KV
-// head), ascending; equal keys by the lower index.  The k-th largest key T is
-// found bit by bit (the largest T with at least k keys >= T); the blocks above T
-// and the first of those equal to T are then written in order.
-__global__ void __launch_bounds__(kSelectThreads) fa_block_select_kernel(const SelectParams p) {
-  __shared__ int s_count;
-  __shared__ int s_warp[2][kSelectThreads / 32];
-  const int item = blockIdx.x;
-  const int b = item / p.s.Hkv;
-  const int n = request_blocks(p, b);
-  const int k = min(p.k_blocks, n);
-  const uint32_t* keys = p.keys + static_cast<size_t>(item) * p.max_blocks;
-  int32_t* out = p.sel + static_cast<size_t>(item) * p.k_blocks;
+// head), ascending; equal keys by the lower index.  The k-th largest key T (the
+// largest T with at least k keys >= T) is found two bits at a time: each step
+// counts the keys at three candidates and costs one barrier.  The blocks above T and
+// the first of those equal to T are then written in order.  One CTA per item;
+// latency bounds it, so the keys stay in registers (thread t holds blocks t, t +
+// 512, ...) unless there are more than 8192 of them.
+template <bool kInRegs>
+__device__ __forceinline__ void select_blocks(const SelectParams& p, int item, int n, int k,
+                                              const uint32_t* keys) {
+  __shared__ int s_count[2][3][kSelectWarps];
+  __shared__ int s_warp[2][2][kSelectWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (tid == 0) p.n_sel[item] = k;
-  for (int i = k + tid; i < p.k_blocks; i += kSelectThreads) out[i] = -1;
-  if (k == 0) return;
-  uint32_t T = 0;
-  for (int bit = 31; bit >= 0; --bit) {
-    const uint32_t cand = T | (1u << bit);
-    int c = 0;
-    for (int i = tid; i < n; i += kSelectThreads) c += keys[i] >= cand;
-    c = __reduce_add_sync(0xffffffffu, c);
-    __syncthreads();
-    if (tid == 0) s_count = 0;
-    __syncthreads();
-    if (lane == 0) atomicAdd(&s_count, c);
-    __syncthreads();
-    if (s_count >= k) T = cand;
-  }
-  // thread t owns blocks [t * per, (t + 1) * per)
-  const int per = (n + kSelectThreads - 1) / kSelectThreads;
-  const int lo = min(tid * per, n), hi = min(lo + per, n);
-  int above = 0, equal = 0;
-  for (int i = lo; i < hi; ++i) {
-    above += keys[i] > T;
-    equal += keys[i] == T;
-  }
-  int ia = above, ie = equal;
+  int32_t* out = p.sel + static_cast<size_t>(item) * p.k_blocks;
+  const int rounds = (n + kSelectThreads - 1) / kSelectThreads;
+  uint32_t mine[kInRegs ? kKeysPerThread : 1];
+  if (kInRegs) {
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int a = __shfl_up_sync(0xffffffffu, ia, o), e = __shfl_up_sync(0xffffffffu, ie, o);
-    if (lane >= o) {
-      ia += a;
-      ie += e;
+    for (int i = 0; i < kKeysPerThread; ++i) {
+      const int at = i * kSelectThreads + tid;
+      mine[i] = at < n ? keys[at] : 0u;  // 0 is below every candidate
     }
   }
-  if (lane == 31) {
-    s_warp[0][warp] = ia;
-    s_warp[1][warp] = ie;
+  uint32_t T = 0;
+  for (int bit = 30; bit >= 0; bit -= 2) {
+    int c1 = 0, c2 = 0, c3 = 0;
+    const uint32_t t1 = T | 1u << bit, t2 = T | 2u << bit, t3 = T | 3u << bit;
+    if (kInRegs) {
+#pragma unroll
+      for (int i = 0; i < kKeysPerThread; ++i) {
+        if (i < rounds) {
+          c1 += mine[i] >= t1;
+          c2 += mine[i] >= t2;
+          c3 += mine[i] >= t3;
+        }
+      }
+    } else {
+      for (int at = tid; at < n; at += kSelectThreads) {
+        const uint32_t key = keys[at];
+        c1 += key >= t1;
+        c2 += key >= t2;
+        c3 += key >= t3;
+      }
+    }
+    c1 = __reduce_add_sync(0xffffffffu, c1);
+    c2 = __reduce_add_sync(0xffffffffu, c2);
+    c3 = __reduce_add_sync(0xffffffffu, c3);
+    const int turn = bit >> 1 & 1;  // two buffers: one barrier a step is enough
+    if (lane == 0) {
+      s_count[turn][0][warp] = c1;
+      s_count[turn][1][warp] = c2;
+      s_count[turn][2][warp] = c3;
+    }
+    __syncthreads();
+    int x = lane < kSelectWarps ? s_count[turn][0][lane] : 0;
+    int y = lane < kSelectWarps ? s_count[turn][1][lane] : 0;
+    int z = lane < kSelectWarps ? s_count[turn][2][lane] : 0;
+    x = __reduce_add_sync(0xffffffffu, x);
+    y = __reduce_add_sync(0xffffffffu, y);
+    z = __reduce_add_sync(0xffffffffu, z);
+    T = z >= k ? t3 : y >= k ? t2 : x >= k ? t1 : T;
   }
+  // keys above T over the whole item, then the order inside it, 512 blocks at a time
+  int above = 0;
+  if (kInRegs) {
+#pragma unroll
+    for (int i = 0; i < kKeysPerThread; ++i)
+      if (i < rounds) above += mine[i] > T;
+  } else {
+    for (int at = tid; at < n; at += kSelectThreads) above += keys[at] > T;
+  }
+  above = __reduce_add_sync(0xffffffffu, above);
+  if (lane == 0) s_count[1][0][warp] = above;  // last read before the last step's barrier
   __syncthreads();
-  int before_a = ia - above, before_e = ie - equal, total_a = 0;
-  for (int w = 0; w < kSelectThreads / 32; ++w) {
-    if (w < warp) {
-      before_a += s_warp[0][w];
-      before_e += s_warp[1][w];
+  above = __reduce_add_sync(0xffffffffu, lane < kSelectWarps ? s_count[1][0][lane] : 0);
+  int ties = k - above;  // blocks equal to T still to be taken
+  int base = 0;
+  for (int i = 0; i < rounds; ++i) {
+    const int at = i * kSelectThreads + tid;
+    uint32_t key = 0;
+    if (kInRegs) {
+#pragma unroll
+      for (int j = 0; j < kKeysPerThread; ++j)
+        if (j == i) key = mine[j];
+    } else if (at < n) {
+      key = keys[at];
     }
-    total_a += s_warp[0][w];
+    const uint32_t upper = __ballot_sync(0xffffffffu, at < n && key > T);
+    const uint32_t equal = __ballot_sync(0xffffffffu, at < n && key == T);
+    const int turn = i & 1;
+    if (lane == 0) {
+      s_warp[turn][0][warp] = __popc(upper);
+      s_warp[turn][1][warp] = __popc(equal);
+    }
+    __syncthreads();
+    int u = lane < kSelectWarps ? s_warp[turn][0][lane] : 0;
+    int e = lane < kSelectWarps ? s_warp[turn][1][lane] : 0;
+    const int u_all = __reduce_add_sync(0xffffffffu, u), e_all = __reduce_add_sync(0xffffffffu, e);
+    const int u_before = __reduce_add_sync(0xffffffffu, lane < warp ? u : 0);
+    const int e_before = __reduce_add_sync(0xffffffffu, lane < warp ? e : 0);
+    const uint32_t below = (1u << lane) - 1;
+    const int eq_rank = e_before + __popc(equal & below);  // among this round's equal keys
+    const bool take = (upper >> lane & 1u) || ((equal >> lane & 1u) && eq_rank < ties);
+    if (take) out[base + u_before + __popc(upper & below) + min(eq_rank, ties)] = at;
+    base += u_all + min(e_all, ties);
+    ties -= min(e_all, ties);
   }
-  const int ties = k - total_a;  // blocks equal to T that are taken
-  int pos = before_a + min(before_e, ties);
-  for (int i = lo; i < hi; ++i) {
-    const uint32_t key = keys[i];
-    if (key > T || (key == T && before_e++ < ties)) out[pos++] = i;
-  }
+}
+
+__global__ void __launch_bounds__(kSelectThreads) fa_block_select_kernel(const SelectParams p) {
+  const int item = blockIdx.x;
+  const int n = request_blocks(p, item / p.s.Hkv);
+  const int k = min(p.k_blocks, n);
+  int32_t* out = p.sel + static_cast<size_t>(item) * p.k_blocks;
+  griddep_wait();  // the keys are complete and visible
+  if (threadIdx.x == 0) p.n_sel[item] = k;
+  for (int i = k + threadIdx.x; i < p.k_blocks; i += kSelectThreads) out[i] = -1;
+  if (k == 0) return;
+  const uint32_t* keys = p.keys + static_cast<size_t>(item) * p.max_blocks;
+  if (n <= kSelectThreads * kKeysPerThread) select_blocks<true>(p, item, n, k, keys);
+  else select_blocks<false>(p, item, n, k, keys);
 }
 
 }  // namespace
@@ -201,8 +268,7 @@ cudaError_t launch_select(const SelectParams& p, cudaStream_t stream) {
   else fa_block_score_kernel<64><<<grid, kScoreThreads, 0, stream>>>(p);
   const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  fa_block_select_kernel<<<items, kSelectThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_dependent(fa_block_select_kernel, dim3(items), dim3(kSelectThreads), 0, stream, p);
 }
 
 }  // namespace fa
