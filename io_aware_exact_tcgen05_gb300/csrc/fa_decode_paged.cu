@@ -105,7 +105,7 @@ __device__ __forceinline__ int request_len(const PagedDecodeParams& p, int b) {
 
 // 16-key blocks of a (request, KV head).
 __device__ __forceinline__ int item_blocks(const PagedDecodeParams& p, int item) {
-  if (p.sel) return min(max(p.n_sel[item], 0), p.max_sel) * (p.s.page_size / kBlockKeys);
+  if (p.sel) return min(max(p.n_sel[item], 0), p.max_sel) << p.block_shift;
   return (request_len(p, item / p.s.Hkv) + kBlockKeys - 1) / kBlockKeys;
 }
 
@@ -138,15 +138,22 @@ __device__ __forceinline__ void make_line(const PagedDecodeParams& p, int row_bl
   __syncthreads();
 }
 
+// Quotient of non-negative values; nearly always both fit 32 bits, where a
+// division takes a quarter of the time.
+__device__ __forceinline__ long long quotient(long long a, int b) {
+  return a <= 0x7fffffffll ? static_cast<long long>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b))
+                           : a / b;
+}
+
 // Blocks per CTA.  At least 8, so that a short request is not cut into pieces
 // that cost more to join than to read, but no more than an item has on average:
 // a segment has a fixed cost of some microseconds, so CTAs should not queue up
 // tiny ones (208 items of one block: REPLACE3).
 __device__ __forceinline__ long long share_of(long long total, int items, int ctas) {
-  const long long even = (total + ctas - 1) / ctas;
-  const long long least = min(static_cast<long long>(kMinShare), max(total / items, 1ll));
+  const long long even = quotient(total + ctas - 1, ctas);
+  const long long least = min(static_cast<long long>(kMinShare), max(quotient(total, items), 1ll));
   if (even <= 16) return max(even, least);
-  return (even + 15) / 16 * 16;  // fewer stretches that straddle two items
+  return (even + 15) & ~15ll;  // fewer stretches that straddle two items
 }
 
 // A CTA walks its stretch of the line segment by segment: blocks [kb0, kb0 + n_seg)
@@ -190,12 +197,13 @@ struct Segment {
       in_item -= static_cast<long long>(n_kb) * row_blocks;
       n_kb = item_blocks(p, ++item);
     }
-    kb0 = static_cast<int>(in_item % n_kb);
+    const int rb = static_cast<int>(quotient(in_item, n_kb));
+    kb0 = static_cast<int>(in_item - static_cast<long long>(rb) * n_kb);
     n_seg = static_cast<int>(min(static_cast<long long>(n_kb - kb0), end - at));
     const int b = item / p.s.Hkv;
-    hk = item % p.s.Hkv;
+    hk = item - b * p.s.Hkv;
     len = request_len(p, b);
-    row0 = static_cast<int>(in_item / n_kb) * tile_rows;
+    row0 = rb * tile_rows;
     n_rows = min(tile_rows, p.rows - row0);
     table = p.block_table + static_cast<size_t>(b) * p.max_blocks;
     qrow0 = static_cast<size_t>(item) * p.rows + row0;
@@ -220,10 +228,10 @@ struct BlockInfo {
 };
 
 __device__ __forceinline__ BlockInfo look_up(const PagedDecodeParams& p, const Segment& sg, int i) {
-  const int ps = p.s.page_size, per_page = ps / kBlockKeys;
+  const int ps = p.s.page_size;
   BlockInfo r = {0, 0x7fffffff, 0.f, 0.f};
   if (i >= sg.n_seg) return r;
-  const int idx = (sg.kb0 + i) / per_page, sub = (sg.kb0 + i) % per_page;
+  const int idx = (sg.kb0 + i) >> p.block_shift, sub = (sg.kb0 + i) & ((1 << p.block_shift) - 1);
   const int blk = p.sel ? p.sel[static_cast<size_t>(sg.item) * p.max_sel + idx] : idx;
   if (blk >= 0 && static_cast<long long>(blk) * ps + sub * kBlockKeys < sg.len) {
     const int page = sg.table[blk];
@@ -321,6 +329,8 @@ __global__ void __launch_bounds__(kThreads, Plan<1>::kCtasPerSm)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
 
+  griddep_launch_dependents();  // the merge waits for this grid's completion
+  griddep_wait();
   make_line(p, row_blocks, s.line);
   const Segment& sg = s.seg;
   if (tid == 0) s.seg.begin(p, row_blocks, 8, s.line);
@@ -550,7 +560,6 @@ __global__ void __launch_bounds__(kThreads, Plan<1>::kCtasPerSm)
     if (tid == 0) s.seg.next(p, row_blocks, 8);
     __syncthreads();
   }
-  griddep_launch_dependents();
 }
 
 // 9 to 32 query rows: the four warps work on the same four blocks (64 keys).  Each
@@ -590,6 +599,8 @@ __global__ void __launch_bounds__(kThreads, Plan<NT>::kCtasPerSm)
   const int g = lane >> 2, t = lane & 3;
   const int dw = warp % DW, vb0 = (warp / DW) * VB;  // channels [32 dw, ..), blocks [vb0, ..)
 
+  griddep_launch_dependents();  // the merge waits for this grid's completion
+  griddep_wait();
   make_line(p, row_blocks, s.line);
   const Segment& sg = s.seg;
   if (tid == 0) s.seg.begin(p, row_blocks, R, s.line);
@@ -857,78 +868,114 @@ __global__ void __launch_bounds__(kThreads, Plan<NT>::kCtasPerSm)
     if (tid == 0) s.seg.next(p, row_blocks, R);
     __syncthreads();
   }
-  griddep_launch_dependents();
 }
 
-// One CTA per (query row, item): joins the partial states of an item that lies in
-// several CTAs' stretches, and writes the rows of items without any key.
-template <int D>
+// Joins the partial states of an item that lies in several CTAs' stretches, in
+// their order, and writes the rows of items without any key.  A row's states go
+// through kSplit warps (four when there are few rows and so, for long contexts, many states
+// per row; else one); each keeps up to four states' loads in flight.
+template <int D, int kSplit>
 __global__ void __launch_bounds__(kThreads)
     fa_decode_paged_merge(const PagedDecodeParams p, int row_blocks, int tile_rows, int ctas,
                           const float* part_o, const float2* part_ml) {
   constexpr int E = D / 32;
+  constexpr int kRows = kWarps / kSplit;  // rows per CTA
+  constexpr int kBatch = 4;
   __shared__ Line line;
-  __shared__ float s_m[kWarps], s_l[kWarps], s_o[kWarps][D];
-  const int row = blockIdx.x, item = blockIdx.y;
-  const int n_kb = item_blocks(p, item);
-  const int rb = row / tile_rows, r = row % tile_rows;
-  const size_t qrow = static_cast<size_t>(item) * p.rows + row;
-  __nv_bfloat16* out = static_cast<__nv_bfloat16*>(p.o) + qrow * D;
-  if (n_kb == 0) {
-    griddep_wait();
-    for (int c = threadIdx.x; c < D; c += kThreads) out[c] = __float2bfloat16_rn(0.f);
-    if (p.lse && threadIdx.x == 0) p.lse[qrow] = neg_inf();
-    return;
-  }
+  __shared__ float s_m[kWarps], s_l[kWarps];
+  __shared__ __align__(16) float s_o[kWarps][D];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int item = blockIdx.y;
+  const int row = blockIdx.x * kRows + warp / kSplit, part = warp % kSplit;
+  // The line is worked out while the partial kernel still runs: nothing that kernel
+  // writes is read for it.
   make_line(p, row_blocks, line);
+  const int n_kb = item_blocks(p, item);
   const int items = p.B * p.s.Hkv;
   const int per = (items + kThreads - 1) / kThreads;
   long long start = line.prefix[item / per];
   for (int i = item / per * per; i < item; ++i)
     start += static_cast<long long>(item_blocks(p, i)) * row_blocks;
+  const int rb = row / tile_rows, r = row - rb * tile_rows;
   start += static_cast<long long>(rb) * n_kb;
   const long long share = share_of(line.prefix[kThreads], items, ctas);
-  const int c0 = static_cast<int>(start / share);
-  const int c1 = static_cast<int>((start + n_kb - 1) / share);
+  int c0 = 0, c1 = 0;
+  if (share <= 0x7fffffffll) {
+    c0 = static_cast<int>(quotient(start, static_cast<int>(share)));
+    c1 = static_cast<int>(quotient(start + n_kb - 1, static_cast<int>(share)));
+  } else {
+    c0 = static_cast<int>(start / share);
+    c1 = static_cast<int>((start + n_kb - 1) / share);
+  }
   // Every CTA waits, also one with nothing to join: what follows this kernel in
   // the stream may then rely on the partial kernel's completion as well.
   griddep_wait();
-  if (c0 == c1) return;  // one CTA finished it
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (n_kb > 0 && c0 == c1 && kSplit == kWarps) return;  // one CTA finished the row
+  const bool joins = row < p.rows && n_kb > 0 && c0 != c1;
+  const size_t qrow = static_cast<size_t>(item) * p.rows + row;
   float M = kNoMax, L = 0.f, o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
-  for (int c = c0 + warp; c <= c1; c += kWarps) {
-    const size_t at = (2 * static_cast<size_t>(c) + (c == c0 ? 1 : 0)) * tile_rows + r;
-    const float2 ml = part_ml[at];
-    const float m_new = fmaxf(M, ml.x);
-    const float a = ex2_approx(M - m_new), w = ex2_approx(ml.x - m_new);
-    M = m_new;
-    L = L * a + w * ml.y;
+  if (joins) {
+    for (int c = c0 + part; c <= c1; c += kSplit * kBatch) {
+      float2 ml[kBatch];
+      float v[kBatch][E];
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = fmaf(w, part_o[at * D + lane * E + e], o[e] * a);
-  }
-  if (lane == 0) {
-    s_m[warp] = M;
-    s_l[warp] = L;
-  }
+      for (int i = 0; i < kBatch; ++i) {
+        const int cc = c + i * kSplit;
+        const size_t at = (2 * static_cast<size_t>(cc) + (cc == c0 ? 1 : 0)) * tile_rows + r;
+        ml[i] = make_float2(kNoMax, 0.f);
 #pragma unroll
-  for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = o[e];
-  __syncthreads();
-  for (int c = threadIdx.x; c < D; c += kThreads) {
-    M = kNoMax;
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s_m[w]);
-    float sum = 0.f, v = 0.f;
-    for (int w = 0; w < kWarps; ++w) {
-      const float wt = ex2_approx(s_m[w] - M);
-      sum = fmaf(wt, s_l[w], sum);
-      v = fmaf(wt, s_o[w][c], v);
+        for (int e = 0; e < E; ++e) v[i][e] = 0.f;
+        if (cc <= c1) {
+          ml[i] = part_ml[at];
+          if constexpr (E == 4) {
+            const float4 x = *reinterpret_cast<const float4*>(part_o + at * D + lane * 4);
+            v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
+          } else {
+            const float2 x = *reinterpret_cast<const float2*>(part_o + at * D + lane * 2);
+            v[i][0] = x.x, v[i][1] = x.y;
+          }
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        const float m_new = fmaxf(M, ml[i].x);
+        const float a = ex2_approx(M - m_new), w = ex2_approx(ml[i].x - m_new);
+        M = m_new;
+        L = L * a + w * ml[i].y;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = fmaf(w, v[i][e], o[e] * a);
+      }
     }
-    const bool empty = sum == 0.f;
-    out[c] = __float2bfloat16_rn(empty ? 0.f : v / sum);
-    if (p.lse && c == 0)
-      p.lse[qrow] = empty ? neg_inf() : (M + __log2f(sum)) * 0.69314718055994530942f;
   }
+  if constexpr (kSplit > 1) {
+    if (lane == 0) {
+      s_m[warp] = M;
+      s_l[warp] = L;
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = o[e];
+    __syncthreads();
+    if (part != 0) return;
+#pragma unroll
+    for (int w = 1; w < kSplit; ++w) {
+      const float m_new = fmaxf(M, s_m[warp + w]);
+      const float a = ex2_approx(M - m_new), b = ex2_approx(s_m[warp + w] - m_new);
+      M = m_new;
+      L = L * a + b * s_l[warp + w];
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = fmaf(b, s_o[warp + w][lane * E + e], o[e] * a);
+    }
+  }
+  if (row >= p.rows || (n_kb > 0 && c0 == c1)) return;
+  const bool empty = L == 0.f;
+  const float inv = empty ? 0.f : 1.f / L;
+  uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + qrow * D + lane * E);
+#pragma unroll
+  for (int e = 0; e < E; e += 2) out[e / 2] = pack_bf16x2(o[e] * inv, o[e + 1] * inv);
+  if (p.lse && lane == 0)
+    p.lse[qrow] = empty ? neg_inf() : (M + __log2f(L)) * 0.69314718055994530942f;
 }
 
 template <int D, int NT>
@@ -942,17 +989,24 @@ cudaError_t launch_nt(const PagedDecodeParams& p, cudaStream_t stream) {
   const int ctas = static_cast<int>(min(static_cast<long long>(kSms * Plan<NT>::kCtasPerSm), most));
   float* part_o = static_cast<float*>(p.workspace);
   float2* part_ml = reinterpret_cast<float2*>(part_o + 2 * static_cast<size_t>(ctas) * 8 * NT * D);
+  const float* c_o = part_o;
+  const float2* c_ml = part_ml;
+  cudaError_t e;
   hook_before(stream);
   if constexpr (NT == 1)
-    fa_decode_paged_narrow<D><<<ctas, kThreads, smem, stream>>>(p, row_blocks, part_o, part_ml);
+    e = launch_dependent(fa_decode_paged_narrow<D>, dim3(ctas), dim3(kThreads), smem, stream, p,
+                         row_blocks, part_o, part_ml);
   else
-    fa_decode_paged_wide<D, NT><<<ctas, kThreads, smem, stream>>>(p, row_blocks, part_o, part_ml);
+    e = launch_dependent(fa_decode_paged_wide<D, NT>, dim3(ctas), dim3(kThreads), smem, stream, p,
+                         row_blocks, part_o, part_ml);
   hook_after(stream);
-  const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  return launch_dependent(fa_decode_paged_merge<D>, dim3(p.rows, p.B * p.s.Hkv), dim3(kThreads), 0,
-                          stream, p, row_blocks, 8 * NT, ctas, static_cast<const float*>(part_o),
-                          static_cast<const float2*>(part_ml));
+  const int items = p.B * p.s.Hkv;
+  if (1LL * p.rows * items <= 8 * kSms)  // REPLACE4
+    return launch_dependent(fa_decode_paged_merge<D, kWarps>, dim3(p.rows, items), dim3(kThreads), 0,
+                            stream, p, row_blocks, 8 * NT, ctas, c_o, c_ml);
+  return launch_dependent(fa_decode_paged_merge<D, 1>, dim3((p.rows + kWarps - 1) / kWarps, items),
+                          dim3(kThreads), 0, stream, p, row_blocks, 8 * NT, ctas, c_o, c_ml);
 }
 
 template <int D>

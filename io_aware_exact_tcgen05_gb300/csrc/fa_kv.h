@@ -95,6 +95,7 @@ struct PagedDecodeParams {
   float* lse;
   void* workspace;
   int B, Hq, Sq, rows, max_blocks, max_sel;
+  int block_shift;       // log2(page_size / 16)
   float scale_log2;
   KvShape s;
 };

@@ -318,6 +318,7 @@ fa_status fa_decode_paged_fp8(const void* q, const void* k_cache, const void* v_
   p.Sq = Sq;
   p.max_blocks = max_blocks;
   p.max_sel = sel ? max_sel : 0;
+  p.block_shift = page_size == 16 ? 0 : page_size == 32 ? 1 : page_size == 64 ? 2 : 3;
   p.scale_log2 = fa::api_scale_log2(scale);
   const cudaError_t e = fa::launch_decode_paged(p, stream);
   if (e != cudaSuccess)

@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 
+#include "fa_internal.h"
 #include "fa_kv.h"
 #include "fa_kv_device.cuh"
 
@@ -63,6 +64,7 @@ __global__ void __launch_bounds__(kAssignThreads) fa_kv_assign_kernel(const KvAs
   const bool first_cta = blockIdx.x == 0;
   long long cu0 = 0, need0 = 0, k0 = 0;  // totals of the requests before this chunk
   if (tid == 0) s_used = 0;
+  griddep_wait();
   for (int base = 0; base < p.B; base += kAssignThreads) {
     const int b = base + tid;
     const bool real = b < p.B;
@@ -174,6 +176,7 @@ __global__ void __launch_bounds__(WriteTile<D, PS>::kThreads)
   const int t_lo = blockIdx.x * stretch;
   const int t_hi = min(t_lo + stretch, p.n_tokens);
   int turn = 0;
+  griddep_wait();
 
   for (int base = t_lo; base < t_hi; base += 32) {
     // every warp finds the runs that start in these 32 tokens
@@ -338,6 +341,7 @@ __global__ void __launch_bounds__(kReadThreads) fa_kv_read_kernel(const KvReadPa
   const long long r = static_cast<long long>(blockIdx.x) * ROWS + threadIdx.x / CPR;
   const int h = blockIdx.y;
   const bool is_v = blockIdx.z != 0;
+  griddep_wait();
   if (r >= p.total_k) return;
   // last sequence with cu_k <= r; behind the last one the row stays as it was
   int a = 0, z = p.nseq;
@@ -373,8 +377,7 @@ __global__ void __launch_bounds__(kReadThreads) fa_kv_read_kernel(const KvReadPa
 
 cudaError_t launch_kv_assign(const KvAssignParams& p, cudaStream_t stream) {
   const int grid = max(1, (p.total_new + kAssignTokens - 1) / kAssignTokens);
-  fa_kv_assign_kernel<<<grid, kAssignThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_dependent(fa_kv_assign_kernel, dim3(grid), dim3(kAssignThreads), 0, stream, p);
 }
 
 namespace {
@@ -388,8 +391,8 @@ cudaError_t launch_write(const KvWriteParams& p, cudaStream_t stream) {
   int stretch = 1;
   while (stretch < PS && work / (2 * stretch) >= 152 * 16) stretch *= 2;
   const dim3 grid((p.n_tokens + stretch - 1) / stretch, p.s.Hkv, 2);
-  fa_kv_write_kernel<D, PS><<<grid, WriteTile<D, PS>::kThreads, 0, stream>>>(p, stretch);
-  return cudaGetLastError();
+  return launch_dependent(fa_kv_write_kernel<D, PS>, grid, dim3(WriteTile<D, PS>::kThreads), 0,
+                          stream, p, stretch);
 }
 
 template <int D>
@@ -411,9 +414,8 @@ cudaError_t launch_kv_write(const KvWriteParams& p, cudaStream_t stream) {
 cudaError_t launch_kv_read(const KvReadParams& p, cudaStream_t stream) {
   const int rows = kReadThreads / (p.s.d / 16);
   const dim3 grid((p.total_k + rows - 1) / rows, p.s.Hkv, 2);
-  if (p.s.d == 128) fa_kv_read_kernel<128><<<grid, kReadThreads, 0, stream>>>(p);
-  else fa_kv_read_kernel<64><<<grid, kReadThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return launch_dependent(p.s.d == 128 ? fa_kv_read_kernel<128> : fa_kv_read_kernel<64>, grid,
+                          dim3(kReadThreads), 0, stream, p);
 }
 
 }  // namespace fa

@@ -23,7 +23,6 @@ constexpr int kScoreBlocks = 64;  // cache blocks per CTA
 constexpr int kRowTile = 16;      // query rows quantised into shared memory at a time
 constexpr int kSelectThreads = 512;
 constexpr int kSelectWarps = kSelectThreads / 32;
-constexpr int kKeysPerThread = 16;  // up to 8192 blocks live in registers
 
 // Order-preserving map of a score to an unsigned key; NaN ranks lowest.
 __device__ __forceinline__ uint32_t score_key(float s) {
@@ -75,24 +74,30 @@ __global__ void __launch_bounds__(kScoreThreads) fa_block_score_kernel(const Sel
   __shared__ float s_scale[kRowTile];
   const int item = blockIdx.y;                  // (request, KV head)
   const int b = item / p.s.Hkv, hk = item % p.s.Hkv;
-  const int n = request_blocks(p, b);
   const int first = blockIdx.x * kScoreBlocks;
-  if (first >= n) {
-    griddep_launch_dependents();
-    return;
-  }
+  griddep_launch_dependents();  // the selection waits for this grid's completion
+  griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int part = lane % LPB, sub = lane / LPB;
   const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) +
                            static_cast<size_t>(item) * p.rows * D;
   constexpr int PER = kScoreBlocks / (WARPS * BPW);
-  // the bounds of all blocks of this warp are on their way while q is quantised
+  // the table's entries and the length are read side by side, and the bounds of
+  // all blocks of this warp are on their way while q is quantised
   float best[PER], ks[PER];
   int4 w[PER];
+  int pages[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int blk = first + (i * WARPS + warp) * BPW + sub;
-    const int page = blk < n ? p.block_table[static_cast<size_t>(b) * p.max_blocks + blk] : -1;
+    pages[i] = blk < p.max_blocks ? p.block_table[static_cast<size_t>(b) * p.max_blocks + blk] : -1;
+  }
+  const int n = request_blocks(p, b);
+  if (first >= n) return;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) {
+    const int blk = first + (i * WARPS + warp) * BPW + sub;
+    const int page = blk < n ? pages[i] : -1;
     best[i] = __int_as_float(0xff800000);
     ks[i] = -1.f;  // no page
     w[i] = make_int4(0, 0, 0, 0);
@@ -133,7 +138,6 @@ __global__ void __launch_bounds__(kScoreThreads) fa_block_score_kernel(const Sel
           forced ? 0xffffffffu : ks[i] < 0.f ? score_key(__int_as_float(0xff800000)) : score_key(best[i]);
     }
   }
-  griddep_launch_dependents();
 }
 
 // The k = min(k_blocks, n) blocks with the largest keys of one (request, KV
@@ -143,18 +147,19 @@ __global__ void __launch_bounds__(kScoreThreads) fa_block_score_kernel(const Sel
 // the first of those equal to T are then written in order.  One CTA per item;
 // latency bounds it, so the keys stay in registers (thread t holds blocks t, t +
 // 512, ...) unless there are more than 8192 of them.
-template <bool kInRegs>
+template <int kRounds>
 __device__ __forceinline__ void select_blocks(const SelectParams& p, int item, int n, int k,
                                               const uint32_t* keys) {
   __shared__ int s_count[2][3][kSelectWarps];
   __shared__ int s_warp[2][2][kSelectWarps];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int32_t* out = p.sel + static_cast<size_t>(item) * p.k_blocks;
-  const int rounds = (n + kSelectThreads - 1) / kSelectThreads;
-  uint32_t mine[kInRegs ? kKeysPerThread : 1];
+  constexpr bool kInRegs = kRounds > 0;
+  const int rounds = kInRegs ? kRounds : (n + kSelectThreads - 1) / kSelectThreads;
+  uint32_t mine[kInRegs ? kRounds : 1];
   if (kInRegs) {
 #pragma unroll
-    for (int i = 0; i < kKeysPerThread; ++i) {
+    for (int i = 0; i < kRounds; ++i) {
       const int at = i * kSelectThreads + tid;
       mine[i] = at < n ? keys[at] : 0u;  // 0 is below every candidate
     }
@@ -165,12 +170,10 @@ __device__ __forceinline__ void select_blocks(const SelectParams& p, int item, i
     const uint32_t t1 = T | 1u << bit, t2 = T | 2u << bit, t3 = T | 3u << bit;
     if (kInRegs) {
 #pragma unroll
-      for (int i = 0; i < kKeysPerThread; ++i) {
-        if (i < rounds) {
-          c1 += mine[i] >= t1;
-          c2 += mine[i] >= t2;
-          c3 += mine[i] >= t3;
-        }
+      for (int i = 0; i < kRounds; ++i) {
+        c1 += mine[i] >= t1;
+        c2 += mine[i] >= t2;
+        c3 += mine[i] >= t3;
       }
     } else {
       for (int at = tid; at < n; at += kSelectThreads) {
@@ -202,8 +205,7 @@ __device__ __forceinline__ void select_blocks(const SelectParams& p, int item, i
   int above = 0;
   if (kInRegs) {
 #pragma unroll
-    for (int i = 0; i < kKeysPerThread; ++i)
-      if (i < rounds) above += mine[i] > T;
+    for (int i = 0; i < kRounds; ++i) above += mine[i] > T;
   } else {
     for (int at = tid; at < n; at += kSelectThreads) above += keys[at] > T;
   }
@@ -213,13 +215,12 @@ __device__ __forceinline__ void select_blocks(const SelectParams& p, int item, i
   above = __reduce_add_sync(0xffffffffu, lane < kSelectWarps ? s_count[1][0][lane] : 0);
   int ties = k - above;  // blocks equal to T still to be taken
   int base = 0;
+#pragma unroll(kInRegs ? kRounds : 1)
   for (int i = 0; i < rounds; ++i) {
     const int at = i * kSelectThreads + tid;
     uint32_t key = 0;
     if (kInRegs) {
-#pragma unroll
-      for (int j = 0; j < kKeysPerThread; ++j)
-        if (j == i) key = mine[j];
+      key = mine[i];
     } else if (at < n) {
       key = keys[at];
     }
@@ -255,8 +256,14 @@ __global__ void __launch_bounds__(kSelectThreads) fa_block_select_kernel(const S
   for (int i = k + threadIdx.x; i < p.k_blocks; i += kSelectThreads) out[i] = -1;
   if (k == 0) return;
   const uint32_t* keys = p.keys + static_cast<size_t>(item) * p.max_blocks;
-  if (n <= kSelectThreads * kKeysPerThread) select_blocks<true>(p, item, n, k, keys);
-  else select_blocks<false>(p, item, n, k, keys);
+  // as few comparisons as the item needs: 512, 1024, 2048, 4096 or 8192 blocks
+  const int rounds = (n + kSelectThreads - 1) / kSelectThreads;
+  if (rounds <= 1) select_blocks<1>(p, item, n, k, keys);
+  else if (rounds <= 2) select_blocks<2>(p, item, n, k, keys);
+  else if (rounds <= 4) select_blocks<4>(p, item, n, k, keys);
+  else if (rounds <= 8) select_blocks<8>(p, item, n, k, keys);
+  else if (rounds <= 16) select_blocks<16>(p, item, n, k, keys);
+  else select_blocks<0>(p, item, n, k, keys);
 }
 
 }  // namespace
@@ -264,9 +271,9 @@ __global__ void __launch_bounds__(kSelectThreads) fa_block_select_kernel(const S
 cudaError_t launch_select(const SelectParams& p, cudaStream_t stream) {
   const int items = p.B * p.s.Hkv;
   const dim3 grid((p.max_blocks + kScoreBlocks - 1) / kScoreBlocks, items);
-  if (p.s.d == 128) fa_block_score_kernel<128><<<grid, kScoreThreads, 0, stream>>>(p);
-  else fa_block_score_kernel<64><<<grid, kScoreThreads, 0, stream>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e =
+      launch_dependent(p.s.d == 128 ? fa_block_score_kernel<128> : fa_block_score_kernel<64>, grid,
+                       dim3(kScoreThreads), 0, stream, p);
   if (e != cudaSuccess) return e;
   return launch_dependent(fa_block_select_kernel, dim3(items), dim3(kSelectThreads), 0, stream, p);
 }
