@@ -299,7 +299,7 @@ fa_status fa_decode_noalloc(const void* q, const void* k_cache, const void* v_ca
  *    [0, num_pages) mark absent pages: their keys are treated as hidden.
  *    Requests may share pages that nothing writes to.
  *  * Page and slot offsets are computed in 64 bits; a cache may be larger than
- *    2^32 bytes.
+ *    2^32 bytes.  Packed tokens per call: at most 2^30.
  */
 
 /*

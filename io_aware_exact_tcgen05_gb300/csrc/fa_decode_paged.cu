@@ -15,7 +15,7 @@
 // and are stored as w * 2^9 * v_scale / v_ref <= 2^15 (v_ref: the largest V scale
 // so far), so a weight keeps f16's 11 bits down to 2^-23 of the largest and is
 // rounded by at most 2^-34 of it below.  (A lag of 2 kept four bits more and
-// moved the maximum on most steps of 32 rows: REPLACE2.)  Sums, maxima and
+// moved the maximum on most steps of 32 rows: 72 us against 66 us.)  Sums, maxima and
 // accumulators are fp32.
 //
 // Operands without shared memory: the contraction index of a product may be
@@ -70,12 +70,6 @@ int grid_ctas(int nt) {
 constexpr float kNoMax = -3.0e38f;
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
-
-__device__ __forceinline__ uint2 ld_stream8(const void* p) {
-  uint2 v;
-  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
-  return v;
-}
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -148,7 +142,7 @@ __device__ __forceinline__ long long quotient(long long a, int b) {
 // Blocks per CTA.  At least 8, so that a short request is not cut into pieces
 // that cost more to join than to read, but no more than an item has on average:
 // a segment has a fixed cost of some microseconds, so CTAs should not queue up
-// tiny ones (208 items of one block: REPLACE3).
+// tiny ones (208 items of one block: 54 us in eights, 22 us one by one).
 __device__ __forceinline__ long long share_of(long long total, int items, int ctas) {
   const long long even = quotient(total + ctas - 1, ctas);
   const long long least = min(static_cast<long long>(kMinShare), max(quotient(total, items), 1ll));
@@ -1002,7 +996,8 @@ cudaError_t launch_nt(const PagedDecodeParams& p, cudaStream_t stream) {
   hook_after(stream);
   if (e != cudaSuccess) return e;
   const int items = p.B * p.s.Hkv;
-  if (1LL * p.rows * items <= 8 * kSms)  // REPLACE4
+  // four warps a row while there are no more rows than the GPU holds CTAs of 128 threads at once
+  if (1LL * p.rows * items <= 16 * kSms)
     return launch_dependent(fa_decode_paged_merge<D, kWarps>, dim3(p.rows, items), dim3(kThreads), 0,
                             stream, p, row_blocks, 8 * NT, ctas, c_o, c_ml);
   return launch_dependent(fa_decode_paged_merge<D, 1>, dim3((p.rows + kWarps - 1) / kWarps, items),

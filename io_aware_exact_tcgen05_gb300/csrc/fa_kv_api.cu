@@ -71,10 +71,10 @@ fa_status fa_kv_assign(const int32_t* seqlens, const int32_t* newlens, int B, in
                        int32_t* block_table, int max_blocks, const int32_t* free_pages, int n_free,
                        int64_t* slot_map, int total_new, int32_t* cu_new, int32_t* seqlens_out,
                        int32_t* cu_seqlens_k, int32_t* n_used, cudaStream_t stream) {
-  if (B < 1 || max_blocks < 1 || n_free < 0 || total_new < 0)
+  if (B < 1 || max_blocks < 1 || n_free < 0 || total_new < 0 || total_new > 1 << 30)
     return api_fail(FA_ERR_INVALID_ARG,
-                    "fa_kv_assign: B=%d max_blocks=%d must be >= 1, n_free=%d total_new=%d >= 0", B,
-                    max_blocks, n_free, total_new);
+                    "fa_kv_assign: B=%d max_blocks=%d must be >= 1, n_free=%d >= 0, total_new=%d in "
+                    "[0, 2^30]", B, max_blocks, n_free, total_new);
   FA_TRY(check_page_size(page_size));
   if (1LL * max_blocks * page_size > 0x7fffffffLL)
     return api_fail(FA_ERR_INVALID_ARG, "max_blocks x page_size exceeds 2^31 - 1 positions");
@@ -132,7 +132,8 @@ fa_status fa_kv_write_fp8(const void* k, const void* v, long long k_stride_h, lo
   fa::KvWriteParams p{};
   p.s = {num_pages, Hkv, page_size, d};
   FA_TRY(check_shape(p.s));
-  if (n_tokens < 0) return api_fail(FA_ERR_INVALID_ARG, "n_tokens (%d) must be >= 0", n_tokens);
+  if (n_tokens < 0 || n_tokens > 1 << 30)
+    return api_fail(FA_ERR_INVALID_ARG, "n_tokens (%d) must lie in [0, 2^30]", n_tokens);
   FA_TRY(need_ptr(k_cache, "k_cache", 16));
   FA_TRY(need_ptr(v_cache, "v_cache", 16));
   FA_TRY(need_ptr(k_scale, "k_scale", 4));
@@ -174,9 +175,10 @@ fa_status fa_kv_read_fp8(const void* k_cache, const void* v_cache, const float* 
   fa::KvReadParams p{};
   p.s = {num_pages, Hkv, page_size, d};
   FA_TRY(check_shape(p.s));
-  if (nseq < 1 || max_blocks < 1 || total_k < 0)
-    return api_fail(FA_ERR_INVALID_ARG, "nseq=%d max_blocks=%d must be >= 1, total_k=%d >= 0", nseq,
-                    max_blocks, total_k);
+  if (nseq < 1 || max_blocks < 1 || total_k < 0 || total_k > 1 << 30)
+    return api_fail(FA_ERR_INVALID_ARG,
+                    "nseq=%d max_blocks=%d must be >= 1, total_k=%d in [0, 2^30]", nseq, max_blocks,
+                    total_k);
   FA_TRY(need_ptr(k_cache, "k_cache", 16));
   FA_TRY(need_ptr(v_cache, "v_cache", 16));
   FA_TRY(need_ptr(k_scale, "k_scale", 4));

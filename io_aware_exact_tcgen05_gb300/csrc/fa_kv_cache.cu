@@ -24,7 +24,7 @@ namespace {
 // L2), and then serves its own stretch of tokens: one launch, no exchange
 // between CTAs.
 constexpr int kAssignThreads = 256;
-constexpr int kAssignTokens = 2048;  // packed tokens per CTA
+constexpr int kAssignTokens = 1024;  // packed tokens per CTA
 
 __device__ __forceinline__ long long block_scan_inclusive(long long v, long long* warp_sums,
                                                           long long* total) {
@@ -59,6 +59,7 @@ __global__ void __launch_bounds__(kAssignThreads) fa_kv_assign_kernel(const KvAs
   __shared__ long long s_sums[kAssignThreads / 32];
   __shared__ int s_used;
   const int tid = threadIdx.x;
+  const int shift = 31 - __clz(p.page_size);  // a power of two
   const long long t_lo = static_cast<long long>(blockIdx.x) * kAssignTokens;
   const long long t_hi = min(t_lo + kAssignTokens, static_cast<long long>(p.total_new));
   const bool first_cta = blockIdx.x == 0;
@@ -72,8 +73,8 @@ __global__ void __launch_bounds__(kAssignThreads) fa_kv_assign_kernel(const KvAs
     const long long add = real ? max(p.newlens[b], 0) : 0;
     long long sum_new, sum_need;
     const long long cu_end = cu0 + block_scan_inclusive(add, s_sums, &sum_new);
-    const long long have = (seq + p.page_size - 1) / p.page_size;
-    const long long full = (seq + add + p.page_size - 1) / p.page_size;
+    const long long have = (seq + p.page_size - 1) >> shift;
+    const long long full = (seq + add + p.page_size - 1) >> shift;
     const bool never = full > p.max_blocks || cu_end > p.total_new;
     const long long need = never ? 0 : full - have;
     const long long end = need0 + block_scan_inclusive(need, s_sums, &sum_need);
@@ -108,9 +109,10 @@ __global__ void __launch_bounds__(kAssignThreads) fa_kv_assign_kernel(const KvAs
       }
       long long slot = -1;
       if (s_live[a]) {
-        const long long pos = s_seq[a] + (t - s_cu[a]);
-        const int blk = static_cast<int>(pos / p.page_size);
-        const int off = static_cast<int>(pos % p.page_size);
+        // a live request fits its table, whose positions fit 31 bits
+        const int pos = s_seq[a] + static_cast<int>(t - s_cu[a]);
+        const int blk = pos >> shift;
+        const int off = pos & (p.page_size - 1);
         int32_t* row = p.block_table + static_cast<long long>(base + a) * p.max_blocks;
         int page;
         if (blk < s_have[a]) {
@@ -144,27 +146,51 @@ __global__ void __launch_bounds__(kAssignThreads) fa_kv_assign_kernel(const KvAs
 //
 // One CTA per (stretch of packed tokens, KV head, K or V) serves the runs that
 // start in its stretch.  HBM bounds long prompts: every value is read once and
-// stays in registers between the maximum and the rounding; a CTA has as many
-// threads as a full page has 128-byte pieces, so each holds at most 8 16-byte
-// pieces, all of them in flight at once.
+// stays in registers between the maximum and the rounding, a thread's 16 pieces of
+// 16 bytes all in flight at once.  (With 8 pieces and twice the threads the cost of finding
+// and closing a run, some 700 instructions a warp, took more issue slots than the
+// data: 88 us against 77 us for 65k tokens of 8 heads, d = 128, 5.4 TB/s.)
+// quantise8 for a scale that is no power of two, by division.  Out of line: eight divisions at every use
+// had the quantising write wait for instructions.
+__device__ __noinline__ uint2 quantise8_divide(uint4 w, float s) {
+  const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+  uint32_t c[4];
+#pragma unroll 1
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t v = i == 0 ? x[0] : i == 1 ? x[1] : i == 2 ? x[2] : x[3];
+    const uint32_t q = pack_e4m3x2(__fdiv_rn(__uint_as_float(v << 16), s),
+                                   __fdiv_rn(__uint_as_float(v & 0xffff0000u), s));
+    if (i == 0) c[0] = q;
+    if (i == 1) c[1] = q;
+    if (i == 2) c[2] = q;
+    if (i == 3) c[3] = q;
+  }
+  return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
+}
+
+constexpr int kPieces = 16;  // 16-byte pieces a thread holds of a full page
+
 template <int D, int PS>
 struct WriteTile {
   static constexpr int kCols = D / 8;  // 16-byte pieces of a row
-  static constexpr int kThreads = PS * kCols / 8 < 32 ? 32 : PS * kCols / 8;
+  static constexpr int kThreads = PS * kCols / kPieces < 32 ? 32 : PS * kCols / kPieces;
   static constexpr int kRows = kThreads / kCols;  // rows of one pass
   static constexpr int kPasses = PS / kRows;
   static constexpr int kWarps = kThreads / 32;
 };
 
 template <int D, int PS>
-__global__ void __launch_bounds__(WriteTile<D, PS>::kThreads)
+__global__ void __launch_bounds__(WriteTile<D, PS>::kThreads, 640 / WriteTile<D, PS>::kThreads)
     fa_kv_write_kernel(const KvWriteParams p, int stretch) {
   using T = WriteTile<D, PS>;
   __shared__ uint32_t s_max[2][T::kWarps];
   __shared__ __half2 s_hi[T::kWarps][D / 2], s_lo[T::kWarps][D / 2];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int h = blockIdx.y;
-  const bool is_v = blockIdx.z != 0;
+  // the heads of one stretch are neighbours in the grid: token-major inputs hold
+  // them side by side
+  const int part = blockIdx.x % (2 * p.s.Hkv);
+  const int h = part % p.s.Hkv;
+  const bool is_v = part >= p.s.Hkv;
   const long long st_h = is_v ? p.v_stride_h : p.k_stride_h;
   const long long st_t = is_v ? p.v_stride_t : p.k_stride_t;
   const int col = tid % T::kCols, row0 = tid / T::kCols;
@@ -173,57 +199,68 @@ __global__ void __launch_bounds__(WriteTile<D, PS>::kThreads)
   float* scales = is_v ? p.v_scale : p.k_scale;
   int8_t* bounds = is_v ? nullptr : p.k_bounds;
   const long long n_slots = static_cast<long long>(p.s.num_pages) * PS;
-  const int t_lo = blockIdx.x * stretch;
+  const int t_lo = blockIdx.x / (2 * p.s.Hkv) * stretch;
   const int t_hi = min(t_lo + stretch, p.n_tokens);
   int turn = 0;
   griddep_wait();
 
-  for (int base = t_lo; base < t_hi; base += 32) {
-    // every warp finds the runs that start in these 32 tokens
-    long long slot = -1;
-    bool starts = false;
-    if (base + lane < t_hi) {
-      slot = p.slot_map[base + lane];
-      starts = slot >= 0 && slot < n_slots;
-      if (starts && slot % PS != 0 && base + lane > 0)
-        starts = p.slot_map[base + lane - 1] != slot - 1;
+  // Every warp reads the slots of the stretch and of a page's length behind it at
+  // once and marks the tokens that follow their predecessor in its page; runs are
+  // then found without another load.
+  constexpr int kWords = PS / 16;       // 2 * PS tokens in words of 32
+  uint32_t follows = 0, begins = 0;     // lane w: masks of word w
+  {
+    long long slots[kWords];
+    long long before = t_lo > 0 ? p.slot_map[t_lo - 1] : -1;
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) {
+      const int t = t_lo + 32 * w + lane;
+      slots[w] = t < p.n_tokens ? p.slot_map[t] : -1;
     }
-    for (uint32_t todo = __ballot_sync(0xffffffffu, starts); todo; todo &= todo - 1) {
+#pragma unroll
+    for (int w = 0; w < kWords; ++w) {
+      long long prev = __shfl_up_sync(0xffffffffu, slots[w], 1);
+      if (lane == 0) prev = before;
+      before = __shfl_sync(0xffffffffu, slots[w], 31);
+      const bool in_run = slots[w] > 0 && slots[w] == prev + 1 && (slots[w] & (PS - 1)) != 0;
+      const bool first = !in_run && slots[w] >= 0 && slots[w] < n_slots && t_lo + 32 * w + lane < t_hi;
+      const uint32_t m = __ballot_sync(0xffffffffu, in_run), n = __ballot_sync(0xffffffffu, first);
+      if (lane == w) follows = m, begins = n;
+    }
+  }
+#pragma unroll 1
+  for (int w = 0; w < (PS + 31) / 32; ++w) {
+#pragma unroll 1
+    for (uint32_t todo = __shfl_sync(0xffffffffu, begins, w); todo; todo &= todo - 1) {
       const int at = __ffs(todo) - 1;
-      const int t = base + at;
-      const long long first = __shfl_sync(0xffffffffu, slot, at);
-      const int page = static_cast<int>(first / PS), off = static_cast<int>(first % PS);
+      const int t = t_lo + 32 * w + at;
+      const long long first = p.slot_map[t];
+      const int page = static_cast<int>(first / PS), off = static_cast<int>(first & (PS - 1));
       const size_t tile = static_cast<size_t>(page) * p.s.Hkv + h;
       float s_old = off > 0 ? scales[tile] : 0.f;
-      const int most = min(PS - off, p.n_tokens - t);
-      int len = 1;
-      while (len < most) {  // up to the first token that does not follow
-        const int j = len + lane;
-        const uint32_t stop =
-            __ballot_sync(0xffffffffu, j >= most || p.slot_map[t + j] != first + j);
-        if (stop) {
-          len += __ffs(stop) - 1;
-          break;
-        }
-        len += 32;
+      int len = 1;  // up to the first token that does not follow
+      for (int u = 32 * w + at + 1; u < 32 * kWords; u = (u | 31) + 1) {
+        const uint32_t stop = ~__shfl_sync(0xffffffffu, follows, u >> 5) >> (u & 31);
+        len += stop ? __ffs(stop) - 1 : 32 - (u & 31);
+        // (the zeros shifted in count as "follows": a set bit below them, or the word's end)
+        if (stop) break;
       }
-      if (!(s_old > 0.f && s_old <= 3.4028235e38f)) s_old = 0.f;
-
+      len = min(len, PS - off);
       uint4 x[T::kPasses];
-      uint32_t m = 0, any = 0;  // largest finite magnitude; largest magnitude bits
+      const __nv_bfloat16* from = src + (t + row0) * st_t;
 #pragma unroll
       for (int i = 0; i < T::kPasses; ++i) {
-        const int r = row0 + i * T::kRows;
         x[i] = make_uint4(0u, 0u, 0u, 0u);
-        if (r < len) x[i] = ld_stream16(src + (t + r) * st_t);
+        if (row0 + i * T::kRows < len) x[i] = ld_stream16(from);
+        from += T::kRows * st_t;
       }
+      uint32_t m = 0;  // largest magnitude of the even and odd values, as bf16 bits
 #pragma unroll
-      for (int i = 0; i < T::kPasses; ++i) {
-        any = __vmaxu2(any, __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
-                                     __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu)));
-      }
-      m = any;
-      const bool odd_values = max(any & 0xffffu, any >> 16) >= 0x7f80u;  // infinities, NaN
+      for (int i = 0; i < T::kPasses; ++i)
+        m = __vmaxu2(m, __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
+                                 __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu)));
+      // infinities or NaN somewhere in the warp
+      const bool odd_values = __any_sync(0xffffffffu, max(m & 0xffffu, m >> 16) >= 0x7f80u);
       if (odd_values) {
         m = 0;
 #pragma unroll
@@ -233,6 +270,7 @@ __global__ void __launch_bounds__(WriteTile<D, PS>::kThreads)
       if (lane == 0) s_max[turn][warp] = top;
       // all reads of the page's old scale and bounds come before this barrier,
       // all writes after it
+      if (!(s_old > 0.f && s_old <= 3.4028235e38f)) s_old = 0.f;
       __half2 old_hi, old_lo;
       if (bounds && off > 0 && tid < D / 2) {
         const char2 a = reinterpret_cast<const char2*>(bounds + tile * 2 * D)[tid];
@@ -257,6 +295,7 @@ __global__ void __launch_bounds__(WriteTile<D, PS>::kThreads)
       const bool pow2 = (__float_as_uint(s) & 0x7fffffu) == 0;
       const float inv = 1.f / s;
       __half2 hi[4], lo[4];
+      uint2* to = reinterpret_cast<uint2*>(dst) + (off + row0) * T::kCols + col;
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         hi[e] = __float2half2_rn(-65504.f);
@@ -266,8 +305,8 @@ __global__ void __launch_bounds__(WriteTile<D, PS>::kThreads)
       for (int i = 0; i < T::kPasses; ++i) {
         const int r = row0 + i * T::kRows;
         if (r < len) {
-          uint2 c = quantise8(x[i], s, inv, pow2);
-          reinterpret_cast<uint2*>(dst)[(off + r) * T::kCols + col] = c;
+          uint2 c = pow2 ? quantise8(x[i], inv) : quantise8_divide(x[i], s);
+          to[i * T::kRows * T::kCols] = c;
           if (bounds) {
             if (odd_values) c = zero_nan_codes(c);
             const uint32_t w[4] = {c.x, c.x >> 16, c.y, c.y >> 16};
@@ -329,48 +368,56 @@ __global__ void __launch_bounds__(WriteTile<D, PS>::kThreads)
 // ------------------------------------------------------------------- read --
 //
 // Packed row r of KV head h is code * scale of the sequence's token, rounded to
-// bf16 (exact for power-of-two scales: e4m3 has 4 significant bits).  One
-// thread turns 16 codes into 32 bytes.
+// bf16 (exact for power-of-two scales: e4m3 has 4 significant bits).  HBM bounds
+// it (1 byte read, 2 written per element).  A thread turns 8 codes into 16 bytes, so
+// a warp's stores are whole 512-byte pieces, and has four rows' loads in flight.
 constexpr int kReadThreads = 256;
+constexpr int kReadPasses = 4;
 
 template <int D>
 __global__ void __launch_bounds__(kReadThreads) fa_kv_read_kernel(const KvReadParams p) {
-  constexpr int CPR = D / 16;
-  constexpr int ROWS = kReadThreads / CPR;
+  constexpr int CPR = D / 8;
+  constexpr int ROWS = kReadThreads / CPR;  // rows of one pass
   const int col = threadIdx.x % CPR;
-  const long long r = static_cast<long long>(blockIdx.x) * ROWS + threadIdx.x / CPR;
   const int h = blockIdx.y;
   const bool is_v = blockIdx.z != 0;
+  const int ps = p.s.page_size, shift = 31 - __clz(ps);
+  const uint8_t* cache = static_cast<const uint8_t*>(is_v ? p.v_cache : p.k_cache) + col * 8;
+  const float* scales = is_v ? p.v_scale : p.k_scale;
+  uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(is_v ? p.v : p.k) +
+                                        static_cast<size_t>(h) * p.total_k * D) + col;
+  long long r = static_cast<long long>(blockIdx.x) * (ROWS * kReadPasses) + threadIdx.x / CPR;
   griddep_wait();
-  if (r >= p.total_k) return;
-  // last sequence with cu_k <= r; behind the last one the row stays as it was
-  int a = 0, z = p.nseq;
-  while (z - a > 1) {
+  // last sequence with cu_k <= r
+  int a = 0;
+  for (int z = p.nseq; z - a > 1;) {
     const int mid = (a + z) >> 1;
     if (p.cu_k[mid] <= r) a = mid; else z = mid;
   }
-  const long long first = p.cu_k[a];
-  if (r < first || r >= p.cu_k[a + 1]) return;
-  const long long pos = r - first;
-  const int ps = p.s.page_size;
-  const long long blk = pos / ps;
-  int page = -1;
-  if (blk < p.max_blocks) page = p.block_table[static_cast<long long>(a) * p.max_blocks + blk];
-  uint4 lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
-  if (page >= 0 && page < p.s.num_pages) {
-    const size_t tile = static_cast<size_t>(page) * p.s.Hkv + h;
-    const float s = (is_v ? p.v_scale : p.k_scale)[tile];
-    const uint8_t* c = static_cast<const uint8_t*>(is_v ? p.v_cache : p.k_cache) +
-                       (tile * ps + static_cast<int>(pos % ps)) * D + col * 16;
-    const uint4 w = *reinterpret_cast<const uint4*>(c);
-    lo = dequantise8(make_uint2(w.x, w.y), s);
-    hi = dequantise8(make_uint2(w.z, w.w), s);
+  uint2 w[kReadPasses];
+  float s[kReadPasses];
+  bool mine[kReadPasses];
+#pragma unroll
+  for (int i = 0; i < kReadPasses; ++i, r += ROWS) {
+    while (a + 1 < p.nseq && p.cu_k[a + 1] <= r) ++a;
+    const long long pos = r - p.cu_k[a];
+    // rows behind the last sequence (and the buffers) stay as they were
+    mine[i] = r < p.total_k && pos >= 0 && r < p.cu_k[a + 1];
+    w[i] = make_uint2(0u, 0u);
+    s[i] = 0.f;
+    if (mine[i] && (pos >> shift) < p.max_blocks) {
+      const int page = p.block_table[static_cast<long long>(a) * p.max_blocks + (pos >> shift)];
+      if (page >= 0 && page < p.s.num_pages) {
+        const size_t tile = static_cast<size_t>(page) * p.s.Hkv + h;
+        s[i] = scales[tile];
+        w[i] = ld_stream8(cache + (tile * ps + static_cast<int>(pos & (ps - 1))) * D);
+      }
+    }
   }
-  uint4* out = reinterpret_cast<uint4*>(
-      static_cast<__nv_bfloat16*>(is_v ? p.v : p.k) +
-      (static_cast<size_t>(h) * p.total_k + r) * D + col * 16);
-  out[0] = lo;
-  out[1] = hi;
+  r -= static_cast<long long>(ROWS) * kReadPasses;
+#pragma unroll
+  for (int i = 0; i < kReadPasses; ++i, r += ROWS)
+    if (mine[i]) out[r * CPR] = dequantise8(w[i], s[i]);
 }
 
 }  // namespace
@@ -390,7 +437,7 @@ cudaError_t launch_write(const KvWriteParams& p, cudaStream_t stream) {
   const long long work = 2LL * p.n_tokens * p.s.Hkv;
   int stretch = 1;
   while (stretch < PS && work / (2 * stretch) >= 152 * 16) stretch *= 2;
-  const dim3 grid((p.n_tokens + stretch - 1) / stretch, p.s.Hkv, 2);
+  const dim3 grid(static_cast<unsigned int>((p.n_tokens + stretch - 1LL) / stretch * 2 * p.s.Hkv));
   return launch_dependent(fa_kv_write_kernel<D, PS>, grid, dim3(WriteTile<D, PS>::kThreads), 0,
                           stream, p, stretch);
 }
@@ -412,7 +459,7 @@ cudaError_t launch_kv_write(const KvWriteParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_kv_read(const KvReadParams& p, cudaStream_t stream) {
-  const int rows = kReadThreads / (p.s.d / 16);
+  const int rows = kReadThreads / (p.s.d / 8) * kReadPasses;
   const dim3 grid((p.total_k + rows - 1) / rows, p.s.Hkv, 2);
   return launch_dependent(p.s.d == 128 ? fa_kv_read_kernel<128> : fa_kv_read_kernel<64>, grid,
                           dim3(kReadThreads), 0, stream, p);

@@ -74,17 +74,20 @@ __device__ __forceinline__ uint4 ld_stream16(const void* p) {
   return v;
 }
 
-// Eight bf16 values / s -> e4m3 codes.  The reciprocal of a power of two is
-// exact, so the product is the quotient; any other scale is divided by.
-__device__ __forceinline__ uint2 quantise8(const uint4& w, float s, float inv, bool pow2) {
+__device__ __forceinline__ uint2 ld_stream8(const void* p) {
+  uint2 v;
+  asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+
+// Eight bf16 values -> e4m3 codes of value * inv (inv = 1 / s for a power-of-two
+// scale: the product is the quotient).
+__device__ __forceinline__ uint2 quantise8(const uint4& w, float inv) {
   const uint32_t x[4] = {w.x, w.y, w.z, w.w};
   uint32_t c[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float lo = __uint_as_float(x[i] << 16), hi = __uint_as_float(x[i] & 0xffff0000u);
-    c[i] = pow2 ? pack_e4m3x2(lo * inv, hi * inv)
-                : pack_e4m3x2(__fdiv_rn(lo, s), __fdiv_rn(hi, s));
-  }
+  for (int i = 0; i < 4; ++i)
+    c[i] = pack_e4m3x2(__uint_as_float(x[i] << 16) * inv, __uint_as_float(x[i] & 0xffff0000u) * inv);
   return make_uint2(c[0] | c[1] << 16, c[2] | c[3] << 16);
 }
 
