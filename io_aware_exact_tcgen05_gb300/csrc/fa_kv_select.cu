@@ -65,77 +65,69 @@ __device__ __forceinline__ int quantise_row(const __nv_bfloat16* q, int8_t* dst)
   return e;
 }
 
+// Four lanes per block, each with a quarter of its 2 * D bounds: a query row costs a
+// block 3.6 instructions (sixteen lanes per block, with two more steps of
+// reduction, took 8.5).  HBM would bound the kernel; the latency of its three dependent
+// loads (length and table, bounds, store) does for all but the longest tables.
 template <int D>
 __global__ void __launch_bounds__(kScoreThreads) fa_block_score_kernel(const SelectParams p) {
-  constexpr int LPB = 2 * D / 16;               // lanes per block: 16 bytes of bounds each
-  constexpr int BPW = 32 / LPB;                 // blocks per warp at a time
-  constexpr int WARPS = kScoreThreads / 32;
+  constexpr int LPB = 4;                        // lanes per block
+  constexpr int VEC = 2 * D / (16 * LPB);       // 16-byte pieces per lane
   __shared__ __align__(16) int8_t s_q[kRowTile][2 * D];
   __shared__ float s_scale[kRowTile];
+  static_assert(kScoreThreads / LPB == kScoreBlocks, "one block per four lanes");
   const int item = blockIdx.y;                  // (request, KV head)
-  const int b = item / p.s.Hkv, hk = item % p.s.Hkv;
-  const int first = blockIdx.x * kScoreBlocks;
-  griddep_wait();
+  const int b = item / p.s.Hkv, hk = item - b * p.s.Hkv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int part = lane % LPB, sub = lane / LPB;
+  const int part = lane % LPB;
+  const int blk = blockIdx.x * kScoreBlocks + threadIdx.x / LPB;
   const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) +
                            static_cast<size_t>(item) * p.rows * D;
-  constexpr int PER = kScoreBlocks / (WARPS * BPW);
-  // the table's entries and the length are read side by side, and the bounds of
-  // all blocks of this warp are on their way while q is quantised
-  float best[PER], ks[PER];
-  int4 w[PER];
-  int pages[PER];
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int blk = first + (i * WARPS + warp) * BPW + sub;
-    pages[i] = blk < p.max_blocks ? p.block_table[static_cast<size_t>(b) * p.max_blocks + blk] : -1;
-  }
+  griddep_wait();
+  // the table's entry and the length are read side by side
+  const int entry = blk < p.max_blocks ? p.block_table[static_cast<size_t>(b) * p.max_blocks + blk] : -1;
   const int n = request_blocks(p, b);
-  if (first >= n) return;
+  if (static_cast<int>(blockIdx.x) * kScoreBlocks >= n) return;
+  const bool ok = blk < n && entry >= 0 && entry < p.s.num_pages;
+  // the bounds are on their way while q is quantised
+  int4 w[VEC];
+  float ks = 0.f;
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int blk = first + (i * WARPS + warp) * BPW + sub;
-    const int page = blk < n ? pages[i] : -1;
-    best[i] = __int_as_float(0xff800000);
-    ks[i] = -1.f;  // no page
-    w[i] = make_int4(0, 0, 0, 0);
-    if (page >= 0 && page < p.s.num_pages) {
-      const size_t tile = static_cast<size_t>(page) * p.s.Hkv + hk;
-      w[i] = __ldg(reinterpret_cast<const int4*>(p.k_bounds + tile * 2 * D + part * 16));
-      ks[i] = p.k_scale[tile];
-    }
+  for (int i = 0; i < VEC; ++i) w[i] = make_int4(0, 0, 0, 0);
+  if (ok) {
+    const size_t tile = static_cast<size_t>(entry) * p.s.Hkv + hk;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+      w[i] = __ldg(reinterpret_cast<const int4*>(p.k_bounds + tile * 2 * D + (i * LPB + part) * 16));
+    ks = p.k_scale[tile];
   }
+  float best = __int_as_float(0xff800000);
   for (int r0 = 0; r0 < p.rows; r0 += kRowTile) {
     const int rows = min(kRowTile, p.rows - r0);
     __syncthreads();
-    for (int r = warp; r < rows; r += WARPS) {
+    for (int r = warp; r < rows; r += kScoreThreads / 32) {
       const int e = quantise_row<D>(q + static_cast<size_t>(r0 + r) * D, s_q[r]);
       if (lane == 0) s_scale[r] = pow2i(e + 2);
     }
     __syncthreads();
+#pragma unroll 2
     for (int r = 0; r < rows; ++r) {
-      const int4 a = *reinterpret_cast<const int4*>(&s_q[r][part * 16]);
-      const float scale = s_scale[r];
+      int u = 0;
 #pragma unroll
-      for (int i = 0; i < PER; ++i) {
-        int u = __dp4a(a.x, w[i].x,
-                       __dp4a(a.y, w[i].y, __dp4a(a.z, w[i].z, __dp4a(a.w, w[i].w, 0))));
-#pragma unroll
-        for (int o = 1; o < LPB; o <<= 1) u += __shfl_xor_sync(0xffffffffu, u, o);
-        const float s = static_cast<float>(u) * ks[i] * scale;
-        if (s > best[i] || s != s) best[i] = s;
+      for (int i = 0; i < VEC; ++i) {
+        const int4 a = *reinterpret_cast<const int4*>(&s_q[r][(i * LPB + part) * 16]);
+        u = __dp4a(a.x, w[i].x, __dp4a(a.y, w[i].y, __dp4a(a.z, w[i].z, __dp4a(a.w, w[i].w, u))));
       }
+      u += __shfl_xor_sync(0xffffffffu, u, 1);
+      u += __shfl_xor_sync(0xffffffffu, u, 2);
+      const float s = static_cast<float>(u) * ks * s_scale[r];
+      if (s > best || s != s) best = s;
     }
   }
-#pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int blk = first + (i * WARPS + warp) * BPW + sub;
-    if (part == 0 && blk < n) {
-      const bool forced = blk < p.n_first || blk >= n - p.n_last;
-      p.keys[static_cast<size_t>(item) * p.max_blocks + blk] =
-          forced ? 0xffffffffu : ks[i] < 0.f ? score_key(__int_as_float(0xff800000)) : score_key(best[i]);
-    }
+  if (part == 0 && blk < n) {
+    const bool forced = blk < p.n_first || blk >= n - p.n_last;
+    p.keys[static_cast<size_t>(item) * p.max_blocks + blk] =
+        forced ? 0xffffffffu : score_key(ok ? best : __int_as_float(0xff800000));
   }
   // the selection may launch now; earlier, its CTAs would take places that this
   // grid's own still need (22.6 us against 18.7 us for 2048 blocks x 64 items)
@@ -145,7 +137,8 @@ __global__ void __launch_bounds__(kScoreThreads) fa_block_score_kernel(const Sel
 // The k = min(k_blocks, n) blocks with the largest keys of one (request, KV
 // head), ascending; equal keys by the lower index.  The k-th largest key T (the
 // largest T with at least k keys >= T) is found two bits at a time: each step
-// counts the keys at three candidates and costs one barrier.  The blocks above T and
+// counts the keys at three candidates and costs one barrier; it ends early when a
+// candidate has exactly k keys at or above it.  The blocks above T and
 // the first of those equal to T are then written in order.  One CTA per item;
 // latency bounds it, so the keys stay in registers (thread t holds blocks t, t +
 // 512, ...) unless there are more than 8192 of them.
@@ -166,8 +159,43 @@ __device__ __forceinline__ void select_blocks(const SelectParams& p, int item, i
       mine[i] = at < n ? keys[at] : 0u;  // 0 is below every candidate
     }
   }
+  // The keys that are not forced agree in their upper bits: the search starts below
+  // them.
+  uint32_t lo = 0xffffffffu, hi = 0u;
+  auto widen = [&](uint32_t key) {
+    if (key != 0xffffffffu) lo = min(lo, key), hi = max(hi, key);
+  };
+  if (kInRegs) {
+#pragma unroll
+    for (int i = 0; i < kRounds; ++i)
+      if (i * kSelectThreads + tid < n) widen(mine[i]);
+  } else {
+    for (int at = tid; at < n; at += kSelectThreads) widen(keys[at]);
+  }
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  if (lane == 0) {
+    s_warp[0][0][warp] = static_cast<int>(lo);
+    s_warp[0][1][warp] = static_cast<int>(hi);
+  }
+  __syncthreads();
+  lo = __reduce_min_sync(0xffffffffu, lane < kSelectWarps ? static_cast<uint32_t>(s_warp[0][0][lane])
+                                                          : 0xffffffffu);
+  hi = __reduce_max_sync(0xffffffffu, lane < kSelectWarps ? static_cast<uint32_t>(s_warp[0][1][lane])
+                                                          : 0u);
   uint32_t T = 0;
-  for (int bit = 30; bit >= 0; bit -= 2) {
+  int bit = 0;
+  if (lo > hi) {
+    T = 0xffffffffu;  // every block is forced
+    bit = -2;
+  } else if (lo == hi) {
+    T = lo;
+    bit = -2;
+  } else {
+    bit = (31 - __clz(lo ^ hi)) & ~1;
+    T = bit < 30 ? hi >> (bit + 2) << (bit + 2) : 0u;
+  }
+  for (; bit >= 0; bit -= 2) {
     int c1 = 0, c2 = 0, c3 = 0;
     const uint32_t t1 = T | 1u << bit, t2 = T | 2u << bit, t3 = T | 3u << bit;
     if (kInRegs) {
@@ -201,8 +229,14 @@ __device__ __forceinline__ void select_blocks(const SelectParams& p, int item, i
     x = __reduce_add_sync(0xffffffffu, x);
     y = __reduce_add_sync(0xffffffffu, y);
     z = __reduce_add_sync(0xffffffffu, z);
+    // exactly k keys from a candidate on: they are the selection, without ties
+    if (z == k || y == k || x == k) {
+      T = (z == k ? t3 : y == k ? t2 : t1) - 1;
+      break;
+    }
     T = z >= k ? t3 : y >= k ? t2 : x >= k ? t1 : T;
   }
+  __syncthreads();  // the counts of the last step have been read
   // keys above T over the whole item, then the order inside it, 512 blocks at a time
   int above = 0;
   if (kInRegs) {
@@ -212,7 +246,7 @@ __device__ __forceinline__ void select_blocks(const SelectParams& p, int item, i
     for (int at = tid; at < n; at += kSelectThreads) above += keys[at] > T;
   }
   above = __reduce_add_sync(0xffffffffu, above);
-  if (lane == 0) s_count[1][0][warp] = above;  // last read before the last step's barrier
+  if (lane == 0) s_count[1][0][warp] = above;
   __syncthreads();
   above = __reduce_add_sync(0xffffffffu, lane < kSelectWarps ? s_count[1][0][lane] : 0);
   int ties = k - above;  // blocks equal to T still to be taken
