@@ -110,7 +110,9 @@ struct Line {
   long long warp_sum[kWarps];
 };
 
-__device__ __forceinline__ void make_line(const PagedDecodeParams& p, int row_blocks, Line& s) {
+// Returns the start of the calling thread's items.
+__device__ __forceinline__ long long make_line(const PagedDecodeParams& p, int row_blocks,
+                                               Line& s) {
   const int items = p.B * p.s.Hkv;
   const int per = (items + kThreads - 1) / kThreads;
   const int lo = min(static_cast<int>(threadIdx.x) * per, items), hi = min(lo + per, items);
@@ -130,6 +132,7 @@ __device__ __forceinline__ void make_line(const PagedDecodeParams& p, int row_bl
   s.prefix[threadIdx.x + 1] = v;
   if (threadIdx.x == 0) s.prefix[0] = 0;
   __syncthreads();
+  return v - own;
 }
 
 // Quotient of non-negative values; nearly always both fit 32 bits, where a
@@ -160,23 +163,24 @@ struct Segment {
   int item, hk, len, n_kb, kb0, n_seg, row0, n_rows;
   bool live;
 
+  // Called by every thread with the start of its items; the one whose items hold
+  // the stretch's start fills the segment in.
   __device__ __forceinline__ void begin(const PagedDecodeParams& p, int row_blocks, int tile_rows,
-                                        const Line& line) {
+                                        const Line& line, long long start) {
     const int items = p.B * p.s.Hkv;
     const long long total = line.prefix[kThreads];
     const long long share = share_of(total, items, gridDim.x);
-    at = share * blockIdx.x;
-    end = min(at + share, total);
-    live = at < end;
-    if (!live) return;
-    int a = 0, z = kThreads;
-    while (z - a > 1) {
-      const int mid = (a + z) >> 1;
-      if (line.prefix[mid] <= at) a = mid; else z = mid;
+    const long long here = share * blockIdx.x;
+    if (here >= total) {
+      if (threadIdx.x == 0) live = false;
+    } else if (start <= here && here < line.prefix[threadIdx.x + 1]) {
+      live = true;
+      at = here;
+      end = min(here + share, total);
+      item = threadIdx.x * ((items + kThreads - 1) / kThreads);
+      in_item = here - start;
+      find(p, row_blocks, tile_rows);
     }
-    item = a * ((items + kThreads - 1) / kThreads);
-    in_item = at - line.prefix[a];
-    find(p, row_blocks, tile_rows);
   }
   __device__ __forceinline__ void next(const PagedDecodeParams& p, int row_blocks, int tile_rows) {
     at += n_seg;
@@ -325,9 +329,9 @@ __global__ void __launch_bounds__(kThreads, Plan<1>::kCtasPerSm)
 
   griddep_launch_dependents();  // the merge waits for this grid's completion
   griddep_wait();
-  make_line(p, row_blocks, s.line);
+  const long long start = make_line(p, row_blocks, s.line);
   const Segment& sg = s.seg;
-  if (tid == 0) s.seg.begin(p, row_blocks, 8, s.line);
+  s.seg.begin(p, row_blocks, 8, s.line, start);
   __syncthreads();
   while (sg.live) {
     uint4 kr[2][KC];
@@ -561,7 +565,10 @@ __global__ void __launch_bounds__(kThreads, Plan<1>::kCtasPerSm)
 // memory as B operands, and each warp adds its 32 channels of O^T (at d = 64 two
 // warps share 32 channels and take two of the blocks each).  So the accumulators
 // of a warp are 32 channels x 32 rows, a quarter of what a warp on its own would
-// hold (its 255 registers left 8 warps per SM: 68 us where this takes REPLACE).
+// hold.  Latency bounds it (a step of 64 keys takes 4100 clocks, of which the two products
+// 1800 and the weights 1230, with 12 warps per SM): 62 us for 24 requests of 500 to 9000 keys, 32
+// rows, 4 KV heads (2.0 TB/s), where a warp with all 32 rows to itself took 68 us and two passes of
+// 16 rows 69 us.
 // The running maxima are the CTA's; the vote on moving them is the barrier that
 // hands the weights over.
 template <int D, int NT>
@@ -595,9 +602,9 @@ __global__ void __launch_bounds__(kThreads, Plan<NT>::kCtasPerSm)
 
   griddep_launch_dependents();  // the merge waits for this grid's completion
   griddep_wait();
-  make_line(p, row_blocks, s.line);
+  const long long start = make_line(p, row_blocks, s.line);
   const Segment& sg = s.seg;
-  if (tid == 0) s.seg.begin(p, row_blocks, R, s.line);
+  s.seg.begin(p, row_blocks, R, s.line, start);
   __syncthreads();
   while (sg.live) {
     const int steps = (sg.n_seg + kWarps - 1) / kWarps;
