@@ -48,7 +48,8 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kBlockKeys = 16;
 constexpr int kSms = 152;
-constexpr int kMinShare = 8;        // 16-key blocks a CTA takes at least
+constexpr int kMinShare = 8;        // places in the line a CTA takes at least
+constexpr int kSegmentCost = 16;    // places a segment's fixed cost takes in the line
 constexpr float kLag = 6.f;         // how far (log2) a weight may exceed the running maximum
 constexpr float kWeightUnit = 512.f;
 
@@ -103,7 +104,14 @@ __device__ __forceinline__ int item_blocks(const PagedDecodeParams& p, int item)
   return (request_len(p, item / p.s.Hkv) + kBlockKeys - 1) / kBlockKeys;
 }
 
-// Where the blocks of the items lie in the one long line: thread t of the CTA
+// Places of a (request, KV head) and row block in the line: its blocks behind
+// kSegmentCost places without work, for what beginning and ending a segment costs (8000 to
+// 10000 clocks; without them 62 us where this takes 52 us: 32 rows of 24 ragged requests).
+__device__ __forceinline__ long long unit_places(int n_kb) {
+  return n_kb > 0 ? n_kb + kSegmentCost : 0;
+}
+
+// Where the units of the items lie in the one long line: thread t of the CTA
 // sums items [t * per, (t + 1) * per), prefix[t] is the start of its first one.
 struct Line {
   long long prefix[kThreads + 1];
@@ -117,7 +125,7 @@ __device__ __forceinline__ long long make_line(const PagedDecodeParams& p, int r
   const int per = (items + kThreads - 1) / kThreads;
   const int lo = min(static_cast<int>(threadIdx.x) * per, items), hi = min(lo + per, items);
   long long own = 0;
-  for (int i = lo; i < hi; ++i) own += item_blocks(p, i);
+  for (int i = lo; i < hi; ++i) own += unit_places(item_blocks(p, i));
   own *= row_blocks;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   long long v = own;
@@ -142,15 +150,14 @@ __device__ __forceinline__ long long quotient(long long a, int b) {
                            : a / b;
 }
 
-// Blocks per CTA.  At least 8, so that a short request is not cut into pieces
-// that cost more to join than to read, but no more than an item has on average:
-// a segment has a fixed cost of some microseconds, so CTAs should not queue up
-// tiny ones (208 items of one block: 54 us in eights, 22 us one by one).
+// Places per CTA.  At least 8, so that a short request is not cut into pieces that
+// cost more to join than to read, but no more than an item has on average, so that
+// CTAs do not queue up tiny ones (208 items of one block: 54 us in eights, 22 us one by one).
 __device__ __forceinline__ long long share_of(long long total, int items, int ctas) {
   const long long even = quotient(total + ctas - 1, ctas);
   const long long least = min(static_cast<long long>(kMinShare), max(quotient(total, items), 1ll));
   if (even <= 16) return max(even, least);
-  return (even + 15) & ~15ll;  // fewer stretches that straddle two items
+  return (even + 3) & ~3ll;  // a step of the wide kernel is four blocks
 }
 
 // A CTA walks its stretch of the line segment by segment: blocks [kb0, kb0 + n_seg)
@@ -188,15 +195,26 @@ struct Segment {
     live = at < end;
     if (live) find(p, row_blocks, tile_rows);
   }
-  // from (item, in_item), which may lie behind the item's end
+  // The segment at (item, in_item), which may lie behind the item's end or in
+  // front of a unit's blocks.
   __device__ __forceinline__ void find(const PagedDecodeParams& p, int row_blocks, int tile_rows) {
     n_kb = item_blocks(p, item);
-    while (in_item >= static_cast<long long>(n_kb) * row_blocks) {
-      in_item -= static_cast<long long>(n_kb) * row_blocks;
+    while (in_item >= unit_places(n_kb) * row_blocks) {
+      in_item -= unit_places(n_kb) * row_blocks;
       n_kb = item_blocks(p, ++item);
     }
-    const int rb = static_cast<int>(quotient(in_item, n_kb));
-    kb0 = static_cast<int>(in_item - static_cast<long long>(rb) * n_kb);
+    const int places = n_kb + kSegmentCost;
+    const int rb = static_cast<int>(quotient(in_item, places));
+    kb0 = static_cast<int>(in_item - static_cast<long long>(rb) * places) - kSegmentCost;
+    if (kb0 < 0) {
+      at -= kb0;
+      in_item -= kb0;
+      kb0 = 0;
+      if (at >= end) {
+        live = false;
+        return;
+      }
+    }
     n_seg = static_cast<int>(min(static_cast<long long>(n_kb - kb0), end - at));
     const int b = item / p.s.Hkv;
     hk = item - b * p.s.Hkv;
@@ -896,9 +914,9 @@ __global__ void __launch_bounds__(kThreads)
   const int per = (items + kThreads - 1) / kThreads;
   long long start = line.prefix[item / per];
   for (int i = item / per * per; i < item; ++i)
-    start += static_cast<long long>(item_blocks(p, i)) * row_blocks;
+    start += unit_places(item_blocks(p, i)) * row_blocks;
   const int rb = row / tile_rows, r = row - rb * tile_rows;
-  start += static_cast<long long>(rb) * n_kb;
+  start += rb * unit_places(n_kb) + kSegmentCost;  // the unit's first block
   const long long share = share_of(line.prefix[kThreads], items, ctas);
   int c0 = 0, c1 = 0;
   if (share <= 0x7fffffffll) {
@@ -986,7 +1004,8 @@ cudaError_t launch_nt(const PagedDecodeParams& p, cudaStream_t stream) {
   const int row_blocks = (p.rows + 8 * NT - 1) / (8 * NT);
   // no more CTAs than there can be shares
   const long long list = p.sel ? p.max_sel : p.max_blocks;
-  const long long most = list * (p.s.page_size / kBlockKeys) * p.B * p.s.Hkv * row_blocks;
+  const long long most =
+      ((list << p.block_shift) + kSegmentCost) * p.B * p.s.Hkv * row_blocks;
   const int ctas = static_cast<int>(min(static_cast<long long>(kSms * Plan<NT>::kCtasPerSm), most));
   float* part_o = static_cast<float*>(p.workspace);
   float2* part_ml = reinterpret_cast<float2*>(part_o + 2 * static_cast<size_t>(ctas) * 8 * NT * D);
