@@ -300,6 +300,10 @@ fa_status fa_decode_noalloc(const void* q, const void* k_cache, const void* v_ca
  *    Requests may share pages that nothing writes to.
  *  * Page and slot offsets are computed in 64 bits; a cache may be larger than
  *    2^32 bytes.  Packed tokens per call: at most 2^30.
+ *  * A workspace belongs to one call at a time: calls that can overlap on the GPU
+ *    (on streams without ordering between them, or in graphs that replay side by
+ *    side) need workspaces of their own.  A call that writes pages must be
+ *    ordered before the calls that read them, as any producer and consumer.
  */
 
 /*
@@ -446,11 +450,11 @@ fa_status fa_selftest_wait_timeout(unsigned int* result, cudaStream_t stream);
 
 /* Profiling hook (the pages ask that a timing confirm which kernel actually
    ran).  start/stop are cudaEvent_t handles created by the caller.  The next
-   fa_fwd, fa_bwd or fa_decode call made on this host thread records `start`
+   fa_fwd, fa_bwd, fa_decode or fa_decode_paged_fp8 call made on this host thread records `start`
    on its stream right before its main kernel (fa_fwd: the attention kernel;
    fa_bwd: the key-tile kernel, not the preprocess or dQ-convert kernels;
-   fa_decode: the split partial kernel, not the merge) and `stop` right after
-   it, then the hook disarms itself.  Passing NULL for both disarms it.  The
+   fa_decode and fa_decode_paged_fp8: the split partial kernel, not the merge)
+   and `stop` right after it, then the hook disarms itself.  Passing NULL for both disarms it.  The
    events are not owned by the library. */
 fa_status fa_profile_next_launch(cudaEvent_t start, cudaEvent_t stop);
 

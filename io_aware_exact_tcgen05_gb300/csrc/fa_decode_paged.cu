@@ -345,8 +345,10 @@ __global__ void __launch_bounds__(kThreads, Plan<1>::kCtasPerSm)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
 
-  griddep_launch_dependents();  // the merge waits for this grid's completion
+  // First the wait, then the signal: once the merge may launch, what this call
+  // reads (lengths, lists) is complete, so the merge may read them before its own wait.
   griddep_wait();
+  griddep_launch_dependents();
   const long long start = make_line(p, row_blocks, s.line);
   const Segment& sg = s.seg;
   s.seg.begin(p, row_blocks, 8, s.line, start);
@@ -618,8 +620,10 @@ __global__ void __launch_bounds__(kThreads, Plan<NT>::kCtasPerSm)
   const int g = lane >> 2, t = lane & 3;
   const int dw = warp % DW, vb0 = (warp / DW) * VB;  // channels [32 dw, ..), blocks [vb0, ..)
 
-  griddep_launch_dependents();  // the merge waits for this grid's completion
+  // First the wait, then the signal: once the merge may launch, what this call
+  // reads (lengths, lists) is complete, so the merge may read them before its own wait.
   griddep_wait();
+  griddep_launch_dependents();
   const long long start = make_line(p, row_blocks, s.line);
   const Segment& sg = s.seg;
   s.seg.begin(p, row_blocks, R, s.line, start);
@@ -906,8 +910,8 @@ __global__ void __launch_bounds__(kThreads)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int item = blockIdx.y;
   const int row = blockIdx.x * kRows + warp / kSplit, part = warp % kSplit;
-  // The line is worked out while the partial kernel still runs: nothing that kernel
-  // writes is read for it.
+  // The line is worked out while the partial kernel still runs: it takes only the
+  // lengths and lists, which were complete before that kernel let this one launch.
   make_line(p, row_blocks, line);
   const int n_kb = item_blocks(p, item);
   const int items = p.B * p.s.Hkv;

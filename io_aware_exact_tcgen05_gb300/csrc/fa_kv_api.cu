@@ -140,6 +140,9 @@ fa_status fa_kv_write_fp8(const void* k, const void* v, long long k_stride_h, lo
   FA_TRY(need_ptr(v_scale, "v_scale", 4));
   if (k_bounds) FA_TRY(need_ptr(k_bounds, "k_bounds", 16));
   if (n_tokens == 0) return fa::api_ok();
+  if (2LL * Hkv * ((n_tokens + 15) / 16) >= 1LL << 31)
+    return api_fail(FA_ERR_INVALID_ARG, "n_tokens (%d) x Hkv (%d) is too large for one call",
+                    n_tokens, Hkv);
   FA_TRY(need_ptr(k, "k", 16));
   FA_TRY(need_ptr(v, "v", 16));
   FA_TRY(need_ptr(slot_map, "slot_map", 8));

@@ -351,6 +351,15 @@ def test_decode_rows_that_see_nothing():
 def test_decode_many_requests():
     lens = [int(x) for x in np.random.RandomState(0).randint(0, 90, 200)]
     _decode_case(lens, 2, 1, 1, 64, 16, seed=4)
+    lens = [int(x) for x in np.random.RandomState(1).randint(0, 20, 700)]
+    _decode_case(lens, 2, 2, 1, 64, 16, seed=5)  # 1400 items: several for each thread of the plan
+    _decode_case(lens[:300], 18, 2, 1, 64, 16, seed=6)
+
+
+def test_decode_many_rows():
+    # several row blocks of the wide kernel, the last one partial, over a few CTAs' stretches
+    _decode_case([700, 31], 24, 2, 11, 64, 32, seed=7)
+    _decode_case([150], 32, 1, 5, 128, 64, seed=8)
 
 
 def test_decode_large_logits_and_zero_scale():
@@ -596,6 +605,62 @@ def test_captured_step_replays_with_other_lengths():
         graph.replay()
         torch.cuda.synchronize()
         check(lens, *args)
+
+
+def test_back_to_back_steps_without_a_host_wait():
+    """Lengths, tokens and lists change from call to call with nothing but the stream
+    between them; every step's results equal those of the same steps taken one by one."""
+    heads, Hq, d, ps, room, B = 2, 8, 64, 16, 40, 5
+    pages = B * room
+    gen = torch.Generator().manual_seed(70)
+    start = [3, 200, 0, 77, 410]
+    kv = [randn_bf16(gen, 2, heads, B, d).to(DEV) for _ in range(24)]
+    qs = [randn_bf16(gen, B, Hq, 1, d).to(DEV) for _ in range(24)]
+
+    def steps(wait):
+        cache = make_cache(71, pages, heads, ps, d)
+        dev = on_gpu(cache)
+        table = i32(make_table(5, start, ps, pages, room=room))
+        free = i32([p for p in range(pages) if p not in set(table.flatten().tolist())])
+        lens, new, out, at = i32(start), i32([1] * B), [], 0
+        filler = torch.zeros(1 << 22, device=DEV)
+        for (k, v), q in zip(kv, qs):
+            filler.add_(1.0)  # work for the next call's early launch to overlap with
+            slots, _, lens, _, used = fa.fa_kv_assign(lens, new, ps, table, free, B)
+            free = free[B:]   # one page for each request that might have taken one
+            fa.fa_kv_write_fp8(k, v, slots, *dev[:4], k_bounds=dev[4])
+            sel, n_sel = fa.fa_select_blocks(q, dev[4], dev[2], table, lens, ps, 6)
+            if wait:
+                torch.cuda.synchronize()
+            a = fa.fa_decode_paged_fp8(q, *dev[:4], table, lens, 0.125)
+            b = fa.fa_decode_paged_fp8(q, *dev[:4], table, lens, 0.125, sel=sel, n_sel=n_sel)
+            out.append((lens, sel, *a, *b))
+            if wait:
+                torch.cuda.synchronize()
+        torch.cuda.synchronize()
+        return out
+
+    for x, y in zip(steps(False), steps(True)):
+        assert all(torch.equal(a, b) for a, b in zip(x, y))
+
+
+def test_two_streams_at_once_with_workspaces_of_their_own():
+    cache = make_cache(80, 300, 2, 16, 128)
+    kc, vc, ks, vs, kb = on_gpu(cache)
+    jobs = []
+    for seed, lens, Sq in ((1, [2500, 1200], 1), (2, [900, 700, 1300], 4)):
+        table = i32(make_table(seed, lens, 16, 300))
+        q = randn_bf16(torch.Generator().manual_seed(seed), len(lens), 16, Sq, 128).to(DEV)
+        ref = fa.fa_decode_paged_fp8(q, kc, vc, ks, vs, table, i32(lens), 0.1)
+        jobs.append((torch.cuda.Stream(), q, table, i32(lens), ref, []))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, q, table, lens, _, got in jobs:
+            got.append(fa.fa_decode_paged_fp8(q, kc, vc, ks, vs, table, lens, 0.1, stream=s))
+    torch.cuda.synchronize()
+    for *_, ref, got in jobs:
+        for o, lse in got:
+            assert torch.equal(o, ref[0]) and torch.equal(lse, ref[1])
 
 
 def test_calls_on_a_side_stream_and_repeatability():
