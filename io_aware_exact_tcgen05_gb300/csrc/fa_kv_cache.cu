@@ -369,55 +369,66 @@ __global__ void __launch_bounds__(WriteTile<D, PS>::kThreads, 640 / WriteTile<D,
 //
 // Packed row r of KV head h is code * scale of the sequence's token, rounded to
 // bf16 (exact for power-of-two scales: e4m3 has 4 significant bits).  HBM bounds
-// it (1 byte read, 2 written per element).  A thread turns 8 codes into 16 bytes, so
-// a warp's stores are whole 512-byte pieces, and has four rows' loads in flight.
+// it (1 byte read, 2 written per element).  A CTA takes 64 packed rows: one thread a row
+// finds its sequence, page and scale, once; then a thread turns 8 codes into 16 bytes, so
+// that a warp's stores are whole 512-byte pieces, with four rows' loads in flight.  (With
+// every thread finding its own rows the lookups took 82% of the issue slots.)
 constexpr int kReadThreads = 256;
-constexpr int kReadPasses = 4;
+constexpr int kReadRows = 64;
 
 template <int D>
 __global__ void __launch_bounds__(kReadThreads) fa_kv_read_kernel(const KvReadParams p) {
   constexpr int CPR = D / 8;
   constexpr int ROWS = kReadThreads / CPR;  // rows of one pass
-  const int col = threadIdx.x % CPR;
+  constexpr int PASSES = kReadRows / ROWS;
+  // a row's first code, -1: zeros, -2: the row stays as it was
+  __shared__ long long s_from[kReadRows];
+  __shared__ float s_scale[kReadRows];
   const int h = blockIdx.y;
   const bool is_v = blockIdx.z != 0;
-  const int ps = p.s.page_size, shift = 31 - __clz(ps);
-  const uint8_t* cache = static_cast<const uint8_t*>(is_v ? p.v_cache : p.k_cache) + col * 8;
-  const float* scales = is_v ? p.v_scale : p.k_scale;
-  uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(is_v ? p.v : p.k) +
-                                        static_cast<size_t>(h) * p.total_k * D) + col;
-  long long r = static_cast<long long>(blockIdx.x) * (ROWS * kReadPasses) + threadIdx.x / CPR;
+  const long long r0 = static_cast<long long>(blockIdx.x) * kReadRows;
   griddep_wait();
-  // last sequence with cu_k <= r
-  int a = 0;
-  for (int z = p.nseq; z - a > 1;) {
-    const int mid = (a + z) >> 1;
-    if (p.cu_k[mid] <= r) a = mid; else z = mid;
-  }
-  uint2 w[kReadPasses];
-  float s[kReadPasses];
-  bool mine[kReadPasses];
-#pragma unroll
-  for (int i = 0; i < kReadPasses; ++i, r += ROWS) {
-    while (a + 1 < p.nseq && p.cu_k[a + 1] <= r) ++a;
+  if (threadIdx.x < kReadRows) {
+    const long long r = r0 + threadIdx.x;
+    const int ps = p.s.page_size, shift = 31 - __clz(ps);
+    int a = 0;  // last sequence with cu_k <= r
+    for (int z = p.nseq; z - a > 1;) {
+      const int mid = (a + z) >> 1;
+      if (p.cu_k[mid] <= r) a = mid; else z = mid;
+    }
     const long long pos = r - p.cu_k[a];
-    // rows behind the last sequence (and the buffers) stay as they were
-    mine[i] = r < p.total_k && pos >= 0 && r < p.cu_k[a + 1];
-    w[i] = make_uint2(0u, 0u);
-    s[i] = 0.f;
-    if (mine[i] && (pos >> shift) < p.max_blocks) {
-      const int page = p.block_table[static_cast<long long>(a) * p.max_blocks + (pos >> shift)];
-      if (page >= 0 && page < p.s.num_pages) {
-        const size_t tile = static_cast<size_t>(page) * p.s.Hkv + h;
-        s[i] = scales[tile];
-        w[i] = ld_stream8(cache + (tile * ps + static_cast<int>(pos & (ps - 1))) * D);
+    long long from = -2;
+    float scale = 0.f;
+    if (r < p.total_k && pos >= 0 && r < p.cu_k[a + 1]) {
+      from = -1;
+      if ((pos >> shift) < p.max_blocks) {
+        const int page = p.block_table[static_cast<long long>(a) * p.max_blocks + (pos >> shift)];
+        if (page >= 0 && page < p.s.num_pages) {
+          const long long tile = static_cast<long long>(page) * p.s.Hkv + h;
+          from = (tile * ps + (pos & (ps - 1))) * D;
+          scale = (is_v ? p.v_scale : p.k_scale)[tile];
+        }
       }
     }
+    s_from[threadIdx.x] = from;
+    s_scale[threadIdx.x] = scale;
   }
-  r -= static_cast<long long>(ROWS) * kReadPasses;
+  __syncthreads();
+  const int col = threadIdx.x % CPR, row = threadIdx.x / CPR;
+  const uint8_t* cache = static_cast<const uint8_t*>(is_v ? p.v_cache : p.k_cache) + col * 8;
+  uint4* out = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(is_v ? p.v : p.k) +
+                                        (static_cast<size_t>(h) * p.total_k + r0) * D) + threadIdx.x;
+  uint2 w[PASSES];
+  long long from[PASSES];
 #pragma unroll
-  for (int i = 0; i < kReadPasses; ++i, r += ROWS)
-    if (mine[i]) out[r * CPR] = dequantise8(w[i], s[i]);
+  for (int i = 0; i < PASSES; ++i) {
+    from[i] = s_from[row + i * ROWS];
+    w[i] = make_uint2(0u, 0u);
+    if (from[i] >= 0) w[i] = ld_stream8(cache + from[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < PASSES; ++i)
+    if (from[i] > -2) out[i * kReadThreads] = dequantise8(w[i], s_scale[row + i * ROWS]);
 }
 
 }  // namespace
@@ -459,8 +470,7 @@ cudaError_t launch_kv_write(const KvWriteParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_kv_read(const KvReadParams& p, cudaStream_t stream) {
-  const int rows = kReadThreads / (p.s.d / 8) * kReadPasses;
-  const dim3 grid((p.total_k + rows - 1) / rows, p.s.Hkv, 2);
+  const dim3 grid((p.total_k + kReadRows - 1) / kReadRows, p.s.Hkv, 2);
   return launch_dependent(p.s.d == 128 ? fa_kv_read_kernel<128> : fa_kv_read_kernel<64>, grid,
                           dim3(kReadThreads), 0, stream, p);
 }
