@@ -93,14 +93,16 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
+// Lengths and counts are read in L2: the merge asks before its own wait, when only L2 is
+// sure to hold what kernels before the partial one wrote.
 __device__ __forceinline__ int request_len(const PagedDecodeParams& p, int b) {
-  return static_cast<int>(min(static_cast<long long>(max(p.seqlens[b], 0)),
+  return static_cast<int>(min(static_cast<long long>(max(__ldcg(p.seqlens + b), 0)),
                               static_cast<long long>(p.max_blocks) * p.s.page_size));
 }
 
 // 16-key blocks of a (request, KV head).
 __device__ __forceinline__ int item_blocks(const PagedDecodeParams& p, int item) {
-  if (p.sel) return min(max(p.n_sel[item], 0), p.max_sel) << p.block_shift;
+  if (p.sel) return min(max(__ldcg(p.n_sel + item), 0), p.max_sel) << p.block_shift;
   return (request_len(p, item / p.s.Hkv) + kBlockKeys - 1) / kBlockKeys;
 }
 
@@ -586,9 +588,10 @@ __global__ void __launch_bounds__(kThreads, Plan<1>::kCtasPerSm)
 // warps share 32 channels and take two of the blocks each).  So the accumulators
 // of a warp are 32 channels x 32 rows, a quarter of what a warp on its own would
 // hold.  Latency bounds it (a step of 64 keys takes 4100 clocks, of which the two products
-// 1800 and the weights 1230, with 12 warps per SM): 62 us for 24 requests of 500 to 9000 keys, 32
-// rows, 4 KV heads (2.0 TB/s), where a warp with all 32 rows to itself took 68 us and two passes of
-// 16 rows 69 us.
+// 1800 and the weights 1230, with 12 warps per SM): 52 us for 24 requests of 500 to 9000 keys, 32
+// rows, 4 KV heads (2.4 TB/s).  Before segments were counted in the line and the merge was a
+// dependent launch, it took 66 us where a warp with all 32 rows to itself took 68 us and two
+// passes of 16 rows 69 us.
 // The running maxima are the CTA's; the vote on moving them is the barrier that
 // hands the weights over.
 template <int D, int NT>

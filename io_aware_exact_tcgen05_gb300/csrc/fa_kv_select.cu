@@ -31,9 +31,11 @@ __device__ __forceinline__ uint32_t score_key(float s) {
   return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
+// (Read in L2: the selection asks before its own wait, when only L2 is sure to hold what
+// kernels before the scores wrote.)
 __device__ __forceinline__ int request_blocks(const SelectParams& p, int b) {
   const int ps = p.s.page_size;
-  const long long n = min(static_cast<long long>(max(p.seqlens[b], 0)),
+  const long long n = min(static_cast<long long>(max(__ldcg(p.seqlens + b), 0)),
                           static_cast<long long>(p.max_blocks) * ps);
   return static_cast<int>((n + ps - 1) / ps);
 }
