@@ -290,7 +290,7 @@ fa_status fa_decode_noalloc(const void* q, const void* k_cache, const void* v_ca
  *  * k_cache, v_cache: e4m3 bytes (OCP FP8 E4M3) [num_pages, Hkv, page_size, d],
  *    16-byte aligned; page_size is 16, 32, 64 or 128, d is 64 or 128.
  *  * k_scale, v_scale: fp32 [num_pages, Hkv], one per (page, KV head); a cached
- *    value is code * scale.  Scales are finite and > 0.
+ *    value is code * scale.  Scales lie in [2^-100, 2^119].
  *  * k_bounds: int8 [num_pages, Hkv, 2, d], 16-byte aligned: per channel the
  *    largest (row 0) and the smallest (row 1) key code of the page in units of 4
  *    codes, rounded outwards (up and down).  Only fa_select_blocks reads it.

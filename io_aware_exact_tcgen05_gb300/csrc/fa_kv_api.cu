@@ -264,7 +264,9 @@ fa_status fa_select_blocks(const void* q, const int8_t* k_bounds, const float* k
 
 size_t fa_decode_paged_fp8_workspace_size(int B, int Hq, int Hkv, int Sq, int d) {
   if (B < 1 || Hq < 1 || Hkv < 1 || Sq < 1 || d < 1 || Hq % Hkv != 0) return 0;
-  return fa::decode_paged_workspace(B, Hkv, Hq / Hkv * Sq, d);
+  const long long rows = 1LL * (Hq / Hkv) * Sq;
+  if (rows > 0x7fffffffLL) return 0;  // the call refuses it
+  return fa::decode_paged_workspace(B, Hkv, static_cast<int>(rows), d);
 }
 
 fa_status fa_decode_paged_fp8(const void* q, const void* k_cache, const void* v_cache,

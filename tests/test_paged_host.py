@@ -223,6 +223,13 @@ def test_decode_refuses_shapes(lib):
     assert fa.fa_decode_paged_fp8_workspace_size(1, 3, 2, 1, 64) == 0
 
 
+def test_decode_rows_past_32_bits(lib):
+    """65536 x 65537 rows are 65536 in 32 bits; 65536 x 32768 are negative there."""
+    for Sq in (65537, 32768):
+        assert fa.fa_decode_paged_fp8_workspace_size(1, 65536, 1, Sq, 64) == 0
+        assert _decode(lib, B=1, Hq=65536, Hkv=1, Sq=Sq) == fa.FA_ERR_INVALID_ARG
+
+
 def test_bindings_refuse_host_tensors(lib):
     z = torch.zeros
     with pytest.raises(TypeError):
