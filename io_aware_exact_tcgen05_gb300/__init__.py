@@ -443,6 +443,14 @@ def _dims(t, name, ndim):
     return t.shape
 
 
+def _int(x, name):
+    """x as a C int: a larger value would be cut to its low 32 bits on the way."""
+    x = int(x)
+    if not -0x80000000 <= x <= 0x7fffffff:
+        raise ValueError(f"{name} ({x}) does not fit 32 bits")
+    return x
+
+
 def _new(shape, dtype, dev, stream):
     """An output or workspace for a call on `stream`: memory that this thread's
     current stream allocates is kept from reuse until `stream` is done with it."""
@@ -494,13 +502,13 @@ def fa_kv_assign(seqlens, newlens, page_size: int, block_table, free_pages, tota
     _have(newlens, "newlens", _I32, (B,), dev)
     n_free, = _dims(free_pages, "free_pages", 1)
     _have(free_pages, "free_pages", _I32, (n_free,), dev)
-    total_new = int(total_new)
+    total_new, page_size = _int(total_new, "total_new"), _int(page_size, "page_size")
     slot_map = _out(slot_map, "slot_map", (total_new,), _I64, dev, stream)
     cu_new = _out(cu_new, "cu_new", (B + 1,), _I32, dev, stream)
     seqlens_out = _out(seqlens_out, "seqlens_out", (B,), _I32, dev, stream)
     cu_seqlens_k = _out(cu_seqlens_k, "cu_seqlens_k", (B + 1,), _I32, dev, stream)
     n_used = _out(n_used, "n_used", (1,), _I32, dev, stream)
-    st = lib.fa_kv_assign(seqlens.data_ptr(), newlens.data_ptr(), B, int(page_size),
+    st = lib.fa_kv_assign(seqlens.data_ptr(), newlens.data_ptr(), B, page_size,
                           block_table.data_ptr(), max_blocks, free_pages.data_ptr(), n_free,
                           slot_map.data_ptr(), total_new, cu_new.data_ptr(),
                           seqlens_out.data_ptr(), cu_seqlens_k.data_ptr(), n_used.data_ptr(),
@@ -520,7 +528,7 @@ def fa_kv_write_fp8(k, v, slot_map, k_cache, v_cache, k_scale, v_scale, k_bounds
     lib, dev = load_library(), _device()
     num_pages, Hkv, ps, d = _need_cache(k_cache, v_cache, k_scale, v_scale, dev)
     n, = _dims(slot_map, "slot_map", 1)
-    _have(slot_map, "slot_map", _I64, (n,), dev)
+    _have(slot_map, "slot_map", _I64, (_int(n, "the number of tokens"),), dev)
     strides = []
     for t, name in ((k, "k"), (v, "v")):
         if not (isinstance(t, torch.Tensor) and t.dtype == _BF16 and t.get_device() == dev
@@ -550,7 +558,7 @@ def fa_kv_read_fp8(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens_k
     nseq, max_blocks = _dims(block_table, "block_table", 2)
     _have(block_table, "block_table", _I32, (nseq, max_blocks), dev)
     _have(cu_seqlens_k, "cu_seqlens_k", _I32, (nseq + 1,), dev)
-    total_k = int(total_k)
+    total_k = _int(total_k, "total_k")
     k = _out(k, "k", (Hkv, total_k, d), _BF16, dev, stream)
     v = _out(v, "v", (Hkv, total_k, d), _BF16, dev, stream)
     st = lib.fa_kv_read_fp8(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(),
@@ -581,7 +589,8 @@ def fa_select_blocks(q, k_bounds, k_scale, block_table, seqlens_k, page_size: in
     _have(k_bounds, "k_bounds", _I8, (num_pages, Hkv, 2, d), dev)
     _have(block_table, "block_table", _I32, (B, max_blocks), dev)
     _have(seqlens_k, "seqlens_k", _I32, (B,), dev)
-    k_blocks = int(k_blocks)
+    k_blocks, page_size = _int(k_blocks, "k_blocks"), _int(page_size, "page_size")
+    n_first, n_last = _int(n_first, "n_first"), _int(n_last, "n_last")
     sel = _out(sel, "sel", (B, Hkv, max(k_blocks, 0)), _I32, dev, stream)
     n_sel = _out(n_sel, "n_sel", (B, Hkv), _I32, dev, stream)
     workspace = _workspace(workspace, lib.fa_select_blocks_workspace_size(B, Hkv, max_blocks), dev,
@@ -589,7 +598,7 @@ def fa_select_blocks(q, k_bounds, k_scale, block_table, seqlens_k, page_size: in
     st = lib.fa_select_blocks(q.data_ptr(), k_bounds.data_ptr(), k_scale.data_ptr(),
                               block_table.data_ptr(), seqlens_k.data_ptr(), sel.data_ptr(),
                               n_sel.data_ptr(), B, Hq, Hkv, Sq, num_pages, max_blocks,
-                              int(page_size), d, k_blocks, int(n_first), int(n_last),
+                              page_size, d, k_blocks, n_first, n_last,
                               workspace.data_ptr(), workspace.nbytes, _stream(stream))
     _check(st, "fa_select_blocks")
     return sel, n_sel

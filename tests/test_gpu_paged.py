@@ -678,6 +678,22 @@ def test_calls_on_a_side_stream_and_repeatability():
         assert torch.equal(o, first[0]) and torch.equal(lse, first[1])
 
 
+def test_sizes_past_32_bits_are_refused_by_the_calls():
+    lens, table = i32([20, 3]), i32(np.zeros((2, 4)))
+    with pytest.raises(ValueError, match="page_size"):
+        fa.fa_kv_assign(lens, lens, (1 << 32) + 16, table, i32([0]), 4)
+    with pytest.raises(ValueError, match="total_new"):
+        fa.fa_kv_assign(lens, lens, 16, table, i32([0]), (1 << 32) + 4)
+    kc, vc, ks, vs, kb = on_gpu(make_cache(1, 2, 1, 16, 64))
+    with pytest.raises(ValueError, match="total_k"):
+        fa.fa_kv_read_fp8(kc, vc, ks, vs, table, i32([0, 1, 2]), (1 << 32) + 2)
+    q = torch.zeros(2, 1, 1, 64, dtype=torch.bfloat16, device=DEV)
+    for kw in (dict(k_blocks=(1 << 32) + 2), dict(n_first=1 << 32), dict(n_last=1 << 32),
+               dict(page_size=(1 << 32) + 16)):
+        with pytest.raises(ValueError, match=next(iter(kw))):
+            fa.fa_select_blocks(q, kb, ks, table, lens, **{"page_size": 16, "k_blocks": 2, **kw})
+
+
 def test_outputs_and_workspaces_are_all_that_is_written():
     guard = 4096
 

@@ -230,6 +230,12 @@ def test_decode_rows_past_32_bits(lib):
         assert _decode(lib, B=1, Hq=65536, Hkv=1, Sq=Sq) == fa.FA_ERR_INVALID_ARG
 
 
+@pytest.mark.parametrize("x", [1 << 31, (1 << 32) + 16, -(1 << 31) - 1])
+def test_sizes_past_32_bits_are_refused(x):
+    with pytest.raises(ValueError, match="32 bits"):
+        fa._int(x, "page_size")
+
+
 def test_bindings_refuse_host_tensors(lib):
     z = torch.zeros
     with pytest.raises(TypeError):
