@@ -452,11 +452,15 @@ def _int(x, name):
 
 
 def _new(shape, dtype, dev, stream):
-    """An output or workspace for a call on `stream`: memory that this thread's
-    current stream allocates is kept from reuse until `stream` is done with it."""
-    t = torch.empty(shape, dtype=dtype, device=dev)
-    if stream is not None and stream != torch.cuda.current_stream():
-        t.record_stream(stream)
+    """An output or workspace for a call on `stream`, from that stream's memory: what
+    the current stream's allocations are cut from may still be in use by its
+    pending work.  The current stream may go on to use it (after a wait)."""
+    here = None if stream is None else torch.cuda.current_stream()
+    if stream == here:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=dev)
+    t.record_stream(here)
     return t
 
 

@@ -678,6 +678,27 @@ def test_calls_on_a_side_stream_and_repeatability():
         assert torch.equal(o, first[0]) and torch.equal(lse, first[1])
 
 
+def test_outputs_on_a_side_stream_are_not_memory_in_use():
+    """Memory that the current stream freed, with its own writes still to come, must not
+    become the output of a call on another stream."""
+    lens = [300, 40]
+    cache = make_cache(51, 30, 2, 16, 64)
+    table = i32(make_table(1, lens, 16, 30))
+    kc, vc, ks, vs, kb = on_gpu(cache)
+    q, n = randn_bf16(torch.Generator().manual_seed(1), 2, 8, 1, 64).to(DEV), i32(lens)
+    want = fa.fa_decode_paged_fp8(q, kc, vc, ks, vs, table, n, 0.125)
+    held = [torch.empty_like(w) for w in want]
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)  # some 10 ms
+    for t in held:
+        t.fill_(7.0)
+    del t, held
+    got = fa.fa_decode_paged_fp8(q, kc, vc, ks, vs, table, n, 0.125, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_sizes_past_32_bits_are_refused_by_the_calls():
     lens, table = i32([20, 3]), i32(np.zeros((2, 4)))
     with pytest.raises(ValueError, match="page_size"):
