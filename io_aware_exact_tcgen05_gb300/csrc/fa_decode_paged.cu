@@ -93,17 +93,24 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return r;
 }
 
-// Lengths and counts are read in L2: the merge asks before its own wait, when only L2 is
-// sure to hold what kernels before the partial one wrote.
+// Where kEarly, the value is read in L2: the merge asks before its own wait, when only
+// L2 is sure to hold what kernels before the partial one wrote.
+template <bool kEarly>
+__device__ __forceinline__ int read_count(const int32_t* p) {
+  return kEarly ? __ldcg(p) : *p;
+}
+
+template <bool kEarly = false>
 __device__ __forceinline__ int request_len(const PagedDecodeParams& p, int b) {
-  return static_cast<int>(min(static_cast<long long>(max(__ldcg(p.seqlens + b), 0)),
+  return static_cast<int>(min(static_cast<long long>(max(read_count<kEarly>(p.seqlens + b), 0)),
                               static_cast<long long>(p.max_blocks) * p.s.page_size));
 }
 
 // 16-key blocks of a (request, KV head).
+template <bool kEarly = false>
 __device__ __forceinline__ int item_blocks(const PagedDecodeParams& p, int item) {
-  if (p.sel) return min(max(__ldcg(p.n_sel + item), 0), p.max_sel) << p.block_shift;
-  return (request_len(p, item / p.s.Hkv) + kBlockKeys - 1) / kBlockKeys;
+  if (p.sel) return min(max(read_count<kEarly>(p.n_sel + item), 0), p.max_sel) << p.block_shift;
+  return (request_len<kEarly>(p, item / p.s.Hkv) + kBlockKeys - 1) / kBlockKeys;
 }
 
 // Places of a (request, KV head) and row block in the line: its blocks behind
@@ -121,13 +128,14 @@ struct Line {
 };
 
 // Returns the start of the calling thread's items.
+template <bool kEarly = false>
 __device__ __forceinline__ long long make_line(const PagedDecodeParams& p, int row_blocks,
                                                Line& s) {
   const int items = p.B * p.s.Hkv;
   const int per = (items + kThreads - 1) / kThreads;
   const int lo = min(static_cast<int>(threadIdx.x) * per, items), hi = min(lo + per, items);
   long long own = 0;
-  for (int i = lo; i < hi; ++i) own += unit_places(item_blocks(p, i));
+  for (int i = lo; i < hi; ++i) own += unit_places(item_blocks<kEarly>(p, i));
   own *= row_blocks;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   long long v = own;
@@ -915,13 +923,13 @@ __global__ void __launch_bounds__(kThreads)
   const int row = blockIdx.x * kRows + warp / kSplit, part = warp % kSplit;
   // The line is worked out while the partial kernel still runs: it takes only the
   // lengths and lists, which were complete before that kernel let this one launch.
-  make_line(p, row_blocks, line);
-  const int n_kb = item_blocks(p, item);
+  make_line<true>(p, row_blocks, line);
+  const int n_kb = item_blocks<true>(p, item);
   const int items = p.B * p.s.Hkv;
   const int per = (items + kThreads - 1) / kThreads;
   long long start = line.prefix[item / per];
   for (int i = item / per * per; i < item; ++i)
-    start += unit_places(item_blocks(p, i)) * row_blocks;
+    start += unit_places(item_blocks<true>(p, i)) * row_blocks;
   const int rb = row / tile_rows, r = row - rb * tile_rows;
   start += rb * unit_places(n_kb) + kSegmentCost;  // the unit's first block
   const long long share = share_of(line.prefix[kThreads], items, ctas);
