@@ -49,7 +49,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kBlockKeys = 16;
 constexpr int kSms = 152;
 constexpr int kMinShare = 8;        // places in the line a CTA takes at least
-constexpr int kSegmentCost = 16;    // places a segment's fixed cost takes in the line
+constexpr int kSegmentCost = 20;    // places a segment's fixed cost takes in the line
 constexpr float kLag = 6.f;         // how far (log2) a weight may exceed the running maximum
 constexpr float kWeightUnit = 512.f;
 
@@ -57,7 +57,7 @@ constexpr float kWeightUnit = 512.f;
 // narrow kernel; more go through the wide one, 32 at a time.
 template <int NT> struct Plan;
 template <> struct Plan<1> { static constexpr int kCtasPerSm = 4; };
-template <> struct Plan<2> { static constexpr int kCtasPerSm = 4; };
+template <> struct Plan<2> { static constexpr int kCtasPerSm = 5; };
 template <> struct Plan<4> { static constexpr int kCtasPerSm = 3; };
 
 int row_tiles(int rows) { return rows <= 8 ? 1 : rows <= 16 ? 2 : 4; }
@@ -115,7 +115,8 @@ __device__ __forceinline__ int item_blocks(const PagedDecodeParams& p, int item)
 
 // Places of a (request, KV head) and row block in the line: its blocks behind
 // kSegmentCost places without work, for what beginning and ending a segment costs (8000 to
-// 10000 clocks; without them 62 us where this takes 52 us: 32 rows of 24 ragged requests).
+// 10000 clocks; 32 rows of 24 ragged requests: 62 us without them where 16 took 52 us, and
+// later 45.9 us with 16, 44.7 with 20, 45.1 with 28).
 __device__ __forceinline__ long long unit_places(int n_kb) {
   return n_kb > 0 ? n_kb + kSegmentCost : 0;
 }
@@ -246,16 +247,17 @@ struct NarrowSmem {
 };
 
 // What a lane looks up for one of its warp's coming blocks (block i of the
-// segment; a hidden one has scales of 0 and points at the cache's start).
+// segment; a hidden one has scales of 0 and the offset kHidden).
 struct BlockInfo {
   long long offset;  // bytes from the start of a cache tensor to the block's first key
   int pos;           // position of the first key; INT_MAX: the block is hidden
   float ks, vs;
 };
 
+template <int kHidden>
 __device__ __forceinline__ BlockInfo look_up(const PagedDecodeParams& p, const Segment& sg, int i) {
   const int ps = p.s.page_size;
-  BlockInfo r = {0, 0x7fffffff, 0.f, 0.f};
+  BlockInfo r = {kHidden, 0x7fffffff, 0.f, 0.f};
   if (i >= sg.n_seg) return r;
   const int idx = (sg.kb0 + i) >> p.block_shift, sub = (sg.kb0 + i) & ((1 << p.block_shift) - 1);
   const int blk = p.sel ? p.sel[static_cast<size_t>(sg.item) * p.max_sel + idx] : idx;
@@ -389,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, Plan<1>::kCtasPerSm)
       }
     };
     const int mine = (sg.n_seg - warp + kWarps - 1) / kWarps;  // blocks warp + i * kWarps
-    BlockInfo info = look_up(p, sg, warp + lane * kWarps);
+    BlockInfo info = look_up<0>(p, sg, warp + lane * kWarps);
     {  // the first block is on its way while the queries are prepared
       const long long off = __shfl_sync(0xffffffffu, info.offset, 0);
       if (mine > 0) {
@@ -416,7 +418,7 @@ __global__ void __launch_bounds__(kThreads, Plan<1>::kCtasPerSm)
     for (int i = 0; i < mine; ++i) {
       const int src = i & 31;
       if (src == 0 && i > 0) {  // the next 32 blocks of this warp, one per lane
-        info = look_up(p, sg, warp + (i + lane) * kWarps);
+        info = look_up<0>(p, sg, warp + (i + lane) * kWarps);
         const long long off = __shfl_sync(0xffffffffu, info.offset, 0);
         load_k(off);
         load_v(off);
@@ -590,18 +592,28 @@ __global__ void __launch_bounds__(kThreads, Plan<1>::kCtasPerSm)
   }
 }
 
+__device__ __forceinline__ void cp_async16(void* to, const void* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
+
 // 9 to 32 query rows: the four warps work on the same four blocks (64 keys).  Each
 // computes the scores of one block for all rows; the weights go through shared
 // memory as B operands, and each warp adds its 32 channels of O^T (at d = 64 two
 // warps share 32 channels and take two of the blocks each).  So the accumulators
 // of a warp are 32 channels x 32 rows, a quarter of what a warp on its own would
-// hold.  Latency bounds it (a step of 64 keys takes 4100 clocks, of which the two products
-// 1800 and the weights 1230, with 12 warps per SM): 52 us for 24 requests of 500 to 9000 keys, 32
-// rows, 4 KV heads (2.4 TB/s).  Before segments were counted in the line and the merge was a
-// dependent launch, it took 66 us where a warp with all 32 rows to itself took 68 us and two
-// passes of 16 rows 69 us.
+// hold.
+// Keys go to registers; values go through shared memory, copied a step ahead, one block
+// per warp: loaded from global memory each warp would take 4 bytes per lane and row (64
+// keys x 32 channels), and those 16 loads cost 6 us of 52.  Hidden blocks are not loaded: all
+// CTAs' reads of one place in their stead cost 1 us of 12 for 200 short items.
+// What bounds it is the chain of a step (scores, weights, vote, products: some 3400 clocks for 64
+// keys) at 12 warps per SM with the shared-memory pipe half busy (the query operands are
+// a third of that): 45 us for 24 requests of 500 to 9000 keys, 32 rows, 4 KV heads
+// (2.7 TB/s).  A warp with all 32 rows to itself took 68 us where this kernel's first form took 66.
 // The running maxima are the CTA's; the vote on moving them is the barrier that
-// hands the weights over.
+// hands the weights over.  A segment's first step moves them without a vote.
 template <int D, int NT>
 struct WideSmem {
   Line line;
@@ -613,7 +625,10 @@ struct WideSmem {
   float vs[kWarps];
   alignas(16) uint2 q[NT * (D / 16) * 32];
   alignas(16) uint2 w[2][kWarps][NT][32];         // P^T of the four blocks, double buffered
-  alignas(16) float o[128 / D][8 * NT][D + 4];
+  union {
+    alignas(16) uint8_t v[2][kWarps][kBlockKeys * D];  // values of the steps to come
+    alignas(16) float o[128 / D][8 * NT][D + 4];              // the segment's result
+  };
 };
 
 template <int D, int NT>
@@ -630,6 +645,16 @@ __global__ void __launch_bounds__(kThreads, Plan<NT>::kCtasPerSm)
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int g = lane >> 2, t = lane & 3;
   const int dw = warp % DW, vb0 = (warp / DW) * VB;  // channels [32 dw, ..), blocks [vb0, ..)
+  // A block's values in shared memory: 16-byte pieces, moved within their row (and at
+  // d = 64 rows 1 and 2 of four changed over) so that the four rows a warp reads at once
+  // lie in different banks.
+  constexpr int V_ODD = D == 128 ? D : 2 * D;           // from row 2t to row 2t + 1
+  const int v_row = lane / (D / 16), v_piece = lane % (D / 16);  // row of 512 / D at a time
+  int v_read;
+  if constexpr (D == 128)
+    v_read = 2 * t * D + ((dw * 2 + (g >> 2)) ^ 2 * t) * 16 + (g & 3) * 4;
+  else
+    v_read = ((t >> 1) * 4 + (t & 1)) * D + ((dw * 2 + (g >> 2)) ^ (t >> 1) * 2) * 16 + (g & 3) * 4;
 
   // First the wait, then the signal: once the merge may launch, what this call
   // reads (lengths, lists) is complete, so the merge may read them before its own wait.
@@ -641,9 +666,9 @@ __global__ void __launch_bounds__(kThreads, Plan<NT>::kCtasPerSm)
   __syncthreads();
   while (sg.live) {
     const int steps = (sg.n_seg + kWarps - 1) / kWarps;
-    uint4 kr[2][KC];
-    uint32_t vr[VB][4];
+    uint4 kr[2][KC] = {};
     auto load_k = [&](long long off) {
+      if (off < 0) return;
       const uint8_t* base = static_cast<const uint8_t*>(p.k_cache) + off + g * D + t * 16;
 #pragma unroll
       for (int i = 0; i < KC; ++i) {
@@ -651,17 +676,33 @@ __global__ void __launch_bounds__(kThreads, Plan<NT>::kCtasPerSm)
         kr[1][i] = ld_stream16(base + 8 * D + i * 64);
       }
     };
-    auto load_v = [&](int v, long long off) {
-      const uint8_t* base = static_cast<const uint8_t*>(p.v_cache) + off + 2 * t * D + dw * 32 + g * 4;
+    // the values of this warp's block of a step, 512 bytes at a time
+    auto copy_v = [&](int step, long long off) {
+      if (off < 0) return;
+      const uint8_t* from = static_cast<const uint8_t*>(p.v_cache) + off + lane * 16;
+      uint8_t* to = s.v[step & 1][warp];
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        vr[v][i] = __ldg(reinterpret_cast<const uint32_t*>(base + ((i & 1) + (i >> 1) * 8) * D));
+      for (int i = 0; i < D / 32; ++i) {
+        const int r = i * (512 / D) + v_row;
+        const int at = D == 128 ? r * D + (v_piece ^ ((r >> 1) & 3) * 2) * 16
+                                : ((r & 12) | (r & 1) << 1 | (r >> 1 & 1)) * D +
+                                      (v_piece ^ ((r >> 2) & 1) * 2) * 16;
+        cp_async16(to + at, from + i * 512);
+      }
     };
     // lane j of every warp looks block j of the coming 32 up, and of the 32 after them
-    BlockInfo info = look_up(p, sg, lane), ahead = look_up(p, sg, 32 + lane);
-    load_k(__shfl_sync(0xffffffffu, info.offset, warp));
-#pragma unroll
-    for (int v = 0; v < VB; ++v) load_v(v, __shfl_sync(0xffffffffu, info.offset, vb0 + v));
+    BlockInfo info = look_up<-1>(p, sg, lane), ahead = look_up<-1>(p, sg, 32 + lane);
+    // blocks that some row does not see whole
+    auto edges = [&] {
+      return __ballot_sync(0xffffffffu, static_cast<long long>(info.pos) + kBlockKeys - 1 > sg.len - p.Sq);
+    };
+    uint32_t edge = edges();
+    {
+      const long long off = __shfl_sync(0xffffffffu, info.offset, warp);
+      load_k(off);
+      copy_v(0, off);
+      cp_async_commit();
+    }
 
     for (int nt = warp; nt < NT; nt += kWarps) {
       const int r = nt * 8 + g;
@@ -691,13 +732,13 @@ __global__ void __launch_bounds__(kThreads, Plan<NT>::kCtasPerSm)
       const int src = (i & 7) * kWarps;  // this step's blocks are lanes src .. src + 3
       if (src == 0 && i > 0) {
         info = ahead;
-        ahead = look_up(p, sg, (i / 8 + 1) * 32 + lane);
+        ahead = look_up<-1>(p, sg, (i / 8 + 1) * 32 + lane);
+        edge = edges();
       }
-      const int pos = __shfl_sync(0xffffffffu, info.pos, src + warp);
       const float ks = __shfl_sync(0xffffffffu, info.ks, src + warp);
       const float vs = __shfl_sync(0xffffffffu, info.vs, src + warp);
-      const long long next = (i & 7) == 7 ? ahead.offset : info.offset;
-      const int next_src = (src + kWarps) & 31;
+      const long long next = __shfl_sync(0xffffffffu, (i & 7) == 7 ? ahead.offset : info.offset,
+                                         (src + kWarps + warp) & 31);
 
       // ---- S^T = K Q^T of this warp's block ----
       float x[NT][4];
@@ -720,7 +761,7 @@ __global__ void __launch_bounds__(kThreads, Plan<NT>::kCtasPerSm)
           }
         }
       }
-      load_k(__shfl_sync(0xffffffffu, next, next_src + warp));  // past the end: the cache's start
+      load_k(next);
 
       // ---- weights against the running maximum ----
       float f[NT][2];
@@ -729,7 +770,8 @@ __global__ void __launch_bounds__(kThreads, Plan<NT>::kCtasPerSm)
         f[nt][0] = ks * c_row[nt][0];
         f[nt][1] = ks * c_row[nt][1];
       }
-      if (static_cast<long long>(pos) + kBlockKeys - 1 > sg.len - p.Sq) {  // as in the narrow kernel
+      if (edge >> (src + warp) & 1u) {  // as in the narrow kernel
+        const int pos = __shfl_sync(0xffffffffu, info.pos, src + warp);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -761,7 +803,15 @@ __global__ void __launch_bounds__(kThreads, Plan<NT>::kCtasPerSm)
         }
         return over;
       };
-      if (__syncthreads_or(put_weights())) {
+      // A segment's first step moves the maxima without a vote.  In front of the barrier that
+      // hands the weights over, a thread's part of the step's values has arrived.
+      bool move = i == 0;
+      if (!move) {
+        move = put_weights();
+        cp_async_wait();
+        move = __syncthreads_or(move);
+      }
+      if (move) {
         // exact maximum of the four blocks' rows; the CTA's state moves to it
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -799,6 +849,7 @@ __global__ void __launch_bounds__(kThreads, Plan<NT>::kCtasPerSm)
             }
           }
         put_weights();
+        cp_async_wait();
         __syncthreads();
       }
 #pragma unroll
@@ -807,17 +858,26 @@ __global__ void __launch_bounds__(kThreads, Plan<NT>::kCtasPerSm)
         l[nt][1] += ws[nt][1];
       }
 
+      copy_v(i + 1, next);  // to the buffer that the step before this one has read
+      cp_async_commit();
+
       // ---- O^T += V^T P^T, this warp's channels and blocks ----
+      const uint8_t* v_at = s.v[i & 1][vb0] + v_read;
 #pragma unroll
       for (int v = 0; v < VB; ++v) {
-        const int vpos = __shfl_sync(0xffffffffu, info.pos, src + vb0 + v);
-        if (static_cast<long long>(vpos) + kBlockKeys - 1 > sg.len - p.Sq) {
+        uint32_t vr[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          vr[r] = *reinterpret_cast<const uint32_t*>(v_at + v * kBlockKeys * D + (r & 1) * V_ODD +
+                                                     (r >> 1) * 8 * D);
+        if (edge >> (src + vb0 + v) & 1u) {
+          const int vpos = __shfl_sync(0xffffffffu, info.pos, src + vb0 + v);
           bool nan = false;
 #pragma unroll
           for (int r = 0; r < 4; ++r) {
             // what lies behind the last key may be anything
-            if (static_cast<long long>(vpos) + 2 * t + (r & 1) + (r >> 1) * 8 >= sg.len) vr[v][r] = 0u;
-            nan |= nan_codes(vr[v][r]) != 0;
+            if (static_cast<long long>(vpos) + 2 * t + (r & 1) + (r >> 1) * 8 >= sg.len) vr[r] = 0u;
+            nan |= nan_codes(vr[r]) != 0;
           }
           if (p.Sq > 1 && __any_sync(0xffffffffu, nan)) {
             // NaN values go to the rows that see their keys, and to no others (as in
@@ -825,8 +885,8 @@ __global__ void __launch_bounds__(kThreads, Plan<NT>::kCtasPerSm)
             uint32_t n[4];
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-              n[r] = nan_codes(vr[v][r]) & 0x38383838u;
-              vr[v][r] &= ~nan_codes(vr[v][r]);
+              n[r] = nan_codes(vr[r]) & 0x38383838u;
+              vr[r] &= ~nan_codes(vr[r]);
             }
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
@@ -851,8 +911,8 @@ __global__ void __launch_bounds__(kThreads, Plan<NT>::kCtasPerSm)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const uint32_t sel = j ? 0x7362u : 0x5140u;
-          const uint32_t lo = __byte_perm(vr[v][0], vr[v][1], sel);
-          const uint32_t hi = __byte_perm(vr[v][2], vr[v][3], sel);
+          const uint32_t lo = __byte_perm(vr[0], vr[1], sel);
+          const uint32_t hi = __byte_perm(vr[2], vr[3], sel);
           a[j][0] = e4m3x2_to_f16x2(lo), a[j][1] = e4m3x2_hi_to_f16x2(lo);
           a[j][2] = e4m3x2_to_f16x2(hi), a[j][3] = e4m3x2_hi_to_f16x2(hi);
         }
@@ -862,11 +922,11 @@ __global__ void __launch_bounds__(kThreads, Plan<NT>::kCtasPerSm)
           mma_f16(acc[0][nt], a[0][0], a[0][1], a[0][2], a[0][3], w.x, w.y);
           mma_f16(acc[1][nt], a[1][0], a[1][1], a[1][2], a[1][3], w.x, w.y);
         }
-        load_v(v, __shfl_sync(0xffffffffu, next, next_src + vb0 + v));
       }
     }
 
     // ---- the CTA's state ----
+    __syncthreads();  // the values have been read: their place takes the result
     const float back = v_ref * (1.f / kWeightUnit);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
