@@ -49,7 +49,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kBlockKeys = 16;
 constexpr int kSms = 152;
 constexpr int kMinShare = 8;        // places in the line a CTA takes at least
-constexpr int kSegmentCost = 20;    // places a segment's fixed cost takes in the line
+constexpr int kSegmentCost = 24;    // places a segment's fixed cost takes in the line
 constexpr float kLag = 6.f;         // how far (log2) a weight may exceed the running maximum
 constexpr float kWeightUnit = 512.f;
 
@@ -116,7 +116,8 @@ __device__ __forceinline__ int item_blocks(const PagedDecodeParams& p, int item)
 // Places of a (request, KV head) and row block in the line: its blocks behind
 // kSegmentCost places without work, for what beginning and ending a segment costs (8000 to
 // 10000 clocks; 32 rows of 24 ragged requests: 62 us without them where 16 took 52 us, and
-// later 45.9 us with 16, 44.7 with 20, 45.1 with 28).
+// later 46.2 us with 16, 45.2 with 24, 46.2 with 32.  A multiple of the smallest share keeps
+// short requests on whole shares: 777 keys take 6.6 us with 24, 7.1 with 20).
 __device__ __forceinline__ long long unit_places(int n_kb) {
   return n_kb > 0 ? n_kb + kSegmentCost : 0;
 }
