@@ -149,7 +149,8 @@ __global__ void __launch_bounds__(kAssignThreads) fa_kv_assign_kernel(const KvAs
 // stays in registers between the maximum and the rounding, a thread's 16 pieces of
 // 16 bytes all in flight at once.  (With 8 pieces and twice the threads the cost of finding
 // and closing a run, some 700 instructions a warp, took more issue slots than the
-// data: 88 us against 77 us for 65k tokens of 8 heads, d = 128, 5.4 TB/s.)
+// data: 88 us against 77 us for 65k tokens of 8 heads, d = 128; with the values fetched into
+// L2 early 70 us, 5.9 TB/s.)
 // quantise8 for a scale that is no power of two, by division.  Out of line: eight divisions at every use
 // had the quantising write wait for instructions.
 __device__ __noinline__ uint2 quantise8_divide(uint4 w, float s) {
@@ -216,6 +217,16 @@ __global__ void __launch_bounds__(WriteTile<D, PS>::kThreads, 640 / WriteTile<D,
     for (int w = 0; w < kWords; ++w) {
       const int t = t_lo + 32 * w + lane;
       slots[w] = t < p.n_tokens ? p.slot_map[t] : -1;
+    }
+    // The values' place follows from the slots, but that they are this stretch's does not:
+    // they are on their way to L2 while the slots are (70 us against 76 us; for one to
+    // four tokens it changes nothing, and 400 or 1520 CTAs ahead 74 and 75 us).
+    if (stretch >= 8) {
+      constexpr int kLines = D / 64;
+      for (int i = tid; i < (t_hi - t_lo) * kLines; i += T::kThreads) {
+        const __nv_bfloat16* line = src - col * 8 + (t_lo + i / kLines) * st_t + i % kLines * 64;
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(line));
+      }
     }
 #pragma unroll
     for (int w = 0; w < kWords; ++w) {
