@@ -151,6 +151,7 @@ __global__ void __launch_bounds__(kAssignThreads) fa_kv_assign_kernel(const KvAs
 // and closing a run, some 700 instructions a warp, took more issue slots than the
 // data: 88 us against 77 us for 65k tokens of 8 heads, d = 128; with the values fetched into
 // L2 early 70 us, 5.9 TB/s.)
+
 // quantise8 for a scale that is no power of two, by division.  Out of line: eight divisions at every use
 // had the quantising write wait for instructions.
 __device__ __noinline__ uint2 quantise8_divide(uint4 w, float s) {
@@ -218,9 +219,10 @@ __global__ void __launch_bounds__(WriteTile<D, PS>::kThreads, 640 / WriteTile<D,
       const int t = t_lo + 32 * w + lane;
       slots[w] = t < p.n_tokens ? p.slot_map[t] : -1;
     }
-    // The values' place follows from the slots, but that they are this stretch's does not:
-    // they are on their way to L2 while the slots are (70 us against 76 us; for one to
-    // four tokens it changes nothing, and 400 or 1520 CTAs ahead 74 and 75 us).
+    // Which values the stretch reads does not depend on the slots: they come to L2 while
+    // the slots come to the registers (70 us against 76 us; stretches of one to four
+    // tokens gain nothing, and fetching those of the CTA 400 or 1520 further on takes 74
+    // or 75 us).
     if (stretch >= 8) {
       constexpr int kLines = D / 64;
       for (int i = tid; i < (t_hi - t_lo) * kLines; i += T::kThreads) {
