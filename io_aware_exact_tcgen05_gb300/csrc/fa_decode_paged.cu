@@ -615,6 +615,17 @@ __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_gr
 // (2.7 TB/s).  A warp with all 32 rows to itself took 68 us where this kernel's first form took 66.
 // The running maxima are the CTA's; the vote on moving them is the barrier that
 // hands the weights over.  A segment's first step moves them without a vote.
+// Four channels of keys 2t, 2t + 1, 2t + 8 and 2t + 9 as B operands, channel j in b[.][j].
+__device__ __forceinline__ void pair_up(const uint32_t (&v)[4], uint32_t (&b)[2][4]) {
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const uint32_t lo = __byte_perm(v[2 * k], v[2 * k + 1], 0x5140);
+    const uint32_t hi = __byte_perm(v[2 * k], v[2 * k + 1], 0x7362);
+    b[k][0] = e4m3x2_to_f16x2(lo), b[k][1] = e4m3x2_hi_to_f16x2(lo);
+    b[k][2] = e4m3x2_to_f16x2(hi), b[k][3] = e4m3x2_hi_to_f16x2(hi);
+  }
+}
+
 template <int D, int NT>
 struct WideSmem {
   Line line;
@@ -624,11 +635,11 @@ struct WideSmem {
   float l[kWarps][8 * NT];
   float mx[kWarps][8 * NT];
   float vs[kWarps];
-  alignas(16) uint2 q[NT * (D / 16) * 32];
-  alignas(16) uint2 w[2][kWarps][NT][32];         // P^T of the four blocks, double buffered
+  alignas(16) uint32_t q[NT / 2 * (D / 16)][32][4];    // A operands of the query rows
+  alignas(16) uint4 w[2][kWarps][NT / 2][32];          // P of the four blocks, double buffered
   union {
     alignas(16) uint8_t v[2][kWarps][kBlockKeys * D];  // values of the steps to come
-    alignas(16) float o[128 / D][8 * NT][D + 4];              // the segment's result
+    alignas(16) float o[128 / D][8 * NT][D + 4];       // the segment's result
   };
 };
 
@@ -641,6 +652,7 @@ __global__ void __launch_bounds__(kThreads, Plan<NT>::kCtasPerSm)
   constexpr int DW = D / 32;           // warps side by side over the channels
   constexpr int VB = DW;               // blocks whose values a warp multiplies
   constexpr int R = 8 * NT;
+  constexpr int MT = NT / 2;           // row tiles of 16
   extern __shared__ __align__(16) unsigned char smem_raw[];
   WideSmem<D, NT>& s = *reinterpret_cast<WideSmem<D, NT>*>(smem_raw);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -708,24 +720,25 @@ __global__ void __launch_bounds__(kThreads, Plan<NT>::kCtasPerSm)
     for (int nt = warp; nt < NT; nt += kWarps) {
       const int r = nt * 8 + g;
       const float c = load_q<D>(p, sg.qrow0 + r, r < sg.n_rows, t, [&](int ks, uint2 v) {
-        s.q[(nt * KS + ks) * 32 + lane] = v;
+        s.q[nt / 2 * KS + ks][lane][nt & 1] = v.x;
+        s.q[nt / 2 * KS + ks][lane][2 + (nt & 1)] = v.y;
       });
       if (t == 0) s.c_row[r] = c;
     }
     __syncthreads();
-    float c_row[NT][2], m[NT][2], l[NT][2], acc[2][NT][4];
+    float c_row[MT][2], m[MT][2], l[MT][2], acc[MT][4][4];  // rows g and g + 8 of a tile
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        c_row[nt][r] = s.c_row[nt * 8 + 2 * t + r];
-        m[nt][r] = kNoMax;
-        l[nt][r] = 0.f;
+        c_row[mt][r] = s.c_row[mt * 16 + r * 8 + g];
+        m[mt][r] = kNoMax;
+        l[mt][r] = 0.f;
       }
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+      for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) acc[j][nt][e] = 0.f;
+        for (int e = 0; e < 4; ++e) acc[mt][j][e] = 0.f;
     }
     float v_ref = 0.f, v_mul = 0.f;
 
@@ -741,66 +754,73 @@ __global__ void __launch_bounds__(kThreads, Plan<NT>::kCtasPerSm)
       const long long next = __shfl_sync(0xffffffffu, (i & 7) == 7 ? ahead.offset : info.offset,
                                          (src + kWarps + warp) & 31);
 
-      // ---- S^T = K Q^T of this warp's block ----
-      float x[NT][4];
+      // ---- S = Q K^T of this warp's block: {row g, key 8u + 2t}, {row g, key + 1}, {row g + 8, ..} x 2
+      float x[MT][2][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[nt][e] = 0.f;
+        for (int e = 0; e < 4; ++e) x[mt][0][e] = x[mt][1][e] = 0.f;
 #pragma unroll
       for (int c = 0; c < KC; ++c) {
         const uint32_t wa[4] = {kr[0][c].x, kr[0][c].y, kr[0][c].z, kr[0][c].w};
         const uint32_t wb[4] = {kr[1][c].x, kr[1][c].y, kr[1][c].z, kr[1][c].w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const uint32_t a0 = e4m3x2_to_f16x2(wa[e]), a2 = e4m3x2_hi_to_f16x2(wa[e]);
-          const uint32_t a1 = e4m3x2_to_f16x2(wb[e]), a3 = e4m3x2_hi_to_f16x2(wb[e]);
+          const uint32_t a0 = e4m3x2_to_f16x2(wa[e]), a1 = e4m3x2_hi_to_f16x2(wa[e]);
+          const uint32_t b0 = e4m3x2_to_f16x2(wb[e]), b1 = e4m3x2_hi_to_f16x2(wb[e]);
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const uint2 q = s.q[(nt * KS + c * 4 + e) * 32 + lane];
-            mma_f16(x[nt], a0, a1, a2, a3, q.x, q.y);
+          for (int mt = 0; mt < MT; ++mt) {
+            const uint4 q = *reinterpret_cast<const uint4*>(s.q[mt * KS + c * 4 + e][lane]);
+            mma_f16(x[mt][0], q.x, q.y, q.z, q.w, a0, a1);
+            mma_f16(x[mt][1], q.x, q.y, q.z, q.w, b0, b1);
           }
         }
       }
       load_k(next);
 
       // ---- weights against the running maximum ----
-      float f[NT][2];
+      float f[MT][2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        f[nt][0] = ks * c_row[nt][0];
-        f[nt][1] = ks * c_row[nt][1];
+      for (int mt = 0; mt < MT; ++mt) {
+        f[mt][0] = ks * c_row[mt][0];
+        f[mt][1] = ks * c_row[mt][1];
       }
       if (edge >> (src + warp) & 1u) {  // as in the narrow kernel
         const int pos = __shfl_sync(0xffffffffu, info.pos, src + warp);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            f[nt][e & 1] = fmaxf(f[nt][e & 1], 1.1754944e-38f);
-            const long long key = static_cast<long long>(pos) + g + (e >> 1) * 8;
-            if (key > sg.len - p.Sq + (sg.row0 + nt * 8 + 2 * t + (e & 1)) % p.Sq)
-              x[nt][e] = neg_inf();
+          for (int r = 0; r < 2; ++r) {
+            f[mt][r] = fmaxf(f[mt][r], 1.1754944e-38f);
+            const int last = sg.len - p.Sq + (sg.row0 + mt * 16 + r * 8 + g) % p.Sq;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const long long key = static_cast<long long>(pos) + 2 * t + (e >> 1) * 8 + (e & 1);
+              if (key > last) x[mt][e >> 1][2 * r + (e & 1)] = neg_inf();
+            }
           }
       }
-      float ws[NT][2];
+      float ws[MT][2];
       auto put_weights = [&] {
         const float unit = vs * v_mul;
         bool over = vs > v_ref;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          float w[4];
+        for (int mt = 0; mt < MT; ++mt) {
+          uint32_t a[2][2];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float arg = fmaf(x[nt][e], f[nt][e & 1], -m[nt][e & 1]);
-            over |= arg > kLag;
-            w[e] = ex2_approx(arg);
+          for (int r = 0; r < 2; ++r) {
+            float w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float arg = fmaf(x[mt][e >> 1][2 * r + (e & 1)], f[mt][r], -m[mt][r]);
+              over |= arg > kLag;
+              w[e] = ex2_approx(arg);
+            }
+            a[0][r] = pack_f16x2(w[0] * unit, w[1] * unit);
+            a[1][r] = pack_f16x2(w[2] * unit, w[3] * unit);
+            ws[mt][r] = (w[0] + w[1]) + (w[2] + w[3]);
           }
-          s.w[i & 1][warp][nt][lane] =
-              make_uint2(transpose8x8(pack_f16x2(w[0] * unit, w[1] * unit)),
-                         transpose8x8(pack_f16x2(w[2] * unit, w[3] * unit)));
-          ws[nt][0] = w[0] + w[2];
-          ws[nt][1] = w[1] + w[3];
+          s.w[i & 1][warp][mt][lane] = make_uint4(a[0][0], a[0][1], a[1][0], a[1][1]);
         }
         return over;
       };
@@ -815,13 +835,14 @@ __global__ void __launch_bounds__(kThreads, Plan<NT>::kCtasPerSm)
       if (move) {
         // exact maximum of the four blocks' rows; the CTA's state moves to it
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            float mx = fmaxf(x[nt][r] * f[nt][r], x[nt][2 + r] * f[nt][r]);
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-            if (g == 0) s.mx[warp][nt * 8 + 2 * t + r] = mx;
+            float mx = fmaxf(fmaxf(x[mt][0][2 * r] * f[mt][r], x[mt][0][2 * r + 1] * f[mt][r]),
+                             fmaxf(x[mt][1][2 * r] * f[mt][r], x[mt][1][2 * r + 1] * f[mt][r]));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+            if (t == 0) s.mx[warp][mt * 16 + r * 8 + g] = mx;
           }
         if (lane == 0) s.vs[warp] = vs;
         __syncthreads();
@@ -834,19 +855,19 @@ __global__ void __launch_bounds__(kThreads, Plan<NT>::kCtasPerSm)
           v_mul = kWeightUnit / top;
         }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            float m_new = m[nt][r];
+            float m_new = m[mt][r];
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) m_new = fmaxf(m_new, s.mx[w][nt * 8 + 2 * t + r]);
-            const float a = ex2_approx(m[nt][r] - m_new);
-            m[nt][r] = m_new;
-            l[nt][r] *= a;
+            for (int w = 0; w < kWarps; ++w) m_new = fmaxf(m_new, s.mx[w][mt * 16 + r * 8 + g]);
+            const float a = ex2_approx(m[mt][r] - m_new);
+            m[mt][r] = m_new;
+            l[mt][r] *= a;
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              acc[j][nt][r] *= a * v_down;
-              acc[j][nt][2 + r] *= a * v_down;
+            for (int j = 0; j < 4; ++j) {
+              acc[mt][j][2 * r] *= a * v_down;
+              acc[mt][j][2 * r + 1] *= a * v_down;
             }
           }
         put_weights();
@@ -854,15 +875,15 @@ __global__ void __launch_bounds__(kThreads, Plan<NT>::kCtasPerSm)
         __syncthreads();
       }
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        l[nt][0] += ws[nt][0];
-        l[nt][1] += ws[nt][1];
+      for (int mt = 0; mt < MT; ++mt) {
+        l[mt][0] += ws[mt][0];
+        l[mt][1] += ws[mt][1];
       }
 
       copy_v(i + 1, next);  // to the buffer that the step before this one has read
       cp_async_commit();
 
-      // ---- O^T += V^T P^T, this warp's channels and blocks ----
+      // ---- O += P V, this warp's channels (4g + j of column g in tile j) and blocks ----
       const uint8_t* v_at = s.v[i & 1][vb0] + v_read;
 #pragma unroll
       for (int v = 0; v < VB; ++v) {
@@ -889,39 +910,35 @@ __global__ void __launch_bounds__(kThreads, Plan<NT>::kCtasPerSm)
               n[r] = nan_codes(vr[r]) & 0x38383838u;
               vr[r] &= ~nan_codes(vr[r]);
             }
+            uint32_t b[2][4];
+            pair_up(n, b);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              const int last = sg.len - p.Sq + (sg.row0 + nt * 8 + g) % p.Sq - vpos - 2 * t;
-              const uint32_t see0 = (last >= 0 ? 0x3c00u : 0u) | (last >= 1 ? 0x3c000000u : 0u);
-              const uint32_t see1 = (last >= 8 ? 0x3c00u : 0u) | (last >= 9 ? 0x3c000000u : 0u);
+            for (int mt = 0; mt < MT; ++mt) {
+              uint32_t see[2][2];
 #pragma unroll
-              for (int j = 0; j < 2; ++j) {
-                const uint32_t sel = j ? 0x7362u : 0x5140u;
-                const uint32_t lo = __byte_perm(n[0], n[1], sel), hi = __byte_perm(n[2], n[3], sel);
+              for (int r = 0; r < 2; ++r) {
+                const int last = sg.len - p.Sq + (sg.row0 + mt * 16 + r * 8 + g) % p.Sq - vpos - 2 * t;
+                see[0][r] = (last >= 0 ? 0x3c00u : 0u) | (last >= 1 ? 0x3c000000u : 0u);
+                see[1][r] = (last >= 8 ? 0x3c00u : 0u) | (last >= 9 ? 0x3c000000u : 0u);
+              }
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
                 float c[4] = {0.f, 0.f, 0.f, 0.f};
-                mma_f16(c, e4m3x2_to_f16x2(lo), e4m3x2_hi_to_f16x2(lo), e4m3x2_to_f16x2(hi),
-                        e4m3x2_hi_to_f16x2(hi), see0, see1);
+                mma_f16(c, see[0][0], see[0][1], see[1][0], see[1][1], b[0][j], b[1][j]);
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                  if (c[e] > 0.f) acc[j][nt][e] = __int_as_float(0x7fffffff);
+                  if (c[e] > 0.f) acc[mt][j][e] = __int_as_float(0x7fffffff);
               }
             }
           }
         }
-        uint32_t a[2][4];
+        uint32_t b[2][4];
+        pair_up(vr, b);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const uint32_t sel = j ? 0x7362u : 0x5140u;
-          const uint32_t lo = __byte_perm(vr[0], vr[1], sel);
-          const uint32_t hi = __byte_perm(vr[2], vr[3], sel);
-          a[j][0] = e4m3x2_to_f16x2(lo), a[j][1] = e4m3x2_hi_to_f16x2(lo);
-          a[j][2] = e4m3x2_to_f16x2(hi), a[j][3] = e4m3x2_hi_to_f16x2(hi);
-        }
+        for (int mt = 0; mt < MT; ++mt) {
+          const uint4 a = s.w[i & 1][vb0 + v][mt][lane];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const uint2 w = s.w[i & 1][vb0 + v][nt][lane];
-          mma_f16(acc[0][nt], a[0][0], a[0][1], a[0][2], a[0][3], w.x, w.y);
-          mma_f16(acc[1][nt], a[1][0], a[1][1], a[1][2], a[1][3], w.x, w.y);
+          for (int j = 0; j < 4; ++j) mma_f16(acc[mt][j], a.x, a.y, a.z, a.w, b[0][j], b[1][j]);
         }
       }
     }
@@ -930,21 +947,22 @@ __global__ void __launch_bounds__(kThreads, Plan<NT>::kCtasPerSm)
     __syncthreads();  // the values have been read: their place takes the result
     const float back = v_ref * (1.f / kWeightUnit);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
+    for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        float sum = l[nt][r];
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        const int row = nt * 8 + 2 * t + r;
-        if (g == 0) {
+        float sum = l[mt][r];
+        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+        const int row = mt * 16 + r * 8 + g;
+        if (t == 0) {
           s.l[warp][row] = sum;
-          if (warp == 0) s.m[row] = m[nt][r];
+          if (warp == 0) s.m[row] = m[mt][r];
         }
 #pragma unroll
-        for (int j = 0; j < 2; ++j)
-          *reinterpret_cast<float2*>(&s.o[warp / DW][row][dw * 32 + g * 4 + 2 * j]) =
-              make_float2(acc[j][nt][r] * back, acc[j][nt][2 + r] * back);
+        for (int e = 0; e < 2; ++e)
+          *reinterpret_cast<float4*>(&s.o[warp / DW][row][dw * 32 + 8 * t + 4 * e]) =
+              make_float4(acc[mt][0][2 * r + e] * back, acc[mt][1][2 * r + e] * back,
+                          acc[mt][2][2 * r + e] * back, acc[mt][3][2 * r + e] * back);
       }
     __syncthreads();
     for (int idx = tid; idx < sg.n_rows * (D / 4); idx += kThreads) {
