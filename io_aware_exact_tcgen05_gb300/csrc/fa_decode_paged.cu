@@ -4,8 +4,10 @@
 // The cache is read once (2 bytes per key, KV head and channel), so HBM bounds
 // the kernel; the arithmetic only has to stay out of the way.  The query rows
 // of a KV head (Hq / Hkv * Sq of them) are the narrow side of two
-// mma.sync.m16n8k16 products in f16 with fp32 accumulation:
+// mma.sync.m16n8k16 products in f16 with fp32 accumulation, up to 8 rows
 //   S^T[16 keys x 8 rows] = K Q^T,   O^T[d x 8 rows] += V^T P^T
+// and from 9 rows on
+//   S[16 rows x 8 keys] = Q K^T,     O[16 rows x d] += P V
 // e4m3 codes become f16 exactly (one conversion per pair).  The page's K scale
 // multiplies the scores in fp32, its V scale the weights in fp32.
 //
@@ -24,7 +26,7 @@
 // (g = lane / 4, t = lane % 4) loads channels [16t, 16t + 16) of keys g and g + 8;
 // for V it loads channels [16g, 16g + 16) of keys 2t, 2t+1, 2t+8 and 2t+9, and one
 // byte permutation pairs two keys of a channel.  The S^T accumulator becomes the
-// P^T operand by movmatrix.
+// P^T operand by movmatrix; that of S is P's operand as it lies.
 //
 // Work: the 16-key blocks of all (request, KV head, row block) are laid end to
 // end and every CTA takes an equal stretch (the lengths are read on the device:
@@ -599,22 +601,6 @@ __device__ __forceinline__ void cp_async16(void* to, const void* from) {
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group 0;" ::: "memory"); }
 
-// 9 to 32 query rows: the four warps work on the same four blocks (64 keys).  Each
-// computes the scores of one block for all rows; the weights go through shared
-// memory as B operands, and each warp adds its 32 channels of O^T (at d = 64 two
-// warps share 32 channels and take two of the blocks each).  So the accumulators
-// of a warp are 32 channels x 32 rows, a quarter of what a warp on its own would
-// hold.
-// Keys go to registers; values go through shared memory, copied a step ahead, one block
-// per warp: loaded from global memory each warp would take 4 bytes per lane and row (64
-// keys x 32 channels), and those 16 loads cost 6 us of 52.  Hidden blocks are not loaded: all
-// CTAs' reads of one place in their stead cost 1 us of 12 for 200 short items.
-// What bounds it is the chain of a step (scores, weights, vote, products: some 3400 clocks for 64
-// keys) at 12 warps per SM with the shared-memory pipe half busy (the query operands are
-// a third of that): 45 us for 24 requests of 500 to 9000 keys, 32 rows, 4 KV heads
-// (2.7 TB/s).  A warp with all 32 rows to itself took 68 us where this kernel's first form took 66.
-// The running maxima are the CTA's; the vote on moving them is the barrier that
-// hands the weights over.  A segment's first step moves them without a vote.
 // Four channels of keys 2t, 2t + 1, 2t + 8 and 2t + 9 as B operands, channel j in b[.][j].
 __device__ __forceinline__ void pair_up(const uint32_t (&v)[4], uint32_t (&b)[2][4]) {
 #pragma unroll
@@ -626,6 +612,23 @@ __device__ __forceinline__ void pair_up(const uint32_t (&v)[4], uint32_t (&b)[2]
   }
 }
 
+// 9 to 32 query rows: the four warps work on the same four blocks (64 keys).  Each
+// computes the scores of one block for all rows; the weights go through shared
+// memory as A operands, and each warp adds its 32 channels of O (at d = 64 two
+// warps share 32 channels and take two of the blocks each).  So the accumulators
+// of a warp are 32 rows x 32 channels, a quarter of what a warp on its own would
+// hold.
+// Keys go to registers; values go through shared memory, copied a step ahead, one block
+// per warp: loaded from global memory each warp would take 4 bytes per lane and row (64
+// keys x 32 channels), and those 16 loads cost 6 us of 52.  Hidden blocks are not loaded: all
+// CTAs' reads of one place in their stead cost 1 us of 12 for 200 short items.
+// Latency bounds it: 11 warps per SM are there, tensor pipe 39% busy, shared memory 51%, issue
+// 38%; the waits are for products and conversions (27%), shared memory (16%), global memory
+// (10%).  43 us for 24 requests of 500 to 9000 keys, 32 rows, 4 KV heads (2.9 TB/s), of which 39
+// remain without any load.  (With the keys as M side, as the narrow kernel has it, 45 us;
+// a warp with all 32 rows to itself 68 us where this kernel's first form took 66.)
+// The running maxima are the CTA's; the vote on moving them is the barrier that
+// hands the weights over.  A segment's first step moves them without a vote.
 template <int D, int NT>
 struct WideSmem {
   Line line;

@@ -461,6 +461,82 @@ def test_decode_long_chosen_list():
     _decode_case([n], 4, 1, 1, 64, ps, seed=20, sel=sel, n_sel=np.array([[300]]))
 
 
+WIDE = [(6, 2, 4, 64), (6, 2, 4, 128), (24, 2, 2, 64), (24, 2, 2, 128), (36, 2, 3, 128)]
+
+
+@pytest.mark.parametrize("Hq,heads,Sq,d", WIDE)
+def test_decode_wide_nan_reaches_only_the_rows_that_see_it(Hq, heads, Sq, d):
+    ps, lens = 16, [237, 20]
+    for which in (0, 1):
+        cache = make_cache(13, 20, heads, ps, d)
+        table = make_table(3, lens, ps, 20)
+        # the newest key of request 0, head 1: hidden from all rows but the last
+        cache.codes[which][table[0, 236 // ps], 1, 236 % ps, 7] = 0x7f
+        _decode_case(lens, Hq, heads, Sq, d, ps, seed=34, cache=cache, table=table)
+        # the next one, at another channel: hidden from the first rows
+        cache.codes[which][table[0, 235 // ps], 1, 235 % ps, d - 1] = 0xff
+        _decode_case(lens, Hq, heads, Sq, d, ps, seed=35, cache=cache, table=table)
+        # an older key of request 1: every row sees it
+        cache.codes[which][table[1, 0], 0, 3, 9] = 0xff
+        _decode_case(lens, Hq, heads, Sq, d, ps, seed=36, cache=cache, table=table)
+
+
+@pytest.mark.parametrize("Hq,heads,Sq,d", WIDE)
+def test_decode_wide_absent_pages_and_what_lies_behind_the_last_key(Hq, heads, Sq, d):
+    ps, lens = 32, [1500, 33, 40, 64, 1]
+    pages = 60
+    cache = make_cache(37, pages, heads, ps, d)
+    table = make_table(38, lens, ps, pages)
+    for b, n in enumerate(lens):
+        for j in range(n, po.pages_of(n, ps) * ps):
+            for c in cache.codes:
+                c[table[b, j // ps], :, j % ps] = 0x7f  # NaN codes
+    _decode_case(lens, Hq, heads, Sq, d, ps, seed=39, cache=cache, table=table)
+    table[0, [0, 7, 8, 9, 10, 30, 46]] = -1
+    table[2, :] = pages  # no page at all: every key is hidden
+    _decode_case(lens, Hq, heads, Sq, d, ps, seed=40, cache=cache, table=table)
+
+
+@pytest.mark.parametrize("Hq,heads,Sq,d", WIDE)
+def test_decode_wide_chosen_blocks_and_far_apart_scales(Hq, heads, Sq, d):
+    ps, lens = 16, [900, 50, 0]
+    cache = make_cache(41, 65, heads, ps, d)
+    rng = np.random.RandomState(42)
+    cache.scale[1] = cache.scale[1] * 2.0 ** rng.randint(-20, 21, cache.scale[1].shape)
+    sel, n_sel = np.full((3, heads, 40), -1), np.zeros((3, heads), int)
+    for b, n in enumerate(lens):
+        for h in range(heads):
+            m = po.pages_of(n, ps)
+            take = min(m, rng.randint(1, 41))
+            sel[b, h, :take] = np.sort(rng.permutation(m)[:take])
+            n_sel[b, h] = take
+    table = make_table(43, lens, ps, 65)
+    _decode_case(lens, Hq, heads, Sq, d, ps, seed=44, cache=cache, table=table)
+    _decode_case(lens, Hq, heads, Sq, d, ps, seed=45, cache=cache, table=table, sel=sel, n_sel=n_sel)
+    sel[0, 0, :7] = [0, 0, 56, 57, -1, 500, 3]  # behind the request, absent, twice the same
+    n_sel[0, 0], n_sel[1, 1] = 7, 90
+    _decode_case(lens, Hq, heads, Sq, d, ps, seed=46, cache=cache, table=table, sel=sel, n_sel=n_sel)
+
+
+def test_decode_wide_offsets_past_32_bits():
+    ps, d, heads = 64, 128, 2
+    pages = (1 << 32) // (ps * d * heads) + 64
+    free, _ = torch.cuda.mem_get_info()
+    if free < 20 << 30:
+        pytest.skip("needs 20 GB")
+    small = make_cache(47, 6, heads, ps, d)
+    parts = on_gpu(small)[:4]
+    at = torch.tensor([pages - 1, 3, pages - 40, pages - 2, 7, pages - 9], device=DEV)
+    big = [torch.empty(pages, *t.shape[1:], dtype=t.dtype, device=DEV) for t in parts]
+    for b, t in zip(big, parts):
+        b[at] = t
+    table = np.array([[0, 1, 2, 3, 4]])
+    q = randn_bf16(torch.Generator().manual_seed(1), 1, 40, 1, d)
+    o, lse = fa.fa_decode_paged_fp8(q.to(DEV), *big, at[torch.from_numpy(table).to(DEV)].int(),
+                                    i32([300]), 0.1)
+    check_attention(o, lse, po.attend(f64(q), small, table, [300], 0.1), 300, d)
+
+
 def test_offsets_past_32_bits():
     # pages of 16 KB: the last ones lie behind 4 GB
     ps, d, heads = 64, 128, 2
