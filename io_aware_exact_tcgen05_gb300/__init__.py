@@ -408,7 +408,7 @@ _F8 = getattr(torch, "float8_e4m3fn", torch.uint8)
 
 
 def _device():
-    """The current device's index; -2 (no tensor's) where there is no driver."""
+    """The current device's index; -2 (no tensor's) where there is no GPU."""
     try:
         return torch._C._cuda_getDevice()
     except RuntimeError:
