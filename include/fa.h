@@ -418,6 +418,9 @@ size_t fa_decode_paged_fp8_workspace_size(int B, int Hq, int Hkv, int Sq, int d)
  * block listed twice counts twice).  Rows that see no key give O = 0, LSE = -inf.
  * What the pages hold behind a request's last key is never used.  A key that
  * holds NaN makes the rows that see it NaN, and no others.
+ * V scales may lie as far apart as their range allows.  Weights are rounded to 11 bits
+ * where they multiply the values; a weight * V scale below 2^-23 of the largest that its
+ * row sees is off by at most 2^-34 of that largest.
  * Any Sq is accepted; for prompts, fa_kv_read_fp8 with fa_fwd_varlen is the
  * faster path (the rows of a KV head are served 32 at a time here).
  */

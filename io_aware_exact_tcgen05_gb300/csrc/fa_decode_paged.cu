@@ -13,12 +13,15 @@
 //
 // f16 and its range: a query row is multiplied by the power of two that puts
 // its largest element into [2^14, 2^15), which loses nothing above 2^-38 of it.
-// Weights are taken against a running maximum m that may lag by 6 (log2 units)
-// and are stored as w * 2^9 * v_scale / v_ref <= 2^15 (v_ref: the largest V scale
-// so far), so a weight keeps f16's 11 bits down to 2^-23 of the largest and is
-// rounded by at most 2^-34 of it below.  (A lag of 2 kept four bits more and
-// moved the maximum on most steps of 32 rows: 72 us against 66 us.)  Sums, maxima and
-// accumulators are fp32.
+// Every row keeps two running maxima, both in log2 units: m over its scores x, against
+// which the softmax's sum l is taken, and mv over x + log2(V scale), against which the
+// weights of the values are stored, as 2^(x + log2(V scale) - mv + 9) in f16.  A maximum
+// may lag by 6, so a stored weight is at most 2^15, keeps f16's 11 bits down to 2^-23 of
+// the largest weight * V scale that the row has met, and is rounded by at most 2^-34 of
+// that below.  With a maximum of its own per row, a loud page takes nothing from the
+// others where the row gives it no weight or does not see it (against the largest V scale
+// met so far, a page 2^30 louder, without weight, left the others 3 bits).  In the
+// end O = acc * 2^(mv - m - 9) / l.  Sums, maxima and accumulators are fp32.
 //
 // Operands without shared memory: the contraction index of a product may be
 // permuted freely, so a lane loads 16-byte pieces of whole rows and hands their
@@ -52,8 +55,8 @@ constexpr int kBlockKeys = 16;
 constexpr int kSms = 152;
 constexpr int kMinShare = 8;        // places in the line a CTA takes at least
 constexpr int kSegmentCost = 24;    // places a segment's fixed cost takes in the line
-constexpr float kLag = 6.f;         // how far (log2) a weight may exceed the running maximum
-constexpr float kWeightUnit = 512.f;
+constexpr float kLag = 6.f;         // how far (log2) a weight may exceed a running maximum
+constexpr float kWeightLog = 9.f;   // log2 of the stored weight of a key at the maximum
 
 // Row tiles of 8 a CTA serves, and CTAs per SM (by registers).  Up to 8 rows the
 // narrow kernel; more go through the wide one, 32 at a time.
@@ -73,6 +76,12 @@ int grid_ctas(int nt) {
 constexpr float kNoMax = -3.0e38f;
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
+
+// How far above m a score may lie before the maxima have to move: by kLag, and so that its
+// stored weight, 2^(score + up), stays below 2^(kWeightLog + kLag).
+__device__ __forceinline__ float most_above(float m, float up) {
+  return fminf(kLag, kWeightLog + kLag - up - m);
+}
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                         uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -246,6 +255,7 @@ struct NarrowSmem {
   Segment seg;
   float m[kWarps][8];
   float l[kWarps][8];
+  float mv[kWarps][8];
   alignas(16) float o[kWarps][8][D + 4];
 };
 
@@ -254,13 +264,13 @@ struct NarrowSmem {
 struct BlockInfo {
   long long offset;  // bytes from the start of a cache tensor to the block's first key
   int pos;           // position of the first key; INT_MAX: the block is hidden
-  float ks, vs;
+  float ks, vl;      // K scale, log2 of the V scale (-inf: a scale of 0, values without weight)
 };
 
 template <int kHidden>
 __device__ __forceinline__ BlockInfo look_up(const PagedDecodeParams& p, const Segment& sg, int i) {
   const int ps = p.s.page_size;
-  BlockInfo r = {kHidden, 0x7fffffff, 0.f, 0.f};
+  BlockInfo r = {kHidden, 0x7fffffff, 0.f, neg_inf()};
   if (i >= sg.n_seg) return r;
   const int idx = (sg.kb0 + i) >> p.block_shift, sub = (sg.kb0 + i) & ((1 << p.block_shift) - 1);
   const int blk = p.sel ? p.sel[static_cast<size_t>(sg.item) * p.max_sel + idx] : idx;
@@ -271,7 +281,7 @@ __device__ __forceinline__ BlockInfo look_up(const PagedDecodeParams& p, const S
       r.offset = (static_cast<long long>(tile) * ps + sub * kBlockKeys) * p.s.d;
       r.pos = blk * ps + sub * kBlockKeys;
       r.ks = p.k_scale[tile];
-      r.vs = p.v_scale[tile];
+      r.vl = __log2f(p.v_scale[tile]);
     }
   }
   return r;
@@ -324,17 +334,31 @@ __device__ __forceinline__ float load_q(const PagedDecodeParams& p, size_t row, 
   return p.scale_log2 * pow2i(ex - 14);
 }
 
+// A partial state of a row: its two maxima and its sum; the accumulator beside it counts in
+// units of 2^(mv - 9).
+using RowState = float4;  // m, l, mv, unused
+__device__ __forceinline__ RowState row_state(float m, float l, float mv) {
+  return make_float4(m, l, mv, 0.f);
+}
+
+// 2^(mv - m - 9) of a finished row: it multiplies acc / l, whose product alone lies in fp32's
+// range for every scale.
+__device__ __forceinline__ float value_unit(float m, float mv) {
+  return ex2_approx(mv - m - kWeightLog);
+}
+
 // Writes one finished output vector (four channels) or partial state.
 template <int D>
 __device__ __forceinline__ void emit(const PagedDecodeParams& p, const Segment& sg, int tile_rows,
-                                     int row, int c, float M, float L, float4 o, float* part_o,
-                                     float2* part_ml) {
+                                     int row, int c, float M, float L, float MV, float4 o,
+                                     float* part_o, RowState* part_ml) {
   if (sg.n_seg == sg.n_kb) {
     const bool empty = L == 0.f;
     const float inv = empty ? 0.f : 1.f / L;
+    const float unit = value_unit(M, MV);
     uint2 w;
-    w.x = pack_bf16x2(o.x * inv, o.y * inv);
-    w.y = pack_bf16x2(o.z * inv, o.w * inv);
+    w.x = pack_bf16x2(o.x * inv * unit, o.y * inv * unit);
+    w.y = pack_bf16x2(o.z * inv * unit, o.w * inv * unit);
     *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + (sg.qrow0 + row) * D + c) = w;
     if (p.lse && c == 0)
       p.lse[sg.qrow0 + row] = empty ? neg_inf() : (M + __log2f(L)) * 0.69314718055994530942f;
@@ -342,7 +366,7 @@ __device__ __forceinline__ void emit(const PagedDecodeParams& p, const Segment& 
     // a CTA's first segment may begin inside an item, its last may end inside one
     const size_t at = (2 * static_cast<size_t>(blockIdx.x) + (sg.kb0 == 0 ? 1 : 0)) * tile_rows + row;
     *reinterpret_cast<float4*>(part_o + at * D + c) = o;
-    if (c == 0) part_ml[at] = make_float2(M, L);
+    if (c == 0) part_ml[at] = row_state(M, L, MV);
   }
 }
 
@@ -350,7 +374,7 @@ __device__ __forceinline__ void emit(const PagedDecodeParams& p, const Segment& 
 template <int D>
 __global__ void __launch_bounds__(kThreads, Plan<1>::kCtasPerSm)
     fa_decode_paged_narrow(const PagedDecodeParams p, int row_blocks, float* part_o,
-                           float2* part_ml) {
+                           RowState* part_ml) {
   constexpr int KC = D / 64;       // 16-byte pieces of a key row per lane
   constexpr int KS = D / 16;       // k-steps of S
   constexpr int MT = D / 16;       // m-tiles of O^T
@@ -411,12 +435,11 @@ __global__ void __launch_bounds__(kThreads, Plan<1>::kCtasPerSm)
       c_row[0] = __shfl_sync(0xffffffffu, c, 8 * t);  // rows 2t and 2t + 1
       c_row[1] = __shfl_sync(0xffffffffu, c, 8 * t + 4);
     }
-    float m[2] = {kNoMax, kNoMax}, l[2] = {0.f, 0.f}, acc[MT][4];
+    float m[2] = {kNoMax, kNoMax}, mv[2] = {kNoMax, kNoMax}, l[2] = {0.f, 0.f}, acc[MT][4];
 #pragma unroll
     for (int j = 0; j < MT; ++j)
 #pragma unroll
       for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
-    float v_ref = 0.f, v_mul = 0.f;  // v_mul = 2^9 / v_ref
 
     for (int i = 0; i < mine; ++i) {
       const int src = i & 31;
@@ -428,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, Plan<1>::kCtasPerSm)
       }
       const int pos = __shfl_sync(0xffffffffu, info.pos, src);
       const float ks = __shfl_sync(0xffffffffu, info.ks, src);
-      const float vs = __shfl_sync(0xffffffffu, info.vs, src);
+      const float vl = __shfl_sync(0xffffffffu, info.vl, src);
       const bool more = i + 1 < mine && src != 31;
       const long long next = __shfl_sync(0xffffffffu, info.offset, (src + 1) & 31);
 
@@ -447,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, Plan<1>::kCtasPerSm)
       }
       if (more) load_k(next);
 
-      // ---- weights against the running maximum ----
+      // ---- weights against the running maxima ----
       const bool edge = static_cast<long long>(pos) + kBlockKeys - 1 > sg.len - p.Sq;
       float f[2] = {ks * c_row[0], ks * c_row[1]};
       if (edge) {  // scores that are not seen become -inf
@@ -459,45 +482,40 @@ __global__ void __launch_bounds__(kThreads, Plan<1>::kCtasPerSm)
         }
       }
       float arg[4];
-      bool over = vs > v_ref;
+      bool over = false;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        arg[e] = fmaf(x[e], f[e & 1], -m[e & 1]);
-        over |= arg[e] > kLag;
+      for (int r = 0; r < 2; ++r) {
+        arg[r] = fmaf(x[r], f[r], -m[r]);
+        arg[2 + r] = fmaf(x[2 + r], f[r], -m[r]);
+        over |= fmaxf(arg[r], arg[2 + r]) > most_above(m[r], vl - mv[r] + kWeightLog);
       }
       if (__any_sync(0xffffffffu, over)) {
-        // exact maximum of the block's rows; the state moves to it
-        float v_down = 1.f;
-        if (vs > v_ref) {
-          v_down = v_ref / vs;  // 0 before the first block
-          v_ref = vs;
-          v_mul = kWeightUnit / vs;
-        }
+        // exact maxima of the block's rows; the state moves to them
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           float mx = fmaxf(x[r] * f[r], x[2 + r] * f[r]);
 #pragma unroll
           for (int o = 4; o < 32; o <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+          const float mxv = fmaxf(mv[r], mx + vl);
           mx = fmaxf(m[r], mx);
-          const float a = ex2_approx(m[r] - mx);
+          l[r] *= ex2_approx(m[r] - mx);
+          const float a = ex2_approx(mv[r] - mxv);
           m[r] = mx;
-          l[r] *= a;
+          mv[r] = mxv;
 #pragma unroll
           for (int j = 0; j < MT; ++j) {
-            acc[j][r] *= a * v_down;
-            acc[j][2 + r] *= a * v_down;
+            acc[j][r] *= a;
+            acc[j][2 + r] *= a;
           }
           arg[r] = fmaf(x[r], f[r], -mx);
           arg[2 + r] = fmaf(x[2 + r], f[r], -mx);
         }
       }
-      const float unit = vs * v_mul;
       float w[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        w[e] = ex2_approx(arg[e]);
-        l[e & 1] += w[e];
-        w[e] *= unit;
+        l[e & 1] += ex2_approx(arg[e]);
+        w[e] = ex2_approx(fmaf(x[e], f[e & 1], vl - mv[e & 1] + kWeightLog));
       }
       const uint32_t pb0 = transpose8x8(pack_f16x2(w[0], w[1]));
       const uint32_t pb1 = transpose8x8(pack_f16x2(w[2], w[3]));
@@ -553,7 +571,6 @@ __global__ void __launch_bounds__(kThreads, Plan<1>::kCtasPerSm)
     }
 
     // ---- merge the warps' states ----
-    const float back = v_ref * (1.f / kWeightUnit);
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       float sum = l[r];
@@ -563,31 +580,35 @@ __global__ void __launch_bounds__(kThreads, Plan<1>::kCtasPerSm)
       if (g == 0) {
         s.m[warp][row] = m[r];
         s.l[warp][row] = sum;
+        s.mv[warp][row] = mv[r];
       }
 #pragma unroll
       for (int j = 0; j < MT; ++j)
         *reinterpret_cast<float2*>(&s.o[warp][row][g * (D / 8) + 2 * j]) =
-            make_float2(acc[j][r] * back, acc[j][2 + r] * back);
+            make_float2(acc[j][r], acc[j][2 + r]);
     }
     __syncthreads();
     for (int idx = tid; idx < sg.n_rows * (D / 4); idx += kThreads) {
       const int row = idx / (D / 4), c = (idx % (D / 4)) * 4;
-      float M = kNoMax;
+      float M = kNoMax, MV = kNoMax;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, s.m[w][row]);
+      for (int w = 0; w < kWarps; ++w) {
+        M = fmaxf(M, s.m[w][row]);
+        MV = fmaxf(MV, s.mv[w][row]);
+      }
       float L = 0.f;
       float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float wt = ex2_approx(s.m[w][row] - M);
+        const float wt = ex2_approx(s.mv[w][row] - MV);
         const float4 v = *reinterpret_cast<const float4*>(&s.o[w][row][c]);
-        L = fmaf(wt, s.l[w][row], L);
+        L = fmaf(ex2_approx(s.m[w][row] - M), s.l[w][row], L);
         o.x = fmaf(wt, v.x, o.x);
         o.y = fmaf(wt, v.y, o.y);
         o.z = fmaf(wt, v.z, o.z);
         o.w = fmaf(wt, v.w, o.w);
       }
-      emit<D>(p, sg, 8, row, c, M, L, o, part_o, part_ml);
+      emit<D>(p, sg, 8, row, c, M, L, MV, o, part_o, part_ml);
     }
     __syncthreads();
     if (tid == 0) s.seg.next(p, row_blocks, 8);
@@ -635,9 +656,10 @@ struct WideSmem {
   Segment seg;
   float c_row[8 * NT];
   float m[8 * NT];
+  float mv[8 * NT];
   float l[kWarps][8 * NT];
   float mx[kWarps][8 * NT];
-  float vs[kWarps];
+  float vl[kWarps];
   alignas(16) uint32_t q[NT / 2 * (D / 16)][32][4];    // A operands of the query rows
   alignas(16) uint4 w[2][kWarps][NT / 2][32];          // P of the four blocks, double buffered
   union {
@@ -649,7 +671,7 @@ struct WideSmem {
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, Plan<NT>::kCtasPerSm)
     fa_decode_paged_wide(const PagedDecodeParams p, int row_blocks, float* part_o,
-                         float2* part_ml) {
+                         RowState* part_ml) {
   constexpr int KC = D / 64;           // 16-byte pieces of a key row per lane
   constexpr int KS = D / 16;           // k-steps of S
   constexpr int DW = D / 32;           // warps side by side over the channels
@@ -729,13 +751,14 @@ __global__ void __launch_bounds__(kThreads, Plan<NT>::kCtasPerSm)
       if (t == 0) s.c_row[r] = c;
     }
     __syncthreads();
-    float c_row[MT][2], m[MT][2], l[MT][2], acc[MT][4][4];  // rows g and g + 8 of a tile
+    float c_row[MT][2], m[MT][2], mv[MT][2], l[MT][2], acc[MT][4][4];  // rows g and g + 8 of a tile
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         c_row[mt][r] = s.c_row[mt * 16 + r * 8 + g];
         m[mt][r] = kNoMax;
+        mv[mt][r] = kNoMax;
         l[mt][r] = 0.f;
       }
 #pragma unroll
@@ -743,7 +766,6 @@ __global__ void __launch_bounds__(kThreads, Plan<NT>::kCtasPerSm)
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[mt][j][e] = 0.f;
     }
-    float v_ref = 0.f, v_mul = 0.f;
 
     for (int i = 0; i < steps; ++i) {
       const int src = (i & 7) * kWarps;  // this step's blocks are lanes src .. src + 3
@@ -753,7 +775,7 @@ __global__ void __launch_bounds__(kThreads, Plan<NT>::kCtasPerSm)
         edge = edges();
       }
       const float ks = __shfl_sync(0xffffffffu, info.ks, src + warp);
-      const float vs = __shfl_sync(0xffffffffu, info.vs, src + warp);
+      const float vl = __shfl_sync(0xffffffffu, info.vl, src + warp);
       const long long next = __shfl_sync(0xffffffffu, (i & 7) == 7 ? ahead.offset : info.offset,
                                          (src + kWarps + warp) & 31);
 
@@ -781,7 +803,7 @@ __global__ void __launch_bounds__(kThreads, Plan<NT>::kCtasPerSm)
       }
       load_k(next);
 
-      // ---- weights against the running maximum ----
+      // ---- weights against the running maxima ----
       float f[MT][2];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
@@ -805,22 +827,24 @@ __global__ void __launch_bounds__(kThreads, Plan<NT>::kCtasPerSm)
       }
       float ws[MT][2];
       auto put_weights = [&] {
-        const float unit = vs * v_mul;
-        bool over = vs > v_ref;
+        bool over = false;
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt) {
           uint32_t a[2][2];
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            float w[4];
+            const float up = vl - mv[mt][r] + kWeightLog, most = most_above(m[mt][r], up);
+            float w[4], wv[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const float arg = fmaf(x[mt][e >> 1][2 * r + (e & 1)], f[mt][r], -m[mt][r]);
-              over |= arg > kLag;
+              const float xe = x[mt][e >> 1][2 * r + (e & 1)];
+              const float arg = fmaf(xe, f[mt][r], -m[mt][r]);
+              over |= arg > most;
               w[e] = ex2_approx(arg);
+              wv[e] = ex2_approx(fmaf(xe, f[mt][r], up));
             }
-            a[0][r] = pack_f16x2(w[0] * unit, w[1] * unit);
-            a[1][r] = pack_f16x2(w[2] * unit, w[3] * unit);
+            a[0][r] = pack_f16x2(wv[0], wv[1]);
+            a[1][r] = pack_f16x2(wv[2], wv[3]);
             ws[mt][r] = (w[0] + w[1]) + (w[2] + w[3]);
           }
           s.w[i & 1][warp][mt][lane] = make_uint4(a[0][0], a[0][1], a[1][0], a[1][1]);
@@ -836,7 +860,7 @@ __global__ void __launch_bounds__(kThreads, Plan<NT>::kCtasPerSm)
         move = __syncthreads_or(move);
       }
       if (move) {
-        // exact maximum of the four blocks' rows; the CTA's state moves to it
+        // exact maxima of the four blocks' rows; the CTA's state moves to them
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -847,30 +871,27 @@ __global__ void __launch_bounds__(kThreads, Plan<NT>::kCtasPerSm)
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
             if (t == 0) s.mx[warp][mt * 16 + r * 8 + g] = mx;
           }
-        if (lane == 0) s.vs[warp] = vs;
+        if (lane == 0) s.vl[warp] = vl;
         __syncthreads();
-        float top = 0.f, v_down = 1.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s.vs[w]);
-        if (top > v_ref) {
-          v_down = v_ref / top;  // 0 before the first block
-          v_ref = top;
-          v_mul = kWeightUnit / top;
-        }
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
-            float m_new = m[mt][r];
+            float m_new = m[mt][r], mv_new = mv[mt][r];
 #pragma unroll
-            for (int w = 0; w < kWarps; ++w) m_new = fmaxf(m_new, s.mx[w][mt * 16 + r * 8 + g]);
-            const float a = ex2_approx(m[mt][r] - m_new);
+            for (int w = 0; w < kWarps; ++w) {
+              const float mx = s.mx[w][mt * 16 + r * 8 + g];
+              m_new = fmaxf(m_new, mx);
+              mv_new = fmaxf(mv_new, mx + s.vl[w]);
+            }
+            l[mt][r] *= ex2_approx(m[mt][r] - m_new);
+            const float a = ex2_approx(mv[mt][r] - mv_new);
             m[mt][r] = m_new;
-            l[mt][r] *= a;
+            mv[mt][r] = mv_new;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              acc[mt][j][2 * r] *= a * v_down;
-              acc[mt][j][2 * r + 1] *= a * v_down;
+              acc[mt][j][2 * r] *= a;
+              acc[mt][j][2 * r + 1] *= a;
             }
           }
         put_weights();
@@ -948,7 +969,6 @@ __global__ void __launch_bounds__(kThreads, Plan<NT>::kCtasPerSm)
 
     // ---- the CTA's state ----
     __syncthreads();  // the values have been read: their place takes the result
-    const float back = v_ref * (1.f / kWeightUnit);
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -959,13 +979,16 @@ __global__ void __launch_bounds__(kThreads, Plan<NT>::kCtasPerSm)
         const int row = mt * 16 + r * 8 + g;
         if (t == 0) {
           s.l[warp][row] = sum;
-          if (warp == 0) s.m[row] = m[mt][r];
+          if (warp == 0) {
+            s.m[row] = m[mt][r];
+            s.mv[row] = mv[mt][r];
+          }
         }
 #pragma unroll
         for (int e = 0; e < 2; ++e)
           *reinterpret_cast<float4*>(&s.o[warp / DW][row][dw * 32 + 8 * t + 4 * e]) =
-              make_float4(acc[mt][0][2 * r + e] * back, acc[mt][1][2 * r + e] * back,
-                          acc[mt][2][2 * r + e] * back, acc[mt][3][2 * r + e] * back);
+              make_float4(acc[mt][0][2 * r + e], acc[mt][1][2 * r + e], acc[mt][2][2 * r + e],
+                          acc[mt][3][2 * r + e]);
       }
     __syncthreads();
     for (int idx = tid; idx < sg.n_rows * (D / 4); idx += kThreads) {
@@ -978,7 +1001,7 @@ __global__ void __launch_bounds__(kThreads, Plan<NT>::kCtasPerSm)
       float L = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) L += s.l[w][row];
-      emit<D>(p, sg, R, row, c, s.m[row], L, o, part_o, part_ml);
+      emit<D>(p, sg, R, row, c, s.m[row], L, s.mv[row], o, part_o, part_ml);
     }
     __syncthreads();
     if (tid == 0) s.seg.next(p, row_blocks, R);
@@ -993,12 +1016,12 @@ __global__ void __launch_bounds__(kThreads, Plan<NT>::kCtasPerSm)
 template <int D, int kSplit>
 __global__ void __launch_bounds__(kThreads)
     fa_decode_paged_merge(const PagedDecodeParams p, int row_blocks, int tile_rows, int ctas,
-                          const float* part_o, const float2* part_ml) {
+                          const float* part_o, const RowState* part_ml) {
   constexpr int E = D / 32;
   constexpr int kRows = kWarps / kSplit;  // rows per CTA
   constexpr int kBatch = 4;
   __shared__ Line line;
-  __shared__ float s_m[kWarps], s_l[kWarps];
+  __shared__ float s_m[kWarps], s_l[kWarps], s_mv[kWarps];
   __shared__ __align__(16) float s_o[kWarps][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int item = blockIdx.y;
@@ -1029,18 +1052,32 @@ __global__ void __launch_bounds__(kThreads)
   if (n_kb > 0 && c0 == c1 && kSplit == kWarps) return;  // one CTA finished the row
   const bool joins = row < p.rows && n_kb > 0 && c0 != c1;
   const size_t qrow = static_cast<size_t>(item) * p.rows + row;
-  float M = kNoMax, L = 0.f, o[E];
+  float M = kNoMax, L = 0.f, MV = kNoMax, o[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) o[e] = 0.f;
+  auto move_to = [&](float m, float mv) {  // the state is taken against m and mv
+    L *= ex2_approx(M - m);
+    const float a = ex2_approx(MV - mv);
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] *= a;
+    M = m;
+    MV = mv;
+  };
+  auto add = [&](float m, float l, float mv, auto&& acc) {  // a state below M and MV
+    L = fmaf(ex2_approx(m - M), l, L);
+    const float w = ex2_approx(mv - MV);
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] = fmaf(w, acc(e), o[e]);
+  };
   if (joins) {
     for (int c = c0 + part; c <= c1; c += kSplit * kBatch) {
-      float2 ml[kBatch];
+      RowState ml[kBatch];
       float v[kBatch][E];
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
         const int cc = c + i * kSplit;
         const size_t at = (2 * static_cast<size_t>(cc) + (cc == c0 ? 1 : 0)) * tile_rows + r;
-        ml[i] = make_float2(kNoMax, 0.f);
+        ml[i] = row_state(kNoMax, 0.f, kNoMax);
 #pragma unroll
         for (int e = 0; e < E; ++e) v[i][e] = 0.f;
         if (cc <= c1) {
@@ -1054,42 +1091,46 @@ __global__ void __launch_bounds__(kThreads)
           }
         }
       }
+      float m = M, mv = MV;
 #pragma unroll
       for (int i = 0; i < kBatch; ++i) {
-        const float m_new = fmaxf(M, ml[i].x);
-        const float a = ex2_approx(M - m_new), w = ex2_approx(ml[i].x - m_new);
-        M = m_new;
-        L = L * a + w * ml[i].y;
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = fmaf(w, v[i][e], o[e] * a);
+        m = fmaxf(m, ml[i].x);
+        mv = fmaxf(mv, ml[i].z);
       }
+      move_to(m, mv);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        add(ml[i].x, ml[i].y, ml[i].z, [&](int e) { return v[i][e]; });
     }
   }
   if constexpr (kSplit > 1) {
     if (lane == 0) {
       s_m[warp] = M;
       s_l[warp] = L;
+      s_mv[warp] = MV;
     }
 #pragma unroll
     for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = o[e];
     __syncthreads();
     if (part != 0) return;
+    float m = M, mv = MV;
 #pragma unroll
     for (int w = 1; w < kSplit; ++w) {
-      const float m_new = fmaxf(M, s_m[warp + w]);
-      const float a = ex2_approx(M - m_new), b = ex2_approx(s_m[warp + w] - m_new);
-      M = m_new;
-      L = L * a + b * s_l[warp + w];
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = fmaf(b, s_o[warp + w][lane * E + e], o[e] * a);
+      m = fmaxf(m, s_m[warp + w]);
+      mv = fmaxf(mv, s_mv[warp + w]);
     }
+    move_to(m, mv);
+#pragma unroll
+    for (int w = 1; w < kSplit; ++w)
+      add(s_m[warp + w], s_l[warp + w], s_mv[warp + w],
+          [&](int e) { return s_o[warp + w][lane * E + e]; });
   }
   if (row >= p.rows || (n_kb > 0 && c0 == c1)) return;
   const bool empty = L == 0.f;
-  const float inv = empty ? 0.f : 1.f / L;
+  const float inv = empty ? 0.f : 1.f / L, unit = value_unit(M, MV);
   uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + qrow * D + lane * E);
 #pragma unroll
-  for (int e = 0; e < E; e += 2) out[e / 2] = pack_bf16x2(o[e] * inv, o[e + 1] * inv);
+  for (int e = 0; e < E; e += 2) out[e / 2] = pack_bf16x2(o[e] * inv * unit, o[e + 1] * inv * unit);
   if (p.lse && lane == 0)
     p.lse[qrow] = empty ? neg_inf() : (M + __log2f(L)) * 0.69314718055994530942f;
 }
@@ -1105,9 +1146,9 @@ cudaError_t launch_nt(const PagedDecodeParams& p, cudaStream_t stream) {
       ((list << p.block_shift) + kSegmentCost) * p.B * p.s.Hkv * row_blocks;
   const int ctas = static_cast<int>(min(static_cast<long long>(kSms * Plan<NT>::kCtasPerSm), most));
   float* part_o = static_cast<float*>(p.workspace);
-  float2* part_ml = reinterpret_cast<float2*>(part_o + 2 * static_cast<size_t>(ctas) * 8 * NT * D);
+  RowState* part_ml = reinterpret_cast<RowState*>(part_o + 2 * static_cast<size_t>(ctas) * 8 * NT * D);
   const float* c_o = part_o;
-  const float2* c_ml = part_ml;
+  const RowState* c_ml = part_ml;
   cudaError_t e;
   hook_before(stream);
   if constexpr (NT == 1)
@@ -1140,7 +1181,7 @@ cudaError_t launch_d(const PagedDecodeParams& p, cudaStream_t stream) {
 size_t decode_paged_workspace(int B, int Hkv, int rows, int d) {
   (void)B, (void)Hkv;
   const int nt = row_tiles(rows);
-  return 2 * static_cast<size_t>(grid_ctas(nt)) * 8 * nt * (d * sizeof(float) + sizeof(float2));
+  return 2 * static_cast<size_t>(grid_ctas(nt)) * 8 * nt * (d * sizeof(float) + sizeof(RowState));
 }
 
 cudaError_t launch_decode_paged(const PagedDecodeParams& p, cudaStream_t stream) {
