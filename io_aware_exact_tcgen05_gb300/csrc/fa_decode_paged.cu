@@ -145,14 +145,13 @@ struct Line {
 };
 
 // Returns the start of the calling thread's items.
-template <bool kEarly = false>
 __device__ __forceinline__ long long make_line(const PagedDecodeParams& p, int row_blocks,
                                                Line& s) {
   const int items = p.B * p.s.Hkv;
   const int per = (items + kThreads - 1) / kThreads;
   const int lo = min(static_cast<int>(threadIdx.x) * per, items), hi = min(lo + per, items);
   long long own = 0;
-  for (int i = lo; i < hi; ++i) own += unit_places(item_blocks<kEarly>(p, i));
+  for (int i = lo; i < hi; ++i) own += unit_places(item_blocks(p, i));
   own *= row_blocks;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   long long v = own;
@@ -187,6 +186,53 @@ __device__ __forceinline__ long long share_of(long long total, int items, int ct
   return (even + 3) & ~3ll;  // a step of the wide kernel is four blocks
 }
 
+// The CTA whose stretch holds a place of the line.
+__device__ __forceinline__ int cta_of(long long place, long long share) {
+  return static_cast<int>(share <= 0x7fffffffll ? quotient(place, static_cast<int>(share))
+                                                : place / share);
+}
+
+// Sum over the warp of values in [0, 2^47).
+__device__ __forceinline__ long long warp_sum(long long v) {
+  const uint32_t lo = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(v) & 0xfffffu);
+  const uint32_t hi = __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(v >> 20));
+  return (static_cast<long long>(hi) << 20) + lo;
+}
+
+// Where an item begins in the line, and the line's length.
+struct Place {
+  long long before[kWarps], all[kWarps];  // of one row block, as each warp has summed them
+
+  // The CTA's threads, before the caller's wait: lengths are read in L2.
+  __device__ __forceinline__ void sum(const PagedDecodeParams& p, int item) {
+    long long total = 0, front = 0;
+    if (p.sel) {
+      const int items = p.B * p.s.Hkv;
+      for (int i = threadIdx.x; i < items; i += kThreads) {
+        const long long n = unit_places(item_blocks<true>(p, i));
+        total += n;
+        front += i < item ? n : 0;
+      }
+    } else {  // the heads of a request are alike
+      const int request = item / p.s.Hkv, heads = item - request * p.s.Hkv;
+      for (int b = threadIdx.x; b < p.B; b += kThreads) {
+        const long long n = unit_places((request_len<true>(p, b) + kBlockKeys - 1) / kBlockKeys);
+        total += n * p.s.Hkv;
+        front += n * (b < request ? p.s.Hkv : b == request ? heads : 0);
+      }
+    }
+    total = warp_sum(total);
+    front = warp_sum(front);
+    if ((threadIdx.x & 31) == 0) {
+      all[threadIdx.x >> 5] = total;
+      before[threadIdx.x >> 5] = front;
+    }
+  }
+  static __device__ __forceinline__ long long of(const long long (&v)[kWarps]) {
+    return (v[0] + v[1]) + (v[2] + v[3]);
+  }
+};
+
 // A CTA walks its stretch of the line segment by segment: blocks [kb0, kb0 + n_seg)
 // of one item (request, KV head) and row block.  One thread keeps the place, in
 // shared memory, so that it takes no registers in the main loop.
@@ -216,11 +262,30 @@ struct Segment {
       find(p, row_blocks, tile_rows);
     }
   }
-  __device__ __forceinline__ void next(const PagedDecodeParams& p, int row_blocks, int tile_rows) {
+  __device__ __forceinline__ void next(const PagedDecodeParams& p, int row_blocks, int tile_rows,
+                                       const Line& line) {
     at += n_seg;
     in_item += n_seg;
     live = at < end;
-    if (live) find(p, row_blocks, tile_rows);
+    if (!live) return;
+    if (in_item >= unit_places(n_kb) * row_blocks) {
+      in_item -= unit_places(n_kb) * row_blocks;
+      // Empty items may follow, in a padded batch thousands: on to the thread whose items hold
+      // the place.  (One after another, 32000 took a thread 17 ms.)
+      if (item_blocks(p, ++item) == 0) {
+        int t = 0;
+        for (int z = kThreads; z - t > 1;) {  // the last one with prefix <= at
+          const int mid = (t + z) >> 1;
+          if (line.prefix[mid] <= at) t = mid; else z = mid;
+        }
+        const int owned = t * ((p.B * p.s.Hkv + kThreads - 1) / kThreads);
+        if (owned > item) {
+          item = owned;
+          in_item = at - line.prefix[t];
+        }
+      }
+    }
+    find(p, row_blocks, tile_rows);
   }
   // The segment at (item, in_item), which may lie behind the item's end or in
   // front of a unit's blocks.
@@ -615,7 +680,7 @@ __global__ void __launch_bounds__(kThreads, Plan<1>::kCtasPerSm)
       emit<D>(p, sg, 8, row, c, M, L, MV, o, part_o, part_ml);
     }
     __syncthreads();
-    if (tid == 0) s.seg.next(p, row_blocks, 8);
+    if (tid == 0) s.seg.next(p, row_blocks, 8, s.line);
     __syncthreads();
   }
 }
@@ -1008,135 +1073,155 @@ __global__ void __launch_bounds__(kThreads, Plan<NT>::kCtasPerSm)
       emit<D>(p, sg, R, row, c, s.m[row], L, s.mv[row], o, part_o, part_ml);
     }
     __syncthreads();
-    if (tid == 0) s.seg.next(p, row_blocks, R);
+    if (tid == 0) s.seg.next(p, row_blocks, R, s.line);
     __syncthreads();
   }
 }
 
-// Joins the partial states of an item that lies in several CTAs' stretches, in
-// their order, and writes the rows of items without any key.  A row's states go
+// Joins the partial states of the units (item and row block) that lie in several CTAs' stretches,
+// in their order, and writes the rows of items without any key.  A row's states go
 // through kSplit warps (four when there are few rows and so, for long contexts, many states
 // per row; else one); each keeps up to four states' loads in flight.
+//
+// A CTA takes `span` groups of kWarps / kSplit rows, one after another in the items' order.  Where
+// its first item begins in the line is summed up while the partial kernel still runs: that takes
+// only the lengths and lists, which were complete before that kernel let this one launch.
+// From there the CTA walks.  (With the whole line built by every warp of a CTA for each
+// group of rows the plan took 40% as many instructions as the attention of 512 items, and grew with
+// the square of the items: 100 ms for 32000 of them, 4000 requests of 8 heads.)
 template <int D, int kSplit>
 __global__ void __launch_bounds__(kThreads)
     fa_decode_paged_merge(const PagedDecodeParams p, int row_blocks, int tile_rows, int ctas,
-                          const float* part_o, const RowState* part_ml) {
+                          int span, const float* part_o, const RowState* part_ml) {
   constexpr int E = D / 32;
-  constexpr int kRows = kWarps / kSplit;  // rows per CTA
+  constexpr int kRows = kWarps / kSplit;  // rows per group
   constexpr int kBatch = 4;
-  __shared__ Line line;
+  __shared__ Place place;
   __shared__ float s_m[kWarps], s_l[kWarps], s_mv[kWarps];
   __shared__ __align__(16) float s_o[kWarps][D];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int item = blockIdx.y;
-  const int row = blockIdx.x * kRows + warp / kSplit, part = warp % kSplit;
-  // The line is worked out while the partial kernel still runs: it takes only the
-  // lengths and lists, which were complete before that kernel let this one launch.
-  make_line<true>(p, row_blocks, line);
-  const int n_kb = item_blocks<true>(p, item);
+  const int part = warp % kSplit;
   const int items = p.B * p.s.Hkv;
-  const int per = (items + kThreads - 1) / kThreads;
-  long long start = line.prefix[item / per];
-  for (int i = item / per * per; i < item; ++i)
-    start += unit_places(item_blocks<true>(p, i)) * row_blocks;
-  const int rb = row / tile_rows, r = row - rb * tile_rows;
-  start += rb * unit_places(n_kb) + kSegmentCost;  // the unit's first block
-  const long long share = share_of(line.prefix[kThreads], items, ctas);
-  int c0 = 0, c1 = 0;
-  if (share <= 0x7fffffffll) {
-    c0 = static_cast<int>(quotient(start, static_cast<int>(share)));
-    c1 = static_cast<int>(quotient(start + n_kb - 1, static_cast<int>(share)));
-  } else {
-    c0 = static_cast<int>(start / share);
-    c1 = static_cast<int>((start + n_kb - 1) / share);
-  }
+  const int groups = (p.rows + kRows - 1) / kRows;  // of an item
+  const int first = blockIdx.x * span;
+  int item = first / groups;
+  int left = min(span, items * groups - first);     // groups still to be taken
+  int row = (first - item * groups) * kRows + warp / kSplit;
+  place.sum(p, item);
+  int n_kb = item_blocks<true>(p, item);
+  __syncthreads();
+  long long start = Place::of(place.before) * row_blocks;
+  const long long share = share_of(Place::of(place.all) * row_blocks, items, ctas);
+  int r, c0, c1;  // row of the unit, the CTAs of its first and last block
+  auto locate = [&] {
+    const int rb = row / tile_rows;
+    r = row - rb * tile_rows;
+    const long long at = start + rb * unit_places(n_kb) + kSegmentCost;  // the unit's first block
+    c0 = cta_of(at, share);
+    c1 = n_kb > 0 ? cta_of(at + n_kb - 1, share) : c0;
+  };
+  locate();
   // Every CTA waits, also one with nothing to join: what follows this kernel in
   // the stream may then rely on the partial kernel's completion as well.
   griddep_wait();
-  if (n_kb > 0 && c0 == c1 && kSplit == kWarps) return;  // one CTA finished the row
-  const bool joins = row < p.rows && n_kb > 0 && c0 != c1;
-  const size_t qrow = static_cast<size_t>(item) * p.rows + row;
-  float M = kNoMax, L = 0.f, MV = kNoMax, o[E];
+  while (true) {
+    if (n_kb == 0 || c0 != c1) {  // else one CTA has finished the rows of the unit
+      const bool real = row < p.rows;
+      const size_t qrow = static_cast<size_t>(item) * p.rows + row;
+      float M = kNoMax, L = 0.f, MV = kNoMax, o[E];
 #pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = 0.f;
-  auto move_to = [&](float m, float mv) {  // the state is taken against m and mv
-    L *= ex2_approx(M - m);
-    const float a = ex2_approx(MV - mv);
+      for (int e = 0; e < E; ++e) o[e] = 0.f;
+      auto move_to = [&](float m, float mv) {  // the state is taken against m and mv
+        L *= ex2_approx(M - m);
+        const float a = ex2_approx(MV - mv);
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] *= a;
-    M = m;
-    MV = mv;
-  };
-  auto add = [&](float m, float l, float mv, auto&& acc) {  // a state below M and MV
-    L = fmaf(ex2_approx(m - M), l, L);
-    const float w = ex2_approx(mv - MV);
+        for (int e = 0; e < E; ++e) o[e] *= a;
+        M = m;
+        MV = mv;
+      };
+      auto add = [&](float m, float l, float mv, auto&& acc) {  // a state below M and MV
+        L = fmaf(ex2_approx(m - M), l, L);
+        const float w = ex2_approx(mv - MV);
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = fmaf(w, acc(e), o[e]);
-  };
-  if (joins) {
-    for (int c = c0 + part; c <= c1; c += kSplit * kBatch) {
-      RowState ml[kBatch];
-      float v[kBatch][E];
+        for (int e = 0; e < E; ++e) o[e] = fmaf(w, acc(e), o[e]);
+      };
+      if (real && n_kb > 0) {
+        for (int c = c0 + part; c <= c1; c += kSplit * kBatch) {
+          RowState ml[kBatch];
+          float v[kBatch][E];
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        const int cc = c + i * kSplit;
-        const size_t at = (2 * static_cast<size_t>(cc) + (cc == c0 ? 1 : 0)) * tile_rows + r;
-        ml[i] = row_state(kNoMax, 0.f, kNoMax);
+          for (int i = 0; i < kBatch; ++i) {
+            const int cc = c + i * kSplit;
+            const size_t slot = (2 * static_cast<size_t>(cc) + (cc == c0 ? 1 : 0)) * tile_rows + r;
+            ml[i] = row_state(kNoMax, 0.f, kNoMax);
 #pragma unroll
-        for (int e = 0; e < E; ++e) v[i][e] = 0.f;
-        if (cc <= c1) {
-          ml[i] = part_ml[at];
-          if constexpr (E == 4) {
-            const float4 x = *reinterpret_cast<const float4*>(part_o + at * D + lane * 4);
-            v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
-          } else {
-            const float2 x = *reinterpret_cast<const float2*>(part_o + at * D + lane * 2);
-            v[i][0] = x.x, v[i][1] = x.y;
+            for (int e = 0; e < E; ++e) v[i][e] = 0.f;
+            if (cc <= c1) {
+              ml[i] = part_ml[slot];
+              if constexpr (E == 4) {
+                const float4 x = *reinterpret_cast<const float4*>(part_o + slot * D + lane * 4);
+                v[i][0] = x.x, v[i][1] = x.y, v[i][2] = x.z, v[i][3] = x.w;
+              } else {
+                const float2 x = *reinterpret_cast<const float2*>(part_o + slot * D + lane * 2);
+                v[i][0] = x.x, v[i][1] = x.y;
+              }
+            }
           }
+          float m = M, mv = MV;
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i) {
+            m = fmaxf(m, ml[i].x);
+            mv = fmaxf(mv, ml[i].z);
+          }
+          move_to(m, mv);
+#pragma unroll
+          for (int i = 0; i < kBatch; ++i)
+            add(ml[i].x, ml[i].y, ml[i].z, [&](int e) { return v[i][e]; });
         }
       }
-      float m = M, mv = MV;
+      if constexpr (kSplit > 1) {
+        if (lane == 0) {
+          s_m[warp] = M;
+          s_l[warp] = L;
+          s_mv[warp] = MV;
+        }
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i) {
-        m = fmaxf(m, ml[i].x);
-        mv = fmaxf(mv, ml[i].z);
+        for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = o[e];
+        __syncthreads();
+        if (part == 0) {
+          float m = M, mv = MV;
+#pragma unroll
+          for (int w = 1; w < kSplit; ++w) {
+            m = fmaxf(m, s_m[warp + w]);
+            mv = fmaxf(mv, s_mv[warp + w]);
+          }
+          move_to(m, mv);
+#pragma unroll
+          for (int w = 1; w < kSplit; ++w)
+            add(s_m[warp + w], s_l[warp + w], s_mv[warp + w],
+                [&](int e) { return s_o[warp + w][lane * E + e]; });
+        }
       }
-      move_to(m, mv);
+      if (real && part == 0) {
+        const bool empty = L == 0.f;
+        const float inv = empty ? 0.f : 1.f / L, unit = value_unit(M, MV);
+        uint32_t* out =
+            reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + qrow * D + lane * E);
 #pragma unroll
-      for (int i = 0; i < kBatch; ++i)
-        add(ml[i].x, ml[i].y, ml[i].z, [&](int e) { return v[i][e]; });
+        for (int e = 0; e < E; e += 2) out[e / 2] = pack_bf16x2(o[e] * inv * unit, o[e + 1] * inv * unit);
+        if (p.lse && lane == 0)
+          p.lse[qrow] = empty ? neg_inf() : (M + __log2f(L)) * 0.69314718055994530942f;
+      }
     }
+    if (kSplit > 1 || --left == 0) break;  // with four warps a row a CTA has one row
+    row += kRows;
+    if (row - warp / kSplit >= p.rows) {  // the next item
+      start += unit_places(n_kb) * row_blocks;
+      n_kb = item_blocks<true>(p, ++item);
+      row = warp / kSplit;
+    }
+    locate();
   }
-  if constexpr (kSplit > 1) {
-    if (lane == 0) {
-      s_m[warp] = M;
-      s_l[warp] = L;
-      s_mv[warp] = MV;
-    }
-#pragma unroll
-    for (int e = 0; e < E; ++e) s_o[warp][lane * E + e] = o[e];
-    __syncthreads();
-    if (part != 0) return;
-    float m = M, mv = MV;
-#pragma unroll
-    for (int w = 1; w < kSplit; ++w) {
-      m = fmaxf(m, s_m[warp + w]);
-      mv = fmaxf(mv, s_mv[warp + w]);
-    }
-    move_to(m, mv);
-#pragma unroll
-    for (int w = 1; w < kSplit; ++w)
-      add(s_m[warp + w], s_l[warp + w], s_mv[warp + w],
-          [&](int e) { return s_o[warp + w][lane * E + e]; });
-  }
-  if (row >= p.rows || (n_kb > 0 && c0 == c1)) return;
-  const bool empty = L == 0.f;
-  const float inv = empty ? 0.f : 1.f / L, unit = value_unit(M, MV);
-  uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + qrow * D + lane * E);
-#pragma unroll
-  for (int e = 0; e < E; e += 2) out[e / 2] = pack_bf16x2(o[e] * inv * unit, o[e + 1] * inv * unit);
-  if (p.lse && lane == 0)
-    p.lse[qrow] = empty ? neg_inf() : (M + __log2f(L)) * 0.69314718055994530942f;
 }
 
 template <int D, int NT>
@@ -1163,13 +1248,18 @@ cudaError_t launch_nt(const PagedDecodeParams& p, cudaStream_t stream) {
                          row_blocks, part_o, part_ml);
   hook_after(stream);
   if (e != cudaSuccess) return e;
+  // Four warps a row while there are no more rows than the GPU holds CTAs at once (8 per SM by
+  // registers), then a warp each and no more CTAs than that.  1024 rows: 24.3 us with four warps
+  // each, 26.0 with one; 2304 rows: 43.5 and 40.3.  2048 CTAs of one group: 45.7 us, 1024 of two 44.1.
   const int items = p.B * p.s.Hkv;
-  // four warps a row while there are no more rows than the GPU holds CTAs of 128 threads at once
-  if (1LL * p.rows * items <= 16 * kSms)
-    return launch_dependent(fa_decode_paged_merge<D, kWarps>, dim3(p.rows, items), dim3(kThreads), 0,
-                            stream, p, row_blocks, 8 * NT, ctas, c_o, c_ml);
-  return launch_dependent(fa_decode_paged_merge<D, 1>, dim3((p.rows + kWarps - 1) / kWarps, items),
-                          dim3(kThreads), 0, stream, p, row_blocks, 8 * NT, ctas, c_o, c_ml);
+  constexpr int kMost = 8 * kSms;
+  if (1LL * p.rows * items <= kMost)
+    return launch_dependent(fa_decode_paged_merge<D, kWarps>, dim3(p.rows * items), dim3(kThreads), 0,
+                            stream, p, row_blocks, 8 * NT, ctas, 1, c_o, c_ml);
+  const int groups = (p.rows + kWarps - 1) / kWarps * items;
+  const int span = (groups + kMost - 1) / kMost;
+  return launch_dependent(fa_decode_paged_merge<D, 1>, dim3((groups + span - 1) / span),
+                          dim3(kThreads), 0, stream, p, row_blocks, 8 * NT, ctas, span, c_o, c_ml);
 }
 
 template <int D>
