@@ -351,7 +351,9 @@ fa_status fa_kv_assign(const int32_t* seqlens, const int32_t* newlens, int B, in
  *                at most +-448; an infinity becomes +-448, a NaN the NaN code
  *   held codes [0, n) = code * s_old / s, rounded again, if s > s_old
  *   k_bounds (NULL: not kept) = the run's bounds, merged for n > 0 with the old
- *                ones times s_old / s, rounded outwards; NaN codes count as 0
+ *                ones times s_old / s, rounded outwards (for a ratio that is no power
+ *                of two also rounded like the codes first: they enclose them either
+ *                way); NaN codes count as 0
  * A scale only grows within a page until its offset 0 is written again.  With
  * power-of-two scales a held code changes only where it becomes subnormal.
  * Codes behind the run are left as they were.  A page must not appear in two

@@ -367,6 +367,14 @@ __global__ void __launch_bounds__(WriteTile<D, PS>::kThreads, 640 / WriteTile<D,
             const float2 u = __half22float2(old_hi), v = __half22float2(old_lo);
             f = make_float2(fmaxf(f.x, ceilf(u.x * ratio)), fmaxf(f.y, ceilf(u.y * ratio)));
             g = make_float2(fminf(g.x, floorf(v.x * ratio)), fminf(g.y, floorf(v.y * ratio)));
+            // A ratio that is no power of two rounds codes, some away from zero.  Rounding keeps
+            // their order, so the bound rounded like a code encloses them.
+            if ((__float_as_uint(ratio) & 0x7fffffu) != 0) {
+              const float2 a = e4m3x2_to_f32x2(pack_e4m3x2(4.f * u.x * ratio, 4.f * u.y * ratio));
+              const float2 b = e4m3x2_to_f32x2(pack_e4m3x2(4.f * v.x * ratio, 4.f * v.y * ratio));
+              f = make_float2(fmaxf(f.x, ceilf(a.x * 0.25f)), fmaxf(f.y, ceilf(a.y * 0.25f)));
+              g = make_float2(fminf(g.x, floorf(b.x * 0.25f)), fminf(g.y, floorf(b.y * 0.25f)));
+            }
           }
           reinterpret_cast<char2*>(bounds + tile * 2 * D)[c] =
               make_char2(static_cast<signed char>(f.x), static_cast<signed char>(f.y));

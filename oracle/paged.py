@@ -119,8 +119,11 @@ class Cache:
             y = np.nan_to_num(E4M3[new], nan=0.0) / 4
             hi, lo = np.ceil(y.max(axis=0)), np.floor(y.min(axis=0))
             if off:
-                hi = np.maximum(hi, np.ceil(self.bounds[page, h, 0] * r))
-                lo = np.minimum(lo, np.floor(self.bounds[page, h, 1] * r))
+                top, low = self.bounds[page, h, 0] * r, self.bounds[page, h, 1] * r
+                hi, lo = np.maximum(hi, np.ceil(top)), np.minimum(lo, np.floor(low))
+                if math.frexp(r)[0] != 0.5:  # held codes are rounded too
+                    hi = np.maximum(hi, np.ceil(E4M3[encode(4 * top)] / 4))
+                    lo = np.minimum(lo, np.floor(E4M3[encode(4 * low)] / 4))
             self.bounds[page, h] = np.stack([hi, lo])
 
     def values(self, which, page, h):
