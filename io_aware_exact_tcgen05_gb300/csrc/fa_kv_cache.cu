@@ -365,8 +365,9 @@ __global__ void __launch_bounds__(WriteTile<D, PS>::kThreads, 640 / WriteTile<D,
               old_lo = __floats2half2_rn(v.x, v.y);
             }
             const float2 u = __half22float2(old_hi), v = __half22float2(old_lo);
-            f = make_float2(fmaxf(f.x, ceilf(u.x * ratio)), fmaxf(f.y, ceilf(u.y * ratio)));
-            g = make_float2(fminf(g.x, floorf(v.x * ratio)), fminf(g.y, floorf(v.y * ratio)));
+            const float by = fmaxf(ratio, 1.1754944e-38f);  // a ratio of 0 would round inwards
+            f = make_float2(fmaxf(f.x, ceilf(u.x * by)), fmaxf(f.y, ceilf(u.y * by)));
+            g = make_float2(fminf(g.x, floorf(v.x * by)), fminf(g.y, floorf(v.y * by)));
             // A ratio that is no power of two rounds codes, some away from zero.  Rounding keeps
             // their order, so the bound rounded like a code encloses them.
             if ((__float_as_uint(ratio) & 0x7fffffu) != 0) {

@@ -50,3 +50,22 @@ def test_bounds_enclose_codes_whose_scale_is_no_power_of_two(d):
     most = np.maximum(4 * old[:, :, 0] * r * np.where(old[:, :, 0] > 0, 1 + 2.0 ** -4, 1 - 2.0 ** -4), new)
     least = np.minimum(4 * old[:, :, 1] * r * np.where(old[:, :, 1] < 0, 1 + 2.0 ** -4, 1 - 2.0 ** -4), new)
     assert np.all(4 * bounds[:, :, 0] < most + 4) and np.all(4 * bounds[:, :, 1] > least - 4)
+
+
+def test_bounds_of_scales_too_far_apart_for_their_ratio():
+    """s_old / s below fp32's range: a bound that is not 0 stays 1 or -1, rounded outwards."""
+    ps, d, pages = 16, 64, 4
+    cache = po.Cache(np.zeros((pages, 1, ps, d), np.uint8), np.zeros((pages, 1, ps, d), np.uint8),
+                     np.zeros((pages, 1)), np.zeros((pages, 1)), np.zeros((pages, 1, 2, d)))
+    dev = on_gpu(cache)
+    gen = torch.Generator().manual_seed(3)
+    for off, n, mult, flat in ((0, 3, 1e-29, 0), (3, 2, 1e21, d // 2), (5, 1, 1e38, d - 8)):
+        k = (torch.randn(1, pages * n, d, generator=gen) * mult).to(torch.bfloat16)
+        k[:, :, :flat] = 0
+        slots = [p * ps + off + i for p in range(pages) for i in range(n)]
+        cache.write(f64(k), f64(k), slots)
+        fa.fa_kv_write_fp8(k.to(DEV), k.to(DEV), torch.tensor(slots, device=DEV), *dev[:4],
+                           k_bounds=dev[4])
+        torch.cuda.synchronize()
+        assert np.array_equal(f64(dev[2]), cache.scale[0])
+        assert np.array_equal(dev[4].cpu().numpy().astype(np.int64), cache.bounds)
