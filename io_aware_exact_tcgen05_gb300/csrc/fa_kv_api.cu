@@ -41,6 +41,9 @@ fa_status check_shape(const fa::KvShape& s) {
   return FA_OK;
 }
 
+// Most query rows of a call: row tiles are rounded up in 32 bits.
+constexpr long long kMaxRows = 0x7fffffffLL - 64;
+
 // Query rows of one KV head: heads of the group x Sq, and the limits of the grids.
 fa_status check_rows(int B, int Hq, int Hkv, int Sq, int max_blocks, int page_size, int* rows) {
   if (B < 1 || Hq < 1 || Sq < 1 || max_blocks < 1)
@@ -52,7 +55,7 @@ fa_status check_rows(int B, int Hq, int Hkv, int Sq, int max_blocks, int page_si
   if (1LL * B * Hkv > 65535)
     return api_fail(FA_ERR_INVALID_ARG, "B x Hkv (%lld) > 65535", 1LL * B * Hkv);
   const long long r = 1LL * (Hq / Hkv) * Sq;
-  if (r * B * Hkv >= (1LL << 31))
+  if (r * B * Hkv > kMaxRows)
     return api_fail(FA_ERR_INVALID_ARG, "tensor too large for 32-bit row indices");
   *rows = static_cast<int>(r);
   return FA_OK;
@@ -265,7 +268,7 @@ fa_status fa_select_blocks(const void* q, const int8_t* k_bounds, const float* k
 size_t fa_decode_paged_fp8_workspace_size(int B, int Hq, int Hkv, int Sq, int d) {
   if (B < 1 || Hq < 1 || Hkv < 1 || Sq < 1 || d < 1 || Hq % Hkv != 0) return 0;
   const long long rows = 1LL * (Hq / Hkv) * Sq;
-  if (rows > 0x7fffffffLL) return 0;  // the call refuses it
+  if (rows > kMaxRows) return 0;  // the call refuses it
   return fa::decode_paged_workspace(B, Hkv, static_cast<int>(rows), d);
 }
 
