@@ -439,9 +439,12 @@ def _have(t, name, dtype, shape, dev):
 def _dims(t, name, ndim):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dim() != ndim:
+    shape = t.shape
+    if len(shape) != ndim:
         raise ValueError(f"{name} must have {ndim} dims")
-    return t.shape
+    if max(shape) > 0x7fffffff:  # cut to its low 32 bits on the way
+        raise ValueError(f"a size of {name} ({max(shape)}) does not fit 32 bits")
+    return shape
 
 
 def _int(x, name):
@@ -581,7 +584,8 @@ def fa_kv_read_fp8(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens_k
 
 
 def fa_select_blocks_workspace_size(B, Hkv, max_blocks) -> int:
-    return int(load_library().fa_select_blocks_workspace_size(B, Hkv, max_blocks))
+    return int(load_library().fa_select_blocks_workspace_size(
+        _int(B, "B"), _int(Hkv, "Hkv"), _int(max_blocks, "max_blocks")))
 
 
 def fa_select_blocks(q, k_bounds, k_scale, block_table, seqlens_k, page_size: int, k_blocks: int,
@@ -616,7 +620,8 @@ def fa_select_blocks(q, k_bounds, k_scale, block_table, seqlens_k, page_size: in
 
 
 def fa_decode_paged_fp8_workspace_size(B, Hq, Hkv, Sq, d) -> int:
-    return int(load_library().fa_decode_paged_fp8_workspace_size(B, Hq, Hkv, Sq, d))
+    return int(load_library().fa_decode_paged_fp8_workspace_size(
+        _int(B, "B"), _int(Hq, "Hq"), _int(Hkv, "Hkv"), _int(Sq, "Sq"), _int(d, "d")))
 
 
 def fa_decode_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seqlens_k,

@@ -2,6 +2,7 @@
 import ctypes
 
 import pytest
+import torch
 
 import io_aware_exact_tcgen05_gb300 as fa
 from io_aware_exact_tcgen05_gb300 import build as fabuild
@@ -33,3 +34,21 @@ def test_rows_that_overflow_when_rounded_up_are_refused(lib, rows):
         assert call(lib, 1, rows) == fa.FA_ERR_INVALID_ARG
         assert b"32-bit row indices" in lib.fa_last_error_detail()
     assert lib.fa_decode_paged_fp8_workspace_size(1, 1, 1, rows, 64) == 0
+
+
+@pytest.mark.parametrize("shape", [(1, (1 << 32) + 4), ((1 << 31), 3)])
+def test_tensor_sizes_past_32_bits_are_refused(shape):
+    """ctypes would pass their low 32 bits: a table of 2^32 + 4 blocks as one of 4."""
+    table = torch.empty(shape, dtype=torch.int32, device="meta")
+    with pytest.raises(ValueError, match="block_table.*32 bits"):
+        fa._dims(table, "block_table", 2)
+
+
+def test_workspace_sizes_of_arguments_past_32_bits_are_refused(lib):
+    with pytest.raises(ValueError, match="32 bits"):
+        fa.fa_select_blocks_workspace_size(1, 2, (1 << 32) + 16)
+    for at in range(5):
+        args = [1, 8, 2, 1, 64]
+        args[at] += 1 << 32
+        with pytest.raises(ValueError, match="32 bits"):
+            fa.fa_decode_paged_fp8_workspace_size(*args)
