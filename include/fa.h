@@ -393,7 +393,8 @@ size_t fa_select_blocks_workspace_size(int B, int Hkv, int max_blocks);
  * fp32.  The first n_first and last n_last blocks of a request are always taken
  * (n_first + n_last <= k_blocks).  Equal scores: the lower block.  Blocks without
  * a page and NaN scores rank last.
- *   q bf16 [B,Hq,Sq,d]; seqlens_k int32 [B] (clamped to [0, max_blocks*page_size])
+ *   q bf16 [B,Hq,Sq,d]; seqlens_k int32 [B] (clamped to [0, max_blocks*page_size]);
+ *   B * Hkv at most 65535
  *   sel int32 [B,Hkv,k_blocks]: block indices, ascending, then -1
  *   n_sel int32 [B,Hkv]: min(k_blocks, ceil(seqlens_k / page_size))
  */
@@ -423,6 +424,8 @@ size_t fa_decode_paged_fp8_workspace_size(int B, int Hq, int Hkv, int Sq, int d)
  * V scales may lie as far apart as their range allows.  Weights are rounded to 11 bits
  * where they multiply the values; a weight * V scale below 2^-23 of the largest that its
  * row sees is off by at most 2^-34 of that largest.
+ * Scores are formed in fp32: where k_scale * max|q| * scale * 448 * d passes 2^126, rows may
+ * become NaN.  B * Hkv is at most 65535 (FA_ERR_INVALID_ARG; split larger batches).
  * Any Sq is accepted; for prompts, fa_kv_read_fp8 with fa_fwd_varlen is the
  * faster path (the rows of a KV head are served 32 at a time here).
  */

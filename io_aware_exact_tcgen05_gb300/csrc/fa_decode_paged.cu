@@ -130,9 +130,11 @@ __device__ __forceinline__ int item_blocks(const PagedDecodeParams& p, int item)
 
 // Places of a (request, KV head) and row block in the line: its blocks behind
 // kSegmentCost places without work, for what beginning and ending a segment costs (8000 to
-// 10000 clocks; 32 rows of 24 ragged requests: 62 us without them where 16 took 52 us, and
-// later 46.2 us with 16, 45.2 with 24, 46.2 with 32.  A multiple of the smallest share keeps
-// short requests on whole shares: 777 keys take 6.6 us with 24, 7.1 with 20).
+// 10000 clocks; 32 rows of 24 ragged requests took 62 us without them where 16 took 52).  Both
+// kernels use one value: 8, 12, 16, 20, 24, 32 take 24.1, 23.7, 23.6, 23.6, 23.9, 24.4 us in geometric
+// mean over 19 cases of up to 32 rows, and 12, 16, 20, 24 take 9.48, 9.42, 9.50, 9.42 us over 33
+// drawn ones, mostly narrow.  (A multiple of the smallest share keeps short requests on whole shares:
+// 777 keys take 6.1 us with 8, 16, 24, and 6.6 to 6.8 with 12 and 20.)
 __device__ __forceinline__ long long unit_places(int n_kb) {
   return n_kb > 0 ? n_kb + kSegmentCost : 0;
 }
@@ -361,7 +363,7 @@ __device__ __forceinline__ uint32_t nan_codes(uint32_t w) {
   return __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu);
 }
 
-// 32 bytes of a query row (16 channels) as f16 times `up`.
+// 16 bytes of a query row (8 channels) as f16 times `up`.
 __device__ __forceinline__ void scale_to_f16(const uint4& w, float up, uint32_t (&h)[4]) {
   const uint32_t x[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -712,11 +714,13 @@ __device__ __forceinline__ void pair_up(const uint32_t (&v)[4], uint32_t (&b)[2]
 // per warp: loaded from global memory each warp would take 4 bytes per lane and row (64
 // keys x 32 channels), and those 16 loads cost 6 us of 52.  Hidden blocks are not loaded: all
 // CTAs' reads of one place in their stead cost 1 us of 12 for 200 short items.
-// Latency bounds it: 11 warps per SM are there, tensor pipe 39% busy, shared memory 51%, issue
-// 38%; the waits are for products and conversions (27%), shared memory (16%), global memory
-// (10%).  43 us for 24 requests of 500 to 9000 keys, 32 rows, 4 KV heads (2.9 TB/s), of which 39
-// remain without any load.  (With the keys as M side, as the narrow kernel has it, 45 us;
-// a warp with all 32 rows to itself 68 us where this kernel's first form took 66.)
+// Latency bounds it: 11 warps per SM are there, tensor pipe 38% busy, shared memory 49%, issue
+// 40%; the waits are for products and conversions (26%), shared memory (16%), global memory
+// (10%).  41.6 us for 24 requests of 500 to 9000 keys, 32 rows, 4 KV heads (3.0 TB/s), of which 36
+// remain without loading keys and values.  (With the keys as M side, as the narrow kernel has it,
+// 45 us where this form took 43; a warp with all 32 rows to itself 68 us where this kernel's
+// first form took 66.)  With a lag of 4 or 2 in place of 6 the maxima move on more steps: 42.7 and
+// 45.3 us, 2% and 5% in geometric mean over 19 cases.
 // The running maxima are the CTA's; the vote on moving them is the barrier that
 // hands the weights over.  A segment's first step moves them without a vote.
 template <int D, int NT>
