@@ -1118,20 +1118,29 @@ __global__ void __launch_bounds__(kThreads)
   const long long share = share_of(Place::of(place.all) * row_blocks, items, ctas);
   int r, c0, c1;  // row of the unit, the CTAs of its first and last block
   auto locate = [&] {
+    if (n_kb == 0) return;
     const int rb = row / tile_rows;
     r = row - rb * tile_rows;
     const long long at = start + rb * unit_places(n_kb) + kSegmentCost;  // the unit's first block
     c0 = cta_of(at, share);
-    c1 = n_kb > 0 ? cta_of(at + n_kb - 1, share) : c0;
+    c1 = cta_of(at + n_kb - 1, share);
   };
   locate();
   // Every CTA waits, also one with nothing to join: what follows this kernel in
   // the stream may then rely on the partial kernel's completion as well.
   griddep_wait();
   while (true) {
-    if (n_kb == 0 || c0 != c1) {  // else one CTA has finished the rows of the unit
-      const bool real = row < p.rows;
-      const size_t qrow = static_cast<size_t>(item) * p.rows + row;
+    const bool real = row < p.rows;
+    const size_t qrow = static_cast<size_t>(item) * p.rows + row;
+    if (n_kb == 0) {  // no key: O = 0, LSE = -inf
+      if (real && part == 0) {
+        uint32_t* out =
+            reinterpret_cast<uint32_t*>(static_cast<__nv_bfloat16*>(p.o) + qrow * D + lane * E);
+#pragma unroll
+        for (int e = 0; e < E; e += 2) out[e / 2] = 0u;
+        if (p.lse && lane == 0) p.lse[qrow] = neg_inf();
+      }
+    } else if (c0 != c1) {  // else one CTA has finished the rows of the unit
       float M = kNoMax, L = 0.f, MV = kNoMax, o[E];
 #pragma unroll
       for (int e = 0; e < E; ++e) o[e] = 0.f;
@@ -1149,7 +1158,7 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
         for (int e = 0; e < E; ++e) o[e] = fmaf(w, acc(e), o[e]);
       };
-      if (real && n_kb > 0) {
+      if (real) {
         for (int c = c0 + part; c <= c1; c += kSplit * kBatch) {
           RowState ml[kBatch];
           float v[kBatch][E];
