@@ -412,8 +412,8 @@ __device__ __forceinline__ RowState row_state(float m, float l, float mv) {
   return make_float4(m, l, mv, 0.f);
 }
 
-// 2^(mv - m - 9) of a finished row: it multiplies acc / l, whose product alone lies in fp32's
-// range for every scale.
+// 2^(mv - m - 9) of a finished row.  It multiplies acc / l: with scales of 2^-100 it divided by a
+// large l would be subnormal.
 __device__ __forceinline__ float value_unit(float m, float mv) {
   return ex2_approx(mv - m - kWeightLog);
 }
