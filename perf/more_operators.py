@@ -85,10 +85,11 @@ def draw(rng):
     slopes = rng.random() < 0.5
     window = rng.choice([0, 0, _spread(rng, 1, 6000)])
     if op == "mask":
-        S = _spread(rng, 1, 131_072)
+        # the order of the documents is all that a seed gives this operator: enough of them that it differs
+        S = _spread(rng, 64, 131_072)
         B = _spread(rng, 1, max(1, min(64, 131_072 // S)))
-        return dict(op=op, B=B, S=S, docs=rng.choice([0, _spread(rng, 1, max(1, min(300, S)))]),
-                    prefix=rng.random() < 0.5, pad=rng.random() < 0.4, causal=rng.random() < 0.8, window=window)
+        return dict(op=op, B=B, S=S, docs=_spread(rng, 7, max(7, min(300, S // 8))), prefix=rng.random() < 0.5,
+                    pad=rng.random() < 0.4, causal=rng.random() < 0.8, window=window and max(window, 16))
     if op == "decode":
         hi = _spread(rng, 1, 32768)
         most = max(1, min(64, 2 * 32768 * 32 * 8 * 128 // (3 * hi * Hkv * d)))
