@@ -437,6 +437,142 @@ fa_status fa_decode_paged_fp8(const void* q, const void* k_cache, const void* v_
                               int page_size, int d, float scale, void* workspace,
                               size_t workspace_bytes, cudaStream_t stream);
 
+/*
+ * Between a projection and the scores
+ * ===================================
+ * fa_qk_norm_rope takes a projection's rows [token][head][channel] and gives the head-major
+ * tensors that the attention reads, in one pass: a norm of every query and key head vector, the
+ * position rotation, and for serving the rows of a padded cache.
+ *
+ * A strided view [B, S, H, d] of bf16 with contiguous channels: element (b, s, h, c) at
+ * ptr[b * stride_b + s * stride_t + h * stride_h + c].  ptr is 16-byte aligned; strides are in
+ * elements, >= 0 and multiples of 8 (those of dimensions of one element do not matter).
+ */
+typedef struct {
+  void* ptr;
+  long long stride_b, stride_t, stride_h;
+} fa_heads;
+
+/*
+ * For each token and head vector x of q and k (d is 64 or 128):
+ *   u = x * r * (weight + weight_offset),  r = 1 / sqrt(mean(x^2) + eps);  u = x without a weight
+ *   y = u with its first rot_dim channels turned: pair i, (a, b) -> (a c_i - b s_i, b c_i + a s_i),
+ *       c_i, s_i = cos, sin of position[freq_axis[i]] * inv_freq[i] (radians); the pairs are channels
+ *       (i, i + rot_dim / 2), or (2 i, 2 i + 1) when interleaved != 0
+ * and v is copied.  Arithmetic is fp32, y is rounded to bf16 once; angles are exact to 2^-31 turns
+ * for every position.
+ *   q view [B,S,Hq,d]; k, v views [B,S,Hkv,d]; v and v_out are NULL together
+ *   q_weight, k_weight  bf16 [d], 16-byte aligned, or NULL: no norm
+ *   positions  int32 [n_axes,B,S], any value; NULL: the token's row (below) on every axis
+ *   inv_freq   fp32 [rot_dim / 2], finite, magnitudes below 2^24; rot_dim is 0 or a multiple of 16 up to d
+ *   freq_axis  uint8 [rot_dim / 2] or NULL (axis 0); frequencies of axes >= n_axes do not turn
+ *   q_out [B,Hq,S,d]; k_out, v_out [B,Hkv,S_out,d]: token s of batch row b is row
+ *   row_start[b] + s (device int32[B]; NULL: 0).  Rows outside [0, S_out) are skipped, rows of no
+ *   token are left as they were.
+ * Outputs must not overlap inputs.
+ */
+fa_status fa_qk_norm_rope(const fa_heads* q, const fa_heads* k, const fa_heads* v, void* q_out,
+                          void* k_out, void* v_out, const int32_t* row_start, int S_out,
+                          const void* q_weight, const void* k_weight, float weight_offset,
+                          float eps, const int32_t* positions, int n_axes, const float* inv_freq,
+                          const uint8_t* freq_axis, int rot_dim, int interleaved, int B, int S,
+                          int Hq, int Hkv, int d, cudaStream_t stream);
+
+/* Bytes of device workspace fa_qk_norm_rope_bwd needs when a weight's gradient is asked for. */
+size_t fa_qk_norm_rope_bwd_workspace_size(int d);
+
+/*
+ * Gradients of fa_qk_norm_rope without row_start.  q, k: the forward's inputs (only read, and only
+ * needed, where there is a weight); dq_out [B,Hq,S,d], dk_out, dv_out [B,Hkv,S,d]: gradients of its
+ * outputs (dv_out and dv NULL together).  Written: the views dq [B,S,Hq,d], dk, dv [B,S,Hkv,d],
+ * none of which may overlap itself or another, and dq_weight, dk_weight fp32 [d] (NULL: not
+ * wanted).  With g = dy turned back and a = g * (weight + weight_offset):
+ *   dx = r * (a - x r mean(a x r)),   dweight = sum over tokens and heads of g x r
+ * Sums are fp32 in a fixed order: the same call gives the same bits.
+ */
+fa_status fa_qk_norm_rope_bwd(const fa_heads* q, const fa_heads* k, const void* dq_out,
+                              const void* dk_out, const void* dv_out, const fa_heads* dq,
+                              const fa_heads* dk, const fa_heads* dv, float* dq_weight,
+                              float* dk_weight, const void* q_weight, const void* k_weight,
+                              float weight_offset, float eps, const int32_t* positions,
+                              int n_axes, const float* inv_freq, const uint8_t* freq_axis,
+                              int rot_dim, int interleaved, int B, int S, int Hq, int Hkv, int d,
+                              void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * Row intervals: documents, prefixes, windows
+ * ===========================================
+ * The visible keys of a row are an interval [lo, hi).  fa_row_bounds writes the intervals of the
+ * usual masks (a caller may as well write its own), fa_mask_plan turns intervals into the tile
+ * plan that fa_fwd_scored and fa_bwd_scored skip by.  Both are made once for all layers of a step.
+ *
+ * Row i of batch row b is position p = i + Sk - Sq of Sk.
+ *   document [start, end): [0, Sk), or with cu_docs (device int32[n_docs + 1], non-decreasing offsets
+ *            into the B * Sk flattened positions) the document that holds b * Sk + p, cut at the
+ *            batch row's ends; positions of no document (and p < 0) see nothing
+ *   causal:  hi = min(end, max(p + 1, start + prefix)), else hi = end
+ *   window:  lo = max(start, p - window + 1) and, not causal, hi = min(hi, p + window); 0: none
+ * prefix (device int32[n_docs], or int32[B] without cu_docs; NULL: 0) is the number of keys at a
+ * document's start that all of its rows see (from its offset in cu_docs, or from the batch row's
+ * start where that cuts it); negative: padding, whose rows see nothing.
+ * row_lo, row_hi int32 [B,Sq] are written; rows without keys get 0, 0.
+ * B * Sq and B * Sk must be below 2^31, B at most 65535.
+ */
+fa_status fa_row_bounds(const int32_t* cu_docs, const int32_t* prefix, int n_docs, int32_t* row_lo,
+                        int32_t* row_hi, int B, int Sq, int Sk, int causal, int window,
+                        cudaStream_t stream);
+
+/* Bytes of a mask plan: 8 per row and some 60 per 128 rows and 128 keys. */
+size_t fa_mask_plan_size(int B, int Sq, int Sk);
+
+/* The tile plan of row_lo, row_hi int32 [B,Sq] (clamped to [0, Sk]; hi <= lo: no keys) into plan
+   (16-byte aligned, fa_mask_plan_size bytes), which holds all that the attention needs of them. */
+fa_status fa_mask_plan(const int32_t* row_lo, const int32_t* row_hi, int B, int Sq, int Sk,
+                       void* plan, size_t plan_bytes, cudaStream_t stream);
+
+/*
+ * Capped and biased scores
+ * ========================
+ * fa_fwd, fa_bwd and fa_decode on scores that are capped, biased by distance and masked by row
+ * intervals.  For row i of query head h at position p = i + Sk - Sq:
+ *   s_ij = scale * <q_i, k_j>
+ *   t_ij = softcap * tanh(s_ij / softcap)      (softcap 0: t = s)
+ *   z_ij = t_ij - slopes[h] * |p - j|          (slopes NULL: z = t)
+ *   O = softmax(z) V, LSE_i = ln sum_j exp(z_ij), over the keys of the row's interval in the plan
+ *   (plan NULL: all) and, when causal != 0, j <= p
+ * softcap is 0 or in [2^-20, 2^20]; slopes device fp32[Hq], finite, any sign (constants: no gradient).
+ * plan: fa_mask_plan of the same B, Sq, Sk; plan_bytes its size.  Rows without keys give O = 0,
+ * LSE = -inf and no gradient.  tanh is off by at most 1e-7 of its value or 2^-22, whichever is larger.
+ */
+fa_status fa_fwd_scored(const void* q, const void* k, const void* v, void* o, float* lse, int B,
+                        int Hq, int Hkv, int Sq, int Sk, int d, int causal, float scale,
+                        float softcap, const float* slopes, const void* plan, size_t plan_bytes,
+                        cudaStream_t stream);
+
+/* Its backward pass, by recomputation as fa_bwd: with P = exp(z - LSE) and dz = P * (dP - D),
+   ds = dz * (1 - (t / softcap)^2), dQ = scale * ds K, dK = scale * ds^T Q, dV = P^T dO.  The scores'
+   arguments are the forward's; workspace holds fa_bwd_workspace_size(B, Hq, Sq, d) bytes. */
+fa_status fa_bwd_scored(const void* q, const void* k, const void* v, const void* o,
+                        const void* dout, const float* lse, void* dq, void* dk, void* dv, int B,
+                        int Hq, int Hkv, int Sq, int Sk, int d, int causal, float scale,
+                        float softcap, const float* slopes, const void* plan, size_t plan_bytes,
+                        void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Bytes of device workspace fa_decode_scored needs. */
+size_t fa_decode_scored_workspace_size(int B, int Hq, int Hkv, int Sk_max, int d, int window);
+
+/*
+ * fa_decode on such scores.  The query of batch row b is position n - 1, n = seqlens_k[b] (clamped
+ * to [0, Sk_max]); it sees the keys [max(0, k_start[b], n - window), n) (k_start device int32[B] or
+ * NULL: 0; window 0: none).  No other key is read.  The split plan depends on the arguments,
+ * never on the values in seqlens_k and k_start.  B is at most 65535.
+ */
+fa_status fa_decode_scored(const void* q, const void* k_cache, const void* v_cache, void* o,
+                           float* lse, const int32_t* seqlens_k, const int32_t* k_start, int B,
+                           int Hq, int Hkv, int Sk_max, int d, float scale, float softcap,
+                           const float* slopes, int window, void* workspace,
+                           size_t workspace_bytes, cudaStream_t stream);
+
 /* Reads the device status words of the current device (this synchronises the
    device).  Returns FA_OK or FA_ERR_TIMEOUT; *code_out (may be NULL) receives
    the raw word (low 16 bits: error code, high 16 bits: wait site).  When
@@ -458,7 +594,7 @@ fa_status fa_selftest_wait_timeout(unsigned int* result, cudaStream_t stream);
 
 /* Profiling hook (the pages ask that a timing confirm which kernel actually
    ran).  start/stop are cudaEvent_t handles created by the caller.  The next
-   fa_fwd, fa_bwd, fa_decode or fa_decode_paged_fp8 call made on this host thread records `start`
+   fa_fwd, fa_bwd, fa_decode (their variants too) or fa_decode_paged_fp8 call made on this host thread records `start`
    on its stream right before its main kernel (fa_fwd: the attention kernel;
    fa_bwd: the key-tile kernel, not the preprocess or dQ-convert kernels;
    fa_decode and fa_decode_paged_fp8: the split partial kernel, not the merge)

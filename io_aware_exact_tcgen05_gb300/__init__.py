@@ -30,10 +30,19 @@ EXPORTED = ("fa_fwd", "fa_bwd", "fa_bwd_workspace_size", "fa_decode", "fa_decode
             "fa_bwd_varlen", "fa_fwd_dropout", "fa_bwd_dropout", "fa_key_mask_words",
             "fa_pack_key_mask", "fa_fwd_fp8", "fa_kv_assign", "fa_kv_write_fp8", "fa_kv_read_fp8",
             "fa_select_blocks", "fa_select_blocks_workspace_size", "fa_decode_paged_fp8",
-            "fa_decode_paged_fp8_workspace_size", "fa_device_status", "fa_selftest_wait_timeout",
+            "fa_decode_paged_fp8_workspace_size", "fa_qk_norm_rope", "fa_qk_norm_rope_bwd",
+            "fa_qk_norm_rope_bwd_workspace_size", "fa_row_bounds", "fa_mask_plan",
+            "fa_mask_plan_size", "fa_fwd_scored", "fa_bwd_scored", "fa_decode_scored",
+            "fa_decode_scored_workspace_size", "fa_device_status", "fa_selftest_wait_timeout",
             "fa_profile_next_launch", "fa_status_string", "fa_last_error_detail", "fa_version")
 
 _lib = None
+
+
+class _Heads(ctypes.Structure):
+    """fa_heads of include/fa.h: a strided view [B, S, H, d]."""
+    _fields_ = [("ptr", ctypes.c_void_p), ("stride_b", ctypes.c_longlong),
+                ("stride_t", ctypes.c_longlong), ("stride_h", ctypes.c_longlong)]
 
 
 class FAError(RuntimeError):
@@ -101,6 +110,25 @@ def load_library(path: str = LIB_PATH):
     lib.fa_select_blocks_workspace_size.restype = Z
     lib.fa_decode_paged_fp8_workspace_size.argtypes = [I, I, I, I, I]
     lib.fa_decode_paged_fp8_workspace_size.restype = Z
+    H = ctypes.POINTER(_Heads)
+    lib.fa_qk_norm_rope.argtypes = [H, H, H, P, P, P, P, I, P, P, F, F, P, I, P, P, I, I, I, I, I, I,
+                                    I, P]
+    lib.fa_qk_norm_rope_bwd.argtypes = [H, H, P, P, P, H, H, H, P, P, P, P, F, F, P, I, P, P, I, I, I,
+                                        I, I, I, I, P, Z, P]
+    lib.fa_row_bounds.argtypes = [P, P, I, P, P, I, I, I, I, I, P]
+    lib.fa_mask_plan.argtypes = [P, P, I, I, I, P, Z, P]
+    lib.fa_fwd_scored.argtypes = [P, P, P, P, P, I, I, I, I, I, I, I, F, F, P, P, Z, P]
+    lib.fa_bwd_scored.argtypes = [P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, F, F, P, P, Z, P, Z, P]
+    lib.fa_decode_scored.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, F, F, P, I, P, Z, P]
+    for f in (lib.fa_qk_norm_rope, lib.fa_qk_norm_rope_bwd, lib.fa_row_bounds, lib.fa_mask_plan,
+              lib.fa_fwd_scored, lib.fa_bwd_scored, lib.fa_decode_scored):
+        f.restype = I
+    lib.fa_qk_norm_rope_bwd_workspace_size.argtypes = [I]
+    lib.fa_mask_plan_size.argtypes = [I, I, I]
+    lib.fa_decode_scored_workspace_size.argtypes = [I, I, I, I, I, I]
+    for f in (lib.fa_qk_norm_rope_bwd_workspace_size, lib.fa_mask_plan_size,
+              lib.fa_decode_scored_workspace_size):
+        f.restype = Z
     lib.fa_status_string.argtypes = [I]
     lib.fa_status_string.restype = ctypes.c_char_p
     lib.fa_last_error_detail.restype = ctypes.c_char_p
@@ -658,6 +686,265 @@ def fa_decode_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seql
                                  ps, d, float(scale), workspace.data_ptr(), workspace.nbytes,
                                  _stream(stream))
     _check(st, "fa_decode_paged_fp8")
+    return o, lse
+
+
+# ------------------------------------- between a projection and the scores --
+
+def _view(t, name, shape, dev):
+    """fa_heads of a bf16 tensor of that shape [B, S, H, d] with contiguous channels."""
+    if not (isinstance(t, torch.Tensor) and t.dtype == _BF16 and t.get_device() == dev
+            and t.shape == shape):
+        _refuse(t, name, _BF16, shape, dev)
+    sb, st, sh, sc = t.stride()
+    if sc != 1:
+        raise ValueError(f"{name} must have contiguous channels")
+    return _Heads(t.data_ptr(), sb, st, sh)
+
+
+def _rotation(positions, inv_freq, freq_axis, q_weight, k_weight, B, S, d, dev):
+    """(n_axes, rot_dim) of a rotation, checked with the weights."""
+    n_axes, rot = 1, 0
+    if inv_freq is not None:
+        half, = _dims(inv_freq, "inv_freq", 1)
+        _have(inv_freq, "inv_freq", _F32, (half,), dev)
+        rot = 2 * half
+        if positions is not None:
+            if positions.dim() == 2:
+                _have(positions, "positions", _I32, (B, S), dev)
+            else:
+                n_axes = _dims(positions, "positions", 3)[0]
+                _have(positions, "positions", _I32, (n_axes, B, S), dev)
+        if freq_axis is not None:
+            _have(freq_axis, "freq_axis", _U8, (half,), dev)
+    elif positions is not None or freq_axis is not None:
+        raise ValueError("positions and freq_axis are given with inv_freq only")
+    for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _have(w, n, _BF16, (d,), dev)
+    return n_axes, rot
+
+
+def fa_qk_norm_rope(q, k, v=None, positions=None, inv_freq=None, freq_axis=None, q_weight=None,
+                    k_weight=None, weight_offset: float = 0.0, eps: float = 1e-6,
+                    interleaved: bool = False, q_out=None, k_out=None, v_out=None, row_start=None,
+                    stream=None):
+    """Norms of query and key heads, rotation and head-major layout in one pass (fa_qk_norm_rope).
+    q [B,S,Hq,d], k and v [B,S,Hkv,d] bf16: any views with contiguous channels, for example of a
+    packed projection.  q_weight/k_weight bf16 [d] (None: no norm); inv_freq fp32 [rot_dim/2] (None:
+    no rotation); positions int32 [B,S] or [n_axes,B,S] (None: the rows written); freq_axis uint8
+    [rot_dim/2].  k_out/v_out may be caches [B,Hkv,S_out,d] whose rows row_start[b] + s (int32 [B])
+    are written.  Returns (q_out [B,Hq,S,d], k_out, v_out or None)."""
+    lib, dev = load_library(), _device()
+    B, S, Hq, d = _dims(q, "q", 4)
+    Hkv = _dims(k, "k", 4)[2]
+    vq, vk = _view(q, "q", (B, S, Hq, d), dev), _view(k, "k", (B, S, Hkv, d), dev)
+    vv = None if v is None else _view(v, "v", (B, S, Hkv, d), dev)
+    n_axes, rot = _rotation(positions, inv_freq, freq_axis, q_weight, k_weight, B, S, d, dev)
+    rows = S
+    if row_start is not None:
+        _have(row_start, "row_start", _I32, (B,), dev)
+        if k_out is None or (v is not None and v_out is None):
+            raise ValueError("row_start is given with the caches k_out and v_out")
+    if k_out is not None:
+        rows = _dims(k_out, "k_out", 4)[2]
+    q_out = _out(q_out, "q_out", (B, Hq, S, d), _BF16, dev, stream)
+    k_out = _out(k_out, "k_out", (B, Hkv, rows, d), _BF16, dev, stream)
+    if v is not None:
+        v_out = _out(v_out, "v_out", (B, Hkv, rows, d), _BF16, dev, stream)
+    elif v_out is not None:
+        raise ValueError("v_out is given with v only")
+    st = lib.fa_qk_norm_rope(vq, vk, vv, q_out.data_ptr(), k_out.data_ptr(), _ptr(v_out),
+                             _ptr(row_start), rows, _ptr(q_weight), _ptr(k_weight),
+                             float(weight_offset), float(eps), _ptr(positions), n_axes,
+                             _ptr(inv_freq), _ptr(freq_axis), rot, int(bool(interleaved)), B, S, Hq,
+                             Hkv, d, _stream(stream))
+    _check(st, "fa_qk_norm_rope")
+    return q_out, k_out, v_out
+
+
+def fa_qk_norm_rope_bwd_workspace_size(d) -> int:
+    return int(load_library().fa_qk_norm_rope_bwd_workspace_size(_int(d, "d")))
+
+
+def fa_qk_norm_rope_bwd(q, k, dq_out, dk_out, dv_out=None, positions=None, inv_freq=None,
+                        freq_axis=None, q_weight=None, k_weight=None, weight_offset: float = 0.0,
+                        eps: float = 1e-6, interleaved: bool = False, dq=None, dk=None, dv=None,
+                        dq_weight=None, dk_weight=None, workspace=None, stream=None):
+    """Gradients of fa_qk_norm_rope (without row_start): dq_out [B,Hq,S,d], dk_out/dv_out
+    [B,Hkv,S,d] bf16 are those of its outputs.  dq [B,S,Hq,d], dk and dv [B,S,Hkv,d] may be views with
+    contiguous channels (of a packed projection's gradient); new ones are contiguous.
+    Returns (dq, dk, dv or None, dq_weight fp32 [d] or None, dk_weight or None)."""
+    lib, dev = load_library(), _device()
+    B, Hq, S, d = _dims(dq_out, "dq_out", 4)
+    Hkv = _dims(dk_out, "dk_out", 4)[1]
+    _have(dq_out, "dq_out", _BF16, (B, Hq, S, d), dev)
+    _have(dk_out, "dk_out", _BF16, (B, Hkv, S, d), dev)
+    n_axes, rot = _rotation(positions, inv_freq, freq_axis, q_weight, k_weight, B, S, d, dev)
+    vq = None if q_weight is None else _view(q, "q", (B, S, Hq, d), dev)
+    vk = None if k_weight is None else _view(k, "k", (B, S, Hkv, d), dev)
+    dq = _new((B, S, Hq, d), _BF16, dev, stream) if dq is None else dq
+    dk = _new((B, S, Hkv, d), _BF16, dev, stream) if dk is None else dk
+    gq, gk, gv = _view(dq, "dq", (B, S, Hq, d), dev), _view(dk, "dk", (B, S, Hkv, d), dev), None
+    if dv_out is not None:
+        _have(dv_out, "dv_out", _BF16, (B, Hkv, S, d), dev)
+        dv = _new((B, S, Hkv, d), _BF16, dev, stream) if dv is None else dv
+        gv = _view(dv, "dv", (B, S, Hkv, d), dev)
+    elif dv is not None:
+        raise ValueError("dv is given with dv_out only")
+    if q_weight is not None:
+        dq_weight = _out(dq_weight, "dq_weight", (d,), _F32, dev, stream)
+    elif dq_weight is not None:
+        raise ValueError("dq_weight is given with q_weight only")
+    if k_weight is not None:
+        dk_weight = _out(dk_weight, "dk_weight", (d,), _F32, dev, stream)
+    elif dk_weight is not None:
+        raise ValueError("dk_weight is given with k_weight only")
+    nbytes = 0
+    if q_weight is not None or k_weight is not None:
+        workspace = _workspace(workspace, lib.fa_qk_norm_rope_bwd_workspace_size(d), dev, stream)
+        nbytes = workspace.nbytes
+    st = lib.fa_qk_norm_rope_bwd(vq, vk, dq_out.data_ptr(), dk_out.data_ptr(), _ptr(dv_out), gq, gk,
+                                 gv, _ptr(dq_weight), _ptr(dk_weight), _ptr(q_weight),
+                                 _ptr(k_weight), float(weight_offset), float(eps), _ptr(positions),
+                                 n_axes, _ptr(inv_freq), _ptr(freq_axis), rot,
+                                 int(bool(interleaved)), B, S, Hq, Hkv, d, _ptr(workspace), nbytes,
+                                 _stream(stream))
+    _check(st, "fa_qk_norm_rope_bwd")
+    return dq, dk, dv, dq_weight, dk_weight
+
+
+# ------------------------------------------------ capped and biased scores --
+
+def fa_row_bounds(B: int, Sq: int, Sk: int, causal: bool, window: int = 0, cu_docs=None, prefix=None,
+                  row_lo=None, row_hi=None, stream=None):
+    """Visible keys [lo, hi) of every row under documents, prefixes and a window (fa_row_bounds).
+    cu_docs int32 [n_docs+1] offsets into the B * Sk flattened positions; prefix int32 [n_docs] ([B]
+    without cu_docs), negative for padding.  Returns (row_lo, row_hi) int32 [B,Sq]."""
+    lib, dev = load_library(), _device()
+    B, Sq, Sk = _int(B, "B"), _int(Sq, "Sq"), _int(Sk, "Sk")
+    if min(B, Sq, Sk) < 1:
+        raise ValueError(f"sizes must be >= 1 (B={B} Sq={Sq} Sk={Sk})")
+    n_docs = 0
+    if cu_docs is not None:
+        n_docs = _dims(cu_docs, "cu_docs", 1)[0] - 1
+        _have(cu_docs, "cu_docs", _I32, (n_docs + 1,), dev)
+    if prefix is not None:
+        _have(prefix, "prefix", _I32, (B if cu_docs is None else n_docs,), dev)
+    row_lo = _out(row_lo, "row_lo", (B, Sq), _I32, dev, stream)
+    row_hi = _out(row_hi, "row_hi", (B, Sq), _I32, dev, stream)
+    st = lib.fa_row_bounds(_ptr(cu_docs), _ptr(prefix), n_docs, row_lo.data_ptr(), row_hi.data_ptr(),
+                           B, Sq, Sk, int(bool(causal)), _int(window, "window"), _stream(stream))
+    _check(st, "fa_row_bounds")
+    return row_lo, row_hi
+
+
+def fa_mask_plan_size(B, Sq, Sk) -> int:
+    return int(load_library().fa_mask_plan_size(_int(B, "B"), _int(Sq, "Sq"), _int(Sk, "Sk")))
+
+
+def fa_mask_plan(row_lo, row_hi, Sk: int, plan=None, stream=None):
+    """The tile plan of row intervals (fa_mask_plan): row_lo, row_hi int32 [B,Sq].  Returns the plan,
+    a uint8 tensor of fa_mask_plan_size(B, Sq, Sk) bytes for fa_fwd_scored and fa_bwd_scored."""
+    lib, dev = load_library(), _device()
+    B, Sq = _dims(row_lo, "row_lo", 2)
+    Sk = _int(Sk, "Sk")
+    _have(row_lo, "row_lo", _I32, (B, Sq), dev)
+    _have(row_hi, "row_hi", _I32, (B, Sq), dev)
+    plan = _out(plan, "plan", (lib.fa_mask_plan_size(B, Sq, Sk),), _U8, dev, stream)
+    st = lib.fa_mask_plan(row_lo.data_ptr(), row_hi.data_ptr(), B, Sq, Sk, plan.data_ptr(),
+                          plan.nbytes, _stream(stream))
+    _check(st, "fa_mask_plan")
+    return plan
+
+
+def _scored_args(q, k, v, slopes, plan, dev):
+    """(B, Hq, Hkv, Sq, Sk, d, plan bytes) of an attention call on capped or biased scores."""
+    B, Hq, Sq, d = _dims(q, "q", 4)
+    _, Hkv, Sk, _ = _dims(k, "k", 4)
+    _have(q, "q", _BF16, (B, Hq, Sq, d), dev)
+    _have(k, "k", _BF16, (B, Hkv, Sk, d), dev)
+    _have(v, "v", _BF16, (B, Hkv, Sk, d), dev)
+    if slopes is not None:
+        _have(slopes, "slopes", _F32, (Hq,), dev)
+    if plan is None:
+        return B, Hq, Hkv, Sq, Sk, d, 0
+    _have(plan, "plan", _U8, (load_library().fa_mask_plan_size(B, Sq, Sk),), dev)
+    return B, Hq, Hkv, Sq, Sk, d, plan.nbytes
+
+
+def fa_fwd_scored(q, k, v, causal: bool, scale: float, softcap: float = 0.0, slopes=None, plan=None,
+                  o=None, lse=None, stream=None):
+    """Attention on capped and biased scores (fa_fwd_scored): q [B,Hq,Sq,d], k/v [B,Hkv,Sk,d] bf16;
+    softcap 0 for none; slopes fp32 [Hq] of the bias -slope * distance; plan from fa_mask_plan.
+    Returns (o, lse)."""
+    lib, dev = load_library(), _device()
+    B, Hq, Hkv, Sq, Sk, d, nplan = _scored_args(q, k, v, slopes, plan, dev)
+    o = _out(o, "o", (B, Hq, Sq, d), _BF16, dev, stream)
+    lse = _out(lse, "lse", (B, Hq, Sq), _F32, dev, stream)
+    st = lib.fa_fwd_scored(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), B,
+                           Hq, Hkv, Sq, Sk, d, int(bool(causal)), float(scale), float(softcap),
+                           _ptr(slopes), _ptr(plan), nplan, _stream(stream))
+    _check(st, "fa_fwd_scored")
+    return o, lse
+
+
+def fa_bwd_scored(q, k, v, o, dout, lse, causal: bool, scale: float, softcap: float = 0.0,
+                  slopes=None, plan=None, dq=None, dk=None, dv=None, workspace=None, stream=None):
+    """dQ, dK, dV of fa_fwd_scored (fa_bwd_scored), with the forward's arguments.  The workspace is
+    fa_bwd_workspace_size(B, Hq, Sq, d) bytes.  Returns (dq, dk, dv)."""
+    lib, dev = load_library(), _device()
+    B, Hq, Hkv, Sq, Sk, d, nplan = _scored_args(q, k, v, slopes, plan, dev)
+    _have(o, "o", _BF16, (B, Hq, Sq, d), dev)
+    _have(dout, "dout", _BF16, (B, Hq, Sq, d), dev)
+    _have(lse, "lse", _F32, (B, Hq, Sq), dev)
+    dq = _out(dq, "dq", (B, Hq, Sq, d), _BF16, dev, stream)
+    dk = _out(dk, "dk", (B, Hkv, Sk, d), _BF16, dev, stream)
+    dv = _out(dv, "dv", (B, Hkv, Sk, d), _BF16, dev, stream)
+    workspace = _workspace(workspace, fa_bwd_workspace_size(B, Hq, Sq, d), dev, stream)
+    st = lib.fa_bwd_scored(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), dout.data_ptr(),
+                           lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, Hq, Hkv,
+                           Sq, Sk, d, int(bool(causal)), float(scale), float(softcap), _ptr(slopes),
+                           _ptr(plan), nplan, workspace.data_ptr(), workspace.nbytes,
+                           _stream(stream))
+    _check(st, "fa_bwd_scored")
+    return dq, dk, dv
+
+
+def fa_decode_scored_workspace_size(B, Hq, Hkv, Sk_max, d, window=0) -> int:
+    return int(load_library().fa_decode_scored_workspace_size(
+        _int(B, "B"), _int(Hq, "Hq"), _int(Hkv, "Hkv"), _int(Sk_max, "Sk_max"), _int(d, "d"),
+        _int(window, "window")))
+
+
+def fa_decode_scored(q, k_cache, v_cache, seqlens_k, scale: float, softcap: float = 0.0, slopes=None,
+                     window: int = 0, k_start=None, o=None, lse=None, workspace=None, stream=None):
+    """Single-query decode on capped and biased scores (fa_decode_scored): q [B,Hq,1,d],
+    k_cache/v_cache [B,Hkv,Sk_max,d] bf16, seqlens_k int32 [B]; window: how many last keys are seen
+    (0: all); k_start int32 [B]: first key.  Returns (o [B,Hq,1,d], lse [B,Hq])."""
+    lib, dev = load_library(), _device()
+    B, Hq, one, d = _dims(q, "q", 4)
+    _, Hkv, Sk_max, _ = _dims(k_cache, "k_cache", 4)
+    if one != 1:
+        raise ValueError(f"q must be [B, Hq, 1, d], got {tuple(q.shape)}")
+    _have(q, "q", _BF16, (B, Hq, 1, d), dev)
+    _have(k_cache, "k_cache", _BF16, (B, Hkv, Sk_max, d), dev)
+    _have(v_cache, "v_cache", _BF16, (B, Hkv, Sk_max, d), dev)
+    _have(seqlens_k, "seqlens_k", _I32, (B,), dev)
+    if k_start is not None:
+        _have(k_start, "k_start", _I32, (B,), dev)
+    if slopes is not None:
+        _have(slopes, "slopes", _F32, (Hq,), dev)
+    window = _int(window, "window")
+    o = _out(o, "o", (B, Hq, 1, d), _BF16, dev, stream)
+    lse = _out(lse, "lse", (B, Hq), _F32, dev, stream)
+    workspace = _workspace(
+        workspace, lib.fa_decode_scored_workspace_size(B, Hq, Hkv, Sk_max, d, window), dev, stream)
+    st = lib.fa_decode_scored(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), o.data_ptr(),
+                              lse.data_ptr(), seqlens_k.data_ptr(), _ptr(k_start), B, Hq, Hkv,
+                              Sk_max, d, float(scale), float(softcap), _ptr(slopes), window,
+                              workspace.data_ptr(), workspace.nbytes, _stream(stream))
+    _check(st, "fa_decode_scored")
     return o, lse
 
 

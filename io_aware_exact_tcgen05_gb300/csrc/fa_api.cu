@@ -17,6 +17,7 @@
 #include "../../include/fa.h"
 #include "fa_internal.h"
 #include "fa_kv.h"
+#include "fa_scored.h"
 
 namespace fa {
 ProfileHook& profile_hook() {
@@ -248,7 +249,8 @@ const fa::DropoutArgs kNoDropout{0u, 0u, 0u, 0u, 1.f, 0u};
 fa_status fwd_launch(const void* q, const void* k, const void* v, void* o, float* lse, int B,
                      int Hq, int Hkv, int Sq, int Sk, int d, int causal, float scale,
                      const SeqLayout& lay, const uint32_t* key_bits, const fa::DropoutArgs& drop,
-                     cudaStream_t stream) {
+                     cudaStream_t stream, const fa::ScoreArgs* scored = nullptr,
+                     bool capped = false) {
   FA_TRY(check_ptr(q, "q"));
   FA_TRY(check_ptr(k, "k"));
   FA_TRY(check_ptr(v, "v"));
@@ -295,7 +297,8 @@ fa_status fwd_launch(const void* q, const void* k, const void* v, void* o, float
   p.rescale_log2 = 8.0f;
   if (1LL * p.n_rbu * p.units_per_rbu >= (1LL << 31))
     return fail(FA_ERR_INVALID_ARG, "grid too large");
-  cudaError_t e = fa::launch_fwd(d, tq, tk, tv, p, stream);
+  cudaError_t e = scored ? fa::launch_fwd_scored(d, tq, tk, tv, p, *scored, capped, stream)
+                         : fa::launch_fwd(d, tq, tk, tv, p, stream);
   if (e != cudaSuccess) return fail(FA_ERR_CUDA, "fa_fwd launch: %s", cudaGetErrorString(e));
   return ok();
 }
@@ -304,7 +307,8 @@ fa_status bwd_launch(const void* q, const void* k, const void* v, const void* o,
                      const float* lse, void* dq, void* dk, void* dv, int B, int Hq, int Hkv,
                      int Sq, int Sk, int d, int causal, float scale, const SeqLayout& lay,
                      const uint32_t* key_bits, const fa::DropoutArgs& drop, void* workspace,
-                     size_t workspace_bytes, cudaStream_t stream) {
+                     size_t workspace_bytes, cudaStream_t stream,
+                     const fa::ScoreArgs* scored = nullptr, bool capped = false) {
   FA_TRY(check_ptr(q, "q"));
   FA_TRY(check_ptr(k, "k"));
   FA_TRY(check_ptr(v, "v"));
@@ -366,9 +370,52 @@ fa_status bwd_launch(const void* q, const void* k, const void* v, const void* o,
     return fail(FA_ERR_INVALID_ARG, "grid too large");
   CUtensorMap tdq;
   FA_TRY(make_map_acc(&tdq, p.dq_acc, 1L * B * Hq, Sq, d));
-  cudaError_t e = fa::launch_bwd(d, tq, tk, tv, tdo, tdq, p, stream);
+  cudaError_t e =
+      scored ? fa::launch_bwd_scored(d, tq, tk, tv, tdo, tdq, p, *scored, capped, stream)
+             : fa::launch_bwd(d, tq, tk, tv, tdo, tdq, p, stream);
   if (e != cudaSuccess) return fail(FA_ERR_CUDA, "fa_bwd launch: %s", cudaGetErrorString(e));
   return ok();
+}
+
+// The arithmetic of capped and biased scores (fa_score.cuh) from the caller's numbers.
+fa_status make_score(float scale, float softcap, const float* slopes, const void* plan,
+                     size_t plan_bytes, int B, int Sq, int Sk, fa::ScoreArgs* out) {
+  if (!std::isfinite(scale) || scale < 0.f)
+    return fail(FA_ERR_INVALID_ARG, "scale (%g) must be finite and >= 0", (double)scale);
+  if (!(softcap == 0.f || (softcap >= 0x1p-20f && softcap <= 0x1p20f)))
+    return fail(FA_ERR_INVALID_ARG, "softcap (%g) must be 0 (none) or lie in [2^-20, 2^20]",
+                (double)softcap);
+  FA_TRY(check_i32(slopes, "slopes"));
+  fa::ScoreArgs sc{};
+  sc.slopes = slopes;
+  if (plan) {
+    FA_TRY(check_ptr(plan, "plan"));
+    const size_t need = fa_mask_plan_size(B, Sq, Sk);
+    if (plan_bytes < need)
+      return fail(FA_ERR_WORKSPACE, "the mask plan of these sizes has %zu bytes, got %zu", need,
+                  plan_bytes);
+    sc.plan = fa::mask_plan_view(plan, B, Sq, Sk);
+  }
+  if (softcap > 0.f) {
+    const double log2e = 1.4426950408889634074, a = static_cast<double>(scale) / softcap;
+    if (2 * a * log2e > FLT_MAX)
+      return fail(FA_ERR_INVALID_ARG, "scale / softcap (%g) is too large", a);
+    sc.a = static_cast<float>(a);
+    sc.two_a_log2e = static_cast<float>(2 * a * log2e);
+    sc.cap_log2e = static_cast<float>(softcap * log2e);
+    sc.inv_cap_log2e = static_cast<float>(1 / (softcap * log2e));
+    // tanh(x) / x = 1 + c1 x^2 + .. + c4 x^8 for |x| <= 5/8, fitted in the maximum norm
+    const double fit[5] = {0.9999998807907104, -0.3333200514316559, 0.13305158913135529,
+                           -0.051847752183675766, 0.015084016136825085};
+    double f = a * softcap * log2e;
+    for (int i = 0; i < 5; ++i, f *= a * a) sc.poly[i] = static_cast<float>(fit[i] * f);
+    // the folded coefficients stay normal numbers in this range (about scale * a^8 the smallest)
+    const double c = a * softcap * log2e;
+    const bool fits = a >= 0x1p-13 && a <= 0x1p11 && c >= 0x1p-12 && c <= 0x1p12;
+    sc.small = fits ? static_cast<float>(0.625 / a) : -1.f;
+  }
+  *out = sc;
+  return FA_OK;
 }
 
 }  // namespace
@@ -443,6 +490,97 @@ fa_status fa_fwd_varlen(const void* q, const void* k, const void* v, void* o, fl
                        total_k, &lay));
   return fwd_launch(q, k, v, o, lse, 1, Hq, Hkv, total_q, total_k, d, causal, scale, lay,
                     key_mask_bits, kNoDropout, stream);
+}
+
+fa_status fa_fwd_scored(const void* q, const void* k, const void* v, void* o, float* lse, int B,
+                        int Hq, int Hkv, int Sq, int Sk, int d, int causal, float scale,
+                        float softcap, const float* slopes, const void* plan, size_t plan_bytes,
+                        cudaStream_t stream) {
+  FA_TRY(check_sizes(B, Hq, Hkv, Sq, Sk, d));
+  fa::ScoreArgs sc{};
+  FA_TRY(make_score(scale, softcap, slopes, plan, plan_bytes, B, Sq, Sk, &sc));
+  SeqLayout lay{};
+  lay.grid_b = B;
+  lay.longest_q = Sq;
+  lay.longest_k = Sk;
+  return fwd_launch(q, k, v, o, lse, B, Hq, Hkv, Sq, Sk, d, causal, scale, lay, nullptr,
+                    kNoDropout, stream, &sc, softcap > 0.f);
+}
+
+fa_status fa_bwd_scored(const void* q, const void* k, const void* v, const void* o,
+                        const void* dout, const float* lse, void* dq, void* dk, void* dv, int B,
+                        int Hq, int Hkv, int Sq, int Sk, int d, int causal, float scale,
+                        float softcap, const float* slopes, const void* plan, size_t plan_bytes,
+                        void* workspace, size_t workspace_bytes, cudaStream_t stream) {
+  FA_TRY(check_sizes(B, Hq, Hkv, Sq, Sk, d));
+  fa::ScoreArgs sc{};
+  FA_TRY(make_score(scale, softcap, slopes, plan, plan_bytes, B, Sq, Sk, &sc));
+  SeqLayout lay{};
+  lay.grid_b = B;
+  lay.longest_q = Sq;
+  lay.longest_k = Sk;
+  return bwd_launch(q, k, v, o, dout, lse, dq, dk, dv, B, Hq, Hkv, Sq, Sk, d, causal, scale, lay,
+                    nullptr, kNoDropout, workspace, workspace_bytes, stream, &sc, softcap > 0.f);
+}
+
+size_t fa_decode_scored_workspace_size(int B, int Hq, int Hkv, int Sk_max, int d, int window) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || Sk_max < 1 || d < 1 || window < 0) return 0;
+  int chunk = 0, n_split = 0;
+  fa::decode_scored_plan(B, Hq, Hkv, Sk_max, window, &chunk, &n_split);
+  const size_t rows = static_cast<size_t>(B) * Hq * n_split;
+  return align256(rows * d * sizeof(float)) + align256(rows * sizeof(float));
+}
+
+fa_status fa_decode_scored(const void* q, const void* k_cache, const void* v_cache, void* o,
+                           float* lse, const int32_t* seqlens_k, const int32_t* k_start, int B,
+                           int Hq, int Hkv, int Sk_max, int d, float scale, float softcap,
+                           const float* slopes, int window, void* workspace,
+                           size_t workspace_bytes, cudaStream_t stream) {
+  FA_TRY(check_sizes(B, Hq, Hkv, 1, Sk_max, d));
+  FA_TRY(check_ptr(q, "q"));
+  FA_TRY(check_ptr(k_cache, "k_cache"));
+  FA_TRY(check_ptr(v_cache, "v_cache"));
+  FA_TRY(check_ptr(o, "o"));
+  FA_TRY(check_i32(lse, "lse"));
+  if (!seqlens_k) return fail(FA_ERR_INVALID_ARG, "seqlens_k is NULL");
+  FA_TRY(check_i32(seqlens_k, "seqlens_k"));
+  FA_TRY(check_i32(k_start, "k_start"));
+  if (window < 0) return fail(FA_ERR_INVALID_ARG, "window (%d) must be >= 0 (0: none)", window);
+  fa::ScoredDecodeParams p{};
+  FA_TRY(make_score(scale, softcap, slopes, nullptr, 0, B, 1, Sk_max, &p.sc));
+  const size_t need = fa_decode_scored_workspace_size(B, Hq, Hkv, Sk_max, d, window);
+  if (!workspace || workspace_bytes < need)
+    return fail(FA_ERR_WORKSPACE, "decode workspace needs %zu bytes, got %zu", need,
+                workspace ? workspace_bytes : size_t(0));
+  FA_TRY(check_ptr(workspace, "workspace"));
+  p.q = q;
+  p.k = k_cache;
+  p.v = v_cache;
+  p.o = o;
+  p.lse = lse;
+  p.seqlens = seqlens_k;
+  p.k_start = k_start;
+  p.window = window;
+  p.capped = softcap > 0.f;
+  p.B = B;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.Sk_max = Sk_max;
+  p.group = Hq / Hkv;
+  fa::decode_scored_plan(B, Hq, Hkv, Sk_max, window, &p.chunk, &p.n_split);
+  const size_t rows = static_cast<size_t>(B) * Hq * p.n_split;
+  p.part_o = static_cast<float*>(workspace);
+  p.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                        align256(rows * d * sizeof(float)));
+  p.scale_log2 = scale_log2_of(scale);
+  // grid: splits x KV heads (times the head groups of 8) x batch rows
+  if (B > 65535 || 1LL * Hkv * ((p.group + 7) / 8) > 65535)
+    return fail(FA_ERR_INVALID_ARG, "decode grid too large (B=%d, Hkv=%d)", B, Hkv);
+  FA_TRY(check_device());
+  const cudaError_t e = fa::launch_decode_scored(d, p, stream);
+  if (e != cudaSuccess)
+    return fail(FA_ERR_CUDA, "fa_decode_scored launch: %s", cudaGetErrorString(e));
+  return ok();
 }
 
 size_t fa_decode_workspace_size(int B, int Hq, int Sk_max, int d) {
@@ -648,7 +786,10 @@ fa_status fa_device_status(unsigned int* code_out, int clear) {
   if (e != cudaSuccess) return fail(FA_ERR_CUDA, "cudaDeviceSynchronize: %s", cudaGetErrorString(e));
   const unsigned int w = fa::read_fwd_status(clear != 0) | fa::read_decode_status(clear != 0) |
                          fa::read_bwd_status(clear != 0) | fa::read_fwd_fp8_status(clear != 0) |
-                         fa::read_selftest_status(clear != 0);
+                         fa::read_selftest_status(clear != 0) |
+                         fa::read_fwd_scored_status(clear != 0) |
+                         fa::read_bwd_scored_status(clear != 0) |
+                         fa::read_decode_scored_status(clear != 0);
   if (code_out) *code_out = w;
   if (w != 0) return fail(FA_ERR_TIMEOUT, "device status word 0x%08x", w);
   return ok();

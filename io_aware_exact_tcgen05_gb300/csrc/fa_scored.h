@@ -1,0 +1,97 @@
+// fa_scored.h -- host-side parameter blocks of the operators around the scores: row intervals
+// and their tile plan (fa_mask_plan.cu), attention with capped and biased scores
+// (fa_fwd_scored.cu, fa_bwd_scored.cu, fa_decode_scored.cu).
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime_api.h>
+
+#include "fa_internal.h"
+
+namespace fa {
+
+// What fa_mask_plan writes, as the attention kernels read it (all in the caller's buffer).
+// rows == nullptr: no plan, every key is visible.
+struct MaskPlan {
+  const int4* qt;    // [B][nq]  per 128-row tile, over its rows with keys: min lo, max hi, max lo, min hi
+                     //          (0, 0, 0, 0 where no row has keys)
+  const int2* rows;  // [B][Sq]  lo, hi of each row; (0, 0) without keys
+  const int2* kt;    // [B][nk]  first and end query tile that may see the 128-key tile
+  const int* by_q1;  // [B][nq]  query tiles, most key tiles first
+  const int* by_q2;  // [B][np]  pairs of query tiles, likewise
+  const int* by_k;   // [B][nk]  key tiles, most query tiles first
+  int nq, np, nk;
+};
+
+// 32-bit words of a plan: qt, rows, kt, by_q1, by_q2, by_k.
+inline size_t mask_plan_words(long long B, long long Sq, long long Sk) {
+  const long long nq = (Sq + 127) / 128, np = (nq + 1) / 2, nk = (Sk + 127) / 128;
+  return static_cast<size_t>(B * (4 * nq + 2 * Sq + 2 * nk + nq + np + nk));
+}
+
+inline MaskPlan mask_plan_view(const void* base, long long B, long long Sq, long long Sk) {
+  MaskPlan m{};
+  if (!base) return m;
+  m.nq = static_cast<int>((Sq + 127) / 128);
+  m.np = (m.nq + 1) / 2;
+  m.nk = static_cast<int>((Sk + 127) / 128);
+  const int* w = static_cast<const int*>(base);
+  m.qt = reinterpret_cast<const int4*>(w);
+  m.rows = reinterpret_cast<const int2*>(w + 4 * B * m.nq);
+  m.kt = reinterpret_cast<const int2*>(w + 4 * B * m.nq + 2 * B * Sq);
+  m.by_q1 = w + 4 * B * m.nq + 2 * B * Sq + 2 * B * m.nk;
+  m.by_q2 = m.by_q1 + B * m.nq;
+  m.by_k = m.by_q2 + B * m.np;
+  return m;
+}
+
+struct RowBoundsParams {
+  const int32_t* cu_docs;  // [n_docs + 1] or nullptr
+  const int32_t* prefix;   // [n_docs], or [B] without documents, or nullptr
+  int32_t* lo;             // [B][Sq]
+  int32_t* hi;
+  int n_docs, B, Sq, Sk, causal, window;
+};
+
+cudaError_t launch_row_bounds(const RowBoundsParams& p, cudaStream_t stream);
+cudaError_t launch_mask_plan(const int32_t* lo, const int32_t* hi, int B, int Sq, int Sk,
+                             const MaskPlan& plan, cudaStream_t stream);
+
+// Scores z = t - slope * |p - j| in units of log2(e), t = cap * tanh(s * scale / cap) (see
+// fa_score.cuh for the arithmetic).
+struct ScoreArgs {
+  float a;             // scale / cap
+  float two_a_log2e;   // 2 * a * log2(e)
+  float cap_log2e;     // cap * log2(e)
+  float inv_cap_log2e; // 1 / cap_log2e
+  float small;         // |s| up to which the polynomial holds
+  float poly[5];       // z = s * (poly[0] + poly[1] s^2 + ...)
+  const float* slopes; // fp32 [Hq] or nullptr
+  MaskPlan plan;
+};
+
+struct ScoredDecodeParams : DecodeParams {
+  const int32_t* k_start;  // int32 [B] or nullptr
+  int window;              // last keys seen; 0: all
+  bool capped;
+  ScoreArgs sc;
+};
+
+void decode_scored_plan(int B, int Hq, int Hkv, int Sk_max, int window, int* chunk,
+                        int* n_split);
+cudaError_t launch_decode_scored(int d, const ScoredDecodeParams& p, cudaStream_t stream);
+unsigned int read_decode_scored_status(bool clear);
+
+cudaError_t launch_fwd_scored(int d, const CUtensorMap& tq, const CUtensorMap& tk,
+                              const CUtensorMap& tv, const FwdParams& base, const ScoreArgs& sc,
+                              bool cap, cudaStream_t stream);
+cudaError_t launch_bwd_scored(int d, const CUtensorMap& tq, const CUtensorMap& tk,
+                              const CUtensorMap& tv, const CUtensorMap& tdo,
+                              const CUtensorMap& tdq, const BwdParams& base, const ScoreArgs& sc,
+                              bool cap, cudaStream_t stream);
+unsigned int read_fwd_scored_status(bool clear);
+unsigned int read_bwd_scored_status(bool clear);
+
+}  // namespace fa
