@@ -403,16 +403,23 @@ fa_status make_score(float scale, float softcap, const float* slopes, const void
     sc.a = static_cast<float>(a);
     sc.two_a_log2e = static_cast<float>(2 * a * log2e);
     sc.cap_log2e = static_cast<float>(softcap * log2e);
-    sc.inv_cap_log2e = static_cast<float>(1 / (softcap * log2e));
-    // tanh(x) / x = 1 + c1 x^2 + .. + c4 x^8 for |x| <= 5/8, fitted in the maximum norm
-    const double fit[5] = {0.9999998807907104, -0.3333200514316559, 0.13305158913135529,
-                           -0.051847752183675766, 0.015084016136825085};
-    double f = a * softcap * log2e;
-    for (int i = 0; i < 5; ++i, f *= a * a) sc.poly[i] = static_cast<float>(fit[i] * f);
-    // the folded coefficients stay normal numbers in this range (about scale * a^8 the smallest)
+    sc.neg_inv_cap2 = static_cast<float>(-1 / (softcap * log2e * softcap * log2e));
+    // tanh(x) / x as polynomials in x^2 for |x| <= 1/4 and 5/8, fitted in the maximum norm
+    const double fit2[3] = {0.9999995827674866, -0.33321958780288696, 0.12842437624931335};
+    const double fit4[5] = {0.9999998807907104, -0.3333200514316559, 0.13305158913135529,
+                            -0.051847752183675766, 0.015084016136825085};
     const double c = a * softcap * log2e;
+    double f = c;
+    for (int i = 0; i < 5; ++i, f *= a * a) {
+      const float c2 = i < 3 ? static_cast<float>(fit2[i] * f) : 0.f;
+      const float c4 = static_cast<float>(fit4[i] * f);
+      if (i < 3) sc.poly2[i] = make_float2(c2, c2);
+      sc.poly4[i] = make_float2(c4, c4);
+    }
+    // the folded coefficients stay normal numbers in this range (about scale * a^8 the smallest)
     const bool fits = a >= 0x1p-13 && a <= 0x1p11 && c >= 0x1p-12 && c <= 0x1p12;
-    sc.small = fits ? static_cast<float>(0.625 / a) : -1.f;
+    sc.small[0] = fits ? static_cast<float>(0.25 / a) : -1.f;
+    sc.small[1] = fits ? static_cast<float>(0.625 / a) : -1.f;
   }
   *out = sc;
   return FA_OK;

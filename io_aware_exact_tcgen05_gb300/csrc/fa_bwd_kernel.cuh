@@ -268,25 +268,25 @@ __global__ void __launch_bounds__(256) fa_bwd_convert(const BwdParams p, long lo
   reinterpret_cast<uint2*>(p.dq)[i] = out;
 }
 
+// The scored modes hold weights times 2^15 (the factor leaves with the LSE's staging, D's staging and
+// dV's epilogue, at no cost): what dS is formed of is then kept in f16, which has 11 bits for every
+// weight above 2^-29 where bf16 has 8.  dS itself is rounded to bf16 for its two products.
+constexpr float kWeightLog2 = 15.f;
+constexpr float kWeightInv = 1.f / 32768.f;
+
 // Weights of one key (a thread) for 32 queries, from raw scores: p = 2^(z + nl) with z in units of
-// log2(e), hidden queries 0; pw gets p in bf16 pairs, pg gets what dS needs: p, times the cap's
-// derivative 1 - tanh^2 when there is one (rounded to bf16 as p itself is; dS is rounded to
-// bf16 behind it in any case).  nl2 holds -LSE of the queries, with the bias of the tile's first key
-// where distances are linear; kb is then the key's own share, else d0 = the first query's
-// position less the key.
-template <bool CAP, bool BIAS>
+// log2(e), hidden queries 0; pw gets p in bf16 pairs, pg in f16 pairs what dS needs: p, times the cap's
+// derivative 1 - tanh^2 when there is one.  nl2 holds -LSE of the queries, with the bias of the tile's
+// first key where distances are linear; kb is then the key's own share.
+//  * WAY 0, 1: every query sees the key, distances are linear and the scores are within the
+//    polynomial's range (of degree 2, 4);
+//  * WAY 2: any tile; d0 = the first query's position less the key.
+template <bool CAP, bool BIAS, int WAY>
 __device__ __forceinline__ void scored_weights(const uint32_t (&sr)[32], const ScoreArgs& sc,
                                                uint64_t c2, const uint64_t* nl2, bool linear,
                                                float slope2, float kb, int d0, bool masked,
                                                const uint16_t* qvis, int row, uint32_t (&pw)[16],
                                                uint32_t* pg) {
-  bool small = true;
-  if (CAP) {
-    float mx = fabsf(__uint_as_float(sr[0]));
-#pragma unroll
-    for (int e = 1; e < 32; ++e) mx = fmaxf(mx, fabsf(__uint_as_float(sr[e])));
-    small = __all_sync(0xffffffffu, mx <= sc.small);
-  }
   const uint64_t kb2 = f2_pack(kb, kb);
   const float df = static_cast<float>(d0);
 #pragma unroll
@@ -294,7 +294,7 @@ __device__ __forceinline__ void scored_weights(const uint32_t (&sr)[32], const S
     const uint64_t s2 = f2_pack(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1]));
     uint64_t add2 = nl2[e];
     if (BIAS) {
-      if (linear) {
+      if (WAY < 2 || linear) {
         add2 = f2_add(add2, kb2);
       } else {
         float a0, a1;
@@ -303,31 +303,36 @@ __device__ __forceinline__ void scored_weights(const uint32_t (&sr)[32], const S
                        fmaf(-slope2, fabsf(df + static_cast<float>(2 * e + 1)), a1));
       }
     }
-    float x0, x1, g0 = 1.f, g1 = 1.f;
+    float x0, x1;
+    uint64_t g2 = 0;
     if (CAP) {
       uint64_t z2;
-      if (small)
-        z2 = f2_mul(s2, cap_small_factor(s2, sc));
+      if (WAY == 2)
+        z2 = f2_pack(cap_one(__uint_as_float(sr[2 * e]), sc),
+                     cap_one(__uint_as_float(sr[2 * e + 1]), sc));
       else
-        z2 = f2_pack(cap_any(__uint_as_float(sr[2 * e]), sc),
-                     cap_any(__uint_as_float(sr[2 * e + 1]), sc));
-      const uint64_t t2 = f2_mul(z2, f2_pack(sc.inv_cap_log2e, sc.inv_cap_log2e));
-      const uint64_t nt2 = f2_mul(z2, f2_pack(-sc.inv_cap_log2e, -sc.inv_cap_log2e));
-      f2_unpack(f2_fma(nt2, t2, f2_pack(1.f, 1.f)), g0, g1);
+        z2 = f2_mul(s2, cap_small_factor<WAY == 0 ? 2 : 4>(s2, sc));
+      const uint64_t w2 = f2_mul(z2, f2_pack(sc.neg_inv_cap2, sc.neg_inv_cap2));
+      g2 = f2_fma(z2, w2, f2_pack(1.f, 1.f));
       f2_unpack(f2_add(z2, add2), x0, x1);
     } else {
       f2_unpack(f2_fma(s2, c2, add2), x0, x1);
     }
     float p0 = ex2_approx(x0);
     float p1 = ex2_approx(x1);
-    if (masked) {
+    if (WAY == 2 && masked) {
       const uint32_t v = *reinterpret_cast<const uint32_t*>(qvis + 2 * e);
-      const int r = row;
-      if (r < static_cast<int>(v & 0xff) || r >= static_cast<int>((v >> 8) & 0xff)) p0 = 0.f;
-      if (r < static_cast<int>((v >> 16) & 0xff) || r >= static_cast<int>(v >> 24)) p1 = 0.f;
+      if (row < static_cast<int>(v & 0xff) || row >= static_cast<int>((v >> 8) & 0xff)) p0 = 0.f;
+      if (row < static_cast<int>((v >> 16) & 0xff) || row >= static_cast<int>(v >> 24)) p1 = 0.f;
     }
     pw[e] = pack_bf16x2(p0, p1);
-    pg[e] = CAP ? pack_bf16x2(p0 * g0, p1 * g1) : pw[e];
+    if (CAP) {
+      float g0, g1;
+      f2_unpack(f2_mul(f2_pack(p0, p1), g2), g0, g1);
+      pg[e] = pack_f16x2(g0, g1);
+    } else {
+      pg[e] = pack_f16x2(p0, p1);
+    }
   }
 }
 
@@ -656,6 +661,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             nl = (lse == neg_inf()) ? neg_inf() : -lse * 1.4426950408889634f;
             nd = -p.delta[ri];
           }
+          if constexpr (SCORED) {
+            nl += kWeightLog2;
+            nd *= kWeightInv;
+          }
           if constexpr (BIAS) {
             // bias of the tile's first key, where distances are linear in the key
             if (linear) nl = fmaf(-sg, static_cast<float>(qi + off - c0), nl);
@@ -698,7 +707,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc) {
           uint32_t sr[32];
-          tmem_ld32(t_S + lane_off + hf * 64 + cc * 32, sr);
+          float largest = 0.f;  // |score|, for the cap's polynomial
+          if constexpr (CAP)
+            tmem_ld32_max_abs(t_S + lane_off + hf * 64 + cc * 32, sr, largest);
+          else
+            tmem_ld32(t_S + lane_off + hf * 64 + cc * 32, sr);
           if (DROP) {
             const uint32_t bh = static_cast<uint32_t>(bz * p.Hq + h);
             uint32_t kw = 0;
@@ -722,10 +735,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_wait_ld();
           uint32_t pw[16];
           if constexpr (SCORED) {
-            scored_weights<CAP, BIAS>(sr, p.sc, c2, nl2 + hf * 32 + cc * 16, linear, slope2,
-                                      sg * static_cast<float>(row),
-                                      q0 + hf * 64 + cc * 32 + off - key, need_mask,
-                                      s.qvis[sb] + hf * 64 + cc * 32, row, pw, pk + cc * 16);
+            const bool plain = !need_mask && linear;
+            const uint64_t* nlc = nl2 + hf * 32 + cc * 16;
+            const float kb = sg * static_cast<float>(row);
+            if (plain && (!CAP || __all_sync(0xffffffffu, largest <= p.sc.small[0])))
+              scored_weights<CAP, BIAS, 0>(sr, p.sc, c2, nlc, true, slope2, kb, 0, false, nullptr, row,
+                                           pw, pk + cc * 16);
+            else if (CAP && plain && __all_sync(0xffffffffu, largest <= p.sc.small[1]))
+              scored_weights<CAP, BIAS, 1>(sr, p.sc, c2, nlc, true, slope2, kb, 0, false, nullptr, row,
+                                           pw, pk + cc * 16);
+            else
+              scored_weights<CAP, BIAS, 2>(sr, p.sc, c2, nlc, linear, slope2, kb,
+                                           q0 + hf * 64 + cc * 32 + off - key, need_mask,
+                                           s.qvis[sb] + hf * 64 + cc * 32, row, pw, pk + cc * 16);
           } else {
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
@@ -769,7 +791,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int e = 0; e < 16; ++e) {
             const int qa = hf * 64 + cc * 32 + 2 * e;
             uint64_t dp2;
-            if (DROP) {  // dP of the dropped weights: keep / (1 - p) * <dO, v>
+            if constexpr (SCORED) {  // (dP - D) / 2^15
+              dp2 = f2_fma(f2_pack(__uint_as_float(dr[2 * e]), __uint_as_float(dr[2 * e + 1])),
+                           f2_pack(kWeightInv, kWeightInv), nd2[qa >> 1]);
+            } else if (DROP) {  // dP of the dropped weights: keep / (1 - p) * <dO, v>
               const uint32_t kb = keepw[cc] >> (2 * e);
               dp2 = f2_fma(f2_pack(__uint_as_float(dr[2 * e]), __uint_as_float(dr[2 * e + 1])),
                            f2_pack((kb & 1u) ? p.drop.scale : 0.f, (kb & 2u) ? p.drop.scale : 0.f),
@@ -779,7 +804,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                            nd2[qa >> 1]);
             }
             float d0, d1;
-            f2_unpack(f2_mul(bf16x2_to_f2(pk[cc * 16 + e]), dp2), d0, d1);
+            f2_unpack(f2_mul(SCORED ? f16x2_to_f2(pk[cc * 16 + e]) : bf16x2_to_f2(pk[cc * 16 + e]),
+                             dp2), d0, d1);
             dw[e] = pack_bf16x2(d0, d1);
           }
           // dS^T to shared memory only: 32 queries = four 16-byte chunks of query block hf
@@ -810,7 +836,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int pass = 0; pass < 2; ++pass) {
           const uint32_t src = (pass == 0) ? t_dK : t_dV;
-          const float mul = (pass == 0) ? p.scale : (DROP ? p.drop.scale : 1.f);
+          const float mul =
+              (pass == 0) ? p.scale : (DROP ? p.drop.scale : SCORED ? kWeightInv : 1.f);
           __nv_bfloat16* dst = (pass == 0) ? dkrow : dvrow;
 #pragma unroll
           for (int c2i = 0; c2i < D / 64; ++c2i) {

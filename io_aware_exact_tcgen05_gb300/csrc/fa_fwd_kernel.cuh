@@ -289,23 +289,34 @@ __device__ __forceinline__ Unit unit_at(const ScoredFwdParams& p, int U) {
 // Scores of 64 keys (columns [64 HALF, +64) of the tile) straight to weights, for a tile that
 // every row of the warp sees whole and whose distances have one sign: with a bias the exponent
 // is s * c + (slope of the sign) * jj + bm, bm = the bias of the tile's first key less the maximum.
-template <int HALF, bool CAP, bool BIAS>
+// DEGREE: of the cap's polynomial (0: no cap, kCapAny: tanh by special functions).  The bias of a pair is stepped from that of the
+// pair four before it, in 16 steps a half: off by some 2^-20 of itself.
+constexpr int kCapAny = -1;
+template <int HALF, int DEGREE, bool BIAS>
 __device__ __forceinline__ void scored_half(const uint32_t (&sr)[kTileN], const ScoreArgs& sc,
                                             uint64_t c2, float sg, float bm, uint32_t t_p,
                                             uint64_t (&sum2)[4], float (&sr_lo)[4],
                                             float (&sr_hi)[4]) {
   uint32_t pk[kTileN / 4];
-  const uint64_t bm2 = f2_pack(bm, bm);
+  uint64_t add2[4];
+  const uint64_t step2 = f2_pack(8.f * sg, 8.f * sg);
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    add2[q] = BIAS ? f2_pack(fmaf(sg, 64.f * HALF + 2 * q, bm), fmaf(sg, 64.f * HALF + 2 * q + 1, bm))
+                   : f2_pack(bm, bm);
 #pragma unroll
   for (int jq = 0; jq < kTileN / 4; ++jq) {
     const int jj = HALF * (kTileN / 4) + jq;
     const uint64_t s2 = f2_pack(__uint_as_float(sr[2 * jj]), __uint_as_float(sr[2 * jj + 1]));
-    const uint64_t add2 =
-        BIAS ? f2_pack(fmaf(sg, static_cast<float>(2 * jj), bm),
-                       fmaf(sg, static_cast<float>(2 * jj + 1), bm))
-             : bm2;
     float x0, x1;
-    f2_unpack(f2_fma(s2, CAP ? cap_small_factor(s2, sc) : c2, add2), x0, x1);
+    if constexpr (DEGREE == kCapAny) {
+      f2_unpack(f2_add(cap_any2(s2, sc), add2[jq & 3]), x0, x1);
+    } else {
+      uint64_t m2 = c2;
+      if constexpr (DEGREE > 0) m2 = cap_small_factor<DEGREE>(s2, sc);
+      f2_unpack(f2_fma(s2, m2, add2[jq & 3]), x0, x1);
+    }
+    if (BIAS) add2[jq & 3] = f2_add(add2[jq & 3], step2);
     const float p0 = ex2_approx(x0);
     const float p1 = ex2_approx(x1);
     pk[jq] = pack_bf16x2(p0, p1);
@@ -315,63 +326,48 @@ __device__ __forceinline__ void scored_half(const uint32_t (&sr)[kTileN], const 
   tmem_st32(t_p + HALF * 32, pk);
 }
 
-// Raw scores -> z in units of log2(e), hidden keys to -inf; p_rel = the row's position less the
-// tile's first key.
+// 32 raw scores of a row (keys from column j0 of the tile) -> z in units of log2(e), hidden keys to
+// -inf; p_rel, lo_rel, hi_rel: the row's position and its interval less the tile's first key.
 template <bool CAP, bool BIAS>
-__device__ __forceinline__ void scored_transform(uint32_t (&sr)[kTileN], const ScoreArgs& sc,
-                                                 float c, bool small, float slope2, int p_rel,
-                                                 bool masked, int lo_rel, int hi_rel) {
-  if (CAP) {
-    if (small) {
+__device__ __forceinline__ void scored_transform(uint32_t (&r)[32], const ScoreArgs& sc, float c,
+                                                 bool small, float slope2, int p_rel, int lo_rel,
+                                                 int hi_rel) {
+  if (CAP && !small) {
 #pragma unroll
-      for (int jj = 0; jj < kTileN; jj += 2) {
-        const uint64_t s2 = f2_pack(__uint_as_float(sr[jj]), __uint_as_float(sr[jj + 1]));
-        float x0, x1;
-        f2_unpack(f2_mul(s2, cap_small_factor(s2, sc)), x0, x1);
-        sr[jj] = __float_as_uint(x0);
-        sr[jj + 1] = __float_as_uint(x1);
-      }
-    } else {
-#pragma unroll
-      for (int jj = 0; jj < kTileN; ++jj)
-        sr[jj] = __float_as_uint(cap_any(__uint_as_float(sr[jj]), sc));
-    }
+    for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(cap_any(__uint_as_float(r[e]), sc));
   } else {
 #pragma unroll
-    for (int jj = 0; jj < kTileN; ++jj) sr[jj] = __float_as_uint(__uint_as_float(sr[jj]) * c);
+    for (int e = 0; e < 32; e += 2) {
+      const uint64_t s2 = f2_pack(__uint_as_float(r[e]), __uint_as_float(r[e + 1]));
+      uint64_t m2 = f2_pack(c, c);
+      if constexpr (CAP) m2 = cap_small_factor<4>(s2, sc);
+      float x0, x1;
+      f2_unpack(f2_mul(s2, m2), x0, x1);
+      r[e] = __float_as_uint(x0);
+      r[e + 1] = __float_as_uint(x1);
+    }
   }
   if (BIAS) {
     const float pf = static_cast<float>(p_rel);
 #pragma unroll
-    for (int jj = 0; jj < kTileN; ++jj)
-      sr[jj] = __float_as_uint(
-          fmaf(-slope2, fabsf(pf - static_cast<float>(jj)), __uint_as_float(sr[jj])));
+    for (int e = 0; e < 32; ++e)
+      r[e] = __float_as_uint(
+          fmaf(-slope2, fabsf(pf - static_cast<float>(e)), __uint_as_float(r[e])));
   }
-  if (masked) {
 #pragma unroll
-    for (int jj = 0; jj < kTileN; ++jj)
-      if (jj < lo_rel || jj >= hi_rel) sr[jj] = 0xff800000u;
-  }
+  for (int e = 0; e < 32; ++e)
+    if (e < lo_rel || e >= hi_rel) r[e] = 0xff800000u;
 }
 
-// Largest |score| of the thread's row and tile (a NaN counts as nothing: its row is NaN anyway).
-__device__ __forceinline__ float largest_abs(const uint32_t (&sr)[kTileN]) {
-  float mx[8];
-#pragma unroll
-  for (int q = 0; q < 8; ++q)
-    mx[q] = fmaxf(fabsf(__uint_as_float(sr[q])), fabsf(__uint_as_float(sr[q + 8])));
-#pragma unroll
-  for (int jj = 16; jj < kTileN; jj += 8)
-#pragma unroll
-    for (int q = 0; q < 8; ++q) mx[q] = fmaxf(mx[q], fabsf(__uint_as_float(sr[jj + q])));
-  return max3f(max3f(mx[0], mx[1], mx[2]), max3f(mx[3], mx[4], mx[5]), fmaxf(mx[6], mx[7]));
-}
-
-// The softmax warps of the scored modes.  As the plain ones, with the running maximum in units of
+// The softmax warps of the scored modes.  Key tiles come last first: under the causal rule the
+// tile that needs the mask is then the one that sets the maximum, and a bias that falls with the
+// distance lets the maximum stand from there on (first tiles first, steep slopes raised it in every
+// tile: 925 us instead of 541 at 2 x 16 heads x 8192 causal, d = 128).  As the plain ones, with the running maximum in units of
 // log2(e) and two ways through a tile:
-//  * fast: every row of the warp sees the whole tile, has a maximum, its distances have one sign,
-//    its scores are within the polynomial's range and the tile's sum stays below kFastLimit;
-//  * general: scores -> z in place (with the mask), the tile's maximum, rescale, weights.
+//  * fast: every row of the warp sees the whole tile and has a maximum, its distances have one
+//    sign, and the tile's sum stays below kFastLimit: scores to weights in registers;
+//  * general: scores -> z in place in TMEM (with the mask), 32 columns at a time, the tile's
+//    maximum, rescale, weights.  Written so that it holds few registers beside the fast way's.
 template <int D, int MODE, typename Smem, typename UnitIndex>
 __device__ __forceinline__ void scored_softmax_warps(Smem& s, const ScoredFwdParams& p,
                                                      uint32_t tmem, int warp, int lane,
@@ -419,16 +415,9 @@ __device__ __forceinline__ void scored_softmax_warps(Smem& s, const ScoredFwdPar
     for (int j = 0; j < n_tiles; ++j) {
       if (!mbar_wait_warp(&s.s_full[t], (ts + j) & 1, abort_flag, kSiteSFull)) return;
       tc_fence_after();
-      uint32_t sr[kTileN];
-#pragma unroll
-      for (int cc = 0; cc < kTileN / 32; ++cc)
-        tmem_ld32(t_s + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[cc * 32]));
-      tmem_wait_ld();
-      const int c0 = (un.j0 + j) * kTileN;
+      const int c0 = (un.j0 + n_tiles - 1 - j) * kTileN;
       const int p_rel = pos - c0;
-      const bool masked = __any_sync(0xffffffffu, c0 < lo || c0 + kTileN > hi);
-      const bool small = !CAP || __all_sync(0xffffffffu, largest_abs(sr) <= sc.small);
-      bool general = masked || !small || __any_sync(0xffffffffu, m == neg_inf());
+      bool general = __any_sync(0xffffffffu, c0 < lo || c0 + kTileN > hi || m == neg_inf());
       float sg = 0.f, bm = -m;
       if (BIAS) {
         // keys at or before every row of the warp, at or after every row, or neither
@@ -438,11 +427,35 @@ __device__ __forceinline__ void scored_softmax_warps(Smem& s, const ScoredFwdPar
         sg = before ? slope2 : -slope2;
         bm = fmaf(-sg, static_cast<float>(p_rel), -m);
       }
-      uint64_t sum2[4] = {0ull, 0ull, 0ull, 0ull};
-      float sr_lo[4] = {0.f, 0.f, 0.f, 0.f}, sr_hi[4] = {0.f, 0.f, 0.f, 0.f};
       if (!general) {
-        scored_half<0, CAP, BIAS>(sr, sc, c2, sg, bm, t_p, sum2, sr_lo, sr_hi);
-        scored_half<1, CAP, BIAS>(sr, sc, c2, sg, bm, t_p, sum2, sr_lo, sr_hi);
+        uint32_t sr[kTileN];
+        float most = 0.f;  // |score|, for the cap's polynomials
+        if constexpr (CAP) {
+          float part[kTileN / 32];
+#pragma unroll
+          for (int cc = 0; cc < kTileN / 32; ++cc)
+            tmem_ld32_max_abs(t_s + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[cc * 32]),
+                              part[cc]);
+          tmem_wait_ld();
+          most = fmaxf(max3f(part[0], part[1], part[2]), part[3]);
+        } else {
+#pragma unroll
+          for (int cc = 0; cc < kTileN / 32; ++cc)
+            tmem_ld32(t_s + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[cc * 32]));
+          tmem_wait_ld();
+        }
+        uint64_t sum2[4] = {0ull, 0ull, 0ull, 0ull};
+        float sr_lo[4] = {0.f, 0.f, 0.f, 0.f}, sr_hi[4] = {0.f, 0.f, 0.f, 0.f};
+        if (!CAP || __all_sync(0xffffffffu, most <= sc.small[0])) {
+          scored_half<0, CAP ? 2 : 0, BIAS>(sr, sc, c2, sg, bm, t_p, sum2, sr_lo, sr_hi);
+          scored_half<1, CAP ? 2 : 0, BIAS>(sr, sc, c2, sg, bm, t_p, sum2, sr_lo, sr_hi);
+        } else if (__all_sync(0xffffffffu, most <= sc.small[1])) {
+          scored_half<0, CAP ? 4 : 0, BIAS>(sr, sc, c2, sg, bm, t_p, sum2, sr_lo, sr_hi);
+          scored_half<1, CAP ? 4 : 0, BIAS>(sr, sc, c2, sg, bm, t_p, sum2, sr_lo, sr_hi);
+        } else {
+          scored_half<0, CAP ? kCapAny : 0, BIAS>(sr, sc, c2, sg, bm, t_p, sum2, sr_lo, sr_hi);
+          scored_half<1, CAP ? kCapAny : 0, BIAS>(sr, sc, c2, sg, bm, t_p, sum2, sr_lo, sr_hi);
+        }
         const float tsum = sum_f2x4(sum2);
         general = __any_sync(0xffffffffu, !(tsum < kFastLimit));
         if (!general) {
@@ -450,30 +463,33 @@ __device__ __forceinline__ void scored_softmax_warps(Smem& s, const ScoredFwdPar
           lr += (sr_lo[0] + sr_lo[1]) + (sr_lo[2] + sr_lo[3]) +
                 ((sr_hi[0] + sr_hi[1]) + (sr_hi[2] + sr_hi[3]));
         } else {
-          // S columns [0, 64) are still in TMEM, those of [64, 128) in registers
-#pragma unroll
-          for (int cc = 0; cc < 2; ++cc)
-            tmem_ld32(t_s + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[cc * 32]));
-          tmem_wait_ld();
+          // scores of [0, 64) are still in TMEM; those of [64, 128) go back over the weights
+          tmem_wait_st();
+          tmem_st32(t_s + 64, *reinterpret_cast<uint32_t(*)[32]>(&sr[64]));
+          tmem_st32(t_s + 96, *reinterpret_cast<uint32_t(*)[32]>(&sr[96]));
           tmem_wait_st();
         }
       }
       bool grow = false;
       float alpha = 1.f;
       if (general) {
-        scored_transform<CAP, BIAS>(sr, sc, c, small, slope2, p_rel, masked, lo - c0,
-                                    hi - c0);
-        float mx8[8];
+        float mx = neg_inf();
+#pragma unroll 1
+        for (int cc = 0; cc < kTileN / 32; ++cc) {
+          uint32_t r[32];
+          float most = 0.f;
+          if constexpr (CAP) tmem_ld32_max_abs(t_s + cc * 32, r, most);
+          else tmem_ld32(t_s + cc * 32, r);
+          tmem_wait_ld();
+          scored_transform<CAP, BIAS>(r, sc, c,
+                                      !CAP || __all_sync(0xffffffffu, most <= sc.small[1]), slope2,
+                                      p_rel - cc * 32, lo - c0 - cc * 32, hi - c0 - cc * 32);
 #pragma unroll
-        for (int q2 = 0; q2 < 8; ++q2)
-          mx8[q2] = fmaxf(__uint_as_float(sr[q2]), __uint_as_float(sr[q2 + 8]));
-#pragma unroll
-        for (int jj = 16; jj < kTileN; jj += 16)
-#pragma unroll
-          for (int q2 = 0; q2 < 8; ++q2)
-            mx8[q2] = max3f(mx8[q2], __uint_as_float(sr[jj + q2]), __uint_as_float(sr[jj + 8 + q2]));
-        const float mx = max3f(max3f(mx8[0], mx8[1], mx8[2]), max3f(mx8[3], mx8[4], mx8[5]),
-                               fmaxf(mx8[6], mx8[7]));
+          for (int e = 0; e < 32; e += 2)
+            mx = max3f(mx, __uint_as_float(r[e]), __uint_as_float(r[e + 1]));
+          tmem_st32(t_s + cc * 32, r);
+        }
+        tmem_wait_st();
         const float m_new = fmaxf(m, mx);
         // as in the plain path: the first visible key always sets the max, and -inf - (-inf) is
         // never formed
@@ -485,20 +501,27 @@ __device__ __forceinline__ void scored_softmax_warps(Smem& s, const ScoredFwdPar
           lr *= alpha;
           m = m_new;
         }
-        const float mc = (m == neg_inf()) ? 0.f : m;
-        const uint64_t one2 = f2_pack(1.f, 1.f), nmc2 = f2_pack(-mc, -mc);
+        const float nmc = (m == neg_inf()) ? 0.f : -m;
+        // weights of columns [32 cc, +32) go to columns [64 + 16 cc, +16): last columns first, so
+        // that no score is overwritten before it is read
+#pragma unroll 1
+        for (int cc = kTileN / 32 - 1; cc >= 0; --cc) {
+          uint32_t r[32], pk[16];
+          tmem_ld32(t_s + cc * 32, r);
+          tmem_wait_ld();
+          float s_lo = 0.f, s_hi = 0.f, part = 0.f;
 #pragma unroll
-        for (int q2 = 0; q2 < 4; ++q2) {
-          sum2[q2] = 0ull;
-          sr_lo[q2] = 0.f;
-          sr_hi[q2] = 0.f;
+          for (int e = 0; e < 16; ++e) {
+            const float p0 = ex2_approx(__uint_as_float(r[2 * e]) + nmc);
+            const float p1 = ex2_approx(__uint_as_float(r[2 * e + 1]) + nmc);
+            pk[e] = pack_bf16x2(p0, p1);
+            part += p0 + p1;
+            add_bf16x2_f32(s_lo, s_hi, pk[e]);
+          }
+          l += part;
+          lr += s_lo + s_hi;
+          tmem_st16(t_p + cc * 16, pk);
         }
-        const uint32_t keep[4] = {~0u, ~0u, ~0u, ~0u};
-        softmax_half<0, false>(sr, one2, nmc2, t_p, sum2, sr_lo, sr_hi, keep);
-        softmax_half<1, false>(sr, one2, nmc2, t_p, sum2, sr_lo, sr_hi, keep);
-        l += sum_f2x4(sum2);
-        lr += (sr_lo[0] + sr_lo[1]) + (sr_lo[2] + sr_lo[3]) +
-              ((sr_hi[0] + sr_hi[1]) + (sr_hi[2] + sr_hi[3]));
       }
       if (j > 0 && __any_sync(0xffffffffu, grow)) {
         // O_t is quiescent here, as in the plain path
@@ -563,8 +586,13 @@ __device__ __forceinline__ void scored_softmax_warps(Smem& s, const ScoredFwdPar
   }
 }
 
+// Threads of a mode.  The scored modes fill the third warpgroup up, so that it can hand registers
+// to the softmax warps (setmaxnreg): 128 x 56 + 256 x 224 = the 384 x 168 of the launch.
+template <int MODE>
+constexpr int kThreadsOf = (MODE & kModeScored) != 0 ? 384 : kThreads;
+
 template <int D, int MODE>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
     fa_fwd_kernel(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                   const __grid_constant__ CUtensorMap tv, const FwdParamsOf<MODE> p) {
   using Smem = FwdSmem<D>;
@@ -618,6 +646,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = &s.abort_flag;
   if (warp == 8) {
     // ------------------------------------------------------ TMA producer --
+    if constexpr (SCORED) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     // K/V stages follow a tile counter g that runs across the CTA's units;
     // the next unit's Q is loaded once the previous unit's last S product
     // has read Q (q_free).
@@ -646,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; j < un.n_tiles; ++j, ++g) {
           const int st = g % NS;
           const int use = g / NS;
-          const int c0 = (un.j0 + j) * kTileN;
+          const int c0 = (SCORED ? un.j0 + un.n_tiles - 1 - j : un.j0 + j) * kTileN;
           // stage st last held tile g - NS: its K was freed in round g - NS,
           // its V in round g - NS + 1
           if (use > 0 && !mbar_wait(&s.kv_free[st], (use - 1) & 1, abort_flag, kSiteKFree)) {
@@ -681,6 +710,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp == 9) {
     // ------------------------------------------------------- MMA issuer --
+    if constexpr (SCORED) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     // The whole warp runs this loop (warp-uniform control flow and operands);
     // one elected lane issues each MMA and commit.  Per unit, round j issues
     // PV_t(j-1) and S_t(j) for each active slot.  A unit's first S products
@@ -765,7 +795,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_drain(&s.drain, 0, kSiteDrain);
     }
   } else if constexpr (SCORED) {
-    scored_softmax_warps<D, MODE>(s, p, tmem, warp, lane, n_units, unit_index);
+    if (warp < 8) {
+      asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+      scored_softmax_warps<D, MODE>(s, p, tmem, warp, lane, n_units, unit_index);
+    } else {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    }
   } else {
     // ---------------------------------------------------- softmax warps --
     const int t = warp >> 2;

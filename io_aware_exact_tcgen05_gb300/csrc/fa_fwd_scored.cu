@@ -21,7 +21,7 @@ cudaError_t launch_dm(const CUtensorMap& tq, const CUtensorMap& tk, const CUtens
   const long long units = static_cast<long long>(p.n_rbu) * p.units_per_rbu;
   const unsigned int grid = static_cast<unsigned int>(std::min<long long>(units, n_sm));
   hook_before(stream);
-  fa_fwd_kernel<D, MODE><<<grid, kThreads, smem, stream>>>(tq, tk, tv, p);
+  fa_fwd_kernel<D, MODE><<<grid, kThreadsOf<MODE>, smem, stream>>>(tq, tk, tv, p);
   hook_after(stream);
   return cudaGetLastError();
 }

@@ -65,9 +65,10 @@ struct ScoreArgs {
   float a;             // scale / cap
   float two_a_log2e;   // 2 * a * log2(e)
   float cap_log2e;     // cap * log2(e)
-  float inv_cap_log2e; // 1 / cap_log2e
-  float small;         // |s| up to which the polynomial holds
-  float poly[5];       // z = s * (poly[0] + poly[1] s^2 + ...)
+  float neg_inv_cap2;  // -1 / cap_log2e^2
+  float small[2];      // |s| up to which the polynomials hold (-1: never)
+  float2 poly2[3];     // z = s * (poly2[0] + poly2[1] s^2 + ...), each twice (for packed pairs)
+  float2 poly4[5];
   const float* slopes; // fp32 [Hq] or nullptr
   MaskPlan plan;
 };
