@@ -278,9 +278,9 @@ constexpr float kWeightInv = 1.f / 32768.f;
 // log2(e), hidden queries 0; pw gets p in bf16 pairs, pg in f16 pairs what dS needs: p, times the cap's
 // derivative 1 - tanh^2 when there is one.  nl2 holds -LSE of the queries, with the bias of the tile's
 // first key where distances are linear; kb is then the key's own share.
-//  * WAY 0, 1: every query sees the key, distances are linear and the scores are within the
-//    polynomial's range (of degree 2, 4);
-//  * WAY 2: any tile; d0 = the first query's position less the key.
+//  * WAY 0, 1, 2: every query sees the key, distances are linear and the scores are within a
+//    polynomial's range (of degree 2, 4, 7);
+//  * WAY 3: any tile; d0 = the first query's position less the key.
 template <bool CAP, bool BIAS, int WAY>
 __device__ __forceinline__ void scored_weights(const uint32_t (&sr)[32], const ScoreArgs& sc,
                                                uint64_t c2, const uint64_t* nl2, bool linear,
@@ -294,7 +294,7 @@ __device__ __forceinline__ void scored_weights(const uint32_t (&sr)[32], const S
     const uint64_t s2 = f2_pack(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1]));
     uint64_t add2 = nl2[e];
     if (BIAS) {
-      if (WAY < 2 || linear) {
+      if (WAY < 3 || linear) {
         add2 = f2_add(add2, kb2);
       } else {
         float a0, a1;
@@ -307,11 +307,16 @@ __device__ __forceinline__ void scored_weights(const uint32_t (&sr)[32], const S
     uint64_t g2 = 0;
     if (CAP) {
       uint64_t z2;
-      if (WAY == 2)
-        z2 = f2_pack(cap_one(__uint_as_float(sr[2 * e]), sc),
-                     cap_one(__uint_as_float(sr[2 * e + 1]), sc));
-      else
+      if (WAY == 3) {
+        z2 = f2_pack(cap_any(__uint_as_float(sr[2 * e]), sc),
+                     cap_any(__uint_as_float(sr[2 * e + 1]), sc));
+      } else if (WAY == 2) {
+        uint64_t y2;
+        const uint64_t m2 = cap_factor7(s2, sc, y2);
+        z2 = f2_mul(y2, m2);
+      } else {
         z2 = f2_mul(s2, cap_small_factor<WAY == 0 ? 2 : 4>(s2, sc));
+      }
       const uint64_t w2 = f2_mul(z2, f2_pack(sc.neg_inv_cap2, sc.neg_inv_cap2));
       g2 = f2_fma(z2, w2, f2_pack(1.f, 1.f));
       f2_unpack(f2_add(z2, add2), x0, x1);
@@ -320,7 +325,7 @@ __device__ __forceinline__ void scored_weights(const uint32_t (&sr)[32], const S
     }
     float p0 = ex2_approx(x0);
     float p1 = ex2_approx(x1);
-    if (WAY == 2 && masked) {
+    if (WAY == 3 && masked) {
       const uint32_t v = *reinterpret_cast<const uint32_t*>(qvis + 2 * e);
       if (row < static_cast<int>(v & 0xff) || row >= static_cast<int>((v >> 8) & 0xff)) p0 = 0.f;
       if (row < static_cast<int>((v >> 16) & 0xff) || row >= static_cast<int>(v >> 24)) p1 = 0.f;
@@ -744,8 +749,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             else if (CAP && plain && __all_sync(0xffffffffu, largest <= p.sc.small[1]))
               scored_weights<CAP, BIAS, 1>(sr, p.sc, c2, nlc, true, slope2, kb, 0, false, nullptr, row,
                                            pw, pk + cc * 16);
+            else if (CAP && plain && __all_sync(0xffffffffu, largest <= p.sc.small[2]))
+              scored_weights<CAP, BIAS, 2>(sr, p.sc, c2, nlc, true, slope2, kb, 0, false, nullptr, row,
+                                           pw, pk + cc * 16);
             else
-              scored_weights<CAP, BIAS, 2>(sr, p.sc, c2, nlc, linear, slope2, kb,
+              scored_weights<CAP, BIAS, 3>(sr, p.sc, c2, nlc, linear, slope2, kb,
                                            q0 + hf * 64 + cc * 32 + off - key, need_mask,
                                            s.qvis[sb] + hf * 64 + cc * 32, row, pw, pk + cc * 16);
           } else {

@@ -95,6 +95,7 @@ __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); 
 // so P, l and O (at most 2^64 per tile per key block) stay far from fp32
 // overflow while the running max is left as it is.
 constexpr float kFastLimit = 18446744073709551616.0f;  // 2^64
+constexpr float kFastLog2 = 56.f;  // the same for 128 weights bounded one by one, with room to spare
 
 // Scores of keys outside [klo, khi) become -inf (weight 0).
 template <int FIRST, int COUNT>
@@ -289,14 +290,12 @@ __device__ __forceinline__ Unit unit_at(const ScoredFwdParams& p, int U) {
 // Scores of 64 keys (columns [64 HALF, +64) of the tile) straight to weights, for a tile that
 // every row of the warp sees whole and whose distances have one sign: with a bias the exponent
 // is s * c + (slope of the sign) * jj + bm, bm = the bias of the tile's first key less the maximum.
-// DEGREE: of the cap's polynomial (0: no cap, kCapAny: tanh by special functions).  The bias of a pair is stepped from that of the
-// pair four before it, in 16 steps a half: off by some 2^-20 of itself.
-constexpr int kCapAny = -1;
-template <int HALF, int DEGREE, bool BIAS>
-__device__ __forceinline__ void scored_half(const uint32_t (&sr)[kTileN], const ScoreArgs& sc,
-                                            uint64_t c2, float sg, float bm, uint32_t t_p,
-                                            uint64_t (&sum2)[4], float (&sr_lo)[4],
-                                            float (&sr_hi)[4]) {
+// The bias of a pair is stepped from that of the pair four before it, in 16 steps a half: off by
+// some 2^-20 of itself.
+template <int HALF, bool BIAS>
+__device__ __forceinline__ void scored_half(const uint32_t (&sr)[kTileN], uint64_t c2, float sg,
+                                            float bm, uint32_t t_p, uint64_t (&sum2)[4],
+                                            float (&sr_lo)[4], float (&sr_hi)[4]) {
   uint32_t pk[kTileN / 4];
   uint64_t add2[4];
   const uint64_t step2 = f2_pack(8.f * sg, 8.f * sg);
@@ -307,15 +306,10 @@ __device__ __forceinline__ void scored_half(const uint32_t (&sr)[kTileN], const 
 #pragma unroll
   for (int jq = 0; jq < kTileN / 4; ++jq) {
     const int jj = HALF * (kTileN / 4) + jq;
-    const uint64_t s2 = f2_pack(__uint_as_float(sr[2 * jj]), __uint_as_float(sr[2 * jj + 1]));
     float x0, x1;
-    if constexpr (DEGREE == kCapAny) {
-      f2_unpack(f2_add(cap_any2(s2, sc), add2[jq & 3]), x0, x1);
-    } else {
-      uint64_t m2 = c2;
-      if constexpr (DEGREE > 0) m2 = cap_small_factor<DEGREE>(s2, sc);
-      f2_unpack(f2_fma(s2, m2, add2[jq & 3]), x0, x1);
-    }
+    f2_unpack(f2_fma(f2_pack(__uint_as_float(sr[2 * jj]), __uint_as_float(sr[2 * jj + 1])), c2,
+                     add2[jq & 3]),
+              x0, x1);
     if (BIAS) add2[jq & 3] = f2_add(add2[jq & 3], step2);
     const float p0 = ex2_approx(x0);
     const float p1 = ex2_approx(x1);
@@ -324,6 +318,66 @@ __device__ __forceinline__ void scored_half(const uint32_t (&sr)[kTileN], const 
     add_bf16x2_f32(sr_lo[jq & 3], sr_hi[jq & 3], pk[jq]);
   }
   tmem_st32(t_p + HALF * 32, pk);
+}
+
+// The same for 32 capped scores (columns [32 cc, +32)); DEGREE: of the cap's polynomial, or kCapAny.
+constexpr int kCapAny = -1;
+template <int DEGREE, bool BIAS>
+__device__ __forceinline__ void capped_chunk(const uint32_t (&r)[32], const ScoreArgs& sc, float sg,
+                                             float bm, uint32_t t_p, uint64_t (&sum2)[2],
+                                             float (&sr_lo)[2], float (&sr_hi)[2]) {
+  uint32_t pk[16];
+  uint64_t add2[4];
+  const uint64_t step2 = f2_pack(8.f * sg, 8.f * sg);
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    add2[q] = BIAS ? f2_pack(fmaf(sg, 2.f * q, bm), fmaf(sg, 2.f * q + 1, bm)) : f2_pack(bm, bm);
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const uint64_t s2 = f2_pack(__uint_as_float(r[2 * e]), __uint_as_float(r[2 * e + 1]));
+    float x0, x1;
+    if constexpr (DEGREE == kCapAny)
+      f2_unpack(f2_add(cap_any2(s2, sc), add2[e & 3]), x0, x1);
+    else
+      f2_unpack(f2_fma(s2, cap_small_factor<DEGREE>(s2, sc), add2[e & 3]), x0, x1);
+    if (BIAS) add2[e & 3] = f2_add(add2[e & 3], step2);
+    const float p0 = ex2_approx(x0);
+    const float p1 = ex2_approx(x1);
+    pk[e] = pack_bf16x2(p0, p1);
+    sum2[e & 1] = f2_add(sum2[e & 1], f2_pack(p0, p1));
+    add_bf16x2_f32(sr_lo[e & 1], sr_hi[e & 1], pk[e]);
+  }
+  tmem_st16(t_p, pk);
+}
+
+// A whole tile of capped scores to weights, 32 columns at a time, last columns first (the weights
+// of columns [32 cc, +32) go over those of [64 + 16 cc, +16), which have been read by then).  The next
+// columns are loaded while these are worked on.  Adds to l and lr.  A loop and not one stretch of
+// code: warps of one CTA may be in different degrees, and three unrolled ones do not fit the
+// instruction cache (2 x 16 heads x 8192 causal, d = 128, scores that need degrees 4 and kCapAny
+// in turn: 976 us unrolled, 640 as loops; degree 2 alone 518 us as a loop, 481 unrolled by 2).
+template <int DEGREE, bool BIAS>
+__device__ __forceinline__ void capped_tile(uint32_t t_s, uint32_t t_p, const ScoreArgs& sc, float sg,
+                                            float bm, float& l, float& lr) {
+  uint64_t sum2[2] = {0ull, 0ull};
+  float sr_lo[2] = {0.f, 0.f}, sr_hi[2] = {0.f, 0.f};
+  uint32_t ra[32], rb[32];
+  tmem_ld32(t_s + 96, ra);
+  tmem_wait_ld();
+#pragma unroll (DEGREE == 2 ? 2 : 1)
+  for (int cc = 3; cc >= 0; cc -= 2) {
+    tmem_ld32(t_s + cc * 32 - 32, rb);
+    capped_chunk<DEGREE, BIAS>(ra, sc, sg, fmaf(sg, 32.f * cc, bm), t_p + cc * 16, sum2, sr_lo, sr_hi);
+    tmem_wait_ld();
+    if (cc > 1) tmem_ld32(t_s + cc * 32 - 64, ra);
+    capped_chunk<DEGREE, BIAS>(rb, sc, sg, fmaf(sg, 32.f * cc - 32.f, bm), t_p + cc * 16 - 16, sum2,
+                               sr_lo, sr_hi);
+    tmem_wait_ld();
+  }
+  float a, b;
+  f2_unpack(f2_add(sum2[0], sum2[1]), a, b);
+  l += a + b;
+  lr += (sr_lo[0] + sr_lo[1]) + (sr_hi[0] + sr_hi[1]);
 }
 
 // 32 raw scores of a row (keys from column j0 of the tile) -> z in units of log2(e), hidden keys to
@@ -427,35 +481,39 @@ __device__ __forceinline__ void scored_softmax_warps(Smem& s, const ScoredFwdPar
         sg = before ? slope2 : -slope2;
         bm = fmaf(-sg, static_cast<float>(p_rel), -m);
       }
-      if (!general) {
-        uint32_t sr[kTileN];
-        float most = 0.f;  // |score|, for the cap's polynomials
-        if constexpr (CAP) {
-          float part[kTileN / 32];
+      if constexpr (CAP) {
+        if (!general) {
+          // the largest |score| says which polynomial holds, and bounds the weights beforehand
+          float most = 0.f;
+          {
+            uint32_t r[32];
+            float part[4];
 #pragma unroll
-          for (int cc = 0; cc < kTileN / 32; ++cc)
-            tmem_ld32_max_abs(t_s + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[cc * 32]),
-                              part[cc]);
-          tmem_wait_ld();
-          most = fmaxf(max3f(part[0], part[1], part[2]), part[3]);
-        } else {
-#pragma unroll
-          for (int cc = 0; cc < kTileN / 32; ++cc)
-            tmem_ld32(t_s + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[cc * 32]));
-          tmem_wait_ld();
+            for (int cc = 0; cc < 4; ++cc) tmem_ld32_max_abs(t_s + cc * 32, r, part[cc]);
+            tmem_wait_ld();
+            most = fmaxf(max3f(part[0], part[1], part[2]), part[3]);
+          }
+          const float top = fmaf(most, c, fmaxf(bm, fmaf(sg, kTileN - 1.f, bm)));
+          general = __any_sync(0xffffffffu, !(top < kFastLog2));
+          if (!general) {
+            if (__all_sync(0xffffffffu, most <= sc.small[0]))
+              capped_tile<2, BIAS>(t_s, t_p, sc, sg, bm, l, lr);
+            else if (__all_sync(0xffffffffu, most <= sc.small[1]))
+              capped_tile<4, BIAS>(t_s, t_p, sc, sg, bm, l, lr);
+            else
+              capped_tile<kCapAny, BIAS>(t_s, t_p, sc, sg, bm, l, lr);
+          }
         }
+      } else if (!general) {
+        uint32_t sr[kTileN];
+#pragma unroll
+        for (int cc = 0; cc < kTileN / 32; ++cc)
+          tmem_ld32(t_s + cc * 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[cc * 32]));
+        tmem_wait_ld();
         uint64_t sum2[4] = {0ull, 0ull, 0ull, 0ull};
         float sr_lo[4] = {0.f, 0.f, 0.f, 0.f}, sr_hi[4] = {0.f, 0.f, 0.f, 0.f};
-        if (!CAP || __all_sync(0xffffffffu, most <= sc.small[0])) {
-          scored_half<0, CAP ? 2 : 0, BIAS>(sr, sc, c2, sg, bm, t_p, sum2, sr_lo, sr_hi);
-          scored_half<1, CAP ? 2 : 0, BIAS>(sr, sc, c2, sg, bm, t_p, sum2, sr_lo, sr_hi);
-        } else if (__all_sync(0xffffffffu, most <= sc.small[1])) {
-          scored_half<0, CAP ? 4 : 0, BIAS>(sr, sc, c2, sg, bm, t_p, sum2, sr_lo, sr_hi);
-          scored_half<1, CAP ? 4 : 0, BIAS>(sr, sc, c2, sg, bm, t_p, sum2, sr_lo, sr_hi);
-        } else {
-          scored_half<0, CAP ? kCapAny : 0, BIAS>(sr, sc, c2, sg, bm, t_p, sum2, sr_lo, sr_hi);
-          scored_half<1, CAP ? kCapAny : 0, BIAS>(sr, sc, c2, sg, bm, t_p, sum2, sr_lo, sr_hi);
-        }
+        scored_half<0, BIAS>(sr, c2, sg, bm, t_p, sum2, sr_lo, sr_hi);
+        scored_half<1, BIAS>(sr, c2, sg, bm, t_p, sum2, sr_lo, sr_hi);
         const float tsum = sum_f2x4(sum2);
         general = __any_sync(0xffffffffu, !(tsum < kFastLimit));
         if (!general) {

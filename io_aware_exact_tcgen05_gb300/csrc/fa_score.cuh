@@ -6,10 +6,10 @@
 // (without a cap: s * scale * log2(e) in place of the first term).
 //
 // tanh is taken two ways:
-//  * |a * s| <= 1/4 or 5/8: a polynomial, tanh(x) = x * (1 + c1 x^2 + ..) up to x^4 or x^8 in the
-//    brackets, fitted in the maximum norm: off by at most 4e-7 or 1e-7 of the value.  Three or five
-//    packed multiply-adds for two scores and no special-function instruction.  The coefficients
-//    arrive with a and cap' folded in.
+//  * |a * s| <= 0.25, 0.7 or 1.4: a polynomial, tanh(x) = x * (1 + c1 x^2 + ..) of degree 2, 4 or 7 in
+//    x^2, fitted to the least relative error: off by at most 4.0e-7, 3.0e-7, 3.4e-7 of the value.  Four,
+//    six or ten packed multiply-adds for two scores and no special-function instruction; the
+//    coefficients arrive with cap' folded in, those of degrees 2 and 4 with a as well.
 //  * else 1 - 2 / (1 + 2^(2 a s log2 e)): two special-function instructions, off by about 2^-22 of
 //    the cap.
 // Both are far below the rounding of the weights to bf16 (2^-9 of a weight).
@@ -32,15 +32,20 @@ __device__ __forceinline__ float cap_any(float s, const ScoreArgs& sc) {
   return fmaf(-2.f * sc.cap_log2e, rcp_approx(1.f + e), sc.cap_log2e);
 }
 
+// The same for two scores of one row, which share a reciprocal (1 / x = y / (x y)); at 2^60 the
+// quotient is 0 beside 1.  (A NaN reaches both: not for scores of different rows.)
 __device__ __forceinline__ uint64_t cap_any2(uint64_t s2, const ScoreArgs& sc) {
-  float e0, e1;
-  f2_unpack(f2_mul(s2, f2_pack(sc.two_a_log2e, sc.two_a_log2e)), e0, e1);
-  f2_unpack(f2_add(f2_pack(ex2_approx(e0), ex2_approx(e1)), f2_pack(1.f, 1.f)), e0, e1);
-  return f2_fma(f2_pack(-2.f * sc.cap_log2e, -2.f * sc.cap_log2e),
-                f2_pack(rcp_approx(e0), rcp_approx(e1)), f2_pack(sc.cap_log2e, sc.cap_log2e));
+  float x0, x1;
+  f2_unpack(f2_mul(s2, f2_pack(sc.two_a_log2e, sc.two_a_log2e)), x0, x1);
+  const float e0 = ex2_approx(fminf(x0, 60.f)), e1 = ex2_approx(fminf(x1, 60.f));
+  f2_unpack(f2_add(f2_pack(e0, e1), f2_pack(1.f, 1.f)), x0, x1);
+  const float r = rcp_approx(x0 * x1);
+  const uint64_t r2 = f2_mul(f2_pack(r, r), f2_pack(x1, x0));
+  return f2_fma(f2_pack(-2.f * sc.cap_log2e, -2.f * sc.cap_log2e), r2,
+                f2_pack(sc.cap_log2e, sc.cap_log2e));
 }
 
-// The factor m with cap' * tanh(a s) = s * m, for two scores with |s| <= small[0] (degree 2) or
+// The factor m with cap' * tanh(a s) = s * m for two scores with |s| <= small[0] (degree 2) or
 // small[1] (degree 4).
 template <int DEGREE>
 __device__ __forceinline__ uint64_t cap_small_factor(uint64_t s2, const ScoreArgs& sc) {
@@ -49,6 +54,16 @@ __device__ __forceinline__ uint64_t cap_small_factor(uint64_t s2, const ScoreArg
   uint64_t m = f2_pack(c[DEGREE].x, c[DEGREE].y);
 #pragma unroll
   for (int i = DEGREE - 1; i >= 0; --i) m = f2_fma(u, m, f2_pack(c[i].x, c[i].y));
+  return m;
+}
+
+// m and y = a s with cap' * tanh(a s) = y * m for two scores with |s| <= small[2].
+__device__ __forceinline__ uint64_t cap_factor7(uint64_t s2, const ScoreArgs& sc, uint64_t& y2) {
+  y2 = f2_mul(s2, f2_pack(sc.a, sc.a));
+  const uint64_t u = f2_mul(y2, y2);
+  uint64_t m = f2_pack(sc.poly7[7].x, sc.poly7[7].y);
+#pragma unroll
+  for (int i = 6; i >= 0; --i) m = f2_fma(u, m, f2_pack(sc.poly7[i].x, sc.poly7[i].y));
   return m;
 }
 

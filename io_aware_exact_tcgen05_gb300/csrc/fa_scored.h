@@ -66,9 +66,10 @@ struct ScoreArgs {
   float two_a_log2e;   // 2 * a * log2(e)
   float cap_log2e;     // cap * log2(e)
   float neg_inv_cap2;  // -1 / cap_log2e^2
-  float small[2];      // |s| up to which the polynomials hold (-1: never)
+  float small[3];      // |s| up to which the polynomials hold (-1: never)
   float2 poly2[3];     // z = s * (poly2[0] + poly2[1] s^2 + ...), each twice (for packed pairs)
   float2 poly4[5];
+  float2 poly7[8];     // z = y * (poly7[0] + poly7[1] y^2 + ...), y = a s
   const float* slopes; // fp32 [Hq] or nullptr
   MaskPlan plan;
 };
