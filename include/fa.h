@@ -526,7 +526,8 @@ fa_status fa_row_bounds(const int32_t* cu_docs, const int32_t* prefix, int n_doc
 size_t fa_mask_plan_size(int B, int Sq, int Sk);
 
 /* The tile plan of row_lo, row_hi int32 [B,Sq] (clamped to [0, Sk]; hi <= lo: no keys) into plan
-   (16-byte aligned, fa_mask_plan_size bytes), which holds all that the attention needs of them. */
+   (16-byte aligned, fa_mask_plan_size bytes), which holds all that the attention needs of them.
+   Sq and Sk are at most 2^31 - 257. */
 fa_status fa_mask_plan(const int32_t* row_lo, const int32_t* row_hi, int B, int Sq, int Sk,
                        void* plan, size_t plan_bytes, cudaStream_t stream);
 
@@ -542,7 +543,10 @@ fa_status fa_mask_plan(const int32_t* row_lo, const int32_t* row_hi, int B, int 
  *   (plan NULL: all) and, when causal != 0, j <= p
  * softcap is 0 or in [2^-20, 2^20]; slopes device fp32[Hq], finite, any sign (constants: no gradient).
  * plan: fa_mask_plan of the same B, Sq, Sk; plan_bytes its size.  Rows without keys give O = 0,
- * LSE = -inf and no gradient.  tanh is off by at most 1e-7 of its value or 2^-22, whichever is larger.
+ * LSE = -inf and no gradient.  What q, dout and o hold in rows without keys, and k and v in front of the
+ * first and behind the last key that any row of the batch row sees, is never used.  (A NaN or infinity in
+ * a key or value between them may reach every row of a 256-row block one of whose rows sees the key.)
+ * tanh is off by at most 4e-7 of its value or 2^-22, whichever is larger.
  */
 fa_status fa_fwd_scored(const void* q, const void* k, const void* v, void* o, float* lse, int B,
                         int Hq, int Hkv, int Sq, int Sk, int d, int causal, float scale,

@@ -123,6 +123,13 @@ __device__ __forceinline__ void st_shared_v4(uint32_t addr, uint32_t a, uint32_t
                : "memory");
 }
 
+// Zeros over one 128-byte row of a 128-row box (all of its swizzled 16-byte chunks).
+__device__ __forceinline__ void clear_row(const void* box, int row) {
+  const uint32_t a = smem_u32(box) + static_cast<uint32_t>(row) * 128;
+#pragma unroll
+  for (int ch = 0; ch < 8; ++ch) st_shared_v4(a + ch * 16, 0u, 0u, 0u, 0u);
+}
+
 // One work unit: a 128-key tile of one KV head of one batch row (or packed
 // sequence), walked against every query tile of the group's heads that sees
 // it.  Numbered key tile major, so under the causal rule the heaviest (tile
@@ -217,9 +224,11 @@ __device__ __forceinline__ BwdUnit bwd_unit_at(const ScoredBwdParams& p, int U) 
   int qt_end = (p.Sq + kTileM - 1) / kTileM;
   if (m.rows) {
     kt = __ldg(m.by_k + static_cast<size_t>(u.b) * m.nk + kt);
-    const int2 q = __ldg(m.kt + static_cast<size_t>(u.b) * m.nk + kt);
+    const int4 q = __ldg(m.kt + static_cast<size_t>(u.b) * m.nk + kt);
     u.qt_lo = q.x;
     qt_end = q.y;
+    u.klo = q.z;
+    u.kend = min(q.w, p.Sk);
   }
   u.c0 = kt * kTileN;
   u.exists = true;
@@ -303,8 +312,7 @@ __device__ __forceinline__ void scored_weights(const uint32_t (&sr)[32], const S
                        fmaf(-slope2, fabsf(df + static_cast<float>(2 * e + 1)), a1));
       }
     }
-    float x0, x1;
-    uint64_t g2 = 0;
+    float x0, x1, g0 = 1.f, g1 = 1.f;  // exponents; the cap's derivatives
     if (CAP) {
       uint64_t z2;
       if (WAY == 3) {
@@ -318,7 +326,7 @@ __device__ __forceinline__ void scored_weights(const uint32_t (&sr)[32], const S
         z2 = f2_mul(s2, cap_small_factor<WAY == 0 ? 2 : 4>(s2, sc));
       }
       const uint64_t w2 = f2_mul(z2, f2_pack(sc.neg_inv_cap2, sc.neg_inv_cap2));
-      g2 = f2_fma(z2, w2, f2_pack(1.f, 1.f));
+      f2_unpack(f2_fma(z2, w2, f2_pack(1.f, 1.f)), g0, g1);
       f2_unpack(f2_add(z2, add2), x0, x1);
     } else {
       f2_unpack(f2_fma(s2, c2, add2), x0, x1);
@@ -327,13 +335,12 @@ __device__ __forceinline__ void scored_weights(const uint32_t (&sr)[32], const S
     float p1 = ex2_approx(x1);
     if (WAY == 3 && masked) {
       const uint32_t v = *reinterpret_cast<const uint32_t*>(qvis + 2 * e);
-      if (row < static_cast<int>(v & 0xff) || row >= static_cast<int>((v >> 8) & 0xff)) p0 = 0.f;
-      if (row < static_cast<int>((v >> 16) & 0xff) || row >= static_cast<int>(v >> 24)) p1 = 0.f;
+      if (row < static_cast<int>(v & 0xff) || row >= static_cast<int>((v >> 8) & 0xff)) p0 = g0 = 0.f;
+      if (row < static_cast<int>((v >> 16) & 0xff) || row >= static_cast<int>(v >> 24)) p1 = g1 = 0.f;
     }
     pw[e] = pack_bf16x2(p0, p1);
     if (CAP) {
-      float g0, g1;
-      f2_unpack(f2_mul(f2_pack(p0, p1), g2), g0, g1);
+      f2_unpack(f2_mul(f2_pack(p0, p1), f2_pack(g0, g1)), g0, g1);
       pg[e] = pack_f16x2(g0, g1);
     } else {
       pg[e] = pack_f16x2(p0, p1);
@@ -655,6 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // after every compute warp has signalled dS of the tile that read it
         // (S^T of the next tile is issued only after that).
         const int sb = gi & 1;
+        bool dead = false;  // scored modes: the query of this hf = 0 thread has no keys
         if (hf == 0) {
           // stored negated so that p = 2^(s*c + nl) and dP - D = dP + nd are one
           // packed FMA / add per pair; rows without keys get nl = -inf (p = 0)
@@ -685,6 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               if (p.causal) hi = min(hi, qi + off + 1);
             }
+            dead = hi <= lo && qi < sq;  // (rows past the end arrive as zeros)
             lo = max(0, min(lo - c0, kTileN));
             hi = max(0, min(hi - c0, kTileN));
             s.qvis[sb][row] = static_cast<uint16_t>(lo | (hi << 8));
@@ -781,6 +790,29 @@ __global__ void __launch_bounds__(kThreads, 1)
           // P columns [64 hf + 16 cc, +16) hold scores this warp already loaded
           tmem_st16(t_S + lane_off + hf * 64 + cc * 16, pw);
         }
+        if constexpr (SCORED) {
+          // Rows and keys that nothing is computed for may hold anything, and a weight of 0 does
+          // not cancel a NaN: Q and dO of queries without keys, and K of keys outside of the
+          // hull of all intervals, become zeros before dV, dK and dQ read them.  (Products that read
+          // them meanwhile only write what is dropped: scores and dP of those rows and keys.)
+          bool cleared = false;
+          if (hf == 0 && __any_sync(0xffffffffu, dead)) {
+            if (!mbar_wait_warp(&s.do_full, gi & 1, abort_flag, kSiteDOFull)) { ok = false; break; }
+            if (dead) {
+              for (int cb = 0; cb < Smem::NB; ++cb) {
+                clear_row(s.q[gi % Smem::kQStages][cb], row);
+                clear_row(s.dout[cb], row);
+              }
+            }
+            cleared = true;
+          }
+          if (hf == 1 && it == 0 && (c0 < klo || c0 + kTileN > kend)) {
+            if (!key_in)
+              for (int cb = 0; cb < Smem::NB; ++cb) clear_row(s.k[cb], row);
+            cleared = true;
+          }
+          if (cleared) fence_proxy_async_smem();
+        }
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -814,6 +846,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             float d0, d1;
             f2_unpack(f2_mul(SCORED ? f16x2_to_f2(pk[cc * 16 + e]) : bf16x2_to_f2(pk[cc * 16 + e]),
                              dp2), d0, d1);
+            if (SCORED && need_mask) {  // hidden entries: 0 whatever dP and D hold
+              if (!(pk[cc * 16 + e] & 0xffffu)) d0 = 0.f;
+              if (!(pk[cc * 16 + e] >> 16)) d1 = 0.f;
+            }
             dw[e] = pack_bf16x2(d0, d1);
           }
           // dS^T to shared memory only: 32 queries = four 16-byte chunks of query block hf

@@ -581,6 +581,24 @@ __device__ __forceinline__ void scored_softmax_warps(Smem& s, const ScoredFwdPar
           tmem_st16(t_p + cc * 16, pk);
         }
       }
+      if (t == 0 && (c0 < un.klo || c0 + kTileN > un.kend)) {
+        // Keys that no row of the unit sees may hold anything, and a weight of 0 does not cancel
+        // a NaN: their values become zeros before either slot's product reads them (slot 1's is
+        // issued after slot 0's).  The tile stays until then: slot 0 has run through every tile
+        // of the CTA, so ts + j is its number.
+        const int g = ts + j;
+        if (!mbar_wait_warp(&s.v_full[g % Smem::NS], (g / Smem::NS) & 1, abort_flag, kSiteVFull)) return;
+        const int key = c0 + row_in_tile;
+        if (key < un.klo || key >= un.kend) {
+          for (int cb = 0; cb < Smem::NB; ++cb) {
+            const uint32_t a = smem_u32(s.v[g % Smem::NS][cb]) + static_cast<uint32_t>(row_in_tile) * 128;
+#pragma unroll
+            for (int ch = 0; ch < 8; ++ch)
+              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(a + ch * 16), "r"(0) : "memory");
+          }
+        }
+        fence_proxy_async_smem();
+      }
       if (j > 0 && __any_sync(0xffffffffu, grow)) {
         // O_t is quiescent here, as in the plain path
 #pragma unroll

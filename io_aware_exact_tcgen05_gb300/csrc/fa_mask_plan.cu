@@ -94,23 +94,25 @@ __global__ void __launch_bounds__(128)
   griddep_launch_dependents();
 }
 
-// First and end query tile whose hull of intervals meets each key tile.
+// First and end query tile whose hull of intervals meets each key tile, and the hull of theirs.
 __global__ void __launch_bounds__(128) fa_plan_keys_kernel(const MaskPlan m) {
   const int b = blockIdx.y;
   const int kt = blockIdx.x * 128 + threadIdx.x;
   griddep_wait();
   const int4* qt = m.qt + static_cast<size_t>(b) * m.nq;
   const int c0 = kt * 128;
-  int first = 0, end = 0;
+  int first = 0, end = 0, lo = 0x7fffffff, hi = 0;
   if (kt < m.nk) {
     for (int t = 0; t < m.nq; ++t) {
       const int4 r = qt[t];
       if (r.x < c0 + 128 && r.y > c0) {
         if (end == 0) first = t;
         end = t + 1;
+        lo = min(lo, r.x);
+        hi = max(hi, r.y);
       }
     }
-    const_cast<int2*>(m.kt)[static_cast<size_t>(b) * m.nk + kt] = make_int2(first, end);
+    const_cast<int4*>(m.kt)[static_cast<size_t>(b) * m.nk + kt] = make_int4(first, end, lo, hi);
   }
   griddep_launch_dependents();
 }
@@ -129,7 +131,7 @@ __global__ void __launch_bounds__(128) fa_plan_order_kernel(const MaskPlan m) {
   griddep_wait();
   if (t >= n) return;
   const int4* qt = m.qt + static_cast<size_t>(b) * m.nq;
-  const int2* kt = m.kt + static_cast<size_t>(b) * m.nk;
+  const int4* kt = m.kt + static_cast<size_t>(b) * m.nk;
   auto load = [&](int x) {
     if (kind == 2) return kt[x].y - kt[x].x;
     if (kind == 0) return key_tiles(qt[x].x, qt[x].y);

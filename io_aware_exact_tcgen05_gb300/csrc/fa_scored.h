@@ -18,17 +18,18 @@ struct MaskPlan {
   const int4* qt;    // [B][nq]  per 128-row tile, over its rows with keys: min lo, max hi, max lo, min hi
                      //          (0, 0, 0, 0 where no row has keys)
   const int2* rows;  // [B][Sq]  lo, hi of each row; (0, 0) without keys
-  const int2* kt;    // [B][nk]  first and end query tile that may see the 128-key tile
+  const int4* kt;    // [B][nk]  first and end query tile that may see the 128-key tile, and the hull
+                     //          of their rows' intervals
   const int* by_q1;  // [B][nq]  query tiles, most key tiles first
   const int* by_q2;  // [B][np]  pairs of query tiles, likewise
   const int* by_k;   // [B][nk]  key tiles, most query tiles first
   int nq, np, nk;
 };
 
-// 32-bit words of a plan: qt, rows, kt, by_q1, by_q2, by_k.
+// 32-bit words of a plan: qt, kt, rows, by_q1, by_q2, by_k.
 inline size_t mask_plan_words(long long B, long long Sq, long long Sk) {
   const long long nq = (Sq + 127) / 128, np = (nq + 1) / 2, nk = (Sk + 127) / 128;
-  return static_cast<size_t>(B * (4 * nq + 2 * Sq + 2 * nk + nq + np + nk));
+  return static_cast<size_t>(B * (4 * nq + 4 * nk + 2 * Sq + nq + np + nk));
 }
 
 inline MaskPlan mask_plan_view(const void* base, long long B, long long Sq, long long Sk) {
@@ -39,9 +40,9 @@ inline MaskPlan mask_plan_view(const void* base, long long B, long long Sq, long
   m.nk = static_cast<int>((Sk + 127) / 128);
   const int* w = static_cast<const int*>(base);
   m.qt = reinterpret_cast<const int4*>(w);
-  m.rows = reinterpret_cast<const int2*>(w + 4 * B * m.nq);
-  m.kt = reinterpret_cast<const int2*>(w + 4 * B * m.nq + 2 * B * Sq);
-  m.by_q1 = w + 4 * B * m.nq + 2 * B * Sq + 2 * B * m.nk;
+  m.kt = reinterpret_cast<const int4*>(w + 4 * B * m.nq);
+  m.rows = reinterpret_cast<const int2*>(w + 4 * B * (m.nq + m.nk));
+  m.by_q1 = w + 4 * B * (m.nq + m.nk) + 2 * B * Sq;
   m.by_q2 = m.by_q1 + B * m.nq;
   m.by_k = m.by_q2 + B * m.np;
   return m;

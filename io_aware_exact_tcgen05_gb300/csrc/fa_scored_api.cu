@@ -32,8 +32,7 @@ fa_status check_rows(const char* who, int B, int Sq, int Sk) {
   if (B < 1 || Sq < 1 || Sk < 1)
     return api_fail(FA_ERR_INVALID_ARG, "%s: sizes must be >= 1 (B=%d Sq=%d Sk=%d)", who, B, Sq, Sk);
   if (B > 65535) return api_fail(FA_ERR_INVALID_ARG, "%s: B (%d) > 65535", who, B);
-  if (1LL * B * Sq >= (1LL << 31) || 1LL * B * Sk >= (1LL << 31) || Sq > 0x7fffffff - 256 ||
-      Sk > 0x7fffffff - 256)
+  if (1LL * B * Sq >= (1LL << 31) || 1LL * B * Sk >= (1LL << 31))
     return api_fail(FA_ERR_INVALID_ARG, "%s: too large for 32-bit row indices", who);
   return FA_OK;
 }
@@ -166,6 +165,8 @@ fa_status fa_mask_plan(const int32_t* row_lo, const int32_t* row_hi, int B, int 
   FA_TRY(check_rows("fa_mask_plan", B, Sq, Sk));
   FA_TRY(check_align(row_lo, "row_lo", 4, false));
   FA_TRY(check_align(row_hi, "row_hi", 4, false));
+  if (Sq > 0x7fffffff - 256 || Sk > 0x7fffffff - 256)  // ends of tiles are 32-bit numbers
+    return api_fail(FA_ERR_INVALID_ARG, "fa_mask_plan: Sq and Sk are at most 2^31 - 257");
   const size_t need = fa_mask_plan_size(B, Sq, Sk);
   if (!plan || plan_bytes < need)
     return api_fail(FA_ERR_WORKSPACE, "the mask plan of these sizes has %zu bytes, got %zu", need,
