@@ -12,7 +12,7 @@
 // operations each.  D / 16 lanes share a head's vector, 16 channels a lane: two 16-byte pieces
 // that hold both members of the lane's pairs, so a rotation needs no exchange; the norm is one
 // reduction over the lanes.  A warp takes 32 * 16 / D heads at once and walks the heads of a token,
-// for which it takes the angles once.
+// whose angles its lanes work out together, once, in shared memory.
 //
 // Angles: a position times a frequency in turns, as 64-bit fixed point, of which whole turns
 // fall off by themselves: exact to 2^-31 turns for any 32-bit position, without 64-bit floating
@@ -21,6 +21,14 @@
 //
 // Sums over a head and the weights' gradients are held in fp32; a CTA adds its share of dw in a
 // fixed order and a second kernel adds the CTAs' likewise: same result every time.
+//
+// The work is one line of steps, of a few heads each: a token's queries, keys and values, then the next
+// token's; every warp takes an equal stretch of it.  Dealing queries, keys and values to different CTAs
+// left two fifths of the time to the slowest; whole tokens left a seventh to the last round.
+//
+// Measured (GB300, inputs from HBM): 2 x 8192 tokens of 16 + 2 x 16 heads, d = 128 forward 71 us (5.7 TB/s,
+// 85% of the measured copy); 3 x 2777 tokens of 28 + 2 x 4 heads with three axes backward 54 us (4.1 TB/s): the
+// chain of two reductions a step at 16 warps per SM, which is what the registers allow.
 #include <algorithm>
 
 #include <cuda_bf16.h>
@@ -33,10 +41,16 @@
 namespace fa {
 namespace {
 
+#ifndef FC
+#define FC 3
+#define BC 2
+#endif
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kPrepCtasPerSm = 3;
-constexpr int kMaxPartialRows = 512;
+// CTAs per SM that the registers allow: the grid is one wave of them.
+constexpr int kFwdCtasPerSm = 4;
+constexpr int kBwdCtasPerSm = 2;
+constexpr int kMaxPartialRows = 512;  // most CTAs of a backward pass
 
 // f / (2 pi) turns as a 64-bit fixed-point fraction (whole turns dropped); 1 / (2 pi) in 64 bits.
 __device__ __forceinline__ uint64_t turns64(float f) {
@@ -62,22 +76,26 @@ __device__ __forceinline__ void turn(uint64_t t, int pos, float& c, float& s) {
   __sincosf(x, &s, &c);
 }
 
+// 16 channels of a lane as fp32 pairs: two pieces of 8.
 struct Vec {
-  float a[8], b[8];
+  uint64_t a[4], b[4];
 };
 
-__device__ __forceinline__ void unpack8(const uint4 w, float (&v)[8]) {
-  const uint32_t x[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    v[2 * e] = __uint_as_float(x[e] << 16);
-    v[2 * e + 1] = __uint_as_float(x[e] & 0xffff0000u);
-  }
+__device__ __forceinline__ void unpack8(const uint4 w, uint64_t (&v)[4]) {
+  v[0] = bf16x2_to_f2(w.x);
+  v[1] = bf16x2_to_f2(w.y);
+  v[2] = bf16x2_to_f2(w.z);
+  v[3] = bf16x2_to_f2(w.w);
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
-  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                    pack_bf16x2(v[6], v[7]));
+__device__ __forceinline__ uint32_t pack2(uint64_t v) {
+  float lo, hi;
+  f2_unpack(v, lo, hi);
+  return pack_bf16x2(lo, hi);
+}
+
+__device__ __forceinline__ uint4 pack8(const uint64_t (&v)[4]) {
+  return make_uint4(pack2(v[0]), pack2(v[1]), pack2(v[2]), pack2(v[3]));
 }
 
 __device__ __forceinline__ uint4 load16(const __nv_bfloat16* p) {
@@ -88,208 +106,339 @@ __device__ __forceinline__ void store16(__nv_bfloat16* p, const uint4 v) {
   *reinterpret_cast<uint4*>(p) = v;
 }
 
-// The lane's pairs turned by (c, s) (back: by -s): channels 2 i and 2 i + 1 of a piece, or the same
-// channel of both pieces.
-__device__ __forceinline__ void turn_pair(float& a, float& b, float c, float s) {
-  const float na = fmaf(a, c, -b * s);
-  b = fmaf(b, c, a * s);
-  a = na;
+__device__ __forceinline__ uint64_t f2_both(float v) { return f2_pack(v, v); }
+
+// Cosines and sines of a token's frequencies (negative sines turn back), laid out so that the
+// lanes of a head read 16 neighbouring bytes each: pairs of pieces 8 frequencies a lane, as two groups
+// of four; interleaved as they come (place_of).
+template <int D>
+struct Angles {
+  float c[D / 2], s[D / 2];
+};
+
+template <int D>
+__device__ __forceinline__ int place_of(int i, bool interleaved) {
+  return interleaved ? i : ((i >> 2 & 1) * (D / 16) + (i >> 3)) * 4 + (i & 3);
 }
 
-__device__ __forceinline__ void rotate(Vec& v, const float (&c)[8], const float (&s)[8],
-                                       bool interleaved, bool back) {
+__device__ __forceinline__ void load_pairs(const float* p, uint64_t (&v)[2]) {
+  const ulonglong2 x = *reinterpret_cast<const ulonglong2*>(p);
+  v[0] = x.x;
+  v[1] = x.y;
+}
+
+__device__ __forceinline__ uint64_t f2_sub(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+// The lane's pairs turned: the same channel of both pieces (a + i b times c + i s), or neighbours
+// when interleaved.  fa, fb: where the lane's two groups of four are.
+template <int D>
+__device__ __forceinline__ void rotate(Vec& v, const Angles<D>& g, int fa, int fb, bool interleaved) {
   if (interleaved) {
+    const float4 ca = *reinterpret_cast<const float4*>(g.c + fa);
+    const float4 sa = *reinterpret_cast<const float4*>(g.s + fa);
+    const float4 cb = *reinterpret_cast<const float4*>(g.c + fb);
+    const float4 sb = *reinterpret_cast<const float4*>(g.s + fb);
+    const float c[8] = {ca.x, ca.y, ca.z, ca.w, cb.x, cb.y, cb.z, cb.w};
+    const float s[8] = {sa.x, sa.y, sa.z, sa.w, sb.x, sb.y, sb.z, sb.w};
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      turn_pair(v.a[2 * e], v.a[2 * e + 1], c[e], back ? -s[e] : s[e]);
-      turn_pair(v.b[2 * e], v.b[2 * e + 1], c[4 + e], back ? -s[4 + e] : s[4 + e]);
+    for (int e = 0; e < 8; ++e) {
+      uint64_t& x = e < 4 ? v.a[e & 3] : v.b[e & 3];
+      float lo, hi;
+      f2_unpack(x, lo, hi);
+      x = f2_fma(x, f2_both(c[e]), f2_mul(f2_pack(hi, lo), f2_pack(-s[e], s[e])));
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) turn_pair(v.a[e], v.b[e], c[e], back ? -s[e] : s[e]);
+    for (int e = 0; e < 4; e += 2) {
+      uint64_t c[2], s[2];
+      load_pairs(g.c + (e ? fb : fa), c);
+      load_pairs(g.s + (e ? fb : fa), s);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const uint64_t x = v.a[e + i], y = v.b[e + i];
+        v.a[e + i] = f2_sub(f2_mul(x, c[i]), f2_mul(y, s[i]));
+        v.b[e + i] = f2_fma(y, c[i], f2_mul(x, s[i]));
+      }
+    }
   }
 }
 
 template <int LPH>
-__device__ __forceinline__ float sum_head(float v) {
+__device__ __forceinline__ float sum_head(uint64_t v) {
+  float lo, hi;
+  f2_unpack(v, lo, hi);
+  float t = lo + hi;
 #pragma unroll
-  for (int o = LPH / 2; o >= 1; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+  for (int o = LPH / 2; o >= 1; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+  return t;
+}
+
+// What the lanes of a warp need of a token besides the data.
+template <int D>
+struct Lane {
+  const Angles<D>* angles;
+  const float* weight;  // the lane's channels, with the offset: four groups of four, D / 4 apart
+  int ca, cb, f_a, f_b;
+  bool turns;           // the lane's channels turn
+};
+
+// One head vector's share of a lane, forward: norm and rotation.
+template <int D>
+__device__ __forceinline__ void forward_vec(Vec& v, const PrepParams& p, const Lane<D>& t, bool norm,
+                                            bool turns) {
+  if (norm) {
+    uint64_t ss = f2_mul(v.a[0], v.a[0]);
+    ss = f2_fma(v.b[0], v.b[0], ss);
+#pragma unroll
+    for (int e = 1; e < 4; ++e) ss = f2_fma(v.a[e], v.a[e], f2_fma(v.b[e], v.b[e], ss));
+    const uint64_t rn2 = f2_both(rsqrtf(sum_head<D / 16>(ss) * (1.f / D) + p.eps));
+#pragma unroll
+    for (int e = 0; e < 4; e += 2) {
+      uint64_t wa[2], wb[2];
+      load_pairs(t.weight + e / 2 * (D / 4), wa);
+      load_pairs(t.weight + (2 + e / 2) * (D / 4), wb);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        v.a[e + i] = f2_mul(v.a[e + i], f2_mul(rn2, wa[i]));
+        v.b[e + i] = f2_mul(v.b[e + i], f2_mul(rn2, wb[i]));
+      }
+    }
+  }
+  if (turns) rotate<D>(v, *t.angles, t.f_a, t.f_b, p.interleaved);
+}
+
+// The same backward: g becomes the gradient of v, dw gathers the weight's.  A lane without a head
+// holds zeros (live false), of which eps = 0 would make NaN.
+template <int D>
+__device__ __forceinline__ void backward_vec(Vec& v, Vec& g, Vec& dw, const PrepParams& p,
+                                             const Lane<D>& t, bool norm, bool turns, bool live) {
+  if (turns) rotate<D>(g, *t.angles, t.f_a, t.f_b, p.interleaved);
+  if (!norm) return;
+  uint64_t ss = f2_mul(v.a[0], v.a[0]);
+  ss = f2_fma(v.b[0], v.b[0], ss);
+#pragma unroll
+  for (int e = 1; e < 4; ++e) ss = f2_fma(v.a[e], v.a[e], f2_fma(v.b[e], v.b[e], ss));
+  const float rn = rsqrtf(sum_head<D / 16>(ss) * (1.f / D) + p.eps);
+  const uint64_t rn2 = f2_both(live ? rn : 0.f);
+  uint64_t dot = 0ull;
+#pragma unroll
+  for (int e = 0; e < 4; e += 2) {
+    uint64_t wa[2], wb[2];
+    load_pairs(t.weight + e / 2 * (D / 4), wa);
+    load_pairs(t.weight + (2 + e / 2) * (D / 4), wb);
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      v.a[e + i] = f2_mul(v.a[e + i], rn2);
+      v.b[e + i] = f2_mul(v.b[e + i], rn2);
+      dw.a[e + i] = f2_fma(g.a[e + i], v.a[e + i], dw.a[e + i]);
+      dw.b[e + i] = f2_fma(g.b[e + i], v.b[e + i], dw.b[e + i]);
+      g.a[e + i] = f2_mul(g.a[e + i], wa[i]);
+      g.b[e + i] = f2_mul(g.b[e + i], wb[i]);
+      dot = f2_fma(g.a[e + i], v.a[e + i], f2_fma(g.b[e + i], v.b[e + i], dot));
+    }
+  }
+  const uint64_t nd2 = f2_both(-sum_head<D / 16>(dot) * (1.f / D));
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    g.a[e] = f2_mul(rn2, f2_fma(nd2, v.a[e], g.a[e]));
+    g.b[e] = f2_mul(rn2, f2_fma(nd2, v.b[e], g.b[e]));
+  }
+}
+
+// Steps [st, end) of one role (0: queries, 1: keys, 2: values) for token (b, s): HPW heads a step.  A step's
+// loads are issued a step ahead (in the backward two steps ahead, or three CTAs of 80 registers, were
+// slower; prefetching the next token into L2 cost an eighth).
+template <int D, bool BACK, int ROLE>
+__device__ __forceinline__ void token_heads(const PrepParams& p, const Lane<D>& t, int b, int s, int row,
+                                            int sub, int st, int end, Vec& dw) {
+  constexpr int HPW = 512 / D;
+  const PrepRole& r = p.role[ROLE];
+  if (st >= end || row < 0 || row >= r.y_rows) return;
+  const bool norm = ROLE < 2 && r.w, turns = ROLE < 2 && t.turns;
+  int h = st * HPW + sub;
+  const __nv_bfloat16* x =
+      static_cast<const __nv_bfloat16*>(r.x) + b * r.xb + s * r.xt + h * r.xh;
+  __nv_bfloat16* y = static_cast<__nv_bfloat16*>(r.y) +
+                     ((static_cast<long long>(b) * r.heads + h) * r.y_rows + row) * D;
+  __nv_bfloat16* dx = BACK ? static_cast<__nv_bfloat16*>(r.dx) + b * r.db + s * r.dt + h * r.dh : nullptr;
+  const long long x_inc = HPW * r.xh, y_inc = static_cast<long long>(HPW) * r.y_rows * D,
+                  d_inc = BACK ? HPW * r.dh : 0;
+  uint4 xa, xb, ga, gb;
+  auto fetch = [&](bool have) {
+    xa = xb = ga = gb = make_uint4(0u, 0u, 0u, 0u);
+    if (!have || h >= r.heads) return;
+    if (!BACK || norm) {
+      xa = load16(x + t.ca);
+      xb = load16(x + t.cb);
+    }
+    if (BACK) {
+      ga = load16(y + t.ca);
+      gb = load16(y + t.cb);
+    }
+  };
+  fetch(true);
+#pragma unroll 1
+  for (; st < end; ++st) {
+    const bool live = h < r.heads;
+    __nv_bfloat16* to = BACK ? dx : y;
+    uint4 oa = BACK ? ga : xa, ob = BACK ? gb : xb;
+    const uint4 va = xa, vb = xb;
+    x += x_inc;
+    y += y_inc;
+    dx += d_inc;
+    h += HPW;
+    fetch(st + 1 < end);
+    if (norm || turns) {
+      Vec v;
+      unpack8(va, v.a);
+      unpack8(vb, v.b);
+      if constexpr (BACK) {
+        Vec g;
+        unpack8(oa, g.a);
+        unpack8(ob, g.b);
+        backward_vec<D>(v, g, dw, p, t, norm, turns, live);
+        oa = pack8(g.a);
+        ob = pack8(g.b);
+      } else {
+        forward_vec<D>(v, p, t, norm, turns);
+        oa = pack8(v.a);
+        ob = pack8(v.b);
+      }
+    }
+    if (live) {
+      store16(to + t.ca, oa);
+      store16(to + t.cb, ob);
+    }
+  }
 }
 
 template <int D, bool BACK>
-__global__ void __launch_bounds__(kThreads, BACK ? 2 : kPrepCtasPerSm)
+__global__ void __launch_bounds__(kThreads, BACK ? kBwdCtasPerSm : kFwdCtasPerSm)
     fa_prep_kernel(const PrepParams p) {
   constexpr int LPH = D / 16;    // lanes per head
   constexpr int HPW = 32 / LPH;  // heads per warp and step
-  __shared__ float dw_red[BACK ? kWarps : 1][BACK ? D : 1];
+  __shared__ __align__(16) Angles<D> angles[kWarps];
+  __shared__ __align__(16) float weight[2][D];  // of queries and keys, with the offset
+  __shared__ float dw_red[BACK ? kWarps : 1][BACK ? 2 * D : 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int blk = blockIdx.x, ri = 0;
-  while (ri < 2 && blk >= p.role[ri].blocks) blk -= p.role[ri++].blocks;
-  const PrepRole& r = p.role[ri];
   const int x = lane % LPH, sub = lane / LPH;
+  Lane<D> tq, tk;
+  tq.angles = &angles[warp];
+  tq.weight = weight[0] + 4 * x;
   // the lane's two pieces of 8 channels
-  const int rot_lanes = r.rotated ? p.rot / 16 : 0;
-  const bool turns = x < rot_lanes;
-  const int ca = turns ? 8 * x : 16 * x;
-  const int cb = turns ? p.rot / 2 + 8 * x : 16 * x + 8;
-  uint64_t t64[8];
-  int axis[8];
+  tq.turns = x < p.rot / 16;
+  tq.ca = tq.turns ? 8 * x : 16 * x;
+  tq.cb = tq.turns ? p.rot / 2 + 8 * x : 16 * x + 8;
+  tq.f_a = 4 * x;
+  tq.f_b = (p.interleaved ? p.rot / 4 : D / 4) + 4 * x;
+  tk = tq;
+  tk.weight = weight[1] + 4 * x;
+  for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
+    // group k of four channels of lane xi, as the lanes' pieces are
+    const __nv_bfloat16* w = static_cast<const __nv_bfloat16*>(p.role[i / D].w);
+    const int k = i % D / (D / 4), xi = i % (D / 4) / 4, e = i % 4;
+    const bool ti = xi < p.rot / 16;
+    const int ch = (k < 2 ? (ti ? 8 * xi : 16 * xi) : (ti ? p.rot / 2 + 8 * xi : 16 * xi + 8)) + 4 * (k & 1) + e;
+    weight[i / D][i % D] = w ? __bfloat162float(w[ch]) + p.w_off : 1.f;
+  }
+  // the lane's share of a token's angles: frequencies lane and lane + 32
+  uint64_t t64[2];
+  int axis[2];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
+  for (int e = 0; e < 2; ++e) {
+    const int i = lane + 32 * e;
     t64[e] = 0;
     axis[e] = 0;
-    if (turns) {
-      const int i = p.interleaved ? (e < 4 ? 4 * x + e : p.rot / 4 + 4 * x + e - 4) : 8 * x + e;
-      axis[e] = p.freq_axis ? p.freq_axis[i] : 0;
-      if (axis[e] < p.n_axes) t64[e] = turns64(p.inv_freq[i]);
-      else axis[e] = 0;
+    if (i < p.rot / 2) {
+      const int ax = p.freq_axis ? p.freq_axis[i] : 0;
+      if (ax < p.n_axes) {
+        t64[e] = turns64(p.inv_freq[i]);
+        axis[e] = ax;
+      }
     }
   }
-  Vec w;
-  const __nv_bfloat16* wp = static_cast<const __nv_bfloat16*>(r.w);
-  if (wp) {
-    unpack8(*reinterpret_cast<const uint4*>(wp + ca), w.a);
-    unpack8(*reinterpret_cast<const uint4*>(wp + cb), w.b);
+  __syncthreads();
+  const int steps_q = (p.role[0].heads + HPW - 1) / HPW, steps_k = (p.role[1].heads + HPW - 1) / HPW;
+  const int steps_v = (p.role[2].heads + HPW - 1) / HPW;
+  const int steps = steps_q + steps_k + steps_v;
+  // The work is one line of steps, token by token, of which every warp takes an equal stretch.
+  const long long tokens = static_cast<long long>(p.B) * p.S, line = tokens * steps;
+  const long long warps = static_cast<long long>(gridDim.x) * kWarps;
+  const long long w = static_cast<long long>(blockIdx.x) * kWarps + warp;
+  const long long share = line / warps, extra = line - share * warps;
+  const long long from = w * share + min(w, extra);
+  long long left = share + (w < extra ? 1 : 0);
+  long long token = from / steps;
+  int st = static_cast<int>(from - token * steps);
+  int b = static_cast<int>(token / p.S);
+  int s = static_cast<int>(token - static_cast<long long>(b) * p.S);
+  Vec dwq, dwk;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      w.a[e] += p.w_off;
-      w.b[e] += p.w_off;
-    }
-  }
-  Vec dw;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) dw.a[e] = dw.b[e] = 0.f;
-  const int n_steps = (r.heads + HPW - 1) / HPW;
-  const int per_part = (n_steps + p.parts - 1) / p.parts;
-  const long long items = static_cast<long long>(p.B) * p.S * p.parts;
-  for (long long it = static_cast<long long>(blk) * kWarps + warp; it < items;
-       it += static_cast<long long>(r.blocks) * kWarps) {
-    const int part = static_cast<int>(it % p.parts);
-    const long long token = it / p.parts;
-    const int b = static_cast<int>(token / p.S);
-    const int s = static_cast<int>(token - static_cast<long long>(b) * p.S);
+  for (int e = 0; e < 4; ++e) dwq.a[e] = dwq.b[e] = dwk.a[e] = dwk.b[e] = 0ull;
+  while (left > 0) {
+    const int end = static_cast<int>(min(static_cast<long long>(steps), st + left));
     const int start = p.row_start ? p.row_start[b] : 0;
-    const int row = ri == 0 ? s : start + s;
-    float c[8], sn[8];
-    if (turns) {
-      if (p.positions && p.n_axes > 1) {
+    if (p.rot > 0) {
+      __syncwarp();  // the last token's angles have been read
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          turn(t64[e], __ldg(p.positions + axis[e] * static_cast<long long>(p.B) * p.S + token),
-               c[e], sn[e]);
-      } else {
-        const int pos = p.positions ? __ldg(p.positions + token) : start + s;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) turn(t64[e], pos, c[e], sn[e]);
+      for (int e = 0; e < 2; ++e) {
+        const int i = lane + 32 * e;
+        if (i < p.rot / 2) {
+          const int pos = p.positions ? __ldg(p.positions + axis[e] * tokens + token) : start + s;
+          float co, si;
+          turn(t64[e], pos, co, si);
+          const int at = place_of<D>(i, p.interleaved);
+          angles[warp].c[at] = co;
+          angles[warp].s[at] = BACK ? -si : si;
+        }
       }
+      __syncwarp();
     }
-    if (row < 0 || row >= r.y_rows) continue;  // warp-uniform: no room in the cache
-    const __nv_bfloat16* xt = static_cast<const __nv_bfloat16*>(r.x) + b * r.xb + s * r.xt;
-    __nv_bfloat16* yt = static_cast<__nv_bfloat16*>(r.y) +
-                        (static_cast<long long>(b) * r.heads * r.y_rows + row) * D;
-    const int step1 = min(n_steps, (part + 1) * per_part);
-#pragma unroll 2
-    for (int st = part * per_part; st < step1; ++st) {
-      const int h = st * HPW + sub;
-      const bool live = h < r.heads;
-      Vec v, g;
-      uint4 va = make_uint4(0u, 0u, 0u, 0u), vb = va, ga = va, gb = va;
-      __nv_bfloat16* yh = yt + static_cast<long long>(h) * r.y_rows * D;
-      if (live) {
-        if (!BACK || wp) {
-          va = load16(xt + h * r.xh + ca);
-          vb = load16(xt + h * r.xh + cb);
-        }
-        if (BACK) {
-          ga = load16(yh + ca);
-          gb = load16(yh + cb);
-        }
-      }
-      if (!wp && !turns) {  // nothing to compute: bits as they are
-        if (live) {
-          __nv_bfloat16* to = BACK ? static_cast<__nv_bfloat16*>(r.dx) + b * r.db + s * r.dt + h * r.dh
-                                   : yh;
-          store16(to + ca, BACK ? ga : va);
-          store16(to + cb, BACK ? gb : vb);
-        }
-        continue;
-      }
-      unpack8(va, v.a);
-      unpack8(vb, v.b);
-      float rn = 1.f;
-      if (wp) {
-        float ss = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(v.a[e], v.a[e], fmaf(v.b[e], v.b[e], ss));
-        rn = rsqrtf(sum_head<LPH>(ss) * (1.f / D) + p.eps);
-      }
-      if (!BACK) {
-        if (wp) {
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            v.a[e] *= rn * w.a[e];
-            v.b[e] *= rn * w.b[e];
-          }
-        }
-        if (turns) rotate(v, c, sn, p.interleaved, false);
-        if (live) {
-          store16(yh + ca, pack8(v.a));
-          store16(yh + cb, pack8(v.b));
-        }
-      } else {
-        unpack8(ga, g.a);
-        unpack8(gb, g.b);
-        if (turns) rotate(g, c, sn, p.interleaved, true);
-        if (wp) {
-          float dot = 0.f;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            v.a[e] *= rn;
-            v.b[e] *= rn;
-            if (live) {
-              dw.a[e] = fmaf(g.a[e], v.a[e], dw.a[e]);
-              dw.b[e] = fmaf(g.b[e], v.b[e], dw.b[e]);
-            }
-            g.a[e] *= w.a[e];
-            g.b[e] *= w.b[e];
-            dot = fmaf(g.a[e], v.a[e], fmaf(g.b[e], v.b[e], dot));
-          }
-          dot = sum_head<LPH>(dot) * (1.f / D);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            g.a[e] = rn * fmaf(-dot, v.a[e], g.a[e]);
-            g.b[e] = rn * fmaf(-dot, v.b[e], g.b[e]);
-          }
-        }
-        if (live) {
-          __nv_bfloat16* to = static_cast<__nv_bfloat16*>(r.dx) + b * r.db + s * r.dt + h * r.dh;
-          store16(to + ca, pack8(g.a));
-          store16(to + cb, pack8(g.b));
-        }
-      }
+    token_heads<D, BACK, 0>(p, tq, b, s, s, sub, st, min(end, steps_q), dwq);
+    token_heads<D, BACK, 1>(p, tk, b, s, start + s, sub, max(0, st - steps_q),
+                            min(end - steps_q, steps_k), dwk);
+    token_heads<D, BACK, 2>(p, tk, b, s, start + s, sub, max(0, st - steps_q - steps_k),
+                            min(end - steps_q - steps_k, steps_v), dwk);
+    left -= end - st;
+    st = 0;
+    ++token;
+    if (++s == p.S) {
+      s = 0;
+      ++b;
     }
   }
   if constexpr (BACK) {
-    if (!r.dw) return;  // CTA-uniform
+    if (!(p.role[0].dw || p.role[1].dw)) return;  // grid-uniform
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
+    for (int k = 0; k < 2; ++k) {
+      const Vec& d = k ? dwk : dwq;
 #pragma unroll
-      for (int o = LPH; o < 32; o <<= 1) {
-        dw.a[e] += __shfl_xor_sync(0xffffffffu, dw.a[e], o);
-        dw.b[e] += __shfl_xor_sync(0xffffffffu, dw.b[e], o);
-      }
-      if (sub == 0) {
-        dw_red[warp][ca + e] = dw.a[e];
-        dw_red[warp][cb + e] = dw.b[e];
+      for (int e = 0; e < 4; ++e) {
+        float v[4];
+        f2_unpack(d.a[e], v[0], v[1]);
+        f2_unpack(d.b[e], v[2], v[3]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int o = LPH; o < 32; o <<= 1) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+        if (sub == 0) {
+          dw_red[warp][k * D + tq.ca + 2 * e] = v[0];
+          dw_red[warp][k * D + tq.ca + 2 * e + 1] = v[1];
+          dw_red[warp][k * D + tq.cb + 2 * e] = v[2];
+          dw_red[warp][k * D + tq.cb + 2 * e + 1] = v[3];
+        }
       }
     }
     __syncthreads();
-    if (threadIdx.x < D) {
+    for (int i = threadIdx.x; i < 2 * D; i += kThreads) {
       float sum = 0.f;
 #pragma unroll
-      for (int wi = 0; wi < kWarps; ++wi) sum += dw_red[wi][threadIdx.x];
-      p.partial[static_cast<size_t>(blockIdx.x) * D + threadIdx.x] = sum;
+      for (int wi = 0; wi < kWarps; ++wi) sum += dw_red[wi][i];
+      p.partial[static_cast<size_t>(blockIdx.x) * 2 * D + i] = sum;
     }
     griddep_launch_dependents();
   }
@@ -300,20 +449,20 @@ template <int D>
 __global__ void __launch_bounds__(8 * D) fa_prep_dw_kernel(const PrepParams p) {
   __shared__ float red[8][D];
   const int ch = threadIdx.x % D, part = threadIdx.x / D;
-  const PrepRole& r = p.role[blockIdx.x];
-  if (!r.dw) return;
-  const int first = blockIdx.x ? p.role[0].blocks : 0;
+  float* dw = p.role[blockIdx.x].dw;
+  if (!dw) return;
   griddep_wait();
   float sum = 0.f;
 #pragma unroll 4
-  for (int k = part; k < r.blocks; k += 8) sum += p.partial[static_cast<size_t>(first + k) * D + ch];
+  for (int k = part; k < p.blocks; k += 8)
+    sum += p.partial[static_cast<size_t>(k) * 2 * D + blockIdx.x * D + ch];
   red[part][ch] = sum;
   __syncthreads();
   if (part == 0) {
     float t = 0.f;
 #pragma unroll
     for (int k = 0; k < 8; ++k) t += red[k][ch];
-    r.dw[ch] = t;
+    dw[ch] = t;
   }
 }
 
@@ -321,39 +470,24 @@ __global__ void __launch_bounds__(8 * D) fa_prep_dw_kernel(const PrepParams p) {
 
 int prep_partial_rows() { return kMaxPartialRows; }
 
-// CTAs are dealt to queries, keys and values by their heads.  With few tokens several warps share
-// a token's heads, as long as there are not enough warps for the device.
-void prep_plan(PrepParams* p, int n_sm) {
+void prep_plan(PrepParams* p, int n_sm, bool back) {
   const int hpw = 32 / (p->d / 16);
-  const long long tokens = static_cast<long long>(p->B) * p->S;
-  int heads = 0, most = 0;
-  for (const PrepRole& r : p->role) {
-    heads += r.heads;
-    most = std::max(most, (r.heads + hpw - 1) / hpw);
-  }
-  const long long want = static_cast<long long>(n_sm) * kWarps;
-  p->parts = static_cast<int>(std::min<long long>(most, std::max(1LL, want / std::max(1LL, 3 * tokens))));
-  const long long items = tokens * p->parts;
-  const int total = std::min(n_sm * kPrepCtasPerSm, kMaxPartialRows - 3);
-  for (PrepRole& r : p->role) {
-    const long long share = std::max(1LL, static_cast<long long>(total) * r.heads / std::max(1, heads));
-    r.blocks = r.heads ? static_cast<int>(std::min(share, (items + kWarps - 1) / kWarps)) : 0;
-  }
+  long long steps = 0;
+  for (const PrepRole& r : p->role) steps += (r.heads + hpw - 1) / hpw;
+  steps *= static_cast<long long>(p->B) * p->S;
+  const int wave = back ? std::min(n_sm * kBwdCtasPerSm, kMaxPartialRows) : n_sm * kFwdCtasPerSm;
+  p->blocks = static_cast<int>(std::min<long long>(wave, (steps + kWarps - 1) / kWarps));
 }
 
-namespace {
-int grid_of(const PrepParams& p) { return p.role[0].blocks + p.role[1].blocks + p.role[2].blocks; }
-}  // namespace
-
 cudaError_t launch_prep(const PrepParams& p, cudaStream_t stream) {
-  if (p.d == 128) fa_prep_kernel<128, false><<<grid_of(p), kThreads, 0, stream>>>(p);
-  else fa_prep_kernel<64, false><<<grid_of(p), kThreads, 0, stream>>>(p);
+  if (p.d == 128) fa_prep_kernel<128, false><<<p.blocks, kThreads, 0, stream>>>(p);
+  else fa_prep_kernel<64, false><<<p.blocks, kThreads, 0, stream>>>(p);
   return cudaGetLastError();
 }
 
 cudaError_t launch_prep_bwd(const PrepParams& p, cudaStream_t stream) {
-  if (p.d == 128) fa_prep_kernel<128, true><<<grid_of(p), kThreads, 0, stream>>>(p);
-  else fa_prep_kernel<64, true><<<grid_of(p), kThreads, 0, stream>>>(p);
+  if (p.d == 128) fa_prep_kernel<128, true><<<p.blocks, kThreads, 0, stream>>>(p);
+  else fa_prep_kernel<64, true><<<p.blocks, kThreads, 0, stream>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !(p.role[0].dw || p.role[1].dw)) return e;
   if (p.d == 128) return launch_dependent(fa_prep_dw_kernel<128>, dim3(2), dim3(1024), 0, stream, p);

@@ -19,8 +19,6 @@ struct PrepRole {
   float* dw;            // backward: fp32 [d] or nullptr
   int y_rows;           // rows of a head in y
   int heads;
-  int rotated;          // 0: values (copied)
-  int blocks;           // CTAs of this role
 };
 
 struct PrepParams {
@@ -29,15 +27,15 @@ struct PrepParams {
   const float* inv_freq;      // [rot / 2]
   const uint8_t* freq_axis;   // [rot / 2] or nullptr: axis 0
   const int32_t* row_start;   // [B] or nullptr: first row of keys and values
-  float* partial;             // backward: [blocks of queries and keys][d]
+  float* partial;             // backward: [blocks][queries, keys][d]
   float w_off, eps;
   int n_axes, rot, interleaved;
   int B, S, d;
-  int parts;                  // warps that share a token's heads
+  int blocks;
 };
 
-// Sets the roles' CTAs and the parts for a device of n_sm SMs.
-void prep_plan(PrepParams* p, int n_sm);
+// Sets the CTAs for a device of n_sm SMs.
+void prep_plan(PrepParams* p, int n_sm, bool back);
 // Most rows of `partial` that a backward pass uses.
 int prep_partial_rows();
 cudaError_t launch_prep(const PrepParams& p, cudaStream_t stream);

@@ -219,8 +219,7 @@ fa_status fa_qk_norm_rope(const fa_heads* q, const fa_heads* k, const fa_heads* 
   p.role[0].heads = Hq;
   p.role[1].heads = Hkv;
   p.role[2].heads = v ? Hkv : 0;
-  p.role[0].rotated = p.role[1].rotated = rot_dim > 0;
-  fa::prep_plan(&p, n_sm);
+  fa::prep_plan(&p, n_sm, false);
   const cudaError_t e = fa::launch_prep(p, stream);
   if (e != cudaSuccess)
     return api_fail(FA_ERR_CUDA, "fa_qk_norm_rope launch: %s", cudaGetErrorString(e));
@@ -228,7 +227,7 @@ fa_status fa_qk_norm_rope(const fa_heads* q, const fa_heads* k, const fa_heads* 
 }
 
 size_t fa_qk_norm_rope_bwd_workspace_size(int d) {
-  return d < 1 ? 0 : static_cast<size_t>(fa::prep_partial_rows()) * d * sizeof(float);
+  return d < 1 ? 0 : static_cast<size_t>(fa::prep_partial_rows()) * 2 * d * sizeof(float);
 }
 
 fa_status fa_qk_norm_rope_bwd(const fa_heads* q, const fa_heads* k, const void* dq_out,
@@ -284,8 +283,7 @@ fa_status fa_qk_norm_rope_bwd(const fa_heads* q, const fa_heads* k, const void* 
   p.role[0].heads = Hq;
   p.role[1].heads = Hkv;
   p.role[2].heads = dv ? Hkv : 0;
-  p.role[0].rotated = p.role[1].rotated = rot_dim > 0;
-  fa::prep_plan(&p, n_sm);
+  fa::prep_plan(&p, n_sm, true);
   const cudaError_t e = fa::launch_prep_bwd(p, stream);
   if (e != cudaSuccess)
     return api_fail(FA_ERR_CUDA, "fa_qk_norm_rope_bwd launch: %s", cudaGetErrorString(e));
