@@ -568,8 +568,8 @@ size_t fa_decode_scored_workspace_size(int B, int Hq, int Hkv, int Sk_max, int d
 /*
  * fa_decode on such scores.  The query of batch row b is position n - 1, n = seqlens_k[b] (clamped
  * to [0, Sk_max]); it sees the keys [max(0, k_start[b], n - window), n) (k_start device int32[B] or
- * NULL: 0; window 0: none).  No other key is read.  The split plan depends on the arguments,
- * never on the values in seqlens_k and k_start.  B is at most 65535.
+ * NULL: 0; window 0: none).  No other key is read.  Grid and workspace depend on the arguments,
+ * never on the values in seqlens_k and k_start.  B * Hq must be below 2^31.
  */
 fa_status fa_decode_scored(const void* q, const void* k_cache, const void* v_cache, void* o,
                            float* lse, const int32_t* seqlens_k, const int32_t* k_start, int B,

@@ -538,11 +538,9 @@ fa_status fa_bwd_scored(const void* q, const void* k, const void* v, const void*
 }
 
 size_t fa_decode_scored_workspace_size(int B, int Hq, int Hkv, int Sk_max, int d, int window) {
-  if (B < 1 || Hq < 1 || Hkv < 1 || Sk_max < 1 || d < 1 || window < 0) return 0;
-  int chunk = 0, n_split = 0;
-  fa::decode_scored_plan(B, Hq, Hkv, Sk_max, window, &chunk, &n_split);
-  const size_t rows = static_cast<size_t>(B) * Hq * n_split;
-  return align256(rows * d * sizeof(float)) + align256(rows * sizeof(float));
+  if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Sk_max < 1 || d < 1 || window < 0) return 0;
+  const fa::DecodeScoredPlan plan = fa::decode_scored_plan(B, Hq, Hkv, Sk_max, d, window);
+  return plan.span_bytes + plan.o_bytes + plan.lse_bytes;
 }
 
 fa_status fa_decode_scored(const void* q, const void* k_cache, const void* v_cache, void* o,
@@ -581,17 +579,21 @@ fa_status fa_decode_scored(const void* q, const void* k_cache, const void* v_cac
   p.Hkv = Hkv;
   p.Sk_max = Sk_max;
   p.group = Hq / Hkv;
-  fa::decode_scored_plan(B, Hq, Hkv, Sk_max, window, &p.chunk, &p.n_split);
-  const size_t rows = static_cast<size_t>(B) * Hq * p.n_split;
-  p.part_o = static_cast<float*>(workspace);
-  p.part_lse = reinterpret_cast<float*>(static_cast<char*>(workspace) +
-                                        align256(rows * d * sizeof(float)));
+  const fa::DecodeScoredPlan plan = fa::decode_scored_plan(B, Hq, Hkv, Sk_max, d, window);
+  p.heads = plan.heads;
+  p.subs = plan.subs;
+  char* base = static_cast<char*>(workspace);
+  p.span = reinterpret_cast<int2*>(base);
+  p.part_o = reinterpret_cast<float*>(base + plan.span_bytes);
+  p.part_lse = reinterpret_cast<float*>(base + plan.span_bytes + plan.o_bytes);
   p.scale_log2 = scale_log2_of(scale);
-  // grid: splits x KV heads (times the head groups of 8) x batch rows
-  if (B > 65535 || 1LL * Hkv * ((p.group + 7) / 8) > 65535)
-    return fail(FA_ERR_INVALID_ARG, "decode grid too large (B=%d, Hkv=%d)", B, Hkv);
+  if (1LL * B * Hq > 0x7fffffffLL)
+    return fail(FA_ERR_INVALID_ARG, "decode grid too large (B=%d, Hq=%d)", B, Hq);
   FA_TRY(check_device());
-  const cudaError_t e = fa::launch_decode_scored(d, p, stream);
+  CUtensorMap tk, tv;
+  FA_TRY(make_map(&tk, k_cache, 1L * B * Hkv, Sk_max, d));
+  FA_TRY(make_map(&tv, v_cache, 1L * B * Hkv, Sk_max, d));
+  const cudaError_t e = fa::launch_decode_scored(d, tk, tv, p, plan, stream);
   if (e != cudaSuccess)
     return fail(FA_ERR_CUDA, "fa_decode_scored launch: %s", cudaGetErrorString(e));
   return ok();

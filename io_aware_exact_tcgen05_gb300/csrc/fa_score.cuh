@@ -67,13 +67,13 @@ __device__ __forceinline__ uint64_t cap_factor7(uint64_t s2, const ScoreArgs& sc
   return m;
 }
 
-// cap' * tanh(a s) of one score, by whichever way holds.
-__device__ __forceinline__ float cap_one(float s, const ScoreArgs& sc) {
+// cap' * tanh(a s) of one score with |s| <= small[1].
+__device__ __forceinline__ float cap_small(float s, const ScoreArgs& sc) {
   const float u = s * s;
   float m = sc.poly4[4].x;
 #pragma unroll
   for (int i = 3; i >= 0; --i) m = fmaf(u, m, sc.poly4[i].x);
-  return fabsf(s) <= sc.small[1] ? s * m : cap_any(s, sc);
+  return s * m;
 }
 
 }  // namespace fa

@@ -75,16 +75,26 @@ struct ScoreArgs {
   MaskPlan plan;
 };
 
+// fa_decode on such scores: sizes, inputs and outputs of DecodeParams (its split plan is not used).
 struct ScoredDecodeParams : DecodeParams {
   const int32_t* k_start;  // int32 [B] or nullptr
   int window;              // last keys seen; 0: all
   bool capped;
+  int heads;               // query heads of a work item (up to 16 of one KV head)
+  int subs;                // work items of a batch row
+  int2* span;              // [B * subs]: first and last CTA of each item
   ScoreArgs sc;
 };
 
-void decode_scored_plan(int B, int Hq, int Hkv, int Sk_max, int window, int* chunk,
-                        int* n_split);
-cudaError_t launch_decode_scored(int d, const ScoredDecodeParams& p, cudaStream_t stream);
+// Workspace: span, then per (CTA, item) slot the partial outputs and their log2-sums.
+struct DecodeScoredPlan {
+  int heads, subs, ctas;
+  size_t slots, span_bytes, o_bytes, lse_bytes;
+};
+DecodeScoredPlan decode_scored_plan(int B, int Hq, int Hkv, int Sk_max, int d, int window);
+cudaError_t launch_decode_scored(int d, const CUtensorMap& tk, const CUtensorMap& tv,
+                                 const ScoredDecodeParams& p, const DecodeScoredPlan& plan,
+                                 cudaStream_t stream);
 unsigned int read_decode_scored_status(bool clear);
 
 cudaError_t launch_fwd_scored(int d, const CUtensorMap& tq, const CUtensorMap& tk,

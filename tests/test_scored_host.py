@@ -177,7 +177,7 @@ def test_scored_attention_refuses_before_any_device_call(lib):
     assert dec(k_start=18) == fa.FA_ERR_INVALID_ARG
     assert dec(nws=64) == fa.FA_ERR_WORKSPACE
     assert dec(cap=float("nan")) == fa.FA_ERR_INVALID_ARG
-    assert dec(B=65536, Sk=1, nws=1 << 40) == fa.FA_ERR_INVALID_ARG
+    assert dec(B=1 << 29, Sk=1, nws=1 << 60) == fa.FA_ERR_INVALID_ARG  # B x Hq past 32 bits
     assert fa.fa_decode_scored_workspace_size(0, 1, 1, 8, 64) == 0
     assert fa.fa_decode_scored_workspace_size(2, 4, 2, 100000, 128, 64) < fa.fa_decode_scored_workspace_size(
         2, 4, 2, 100000, 128)
