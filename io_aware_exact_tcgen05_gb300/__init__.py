@@ -691,6 +691,22 @@ def fa_decode_paged_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seql
 
 # ------------------------------------- between a projection and the scores --
 
+# Sizes that depend on numbers alone are asked for once.
+@functools.lru_cache(4096)
+def _plan_bytes(B, Sq, Sk):
+    return load_library().fa_mask_plan_size(B, Sq, Sk)
+
+
+@functools.lru_cache(4096)
+def _decode_scored_bytes(B, Hq, Hkv, Sk_max, d, window):
+    return load_library().fa_decode_scored_workspace_size(B, Hq, Hkv, Sk_max, d, window)
+
+
+@functools.lru_cache(4096)
+def _bwd_bytes(B, Hq, Sq, d):
+    return load_library().fa_bwd_workspace_size(B, Hq, Sq, d)
+
+
 def _view(t, name, shape, dev):
     """fa_heads of a bf16 tensor of that shape [B, S, H, d] with contiguous channels."""
     if not (isinstance(t, torch.Tensor) and t.dtype == _BF16 and t.get_device() == dev
@@ -851,9 +867,10 @@ def fa_mask_plan(row_lo, row_hi, Sk: int, plan=None, stream=None):
     Sk = _int(Sk, "Sk")
     _have(row_lo, "row_lo", _I32, (B, Sq), dev)
     _have(row_hi, "row_hi", _I32, (B, Sq), dev)
-    plan = _out(plan, "plan", (lib.fa_mask_plan_size(B, Sq, Sk),), _U8, dev, stream)
-    st = lib.fa_mask_plan(row_lo.data_ptr(), row_hi.data_ptr(), B, Sq, Sk, plan.data_ptr(),
-                          plan.nbytes, _stream(stream))
+    nbytes = _plan_bytes(B, Sq, Sk)
+    plan = _out(plan, "plan", (nbytes,), _U8, dev, stream)
+    st = lib.fa_mask_plan(row_lo.data_ptr(), row_hi.data_ptr(), B, Sq, Sk, plan.data_ptr(), nbytes,
+                          _stream(stream))
     _check(st, "fa_mask_plan")
     return plan
 
@@ -869,8 +886,9 @@ def _scored_args(q, k, v, slopes, plan, dev):
         _have(slopes, "slopes", _F32, (Hq,), dev)
     if plan is None:
         return B, Hq, Hkv, Sq, Sk, d, 0
-    _have(plan, "plan", _U8, (load_library().fa_mask_plan_size(B, Sq, Sk),), dev)
-    return B, Hq, Hkv, Sq, Sk, d, plan.nbytes
+    nbytes = _plan_bytes(B, Sq, Sk)
+    _have(plan, "plan", _U8, (nbytes,), dev)
+    return B, Hq, Hkv, Sq, Sk, d, nbytes
 
 
 def fa_fwd_scored(q, k, v, causal: bool, scale: float, softcap: float = 0.0, slopes=None, plan=None,
@@ -901,7 +919,7 @@ def fa_bwd_scored(q, k, v, o, dout, lse, causal: bool, scale: float, softcap: fl
     dq = _out(dq, "dq", (B, Hq, Sq, d), _BF16, dev, stream)
     dk = _out(dk, "dk", (B, Hkv, Sk, d), _BF16, dev, stream)
     dv = _out(dv, "dv", (B, Hkv, Sk, d), _BF16, dev, stream)
-    workspace = _workspace(workspace, fa_bwd_workspace_size(B, Hq, Sq, d), dev, stream)
+    workspace = _workspace(workspace, _bwd_bytes(B, Hq, Sq, d), dev, stream)
     st = lib.fa_bwd_scored(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), dout.data_ptr(),
                            lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, Hq, Hkv,
                            Sq, Sk, d, int(bool(causal)), float(scale), float(softcap), _ptr(slopes),
@@ -938,8 +956,7 @@ def fa_decode_scored(q, k_cache, v_cache, seqlens_k, scale: float, softcap: floa
     window = _int(window, "window")
     o = _out(o, "o", (B, Hq, 1, d), _BF16, dev, stream)
     lse = _out(lse, "lse", (B, Hq), _F32, dev, stream)
-    workspace = _workspace(
-        workspace, lib.fa_decode_scored_workspace_size(B, Hq, Hkv, Sk_max, d, window), dev, stream)
+    workspace = _workspace(workspace, _decode_scored_bytes(B, Hq, Hkv, Sk_max, d, window), dev, stream)
     st = lib.fa_decode_scored(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), o.data_ptr(),
                               lse.data_ptr(), seqlens_k.data_ptr(), _ptr(k_start), B, Hq, Hkv,
                               Sk_max, d, float(scale), float(softcap), _ptr(slopes), window,

@@ -326,11 +326,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         // ---- scores of 16 keys: two tiles of 8 ----
         float sc[2][4];
-  #pragma unroll
+#pragma unroll
         for (int nt = 0; nt < 2; ++nt) {
-  #pragma unroll
+#pragma unroll
           for (int e = 0; e < 4; ++e) sc[nt][e] = 0.f;
-  #pragma unroll
+#pragma unroll
           for (int q = 0; q < D / 32; ++q) {
             uint32_t b[4];
             ldsm4(kb + chunk_at<D>(r0 + nt * 8 + (lane & 7), 4 * q + (lane >> 3)), b);
@@ -341,34 +341,34 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---- z, in units of log2(e) ----
         if (p.capped) {
           float most = 0.f;
-  #pragma unroll
+#pragma unroll
           for (int nt = 0; nt < 2; ++nt)
-  #pragma unroll
+#pragma unroll
             for (int e = 0; e < 2 * HALVES; ++e) most = fmaxf(most, fabsf(sc[nt][e]));
           if (__all_sync(0xffffffffu, most <= p.sc.small[1])) {
-  #pragma unroll
+#pragma unroll
             for (int nt = 0; nt < 2; ++nt)
-  #pragma unroll
+#pragma unroll
               for (int e = 0; e < 2 * HALVES; ++e) sc[nt][e] = cap_small(sc[nt][e], p.sc);
           } else {
-  #pragma unroll
+#pragma unroll
             for (int nt = 0; nt < 2; ++nt)
-  #pragma unroll
+#pragma unroll
               for (int e = 0; e < 2 * HALVES; ++e) sc[nt][e] = cap_any(sc[nt][e], p.sc);
           }
         } else {
-  #pragma unroll
+#pragma unroll
           for (int nt = 0; nt < 2; ++nt)
-  #pragma unroll
+#pragma unroll
             for (int e = 0; e < 2 * HALVES; ++e) sc[nt][e] *= p.scale_log2;
         }
         float mx[HALVES];
-  #pragma unroll
+#pragma unroll
         for (int u = 0; u < HALVES; ++u) {
           mx[u] = neg_inf();
-  #pragma unroll
+#pragma unroll
           for (int nt = 0; nt < 2; ++nt)
-  #pragma unroll
+#pragma unroll
             for (int e = 0; e < 2; ++e) {
               const int key = nt * 8 + 2 * kc + e;
               float& z = sc[nt][2 * u + e];
@@ -382,7 +382,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // ---- online softmax, per head ----
         bool grow = false;
         float alpha[HALVES];
-  #pragma unroll
+#pragma unroll
         for (int u = 0; u < HALVES; ++u) {
           // m_new - m is formed only once m is finite: -inf - (-inf) is never evaluated
           const bool first = m[u] == neg_inf() && mx[u] != neg_inf();
@@ -392,10 +392,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           grow = grow || up;
         }
         if (__any_sync(0xffffffffu, grow)) {
-  #pragma unroll
+#pragma unroll
           for (int u = 0; u < HALVES; ++u) {
             l[u] *= alpha[u];
-  #pragma unroll
+#pragma unroll
             for (int i = 0; i < D / 8; ++i) {
               o[i][2 * u] *= alpha[u];
               o[i][2 * u + 1] *= alpha[u];
@@ -403,10 +403,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         uint32_t hi[4] = {0u, 0u, 0u, 0u}, lo[4] = {0u, 0u, 0u, 0u};  // weights as the second product's rows
-  #pragma unroll
+#pragma unroll
         for (int u = 0; u < HALVES; ++u) {
           const float mc = m[u] == neg_inf() ? 0.f : m[u];
-  #pragma unroll
+#pragma unroll
           for (int nt = 0; nt < 2; ++nt) {
             const float p0 = ex2_approx(sc[nt][2 * u] - mc), p1 = ex2_approx(sc[nt][2 * u + 1] - mc);
             l[u] += p0 + p1;
@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
         // ---- O += w V ----
-  #pragma unroll
+#pragma unroll
         for (int i = 0; i < D / 8; i += 2) {
           uint32_t b[4];
           ldsm4_t(vb + chunk_at<D>(r0 + (lane & 15), i + (lane >> 4)), b);
