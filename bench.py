@@ -469,8 +469,8 @@ def run_ours(args):
             v_cpu, threads, sample = cpu_oracle_sample(w, budget_s=args.cpu_budget)
             cpu = {"value": v_cpu, "unit": "TFLOP/s", "cores": threads, "kind": "oracle",
                    "sample": sample}
-        trafficb = _traffic("fa_bwd_main", "fa_bwd.cu")
-        trafficf = _traffic("fa_fwd_kernel", "fa_fwd.cu")
+        trafficb = _traffic("fa_bwd_main", "fa_bwd_kernel.cuh")
+        trafficf = _traffic("fa_fwd_kernel", "fa_fwd_kernel.cuh")
         line = {
             "metric": METRIC, "value": value, "unit": "TFLOP/s", "n_gpus": ws,
             "steps": args.steps, "warmup": max(3, args.warmup), "ms_per_step": ms_per_step,
