@@ -100,10 +100,11 @@ struct BwdSmem {
   float dq_stage[4][2][32 * 32];    // per drain warp: two 32x32 fp32 boxes, 128B swizzle
   float nlse2[2][kTileM];           // -LSE * log2(e), -inf for rows without keys
   float ndelta[2][kTileM];          // -D_i; both double-buffered by tile parity
-  // scored modes: the keys of the tile that each query sees, first | end << 8 (relative to the
-  // tile), and whether a group of 32 queries sees all of it
+  // scored modes: the keys of the tile that each query sees, first | end << 8 (relative to the tile;
+  // 128 and 0 for a query that sees none anywhere)
+  // and of each group of 32 queries: 1 all of them see all of it, 2 one sees none anywhere
   uint16_t qvis[2][kTileM];
-  uint32_t qfull[2][4];
+  alignas(16) uint32_t qfull[2][4];
   uint64_t stat_ready[2];
   uint64_t kv_full;
   uint64_t q_full[kQStages], q_empty[kQStages];
@@ -283,13 +284,30 @@ __global__ void __launch_bounds__(256) fa_bwd_convert(const BwdParams p, long lo
 constexpr float kWeightLog2 = 15.f;
 constexpr float kWeightInv = 1.f / 32768.f;
 
+// 32 raw scores to z in place, by the way that holds for the warp's largest magnitude.
+__device__ __forceinline__ void scored_cap(uint32_t (&sr)[32], const ScoreArgs& sc, float largest) {
+  if (__all_sync(0xffffffffu, largest <= sc.small[1])) {
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+      const uint64_t s2 = f2_pack(__uint_as_float(sr[e]), __uint_as_float(sr[e + 1]));
+      float a, b;
+      f2_unpack(f2_mul(s2, cap_small_factor<4>(s2, sc)), a, b);
+      sr[e] = __float_as_uint(a);
+      sr[e + 1] = __float_as_uint(b);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 32; ++e) sr[e] = __float_as_uint(cap_any(__uint_as_float(sr[e]), sc));
+  }
+}
+
 // Weights of one key (a thread) for 32 queries, from raw scores: p = 2^(z + nl) with z in units of
 // log2(e), hidden queries 0; pw gets p in bf16 pairs, pg in f16 pairs what dS needs: p, times the cap's
 // derivative 1 - tanh^2 when there is one.  nl2 holds -LSE of the queries, with the bias of the tile's
 // first key where distances are linear; kb is then the key's own share.
 //  * WAY 0, 1, 2: every query sees the key, distances are linear and the scores are within a
 //    polynomial's range (of degree 2, 4, 7);
-//  * WAY 3: any tile; d0 = the first query's position less the key.
+//  * WAY 3: any tile, with a cap from z (scored_cap); d0 = the first query's position less the key.
 template <bool CAP, bool BIAS, int WAY>
 __device__ __forceinline__ void scored_weights(const uint32_t (&sr)[32], const ScoreArgs& sc,
                                                uint64_t c2, const uint64_t* nl2, bool linear,
@@ -298,6 +316,9 @@ __device__ __forceinline__ void scored_weights(const uint32_t (&sr)[32], const S
                                                uint32_t* pg) {
   const uint64_t kb2 = f2_pack(kb, kb);
   const float df = static_cast<float>(d0);
+  // Hidden queries: with 127 - row added to the bytes first, end of each query, bit 7 says "past
+  // the row", and nothing carries over (the bytes are at most 128).
+  const uint32_t rows4 = 0x01010101u * static_cast<uint32_t>(127 - row);
 #pragma unroll
   for (int e = 0; e < 16; ++e) {
     const uint64_t s2 = f2_pack(__uint_as_float(sr[2 * e]), __uint_as_float(sr[2 * e + 1]));
@@ -316,8 +337,7 @@ __device__ __forceinline__ void scored_weights(const uint32_t (&sr)[32], const S
     if (CAP) {
       uint64_t z2;
       if (WAY == 3) {
-        z2 = f2_pack(cap_any(__uint_as_float(sr[2 * e]), sc),
-                     cap_any(__uint_as_float(sr[2 * e + 1]), sc));
+        z2 = s2;  // z already (scored_cap)
       } else if (WAY == 2) {
         uint64_t y2;
         const uint64_t m2 = cap_factor7(s2, sc, y2);
@@ -334,9 +354,10 @@ __device__ __forceinline__ void scored_weights(const uint32_t (&sr)[32], const S
     float p0 = ex2_approx(x0);
     float p1 = ex2_approx(x1);
     if (WAY == 3 && masked) {
-      const uint32_t v = *reinterpret_cast<const uint32_t*>(qvis + 2 * e);
-      if (row < static_cast<int>(v & 0xff) || row >= static_cast<int>((v >> 8) & 0xff)) p0 = g0 = 0.f;
-      if (row < static_cast<int>((v >> 16) & 0xff) || row >= static_cast<int>(v >> 24)) p1 = g1 = 0.f;
+      const uint32_t v = *reinterpret_cast<const uint32_t*>(qvis + 2 * e) + rows4;
+      const uint32_t seen = (v >> 8) & ~v;  // end past the row, first not
+      if (!(seen & 0x80u)) p0 = g0 = 0.f;
+      if (!(seen & 0x800000u)) p1 = g1 = 0.f;
     }
     pw[e] = pack_bf16x2(p0, p1);
     if (CAP) {
@@ -643,6 +664,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t w = __ldg(p.key_bits + static_cast<size_t>(bz) * p.mask_words + key / 32);
         key_in = (w >> (key & 31)) & 1u;
       }
+      const bool edge = SCORED && (c0 < klo || c0 + kTileN > kend);  // keys that no query sees
       const uint32_t key8 = static_cast<uint32_t>(key) >> 3;
       for (int it = 0; it < n_it; ++it) {
         const int gi = ig + it;  // this iteration's index across units (barrier phases)
@@ -662,7 +684,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         // after every compute warp has signalled dS of the tile that read it
         // (S^T of the next tile is issued only after that).
         const int sb = gi & 1;
-        bool dead = false;  // scored modes: the query of this hf = 0 thread has no keys
         if (hf == 0) {
           // stored negated so that p = 2^(s*c + nl) and dP - D = dP + nd are one
           // packed FMA / add per pair; rows without keys get nl = -inf (p = 0)
@@ -693,12 +714,13 @@ __global__ void __launch_bounds__(kThreads, 1)
               }
               if (p.causal) hi = min(hi, qi + off + 1);
             }
-            dead = hi <= lo && qi < sq;  // (rows past the end arrive as zeros)
-            lo = max(0, min(lo - c0, kTileN));
-            hi = max(0, min(hi - c0, kTileN));
+            const bool dead = hi <= lo && qi < sq;  // (rows past the end arrive as zeros)
+            lo = dead ? kTileN : max(0, min(lo - c0, kTileN));
+            hi = dead ? 0 : max(0, min(hi - c0, kTileN));
             s.qvis[sb][row] = static_cast<uint16_t>(lo | (hi << 8));
             const bool full = __all_sync(0xffffffffu, lo == 0 && hi == kTileN);
-            if (lane == 0) s.qfull[sb][grp] = full;
+            const bool any_dead = __any_sync(0xffffffffu, dead);
+            if (lane == 0) s.qfull[sb][grp] = (full ? 1u : 0u) | (any_dead ? 2u : 0u);
           }
           s.nlse2[sb][row] = nl;
           s.ndelta[sb][row] = nd;
@@ -712,20 +734,79 @@ __global__ void __launch_bounds__(kThreads, 1)
         // visible queries of this key row: q >= key - off (causal), key in [klo, kend)
         const int qmin = p.causal ? key - off : -0x7fffffff;
         bool need_mask = !key_in || (p.causal && q0 + hf * 64 < qmin);
-        if constexpr (SCORED)
-          need_mask = __any_sync(0xffffffffu, !s.qfull[sb][2 * hf] || !s.qfull[sb][2 * hf + 1]);
+        bool guard_ds = false;  // scored modes: dP or D may be anything where the weight is 0
+        if constexpr (SCORED) {
+          const uint4 f = *reinterpret_cast<const uint4*>(s.qfull[sb]);
+          need_mask = __any_sync(0xffffffffu, !((hf ? f.z & f.w : f.x & f.y) & 1u));
+          guard_ds = __any_sync(0xffffffffu, ((f.x | f.y | f.z | f.w) & 2u) != 0) || edge;
+        }
         if (!mbar_wait_warp(&s.s_full, gi & 1, abort_flag, kSiteS)) { ok = false; break; }
         tc_fence_after();
+        if constexpr (SCORED) {
+          // Rows and keys that nothing is computed for may hold anything, and a weight of 0 does
+          // not cancel a NaN: Q and dO of queries without keys, and K of keys outside of the
+          // hull of all intervals, become zeros before dV, dK and dQ read them.  (Products that read
+          // them meanwhile only write what is dropped: dP of those rows and keys.)
+          if (guard_ds) {
+            if (hf == 1) {
+              if (it == 0 && !key_in)
+                for (int cb = 0; cb < Smem::NB; ++cb) clear_row(s.k[cb], row);
+            } else {
+              if (!mbar_wait_warp(&s.do_full, gi & 1, abort_flag, kSiteDOFull)) { ok = false; break; }
+              if (s.qvis[sb][row] == kTileN)
+                for (int cb = 0; cb < Smem::NB; ++cb) {
+                  clear_row(s.q[gi % Smem::kQStages][cb], row);
+                  clear_row(s.dout[cb], row);
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+        }
         uint32_t pk[32];  // this half's P^T, bf16 pairs
         uint32_t keepw[2] = {~0u, ~0u};  // dropout: bit q = query hf*64 + 32 cc + q kept
+        if constexpr (SCORED) {
+          // (with a cap, one copy in a loop instead of two is 6% faster where tiles differ in their way, and
+          // 3 to 6% slower where they do not)
+          const bool plain = !need_mask && linear;
+          const float kb = sg * static_cast<float>(row);
+#pragma unroll
+          for (int cc = 0; cc < 2; ++cc) {
+            uint32_t sr[32], pw[16], pg[16];
+            float largest = 0.f;  // |score|, for the cap's polynomials
+            if constexpr (CAP)
+              tmem_ld32_max_abs(t_S + lane_off + hf * 64 + cc * 32, sr, largest);
+            else
+              tmem_ld32(t_S + lane_off + hf * 64 + cc * 32, sr);
+            tmem_wait_ld();
+            const uint64_t* nlc = nl2 + hf * 32 + cc * 16;
+            if (plain && (!CAP || __all_sync(0xffffffffu, largest <= p.sc.small[0]))) {
+              scored_weights<CAP, BIAS, 0>(sr, p.sc, c2, nlc, true, slope2, kb, 0, false, nullptr, row,
+                                           pw, pg);
+            } else if (CAP && plain && __all_sync(0xffffffffu, largest <= p.sc.small[1])) {
+              scored_weights<CAP, BIAS, 1>(sr, p.sc, c2, nlc, true, slope2, kb, 0, false, nullptr, row,
+                                           pw, pg);
+            } else if (CAP && plain && __all_sync(0xffffffffu, largest <= p.sc.small[2])) {
+              scored_weights<CAP, BIAS, 2>(sr, p.sc, c2, nlc, true, slope2, kb, 0, false, nullptr, row,
+                                           pw, pg);
+            } else {
+              if constexpr (CAP) scored_cap(sr, p.sc, largest);
+              scored_weights<CAP, BIAS, 3>(sr, p.sc, c2, nlc, linear, slope2, kb,
+                                           q0 + hf * 64 + cc * 32 + off - key, need_mask,
+                                           s.qvis[sb] + hf * 64 + cc * 32, row, pw, pg);
+            }
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+              if (cc == 0) pk[e] = pg[e];
+              else pk[16 + e] = pg[e];
+            }
+            tmem_st16(t_S + lane_off + hf * 64 + cc * 16, pw);
+          }
+        } else {
 #pragma unroll
         for (int cc = 0; cc < 2; ++cc) {
           uint32_t sr[32];
-          float largest = 0.f;  // |score|, for the cap's polynomial
-          if constexpr (CAP)
-            tmem_ld32_max_abs(t_S + lane_off + hf * 64 + cc * 32, sr, largest);
-          else
-            tmem_ld32(t_S + lane_off + hf * 64 + cc * 32, sr);
+          tmem_ld32(t_S + lane_off + hf * 64 + cc * 32, sr);
           if (DROP) {
             const uint32_t bh = static_cast<uint32_t>(bz * p.Hq + h);
             uint32_t kw = 0;
@@ -748,24 +829,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tmem_wait_ld();
           uint32_t pw[16];
-          if constexpr (SCORED) {
-            const bool plain = !need_mask && linear;
-            const uint64_t* nlc = nl2 + hf * 32 + cc * 16;
-            const float kb = sg * static_cast<float>(row);
-            if (plain && (!CAP || __all_sync(0xffffffffu, largest <= p.sc.small[0])))
-              scored_weights<CAP, BIAS, 0>(sr, p.sc, c2, nlc, true, slope2, kb, 0, false, nullptr, row,
-                                           pw, pk + cc * 16);
-            else if (CAP && plain && __all_sync(0xffffffffu, largest <= p.sc.small[1]))
-              scored_weights<CAP, BIAS, 1>(sr, p.sc, c2, nlc, true, slope2, kb, 0, false, nullptr, row,
-                                           pw, pk + cc * 16);
-            else if (CAP && plain && __all_sync(0xffffffffu, largest <= p.sc.small[2]))
-              scored_weights<CAP, BIAS, 2>(sr, p.sc, c2, nlc, true, slope2, kb, 0, false, nullptr, row,
-                                           pw, pk + cc * 16);
-            else
-              scored_weights<CAP, BIAS, 3>(sr, p.sc, c2, nlc, linear, slope2, kb,
-                                           q0 + hf * 64 + cc * 32 + off - key, need_mask,
-                                           s.qvis[sb] + hf * 64 + cc * 32, row, pw, pk + cc * 16);
-          } else {
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const int qa = hf * 64 + cc * 32 + 2 * e;
@@ -786,32 +849,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               pw[e] &= ((kb & 1u) ? 0x0000ffffu : 0u) | ((kb & 2u) ? 0xffff0000u : 0u);
             }
           }
-          }
           // P columns [64 hf + 16 cc, +16) hold scores this warp already loaded
           tmem_st16(t_S + lane_off + hf * 64 + cc * 16, pw);
         }
-        if constexpr (SCORED) {
-          // Rows and keys that nothing is computed for may hold anything, and a weight of 0 does
-          // not cancel a NaN: Q and dO of queries without keys, and K of keys outside of the
-          // hull of all intervals, become zeros before dV, dK and dQ read them.  (Products that read
-          // them meanwhile only write what is dropped: scores and dP of those rows and keys.)
-          bool cleared = false;
-          if (hf == 0 && __any_sync(0xffffffffu, dead)) {
-            if (!mbar_wait_warp(&s.do_full, gi & 1, abort_flag, kSiteDOFull)) { ok = false; break; }
-            if (dead) {
-              for (int cb = 0; cb < Smem::NB; ++cb) {
-                clear_row(s.q[gi % Smem::kQStages][cb], row);
-                clear_row(s.dout[cb], row);
-              }
-            }
-            cleared = true;
-          }
-          if (hf == 1 && it == 0 && (c0 < klo || c0 + kTileN > kend)) {
-            if (!key_in)
-              for (int cb = 0; cb < Smem::NB; ++cb) clear_row(s.k[cb], row);
-            cleared = true;
-          }
-          if (cleared) fence_proxy_async_smem();
         }
         tmem_wait_st();
         tc_fence_before();
@@ -821,44 +861,49 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!mbar_wait_warp(&s.dp_full, gi & 1, abort_flag, kSiteDP)) { ok = false; break; }
         tc_fence_after();
         const uint32_t blk = ds_base + hf * (kTileN * 128) + row * 128;  // query block hf
+        auto ds_tile = [&](auto guard) {
+          constexpr bool GUARD = decltype(guard)::value;
+#pragma unroll (GUARD ? 1 : 2)
+          for (int cc = 0; cc < 2; ++cc) {
+            uint32_t dr[32];
+            tmem_ld32(t_dP + lane_off + hf * 64 + cc * 32, dr);
+            tmem_wait_ld();
+            uint32_t dw[16];
 #pragma unroll
-        for (int cc = 0; cc < 2; ++cc) {
-          uint32_t dr[32];
-          tmem_ld32(t_dP + lane_off + hf * 64 + cc * 32, dr);
-          tmem_wait_ld();
-          uint32_t dw[16];
-#pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const int qa = hf * 64 + cc * 32 + 2 * e;
-            uint64_t dp2;
-            if constexpr (SCORED) {  // (dP - D) / 2^15
-              dp2 = f2_fma(f2_pack(__uint_as_float(dr[2 * e]), __uint_as_float(dr[2 * e + 1])),
-                           f2_pack(kWeightInv, kWeightInv), nd2[qa >> 1]);
-            } else if (DROP) {  // dP of the dropped weights: keep / (1 - p) * <dO, v>
-              const uint32_t kb = keepw[cc] >> (2 * e);
-              dp2 = f2_fma(f2_pack(__uint_as_float(dr[2 * e]), __uint_as_float(dr[2 * e + 1])),
-                           f2_pack((kb & 1u) ? p.drop.scale : 0.f, (kb & 2u) ? p.drop.scale : 0.f),
-                           nd2[qa >> 1]);
-            } else {
-              dp2 = f2_add(f2_pack(__uint_as_float(dr[2 * e]), __uint_as_float(dr[2 * e + 1])),
-                           nd2[qa >> 1]);
+            for (int e = 0; e < 16; ++e) {
+              const int qa = hf * 64 + cc * 32 + 2 * e;
+              uint64_t dp2;
+              if constexpr (SCORED) {  // (dP - D) / 2^15
+                dp2 = f2_fma(f2_pack(__uint_as_float(dr[2 * e]), __uint_as_float(dr[2 * e + 1])),
+                             f2_pack(kWeightInv, kWeightInv), nd2[qa >> 1]);
+              } else if (DROP) {  // dP of the dropped weights: keep / (1 - p) * <dO, v>
+                const uint32_t kb = keepw[cc] >> (2 * e);
+                dp2 = f2_fma(f2_pack(__uint_as_float(dr[2 * e]), __uint_as_float(dr[2 * e + 1])),
+                             f2_pack((kb & 1u) ? p.drop.scale : 0.f, (kb & 2u) ? p.drop.scale : 0.f),
+                             nd2[qa >> 1]);
+              } else {
+                dp2 = f2_add(f2_pack(__uint_as_float(dr[2 * e]), __uint_as_float(dr[2 * e + 1])),
+                             nd2[qa >> 1]);
+              }
+              const uint32_t w = GUARD ? (cc ? pk[16 + e] : pk[e]) : pk[cc * 16 + e];
+              float d0, d1;
+              f2_unpack(f2_mul(SCORED ? f16x2_to_f2(w) : bf16x2_to_f2(w), dp2), d0, d1);
+              if (GUARD) {  // hidden entries: 0 whatever dP and D hold
+                if (!(w & 0xffffu)) d0 = 0.f;
+                if (!(w >> 16)) d1 = 0.f;
+              }
+              dw[e] = pack_bf16x2(d0, d1);
             }
-            float d0, d1;
-            f2_unpack(f2_mul(SCORED ? f16x2_to_f2(pk[cc * 16 + e]) : bf16x2_to_f2(pk[cc * 16 + e]),
-                             dp2), d0, d1);
-            if (SCORED && need_mask) {  // hidden entries: 0 whatever dP and D hold
-              if (!(pk[cc * 16 + e] & 0xffffu)) d0 = 0.f;
-              if (!(pk[cc * 16 + e] >> 16)) d1 = 0.f;
-            }
-            dw[e] = pack_bf16x2(d0, d1);
-          }
-          // dS^T to shared memory only: 32 queries = four 16-byte chunks of query block hf
+            // dS^T to shared memory only: 32 queries = four 16-byte chunks of query block hf
 #pragma unroll
-          for (int ch = 0; ch < 4; ++ch) {
-            const uint32_t chunk = static_cast<uint32_t>((cc * 4 + ch) ^ (row & 7));
-            st_shared_v4(blk + chunk * 16, dw[4 * ch], dw[4 * ch + 1], dw[4 * ch + 2], dw[4 * ch + 3]);
+            for (int ch = 0; ch < 4; ++ch) {
+              const uint32_t chunk = static_cast<uint32_t>((cc * 4 + ch) ^ (row & 7));
+              st_shared_v4(blk + chunk * 16, dw[4 * ch], dw[4 * ch + 1], dw[4 * ch + 2], dw[4 * ch + 3]);
+            }
           }
-        }
+        };
+        if (SCORED && guard_ds) ds_tile(std::true_type{});
+        else ds_tile(std::false_type{});
         fence_proxy_async_smem();
         tc_fence_before();
         __syncwarp();
