@@ -317,7 +317,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int i = lane; i < 16 * (D / 8); i += 32) {
             const int row = i / (D / 8);
             if (row >= n_keys)
-              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vb + chunk_at<D>(r0 + row, i % (D / 8))),
+              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(
+                               vb + chunk_at<D>(r0 + row, i % (D / 8))),
                            "r"(0)
                            : "memory");
           }
@@ -412,7 +413,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             l[u] += p0 + p1;
             const uint32_t w2 = pack_bf16x2(p0, p1);
             hi[2 * nt + u] = w2;
-            lo[2 * nt + u] = pack_bf16x2(p0 - __uint_as_float(w2 << 16), p1 - __uint_as_float(w2 & 0xffff0000u));
+            lo[2 * nt + u] = pack_bf16x2(p0 - __uint_as_float(w2 << 16),
+                                         p1 - __uint_as_float(w2 & 0xffff0000u));
           }
         }
         // ---- O += w V ----

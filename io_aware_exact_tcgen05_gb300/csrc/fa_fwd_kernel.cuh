@@ -57,7 +57,7 @@ constexpr uint32_t kTmemCols = 512;
 // wait-site ids reported in the status word
 enum : unsigned int {
   kSiteQ = 1, kSiteKFree, kSiteVFree, kSiteKFull, kSiteVFull, kSitePFull, kSiteSFull,
-  kSiteOFull, kSiteDrain
+  kSiteOFull, kSiteDrain, kSiteVRaw
 };
 
 template <int D>
@@ -80,6 +80,7 @@ struct FwdSmem {
   uint64_t o_empty[2];          // the slot's softmax warps have read O
   uint64_t s_full[2], p_full[2], o_full[2];
   uint64_t drain;  // MMA teardown after an abort
+  uint64_t v_raw[NS];  // scored modes: V of an edge tile has arrived (see edge_tile)
   uint32_t tmem_base;
   int abort_flag;
 };
@@ -287,6 +288,53 @@ __device__ __forceinline__ Unit unit_at(const ScoredFwdParams& p, int U) {
   return u;
 }
 
+// Keys of the unit's tile j (last tiles first) that no row of the unit sees may hold anything, and a weight
+// of 0 does not cancel a NaN.  Only a unit's first and last tile have such keys: V of an edge tile is
+// loaded for a helper warp, which makes zeros of those keys' values and then hands the stage on.
+// (In the softmax warps or in the MMA warp the mere presence of this cost 3 to 5%.)
+__device__ __forceinline__ bool edge_tile(const Unit& u, int j) {
+  const int c0 = (u.j0 + u.n_tiles - 1 - j) * kTileN;
+  return c0 < u.klo || c0 + kTileN > u.kend;
+}
+
+template <typename Smem>
+__device__ __forceinline__ void edge_warp(Smem& s, const ScoredFwdParams& p, int lane, int n_units) {
+  volatile int* abort_flag = &s.abort_flag;
+  int g = 0;                    // tiles before the unit, as the producer counts them
+  uint32_t uses[Smem::NS] = {};  // edge tiles each stage has held
+  for (int k = 0; k * static_cast<int>(gridDim.x) < n_units; ++k) {
+    const int G = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
+    const int U = k * G + ((k & 1) ? (G - 1 - c) : c);
+    if (U >= n_units) continue;
+    const Unit un = unit_at(p, U);
+    for (int e = 0; e < (un.n_tiles > 1 ? 2 : un.n_tiles); ++e) {
+      const int j = e == 0 ? 0 : un.n_tiles - 1;
+      if (!edge_tile(un, j)) continue;
+      const int st = (g + j) % Smem::NS;
+#pragma unroll
+      for (int i = 0; i < Smem::NS; ++i)
+        if (i == st) {
+          if (!mbar_wait_warp(&s.v_raw[i], uses[i] & 1, abort_flag, kSiteVRaw)) return;
+          ++uses[i];
+        }
+      const int c0 = (un.j0 + un.n_tiles - 1 - j) * kTileN;
+      const uint32_t v0 = smem_u32(s.v[st][0]);
+      for (int i = lane; i < kTileN * Smem::NB; i += 32) {  // box after box of 128-byte rows
+        const int key = c0 + i % kTileN;
+        if (key >= un.klo && key < un.kend) continue;
+#pragma unroll
+        for (int ch = 0; ch < 8; ++ch)
+          asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(v0 + i * 128 + ch * 16), "r"(0)
+                       : "memory");
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&s.v_full[st]);
+    }
+    g += un.n_tiles;
+  }
+}
+
 // Scores of 64 keys (columns [64 HALF, +64) of the tile) straight to weights, for a tile that
 // every row of the warp sees whole and whose distances have one sign: with a bias the exponent
 // is s * c + (slope of the sign) * jj + bm, bm = the bias of the tile's first key less the maximum.
@@ -415,9 +463,10 @@ __device__ __forceinline__ void scored_transform(uint32_t (&r)[32], const ScoreA
 
 // The softmax warps of the scored modes.  Key tiles come last first: under the causal rule the
 // tile that needs the mask is then the one that sets the maximum, and a bias that falls with the
-// distance lets the maximum stand from there on (first tiles first, steep slopes raised it in every
-// tile: 925 us instead of 541 at 2 x 16 heads x 8192 causal, d = 128).  As the plain ones, with the running maximum in units of
-// log2(e) and two ways through a tile:
+// distance lets the maximum stand from there on (first tiles first, steep slopes raised it in
+// every tile and took 1.7 times as long at 2 x 16 heads x 8192 causal, d = 128; now 455 us, without
+// a bias 430).  As the plain ones, with the running maximum in units of log2(e) and two ways through
+// a tile:
 //  * fast: every row of the warp sees the whole tile and has a maximum, its distances have one
 //    sign, and the tile's sum stays below kFastLimit: scores to weights in registers;
 //  * general: scores -> z in place in TMEM (with the mask), 32 columns at a time, the tile's
@@ -581,24 +630,6 @@ __device__ __forceinline__ void scored_softmax_warps(Smem& s, const ScoredFwdPar
           tmem_st16(t_p + cc * 16, pk);
         }
       }
-      if (t == 0 && (c0 < un.klo || c0 + kTileN > un.kend)) {
-        // Keys that no row of the unit sees may hold anything, and a weight of 0 does not cancel
-        // a NaN: their values become zeros before either slot's product reads them (slot 1's is
-        // issued after slot 0's).  The tile stays until then: slot 0 has run through every tile
-        // of the CTA, so ts + j is its number.
-        const int g = ts + j;
-        if (!mbar_wait_warp(&s.v_full[g % Smem::NS], (g / Smem::NS) & 1, abort_flag, kSiteVFull)) return;
-        const int key = c0 + row_in_tile;
-        if (key < un.klo || key >= un.kend) {
-          for (int cb = 0; cb < Smem::NB; ++cb) {
-            const uint32_t a = smem_u32(s.v[g % Smem::NS][cb]) + static_cast<uint32_t>(row_in_tile) * 128;
-#pragma unroll
-            for (int ch = 0; ch < 8; ++ch)
-              asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(a + ch * 16), "r"(0) : "memory");
-          }
-        }
-        fence_proxy_async_smem();
-      }
       if (j > 0 && __any_sync(0xffffffffu, grow)) {
         // O_t is quiescent here, as in the plain path
 #pragma unroll
@@ -700,6 +731,7 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
       mbar_init(&s.k_full[i], 1);
       mbar_init(&s.v_full[i], 1);
       mbar_init(&s.kv_free[i], 1);
+      if constexpr (SCORED) mbar_init(&s.v_raw[i], 1);
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&s.s_full[t], 1);
@@ -733,6 +765,7 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
       const uint64_t keep = policy_evict_last();
       int g = 0, uq = 0;               // tiles and Q loads issued so far
       int k_issued = 0, v_issued = 0;  // (global tile counts, for the abort drain)
+      uint32_t edges = 0, raw_parity = 0;  // stages with V of an edge tile; parity after its load
       bool ok = true;
       for (int k = 0; ok && k * static_cast<int>(gridDim.x) < n_units; ++k) {
         const int U = unit_index(k);
@@ -769,9 +802,18 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
               break;
             }
           }
-          mbar_arrive_expect_tx(&s.v_full[st], NB * kBoxBytes);
+          uint64_t* v_bar = &s.v_full[st];
+          if constexpr (SCORED) {
+            edges &= ~(1u << st);
+            if (edge_tile(un, j)) {
+              v_bar = &s.v_raw[st];
+              edges |= 1u << st;
+              raw_parity ^= 1u << st;
+            }
+          }
+          mbar_arrive_expect_tx(v_bar, NB * kBoxBytes);
           for (int cb = 0; cb < NB; ++cb)
-            tma_load_3d_hint(s.v[st][cb], &tv, &s.v_full[st], cb * 64, c0, zkv, keep);
+            tma_load_3d_hint(s.v[st][cb], &tv, v_bar, cb * 64, c0, zkv, keep);
           v_issued = g + 1;
         }
       }
@@ -780,8 +822,13 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
         if (uq > 0) mbar_drain(&s.bar_q, (uq - 1) & 1, kSiteDrain);
         for (int j = max(0, k_issued - NS); j < k_issued; ++j)
           mbar_drain(&s.k_full[j % NS], (j / NS) & 1, kSiteDrain);
-        for (int j = max(0, v_issued - NS); j < v_issued; ++j)
-          mbar_drain(&s.v_full[j % NS], (j / NS) & 1, kSiteDrain);
+        for (int j = max(0, v_issued - NS); j < v_issued; ++j) {
+          const int i = j % NS;
+          if (edges >> i & 1)
+            mbar_drain(&s.v_raw[i], (raw_parity >> i & 1) ^ 1, kSiteDrain);
+          else
+            mbar_drain(&s.v_full[i], (j / NS) & 1, kSiteDrain);
+        }
       }
     }
   } else if (warp == 9) {
@@ -876,6 +923,7 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
       scored_softmax_warps<D, MODE>(s, p, tmem, warp, lane, n_units, unit_index);
     } else {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+      if (warp == 10) edge_warp(s, p, lane, n_units);
     }
   } else {
     // ---------------------------------------------------- softmax warps --

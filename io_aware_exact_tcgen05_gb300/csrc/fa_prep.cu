@@ -342,7 +342,8 @@ __global__ void __launch_bounds__(kThreads, BACK ? kBwdCtasPerSm : kFwdCtasPerSm
     const __nv_bfloat16* w = static_cast<const __nv_bfloat16*>(p.role[i / D].w);
     const int k = i % D / (D / 4), xi = i % (D / 4) / 4, e = i % 4;
     const bool ti = xi < p.rot / 16;
-    const int ch = (k < 2 ? (ti ? 8 * xi : 16 * xi) : (ti ? p.rot / 2 + 8 * xi : 16 * xi + 8)) + 4 * (k & 1) + e;
+    const int ch = (k < 2 ? (ti ? 8 * xi : 16 * xi) : (ti ? p.rot / 2 + 8 * xi : 16 * xi + 8)) +
+                   4 * (k & 1) + e;
     weight[i / D][i % D] = w ? __bfloat162float(w[ch]) + p.w_off : 1.f;
   }
   // the lane's share of a token's angles: frequencies lane and lane + 32
