@@ -41,10 +41,6 @@
 namespace fa {
 namespace {
 
-#ifndef FC
-#define FC 3
-#define BC 2
-#endif
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 // CTAs per SM that the registers allow: the grid is one wave of them.
