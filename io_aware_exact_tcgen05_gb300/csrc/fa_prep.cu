@@ -27,8 +27,9 @@
 // left two fifths of the time to the slowest; whole tokens left a seventh to the last round.
 //
 // Measured (GB300, inputs from HBM): 2 x 8192 tokens of 16 + 2 x 16 heads, d = 128 forward 71 us (5.7 TB/s,
-// 85% of the measured copy); 3 x 2777 tokens of 28 + 2 x 4 heads with three axes backward 54 us (4.1 TB/s): the
-// chain of two reductions a step at 16 warps per SM, which is what the registers allow.
+// 85% of the measured copy); 3 x 2777 tokens of 28 + 2 x 4 heads with three axes backward 52 us (4.3 TB/s): the
+// chain of two reductions a step at 16 warps per SM, which is what the registers allow (a token's positions
+// loaded a token ahead, or the sums of dw in shared memory, changed nothing).
 #include <algorithm>
 
 #include <cuda_bf16.h>
@@ -441,24 +442,26 @@ __global__ void __launch_bounds__(kThreads, BACK ? kBwdCtasPerSm : kFwdCtasPerSm
   }
 }
 
-// dw of queries (CTA 0) and keys (CTA 1) from the CTAs' shares, 8 interleaved sums a channel.
-template <int D>
-__global__ void __launch_bounds__(8 * D) fa_prep_dw_kernel(const PrepParams p) {
-  __shared__ float red[8][D];
-  const int ch = threadIdx.x % D, part = threadIdx.x / D;
-  float* dw = p.role[blockIdx.x].dw;
-  if (!dw) return;
+// dw of queries (blockIdx.y 0) and keys (1) from the CTAs' shares: 32 channels a CTA, a warp adds every 32nd
+// share, and the warps' sums are added in order.  (Two CTAs of D channels with 8 sums each were a chain of
+// loads of 5 us.)
+__global__ void __launch_bounds__(1024) fa_prep_dw_kernel(const PrepParams p) {
+  __shared__ float red[32][33];
+  const int lane = threadIdx.x & 31, part = threadIdx.x >> 5;
+  const int ch = blockIdx.x * 32 + lane;
+  float* dw = p.role[blockIdx.y].dw;
   griddep_wait();
+  if (!dw) return;
   float sum = 0.f;
-#pragma unroll 4
-  for (int k = part; k < p.blocks; k += 8)
-    sum += p.partial[static_cast<size_t>(k) * 2 * D + blockIdx.x * D + ch];
-  red[part][ch] = sum;
+#pragma unroll 8
+  for (int k = part; k < p.blocks; k += 32)
+    sum += p.partial[static_cast<size_t>(k) * 2 * p.d + blockIdx.y * p.d + ch];
+  red[part][lane] = sum;
   __syncthreads();
   if (part == 0) {
     float t = 0.f;
 #pragma unroll
-    for (int k = 0; k < 8; ++k) t += red[k][ch];
+    for (int k = 0; k < 32; ++k) t += red[k][lane];
     dw[ch] = t;
   }
 }
@@ -487,8 +490,7 @@ cudaError_t launch_prep_bwd(const PrepParams& p, cudaStream_t stream) {
   else fa_prep_kernel<64, true><<<p.blocks, kThreads, 0, stream>>>(p);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || !(p.role[0].dw || p.role[1].dw)) return e;
-  if (p.d == 128) return launch_dependent(fa_prep_dw_kernel<128>, dim3(2), dim3(1024), 0, stream, p);
-  return launch_dependent(fa_prep_dw_kernel<64>, dim3(2), dim3(512), 0, stream, p);
+  return launch_dependent(fa_prep_dw_kernel, dim3(p.d / 32, 2), dim3(1024), 0, stream, p);
 }
 
 }  // namespace fa
