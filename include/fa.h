@@ -544,8 +544,9 @@ fa_status fa_mask_plan(const int32_t* row_lo, const int32_t* row_hi, int B, int 
  * softcap is 0 or in [2^-20, 2^20]; slopes device fp32[Hq], finite, any sign (constants: no gradient).
  * plan: fa_mask_plan of the same B, Sq, Sk; plan_bytes its size.  Rows without keys give O = 0,
  * LSE = -inf and no gradient.  What q, dout and o hold in rows without keys, and k and v in front of the
- * first and behind the last key that any row of the batch row sees, is never used.  (A NaN or infinity in
- * a key or value between them may reach every row of a 256-row block one of whose rows sees the key.)
+ * first and behind the last key that any row of the batch row sees, is never used.  A NaN in a query, or in a
+ * key or value between those, reaches the rows that see it; in a key or value, and infinities there, it may
+ * reach every row of a 256-row block one of whose rows sees the key.
  * tanh is off by at most 4e-7 of its value or 2^-22, whichever is larger.
  */
 fa_status fa_fwd_scored(const void* q, const void* k, const void* v, void* o, float* lse, int B,
@@ -569,7 +570,8 @@ size_t fa_decode_scored_workspace_size(int B, int Hq, int Hkv, int Sk_max, int d
  * fa_decode on such scores.  The query of batch row b is position n - 1, n = seqlens_k[b] (clamped
  * to [0, Sk_max]); it sees the keys [max(0, k_start[b], n - window), n) (k_start device int32[B] or
  * NULL: 0; window 0: none).  No other key is read.  Grid and workspace depend on the arguments,
- * never on the values in seqlens_k and k_start.  B * Hq must be below 2^31.
+ * never on the values in seqlens_k and k_start.  A NaN reaches the batch rows that see it and no
+ * others.  B * Hq must be below 2^31.
  */
 fa_status fa_decode_scored(const void* q, const void* k_cache, const void* v_cache, void* o,
                            float* lse, const int32_t* seqlens_k, const int32_t* k_start, int B,

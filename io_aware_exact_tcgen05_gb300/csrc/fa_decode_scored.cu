@@ -462,16 +462,15 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < kComputeWarps; ++i) M = fmaxf(M, s.red_m[i][h]);
         float L = 0.f, acc = 0.f;
-        if (M != neg_inf()) {
 #pragma unroll
-          for (int i = 0; i < kComputeWarps; ++i) {
-            const float wt = (s.red_m[i][h] == neg_inf()) ? 0.f : ex2_approx(s.red_m[i][h] - M);
-            L = fmaf(wt, s.red_l[i][h], L);
-            acc = fmaf(wt, s.red_o[i][hh][e], acc);
-          }
+        for (int i = 0; i < kComputeWarps; ++i) {
+          const float wt = (s.red_m[i][h] == neg_inf()) ? 0.f : ex2_approx(s.red_m[i][h] - M);
+          L = fmaf(wt, s.red_l[i][h], L);
+          acc = fmaf(wt, s.red_o[i][hh][e], acc);
         }
-        p.part_o[(at * p.heads + h) * D + e] = (L > 0.f) ? acc / L : 0.f;
-        if (e == 0) p.part_lse[at * p.heads + h] = (L > 0.f) ? M + __log2f(L) : neg_inf();
+        // (a NaN in a visible key makes L one, which is not 0: it reaches O and LSE)
+        p.part_o[(at * p.heads + h) * D + e] = L != 0.f ? acc / L : 0.f;
+        if (e == 0) p.part_lse[at * p.heads + h] = L != 0.f ? M + __log2f(L) : neg_inf();
       }
     }
     if (leave) break;  // every compute warp leaves together
@@ -498,18 +497,16 @@ __global__ void __launch_bounds__(D) fa_decode_scored_join(const ScoredDecodePar
     const size_t row0 = (static_cast<size_t>(span.x) + item) * p.heads + hg % p.heads;
     const int n = span.y - span.x + 1;
     for (int i = 0; i < n; ++i) M = fmaxf(M, p.part_lse[row0 + static_cast<size_t>(i) * p.heads]);
-    if (M != neg_inf()) {
 #pragma unroll 4
-      for (int i = 0; i < n; ++i) {
-        const size_t row = row0 + static_cast<size_t>(i) * p.heads;
-        const float ls = p.part_lse[row];
-        const float wt = (ls == neg_inf()) ? 0.f : ex2_approx(ls - M);
-        wsum += wt;
-        o = fmaf(wt, p.part_o[row * D + e], o);
-      }
+    for (int i = 0; i < n; ++i) {
+      const size_t row = row0 + static_cast<size_t>(i) * p.heads;
+      const float ls = p.part_lse[row];
+      const float wt = (ls == neg_inf()) ? 0.f : ex2_approx(ls - M);
+      wsum += wt;
+      o = fmaf(wt, p.part_o[row * D + e], o);
     }
   }
-  const bool live = wsum > 0.f;
+  const bool live = wsum != 0.f;  // (NaN is live)
   reinterpret_cast<__nv_bfloat16*>(p.o)[static_cast<size_t>(bh) * D + e] =
       __float2bfloat16_rn(live ? o / wsum : 0.f);
   if (p.lse && e == 0)

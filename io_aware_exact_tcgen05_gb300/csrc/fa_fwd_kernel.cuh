@@ -655,7 +655,7 @@ __device__ __forceinline__ void scored_softmax_warps(Smem& s, const ScoredFwdPar
     if (warp_aborted(abort_flag)) return;
     // ---- epilogue: O = u / lr, LSE = m ln 2 + ln l; zeros and -inf without keys ----
     {
-      const bool live = l > 0.f && !dead;
+      const bool live = l != 0.f && !dead;  // (a NaN in a visible key makes l one: it reaches O and LSE)
       const float inv = live ? 1.f / lr : 0.f;
       const bool in_range = i < un.sq;
       const size_t row = (static_cast<size_t>(un.bz) * p.Hq + h) * p.Sq + i;

@@ -56,6 +56,13 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
+// The smaller of two; NaN where one is.
+__device__ __forceinline__ float min_or_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 // cap' * tanh(a s) for any s.
 __device__ __forceinline__ float cap_any(float s, const ScoreArgs& sc) {
   const float e = ex2_approx(s * sc.two_a_log2e);
@@ -67,7 +74,7 @@ __device__ __forceinline__ float cap_any(float s, const ScoreArgs& sc) {
 __device__ __forceinline__ uint64_t cap_any2(uint64_t s2, const ScoreArgs& sc) {
   float x0, x1;
   f2_unpack(f2_mul(s2, f2_pack(sc.two_a_log2e, sc.two_a_log2e)), x0, x1);
-  const float e0 = ex2_approx(fminf(x0, 60.f)), e1 = ex2_approx(fminf(x1, 60.f));
+  const float e0 = ex2_approx(min_or_nan(x0, 60.f)), e1 = ex2_approx(min_or_nan(x1, 60.f));
   f2_unpack(f2_add(f2_pack(e0, e1), f2_pack(1.f, 1.f)), x0, x1);
   const float r = rcp_approx(x0 * x1);
   const uint64_t r2 = f2_mul(f2_pack(r, r), f2_pack(x1, x0));

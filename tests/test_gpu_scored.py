@@ -183,6 +183,63 @@ def test_what_nothing_sees_may_hold_anything(garbage, cap, bias):
         assert float(x.masked_select(dead[:, None, :, None].to(DEV)).abs().sum()) == 0.0
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("cap,bias,planned", [(0.0, False, False), (0.0, False, True), (20.0, False, True),
+                                              (0.0, True, False), (2.0, True, True)])
+@pytest.mark.parametrize("where", ["q", "k", "v"])
+def test_a_nan_reaches_the_rows_that_see_it(where, cap, bias, planned, d):
+    # and none outside of their 256-row blocks: row 300 (of q), or key 300 (of k or v) under the causal rule
+    B, H, S, at = 1, 2, 700, 300
+    t = workloads.random_qkv(B, H, H, S, S, d, seed=5, with_dout=True)
+    sl = _slopes(H) if bias else None
+    lo, hi = so.row_bounds(B, S, S, True)
+    r = so.attend(*(to_np(t[n]) for n in ("q", "k", "v")), 0.09, lo, hi, cap, None if sl is None else sl.double().numpy(),
+                  to_np(t["dout"]), bounds=True)
+    t[where][:, :, at] = float("nan")
+    q, k, v, do = (t[n].to(DEV) for n in ("q", "k", "v", "dout"))
+    plan = fa.fa_mask_plan(*fa.fa_row_bounds(B, S, S, True), S) if planned else None
+    how = dict(softcap=cap, slopes=None if sl is None else sl.to(DEV), plan=plan)
+    o, lse = fa.fa_fwd_scored(q, k, v, not planned, 0.09, **how)
+    dq, dk, dv = fa.fa_bwd_scored(q, k, v, o, do, lse, not planned, 0.09, **how)
+    torch.cuda.synchronize()
+    _status_ok()
+    sees = slice(at, at + 1) if where == "q" else slice(at, S)
+    assert bool(o[:, :, sees].isnan().all())
+    assert bool(dq[:, :, sees].isnan().all())
+    if where != "v":
+        assert bool(lse[:, :, sees].isnan().all())
+        assert bool(dk[:, :, :at + 1].isnan().all())
+    else:
+        _within(lse, r["lse"], r["tol_lse"], "LSE")
+    for part in [slice(0, 256)] + ([slice(512, S)] if where == "q" else []):
+        _within(o[:, :, part], r["o"][:, :, part], r["tol_o"][:, :, part], "O")
+        _within(dq[:, :, part], r["dq"][:, :, part], r["tol_dq"][:, :, part], "dq")
+        _within(lse[:, :, part], r["lse"][:, :, part], r["tol_lse"][:, :, part], "LSE")
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", [(4, 2, 64), (16, 1, 128)])
+@pytest.mark.parametrize("cap", [0.0, 2.0])
+def test_decode_a_nan_reaches_the_rows_that_see_it(cap, Hq, Hkv, d):
+    lens, room, at = [700, 300, 301, 699, 1], 700, 300
+    B = len(lens)
+    t = workloads.random_qkv(B, Hq, Hkv, 1, room, d, seed=6)
+    q, k, v = (t[n].to(DEV) for n in ("q", "k", "v"))
+    for where in (k, v):
+        clean = fa.fa_decode_scored(q, k, v, _i32(lens), 0.1, cap), fa.fa_decode_scored(q, k, v, _i32(lens), 0.1, cap, window=390)
+        kept = where[:, :, at].clone()
+        where[:, :, at] = float("nan")
+        dirty = fa.fa_decode_scored(q, k, v, _i32(lens), 0.1, cap), fa.fa_decode_scored(q, k, v, _i32(lens), 0.1, cap, window=390)
+        where[:, :, at] = kept
+        for (o0, l0), (o, lse), windowed in zip(clean, dirty, (False, True)):
+            for b, n in enumerate(lens):
+                if n > at and not (windowed and n - 390 > at):
+                    assert bool(o[b].isnan().all()), (n, windowed)
+                    assert bool(lse[b].isnan().all()) == (where is k), (n, windowed)
+                else:
+                    assert torch.equal(o[b], o0[b]) and torch.equal(lse[b], l0[b]), (n, windowed)
+    _status_ok()
+
+
 def test_plain_scores_equal_the_plain_kernels():
     # without cap, bias and plan these are fa_fwd's sums over the same tiles: equal up to the order of tiles
     t = workloads.random_qkv(2, 4, 2, 300, 300, 128, seed=9)
