@@ -24,7 +24,7 @@
 // divided by the sum of the *rounded* weights (what the PV product used), l
 // (fp32, unrounded) gives the LSE.
 //
-// Method: as fa_fwd.cu ("Flash Attention" history page 1.2, 1.3, 2.1, 2.3;
+// Method: as fa_fwd_kernel.cuh ("Flash Attention" history page 1.2, 1.3, 2.1, 2.3;
 // FlashAttention_01 page, online-softmax derivation and masking rule).
 #include <algorithm>
 
