@@ -181,6 +181,13 @@ struct Unit {
   bool rows, active1;    // rows: slot 0 has rows at all
 };
 
+// In the scored modes a slot takes part in the rounds (last tiles first) whose tile its rows see.
+struct ScoredUnit : Unit {
+  int begin0, end0, begin1, end1;  // rounds of slots 0 and 1
+  __device__ __forceinline__ int begin(int t) const { return t ? begin1 : begin0; }
+  __device__ __forceinline__ int end(int t) const { return t ? end1 : end0; }
+};
+
 __device__ __forceinline__ Unit unit_at(const FwdParams& p, int U) {
   Unit u;
   const int rbu = p.n_rbu - 1 - U / p.units_per_rbu;
@@ -233,13 +240,13 @@ __device__ __forceinline__ Unit unit_at(const FwdParams& p, int U) {
 
 // The scored modes' units: with a plan the row blocks of a batch row come in the plan's order
 // (most key tiles first), and a unit visits the tiles of its rows' hull.
-__device__ __forceinline__ Unit unit_at(const ScoredFwdParams& p, int U) {
-  Unit u;
+__device__ __forceinline__ ScoredUnit unit_at(const ScoredFwdParams& p, int U) {
+  ScoredUnit u;
   const MaskPlan& m = p.sc.plan;
   const int rank = U / p.units_per_rbu;
   const int w = U % p.units_per_rbu;
   int rbu = p.n_rbu - 1 - rank;
-  int lo = 0, hi = p.Sk;
+  int lo0 = 0, hi0 = p.Sk, lo1 = 0, hi1 = p.Sk;  // hulls of the slots' rows
   if (p.pack_heads) {
     const int hpairs = p.Hq >> 1;
     u.b = w / hpairs;
@@ -248,8 +255,8 @@ __device__ __forceinline__ Unit unit_at(const ScoredFwdParams& p, int U) {
     if (m.rows) {
       rbu = __ldg(m.by_q1 + static_cast<size_t>(u.b) * m.nq + rank);
       const int4 r = __ldg(m.qt + static_cast<size_t>(u.b) * m.nq + rbu);
-      lo = r.x;
-      hi = r.y;
+      lo0 = lo1 = r.x;
+      hi0 = hi1 = r.y;
     }
     u.r0 = u.r1 = rbu * kTileM;
   } else {
@@ -259,9 +266,13 @@ __device__ __forceinline__ Unit unit_at(const ScoredFwdParams& p, int U) {
       rbu = __ldg(m.by_q2 + static_cast<size_t>(u.b) * m.np + rank);
       const int4* qt = m.qt + static_cast<size_t>(u.b) * m.nq + 2 * rbu;
       const int4 r = __ldg(qt);
-      const int4 r1 = 2 * rbu + 1 < m.nq ? __ldg(qt + 1) : make_int4(0, 0, 0, 0);
-      lo = r.y == 0 ? r1.x : r1.y == 0 ? r.x : min(r.x, r1.x);
-      hi = max(r.y, r1.y);
+      lo0 = r.x;
+      hi0 = r.y;
+      if (2 * rbu + 1 < m.nq) {
+        const int4 r1 = __ldg(qt + 1);
+        lo1 = r1.x;
+        hi1 = r1.y;
+      }
     }
     u.r0 = rbu * 2 * kTileM;
     u.r1 = u.r0 + kTileM;
@@ -274,16 +285,26 @@ __device__ __forceinline__ Unit unit_at(const ScoredFwdParams& p, int U) {
   u.active1 = u.r1 < u.sq;
   u.hk = u.h0 / p.group;
   if (p.causal) {
-    const int last_row = min((u.active1 ? u.r1 : u.r0) + kTileM - 1, u.sq - 1);
-    hi = min(hi, last_row + u.off + 1);
+    hi0 = min(hi0, min(u.r0 + kTileM, u.sq) + u.off);
+    hi1 = min(hi1, min(u.r1 + kTileM, u.sq) + u.off);
   }
-  u.klo = lo;
-  u.kend = hi;
-  u.j0 = 0;
-  u.n_tiles = 0;
-  if (hi > lo) {
-    u.j0 = lo / kTileN;
-    u.n_tiles = (hi + kTileN - 1) / kTileN - u.j0;
+  if (hi0 <= lo0) lo0 = 0x7fffffff, hi0 = 0;
+  if (hi1 <= lo1 || !u.active1) lo1 = 0x7fffffff, hi1 = 0;
+  u.klo = min(lo0, lo1);
+  u.kend = max(hi0, hi1);
+  u.j0 = u.n_tiles = u.begin0 = u.end0 = u.begin1 = u.end1 = 0;
+  if (u.kend > 0) {
+    const int end = (u.kend + kTileN - 1) / kTileN;
+    u.j0 = u.klo / kTileN;
+    u.n_tiles = end - u.j0;
+    if (hi0 > 0) {
+      u.begin0 = end - (hi0 + kTileN - 1) / kTileN;
+      u.end0 = end - lo0 / kTileN;
+    }
+    if (hi1 > 0) {
+      u.begin1 = end - (hi1 + kTileN - 1) / kTileN;
+      u.end1 = end - lo1 / kTileN;
+    }
   }
   return u;
 }
@@ -490,9 +511,9 @@ __device__ __forceinline__ void scored_softmax_warps(Smem& s, const ScoredFwdPar
   for (int k = 0; k * static_cast<int>(gridDim.x) < n_units; ++k) {
     const int U = unit_index(k);
     if (U >= n_units) continue;
-    const Unit un = unit_at(p, U);
+    const ScoredUnit un = unit_at(p, U);
     if (t == 1 && !un.active1) continue;
-    const int n_tiles = un.n_tiles;
+    const int first_j = un.begin(t), n_tiles = un.end(t) - first_j;
     const int i = (t == 0 ? un.r0 : un.r1) + row_in_tile;
     const int h = (t == 0) ? un.h0 : un.h1;
     const int pos = i + un.off;
@@ -518,7 +539,7 @@ __device__ __forceinline__ void scored_softmax_warps(Smem& s, const ScoredFwdPar
     for (int j = 0; j < n_tiles; ++j) {
       if (!mbar_wait_warp(&s.s_full[t], (ts + j) & 1, abort_flag, kSiteSFull)) return;
       tc_fence_after();
-      const int c0 = (un.j0 + n_tiles - 1 - j) * kTileN;
+      const int c0 = (un.j0 + un.n_tiles - 1 - first_j - j) * kTileN;
       const int p_rel = pos - c0;
       bool general = __any_sync(0xffffffffu, c0 < lo || c0 + kTileN > hi || m == neg_inf());
       float sg = 0.f, bm = -m;
@@ -852,7 +873,7 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
     for (int k = 0; ok && k * static_cast<int>(gridDim.x) < n_units; ++k) {
       const int U = unit_index(k);
       if (U >= n_units) continue;
-      const Unit un = unit_at(p, U);
+      const auto un = unit_at(p, U);
       if (un.n_tiles == 0) continue;
       const int n = un.n_tiles;
       const int nslots = un.active1 ? 2 : 1;
@@ -867,16 +888,28 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
           ok = false;
           break;
         }
+        if constexpr (SCORED) {  // every V stage in turn, whichever slots take part
+          if (j > 0 && !mbar_wait_warp(&s.v_full[gv % NS], (gv / NS) & 1, abort_flag, kSiteVFull)) {
+            ok = false;
+            break;
+          }
+        }
         const uint64_t kd = desc_add(kd0, static_cast<uint32_t>(gk % NS) * kStage);
         const uint64_t vd = desc_add(vd0, static_cast<uint32_t>(((gv % NS) + NS) % NS) * kStage);
         for (int t = 0; t < nslots; ++t) {
           const uint32_t t_s = tmem + t * kTileN;
-          if (j > 0) {
+          int jt = j, n_t = n;  // round of the slot, and how many it has
+          if constexpr (SCORED) {
+            jt = j - un.begin(t);
+            n_t = un.end(t) - un.begin(t);
+            if (jt < 0 || jt > n_t || n_t == 0) continue;
+          }
+          if (jt > 0) {
             // O_t += P_t(j-1) V_{j-1}; P_t lives in the last 64 columns of S_t
-            if (!mbar_wait_warp(&s.p_full[t], (ts[t] + j - 1) & 1, abort_flag, kSitePFull) ||
-                (t == 0 &&
+            if (!mbar_wait_warp(&s.p_full[t], (ts[t] + jt - 1) & 1, abort_flag, kSitePFull) ||
+                (!SCORED && t == 0 &&
                  !mbar_wait_warp(&s.v_full[gv % NS], (gv / NS) & 1, abort_flag, kSiteVFull)) ||
-                (j == 1 && us[t] > 0 &&
+                (jt == 1 && us[t] > 0 &&
                  !mbar_wait_warp(&s.o_empty[t], (us[t] - 1) & 1, abort_flag, kSiteOFull))) {
               ok = false;
               break;
@@ -884,12 +917,12 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
             tc_fence_after();
             const uint32_t t_o = tmem + 2 * kTileN + t * D;
             const uint32_t t_p = t_s + kTileN / 2;
-            mma_ts_warp(t_o, t_p, vd, idesc_pv, j > 1 ? 1u : 0u);
+            mma_ts_warp(t_o, t_p, vd, idesc_pv, jt > 1 ? 1u : 0u);
 #pragma unroll
             for (int kk = 1; kk < kTileN / 16; ++kk)
               mma_ts_warp(t_o, t_p + kk * 8, desc_add(vd, kk * 16 * 128), idesc_pv, 1u);
           }
-          if (j < n) {
+          if (jt < n_t) {
             // S_t = Q_t K_j^T
             const uint64_t qd = t ? qd1 : qd0;
 #pragma unroll
@@ -908,8 +941,10 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
       }
       g += n;
       for (int t = 0; t < nslots; ++t) {
-        ts[t] += n;
-        ++us[t];
+        int n_t = n;
+        if constexpr (SCORED) n_t = un.end(t) - un.begin(t);
+        ts[t] += n_t;
+        us[t] += n_t > 0;
       }
     }
     if (warp_aborted(abort_flag)) {
