@@ -199,8 +199,8 @@ struct ScoredBwdParams : BwdParams {
 template <int MODE>
 using BwdParamsOf = std::conditional_t<(MODE & kBwdScored) != 0, ScoredBwdParams, BwdParams>;
 
-// The scored modes' units: with a plan, the key tiles of each batch row in the plan's order and
-// the query tiles that may see them.
+// The scored modes' units: with a plan, the key tiles in the plan's order (over all batch rows, or
+// where units go group by group within each) and the query tiles that may see them.
 __device__ __forceinline__ BwdUnit bwd_unit_at(const ScoredBwdParams& p, int U) {
   BwdUnit u;
   const MaskPlan& m = p.sc.plan;
@@ -224,7 +224,14 @@ __device__ __forceinline__ BwdUnit bwd_unit_at(const ScoredBwdParams& p, int U) 
   u.qt_lo = 0;
   int qt_end = (p.Sq + kTileM - 1) / kTileM;
   if (m.rows) {
-    kt = __ldg(m.by_k + static_cast<size_t>(u.b) * m.nk + kt);
+    if (cnt == BH) {  // one group: in order over all batch rows
+      kt = __ldg(m.by_k + U / p.Hkv);
+      u.hk = U % p.Hkv;
+      u.b = u.bz = kt / m.nk;
+    } else {
+      kt = __ldg(m.by_k_row + static_cast<size_t>(u.b) * m.nk + kt);
+    }
+    kt -= u.b * m.nk;
     const int4 q = __ldg(m.kt + static_cast<size_t>(u.b) * m.nk + kt);
     u.qt_lo = q.x;
     qt_end = q.y;

@@ -238,32 +238,37 @@ __device__ __forceinline__ Unit unit_at(const FwdParams& p, int U) {
   return u;
 }
 
-// The scored modes' units: with a plan the row blocks of a batch row come in the plan's order
-// (most key tiles first), and a unit visits the tiles of its rows' hull.
+// The scored modes' units: with a plan the row blocks come in the plan's order (most key tiles
+// first), and a slot visits the tiles of its rows' hull.
 __device__ __forceinline__ ScoredUnit unit_at(const ScoredFwdParams& p, int U) {
   ScoredUnit u;
   const MaskPlan& m = p.sc.plan;
-  const int rank = U / p.units_per_rbu;
-  const int w = U % p.units_per_rbu;
-  int rbu = p.n_rbu - 1 - rank;
+  const int heads = p.pack_heads ? p.Hq >> 1 : p.Hq;  // units of a batch row and row block
+  int w, rbu;
+  if (m.rows) {
+    const int tile = __ldg((p.pack_heads ? m.by_q1 : m.by_q2) + U / heads);
+    w = U % heads;
+    u.b = tile / p.n_rbu;
+    rbu = tile - u.b * p.n_rbu;
+  } else {
+    w = U % p.units_per_rbu;
+    rbu = p.n_rbu - 1 - U / p.units_per_rbu;
+    u.b = w / heads;
+    w -= u.b * heads;
+  }
   int lo0 = 0, hi0 = p.Sk, lo1 = 0, hi1 = p.Sk;  // hulls of the slots' rows
   if (p.pack_heads) {
-    const int hpairs = p.Hq >> 1;
-    u.b = w / hpairs;
-    u.h0 = 2 * (w % hpairs);
+    u.h0 = 2 * w;
     u.h1 = u.h0 + 1;
     if (m.rows) {
-      rbu = __ldg(m.by_q1 + static_cast<size_t>(u.b) * m.nq + rank);
       const int4 r = __ldg(m.qt + static_cast<size_t>(u.b) * m.nq + rbu);
       lo0 = lo1 = r.x;
       hi0 = hi1 = r.y;
     }
     u.r0 = u.r1 = rbu * kTileM;
   } else {
-    u.b = w / p.Hq;
-    u.h0 = u.h1 = w % p.Hq;
+    u.h0 = u.h1 = w;
     if (m.rows) {
-      rbu = __ldg(m.by_q2 + static_cast<size_t>(u.b) * m.np + rank);
       const int4* qt = m.qt + static_cast<size_t>(u.b) * m.nq + 2 * rbu;
       const int4 r = __ldg(qt);
       lo0 = r.x;

@@ -7,6 +7,8 @@
 //
 // Every kernel here is bound by its launch and a short chain of dependent loads: the work
 // is 8 bytes a row.
+#include <algorithm>
+
 #include <cuda_runtime.h>
 
 #include "fa_internal.h"
@@ -56,6 +58,10 @@ __global__ void __launch_bounds__(256) fa_row_bounds_kernel(const RowBoundsParam
   p.hi[idx] = static_cast<int>(hi);
 }
 
+__device__ __forceinline__ int key_tiles(int4 r) {
+  return r.y > r.x ? (r.y + 127) / 128 - r.x / 128 : 0;
+}
+
 // The intervals clamped to [0, Sk], and their extremes over each 128-row tile.
 __global__ void __launch_bounds__(128)
     fa_plan_rows_kernel(const int32_t* lo, const int32_t* hi, int Sq, int Sk, const MaskPlan m) {
@@ -89,12 +95,15 @@ __global__ void __launch_bounds__(128)
                        max(max(red[0][2], red[1][2]), max(red[2][2], red[3][2])),
                        min(min(red[0][3], red[1][3]), min(red[2][3], red[3][3])));
     if (r.y == 0) r = make_int4(0, 0, 0, 0);
-    const_cast<int4*>(m.qt)[static_cast<size_t>(b) * m.nq + t] = r;
+    const size_t at = static_cast<size_t>(b) * m.nq + t;
+    const_cast<int4*>(m.qt)[at] = r;
+    const_cast<int*>(m.work)[at] = key_tiles(r);
   }
   griddep_launch_dependents();
 }
 
-// First and end query tile whose hull of intervals meets each key tile, and the hull of theirs.
+// First and end query tile whose hull of intervals meets each key tile, and the hull of theirs;
+// the work of pairs of query tiles and of key tiles.
 __global__ void __launch_bounds__(128) fa_plan_keys_kernel(const MaskPlan m) {
   const int b = blockIdx.y;
   const int kt = blockIdx.x * 128 + threadIdx.x;
@@ -112,43 +121,42 @@ __global__ void __launch_bounds__(128) fa_plan_keys_kernel(const MaskPlan m) {
         hi = max(hi, r.y);
       }
     }
-    const_cast<int4*>(m.kt)[static_cast<size_t>(b) * m.nk + kt] = make_int4(first, end, lo, hi);
+    const size_t at = static_cast<size_t>(b) * m.nk + kt;
+    const_cast<int4*>(m.kt)[at] = make_int4(first, end, lo, hi);
+    const_cast<int*>(m.work)[static_cast<size_t>(m.B) * (m.nq + m.np) + at] = end - first;
   }
+  if (kt < m.np)
+    const_cast<int*>(m.work)[static_cast<size_t>(m.B) * m.nq + static_cast<size_t>(b) * m.np + kt] =
+        key_tiles(qt[2 * kt]) + (2 * kt + 1 < m.nq ? key_tiles(qt[2 * kt + 1]) : 0);
   griddep_launch_dependents();
 }
 
-__device__ __forceinline__ int key_tiles(int lo, int hi) {
-  return hi > lo ? (hi + 127) / 128 - lo / 128 : 0;
-}
-
-// The tiles of each batch row in the order of their work, by rank: the number of tiles with more
-// (or as much, and a lower number).  Causal masks give late query tiles and early key tiles more
-// work, so equal query tiles rank late ones first.
-__global__ void __launch_bounds__(128) fa_plan_order_kernel(const MaskPlan m) {
-  const int b = blockIdx.y, kind = blockIdx.z;
-  const int n = kind == 0 ? m.nq : kind == 1 ? m.np : m.nk;
-  const int t = blockIdx.x * 128 + threadIdx.x;
+// The order of the tiles by rank: the number of tiles with more work (or as much, before them in
+// ties).  A warp per tile.  Over all batch rows together: with an order for each, taken side by side, the
+// slowest of 152 CTAs had 10% more than the mean where the rows' masks differ.  Causal masks
+// give late query tiles and early key tiles more work, so ties of query tiles rank late ones first.
+__global__ void __launch_bounds__(256) fa_plan_order_kernel(const MaskPlan m) {
+  const int kind = blockIdx.y;  // query tiles, pairs of them, key tiles, key tiles of a batch row
+  const int per_row = kind == 0 ? m.nq : kind == 1 ? m.np : m.nk;
+  const int n = m.B * per_row;
+  const long long e = blockIdx.x * 8ll + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
   griddep_wait();
-  if (t >= n) return;
-  const int4* qt = m.qt + static_cast<size_t>(b) * m.nq;
-  const int4* kt = m.kt + static_cast<size_t>(b) * m.nk;
-  auto load = [&](int x) {
-    if (kind == 2) return kt[x].y - kt[x].x;
-    if (kind == 0) return key_tiles(qt[x].x, qt[x].y);
-    const int4 r = qt[2 * x];
-    const int4 s = 2 * x + 1 < m.nq ? qt[2 * x + 1] : make_int4(0, 0, 0, 0);
-    if (s.y == 0) return key_tiles(r.x, r.y);
-    if (r.y == 0) return key_tiles(s.x, s.y);
-    return key_tiles(min(r.x, s.x), max(r.y, s.y));
-  };
-  const int mine = load(t);
+  if (e >= n) return;
+  const int tile = static_cast<int>(e);
+  const long long skip = kind == 0 ? 0 : 1ll * m.B * (kind == 1 ? m.nq : m.nq + m.np);
+  const int* work = m.work + skip;
+  const int first = kind == 3 ? tile / per_row * per_row : 0, end = kind == 3 ? first + per_row : n;
+  const int mine = work[tile];
   int rank = 0;
-  for (int x = 0; x < n; ++x) {
-    const int l = load(x);
-    rank += l > mine || (l == mine && (kind == 2 ? x < t : x > t));
+#pragma unroll 4
+  for (int x = first + lane; x < end; x += 32) {
+    const int l = work[x];
+    rank += l > mine || (l == mine && (kind >= 2 ? x < tile : x > tile));
   }
-  int* out = const_cast<int*>(kind == 0 ? m.by_q1 : kind == 1 ? m.by_q2 : m.by_k);
-  out[static_cast<size_t>(b) * n + rank] = t;
+  rank = __reduce_add_sync(0xffffffffu, rank);
+  int* out = const_cast<int*>(kind == 0 ? m.by_q1 : kind == 1 ? m.by_q2 : kind == 2 ? m.by_k : m.by_k_row);
+  if (lane == 0) out[first + rank] = tile;
 }
 
 }  // namespace
@@ -164,10 +172,12 @@ cudaError_t launch_mask_plan(const int32_t* lo, const int32_t* hi, int B, int Sq
   fa_plan_rows_kernel<<<dim3(m.nq, B), 128, 0, stream>>>(lo, hi, Sq, Sk, m);
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess)
-    e = launch_dependent(fa_plan_keys_kernel, dim3((m.nk + 127) / 128, B), dim3(128), 0, stream, m);
-  const int most = m.nq > m.nk ? m.nq : m.nk;
+    e = launch_dependent(fa_plan_keys_kernel, dim3((std::max(m.nk, m.np) + 127) / 128, B), dim3(128), 0,
+                         stream, m);
+  const long long most = 1ll * B * std::max(m.nq, m.nk);
   if (e == cudaSuccess)
-    e = launch_dependent(fa_plan_order_kernel, dim3((most + 127) / 128, B, 3), dim3(128), 0, stream, m);
+    e = launch_dependent(fa_plan_order_kernel, dim3(static_cast<unsigned int>((most + 7) / 8), 4),
+                         dim3(256), 0, stream, m);
   return e;
 }
 

@@ -20,21 +20,25 @@ struct MaskPlan {
   const int2* rows;  // [B][Sq]  lo, hi of each row; (0, 0) without keys
   const int4* kt;    // [B][nk]  first and end query tile that may see the 128-key tile, and the hull
                      //          of their rows' intervals
-  const int* by_q1;  // [B][nq]  query tiles, most key tiles first
-  const int* by_q2;  // [B][np]  pairs of query tiles, likewise
-  const int* by_k;   // [B][nk]  key tiles, most query tiles first
-  int nq, np, nk;
+  // tiles (batch row * tiles of a row + tile) in the order of their work, most first
+  const int* by_q1;    // [B * nq]  query tiles by key tiles
+  const int* by_q2;    // [B * np]  pairs of query tiles, likewise
+  const int* by_k;     // [B * nk]  key tiles by query tiles
+  const int* by_k_row; // [B][nk]   the same within each batch row
+  const int* work;     // [B * (nq + np + nk)]  what they are ordered by
+  int B, nq, np, nk;
 };
 
-// 32-bit words of a plan: qt, kt, rows, by_q1, by_q2, by_k.
+// 32-bit words of a plan: qt, kt, rows, by_q1, by_q2, by_k, by_k_row, work.
 inline size_t mask_plan_words(long long B, long long Sq, long long Sk) {
   const long long nq = (Sq + 127) / 128, np = (nq + 1) / 2, nk = (Sk + 127) / 128;
-  return static_cast<size_t>(B * (4 * nq + 4 * nk + 2 * Sq + nq + np + nk));
+  return static_cast<size_t>(B * (4 * nq + 4 * nk + 2 * Sq + 2 * (nq + np + nk) + nk));
 }
 
 inline MaskPlan mask_plan_view(const void* base, long long B, long long Sq, long long Sk) {
   MaskPlan m{};
   if (!base) return m;
+  m.B = static_cast<int>(B);
   m.nq = static_cast<int>((Sq + 127) / 128);
   m.np = (m.nq + 1) / 2;
   m.nk = static_cast<int>((Sk + 127) / 128);
@@ -45,6 +49,8 @@ inline MaskPlan mask_plan_view(const void* base, long long B, long long Sq, long
   m.by_q1 = w + 4 * B * (m.nq + m.nk) + 2 * B * Sq;
   m.by_q2 = m.by_q1 + B * m.nq;
   m.by_k = m.by_q2 + B * m.np;
+  m.by_k_row = m.by_k + B * m.nk;
+  m.work = m.by_k_row + B * m.nk;
   return m;
 }
 
