@@ -103,38 +103,48 @@ __global__ void __launch_bounds__(128)
 }
 
 // First and end query tile whose hull of intervals meets each key tile, and the hull of theirs;
-// the work of pairs of query tiles and of key tiles.
-__global__ void __launch_bounds__(128) fa_plan_keys_kernel(const MaskPlan m) {
-  const int b = blockIdx.y;
-  const int kt = blockIdx.x * 128 + threadIdx.x;
+// the work of key tiles and of pairs of query tiles.  A warp per key tile.
+__global__ void __launch_bounds__(256) fa_plan_keys_kernel(const MaskPlan m) {
+  const int b = blockIdx.y, lane = threadIdx.x & 31;
+  const int kt = blockIdx.x * 8 + (threadIdx.x >> 5);
   griddep_wait();
   const int4* qt = m.qt + static_cast<size_t>(b) * m.nq;
   const int c0 = kt * 128;
-  int first = 0, end = 0, lo = 0x7fffffff, hi = 0;
   if (kt < m.nk) {
-    for (int t = 0; t < m.nq; ++t) {
+    int first = 0x7fffffff, end = 0, lo = 0x7fffffff, hi = 0;
+#pragma unroll 4
+    for (int t = lane; t < m.nq; t += 32) {
       const int4 r = qt[t];
       if (r.x < c0 + 128 && r.y > c0) {
-        if (end == 0) first = t;
+        first = min(first, t);
         end = t + 1;
         lo = min(lo, r.x);
         hi = max(hi, r.y);
       }
     }
-    const size_t at = static_cast<size_t>(b) * m.nk + kt;
-    const_cast<int4*>(m.kt)[at] = make_int4(first, end, lo, hi);
-    const_cast<int*>(m.work)[static_cast<size_t>(m.B) * (m.nq + m.np) + at] = end - first;
+    first = __reduce_min_sync(0xffffffffu, first);
+    end = __reduce_max_sync(0xffffffffu, end);
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    if (end == 0) first = 0;
+    if (lane == 0) {
+      const size_t at = static_cast<size_t>(b) * m.nk + kt;
+      const_cast<int4*>(m.kt)[at] = make_int4(first, end, lo, hi);
+      const_cast<int*>(m.work)[static_cast<size_t>(m.B) * (m.nq + m.np) + at] = end - first;
+    }
   }
-  if (kt < m.np)
+  if (kt < m.np && lane == 0)
     const_cast<int*>(m.work)[static_cast<size_t>(m.B) * m.nq + static_cast<size_t>(b) * m.np + kt] =
         key_tiles(qt[2 * kt]) + (2 * kt + 1 < m.nq ? key_tiles(qt[2 * kt + 1]) : 0);
   griddep_launch_dependents();
 }
 
 // The order of the tiles by rank: the number of tiles with more work (or as much, before them in
-// ties).  A warp per tile.  Over all batch rows together: with an order for each, taken side by side, the
-// slowest of 152 CTAs had 10% more than the mean where the rows' masks differ.  Causal masks
-// give late query tiles and early key tiles more work, so ties of query tiles rank late ones first.
+// ties).  A warp per tile.  Over all batch rows together: with an order for each, taken side by
+// side, the slowest of 152 CTAs had 10% more than the mean where the rows' masks differ.  Causal
+// masks give late query tiles and early key tiles more work, so ties of query tiles rank late ones
+// first.  (5 us with the two kernels before at 2 x 8192 rows, 0.1 ms at 10^6; 8 tiles a warp, which
+// share its loads: 6 us, 0.18 ms.)
 __global__ void __launch_bounds__(256) fa_plan_order_kernel(const MaskPlan m) {
   const int kind = blockIdx.y;  // query tiles, pairs of them, key tiles, key tiles of a batch row
   const int per_row = kind == 0 ? m.nq : kind == 1 ? m.np : m.nk;
@@ -148,14 +158,18 @@ __global__ void __launch_bounds__(256) fa_plan_order_kernel(const MaskPlan m) {
   const int* work = m.work + skip;
   const int first = kind == 3 ? tile / per_row * per_row : 0, end = kind == 3 ? first + per_row : n;
   const int mine = work[tile];
+  // least work that counts in front of the tile and behind it
+  const int front = kind >= 2 ? mine : mine + 1, behind = kind >= 2 ? mine + 1 : mine;
   int rank = 0;
 #pragma unroll 4
-  for (int x = first + lane; x < end; x += 32) {
-    const int l = work[x];
-    rank += l > mine || (l == mine && (kind >= 2 ? x < tile : x > tile));
-  }
+  for (int x = first + lane; x < tile; x += 32) rank += work[x] >= front;
+#pragma unroll 4
+  for (int x = tile + 1 + lane; x < end; x += 32) rank += work[x] >= behind;
   rank = __reduce_add_sync(0xffffffffu, rank);
-  int* out = const_cast<int*>(kind == 0 ? m.by_q1 : kind == 1 ? m.by_q2 : kind == 2 ? m.by_k : m.by_k_row);
+  int* out = const_cast<int*>(kind == 0   ? m.by_q1
+                              : kind == 1 ? m.by_q2
+                              : kind == 2 ? m.by_k
+                                          : m.by_k_row);
   if (lane == 0) out[first + rank] = tile;
 }
 
@@ -172,8 +186,8 @@ cudaError_t launch_mask_plan(const int32_t* lo, const int32_t* hi, int B, int Sq
   fa_plan_rows_kernel<<<dim3(m.nq, B), 128, 0, stream>>>(lo, hi, Sq, Sk, m);
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess)
-    e = launch_dependent(fa_plan_keys_kernel, dim3((std::max(m.nk, m.np) + 127) / 128, B), dim3(128), 0,
-                         stream, m);
+    e = launch_dependent(fa_plan_keys_kernel, dim3((std::max(m.nk, m.np) + 7) / 8, B), dim3(256), 0, stream,
+                         m);
   const long long most = 1ll * B * std::max(m.nq, m.nk);
   if (e == cudaSuccess)
     e = launch_dependent(fa_plan_order_kernel, dim3(static_cast<unsigned int>((most + 7) / 8), 4),
