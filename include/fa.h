@@ -563,7 +563,7 @@ fa_status fa_bwd_scored(const void* q, const void* k, const void* v, const void*
                         float softcap, const float* slopes, const void* plan, size_t plan_bytes,
                         void* workspace, size_t workspace_bytes, cudaStream_t stream);
 
-/* Bytes of device workspace fa_decode_scored needs. */
+/* Bytes of device workspace fa_decode_scored needs; 0: none, and its workspace may be NULL. */
 size_t fa_decode_scored_workspace_size(int B, int Hq, int Hkv, int Sk_max, int d, int window);
 
 /*

@@ -956,11 +956,14 @@ def fa_decode_scored(q, k_cache, v_cache, seqlens_k, scale: float, softcap: floa
     window = _int(window, "window")
     o = _out(o, "o", (B, Hq, 1, d), _BF16, dev, stream)
     lse = _out(lse, "lse", (B, Hq), _F32, dev, stream)
-    workspace = _workspace(workspace, _decode_scored_bytes(B, Hq, Hkv, Sk_max, d, window), dev, stream)
+    nbytes = _decode_scored_bytes(B, Hq, Hkv, Sk_max, d, window)
+    if nbytes or workspace is not None:
+        workspace = _workspace(workspace, nbytes, dev, stream)
+        nbytes = workspace.nbytes
     st = lib.fa_decode_scored(q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), o.data_ptr(),
                               lse.data_ptr(), seqlens_k.data_ptr(), _ptr(k_start), B, Hq, Hkv,
                               Sk_max, d, float(scale), float(softcap), _ptr(slopes), window,
-                              workspace.data_ptr(), workspace.nbytes, _stream(stream))
+                              _ptr(workspace), nbytes, _stream(stream))
     _check(st, "fa_decode_scored")
     return o, lse
 

@@ -561,10 +561,12 @@ fa_status fa_decode_scored(const void* q, const void* k_cache, const void* v_cac
   fa::ScoredDecodeParams p{};
   FA_TRY(make_score(scale, softcap, slopes, nullptr, 0, B, 1, Sk_max, &p.sc));
   const size_t need = fa_decode_scored_workspace_size(B, Hq, Hkv, Sk_max, d, window);
-  if (!workspace || workspace_bytes < need)
-    return fail(FA_ERR_WORKSPACE, "decode workspace needs %zu bytes, got %zu", need,
-                workspace ? workspace_bytes : size_t(0));
-  FA_TRY(check_ptr(workspace, "workspace"));
+  if (need > 0) {
+    if (!workspace || workspace_bytes < need)
+      return fail(FA_ERR_WORKSPACE, "decode workspace needs %zu bytes, got %zu", need,
+                  workspace ? workspace_bytes : size_t(0));
+    FA_TRY(check_ptr(workspace, "workspace"));
+  }
   p.q = q;
   p.k = k_cache;
   p.v = v_cache;
@@ -580,6 +582,7 @@ fa_status fa_decode_scored(const void* q, const void* k_cache, const void* v_cac
   p.Sk_max = Sk_max;
   p.group = Hq / Hkv;
   const fa::DecodeScoredPlan plan = fa::decode_scored_plan(B, Hq, Hkv, Sk_max, d, window);
+  p.direct = plan.direct;
   p.heads = plan.heads;
   p.subs = plan.subs;
   char* base = static_cast<char*>(workspace);

@@ -16,9 +16,13 @@
 // into the next item while the others write the last one's state away, so the ring never drains.
 //
 // Measured (GB300, graph, d = 128): 32 requests of 8 KV heads with 4 query heads each, windows of 4096 keys
-// 84 us (6.3 TB/s, 94% of the measured copy; the CUDA cores in splits of 512 keys took 164, in equal stretches
+// 84 to 85 us (6.2 TB/s, 93% of the measured copy; the CUDA cores in splits of 512 keys took 164, in equal stretches
 // 107), the same without a window, 1k to 32k keys, 330 us (6.9 TB/s; fa_decode 355); 8 query heads a KV
 // head 101 us (fa_decode 239).
+//
+// Where items are short and at most two per SM (kDirectItems), each is one CTA's, which writes the results
+// itself: one launch, no workspace and no line to sum up (16 requests of 512 keys with 8 KV heads 7.8 us
+// against 14.3).
 //
 // The state of an item's stretch goes to slot (CTA + item), which no other stretch has: along the
 // line one of the two grows with every stretch.  The join adds an item's states by the rescale rule.
@@ -137,6 +141,23 @@ __device__ __forceinline__ void pass(const ScoredDecodeParams& p, Walk& w, int n
   }
 }
 
+// Query heads of an item: the first, and how many.
+__device__ __forceinline__ int2 heads_of(const ScoredDecodeParams& p, const Walk& w) {
+  const int n_hsub = p.subs / p.Hkv;
+  const int hk = w.sub / n_hsub, h_in = (w.sub - hk * n_hsub) * p.heads;
+  return make_int2(hk * p.group + h_in, min(p.heads, p.group - h_in));
+}
+
+// O = 0, LSE = -inf of an item without keys.
+template <int D>
+__device__ __forceinline__ void write_empty(const ScoredDecodeParams& p, const Walk& w) {
+  const int2 hq = heads_of(p, w);
+  const size_t row = static_cast<size_t>(w.b) * p.Hq + hq.x;
+  for (int i = threadIdx.x; i < hq.y * D; i += kThreads)
+    reinterpret_cast<__nv_bfloat16*>(p.o)[row * D + i] = __float2bfloat16_rn(0.f);
+  if (p.lse && static_cast<int>(threadIdx.x) < hq.y) p.lse[row + threadIdx.x] = neg_inf();
+}
+
 // One vote and barrier of the compute warps.
 __device__ __forceinline__ bool compute_any(bool x) {
   uint32_t r;
@@ -169,63 +190,77 @@ __global__ void __launch_bounds__(kThreads, 1)
     s.first_b = p.B;
     fence_barrier_init();
   }
-  // ---- the line: stages of every batch row, summed kThreads rows at a time; twice (unless the
-  //      rows fit one time), since the CTA's stretch follows from the total
-  long long before = 0;  // stages (of one item a row) of the rows so far
-  int mine = 0;          // stages of this thread's row, and of all up to it
-  long long upto = 0;
-  auto sum_rows = [&](int b0) {
-    const int b = b0 + static_cast<int>(threadIdx.x);
-    mine = b < p.B ? stages_of<D>(visible_keys(p, b)) : 0;
-    long long sum = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long up = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += up;
-    }
-    __syncthreads();  // the last time's sums have been read
-    if (lane == 31) s.scan[warp] = sum;
-    __syncthreads();
-    long long base = 0, all = 0;
-#pragma unroll
-    for (int i = 0; i < kThreads / 32; ++i) {
-      if (i < warp) base += s.scan[i];
-      all += s.scan[i];
-    }
-    upto = before + base + sum;
-    before += all;
-  };
-  for (int b0 = 0; b0 < p.B; b0 += kThreads) sum_rows(b0);
-  const long long total = before * p.subs;
-  const long long share = total / gridDim.x, extra = total - share * gridDim.x, c = blockIdx.x;
-  const long long from = c * share + min(c, extra), to = from + share + (c < extra ? 1 : 0);
-  if (from == to) return;  // (CTA-uniform) nothing for this CTA
-  auto find = [&](int b0) {
-    const long long lo = (upto - mine) * p.subs;
-    if (mine > 0 && from >= lo && from < upto * p.subs) {
-      s.first_b = b0 + static_cast<int>(threadIdx.x);
-      s.before = lo;
-    }
-  };
-  if (p.B <= kThreads) {
-    find(0);
-  } else {
-    before = 0;
-    for (int b0 = 0; b0 < p.B; b0 += kThreads) {
-      sum_rows(b0);
-      find(b0);
-    }
-  }
-  __syncthreads();
   Walk w;
-  w.b = s.first_b;
-  w.seen = visible_keys(p, w.b);
-  w.n_stages = stages_of<D>(w.seen);
-  w.left = to - from;
-  {
-    const long long r = from - s.before;
-    w.sub = static_cast<int>(r / w.n_stages);
-    w.stage = static_cast<int>(r - static_cast<long long>(w.sub) * w.n_stages);
+  if (p.direct) {
+    w.b = static_cast<int>(blockIdx.x) / p.subs;
+    w.sub = static_cast<int>(blockIdx.x) - w.b * p.subs;
+    w.seen = visible_keys(p, w.b);
+    w.n_stages = stages_of<D>(w.seen);
+    w.stage = 0;
+    w.left = w.n_stages;
+    __syncthreads();
+    if (w.left == 0) {  // (CTA-uniform)
+      write_empty<D>(p, w);
+      return;
+    }
+  } else {
+    // ---- the line: stages of every batch row, summed kThreads rows at a time; twice (unless the
+    //      rows fit one time), since the CTA's stretch follows from the total
+    long long before = 0;  // stages (of one item a row) of the rows so far
+    int mine = 0;          // stages of this thread's row, and of all up to it
+    long long upto = 0;
+    auto sum_rows = [&](int b0) {
+      const int b = b0 + static_cast<int>(threadIdx.x);
+      mine = b < p.B ? stages_of<D>(visible_keys(p, b)) : 0;
+      long long sum = mine;
+  #pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long up = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += up;
+      }
+      __syncthreads();  // the last time's sums have been read
+      if (lane == 31) s.scan[warp] = sum;
+      __syncthreads();
+      long long base = 0, all = 0;
+  #pragma unroll
+      for (int i = 0; i < kThreads / 32; ++i) {
+        if (i < warp) base += s.scan[i];
+        all += s.scan[i];
+      }
+      upto = before + base + sum;
+      before += all;
+    };
+    for (int b0 = 0; b0 < p.B; b0 += kThreads) sum_rows(b0);
+    const long long total = before * p.subs;
+    const long long share = total / gridDim.x, extra = total - share * gridDim.x, c = blockIdx.x;
+    const long long from = c * share + min(c, extra), to = from + share + (c < extra ? 1 : 0);
+    if (from == to) return;  // (CTA-uniform) nothing for this CTA
+    auto find = [&](int b0) {
+      const long long lo = (upto - mine) * p.subs;
+      if (mine > 0 && from >= lo && from < upto * p.subs) {
+        s.first_b = b0 + static_cast<int>(threadIdx.x);
+        s.before = lo;
+      }
+    };
+    if (p.B <= kThreads) {
+      find(0);
+    } else {
+      before = 0;
+      for (int b0 = 0; b0 < p.B; b0 += kThreads) {
+        sum_rows(b0);
+        find(b0);
+      }
+    }
+    __syncthreads();
+    w.b = s.first_b;
+    w.seen = visible_keys(p, w.b);
+    w.n_stages = stages_of<D>(w.seen);
+    w.left = to - from;
+    {
+      const long long r = from - s.before;
+      w.sub = static_cast<int>(r / w.n_stages);
+      w.stage = static_cast<int>(r - static_cast<long long>(w.sub) * w.n_stages);
+    }
   }
   volatile int* abort_flag = &s.abort_flag;
   const int n_hsub = p.subs / p.Hkv;
@@ -265,33 +300,38 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   // --------------------------------------------------------------- compute --
   const int hr = lane >> 2, kc = lane & 3;  // this lane's heads hr, hr + 8; keys 2 kc, 2 kc + 1 (+ 8)
-  int g = 0;
-  bool ok = true;
-  while (w.left > 0) {
-    const int n = static_cast<int>(min(w.left, static_cast<long long>(w.n_stages - w.stage)));
-    const int hk = w.sub / n_hsub;
-    const int h_in = (w.sub - hk * n_hsub) * p.heads;  // first head of the item in its group
-    const int hq0 = hk * p.group + h_in;
-    const int n_heads = min(p.heads, p.group - h_in);
-    // queries as the first product's rows; heads that are not there are 0
-    uint32_t qa[D / 16][4];
+  // Queries as the first product's rows (heads that are not there are 0) and the bias per head of an
+  // item: loaded before the last item's state is written, which hides their latency.
+  uint32_t qa[D / 16][4];
+  float slope2[HALVES];
+  auto load_queries = [&](const Walk& at) {
+    const int2 hq = heads_of(p, at);
 #pragma unroll
     for (int half = 0; half < 2; ++half) {
       const int h = hr + 8 * half;
       const uint32_t* row = reinterpret_cast<const uint32_t*>(p.q) +
-                            (static_cast<size_t>(w.b) * p.Hq + hq0 + h) * (D / 2);
+                            (static_cast<size_t>(at.b) * p.Hq + hq.x + h) * (D / 2);
 #pragma unroll
       for (int ks = 0; ks < D / 16; ++ks) {
-        const bool have = half < HALVES && h < n_heads;
+        const bool have = half < HALVES && h < hq.y;
         qa[ks][half] = have ? __ldg(row + ks * 8 + kc) : 0u;
         qa[ks][half + 2] = have ? __ldg(row + ks * 8 + 4 + kc) : 0u;
       }
     }
-    float slope2[HALVES], m[HALVES], l[HALVES];  // per head: bias, running max of z, denominator
+#pragma unroll
+    for (int u = 0; u < HALVES; ++u)
+      slope2[u] = p.sc.slopes && hr + 8 * u < hq.y
+                      ? __ldg(p.sc.slopes + hq.x + hr + 8 * u) * 1.4426950408889634f : 0.f;
+  };
+  load_queries(w);
+  int g = 0;
+  bool ok = true;
+  while (w.left > 0) {
+    const int n = static_cast<int>(min(w.left, static_cast<long long>(w.n_stages - w.stage)));
+    const int hq0 = heads_of(p, w).x, n_heads = heads_of(p, w).y;
+    float m[HALVES], l[HALVES];  // per head: running max of z, denominator
 #pragma unroll
     for (int u = 0; u < HALVES; ++u) {
-      slope2[u] = p.sc.slopes && hr + 8 * u < n_heads
-                      ? __ldg(p.sc.slopes + hq0 + hr + 8 * u) * 1.4426950408889634f : 0.f;
       m[u] = neg_inf();
       l[u] = 0.f;
     }
@@ -431,10 +471,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&s.empty[slot]);
     }
+    Walk next = w;
+    pass<D>(p, next, n);
+    if (next.left > 0) load_queries(next);
     // ---- the warps' states, 8 heads at a time, to the stretch's slot ----
     const int item = w.b * p.subs + w.sub;
     const size_t at = static_cast<size_t>(blockIdx.x) + item;
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 0 && !p.direct) {
       if (w.stage == 0) p.span[item].x = blockIdx.x;
       if (w.stage + n == w.n_stages) p.span[item].y = blockIdx.x;
     }
@@ -469,12 +512,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           acc = fmaf(wt, s.red_o[i][hh][e], acc);
         }
         // (a NaN in a visible key makes L one, which is not 0: it reaches O and LSE)
-        p.part_o[(at * p.heads + h) * D + e] = L != 0.f ? acc / L : 0.f;
-        if (e == 0) p.part_lse[at * p.heads + h] = L != 0.f ? M + __log2f(L) : neg_inf();
+        const float out = L != 0.f ? acc / L : 0.f, lse2 = L != 0.f ? M + __log2f(L) : neg_inf();
+        if (p.direct) {
+          const size_t row = static_cast<size_t>(w.b) * p.Hq + hq0 + h;
+          reinterpret_cast<__nv_bfloat16*>(p.o)[row * D + e] = __float2bfloat16_rn(out);
+          if (p.lse && e == 0) p.lse[row] = lse2 * 0.69314718055994530942f;
+        } else {
+          p.part_o[(at * p.heads + h) * D + e] = out;
+          if (e == 0) p.part_lse[at * p.heads + h] = lse2;
+        }
       }
     }
     if (leave) break;  // every compute warp leaves together
-    pass<D>(p, w, n);
+    w = next;
     if (w.left > 0 && compute_any(*abort_flag)) break;  // the sums have been read
   }
   griddep_launch_dependents();
@@ -534,11 +584,14 @@ cudaError_t launch_d(const CUtensorMap& tk, const CUtensorMap& tv, const ScoredD
                      int ctas, cudaStream_t stream) {
   cudaError_t e = p.heads <= 8 ? launch_dh<D, 1>(tk, tv, p, ctas, stream)
                                : launch_dh<D, 2>(tk, tv, p, ctas, stream);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || p.direct) return e;
   return launch_dependent(fa_decode_scored_join<D>, dim3(p.B * p.Hq), dim3(D), 0, stream, p);
 }
 
 constexpr int kMaxCtas = 256;  // one per SM, and what the workspace has slots for
+// Items that are one CTA's each.  8 to 304 items of 1 or 2 stages took 4.4 to 10.9 us and in a line 6.8 to 14.7; 32 to
+// 304 items of up to 8 stages 7 to 28 and 8 to 32; fewer items of 4 stages 7.6 and 7.0; more items 5% more.
+constexpr int kDirectItems = 304, kDirectStages = 8, kDirectFewStages = 2, kDirectMany = 32;
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
@@ -551,6 +604,13 @@ DecodeScoredPlan decode_scored_plan(int B, int Hq, int Hkv, int Sk_max, int d, i
   r.subs = Hkv * ((group + r.heads - 1) / r.heads);
   const long long keys = window > 0 ? std::min(window, Sk_max) : Sk_max;
   const long long items = static_cast<long long>(B) * r.subs;
+  const int stage = d == 128 ? kStageKeys<128> : kStageKeys<64>;
+  const long long stages = (keys + stage - 1) / stage;
+  if (items <= kDirectItems && stages <= (items >= kDirectMany ? kDirectStages : kDirectFewStages)) {
+    r.direct = true;
+    r.ctas = static_cast<int>(items);
+    return r;
+  }
   const long long line = items * ((keys + 127) / 128);
   r.ctas = static_cast<int>(std::min<long long>(line, kMaxCtas));
   r.slots = static_cast<size_t>(items + r.ctas);
@@ -567,7 +627,7 @@ cudaError_t launch_decode_scored(int d, const CUtensorMap& tk, const CUtensorMap
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  const int ctas = std::min(plan.ctas, n_sm);
+  const int ctas = plan.direct ? plan.ctas : std::min(plan.ctas, n_sm);
   return d == 128 ? launch_d<128>(tk, tv, p, ctas, stream) : launch_d<64>(tk, tv, p, ctas, stream);
 }
 

@@ -88,12 +88,14 @@ struct ScoredDecodeParams : DecodeParams {
   bool capped;
   int heads;               // query heads of a work item (up to 16 of one KV head)
   int subs;                // work items of a batch row
+  bool direct;             // a CTA per item, which writes the results
   int2* span;              // [B * subs]: first and last CTA of each item
   ScoreArgs sc;
 };
 
 // Workspace: span, then per (CTA, item) slot the partial outputs and their log2-sums.
 struct DecodeScoredPlan {
+  bool direct;  // needs none
   int heads, subs, ctas;
   size_t slots, span_bytes, o_bytes, lse_bytes;
 };

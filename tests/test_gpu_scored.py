@@ -312,6 +312,12 @@ DECODE = [
     (2, 24, 2, 64, 2000, [2000, 1999], 513, [1900, 0], 2.0, False),
     (2, 4, 4, 128, 9000, [9000, 4321], 4096, None, 30.0, True),
     (3, 2, 2, 64, 300, [400, -5, 300], 0, [-7, 0, 1000], 10.0, False),   # clamped lengths and starts
+    # short items, each one block's
+    (12, 12, 4, 128, 1024, [1024, 0, 1, 127, 128, 129, 1023, 500, 384, 2, 0, 700], 0, None, 8.0, True),
+    (12, 12, 4, 128, 1024, [1024, 0, 1, 127, 128, 129, 1023, 500, 384, 2, 0, 700], 300, [0, 0, 1, 120] + [3] * 8, 0.0, True),
+    (5, 40, 2, 64, 500, [500, 256, 257, 0, 77], 0, [499, 0, 256, 0, 80], 3.0, True),
+    (19, 16, 16, 64, 1500, [79 * i for i in range(19)], 0, None, 20.0, False),
+    (3, 8, 8, 128, 5000, [5000, 130, 4099], 200, None, 2.0, True),
 ]
 
 

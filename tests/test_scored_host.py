@@ -175,7 +175,9 @@ def test_scored_attention_refuses_before_any_device_call(lib):
     assert dec(Hkv=3) == fa.FA_ERR_INVALID_ARG
     assert dec(window=-1) == fa.FA_ERR_INVALID_ARG
     assert dec(k_start=18) == fa.FA_ERR_INVALID_ARG
-    assert dec(nws=64) == fa.FA_ERR_WORKSPACE
+    assert dec(Sk=1000, nws=64) == dec(Sk=1000, ws=0) == fa.FA_ERR_WORKSPACE
+    assert fa.fa_decode_scored_workspace_size(2, 4, 2, 100, 128) == 0 < fa.fa_decode_scored_workspace_size(2, 4, 2, 1000, 128)
+    assert fa.fa_decode_scored_workspace_size(2, 4, 2, 1000, 128, 256) == 0  # a short window
     assert dec(cap=float("nan")) == fa.FA_ERR_INVALID_ARG
     assert dec(B=1 << 29, Sk=1, nws=1 << 60) == fa.FA_ERR_INVALID_ARG  # B x Hq past 32 bits
     assert fa.fa_decode_scored_workspace_size(0, 1, 1, 8, 64) == 0
