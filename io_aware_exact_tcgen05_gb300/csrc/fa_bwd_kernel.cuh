@@ -196,6 +196,10 @@ enum : int { kBwdPlain = 0, kBwdDropout = 2, kBwdCap = 4, kBwdBias = 8, kBwdScor
 struct ScoredBwdParams : BwdParams {
   ScoreArgs sc;
 };
+// Threads of a mode.  The scored modes fill the fourth warpgroup up, so that its registers can go to
+// the drain warps (setmaxnreg): 128 x (128 + 128 + 200 + 56) = the 512 x 128 of the launch.
+template <int MODE>
+constexpr int kThreadsOf = (MODE & kBwdScored) != 0 ? 512 : kThreads;
 template <int MODE>
 using BwdParamsOf = std::conditional_t<(MODE & kBwdScored) != 0, ScoredBwdParams, BwdParams>;
 
@@ -382,7 +386,7 @@ __device__ __forceinline__ void scored_weights(const uint32_t (&sr)[32], const S
 
 // ------------------------------------------------------------------ main --
 template <int D, int MODE>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
     fa_bwd_main(const __grid_constant__ CUtensorMap tq, const __grid_constant__ CUtensorMap tk,
                 const __grid_constant__ CUtensorMap tv, const __grid_constant__ CUtensorMap tdo,
                 const __grid_constant__ CUtensorMap tdq, const BwdParamsOf<MODE> p) {
@@ -452,6 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = &s.abort_flag;
 
   if (warp == kWarpProducer) {
+    if constexpr (SCORED) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     // ------------------------------------------------------ TMA producer --
     // Q/dO stages follow an iteration counter that runs across the CTA's
     // units; a unit's K/V load waits until the previous unit's last MMA has
@@ -517,6 +522,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
   } else if (warp == kWarpMma) {
+    if constexpr (SCORED) asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
     // ------------------------------------------------------- MMA issuer --
     // The whole warp runs this loop (warp-uniform control flow and operands);
     // one elected lane issues each MMA and commit.  Per-tile barrier phases
@@ -972,7 +978,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         ++uk;
       }
     }
+  } else if (SCORED && warp > kWarpMma) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
   } else if (warp < 12) {
+    if constexpr (SCORED) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
     // --------------------------------------------- dQ drain (warps 8-11) --
     // Each warp moves its 32 query rows of dQ from TMEM to global memory with
     // TMA reduce-adds through its own 8 KB of staging (two 32x32 fp32 boxes,
@@ -1010,24 +1019,35 @@ __global__ void __launch_bounds__(kThreads, 1)
           break;
         }
         tc_fence_after();
-        uint32_t r0[32], r1[32];
+        uint32_t r0[32], r1[32], r2[32], r3[32];
         tmem_ld32(t_dP + lane_off, r0);
         tmem_ld32(t_dP + lane_off + 32, r1);
+        if constexpr (SCORED && D == 128) {  // the whole row, in the registers of the idle warps
+          tmem_ld32(t_dP + lane_off + 64, r2);
+          tmem_ld32(t_dP + lane_off + 96, r3);
+        }
         tmem_wait_ld();
+        if constexpr (SCORED) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s.dq_empty);
+        }
         // the previous tile's reduces must have read the staging (waiting at
         // the end of that tile instead measured slower)
         if (lane == 0) bulk_wait_read0();
         __syncwarp();
         stage_64(r0, r1);
-        if constexpr (D == 128) {
-          tmem_ld32(t_dP + lane_off + 64, r0);
-          tmem_ld32(t_dP + lane_off + 96, r1);
-          tmem_wait_ld();
+        if constexpr (!SCORED) {
+          if constexpr (D == 128) {
+            tmem_ld32(t_dP + lane_off + 64, r2);
+            tmem_ld32(t_dP + lane_off + 96, r3);
+            tmem_wait_ld();
+          }
+          // dQ is out of TMEM: dP^T of the next tile may reuse the columns
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s.dq_empty);
         }
-        // dQ is out of TMEM: dP^T of the next tile may reuse the columns
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s.dq_empty);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) {
@@ -1038,7 +1058,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if constexpr (D == 128) {
           if (lane == 0) bulk_wait_read0();
           __syncwarp();
-          stage_64(r0, r1);
+          stage_64(r2, r3);
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
@@ -1121,7 +1141,7 @@ cudaError_t launch_bwd_mode(const CUtensorMap& tq, const CUtensorMap& tk, const 
   }
   if (grid > 0) {  // packed sequences that all lack keys: dQ stays zero
     hook_before(stream);
-    fa_bwd_main<D, MODE><<<grid, kThreads, smem, stream>>>(tq, tk, tv, tdo, tdq, pu);
+    fa_bwd_main<D, MODE><<<grid, kThreadsOf<MODE>, smem, stream>>>(tq, tk, tv, tdo, tdq, pu);
     hook_after(stream);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
