@@ -197,7 +197,9 @@ struct ScoredBwdParams : BwdParams {
   ScoreArgs sc;
 };
 // Threads of a mode.  The scored modes fill the fourth warpgroup up, so that its registers can go to
-// the drain warps (setmaxnreg): 128 x (128 + 128 + 200 + 56) = the 512 x 128 of the launch.
+// the compute and drain warps (setmaxnreg): 128 x (144 + 144 + 168 + 56) = the 512 x 128 of the launch.
+// (2 x 16 heads x 8192, documents and bias: 650 us with 128 each, 636 with 200 for the drain warps
+// alone, 595 so; capped scores past the polynomials 1570 with 136 and 184, 1445 so.)
 template <int MODE>
 constexpr int kThreadsOf = (MODE & kBwdScored) != 0 ? 512 : kThreads;
 template <int MODE>
@@ -652,6 +654,7 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
       }
     }
   } else if (warp < 8) {
+    if constexpr (SCORED) asm volatile("setmaxnreg.inc.sync.aligned.u32 144;");
     // ---------------------------------------------------- compute warps --
     const int grp = warp & 3;           // TMEM lane group
     const int hf = warp >> 2;           // query columns [64 hf, 64 hf + 64)
@@ -981,7 +984,7 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
   } else if (SCORED && warp > kWarpMma) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
   } else if (warp < 12) {
-    if constexpr (SCORED) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+    if constexpr (SCORED) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
     // --------------------------------------------- dQ drain (warps 8-11) --
     // Each warp moves its 32 query rows of dQ from TMEM to global memory with
     // TMA reduce-adds through its own 8 KB of staging (two 32x32 fp32 boxes,
