@@ -56,7 +56,8 @@
 // thread; warps w and w+4 share the lanes of group w and split the 128 query
 // columns, so P and dS need no cross-warp exchange), warps 8-11 drain dQ (one
 // query row per thread, 8 KB of staging each), warp 12 TMA producer, warp 13
-// MMA issuer and TMEM owner.
+// MMA issuer and TMEM owner.  (Scored modes, 512 threads: warps 14 and 15 lend
+// their registers.)
 #pragma once
 
 #include <algorithm>

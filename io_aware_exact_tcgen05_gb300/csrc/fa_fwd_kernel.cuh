@@ -26,7 +26,8 @@
 //
 // Warp roles (320 threads): warps 0-3 softmax of slot 0, warps 4-7 softmax of
 // slot 1 (a warp may only touch TMEM lanes 32*(warp%4) .. +31, which are the
-// rows it owns), warp 8 TMA producer, warp 9 MMA issuer and TMEM owner.
+// rows it owns), warp 8 TMA producer, warp 9 MMA issuer and TMEM owner.  (Scored
+// modes, 384 threads: warp 10 clears values that no row sees, warp 11 lends its registers.)
 //
 // The kernel is persistent: one CTA per SM walks a fixed sequence of work
 // units (the heavy-first list, taken in alternating directions block by
@@ -490,8 +491,8 @@ __device__ __forceinline__ void scored_transform(uint32_t (&r)[32], const ScoreA
 // The softmax warps of the scored modes.  Key tiles come last first: under the causal rule the
 // tile that needs the mask is then the one that sets the maximum, and a bias that falls with the
 // distance lets the maximum stand from there on (first tiles first, steep slopes raised it in
-// every tile and took 1.7 times as long at 2 x 16 heads x 8192 causal, d = 128; now 455 us, without
-// a bias 430).  As the plain ones, with the running maximum in units of log2(e) and two ways through
+// every tile and took 1.7 times as long at 2 x 16 heads x 8192 causal, d = 128; now 437 us, without
+// a bias 425).  As the plain ones, with the running maximum in units of log2(e) and two ways through
 // a tile:
 //  * fast: every row of the warp sees the whole tile and has a maximum, its distances have one
 //    sign, and the tile's sum stays below kFastLimit: scores to weights in registers;
