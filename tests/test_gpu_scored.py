@@ -118,6 +118,63 @@ def test_masks(mask, score):
         _run(B, Hq, Hkv, Sq, Sk, d, causal, cap, _slopes(Hq) if bias else None, window, cu, prefix, seed=11)
 
 
+@pytest.mark.parametrize("Hq,Hkv,d,cap,bias", [(1, 1, 64, 0.0, False), (3, 3, 128, 9.0, True), (4, 2, 64, 9.0, False)])
+@pytest.mark.parametrize("causal", [False, True])
+def test_intervals_that_differ_from_tile_to_tile(causal, Hq, Hkv, d, cap, bias):
+    # the caller's own intervals, one for each 128 rows: far apart within a pair of tiles, in both orders, one or
+    # both without keys, an edge inside a tile; with the causal rule of the call on top
+    B, S = 2, 900
+    tiles = [[(0, 100), (700, 900), (700, 900), (0, 100), (0, 0), (128, 256), (5, 6), (9, 3)],
+             [(0, 0), (5, 5), (0, 900), (899, 900), (127, 129), (255, 257), (300, 300), (0, 1)]]
+    lo, hi = np.zeros((B, S), np.int64), np.zeros((B, S), np.int64)
+    for b in range(B):
+        for i in range(S):
+            lo[b, i], hi[b, i] = tiles[b][i // 128]
+    lo[1, 300], hi[1, 300] = -50, 5000  # clamped
+    t = workloads.random_qkv(B, Hq, Hkv, S, S, d, seed=21, with_dout=True)
+    q, k, v, do = (t[n].to(DEV) for n in ("q", "k", "v", "dout"))
+    plan = fa.fa_mask_plan(_i32(lo.tolist()), _i32(hi.tolist()), S)
+    sl = _slopes(Hq, 0.1) if bias else None
+    how = dict(softcap=cap, slopes=None if sl is None else sl.to(DEV), plan=plan)
+    o, lse = fa.fa_fwd_scored(q, k, v, causal, 0.1, **how)
+    g = fa.fa_bwd_scored(q, k, v, o, do, lse, causal, 0.1, **how)
+    torch.cuda.synchronize()
+    _status_ok()
+    lo, hi = np.maximum(lo, 0), np.minimum(hi, S)
+    if causal:
+        hi = np.minimum(hi, np.arange(S) + 1)
+    r = so.attend(*(to_np(t[n]) for n in ("q", "k", "v")), 0.1, lo, hi, cap, None if sl is None else sl.double().numpy(),
+                  to_np(t["dout"]), bounds=True)
+    _within(o, r["o"], r["tol_o"], "O")
+    _within(lse, r["lse"], r["tol_lse"], "LSE")
+    for n, x in zip(("dq", "dk", "dv"), g):
+        _within(x, r[n], r["tol_" + n], n)
+
+
+def test_batch_rows_of_very_different_work_in_one_plan():
+    # tiles go by their work over all batch rows together: each batch row as if it were alone
+    B, S, H, d = 40, 384, 2, 64
+    rng = np.random.RandomState(4)
+    lo = np.sort(rng.randint(0, S, (B, S)), axis=1) * (rng.rand(B, 1) < 0.5)
+    hi = np.minimum(S, lo + rng.randint(0, S, (B, 1)))
+    t = workloads.random_qkv(B, H, H, S, S, d, seed=22, with_dout=True)
+    q, k, v, do = (t[n].to(DEV) for n in ("q", "k", "v", "dout"))
+    lo, hi = _i32(lo.tolist()), _i32(hi.tolist())
+    plan = fa.fa_mask_plan(lo, hi, S)
+    o, lse = fa.fa_fwd_scored(q, k, v, False, 0.125, softcap=8.0, plan=plan)
+    dq, dk, dv = fa.fa_bwd_scored(q, k, v, o, do, lse, False, 0.125, softcap=8.0, plan=plan)
+    for b in range(0, B, 3):
+        one = [x[b:b + 1].contiguous() for x in (q, k, v)]
+        p1 = fa.fa_mask_plan(lo[b:b + 1].contiguous(), hi[b:b + 1].contiguous(), S)
+        o1, l1 = fa.fa_fwd_scored(*one, False, 0.125, softcap=8.0, plan=p1)
+        g1 = fa.fa_bwd_scored(*one, o1, do[b:b + 1].contiguous(), l1, False, 0.125, softcap=8.0, plan=p1)
+        assert torch.equal(o[b], o1[0]) and torch.equal(lse[b], l1[0])
+        assert torch.equal(dk[b], g1[1][0]) and torch.equal(dv[b], g1[2][0])
+        # dQ is added in any order: fp32 sums of at most 3 tiles, then one rounding to bf16
+        assert ((dq[b].float() - g1[0][0].float()).abs() <= 2.0 ** -7 * dq[b].float().abs() + 1e-6).all()
+    _status_ok()
+
+
 def test_steep_and_negative_slopes_and_scale_zero():
     steep = torch.tensor([40.0, -0.05, 0.0, 1e-4])
     _run(1, 4, 4, 300, 300, 128, True, 0.0, steep, planned=False)

@@ -218,6 +218,41 @@ def test_scores_that_overflow_the_running_maximum_and_come_back():
         _within(lse, r["lse"], r["tol_lse"], "LSE")
 
 
+@pytest.mark.parametrize("B,H,S,planned", [(2, 2, 65536, True), (8, 2, 16384, True), (2, 2, 65536, False)])
+def test_backward_in_groups_that_fit_the_l2_cache(B, H, S, planned):
+    # the gradients' accumulators exceed twice the L2: heads go group by group, in alternating order of work
+    d = 128
+    g = torch.Generator(device=DEV).manual_seed(3)
+    q, k, v, do = (torch.randn(B, H, S, d, device=DEV, dtype=BF, generator=g) for _ in range(4))
+    if not planned:  # the causal rule alone, over fewer keys than queries, to keep it short
+        k, v = k[:, :, :1024].contiguous(), v[:, :, :1024].contiguous()
+    Sk = k.shape[2]
+    cu = torch.arange(0, B * S + 1, 1000, dtype=torch.int32, device=DEV)
+    cu[-1] = B * S
+
+    def run(rows, heads):
+        x = [y[rows, heads].contiguous() for y in (q, k, v, do)]
+        plan = None
+        if planned:
+            plan = fa.fa_mask_plan(lo[rows].contiguous(), hi[rows].contiguous(), Sk)
+        o, lse = fa.fa_fwd_scored(*x[:3], not planned, 0.09, softcap=20.0, plan=plan)
+        return (o, lse) + fa.fa_bwd_scored(*x[:3], o, x[3], lse, not planned, 0.09, softcap=20.0, plan=plan)
+
+    if planned:
+        lo, hi = fa.fa_row_bounds(B, S, Sk, True, window=300, cu_docs=cu)
+    every = run(slice(0, B), slice(0, H))
+    for b in range(0, B, max(1, B - 1)):
+        one = run(slice(b, b + 1), slice(H - 1, H))
+        for n, x, y in zip(("o", "lse", "dq", "dk", "dv"), every, one):
+            x = x[b:b + 1, H - 1:H]
+            if n == "dq":  # added in any order: fp32 sums, then one rounding to bf16
+                far = (x.float() - y.float()).abs() - 2.0 ** -7 * y.float().abs()
+                assert float(far.max()) <= 1e-5 * float(y.float().abs().max())
+            else:
+                assert torch.equal(x, y), n
+    _status_ok()
+
+
 def test_two_steps_at_once_on_two_streams():
     # the same plan and caches read by two streams; outputs and workspaces of their own
     B, H, S, d = 2, 4, 512, 64
