@@ -286,14 +286,22 @@ __global__ void __launch_bounds__(256) fa_bwd_pre(const BwdParams p, long long r
 }
 
 // --------------------------------------------------------------- convert --
+constexpr int kConvert = 4;  // 16-byte pieces a thread, loaded together (8 as fast; 1: 2.5 us more of 230)
+
 __global__ void __launch_bounds__(256) fa_bwd_convert(const BwdParams p, long long n4) {
-  const long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
-  if (i >= n4) return;
-  const float4 a = reinterpret_cast<const float4*>(p.dq_acc)[i];
-  uint2 out;
-  out.x = pack_bf16x2(a.x * p.scale, a.y * p.scale);
-  out.y = pack_bf16x2(a.z * p.scale, a.w * p.scale);
-  reinterpret_cast<uint2*>(p.dq)[i] = out;
+  const long long i0 = static_cast<long long>(blockIdx.x) * (256 * kConvert) + threadIdx.x;
+  float4 a[kConvert];
+#pragma unroll
+  for (int k = 0; k < kConvert; ++k)
+    if (i0 + k * 256 < n4) a[k] = __ldcs(reinterpret_cast<const float4*>(p.dq_acc) + i0 + k * 256);
+#pragma unroll
+  for (int k = 0; k < kConvert; ++k) {
+    if (i0 + k * 256 >= n4) break;
+    uint2 out;
+    out.x = pack_bf16x2(a[k].x * p.scale, a[k].y * p.scale);
+    out.y = pack_bf16x2(a[k].z * p.scale, a[k].w * p.scale);
+    reinterpret_cast<uint2*>(p.dq)[i0 + k * 256] = out;
+  }
 }
 
 // The scored modes hold weights times 2^15 (the factor leaves with the LSE's staging, D's staging and
@@ -1151,7 +1159,8 @@ cudaError_t launch_bwd_mode(const CUtensorMap& tq, const CUtensorMap& tk, const 
     if (e != cudaSuccess) return e;
   }
   const long long n4 = rows * D / 4;
-  fa_bwd_convert<<<static_cast<unsigned int>((n4 + 255) / 256), 256, 0, stream>>>(p, n4);
+  fa_bwd_convert<<<static_cast<unsigned int>((n4 + 256 * kConvert - 1) / (256 * kConvert)), 256, 0,
+                   stream>>>(p, n4);
   return cudaGetLastError();
 }
 
