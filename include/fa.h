@@ -552,7 +552,11 @@ fa_status fa_mask_plan(const int32_t* row_lo, const int32_t* row_hi, int B, int 
 fa_status fa_fwd_scored(const void* q, const void* k, const void* v, void* o, float* lse, int B,
                         int Hq, int Hkv, int Sq, int Sk, int d, int causal, float scale,
                         float softcap, const float* slopes, const void* plan, size_t plan_bytes,
-                        cudaStream_t stream);
+                        void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Bytes of device workspace (16-byte aligned) with which fa_fwd_scored splits the keys of few rows over
+   the GPU; 0: such sizes are not split.  Without it (NULL) the call gives the same, later. */
+size_t fa_fwd_scored_workspace_size(int B, int Hq, int Hkv, int Sq, int Sk, int d);
 
 /* Its backward pass, by recomputation as fa_bwd: with P = exp(z - LSE) and dz = P * (dP - D),
    ds = dz * (1 - (t / softcap)^2), dQ = scale * ds K, dK = scale * ds^T Q, dV = P^T dO.  The scores'

@@ -32,8 +32,8 @@ EXPORTED = ("fa_fwd", "fa_bwd", "fa_bwd_workspace_size", "fa_decode", "fa_decode
             "fa_select_blocks", "fa_select_blocks_workspace_size", "fa_decode_paged_fp8",
             "fa_decode_paged_fp8_workspace_size", "fa_qk_norm_rope", "fa_qk_norm_rope_bwd",
             "fa_qk_norm_rope_bwd_workspace_size", "fa_row_bounds", "fa_mask_plan",
-            "fa_mask_plan_size", "fa_fwd_scored", "fa_bwd_scored", "fa_decode_scored",
-            "fa_decode_scored_workspace_size", "fa_device_status", "fa_selftest_wait_timeout",
+            "fa_mask_plan_size", "fa_fwd_scored", "fa_fwd_scored_workspace_size", "fa_bwd_scored",
+            "fa_decode_scored", "fa_decode_scored_workspace_size", "fa_device_status", "fa_selftest_wait_timeout",
             "fa_profile_next_launch", "fa_status_string", "fa_last_error_detail", "fa_version")
 
 _lib = None
@@ -117,7 +117,7 @@ def load_library(path: str = LIB_PATH):
                                         I, I, I, I, P, Z, P]
     lib.fa_row_bounds.argtypes = [P, P, I, P, P, I, I, I, I, I, P]
     lib.fa_mask_plan.argtypes = [P, P, I, I, I, P, Z, P]
-    lib.fa_fwd_scored.argtypes = [P, P, P, P, P, I, I, I, I, I, I, I, F, F, P, P, Z, P]
+    lib.fa_fwd_scored.argtypes = [P, P, P, P, P, I, I, I, I, I, I, I, F, F, P, P, Z, P, Z, P]
     lib.fa_bwd_scored.argtypes = [P, P, P, P, P, P, P, P, P, I, I, I, I, I, I, I, F, F, P, P, Z, P, Z, P]
     lib.fa_decode_scored.argtypes = [P, P, P, P, P, P, P, I, I, I, I, I, F, F, P, I, P, Z, P]
     for f in (lib.fa_qk_norm_rope, lib.fa_qk_norm_rope_bwd, lib.fa_row_bounds, lib.fa_mask_plan,
@@ -125,9 +125,10 @@ def load_library(path: str = LIB_PATH):
         f.restype = I
     lib.fa_qk_norm_rope_bwd_workspace_size.argtypes = [I]
     lib.fa_mask_plan_size.argtypes = [I, I, I]
+    lib.fa_fwd_scored_workspace_size.argtypes = [I, I, I, I, I, I]
     lib.fa_decode_scored_workspace_size.argtypes = [I, I, I, I, I, I]
     for f in (lib.fa_qk_norm_rope_bwd_workspace_size, lib.fa_mask_plan_size,
-              lib.fa_decode_scored_workspace_size):
+              lib.fa_fwd_scored_workspace_size, lib.fa_decode_scored_workspace_size):
         f.restype = Z
     lib.fa_status_string.argtypes = [I]
     lib.fa_status_string.restype = ctypes.c_char_p
@@ -891,18 +892,32 @@ def _scored_args(q, k, v, slopes, plan, dev):
     return B, Hq, Hkv, Sq, Sk, d, nbytes
 
 
+@functools.lru_cache(4096)
+def _fwd_scored_bytes(B, Hq, Hkv, Sq, Sk, d):
+    return load_library().fa_fwd_scored_workspace_size(B, Hq, Hkv, Sq, Sk, d)
+
+
+def fa_fwd_scored_workspace_size(B, Hq, Hkv, Sq, Sk, d) -> int:
+    return int(load_library().fa_fwd_scored_workspace_size(
+        _int(B, "B"), _int(Hq, "Hq"), _int(Hkv, "Hkv"), _int(Sq, "Sq"), _int(Sk, "Sk"), _int(d, "d")))
+
+
 def fa_fwd_scored(q, k, v, causal: bool, scale: float, softcap: float = 0.0, slopes=None, plan=None,
-                  o=None, lse=None, stream=None):
+                  o=None, lse=None, workspace=None, stream=None):
     """Attention on capped and biased scores (fa_fwd_scored): q [B,Hq,Sq,d], k/v [B,Hkv,Sk,d] bf16;
-    softcap 0 for none; slopes fp32 [Hq] of the bias -slope * distance; plan from fa_mask_plan.
-    Returns (o, lse)."""
+    softcap 0 for none; slopes fp32 [Hq] of the bias -slope * distance; plan from fa_mask_plan.  The
+    workspace is fa_fwd_scored_workspace_size(B, Hq, Hkv, Sq, Sk, d) bytes.  Returns (o, lse)."""
     lib, dev = load_library(), _device()
     B, Hq, Hkv, Sq, Sk, d, nplan = _scored_args(q, k, v, slopes, plan, dev)
     o = _out(o, "o", (B, Hq, Sq, d), _BF16, dev, stream)
     lse = _out(lse, "lse", (B, Hq, Sq), _F32, dev, stream)
+    nbytes = _fwd_scored_bytes(B, Hq, Hkv, Sq, Sk, d)
+    if nbytes or workspace is not None:
+        workspace = _workspace(workspace, nbytes, dev, stream)
+        nbytes = workspace.nbytes
     st = lib.fa_fwd_scored(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), B,
                            Hq, Hkv, Sq, Sk, d, int(bool(causal)), float(scale), float(softcap),
-                           _ptr(slopes), _ptr(plan), nplan, _stream(stream))
+                           _ptr(slopes), _ptr(plan), nplan, _ptr(workspace), nbytes, _stream(stream))
     _check(st, "fa_fwd_scored")
     return o, lse
 

@@ -250,7 +250,7 @@ fa_status fwd_launch(const void* q, const void* k, const void* v, void* o, float
                      int Hq, int Hkv, int Sq, int Sk, int d, int causal, float scale,
                      const SeqLayout& lay, const uint32_t* key_bits, const fa::DropoutArgs& drop,
                      cudaStream_t stream, const fa::ScoreArgs* scored = nullptr,
-                     bool capped = false) {
+                     bool capped = false, const fa::FwdSplit& split = fa::FwdSplit{1, nullptr, nullptr}) {
   FA_TRY(check_ptr(q, "q"));
   FA_TRY(check_ptr(k, "k"));
   FA_TRY(check_ptr(v, "v"));
@@ -297,7 +297,7 @@ fa_status fwd_launch(const void* q, const void* k, const void* v, void* o, float
   p.rescale_log2 = 8.0f;
   if (1LL * p.n_rbu * p.units_per_rbu >= (1LL << 31))
     return fail(FA_ERR_INVALID_ARG, "grid too large");
-  cudaError_t e = scored ? fa::launch_fwd_scored(d, tq, tk, tv, p, *scored, capped, stream)
+  cudaError_t e = scored ? fa::launch_fwd_scored(d, tq, tk, tv, p, *scored, split, capped, stream)
                          : fa::launch_fwd(d, tq, tk, tv, p, stream);
   if (e != cudaSuccess) return fail(FA_ERR_CUDA, "fa_fwd launch: %s", cudaGetErrorString(e));
   return ok();
@@ -509,16 +509,33 @@ fa_status fa_fwd_varlen(const void* q, const void* k, const void* v, void* o, fl
 fa_status fa_fwd_scored(const void* q, const void* k, const void* v, void* o, float* lse, int B,
                         int Hq, int Hkv, int Sq, int Sk, int d, int causal, float scale,
                         float softcap, const float* slopes, const void* plan, size_t plan_bytes,
-                        cudaStream_t stream) {
+                        void* workspace, size_t workspace_bytes, cudaStream_t stream) {
   FA_TRY(check_sizes(B, Hq, Hkv, Sq, Sk, d));
   fa::ScoreArgs sc{};
   FA_TRY(make_score(scale, softcap, slopes, plan, plan_bytes, B, Sq, Sk, &sc));
+  fa::FwdSplit split{1, nullptr, nullptr};
+  const size_t need = fa_fwd_scored_workspace_size(B, Hq, Hkv, Sq, Sk, d);
+  if (workspace && need > 0) {
+    if (workspace_bytes < need)
+      return fail(FA_ERR_WORKSPACE, "the workspace of these sizes has %zu bytes, got %zu", need,
+                  workspace_bytes);
+    FA_TRY(check_ptr(workspace, "workspace"));
+    split.n = fa::fwd_scored_splits(B, Hq, Hkv, Sq, Sk);
+    split.part_o = static_cast<float*>(workspace);
+    split.part_lse = split.part_o + static_cast<size_t>(split.n) * B * Hq * Sq * d;
+  }
   SeqLayout lay{};
   lay.grid_b = B;
   lay.longest_q = Sq;
   lay.longest_k = Sk;
   return fwd_launch(q, k, v, o, lse, B, Hq, Hkv, Sq, Sk, d, causal, scale, lay, nullptr,
-                    kNoDropout, stream, &sc, softcap > 0.f);
+                    kNoDropout, stream, &sc, softcap > 0.f, split);
+}
+
+size_t fa_fwd_scored_workspace_size(int B, int Hq, int Hkv, int Sq, int Sk, int d) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Sq < 1 || Sk < 1 || d < 1) return 0;
+  const int n = fa::fwd_scored_splits(B, Hq, Hkv, Sq, Sk);
+  return n > 1 ? static_cast<size_t>(n) * B * Hq * Sq * (d + 1) * sizeof(float) : 0;
 }
 
 fa_status fa_bwd_scored(const void* q, const void* k, const void* v, const void* o,

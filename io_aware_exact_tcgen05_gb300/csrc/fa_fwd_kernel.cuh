@@ -38,6 +38,7 @@
 #pragma once
 
 #include <algorithm>
+#include <limits>
 #include <type_traits>
 
 #include <cuda_runtime.h>
@@ -92,6 +93,8 @@ constexpr size_t fwd_smem_bytes() {
 }
 
 __device__ __forceinline__ float neg_inf() { return __int_as_float(0xff800000); }
+// In place of a part's LSE (which is never +inf): the row's unit was too short to split, and wrote the results.
+constexpr float kWhole = std::numeric_limits<float>::infinity();
 
 // Fast-path bound on a row's fp32 tile sum: every weight stays below 2^64,
 // so P, l and O (at most 2^64 per tile per key block) stay far from fp32
@@ -167,6 +170,7 @@ enum : int {
 
 struct ScoredFwdParams : FwdParams {
   ScoreArgs sc;
+  FwdSplit split;
 };
 template <int MODE>
 using FwdParamsOf = std::conditional_t<(MODE & kModeScored) != 0, ScoredFwdParams, FwdParams>;
@@ -182,8 +186,11 @@ struct Unit {
   bool rows, active1;    // rows: slot 0 has rows at all
 };
 
+constexpr int kPartTiles = 5;  // least tiles of a part of a split unit
+
 // In the scored modes a slot takes part in the rounds (last tiles first) whose tile its rows see.
 struct ScoredUnit : Unit {
+  int part, parts;                 // of the unit's tiles (FwdSplit)
   int begin0, end0, begin1, end1;  // rounds of slots 0 and 1
   __device__ __forceinline__ int begin(int t) const { return t ? begin1 : begin0; }
   __device__ __forceinline__ int end(int t) const { return t ? end1 : end0; }
@@ -243,6 +250,12 @@ __device__ __forceinline__ Unit unit_at(const FwdParams& p, int U) {
 // first), and a slot visits the tiles of its rows' hull.
 __device__ __forceinline__ ScoredUnit unit_at(const ScoredFwdParams& p, int U) {
   ScoredUnit u;
+  u.part = 0;
+  u.parts = 1;
+  if (p.split.n > 1) {  // parts of a unit are neighbours
+    u.part = U % p.split.n;
+    U /= p.split.n;
+  }
   const MaskPlan& m = p.sc.plan;
   const int heads = p.pack_heads ? p.Hq >> 1 : p.Hq;  // units of a batch row and row block
   int w, rbu;
@@ -310,6 +323,19 @@ __device__ __forceinline__ ScoredUnit unit_at(const ScoredFwdParams& p, int U) {
     if (hi1 > 0) {
       u.begin1 = end - (hi1 + kTileN - 1) / kTileN;
       u.end1 = end - lo1 / kTileN;
+    }
+    if (p.split.n > 1) {
+      // equal parts of the rounds, of kPartTiles or more; those that are left over are empty
+      const int n = u.n_tiles;
+      u.parts = max(1, min(p.split.n, n / kPartTiles));
+      const int from = u.part < u.parts ? n * u.part / u.parts : 0;
+      const int to = u.part < u.parts ? n * (u.part + 1) / u.parts : 0;
+      u.j0 += n - to;
+      u.n_tiles = to - from;
+      u.begin0 = max(u.begin0 - from, 0);
+      u.end0 = max(min(u.end0, to) - from, u.begin0);
+      u.begin1 = max(u.begin1 - from, 0);
+      u.end1 = max(min(u.end1, to) - from, u.begin1);
     }
   }
   return u;
@@ -684,8 +710,9 @@ __device__ __forceinline__ void scored_softmax_warps(Smem& s, const ScoredFwdPar
     {
       const bool live = l != 0.f && !dead;  // (a NaN in a visible key makes l one: it reaches O and LSE)
       const float inv = live ? 1.f / lr : 0.f;
-      const bool in_range = i < un.sq;
+      const bool in_range = i < un.sq && (un.parts > 1 || un.part == 0);
       const size_t row = (static_cast<size_t>(un.bz) * p.Hq + h) * p.Sq + i;
+      const size_t part = static_cast<size_t>(un.part) * p.B * p.Hq * p.Sq + row;
       __nv_bfloat16* orow = reinterpret_cast<__nv_bfloat16*>(p.o) + row * D;
 #pragma unroll 1
       for (int cc = 0; cc < D / 32; ++cc) {
@@ -693,6 +720,17 @@ __device__ __forceinline__ void scored_softmax_warps(Smem& s, const ScoredFwdPar
         if (n_tiles > 0) {
           tmem_ld32(t_o + cc * 32, orr);
           tmem_wait_ld();
+        }
+        if (un.parts > 1) {  // a part: the join reads it where its LSE is not -inf
+          if (in_range && live) {
+            float4* dst = reinterpret_cast<float4*>(p.split.part_o + part * D + cc * 32);
+#pragma unroll
+            for (int q2 = 0; q2 < 8; ++q2)
+              dst[q2] = make_float4(
+                  __uint_as_float(orr[4 * q2]) * inv, __uint_as_float(orr[4 * q2 + 1]) * inv,
+                  __uint_as_float(orr[4 * q2 + 2]) * inv, __uint_as_float(orr[4 * q2 + 3]) * inv);
+          }
+          continue;
         }
         uint32_t pk[16];
 #pragma unroll
@@ -707,8 +745,9 @@ __device__ __forceinline__ void scored_softmax_warps(Smem& s, const ScoredFwdPar
             dst[q2] = make_uint4(pk[4 * q2], pk[4 * q2 + 1], pk[4 * q2 + 2], pk[4 * q2 + 3]);
         }
       }
-      if (in_range && p.lse)
-        p.lse[row] = live ? fmaf(m, 0.69314718055994531f, logf(l)) : neg_inf();
+      const float lse = live ? fmaf(m, 0.69314718055994531f, logf(l)) : neg_inf();
+      if (in_range && p.split.n > 1) p.split.part_lse[part] = un.parts > 1 ? lse : kWhole;
+      if (in_range && un.parts == 1 && p.lse) p.lse[row] = lse;
     }
     if (n_tiles > 0) {
       tc_fence_before();
@@ -741,7 +780,8 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
                                      ~uintptr_t(1023));
   const int warp = threadIdx.x >> 5;
   const int lane = threadIdx.x & 31;
-  const int n_units = p.n_rbu * p.units_per_rbu;
+  int n_units = p.n_rbu * p.units_per_rbu;
+  if constexpr (SCORED) n_units *= p.split.n;
   // The k-th unit of this CTA: units run heavy to light, so blocks of
   // gridDim.x units are walked alternately forwards and backwards (the
   // heaviest unit of one block pairs with the lightest of the next).

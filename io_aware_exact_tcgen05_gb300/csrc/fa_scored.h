@@ -105,9 +105,16 @@ cudaError_t launch_decode_scored(int d, const CUtensorMap& tk, const CUtensorMap
                                  cudaStream_t stream);
 unsigned int read_decode_scored_status(bool clear);
 
+// Parts that the key tiles of a unit are split into, and what holds their results.
+struct FwdSplit {
+  int n;            // 1: not split
+  float* part_o;    // [n][B * Hq * Sq][d]  O of each part
+  float* part_lse;  // [n][B * Hq * Sq]     its LSE; -inf without keys; kWhole: the row is done
+};
+int fwd_scored_splits(int B, int Hq, int Hkv, int Sq, int Sk);
 cudaError_t launch_fwd_scored(int d, const CUtensorMap& tq, const CUtensorMap& tk,
                               const CUtensorMap& tv, const FwdParams& base, const ScoreArgs& sc,
-                              bool cap, cudaStream_t stream);
+                              const FwdSplit& split, bool cap, cudaStream_t stream);
 cudaError_t launch_bwd_scored(int d, const CUtensorMap& tq, const CUtensorMap& tk,
                               const CUtensorMap& tv, const CUtensorMap& tdo,
                               const CUtensorMap& tdq, const BwdParams& base, const ScoreArgs& sc,

@@ -151,6 +151,68 @@ def test_intervals_that_differ_from_tile_to_tile(causal, Hq, Hkv, d, cap, bias):
         _within(x, r[n], r["tol_" + n], n)
 
 
+SPLIT = [
+    # B, Hq, Hkv, Sq, Sk, d, causal, cap, slopes?, window, cu, prefix: few rows, keys of many tiles
+    (1, 2, 1, 1, 2000, 64, True, 0.0, False, 0, None, None),
+    (1, 3, 3, 130, 1700, 128, True, 20.0, True, 0, None, None),
+    (2, 4, 2, 200, 2500, 64, False, 4.0, False, 0, None, None),
+    (2, 2, 2, 300, 2000, 64, True, 0.0, True, 900, [0, 1850, 1900, 2000, 3000, 3990], [0, 0, 30, 1000, -1]),
+    (1, 1, 1, 700, 1500, 128, True, 2.0, False, 0, [100, 1400], [1290]),
+]
+
+
+@pytest.mark.parametrize("case", SPLIT)
+def test_few_rows_with_long_keys(case):
+    # split over the GPU (with a workspace), the same without
+    B, Hq, Hkv, Sq, Sk, d, causal, cap, bias, window, cu, prefix = case
+    assert fa.fa_fwd_scored_workspace_size(B, Hq, Hkv, Sq, Sk, d) > 0
+    sl = _slopes(Hq, 0.2) if bias else None
+    planned = bool(window or cu)
+    r = _run(B, Hq, Hkv, Sq, Sk, d, causal, cap, sl, window, cu, prefix, seed=31, planned=planned)
+    t = workloads.random_qkv(B, Hq, Hkv, Sq, Sk, d, seed=31, q_mult=1.0, with_dout=True)
+    q, k, v = (t[n].to(DEV) for n in ("q", "k", "v"))
+    plan = None
+    if planned:
+        lo, hi = fa.fa_row_bounds(B, Sq, Sk, causal, window=window, cu_docs=_i32(cu), prefix=_i32(prefix))
+        plan = fa.fa_mask_plan(lo, hi, Sk)
+    o, lse = torch.empty_like(q), torch.empty(B, Hq, Sq, device=DEV)
+    slopes = None if sl is None else sl.to(DEV)
+    st = fa.load_library().fa_fwd_scored(
+        q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(), B, Hq, Hkv, Sq, Sk, d,
+        int(causal and not planned), 1.0 / math.sqrt(d), cap, None if slopes is None else slopes.data_ptr(),
+        None if plan is None else plan.data_ptr(), 0 if plan is None else plan.nbytes, None, 0, None)
+    torch.cuda.synchronize()
+    assert st == fa.FA_OK
+    _within(o, r["o"], r["tol_o"], "O")
+    _within(lse, r["lse"], r["tol_lse"], "LSE")
+
+
+def test_few_rows_with_long_keys_and_nan():
+    # a NaN in a key or value reaches the rows that see it through the join as well; what lies in front of the first
+    # and behind the last visible key is not used
+    B, H, Sq, Sk, d = 1, 2, 100, 3000, 64
+    t = workloads.random_qkv(B, H, H, Sq, Sk, d, seed=32)
+    lo = np.full((B, Sq), 500)
+    hi = np.full((B, Sq), 2600)
+    hi[:, :10], hi[:, 10:20] = 2000, 0
+    r = so.attend(*(to_np(t[n]) for n in ("q", "k", "v")), 0.1, lo, hi, 5.0, bounds=True)
+    q, k, v = (t[n].to(DEV) for n in ("q", "k", "v"))
+    for x in (k, v):
+        x[:, :, :500] = float("nan")
+        x[:, :, 2600:] = float("inf")
+    plan = fa.fa_mask_plan(_i32(lo.tolist()), _i32(hi.tolist()), Sk)
+    assert fa.fa_fwd_scored_workspace_size(B, H, H, Sq, Sk, d) > 0
+    o, lse = fa.fa_fwd_scored(q, k, v, False, 0.1, softcap=5.0, plan=plan)
+    _within(o, r["o"], r["tol_o"], "O")
+    _within(lse, r["lse"], r["tol_lse"], "LSE")
+    k[:, :, 2400] = float("nan")
+    o, lse = fa.fa_fwd_scored(q, k, v, False, 0.1, softcap=5.0, plan=plan)
+    assert bool(o[:, :, 20:].isnan().all()) and bool(lse[:, :, 20:].isnan().all())
+    assert bool((o[:, :, 10:20] == 0).all()) and bool((lse[:, :, 10:20] == -math.inf).all())
+    _within(lse[:, :, :10], r["lse"][:, :, :10], r["tol_lse"][:, :, :10], "LSE")
+    _status_ok()
+
+
 def test_batch_rows_of_very_different_work_in_one_plan():
     # tiles go by their work over all batch rows together: each batch row as if it were alone
     B, S, H, d = 40, 384, 2, 64

@@ -46,6 +46,34 @@ def test_attention_writes_its_outputs_and_nothing_else(d, Hq, Hkv):
         assert not c.untouched_rows(np.zeros(c.t.numel() // d)).any(), n
 
 
+def test_split_attention_writes_its_outputs_and_nothing_else():
+    B, Hq, Hkv, Sq, Sk, d = 1, 3, 1, 70, 2100, 64
+    t = workloads.random_qkv(B, Hq, Hkv, Sq, Sk, d, seed=4)
+    nbytes = fa.fa_fwd_scored_workspace_size(B, Hq, Hkv, Sq, Sk, d)
+    assert nbytes > 0
+    o, lse, ws = _carve(((B, Hq, Sq, d), BF), ((B, Hq, Sq), torch.float32), ((nbytes,), torch.uint8))
+    q, k, v = (t[n].to(DEV) for n in ("q", "k", "v"))
+    fa.fa_fwd_scored(q, k, v, True, 0.1, softcap=6.0, o=o.t, lse=lse.t, workspace=ws.t)
+    # captured and replayed over the same workspace
+    g = torch.cuda.CUDAGraph()
+    o2, lse2 = torch.empty_like(q), torch.empty(B, Hq, Sq, device=DEV)
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        fa.fa_fwd_scored(q, k, v, True, 0.1, softcap=6.0, o=o2, lse=lse2, workspace=ws.t)
+    ws.t.fill_(0xff)  # every part is written anew
+    for _ in range(2):
+        g.replay()
+    torch.cuda.synchronize()
+    _status_ok()
+    for n, c in dict(o=o, lse=lse, workspace=ws).items():
+        c.check_guards(n)
+    assert torch.equal(o.t, o2) and torch.equal(lse.t, lse2)
+    lo, hi = so.row_bounds(B, Sq, Sk, True)
+    r = so.attend(*(to_np(t[n]) for n in ("q", "k", "v")), 0.1, lo, hi, 6.0, bounds=True)
+    _within(o2, r["o"], r["tol_o"], "O")
+    _within(lse2, r["lse"], r["tol_lse"], "LSE")
+
+
 @pytest.mark.parametrize("Hq,Hkv", [(1, 1), (6, 2), (20, 1), (33, 3)])
 @pytest.mark.parametrize("d", [64, 128])
 def test_decode_writes_its_outputs_and_nothing_else(Hq, Hkv, d):

@@ -139,9 +139,9 @@ def test_oracle_angles_are_exact_far_out():
 # ---------------------------------------------------------------- refusals --
 
 def _fwd(lib, q=16, lse=None, B=1, Hq=2, Hkv=2, Sq=8, Sk=8, d=128, scale=0.1, cap=0.0, slopes=None, plan=None,
-         nplan=0):
+         nplan=0, ws=None, nws=0):
     return lib.fa_fwd_scored(P(q), P(16), P(16), P(16), P(lse), B, Hq, Hkv, Sq, Sk, d, 1, F(scale), F(cap),
-                             P(slopes), P(plan), nplan, None)
+                             P(slopes), P(plan), nplan, P(ws), nws, None)
 
 
 def test_scored_attention_refuses_before_any_device_call(lib):
@@ -158,6 +158,11 @@ def test_scored_attention_refuses_before_any_device_call(lib):
     assert _fwd(lib, slopes=18) == fa.FA_ERR_INVALID_ARG
     need = fa.fa_mask_plan_size(1, 8, 8)
     assert _fwd(lib, plan=256, nplan=need - 1) == fa.FA_ERR_WORKSPACE
+    split = fa.fa_fwd_scored_workspace_size(1, 2, 2, 8, 5000, 128)  # few rows, long keys
+    assert split > 0 == fa.fa_fwd_scored_workspace_size(1, 2, 2, 8, 600, 128) == fa.fa_fwd_scored_workspace_size(
+        8, 32, 8, 4096, 4096, 128) == fa.fa_fwd_scored_workspace_size(1, 3, 2, 8, 5000, 128)
+    assert _fwd(lib, Sk=5000, ws=256, nws=split - 1) == fa.FA_ERR_WORKSPACE
+    assert _fwd(lib, Sk=5000, ws=264, nws=split) == fa.FA_ERR_INVALID_ARG
     assert _fwd(lib, plan=260, nplan=need) == fa.FA_ERR_INVALID_ARG
 
     def bwd(ws=256, nws=1 << 20, cap=0.0, plan=None, nplan=0):
