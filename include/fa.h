@@ -560,12 +560,16 @@ size_t fa_fwd_scored_workspace_size(int B, int Hq, int Hkv, int Sq, int Sk, int 
 
 /* Its backward pass, by recomputation as fa_bwd: with P = exp(z - LSE) and dz = P * (dP - D),
    ds = dz * (1 - (t / softcap)^2), dQ = scale * ds K, dK = scale * ds^T Q, dV = P^T dO.  The scores'
-   arguments are the forward's; workspace holds fa_bwd_workspace_size(B, Hq, Sq, d) bytes. */
+   arguments are the forward's; workspace holds fa_bwd_workspace_size(B, Hq, Sq, d) bytes.  Where
+   fa_bwd_scored_workspace_size is more and as much is there, the queries of few keys are split over
+   the GPU: the same gradients, sooner. */
 fa_status fa_bwd_scored(const void* q, const void* k, const void* v, const void* o,
                         const void* dout, const float* lse, void* dq, void* dk, void* dv, int B,
                         int Hq, int Hkv, int Sq, int Sk, int d, int causal, float scale,
                         float softcap, const float* slopes, const void* plan, size_t plan_bytes,
                         void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+size_t fa_bwd_scored_workspace_size(int B, int Hq, int Hkv, int Sq, int Sk, int d);
 
 /* Bytes of device workspace fa_decode_scored needs; 0: none, and its workspace may be NULL. */
 size_t fa_decode_scored_workspace_size(int B, int Hq, int Hkv, int Sk_max, int d, int window);

@@ -33,7 +33,7 @@ EXPORTED = ("fa_fwd", "fa_bwd", "fa_bwd_workspace_size", "fa_decode", "fa_decode
             "fa_decode_paged_fp8_workspace_size", "fa_qk_norm_rope", "fa_qk_norm_rope_bwd",
             "fa_qk_norm_rope_bwd_workspace_size", "fa_row_bounds", "fa_mask_plan",
             "fa_mask_plan_size", "fa_fwd_scored", "fa_fwd_scored_workspace_size", "fa_bwd_scored",
-            "fa_decode_scored", "fa_decode_scored_workspace_size", "fa_device_status", "fa_selftest_wait_timeout",
+            "fa_bwd_scored_workspace_size", "fa_decode_scored", "fa_decode_scored_workspace_size", "fa_device_status", "fa_selftest_wait_timeout",
             "fa_profile_next_launch", "fa_status_string", "fa_last_error_detail", "fa_version")
 
 _lib = None
@@ -126,9 +126,11 @@ def load_library(path: str = LIB_PATH):
     lib.fa_qk_norm_rope_bwd_workspace_size.argtypes = [I]
     lib.fa_mask_plan_size.argtypes = [I, I, I]
     lib.fa_fwd_scored_workspace_size.argtypes = [I, I, I, I, I, I]
+    lib.fa_bwd_scored_workspace_size.argtypes = [I, I, I, I, I, I]
     lib.fa_decode_scored_workspace_size.argtypes = [I, I, I, I, I, I]
     for f in (lib.fa_qk_norm_rope_bwd_workspace_size, lib.fa_mask_plan_size,
-              lib.fa_fwd_scored_workspace_size, lib.fa_decode_scored_workspace_size):
+              lib.fa_fwd_scored_workspace_size, lib.fa_bwd_scored_workspace_size,
+              lib.fa_decode_scored_workspace_size):
         f.restype = Z
     lib.fa_status_string.argtypes = [I]
     lib.fa_status_string.restype = ctypes.c_char_p
@@ -703,11 +705,6 @@ def _decode_scored_bytes(B, Hq, Hkv, Sk_max, d, window):
     return load_library().fa_decode_scored_workspace_size(B, Hq, Hkv, Sk_max, d, window)
 
 
-@functools.lru_cache(4096)
-def _bwd_bytes(B, Hq, Sq, d):
-    return load_library().fa_bwd_workspace_size(B, Hq, Sq, d)
-
-
 def _view(t, name, shape, dev):
     """fa_heads of a bf16 tensor of that shape [B, S, H, d] with contiguous channels."""
     if not (isinstance(t, torch.Tensor) and t.dtype == _BF16 and t.get_device() == dev
@@ -922,10 +919,21 @@ def fa_fwd_scored(q, k, v, causal: bool, scale: float, softcap: float = 0.0, slo
     return o, lse
 
 
+@functools.lru_cache(4096)
+def _bwd_scored_bytes(B, Hq, Hkv, Sq, Sk, d):
+    return load_library().fa_bwd_scored_workspace_size(B, Hq, Hkv, Sq, Sk, d)
+
+
+def fa_bwd_scored_workspace_size(B, Hq, Hkv, Sq, Sk, d) -> int:
+    return int(load_library().fa_bwd_scored_workspace_size(
+        _int(B, "B"), _int(Hq, "Hq"), _int(Hkv, "Hkv"), _int(Sq, "Sq"), _int(Sk, "Sk"), _int(d, "d")))
+
+
 def fa_bwd_scored(q, k, v, o, dout, lse, causal: bool, scale: float, softcap: float = 0.0,
                   slopes=None, plan=None, dq=None, dk=None, dv=None, workspace=None, stream=None):
     """dQ, dK, dV of fa_fwd_scored (fa_bwd_scored), with the forward's arguments.  The workspace is
-    fa_bwd_workspace_size(B, Hq, Sq, d) bytes.  Returns (dq, dk, dv)."""
+    fa_bwd_scored_workspace_size(B, Hq, Hkv, Sq, Sk, d) bytes; fa_bwd_workspace_size(B, Hq, Sq, d) are
+    enough, but few keys are then not split over the GPU.  Returns (dq, dk, dv)."""
     lib, dev = load_library(), _device()
     B, Hq, Hkv, Sq, Sk, d, nplan = _scored_args(q, k, v, slopes, plan, dev)
     _have(o, "o", _BF16, (B, Hq, Sq, d), dev)
@@ -934,7 +942,7 @@ def fa_bwd_scored(q, k, v, o, dout, lse, causal: bool, scale: float, softcap: fl
     dq = _out(dq, "dq", (B, Hq, Sq, d), _BF16, dev, stream)
     dk = _out(dk, "dk", (B, Hkv, Sk, d), _BF16, dev, stream)
     dv = _out(dv, "dv", (B, Hkv, Sk, d), _BF16, dev, stream)
-    workspace = _workspace(workspace, _bwd_bytes(B, Hq, Sq, d), dev, stream)
+    workspace = _workspace(workspace, _bwd_scored_bytes(B, Hq, Hkv, Sq, Sk, d), dev, stream)
     st = lib.fa_bwd_scored(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), dout.data_ptr(),
                            lse.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), B, Hq, Hkv,
                            Sq, Sk, d, int(bool(causal)), float(scale), float(softcap), _ptr(slopes),

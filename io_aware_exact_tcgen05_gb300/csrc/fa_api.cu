@@ -308,7 +308,8 @@ fa_status bwd_launch(const void* q, const void* k, const void* v, const void* o,
                      int Sq, int Sk, int d, int causal, float scale, const SeqLayout& lay,
                      const uint32_t* key_bits, const fa::DropoutArgs& drop, void* workspace,
                      size_t workspace_bytes, cudaStream_t stream,
-                     const fa::ScoreArgs* scored = nullptr, bool capped = false) {
+                     const fa::ScoreArgs* scored = nullptr, bool capped = false,
+                     const fa::BwdSplit& split = fa::BwdSplit{1, nullptr}) {
   FA_TRY(check_ptr(q, "q"));
   FA_TRY(check_ptr(k, "k"));
   FA_TRY(check_ptr(v, "v"));
@@ -371,7 +372,7 @@ fa_status bwd_launch(const void* q, const void* k, const void* v, const void* o,
   CUtensorMap tdq;
   FA_TRY(make_map_acc(&tdq, p.dq_acc, 1L * B * Hq, Sq, d));
   cudaError_t e =
-      scored ? fa::launch_bwd_scored(d, tq, tk, tv, tdo, tdq, p, *scored, capped, stream)
+      scored ? fa::launch_bwd_scored(d, tq, tk, tv, tdo, tdq, p, *scored, split, capped, stream)
              : fa::launch_bwd(d, tq, tk, tv, tdo, tdq, p, stream);
   if (e != cudaSuccess) return fail(FA_ERR_CUDA, "fa_bwd launch: %s", cudaGetErrorString(e));
   return ok();
@@ -546,12 +547,25 @@ fa_status fa_bwd_scored(const void* q, const void* k, const void* v, const void*
   FA_TRY(check_sizes(B, Hq, Hkv, Sq, Sk, d));
   fa::ScoreArgs sc{};
   FA_TRY(make_score(scale, softcap, slopes, plan, plan_bytes, B, Sq, Sk, &sc));
+  fa::BwdSplit split{1, nullptr};
+  if (workspace && workspace_bytes >= fa_bwd_scored_workspace_size(B, Hq, Hkv, Sq, Sk, d)) {
+    split.n = fa::bwd_scored_splits(B, Hq, Hkv, Sq, Sk);
+    split.part = reinterpret_cast<float*>(static_cast<char*>(workspace) +
+                                          fa_bwd_workspace_size(B, Hq, Sq, d));
+  }
   SeqLayout lay{};
   lay.grid_b = B;
   lay.longest_q = Sq;
   lay.longest_k = Sk;
   return bwd_launch(q, k, v, o, dout, lse, dq, dk, dv, B, Hq, Hkv, Sq, Sk, d, causal, scale, lay,
-                    nullptr, kNoDropout, workspace, workspace_bytes, stream, &sc, softcap > 0.f);
+                    nullptr, kNoDropout, workspace, workspace_bytes, stream, &sc, softcap > 0.f, split);
+}
+
+size_t fa_bwd_scored_workspace_size(int B, int Hq, int Hkv, int Sq, int Sk, int d) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || Sq < 1 || Sk < 1 || d < 1) return 0;
+  const int n = fa::bwd_scored_splits(B, Hq, Hkv, Sq, Sk);
+  return fa_bwd_workspace_size(B, Hq, Sq, d) +
+         (n > 1 ? sizeof(float) * 2 * n * B * Hkv * Sk * d : size_t(0));
 }
 
 size_t fa_decode_scored_workspace_size(int B, int Hq, int Hkv, int Sk_max, int d, int window) {

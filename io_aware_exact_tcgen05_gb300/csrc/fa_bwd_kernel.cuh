@@ -194,9 +194,20 @@ __device__ __forceinline__ BwdUnit bwd_unit_at(const BwdParams& p, int U) {
 // kBwdScored, with kBwdCap and kBwdBias.
 enum : int { kBwdPlain = 0, kBwdDropout = 2, kBwdCap = 4, kBwdBias = 8, kBwdScored = 16 };
 
+constexpr int kPartIts = 12;  // least iterations of a part of a split unit
+
 struct ScoredBwdParams : BwdParams {
   ScoreArgs sc;
+  BwdSplit split;
 };
+
+struct ScoredBwdUnit : BwdUnit {
+  int part, parts, first;  // first: of all iterations of the unit, the part's
+};
+
+// The iteration (head and query tile) that a unit's it-th is.
+__device__ __forceinline__ int iteration(const BwdUnit&, int it) { return it; }
+__device__ __forceinline__ int iteration(const ScoredBwdUnit& u, int it) { return u.first + it; }
 // Threads of a mode.  The scored modes fill the fourth warpgroup up, so that its registers can go to
 // the compute and drain warps (setmaxnreg): 128 x (144 + 144 + 168 + 56) = the 512 x 128 of the launch.
 // (2 x 16 heads x 8192, documents and bias: 650 us with 128 each, 636 with 200 for the drain warps
@@ -208,8 +219,13 @@ using BwdParamsOf = std::conditional_t<(MODE & kBwdScored) != 0, ScoredBwdParams
 
 // The scored modes' units: with a plan, the key tiles in the plan's order (over all batch rows, or
 // where units go group by group within each) and the query tiles that may see them.
-__device__ __forceinline__ BwdUnit bwd_unit_at(const ScoredBwdParams& p, int U) {
-  BwdUnit u;
+__device__ __forceinline__ ScoredBwdUnit bwd_unit_at(const ScoredBwdParams& p, int U) {
+  ScoredBwdUnit u;
+  u.part = 0;
+  if (p.split.n > 1) {  // parts of a unit are neighbours
+    u.part = U % p.split.n;
+    U /= p.split.n;
+  }
   const MaskPlan& m = p.sc.plan;
   const int BH = p.grid_b * p.Hkv;
   const int per_group = p.n_kt * p.unit_group;
@@ -254,6 +270,16 @@ __device__ __forceinline__ BwdUnit bwd_unit_at(const ScoredBwdParams& p, int U) 
   if (p.causal) u.qt_lo = max(u.qt_lo, max(0, u.c0 - u.off) / kTileM);
   u.n_qt = max(0, qt_end - u.qt_lo);
   u.n_it = u.n_qt * p.group;
+  u.first = 0;
+  u.parts = 1;
+  if (p.split.n > 1) {
+    // equal parts of the iterations, of kPartIts or more; those that are left over are empty
+    const int n = u.n_it;
+    u.parts = max(1, min(p.split.n, n / kPartIts));
+    const bool have = u.part < u.parts;
+    u.first = have ? n * u.part / u.parts : 0;
+    u.n_it = have ? n * (u.part + 1) / u.parts - u.first : 0;
+  }
   return u;
 }
 
@@ -416,7 +442,8 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
     return;
   }
 
-  const int n_units = p.n_kt * p.grid_b * p.Hkv;
+  int n_units = p.n_kt * p.grid_b * p.Hkv;
+  if constexpr ((MODE & kBwdScored) != 0) n_units *= p.split.n;
   // The k-th unit of this CTA (units run heavy to light: key tile 0 first
   // under the causal rule); blocks of gridDim.x units are walked alternately
   // forwards and backwards so heavy and light units pair up.
@@ -483,7 +510,7 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
       for (int k = 0; ok && k * static_cast<int>(gridDim.x) < n_units; ++k) {
         const int U = unit_index(k);
         if (U >= n_units) continue;
-        const BwdUnit un = bwd_unit_at(p, U);
+        const auto un = bwd_unit_at(p, U);
         if (!un.exists || un.n_it == 0) continue;
         if (uk > 0 && !mbar_wait(&s.kv_empty, (uk - 1) & 1, abort_flag, kSiteKV)) break;
         const int zkv = un.bz * p.Hkv + un.hk;
@@ -496,8 +523,8 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
         for (int it = 0; it < un.n_it; ++it, ++ig) {
           const int st = ig % Smem::kQStages;
           const int use = ig / Smem::kQStages;
-          const int g = it / un.n_qt;
-          const int q0 = (un.qt_lo + it % un.n_qt) * kTileM;
+          const int g = iteration(un, it) / un.n_qt;
+          const int q0 = (un.qt_lo + iteration(un, it) % un.n_qt) * kTileM;
           const int zq = un.bz * p.Hq + un.hk * p.group + g;
           // The stage frees only once the dQ reduce staged in it has been
           // read (about a tile's time): meanwhile pull this tile's Q and dO
@@ -561,7 +588,7 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
       for (int k = 0; ok && k * static_cast<int>(gridDim.x) < n_units; ++k) {
         const int U = unit_index(k);
         if (U >= n_units) continue;
-        const BwdUnit un = bwd_unit_at(p, U);
+        const auto un = bwd_unit_at(p, U);
         if (!un.exists || un.n_it == 0) continue;
         if (!mbar_wait_warp(&s.kv_full, uk & 1, abort_flag, kSiteKV)) break;
         for (int it = 0; ok && it < un.n_it; ++it, ++ig) {
@@ -682,7 +709,7 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
     for (int k = 0; ok && k * static_cast<int>(gridDim.x) < n_units; ++k) {
       const int U = unit_index(k);
       if (U >= n_units) continue;
-      const BwdUnit un = bwd_unit_at(p, U);
+      const auto un = bwd_unit_at(p, U);
       if (!un.exists) continue;
       const int c0 = un.c0, klo = un.klo, kend = un.kend, kseq = un.kseq, sq = un.sq;
       const int qb = un.qb, bz = un.bz, off = un.off, qt_lo = un.qt_lo, n_qt = un.n_qt;
@@ -697,8 +724,8 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
       const uint32_t key8 = static_cast<uint32_t>(key) >> 3;
       for (int it = 0; it < n_it; ++it) {
         const int gi = ig + it;  // this iteration's index across units (barrier phases)
-        const int g = it / n_qt;
-        const int q0 = (qt_lo + it % n_qt) * kTileM;
+        const int g = iteration(un, it) / n_qt;
+        const int q0 = (qt_lo + iteration(un, it) % n_qt) * kTileM;
         const int h = hk * p.group + g;
         float slope2 = 0.f, sg = 0.f;  // bias: slope, and the slope of the distance's sign
         bool linear = true;            // every distance of this tile has one sign
@@ -947,7 +974,14 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
       // warp-uniform: the TMEM loads below are warp-collective, only the stores
       // depend on the lane's key
       {
-        const bool store = key < kseq;
+        bool store = key < kseq;
+        float* part = nullptr;  // where the unit is split: this key's row of dK's part
+        if constexpr (SCORED) {
+          store = store && un.part < un.parts;
+          if (un.parts > 1)
+            part = p.split.part + ((static_cast<size_t>(un.part) * 2 * p.B + bz) * p.Hkv + hk) * p.Sk * D +
+                   static_cast<size_t>(key) * D;
+        }
         const size_t kr = (static_cast<size_t>(bz) * p.Hkv + hk) * p.Sk + key;
         __nv_bfloat16* dkrow = reinterpret_cast<__nv_bfloat16*>(p.dk) + kr * D;
         __nv_bfloat16* dvrow = reinterpret_cast<__nv_bfloat16*>(p.dv) + kr * D;
@@ -967,6 +1001,19 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
             } else {
 #pragma unroll
               for (int e = 0; e < 32; ++e) r[e] = 0u;
+            }
+            if constexpr (SCORED) {
+              if (part) {
+                if (store) {
+                  float4* d4 = reinterpret_cast<float4*>(
+                      part + static_cast<size_t>(pass) * p.B * p.Hkv * p.Sk * D + cc * 32);
+#pragma unroll
+                  for (int e = 0; e < 8; ++e)
+                    d4[e] = make_float4(__uint_as_float(r[4 * e]) * mul, __uint_as_float(r[4 * e + 1]) * mul,
+                                        __uint_as_float(r[4 * e + 2]) * mul, __uint_as_float(r[4 * e + 3]) * mul);
+                }
+                continue;
+              }
             }
             uint32_t pw[16];
 #pragma unroll
@@ -1018,11 +1065,11 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
     for (int k = 0; ok && k * static_cast<int>(gridDim.x) < n_units; ++k) {
       const int U = unit_index(k);
       if (U >= n_units) continue;
-      const BwdUnit un = bwd_unit_at(p, U);
+      const auto un = bwd_unit_at(p, U);
       if (!un.exists || un.n_it == 0) continue;
       for (int it = 0; it < un.n_it; ++it, ++ig) {
-        const int g = it / un.n_qt;
-        const int q0 = (un.qt_lo + it % un.n_qt) * kTileM;
+        const int g = iteration(un, it) / un.n_qt;
+        const int q0 = (un.qt_lo + iteration(un, it) % un.n_qt) * kTileM;
         const int h = un.hk * p.group + g;
         const int row = un.qb + q0 + wq * 32;
         const int zz = un.bz * p.Hq + h;
@@ -1093,6 +1140,33 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
   }
 }
 
+// dK and dV of the key tiles whose units are split: the parts' sums, in order.
+template <int D>
+__global__ void __launch_bounds__(256) fa_bwd_join(const ScoredBwdParams p) {
+  griddep_wait();
+  const ScoredBwdUnit un = bwd_unit_at(p, static_cast<int>(blockIdx.x) * p.split.n);
+  if (un.parts == 1) return;
+  const size_t rows = static_cast<size_t>(p.B) * p.Hkv * p.Sk;
+  const size_t row0 = (static_cast<size_t>(un.bz) * p.Hkv + un.hk) * p.Sk + un.c0;
+  const int keys = min(kTileN, p.Sk - un.c0);
+  for (int i = threadIdx.x; i < 2 * keys * (D / 4); i += 256) {
+    const bool is_v = i >= keys * (D / 4);
+    const int at = is_v ? i - keys * (D / 4) : i;  // four channels of the tile
+    const float4* src = reinterpret_cast<const float4*>(p.split.part + ((is_v ? rows : 0) + row0) * D) + at;
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int s = 0; s < un.parts; ++s) {
+      const float4 b = src[static_cast<size_t>(s) * 2 * rows * (D / 4)];
+      a.x += b.x;
+      a.y += b.y;
+      a.z += b.z;
+      a.w += b.w;
+    }
+    reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(is_v ? p.dv : p.dk) + row0 * D)[at] =
+        make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
+  }
+}
+
 // The three kernels of a backward pass.
 template <int D, int MODE>
 cudaError_t launch_bwd_mode(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
@@ -1118,7 +1192,9 @@ cudaError_t launch_bwd_mode(const CUtensorMap& tq, const CUtensorMap& tk, const 
   if (e != cudaSuccess) return e;
   const long long l2 = std::max(1LL << 20, static_cast<long long>(l2_bytes));
   const long long units = static_cast<long long>(p.n_kt) * p.grid_b * p.Hkv;
-  const unsigned int grid = static_cast<unsigned int>(std::min<long long>(units, n_sm));
+  long long all_units = units;
+  if constexpr ((MODE & kBwdScored) != 0) all_units *= p.split.n;
+  const unsigned int grid = static_cast<unsigned int>(std::min<long long>(all_units, n_sm));
   // Pairs per group.  A pair's dQ accumulators and Q/dO tiles take 8 bytes
   // per row and head-dim column of each of its query heads.  While all pairs
   // together stay within about twice L2 they form one group (the plain
@@ -1157,6 +1233,12 @@ cudaError_t launch_bwd_mode(const CUtensorMap& tq, const CUtensorMap& tk, const 
     hook_after(stream);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
+  }
+  if constexpr ((MODE & kBwdScored) != 0) {
+    if (p.split.n > 1) {
+      e = launch_dependent(fa_bwd_join<D>, dim3(static_cast<unsigned int>(units)), dim3(256), 0, stream, pu);
+      if (e != cudaSuccess) return e;
+    }
   }
   const long long n4 = rows * D / 4;
   fa_bwd_convert<<<static_cast<unsigned int>((n4 + 256 * kConvert - 1) / (256 * kConvert)), 256, 0,

@@ -115,10 +115,16 @@ int fwd_scored_splits(int B, int Hq, int Hkv, int Sq, int Sk);
 cudaError_t launch_fwd_scored(int d, const CUtensorMap& tq, const CUtensorMap& tk,
                               const CUtensorMap& tv, const FwdParams& base, const ScoreArgs& sc,
                               const FwdSplit& split, bool cap, cudaStream_t stream);
+// Parts that the query tiles of a key tile's unit (of all heads of the group) are split into.
+struct BwdSplit {
+  int n;        // 1: not split
+  float* part;  // [n][2][B * Hkv * Sk][d]  dK and dV of each part
+};
+int bwd_scored_splits(int B, int Hq, int Hkv, int Sq, int Sk);
 cudaError_t launch_bwd_scored(int d, const CUtensorMap& tq, const CUtensorMap& tk,
                               const CUtensorMap& tv, const CUtensorMap& tdo,
                               const CUtensorMap& tdq, const BwdParams& base, const ScoreArgs& sc,
-                              bool cap, cudaStream_t stream);
+                              const BwdSplit& split, bool cap, cudaStream_t stream);
 unsigned int read_fwd_scored_status(bool clear);
 unsigned int read_bwd_scored_status(bool clear);
 

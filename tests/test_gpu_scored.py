@@ -187,6 +187,39 @@ def test_few_rows_with_long_keys(case):
     _within(lse, r["lse"], r["tol_lse"], "LSE")
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("cap,bias", [(0.0, False), (9.0, False), (0.0, True), (3.0, True)])
+@pytest.mark.parametrize("B,Hq,Hkv,Sq,Sk,causal,window,cu,prefix", [
+    (1, 16, 1, 400, 300, True, 0, None, None),                                # Sq > Sk: rows in front of the first key
+    (1, 40, 2, 257, 130, False, 0, None, None),
+    (2, 12, 1, 513, 513, True, 200, [0, 100, 260, 513, 800, 1026], [7, 0, -1, 300, 0]),
+])
+def test_backward_of_many_heads_on_few_keys(B, Hq, Hkv, Sq, Sk, causal, window, cu, prefix, cap, bias, d):
+    # query heads and tiles of a key tile are split over the GPU
+    assert fa.fa_bwd_scored_workspace_size(B, Hq, Hkv, Sq, Sk, d) > fa.fa_bwd_workspace_size(B, Hq, Sq, d)
+    _run(B, Hq, Hkv, Sq, Sk, d, causal, cap, _slopes(Hq, 0.3) if bias else None, window, cu, prefix, seed=41,
+         planned=cu is not None)
+
+
+def test_backward_of_many_heads_on_few_keys_where_nothing_looks():
+    B, Hq, Hkv, S, d = 1, 24, 2, 420, 64
+    cu, prefix = [0, 50, 370, 420], [-1, 0, -1]
+    t = workloads.random_qkv(B, Hq, Hkv, S, S, d, seed=42, with_dout=True)
+    lo, hi = so.row_bounds(B, S, S, True, 0, cu, prefix)
+    dead = torch.from_numpy(hi <= lo)
+    r = so.attend(*(to_np(t[n]) for n in ("q", "k", "v")), 0.09, lo, hi, 9.0, None, to_np(t["dout"]), bounds=True)
+    for x in t.values():
+        x.masked_fill_(dead[:, None, :, None], float("nan"))
+    q, k, v, do = (t[n].to(DEV) for n in ("q", "k", "v", "dout"))
+    plan = fa.fa_mask_plan(*fa.fa_row_bounds(B, S, S, True, cu_docs=_i32(cu), prefix=_i32(prefix)), S)
+    o, lse = fa.fa_fwd_scored(q, k, v, False, 0.09, softcap=9.0, plan=plan)
+    g = fa.fa_bwd_scored(q, k, v, o, do, lse, False, 0.09, softcap=9.0, plan=plan)
+    torch.cuda.synchronize()
+    _status_ok()
+    for n, x in zip(("dq", "dk", "dv"), g):
+        _within(x, r[n], r["tol_" + n], n)
+
+
 def test_few_rows_with_long_keys_and_nan():
     # a NaN in a key or value reaches the rows that see it through the join as well; what lies in front of the first
     # and behind the last visible key is not used

@@ -46,6 +46,31 @@ def test_attention_writes_its_outputs_and_nothing_else(d, Hq, Hkv):
         assert not c.untouched_rows(np.zeros(c.t.numel() // d)).any(), n
 
 
+def test_split_backward_writes_its_outputs_and_nothing_else():
+    B, Hq, Hkv, Sq, Sk, d = 1, 24, 1, 140, 300, 64
+    t = workloads.random_qkv(B, Hq, Hkv, Sq, Sk, d, seed=5, with_dout=True)
+    nbytes = fa.fa_bwd_scored_workspace_size(B, Hq, Hkv, Sq, Sk, d)
+    assert nbytes > fa.fa_bwd_workspace_size(B, Hq, Sq, d)
+    dq, dk, dv, ws = _carve(((B, Hq, Sq, d), BF), ((B, Hkv, Sk, d), BF), ((B, Hkv, Sk, d), BF), ((nbytes,), torch.uint8))
+    q, k, v, do = (t[n].to(DEV) for n in ("q", "k", "v", "dout"))
+    o, lse = fa.fa_fwd_scored(q, k, v, True, 0.1, softcap=6.0)
+    lo, hi = so.row_bounds(B, Sq, Sk, True)
+    r = so.attend(*(to_np(t[n]) for n in ("q", "k", "v")), 0.1, lo, hi, 6.0, None, to_np(t["dout"]), bounds=True)
+    first = None
+    for _ in range(2):
+        ws.t.fill_(0xff)  # every part is written anew
+        fa.fa_bwd_scored(q, k, v, o, do, lse, True, 0.1, softcap=6.0, dq=dq.t, dk=dk.t, dv=dv.t, workspace=ws.t)
+        torch.cuda.synchronize()
+        _status_ok()
+        for n, c in dict(dq=dq, dk=dk, dv=dv, workspace=ws).items():
+            c.check_guards(n)
+        for n, c in dict(dq=dq, dk=dk, dv=dv).items():
+            _within(c.t, r[n], r["tol_" + n], n)
+        if first:  # parts are added in order
+            assert torch.equal(first[0], dk.t) and torch.equal(first[1], dv.t)
+        first = dk.t.clone(), dv.t.clone()
+
+
 def test_split_attention_writes_its_outputs_and_nothing_else():
     B, Hq, Hkv, Sq, Sk, d = 1, 3, 1, 70, 2100, 64
     t = workloads.random_qkv(B, Hq, Hkv, Sq, Sk, d, seed=4)
@@ -264,7 +289,10 @@ def test_backward_in_groups_that_fit_the_l2_cache(B, H, S, planned):
         if planned:
             plan = fa.fa_mask_plan(lo[rows].contiguous(), hi[rows].contiguous(), Sk)
         o, lse = fa.fa_fwd_scored(*x[:3], not planned, 0.09, softcap=20.0, plan=plan)
-        return (o, lse) + fa.fa_bwd_scored(*x[:3], o, x[3], lse, not planned, 0.09, softcap=20.0, plan=plan)
+        # (with this workspace few keys are not split over the GPU, so that dK and dV are sums of one order)
+        ws = torch.empty(fa.fa_bwd_workspace_size(*lse.shape[:2], S, d), dtype=torch.uint8, device=DEV)
+        return (o, lse) + fa.fa_bwd_scored(*x[:3], o, x[3], lse, not planned, 0.09, softcap=20.0, plan=plan,
+                                           workspace=ws)
 
     if planned:
         lo, hi = fa.fa_row_bounds(B, S, Sk, True, window=300, cu_docs=cu)

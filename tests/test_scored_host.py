@@ -162,6 +162,9 @@ def test_scored_attention_refuses_before_any_device_call(lib):
     assert split > 0 == fa.fa_fwd_scored_workspace_size(1, 2, 2, 8, 600, 128) == fa.fa_fwd_scored_workspace_size(
         8, 32, 8, 4096, 4096, 128) == fa.fa_fwd_scored_workspace_size(1, 3, 2, 8, 5000, 128)
     assert _fwd(lib, Sk=5000, ws=256, nws=split - 1) == fa.FA_ERR_WORKSPACE
+    plain = fa.fa_bwd_workspace_size(1, 32, 512, 128)  # enough for any call; many heads on few keys may use more
+    assert fa.fa_bwd_scored_workspace_size(1, 32, 2, 512, 512, 128) > plain == fa.fa_bwd_scored_workspace_size(
+        1, 32, 32, 512, 512, 128)
     assert _fwd(lib, Sk=5000, ws=264, nws=split) == fa.FA_ERR_INVALID_ARG
     assert _fwd(lib, plan=260, nplan=need) == fa.FA_ERR_INVALID_ARG
 
