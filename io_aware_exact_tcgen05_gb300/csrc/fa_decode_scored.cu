@@ -16,8 +16,8 @@
 // into the next item while the others write the last one's state away, so the ring never drains.
 //
 // Measured (GB300, graph, d = 128): 32 requests of 8 KV heads with 4 query heads each, windows of 4096 keys
-// 84 to 85 us (6.2 TB/s, 93% of the measured copy; the CUDA cores in splits of 512 keys took 164, in equal stretches
-// 107), the same without a window, 1k to 32k keys, 330 us (6.9 TB/s; fa_decode 355); 8 query heads a KV
+// 84 to 85 us (6.2 TB/s, 93% of the measured copy; the CUDA cores in splits of 512 keys took 164, in
+// equal stretches 107), the same without a window, 1k to 32k keys, 330 us (6.9 TB/s; fa_decode 355); 8 query heads a KV
 // head 101 us (fa_decode 239).
 //
 // Where items are short and at most two per SM (kDirectItems), each is one CTA's, which writes the results
@@ -589,8 +589,9 @@ cudaError_t launch_d(const CUtensorMap& tk, const CUtensorMap& tv, const ScoredD
 }
 
 constexpr int kMaxCtas = 256;  // one per SM, and what the workspace has slots for
-// Items that are one CTA's each.  8 to 304 items of 1 or 2 stages took 4.4 to 10.9 us and in a line 6.8 to 14.7; 32 to
-// 304 items of up to 8 stages 7 to 28 and 8 to 32; fewer items of 4 stages 7.6 and 7.0; more items 5% more.
+// Items that are one CTA's each.  8 to 304 items of 1 or 2 stages took 4.4 to 10.9 us and in a line
+// 6.8 to 14.7; 32 to 304 items of up to 8 stages 7 to 28 and 8 to 32; fewer items of 4 stages 7.6
+// and 7.0; more items 5% more.
 constexpr int kDirectItems = 304, kDirectStages = 8, kDirectFewStages = 2, kDirectMany = 32;
 
 size_t up256(size_t x) { return (x + 255) & ~size_t(255); }

@@ -84,9 +84,9 @@ cudaError_t launch_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUtenso
 
 }  // namespace
 
-// Units that leave half of the SMs or more without work are split, into parts that still fit the SMs at once: 8 heads
-// of 128 rows and 32768 keys 440 -> 35 us, 8 of 512 and 8192 115 -> 31.  (Up to twice the SMs: 128 units of 16
-// tiles 36 -> 48, 16 of 64 tiles 43 us.)
+// Units that leave half of the SMs or more without work are split, into parts that still fit the
+// SMs at once: 8 heads of 128 rows and 32768 keys 440 -> 35 us, 8 of 512 and 8192 115 -> 30.  (Up to
+// twice the SMs: 128 units of 16 tiles 36 -> 48, 16 of 64 tiles 43 us.)
 int fwd_scored_splits(int B, int Hq, int Hkv, int Sq, int Sk) {
   const int group = Hq / Hkv;
   const long long units = group % 2 == 0 ? 1LL * B * (Hq / 2) * ((Sq + kTileM - 1) / kTileM)
