@@ -716,6 +716,20 @@ def _view(t, name, shape, dev):
     return _Heads(t.data_ptr(), sb, st, sh)
 
 
+def _out_view(t, name, shape, dev, stream):
+    """An output [B, S, H, d] and its fa_heads: the caller's view, or a new tensor."""
+    if t is not None:
+        return t, _view(t, name, shape, dev)
+    t = _new(shape, _BF16, dev, stream)
+    _, S, H, d = shape
+    return t, _Heads(t.data_ptr(), S * H * d, H * d, d)
+
+
+@functools.lru_cache(None)
+def _prep_bwd_bytes(d):
+    return load_library().fa_qk_norm_rope_bwd_workspace_size(d)
+
+
 def _rotation(positions, inv_freq, freq_axis, q_weight, k_weight, B, S, d, dev):
     """(n_axes, rot_dim) of a rotation, checked with the weights."""
     n_axes, rot = 1, 0
@@ -797,13 +811,12 @@ def fa_qk_norm_rope_bwd(q, k, dq_out, dk_out, dv_out=None, positions=None, inv_f
     n_axes, rot = _rotation(positions, inv_freq, freq_axis, q_weight, k_weight, B, S, d, dev)
     vq = None if q_weight is None else _view(q, "q", (B, S, Hq, d), dev)
     vk = None if k_weight is None else _view(k, "k", (B, S, Hkv, d), dev)
-    dq = _new((B, S, Hq, d), _BF16, dev, stream) if dq is None else dq
-    dk = _new((B, S, Hkv, d), _BF16, dev, stream) if dk is None else dk
-    gq, gk, gv = _view(dq, "dq", (B, S, Hq, d), dev), _view(dk, "dk", (B, S, Hkv, d), dev), None
+    dq, gq = _out_view(dq, "dq", (B, S, Hq, d), dev, stream)
+    dk, gk = _out_view(dk, "dk", (B, S, Hkv, d), dev, stream)
+    gv = None
     if dv_out is not None:
         _have(dv_out, "dv_out", _BF16, (B, Hkv, S, d), dev)
-        dv = _new((B, S, Hkv, d), _BF16, dev, stream) if dv is None else dv
-        gv = _view(dv, "dv", (B, S, Hkv, d), dev)
+        dv, gv = _out_view(dv, "dv", (B, S, Hkv, d), dev, stream)
     elif dv is not None:
         raise ValueError("dv is given with dv_out only")
     if q_weight is not None:
@@ -816,7 +829,7 @@ def fa_qk_norm_rope_bwd(q, k, dq_out, dk_out, dv_out=None, positions=None, inv_f
         raise ValueError("dk_weight is given with k_weight only")
     nbytes = 0
     if q_weight is not None or k_weight is not None:
-        workspace = _workspace(workspace, lib.fa_qk_norm_rope_bwd_workspace_size(d), dev, stream)
+        workspace = _workspace(workspace, _prep_bwd_bytes(d), dev, stream)
         nbytes = workspace.nbytes
     st = lib.fa_qk_norm_rope_bwd(vq, vk, dq_out.data_ptr(), dk_out.data_ptr(), _ptr(dv_out), gq, gk,
                                  gv, _ptr(dq_weight), _ptr(dk_weight), _ptr(q_weight),
