@@ -547,7 +547,7 @@ fa_status fa_mask_plan(const int32_t* row_lo, const int32_t* row_hi, int B, int 
  * first and behind the last key that any row of the batch row sees, is never used.  A NaN in a query, or in a
  * key or value between those, reaches the rows that see it; in a key or value, and infinities there, it may
  * reach every row of a 256-row block one of whose rows sees the key.
- * tanh is off by at most 4e-7 of its value or 2^-22, whichever is larger.
+ * t is off by at most 4e-7 of its value or 2^-22 * min(softcap, 256), whichever is larger.
  */
 fa_status fa_fwd_scored(const void* q, const void* k, const void* v, void* o, float* lse, int B,
                         int Hq, int Hkv, int Sq, int Sk, int d, int causal, float scale,

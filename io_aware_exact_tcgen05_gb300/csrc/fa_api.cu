@@ -423,11 +423,13 @@ fa_status make_score(float scale, float softcap, const float* slopes, const void
       if (i < 5) sc.poly4[i] = make_float2(f4, f4);
       sc.poly7[i] = make_float2(f7, f7);
     }
-    // the folded coefficients stay normal numbers in this range (about scale * a^8 the smallest)
-    const bool fits = a >= 0x1p-13 && a <= 0x1p11 && c >= 0x1p-12 && c <= 0x1p12;
-    sc.small[0] = fits ? static_cast<float>(0.25 / a) : -1.f;
-    sc.small[1] = fits ? static_cast<float>(0.7 / a) : -1.f;
-    sc.small[2] = a >= 0x1p-60 && a <= 0x1p60 ? static_cast<float>(1.4 / a) : -1.f;
+    // where the folded coefficients stay normal numbers: the smallest is about scale * a^4 for degree 2,
+    // scale * a^8 for degree 4; those of degree 7 hold the cap alone
+    const bool fits = a <= 0x1p11 && c >= 0x1p-12 && c <= 0x1p12;
+    sc.small[0] = fits && a >= 0x1p-27 ? static_cast<float>(0.25 / a) : -1.f;
+    sc.small[1] = fits && a >= 0x1p-13 ? static_cast<float>(0.7 / a) : -1.f;
+    sc.small[2] = static_cast<float>(std::min(1.4 / a, static_cast<double>(FLT_MAX)));
+    sc.wide = softcap > fa::kWideCap;
   }
   *out = sc;
   return FA_OK;

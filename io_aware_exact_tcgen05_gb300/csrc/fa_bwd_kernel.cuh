@@ -191,8 +191,10 @@ __device__ __forceinline__ BwdUnit bwd_unit_at(const BwdParams& p, int U) {
 }
 
 // Kernel modes.  Scored modes (capped and biased scores, row intervals of a mask plan) are
-// kBwdScored, with kBwdCap and kBwdBias.
-enum : int { kBwdPlain = 0, kBwdDropout = 2, kBwdCap = 4, kBwdBias = 8, kBwdScored = 16 };
+// kBwdScored, with kBwdCap (under a cap above kWideCap kBwdWide as well) and kBwdBias.
+enum : int {
+  kBwdPlain = 0, kBwdDropout = 2, kBwdCap = 4, kBwdBias = 8, kBwdScored = 16, kBwdWide = 32
+};
 
 constexpr int kPartIts = 12;  // least iterations of a part of a split unit
 
@@ -337,6 +339,7 @@ constexpr float kWeightLog2 = 15.f;
 constexpr float kWeightInv = 1.f / 32768.f;
 
 // 32 raw scores to z in place, by the way that holds for the warp's largest magnitude.
+template <bool WIDE>
 __device__ __forceinline__ void scored_cap(uint32_t (&sr)[32], const ScoreArgs& sc, float largest) {
   if (__all_sync(0xffffffffu, largest <= sc.small[1])) {
 #pragma unroll
@@ -349,7 +352,10 @@ __device__ __forceinline__ void scored_cap(uint32_t (&sr)[32], const ScoreArgs& 
     }
   } else {
 #pragma unroll
-    for (int e = 0; e < 32; ++e) sr[e] = __float_as_uint(cap_any(__uint_as_float(sr[e]), sc));
+    for (int e = 0; e < 32; ++e) {
+      const float x = __uint_as_float(sr[e]);
+      sr[e] = __float_as_uint(WIDE ? cap_wide(x, sc) : cap_any(x, sc));
+    }
   }
 }
 
@@ -430,7 +436,7 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
   using Smem = BwdSmem<D>;
   constexpr bool DROP = MODE == kBwdDropout;
   constexpr bool SCORED = (MODE & kBwdScored) != 0;
-  constexpr bool CAP = (MODE & kBwdCap) != 0, BIAS = (MODE & kBwdBias) != 0;
+  constexpr bool CAP = (MODE & kBwdCap) != 0, WIDE = (MODE & kBwdWide) != 0, BIAS = (MODE & kBwdBias) != 0;
   constexpr int NB = Smem::NB;
   constexpr uint32_t kBoxBytes = Smem::kBox * 2;
   extern __shared__ __align__(1024) unsigned char smem_raw[];
@@ -846,7 +852,7 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
               scored_weights<CAP, BIAS, 2>(sr, p.sc, c2, nlc, true, slope2, kb, 0, false, nullptr, row,
                                            pw, pg);
             } else {
-              if constexpr (CAP) scored_cap(sr, p.sc, largest);
+              if constexpr (CAP) scored_cap<WIDE>(sr, p.sc, largest);
               scored_weights<CAP, BIAS, 3>(sr, p.sc, c2, nlc, linear, slope2, kb,
                                            q0 + hf * 64 + cc * 32 + off - key, need_mask,
                                            s.qvis[sb] + hf * 64 + cc * 32, row, pw, pg);

@@ -10,6 +10,10 @@ template <int D>
 cudaError_t launch_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                      const CUtensorMap& tdo, const CUtensorMap& tdq, const ScoredBwdParams& p,
                      bool cap, cudaStream_t stream) {
+  if (cap && p.sc.wide)
+    return p.sc.slopes
+               ? launch_bwd_mode<D, kBwdScored | kBwdCap | kBwdWide | kBwdBias>(tq, tk, tv, tdo, tdq, p, stream)
+               : launch_bwd_mode<D, kBwdScored | kBwdCap | kBwdWide>(tq, tk, tv, tdo, tdq, p, stream);
   if (cap && p.sc.slopes)
     return launch_bwd_mode<D, kBwdScored | kBwdCap | kBwdBias>(tq, tk, tv, tdo, tdq, p, stream);
   if (cap) return launch_bwd_mode<D, kBwdScored | kBwdCap>(tq, tk, tv, tdo, tdq, p, stream);

@@ -391,6 +391,11 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
               for (int e = 0; e < 2 * HALVES; ++e) sc[nt][e] = cap_small(sc[nt][e], p.sc);
+          } else if (p.sc.wide) {
+#pragma unroll
+            for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+              for (int e = 0; e < 2 * HALVES; ++e) sc[nt][e] = cap_wide(sc[nt][e], p.sc);
           } else {
 #pragma unroll
             for (int nt = 0; nt < 2; ++nt)

@@ -165,7 +165,8 @@ __device__ __forceinline__ float sum_f2x4(const uint64_t (&v)[4]) {
 // and biased scores, row intervals of a mask plan) are kModeScored, with kModeCap and kModeBias.
 enum : int {
   kModePlain = 0, kModeKeyBits = 1, kModeDropout = 2,
-  kModeCap = 4, kModeBias = 8, kModeScored = 16
+  kModeCap = 4, kModeBias = 8, kModeScored = 16,
+  kModeWide = 32  // with kModeCap: a cap above kWideCap.  (As a branch of kModeCap: 3% on documents under a cap of 30.)
 };
 
 struct ScoredFwdParams : FwdParams {
@@ -483,13 +484,16 @@ __device__ __forceinline__ void capped_tile(uint32_t t_s, uint32_t t_p, const Sc
 
 // 32 raw scores of a row (keys from column j0 of the tile) -> z in units of log2(e), hidden keys to
 // -inf; p_rel, lo_rel, hi_rel: the row's position and its interval less the tile's first key.
-template <bool CAP, bool BIAS>
+template <bool CAP, bool WIDE, bool BIAS>
 __device__ __forceinline__ void scored_transform(uint32_t (&r)[32], const ScoreArgs& sc, float c,
                                                  bool small, float slope2, int p_rel, int lo_rel,
                                                  int hi_rel) {
   if (CAP && !small) {
 #pragma unroll
-    for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(cap_any(__uint_as_float(r[e]), sc));
+    for (int e = 0; e < 32; ++e) {
+      const float x = __uint_as_float(r[e]);
+      r[e] = __float_as_uint(WIDE ? cap_wide(x, sc) : cap_any(x, sc));
+    }
   } else {
 #pragma unroll
     for (int e = 0; e < 32; e += 2) {
@@ -528,7 +532,7 @@ template <int D, int MODE, typename Smem, typename UnitIndex>
 __device__ __forceinline__ void scored_softmax_warps(Smem& s, const ScoredFwdParams& p,
                                                      uint32_t tmem, int warp, int lane,
                                                      int n_units, UnitIndex unit_index) {
-  constexpr bool CAP = (MODE & kModeCap) != 0, BIAS = (MODE & kModeBias) != 0;
+  constexpr bool CAP = (MODE & kModeCap) != 0, WIDE = (MODE & kModeWide) != 0, BIAS = (MODE & kModeBias) != 0;
   volatile int* abort_flag = &s.abort_flag;
   const ScoreArgs& sc = p.sc;
   const int t = warp >> 2;
@@ -602,6 +606,8 @@ __device__ __forceinline__ void scored_softmax_warps(Smem& s, const ScoredFwdPar
               capped_tile<2, BIAS>(t_s, t_p, sc, sg, bm, l, lr);
             else if (__all_sync(0xffffffffu, most <= sc.small[1]))
               capped_tile<4, BIAS>(t_s, t_p, sc, sg, bm, l, lr);
+            else if constexpr (WIDE)  // one by one, the general way
+              general = true;
             else
               capped_tile<kCapAny, BIAS>(t_s, t_p, sc, sg, bm, l, lr);
           }
@@ -641,7 +647,7 @@ __device__ __forceinline__ void scored_softmax_warps(Smem& s, const ScoredFwdPar
           if constexpr (CAP) tmem_ld32_max_abs(t_s + cc * 32, r, most);
           else tmem_ld32(t_s + cc * 32, r);
           tmem_wait_ld();
-          scored_transform<CAP, BIAS>(r, sc, c,
+          scored_transform<CAP, WIDE, BIAS>(r, sc, c,
                                       !CAP || __all_sync(0xffffffffu, most <= sc.small[1]), slope2,
                                       p_rel - cc * 32, lo - c0 - cc * 32, hi - c0 - cc * 32);
 #pragma unroll

@@ -75,6 +75,10 @@ cudaError_t launch_dm(const CUtensorMap& tq, const CUtensorMap& tk, const CUtens
 template <int D>
 cudaError_t launch_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                      const ScoredFwdParams& p, bool cap, cudaStream_t stream) {
+  if (cap && p.sc.wide)
+    return p.sc.slopes
+               ? launch_dm<D, kModeScored | kModeCap | kModeWide | kModeBias>(tq, tk, tv, p, stream)
+               : launch_dm<D, kModeScored | kModeCap | kModeWide>(tq, tk, tv, p, stream);
   if (cap && p.sc.slopes)
     return launch_dm<D, kModeScored | kModeCap | kModeBias>(tq, tk, tv, p, stream);
   if (cap) return launch_dm<D, kModeScored | kModeCap>(tq, tk, tv, p, stream);

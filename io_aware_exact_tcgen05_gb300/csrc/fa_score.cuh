@@ -11,8 +11,10 @@
 //    six or ten packed multiply-adds for two scores and no special-function instruction; the
 //    coefficients arrive with cap' folded in, those of degrees 2 and 4 with a as well.
 //  * else 1 - 2 / (1 + 2^(2 a s log2 e)): two special-function instructions, off by about 2^-22 of
-//    the cap.
-// Both are far below the rounding of the weights to bf16 (2^-9 of a weight).
+//    the cap, whatever the score.
+// Both are far below the rounding of the weights to bf16 (2^-9 of a weight) while the cap is small: 6e-5 of
+// an exponent at the largest cap that takes the second for every score of a tile (kWideCap; at 2^20 it
+// would be a quarter of one).  Above that each score takes the way that keeps its own accuracy (cap_wide).
 #pragma once
 
 #include "fa_scored.h"
@@ -102,6 +104,16 @@ __device__ __forceinline__ uint64_t cap_factor7(uint64_t s2, const ScoreArgs& sc
 #pragma unroll
   for (int i = 6; i >= 0; --i) m = f2_fma(u, m, f2_pack(sc.poly7[i].x, sc.poly7[i].y));
   return m;
+}
+
+// cap' * tanh(a s) of any score under any cap, off by what its own size allows: the degree-7 form in
+// y = a s, whose coefficients hold cap' alone and fit for every a; past its range cap_any (|tanh| > 0.88).
+__device__ __forceinline__ float cap_wide(float s, const ScoreArgs& sc) {
+  const float y = s * sc.a, u = y * y;
+  float m = sc.poly7[7].x;
+#pragma unroll
+  for (int i = 6; i >= 0; --i) m = fmaf(u, m, sc.poly7[i].x);
+  return fabsf(s) <= sc.small[2] ? y * m : cap_any(s, sc);
 }
 
 // cap' * tanh(a s) of one score with |s| <= small[1].

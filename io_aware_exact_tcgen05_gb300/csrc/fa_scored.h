@@ -68,12 +68,14 @@ cudaError_t launch_mask_plan(const int32_t* lo, const int32_t* hi, int B, int Sq
 
 // Scores z = t - slope * |p - j| in units of log2(e), t = cap * tanh(s * scale / cap) (see
 // fa_score.cuh for the arithmetic).
+constexpr float kWideCap = 256.f;
 struct ScoreArgs {
   float a;             // scale / cap
   float two_a_log2e;   // 2 * a * log2(e)
   float cap_log2e;     // cap * log2(e)
   float neg_inv_cap2;  // -1 / cap_log2e^2
   float small[3];      // |s| up to which the polynomials hold (-1: never)
+  int wide;            // the cap is above kWideCap: scores past the polynomials one by one (cap_wide)
   float2 poly2[3];     // z = s * (poly2[0] + poly2[1] s^2 + ...), each twice (for packed pairs)
   float2 poly4[5];
   float2 poly7[8];     // z = y * (poly7[0] + poly7[1] y^2 + ...), y = a s

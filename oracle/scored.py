@@ -78,7 +78,7 @@ def attend(q, k, v, scale, lo, hi, cap=0.0, slopes=None, dout=None, bounds=False
                 # exponents: d products of a score added in fp32 in any order, the cap, the bias, the sum
                 absS = np.where(seen, np.abs(qq0) @ np.abs(kk0).T * scale, 0.0)
                 far = np.abs(p[:, None] - j[None]) * abs(slope)
-                ez = (d + 8) * F32 * absS + 2.0 ** -20 * (np.abs(t) + far) + (2.0 ** -21 * cap) + 2.0 ** -21
+                ez = (d + 8) * F32 * absS + 2.0 ** -20 * (np.abs(t) + far) + 2.0 ** -21 * min(cap, 256.0) + 2.0 ** -21
                 ez = np.where(seen, ez, 0.0)
                 el = (P * ez).sum(1) + Sk * F32 + 2.0 ** -20 * (1 + np.abs(np.where(live, r["lse"][b, h], 0)))
                 r["tol_lse"][b, h] = el
