@@ -522,7 +522,7 @@ fa_status fa_row_bounds(const int32_t* cu_docs, const int32_t* prefix, int n_doc
                         int32_t* row_hi, int B, int Sq, int Sk, int causal, int window,
                         cudaStream_t stream);
 
-/* Bytes of a mask plan: 8 per row and some 70 per 128 rows and 128 keys. */
+/* Bytes of a mask plan: 8 per row, some 30 per 128 rows and 50 per 128 keys. */
 size_t fa_mask_plan_size(int B, int Sq, int Sk);
 
 /* The tile plan of row_lo, row_hi int32 [B,Sq] (clamped to [0, Sk]; hi <= lo: no keys) into plan
@@ -543,10 +543,11 @@ fa_status fa_mask_plan(const int32_t* row_lo, const int32_t* row_hi, int B, int 
  *   (plan NULL: all) and, when causal != 0, j <= p
  * softcap is 0 or in [2^-20, 2^20]; slopes device fp32[Hq], finite, any sign (constants: no gradient).
  * plan: fa_mask_plan of the same B, Sq, Sk; plan_bytes its size.  Rows without keys give O = 0,
- * LSE = -inf and no gradient.  What q, dout and o hold in rows without keys, and k and v in front of the
- * first and behind the last key that any row of the batch row sees, is never used.  A NaN in a query, or in a
- * key or value between those, reaches the rows that see it; in a key or value, and infinities there, it may
- * reach every row of a 256-row block one of whose rows sees the key.
+ * LSE = -inf and no gradient.  What q, dout and o hold in rows without keys, and k and v in keys that no row
+ * of the batch row sees (causal counted in), is never used.  A NaN in a query, or in a key or value that some row
+ * sees, reaches the rows that see it.  In a key or value, it and infinities may reach O of every row of a
+ * 256-row block one of whose rows sees the key, and dq of every row between the first and the last 128-row block
+ * that see a key of its 128-key tile; in a query or dout between those blocks, dk and dv of the tile.
  * t is off by at most 4e-7 of its value or 2^-22 * min(softcap, 256), whichever is larger.
  */
 fa_status fa_fwd_scored(const void* q, const void* k, const void* v, void* o, float* lse, int B,

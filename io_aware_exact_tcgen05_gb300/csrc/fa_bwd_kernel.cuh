@@ -264,8 +264,7 @@ __device__ __forceinline__ ScoredBwdUnit bwd_unit_at(const ScoredBwdParams& p, i
     const int4 q = __ldg(m.kt + static_cast<size_t>(u.b) * m.nk + kt);
     u.qt_lo = q.x;
     qt_end = q.y;
-    u.klo = q.z;
-    u.kend = min(q.w, p.Sk);
+    u.klo = p.causal ? q.w : q.z;
   }
   u.c0 = kt * kTileN;
   u.exists = true;
@@ -806,13 +805,21 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
         tc_fence_after();
         if constexpr (SCORED) {
           // Rows and keys that nothing is computed for may hold anything, and a weight of 0 does
-          // not cancel a NaN: Q and dO of queries without keys, and K of keys outside of the
-          // hull of all intervals, become zeros before dV, dK and dQ read them.  (Products that read
+          // not cancel a NaN: Q and dO of queries without keys, and K of keys that no query sees,
+          // become zeros before dV, dK and dQ read them.  (Products that read
           // them meanwhile only write what is dropped: dP of those rows and keys.)
           if (guard_ds) {
             if (hf == 1) {
-              if (it == 0 && !key_in)
-                for (int cb = 0; cb < Smem::NB; ++cb) clear_row(s.k[cb], row);
+              if (it == 0 && edge) {
+                bool seen = key < kend;
+                if (p.sc.plan.rows) {
+                  const uint4* bits = p.causal ? p.sc.plan.seen_causal : p.sc.plan.seen;
+                  const size_t at = static_cast<size_t>(bz) * p.n_kt + c0 / kTileN;
+                  seen = __ldg(reinterpret_cast<const uint32_t*>(bits + at) + grp) >> lane & 1u;
+                }
+                if (!seen)
+                  for (int cb = 0; cb < Smem::NB; ++cb) clear_row(s.k[cb], row);
+              }
             } else {
               if (!mbar_wait_warp(&s.do_full, gi & 1, abort_flag, kSiteDOFull)) { ok = false; break; }
               if (s.qvis[sb][row] == kTileN)

@@ -343,12 +343,58 @@ __device__ __forceinline__ ScoredUnit unit_at(const ScoredFwdParams& p, int U) {
 }
 
 // Keys of the unit's tile j (last tiles first) that no row of the unit sees may hold anything, and a weight
-// of 0 does not cancel a NaN.  Only a unit's first and last tile have such keys: V of an edge tile is
-// loaded for a helper warp, which makes zeros of those keys' values and then hands the stage on.
+// of 0 does not cancel a NaN.  Mostly only a unit's first and last tile have such keys; with a plan also those
+// behind the first row's position where the causal rule cuts intervals, and any where its rows' intervals
+// leave keys between them out (padding between documents).  V of such a tile is loaded for a helper warp,
+// which makes zeros of those keys' values and then hands the stage on.
 // (In the softmax warps or in the MMA warp the mere presence of this cost 3 to 5%.)
 __device__ __forceinline__ bool edge_tile(const Unit& u, int j) {
   const int c0 = (u.j0 + u.n_tiles - 1 - j) * kTileN;
   return c0 < u.klo || c0 + kTileN > u.kend;
+}
+
+// The end of the keys from klo on that are each seen by some row of the unit: kend, unless the plan or the
+// causal rule leaves some out.  (Apart from unit_at: there, in every warp, it cost 1%.)
+__device__ __forceinline__ int all_seen_until(const ScoredUnit& u, const ScoredFwdParams& p) {
+  if (!p.sc.plan.rows) return u.kend;
+  const int t = u.r0 / kTileM;
+  const int4* qt = p.sc.plan.qt + static_cast<size_t>(u.b) * p.sc.plan.nq + t;
+  int4 r = __ldg(qt);
+  if (!p.pack_heads && t + 1 < p.sc.plan.nq) {
+    const int4 r1 = __ldg(qt + 1);
+    r.z |= r1.z | (r.y > 0 && r1.y > 0 && (r.y < r1.x || r1.y < r.x));
+    r.w |= r1.w;
+  }
+  if (r.z) return 0;
+  return p.causal && r.w ? min(u.kend, u.r0 + u.off + 1) : u.kend;  // the rule hides those from no row
+}
+
+// Which keys of the tile from key c0 any row of the unit sees: lane w (and w + 4, ..) has those of keys
+// [32 w, +32).
+__device__ __forceinline__ uint32_t keys_seen(const ScoredUnit& u, const ScoredFwdParams& p, bool hull, int c0,
+                                              int lane) {
+  if (hull) {
+    const int at = c0 + 32 * (lane & 3);
+    return bits_below(u.kend - at) & ~bits_below(u.klo - at);
+  }
+  const int2* rows = p.sc.plan.rows + static_cast<size_t>(u.b) * p.Sq;
+  uint32_t mine = 0u;
+#pragma unroll 1
+  for (int w = 0; w < 4; ++w) {
+    const int at = c0 + 32 * w;
+    uint32_t bits = 0u;
+#pragma unroll 1
+    for (int k = 0; k < (p.pack_heads ? 4 : 8); ++k) {  // (slots of packed heads have the same rows)
+      const int i = u.r0 + 32 * k + lane;
+      if (i >= u.sq) continue;
+      const int2 r = __ldg(rows + i);
+      const int hi = p.causal ? min(r.y, i + u.off + 1) : r.y;
+      if (hi > r.x) bits |= bits_below(hi - at) & ~bits_below(r.x - at);
+    }
+    bits = __reduce_or_sync(0xffffffffu, bits);
+    if ((lane & 3) == w) mine = bits;
+  }
+  return mine;
 }
 
 template <typename Smem>
@@ -360,22 +406,25 @@ __device__ __forceinline__ void edge_warp(Smem& s, const ScoredFwdParams& p, int
     const int G = static_cast<int>(gridDim.x), c = static_cast<int>(blockIdx.x);
     const int U = k * G + ((k & 1) ? (G - 1 - c) : c);
     if (U >= n_units) continue;
-    const Unit un = unit_at(p, U);
-    for (int e = 0; e < (un.n_tiles > 1 ? 2 : un.n_tiles); ++e) {
-      const int j = e == 0 ? 0 : un.n_tiles - 1;
+    ScoredUnit un = unit_at(p, U);
+    const int until = all_seen_until(un, p);
+    const bool hull = until == un.kend;  // which klo and kend tell all of
+    un.kend = until;
+    for (int j = 0; j < un.n_tiles; ++j) {
       if (!edge_tile(un, j)) continue;
       const int st = (g + j) % Smem::NS;
+      const int c0 = (un.j0 + un.n_tiles - 1 - j) * kTileN;
+      const uint32_t seen = keys_seen(un, p, hull, c0, lane);
 #pragma unroll
       for (int i = 0; i < Smem::NS; ++i)
         if (i == st) {
           if (!mbar_wait_warp(&s.v_raw[i], uses[i] & 1, abort_flag, kSiteVRaw)) return;
           ++uses[i];
         }
-      const int c0 = (un.j0 + un.n_tiles - 1 - j) * kTileN;
       const uint32_t v0 = smem_u32(s.v[st][0]);
-      for (int i = lane; i < kTileN * Smem::NB; i += 32) {  // box after box of 128-byte rows
-        const int key = c0 + i % kTileN;
-        if (key >= un.klo && key < un.kend) continue;
+      for (int i = lane; i < kTileN * Smem::NB; i += 32) {  // box after box of 128-byte rows, a key each
+        const uint32_t word = __shfl_sync(0xffffffffu, seen, i >> 5 & 3);
+        if (word >> lane & 1) continue;
 #pragma unroll
         for (int ch = 0; ch < 8; ++ch)
           asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(v0 + i * 128 + ch * 16), "r"(0)
@@ -843,7 +892,7 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
       for (int k = 0; ok && k * static_cast<int>(gridDim.x) < n_units; ++k) {
         const int U = unit_index(k);
         if (U >= n_units) continue;
-        const Unit un = unit_at(p, U);
+        auto un = unit_at(p, U);
         if (un.n_tiles == 0) continue;
         if (uq > 0 && !mbar_wait(&s.q_free, (uq - 1) & 1, abort_flag, kSiteQ)) break;
         mbar_arrive_expect_tx(&s.bar_q, (un.active1 ? 2 : 1) * NB * kBoxBytes);
@@ -854,6 +903,7 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
         }
         ++uq;
         const int zkv = un.bz * p.Hkv + un.hk;
+        if constexpr (SCORED) un.kend = all_seen_until(un, p);
         for (int j = 0; j < un.n_tiles; ++j, ++g) {
           const int st = g % NS;
           const int use = g / NS;

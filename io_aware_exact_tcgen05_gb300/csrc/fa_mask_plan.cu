@@ -12,6 +12,7 @@
 #include <cuda_runtime.h>
 
 #include "fa_internal.h"
+#include "fa_score.cuh"
 #include "fa_scored.h"
 #include "sm103_ptx.cuh"
 
@@ -62,11 +63,17 @@ __device__ __forceinline__ int key_tiles(int4 r) {
   return r.y > r.x ? (r.y + 127) / 128 - r.x / 128 : 0;
 }
 
-// The intervals clamped to [0, Sk], and their extremes over each 128-row tile.
+// The intervals clamped to [0, Sk], and their extremes over each 128-row tile.  Where the interval of
+// every row with keys meets or touches that of the row with keys before it, as with documents, windows and
+// prefixes, no key between the extremes is unseen; only else is it looked for, every row's end against
+// every interval.
 __global__ void __launch_bounds__(128)
     fa_plan_rows_kernel(const int32_t* lo, const int32_t* hi, int Sq, int Sk, const MaskPlan m) {
-  __shared__ int red[4][4];
+  __shared__ int2 row[128];
+  __shared__ int4 red[4];       // of a warp's rows: min lo, max hi, intervals apart, past their positions
+  __shared__ int2 ends[4][2];   // the first and the last interval of a warp's rows
   const int b = blockIdx.y, t = blockIdx.x;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int i = t * 128 + threadIdx.x;
   int l = 0, h = 0;
   if (i < Sq) {
@@ -77,24 +84,43 @@ __global__ void __launch_bounds__(128)
     const_cast<int2*>(m.rows)[idx] = make_int2(l, h);
   }
   const bool live = h > l;
+  const uint32_t alive = __ballot_sync(0xffffffffu, live);
+  const uint32_t before = alive & ((1u << lane) - 1);
+  const int last = before ? 31 - __clz(before) : lane;
+  const int pl = __shfl_sync(0xffffffffu, l, last), ph = __shfl_sync(0xffffffffu, h, last);
+  const bool breaks = __any_sync(0xffffffffu, live && before && (l > ph || pl > h));
+  const bool past = __any_sync(0xffffffffu, live && h > i + Sk - Sq + 1);
   const int mn_l = __reduce_min_sync(0xffffffffu, live ? l : 0x7fffffff);
   const int mx_h = __reduce_max_sync(0xffffffffu, live ? h : 0);
-  const int mx_l = __reduce_max_sync(0xffffffffu, live ? l : 0);
-  const int mn_h = __reduce_min_sync(0xffffffffu, live ? h : 0x7fffffff);
-  const int w = threadIdx.x >> 5;
-  if ((threadIdx.x & 31) == 0) {
-    red[w][0] = mn_l;
-    red[w][1] = mx_h;
-    red[w][2] = mx_l;
-    red[w][3] = mn_h;
-  }
+  row[threadIdx.x] = make_int2(l, h);
+  if (live && !before) ends[w][0] = make_int2(l, h);
+  if (live && !(alive >> lane >> 1)) ends[w][1] = make_int2(l, h);
+  if (lane == 0) red[w] = make_int4(mn_l, mx_h, breaks, past);
   __syncthreads();
+  int first = 0x7fffffff, end = 0, prev = -1;
+  bool apart = false, beyond = false;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const int4 r = red[k];
+    if (r.y == 0) continue;
+    if (prev >= 0 && (ends[k][0].x > ends[prev][1].y || ends[prev][1].x > ends[k][0].y)) apart = true;
+    prev = k;
+    first = min(first, r.x);
+    end = max(end, r.y);
+    apart = apart || r.z;
+    beyond = beyond || r.w;
+  }
+  int gaps = 0;
+  if (apart) {  // (CTA-uniform)
+    bool bare = live && h < end;  // key h, which this row does not see, is in no row's interval
+    if (bare) {
+#pragma unroll 8
+      for (int k = 0; k < 128; ++k) bare = bare && !(row[k].x <= h && row[k].y > h);
+    }
+    gaps = __syncthreads_or(bare);
+  }
   if (threadIdx.x == 0) {
-    int4 r = make_int4(min(min(red[0][0], red[1][0]), min(red[2][0], red[3][0])),
-                       max(max(red[0][1], red[1][1]), max(red[2][1], red[3][1])),
-                       max(max(red[0][2], red[1][2]), max(red[2][2], red[3][2])),
-                       min(min(red[0][3], red[1][3]), min(red[2][3], red[3][3])));
-    if (r.y == 0) r = make_int4(0, 0, 0, 0);
+    const int4 r = end > 0 ? make_int4(first, end, gaps ? 1 : 0, beyond ? 1 : 0) : make_int4(0, 0, 0, 0);
     const size_t at = static_cast<size_t>(b) * m.nq + t;
     const_cast<int4*>(m.qt)[at] = r;
     const_cast<int*>(m.work)[at] = key_tiles(r);
@@ -102,34 +128,103 @@ __global__ void __launch_bounds__(128)
   griddep_launch_dependents();
 }
 
-// First and end query tile whose hull of intervals meets each key tile, and the hull of theirs;
-// the work of key tiles and of pairs of query tiles.  A warp per key tile.
-__global__ void __launch_bounds__(256) fa_plan_keys_kernel(const MaskPlan m) {
+// The bits of all lanes together; true where they are all of those there.
+__device__ __forceinline__ bool gather_bits(uint32_t (&bits)[4], const uint32_t (&there)[4]) {
+  bool all = true;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    bits[w] = __reduce_or_sync(0xffffffffu, bits[w]);
+    all = all && bits[w] == there[w];
+  }
+  return all;
+}
+
+// First and end query tile whose hull of intervals meets each key tile, and which of its keys any row sees,
+// also under the causal rule; the work of key tiles and of pairs of query tiles.  A warp per key tile.  The
+// rows of a query tile are looked at one by one only where no hull holds the whole tile and its own does not
+// tell: where keys within it are in no row's interval, or where the causal rule cuts into it.
+__global__ void __launch_bounds__(256) fa_plan_keys_kernel(const MaskPlan m, int Sq, int Sk) {
   const int b = blockIdx.y, lane = threadIdx.x & 31;
   const int kt = blockIdx.x * 8 + (threadIdx.x >> 5);
   griddep_wait();
   const int4* qt = m.qt + static_cast<size_t>(b) * m.nq;
-  const int c0 = kt * 128;
+  const int c0 = kt * 128, c1 = min(c0 + 128, Sk), off = Sk - Sq;
   if (kt < m.nk) {
-    int first = 0x7fffffff, end = 0, lo = 0x7fffffff, hi = 0;
-#pragma unroll 4
-    for (int t = lane; t < m.nq; t += 32) {
-      const int4 r = qt[t];
-      if (r.x < c0 + 128 && r.y > c0) {
-        first = min(first, t);
-        end = t + 1;
-        lo = min(lo, r.x);
-        hi = max(hi, r.y);
+    int first = 0x7fffffff, end = 0;
+    bool whole = false, whole_causal = false;  // a hull without gaps holds the tile
+    for (int t0 = lane; t0 - lane < m.nq; t0 += 128) {
+      int4 r[4];
+      bool meets[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
+        r[u] = t0 + 32 * u < m.nq ? qt[t0 + 32 * u] : make_int4(0, 0, 0, 0);
+#pragma unroll
+      for (int u = 0; u < 4; ++u) meets[u] = r[u].x < c1 && r[u].y > c0;
+      // (none does mostly, where documents are many)
+      if (!__any_sync(0xffffffffu, meets[0] || meets[1] || meets[2] || meets[3])) continue;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (t0 - lane + 32 * u >= m.nq) break;
+        if (!meets[u]) continue;
+        first = min(first, t0 + 32 * u);
+        end = t0 + 32 * u + 1;
+        const bool holds = r[u].x <= c0 && r[u].y >= c1 && !r[u].z;
+        whole = whole || holds;
+        whole_causal = whole_causal || (holds && (!r[u].w || (t0 + 32 * u) * 128 + off >= c1 - 1));
       }
     }
     first = __reduce_min_sync(0xffffffffu, first);
     end = __reduce_max_sync(0xffffffffu, end);
-    lo = __reduce_min_sync(0xffffffffu, lo);
-    hi = __reduce_max_sync(0xffffffffu, hi);
     if (end == 0) first = 0;
+    whole = __any_sync(0xffffffffu, whole);
+    whole_causal = __any_sync(0xffffffffu, whole_causal);
+    const size_t at = static_cast<size_t>(b) * m.nk + kt;
+    uint32_t there[4] = {0u, 0u, 0u, 0u};
+    add_span(there, 0, c1 - c0);
+    uint32_t any[4], causal[4];
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      any[w] = whole ? there[w] : 0u;
+      causal[w] = whole_causal ? there[w] : 0u;
+    }
+    for (int t0 = first & ~31; t0 < end && !(whole && whole_causal); t0 += 32) {
+      const int t = t0 + lane;
+      const int4 r = t < m.nq ? qt[t] : make_int4(0, 0, 0, 0);
+      bool rows = false;
+      if (r.x < c1 && r.y > c0) {
+        // positions of the tile's first and last row
+        const int p0 = t * 128 + off, p1 = min(t * 128 + 127, Sq - 1) + off;
+        const bool cut = r.w && p0 < c1 - 1;
+        if (!r.z) {
+          add_span(any, r.x - c0, r.y - c0);
+          if (!cut) add_span(causal, r.x - c0, r.y - c0);
+        }
+        rows = r.z || (cut && p1 >= c0);
+      }
+      uint32_t look = __ballot_sync(0xffffffffu, rows);
+      do {
+        if (look) {
+          const int i0 = (t0 + __ffs(look) - 1) * 128 + lane;
+          look &= look - 1;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int i = i0 + 32 * k;
+            if (i >= Sq) continue;
+            const int2 s = m.rows[static_cast<size_t>(b) * Sq + i];
+            add_span(any, s.x - c0, s.y - c0);
+            const int h = min(s.y, i + off + 1);
+            if (h > s.x) add_span(causal, s.x - c0, h - c0);
+          }
+        }
+        whole = gather_bits(any, there);
+        whole_causal = gather_bits(causal, there);
+      } while (look && !(whole && whole_causal));
+    }
     if (lane == 0) {
-      const size_t at = static_cast<size_t>(b) * m.nk + kt;
-      const_cast<int4*>(m.kt)[at] = make_int4(first, end, lo, hi);
+      const int full = c1 == c0 + 128;  // (keys that are not there are not seen)
+      const_cast<int4*>(m.kt)[at] = make_int4(first, end, whole && full ? 0 : kUnseen, whole_causal && full ? 0 : kUnseen);
+      const_cast<uint4*>(m.seen)[at] = make_uint4(any[0], any[1], any[2], any[3]);
+      const_cast<uint4*>(m.seen_causal)[at] = make_uint4(causal[0], causal[1], causal[2], causal[3]);
       const_cast<int*>(m.work)[static_cast<size_t>(m.B) * (m.nq + m.np) + at] = end - first;
     }
   }
@@ -187,7 +282,7 @@ cudaError_t launch_mask_plan(const int32_t* lo, const int32_t* hi, int B, int Sq
   cudaError_t e = cudaGetLastError();
   if (e == cudaSuccess)
     e = launch_dependent(fa_plan_keys_kernel, dim3((std::max(m.nk, m.np) + 7) / 8, B), dim3(256), 0, stream,
-                         m);
+                         m, Sq, Sk);
   const long long most = 1ll * B * std::max(m.nq, m.nk);
   if (e == cudaSuccess)
     e = launch_dependent(fa_plan_order_kernel, dim3(static_cast<unsigned int>((most + 7) / 8), 4),

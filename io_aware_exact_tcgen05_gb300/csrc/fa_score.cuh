@@ -37,6 +37,17 @@ __device__ __forceinline__ void tmem_ld32_max_abs(uint32_t taddr, uint32_t (&r)[
       : "r"(taddr));
 }
 
+// The n lowest bits of a word (none for n < 0, all for n > 32).
+__device__ __forceinline__ uint32_t bits_below(int n) {
+  return static_cast<uint32_t>((1ull << max(0, min(n, 32))) - 1);
+}
+
+// Sets bits [a, e) of 128, a <= e, of which what lies outside falls off.
+__device__ __forceinline__ void add_span(uint32_t (&bits)[4], int a, int e) {
+#pragma unroll
+  for (int w = 0; w < 4; ++w) bits[w] |= bits_below(e - 32 * w) & ~bits_below(a - 32 * w);
+}
+
 // Two fp32 values -> f16 pair (round to nearest even), and back (exact).
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;

@@ -15,11 +15,15 @@ namespace fa {
 // What fa_mask_plan writes, as the attention kernels read it (all in the caller's buffer).
 // rows == nullptr: no plan, every key is visible.
 struct MaskPlan {
-  const int4* qt;    // [B][nq]  per 128-row tile, over its rows with keys: min lo, max hi, max lo, min hi
-                     //          (0, 0, 0, 0 where no row has keys)
+  const int4* qt;    // [B][nq]  per 128-row tile, over its rows with keys: min lo, max hi, whether a key
+                     //          between them is in no row's interval, whether a row's interval goes
+                     //          past its own position (0, 0, 0, 0 where no row has keys)
+  const uint4* seen; // [B][nk]  which of the 128 keys of a tile any row of the batch row sees
+  const uint4* seen_causal;  // the same under the causal rule
+  const int4* kt;    // [B][nk]  first and end query tile that may see the 128-key tile; 0 where every key of
+                     //          it is seen (by some row of the batch row), else kUnseen; the same
+                     //          under the causal rule
   const int2* rows;  // [B][Sq]  lo, hi of each row; (0, 0) without keys
-  const int4* kt;    // [B][nk]  first and end query tile that may see the 128-key tile, and the hull
-                     //          of their rows' intervals
   // tiles (batch row * tiles of a row + tile) in the order of their work, most first
   const int* by_q1;    // [B * nq]  query tiles by key tiles
   const int* by_q2;    // [B * np]  pairs of query tiles, likewise
@@ -29,10 +33,12 @@ struct MaskPlan {
   int B, nq, np, nk;
 };
 
-// 32-bit words of a plan: qt, kt, rows, by_q1, by_q2, by_k, by_k_row, work.
+constexpr int kUnseen = 0x7fffffff;
+
+// 32-bit words of a plan: qt, seen, seen_causal, kt, rows, by_q1, by_q2, by_k, by_k_row, work.
 inline size_t mask_plan_words(long long B, long long Sq, long long Sk) {
   const long long nq = (Sq + 127) / 128, np = (nq + 1) / 2, nk = (Sk + 127) / 128;
-  return static_cast<size_t>(B * (4 * nq + 4 * nk + 2 * Sq + 2 * (nq + np + nk) + nk));
+  return static_cast<size_t>(B * (4 * nq + 12 * nk + 2 * Sq + 2 * (nq + np + nk) + nk));
 }
 
 inline MaskPlan mask_plan_view(const void* base, long long B, long long Sq, long long Sk) {
@@ -44,9 +50,15 @@ inline MaskPlan mask_plan_view(const void* base, long long B, long long Sq, long
   m.nk = static_cast<int>((Sk + 127) / 128);
   const int* w = static_cast<const int*>(base);
   m.qt = reinterpret_cast<const int4*>(w);
-  m.kt = reinterpret_cast<const int4*>(w + 4 * B * m.nq);
-  m.rows = reinterpret_cast<const int2*>(w + 4 * B * (m.nq + m.nk));
-  m.by_q1 = w + 4 * B * (m.nq + m.nk) + 2 * B * Sq;
+  w += 4 * B * m.nq;
+  m.seen = reinterpret_cast<const uint4*>(w);
+  w += 4 * B * m.nk;
+  m.seen_causal = reinterpret_cast<const uint4*>(w);
+  w += 4 * B * m.nk;
+  m.kt = reinterpret_cast<const int4*>(w);
+  w += 4 * B * m.nk;
+  m.rows = reinterpret_cast<const int2*>(w);
+  m.by_q1 = w + 2 * B * Sq;
   m.by_q2 = m.by_q1 + B * m.nq;
   m.by_k = m.by_q2 + B * m.np;
   m.by_k_row = m.by_k + B * m.nk;
