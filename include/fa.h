@@ -542,7 +542,8 @@ fa_status fa_mask_plan(const int32_t* row_lo, const int32_t* row_hi, int B, int 
  *   O = softmax(z) V, LSE_i = ln sum_j exp(z_ij), over the keys of the row's interval in the plan
  *   (plan NULL: all) and, when causal != 0, j <= p
  * softcap is 0 or in [2^-20, 2^20]; slopes device fp32[Hq], finite, any sign (constants: no gradient).
- * plan: fa_mask_plan of the same B, Sq, Sk; plan_bytes its size.  Rows without keys give O = 0,
+ * plan: fa_mask_plan of the same B, Sq, Sk; plan_bytes its size.  (A plan of others, with as many bytes, is
+ * refused on the device: the outputs are not computed, and fa_device_status says so.)  Rows without keys give O = 0,
  * LSE = -inf and no gradient.  What q, dout and o hold in rows without keys, and k and v in keys that no row
  * of the batch row sees (causal counted in), is never used.  A NaN in a query, or in a key or value that some row
  * sees, reaches the rows that see it.  In a key or value, it and infinities may reach O of every row of a
@@ -589,7 +590,8 @@ fa_status fa_decode_scored(const void* q, const void* k_cache, const void* v_cac
                            size_t workspace_bytes, cudaStream_t stream);
 
 /* Reads the device status words of the current device (this synchronises the
-   device).  Returns FA_OK or FA_ERR_TIMEOUT; *code_out (may be NULL) receives
+   device).  Returns FA_OK, FA_ERR_TIMEOUT, or FA_ERR_INVALID_ARG where a kernel
+   was given a mask plan of other sizes (code 4); *code_out (may be NULL) receives
    the raw word (low 16 bits: error code, high 16 bits: wait site).  When
    clear != 0 the words are reset to 0 afterwards. */
 fa_status fa_device_status(unsigned int* code_out, int clear);

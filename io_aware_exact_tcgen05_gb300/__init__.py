@@ -883,6 +883,7 @@ def fa_mask_plan(row_lo, row_hi, Sk: int, plan=None, stream=None):
     st = lib.fa_mask_plan(row_lo.data_ptr(), row_hi.data_ptr(), B, Sq, Sk, plan.data_ptr(), nbytes,
                           _stream(stream))
     _check(st, "fa_mask_plan")
+    plan.fa_sizes = B, Sq, Sk  # for the calls that take it: other sizes may have as many bytes
     return plan
 
 
@@ -899,6 +900,8 @@ def _scored_args(q, k, v, slopes, plan, dev):
         return B, Hq, Hkv, Sq, Sk, d, 0
     nbytes = _plan_bytes(B, Sq, Sk)
     _have(plan, "plan", _U8, (nbytes,), dev)
+    if getattr(plan, "fa_sizes", (B, Sq, Sk)) != (B, Sq, Sk):
+        raise ValueError(f"plan was made for B, Sq, Sk = {plan.fa_sizes}, the call has {(B, Sq, Sk)}")
     return B, Hq, Hkv, Sq, Sk, d, nbytes
 
 

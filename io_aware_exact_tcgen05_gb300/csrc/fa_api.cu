@@ -843,6 +843,8 @@ fa_status fa_device_status(unsigned int* code_out, int clear) {
                          fa::read_bwd_scored_status(clear != 0) |
                          fa::read_decode_scored_status(clear != 0);
   if (code_out) *code_out = w;
+  if ((w & 0xffffu) == 4u)
+    return fail(FA_ERR_INVALID_ARG, "a kernel got a mask plan of other sizes (status word 0x%08x)", w);
   if (w != 0) return fail(FA_ERR_TIMEOUT, "device status word 0x%08x", w);
   return ok();
 }

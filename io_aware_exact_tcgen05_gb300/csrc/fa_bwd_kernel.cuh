@@ -85,7 +85,7 @@ constexpr uint32_t kTmemCols = 512;
 
 enum : unsigned int {
   kSiteKV = 1, kSiteQFull, kSiteQEmpty, kSiteS, kSiteP, kSiteDP, kSiteDS, kSiteDQFull,
-  kSiteDQEmpty, kSiteDKV, kSiteDrain, kSiteAlign, kSiteStat, kSiteDOFull, kSiteDOEmpty
+  kSiteDQEmpty, kSiteDKV, kSiteDrain, kSiteAlign, kSiteStat, kSiteDOFull, kSiteDOEmpty, kSitePlan
 };
 
 template <int D>
@@ -458,6 +458,12 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
     return k * G + ((k & 1) ? (G - 1 - cb) : cb);
   };
 
+  if constexpr (SCORED) {
+    if (!plan_fits(p.sc.plan, p.Sq, p.Sk)) {
+      if (threadIdx.x == 0 && blockIdx.x == 0) raise_status(kStatusPlan, kSitePlan);
+      return;
+    }
+  }
   if (threadIdx.x == 0) {
     mbar_init(&s.kv_full, 1);
     for (int i = 0; i < Smem::kQStages; ++i) {
@@ -1157,6 +1163,7 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
 template <int D>
 __global__ void __launch_bounds__(256) fa_bwd_join(const ScoredBwdParams p) {
   griddep_wait();
+  if (!plan_fits(p.sc.plan, p.Sq, p.Sk)) return;
   const ScoredBwdUnit un = bwd_unit_at(p, static_cast<int>(blockIdx.x) * p.split.n);
   if (un.parts == 1) return;
   const size_t rows = static_cast<size_t>(p.B) * p.Hkv * p.Sk;

@@ -59,7 +59,7 @@ constexpr uint32_t kTmemCols = 512;
 // wait-site ids reported in the status word
 enum : unsigned int {
   kSiteQ = 1, kSiteKFree, kSiteVFree, kSiteKFull, kSiteVFull, kSitePFull, kSiteSFull,
-  kSiteOFull, kSiteDrain, kSiteVRaw
+  kSiteOFull, kSiteDrain, kSiteVRaw, kSitePlan
 };
 
 template <int D>
@@ -846,6 +846,12 @@ __global__ void __launch_bounds__(kThreadsOf<MODE>, 1)
     return k * G + ((k & 1) ? (G - 1 - c) : c);
   };
 
+  if constexpr (SCORED) {
+    if (!plan_fits(p.sc.plan, p.Sq, p.Sk)) {
+      if (threadIdx.x == 0 && blockIdx.x == 0) raise_status(kStatusPlan, kSitePlan);
+      return;
+    }
+  }
   if (threadIdx.x == 0) {
     mbar_init(&s.bar_q, 1);
     mbar_init(&s.q_free, 1);

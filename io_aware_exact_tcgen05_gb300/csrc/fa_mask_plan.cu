@@ -124,6 +124,7 @@ __global__ void __launch_bounds__(128)
     const size_t at = static_cast<size_t>(b) * m.nq + t;
     const_cast<int4*>(m.qt)[at] = r;
     const_cast<int*>(m.work)[at] = key_tiles(r);
+    if (at == 0) *const_cast<int4*>(m.sizes) = make_int4(m.B, Sq, Sk, kPlanMark);
   }
   griddep_launch_dependents();
 }

@@ -37,6 +37,15 @@ __device__ __forceinline__ void tmem_ld32_max_abs(uint32_t taddr, uint32_t (&r)[
       : "r"(taddr));
 }
 
+// Whether the plan (if any) was made for these sizes.  The tiles and offsets in one of others would lead out of the
+// tensors; a kernel that gets one records kStatusPlan and returns.
+constexpr unsigned int kStatusPlan = 4u;
+__device__ __forceinline__ bool plan_fits(const MaskPlan& m, int Sq, int Sk) {
+  if (!m.rows) return true;
+  const int4 s = __ldg(m.sizes);
+  return s.x == m.B && s.y == Sq && s.z == Sk && s.w == kPlanMark;
+}
+
 // The n lowest bits of a word (none for n < 0, all for n > 32).
 __device__ __forceinline__ uint32_t bits_below(int n) {
   return static_cast<uint32_t>((1ull << max(0, min(n, 32))) - 1);

@@ -15,6 +15,7 @@ namespace fa {
 // What fa_mask_plan writes, as the attention kernels read it (all in the caller's buffer).
 // rows == nullptr: no plan, every key is visible.
 struct MaskPlan {
+  const int4* sizes; // B, Sq, Sk, kPlanMark: what the kernels know a plan of theirs by (plan_fits)
   const int4* qt;    // [B][nq]  per 128-row tile, over its rows with keys: min lo, max hi, whether a key
                      //          between them is in no row's interval, whether a row's interval goes
                      //          past its own position (0, 0, 0, 0 where no row has keys)
@@ -35,10 +36,12 @@ struct MaskPlan {
 
 constexpr int kUnseen = 0x7fffffff;
 
-// 32-bit words of a plan: qt, seen, seen_causal, kt, rows, by_q1, by_q2, by_k, by_k_row, work.
+constexpr int kPlanMark = 0x6d61736b;
+
+// 32-bit words of a plan: sizes, qt, seen, seen_causal, kt, rows, by_q1, by_q2, by_k, by_k_row, work.
 inline size_t mask_plan_words(long long B, long long Sq, long long Sk) {
   const long long nq = (Sq + 127) / 128, np = (nq + 1) / 2, nk = (Sk + 127) / 128;
-  return static_cast<size_t>(B * (4 * nq + 12 * nk + 2 * Sq + 2 * (nq + np + nk) + nk));
+  return static_cast<size_t>(4 + B * (4 * nq + 12 * nk + 2 * Sq + 2 * (nq + np + nk) + nk));
 }
 
 inline MaskPlan mask_plan_view(const void* base, long long B, long long Sq, long long Sk) {
@@ -49,6 +52,8 @@ inline MaskPlan mask_plan_view(const void* base, long long B, long long Sq, long
   m.np = (m.nq + 1) / 2;
   m.nk = static_cast<int>((Sk + 127) / 128);
   const int* w = static_cast<const int*>(base);
+  m.sizes = reinterpret_cast<const int4*>(w);
+  w += 4;
   m.qt = reinterpret_cast<const int4*>(w);
   w += 4 * B * m.nq;
   m.seen = reinterpret_cast<const uint4*>(w);

@@ -17,7 +17,7 @@ namespace fa {
 
 // Device status word, one per translation unit (internal linkage, so no
 // relocatable device code is needed): 0 = OK, otherwise the first error raised
-// by any CTA of a kernel in that unit.  Low 16 bits: 1 = a wait timed out.
+// by any CTA of a kernel in that unit.  Low 16 bits: 1 = a wait timed out, 4 = a mask plan of other sizes.
 // Upper 16 bits: the site id of the wait.
 static __device__ unsigned int g_status = 0;
 
