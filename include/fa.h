@@ -459,8 +459,8 @@ typedef struct {
  *   y = u with its first rot_dim channels turned: pair i, (a, b) -> (a c_i - b s_i, b c_i + a s_i),
  *       c_i, s_i = cos, sin of position[freq_axis[i]] * inv_freq[i] (radians); the pairs are channels
  *       (i, i + rot_dim / 2), or (2 i, 2 i + 1) when interleaved != 0
- * and v is copied.  Arithmetic is fp32, y is rounded to bf16 once; angles are exact to 2^-31 turns
- * for every position.
+ * and v is copied.  Arithmetic is fp32, y is rounded to bf16 once; angles are reduced exactly, to 2^-31 turns
+ * for every position and frequency, and c_i, s_i off by less than 2^-19.
  *   q view [B,S,Hq,d]; k, v views [B,S,Hkv,d]; v and v_out are NULL together
  *   q_weight, k_weight  bf16 [d], 16-byte aligned, or NULL: no norm
  *   positions  int32 [n_axes,B,S], any value; NULL: the token's row (below) on every axis

@@ -15,9 +15,10 @@
 // whose angles its lanes work out together, once, in shared memory.
 //
 // Angles: a position times a frequency in turns, as 64-bit fixed point, of which whole turns
-// fall off by themselves: exact to 2^-31 turns for any 32-bit position, without 64-bit floating
-// point.  Sine and cosine of the remainder (within half a turn) are the fast ones, off by 2^-20.5 at
-// most, a 2000th of what the rounding of y to bf16 may do.
+// fall off by themselves: exact to 2^-31 turns for any 32-bit position and any frequency below 2^24, without
+// 64-bit floating point.  The remainder (within half a turn) goes to fp32, 2^-25 and 2^-26 turns for its two roundings;
+// its sine and cosine are the fast ones, off by 2^-20.5 at most: 2^-19.9 together, a 2000th of what the rounding
+// of y to bf16 may do.
 //
 // Sums over a head and the weights' gradients are held in fp32; a CTA adds its share of dw in a
 // fixed order and a second kernel adds the CTAs' likewise: same result every time.
@@ -28,8 +29,9 @@
 //
 // Measured (GB300, inputs from HBM): 2 x 8192 tokens of 16 + 2 x 16 heads, d = 128 forward 71 us (5.7 TB/s,
 // 85% of the measured copy); 3 x 2777 tokens of 28 + 2 x 4 heads with three axes backward 52 us (4.3 TB/s): the
-// chain of two reductions a step at 16 warps per SM, which is what the registers allow (a token's positions
-// loaded a token ahead, or the sums of dw in shared memory, changed nothing).
+// chain of two reductions a step at 16 warps per SM, which is what the registers allow, with 72 bytes of a thread
+// spilled (forward: 64 registers and 44 bytes).  (A token's positions loaded a token ahead, or the sums of dw in
+// shared memory, changed nothing.)
 #include <algorithm>
 
 #include <cuda_bf16.h>
@@ -49,18 +51,21 @@ constexpr int kFwdCtasPerSm = 4;
 constexpr int kBwdCtasPerSm = 2;
 constexpr int kMaxPartialRows = 512;  // most CTAs of a backward pass
 
-// f / (2 pi) turns as a 64-bit fixed-point fraction (whole turns dropped); 1 / (2 pi) in 64 bits.
+// f / (2 pi) turns as a 64-bit fixed-point fraction (whole turns dropped), cut off below 2^-64: 1 / (2 pi) in
+// 128 bits, of which a position and a frequency up to 2^24 take 55 away.
 __device__ __forceinline__ uint64_t turns64(float f) {
-  constexpr uint64_t kInvTwoPi = 0x28BE60DB9391054Aull;  // floor(2^64 / (2 pi))
+  constexpr uint64_t kHi = 0x28BE60DB9391054Aull, kLo = 0x7F09D5F47D4D3770ull;  // floor(2^128 / (2 pi))
   const uint32_t bits = __float_as_uint(f);
   const int ex = static_cast<int>((bits >> 23) & 255);
   const uint64_t mant = (bits & 0x7fffffu) | (ex ? 0x800000u : 0u);
   const int sh = (ex ? ex : 1) - 150;  // f = mant * 2^sh
-  const uint64_t lo = mant * kInvTwoPi, hi = __umul64hi(mant, kInvTwoPi);
+  const uint64_t low = mant * kLo, w0 = mant * kHi, w1 = w0 + __umul64hi(mant, kLo);
+  const uint64_t w2 = __umul64hi(mant, kHi) + (w1 < w0);  // mant / (2 pi) = w2 : w1 : low
   uint64_t t;
-  if (sh >= 0) t = sh < 64 ? lo << sh : 0;
-  else if (sh > -64) t = (lo >> -sh) | (hi << (64 + sh));
-  else t = sh > -128 ? hi >> (-sh - 64) : 0;
+  if (sh > 0) t = sh < 64 ? (w1 << sh) | (low >> (64 - sh)) : 0;
+  else if (sh == 0) t = w1;
+  else if (sh > -64) t = (w1 >> -sh) | (w2 << (64 + sh));
+  else t = sh > -128 ? w2 >> (-sh - 64) : 0;
   return (bits >> 31) ? 0 - t : t;
 }
 
