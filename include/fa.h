@@ -564,7 +564,7 @@ size_t fa_fwd_scored_workspace_size(int B, int Hq, int Hkv, int Sq, int Sk, int 
    ds = dz * (1 - (t / softcap)^2), dQ = scale * ds K, dK = scale * ds^T Q, dV = P^T dO.  The scores'
    arguments are the forward's; workspace holds fa_bwd_workspace_size(B, Hq, Sq, d) bytes.  Where
    fa_bwd_scored_workspace_size is more and as much is there, the queries of few keys are split over
-   the GPU: the same gradients, sooner. */
+   the GPU: the same gradients, sooner.  In ds, weights below 2^-29 count in steps of 2^-39. */
 fa_status fa_bwd_scored(const void* q, const void* k, const void* v, const void* o,
                         const void* dout, const float* lse, void* dq, void* dk, void* dv, int B,
                         int Hq, int Hkv, int Sq, int Sk, int d, int causal, float scale,
@@ -579,7 +579,7 @@ size_t fa_decode_scored_workspace_size(int B, int Hq, int Hkv, int Sk_max, int d
 /*
  * fa_decode on such scores.  The query of batch row b is position n - 1, n = seqlens_k[b] (clamped
  * to [0, Sk_max]); it sees the keys [max(0, k_start[b], n - window), n) (k_start device int32[B] or
- * NULL: 0; window 0: none).  No other key is read.  Grid and workspace depend on the arguments,
+ * NULL: 0; window 0: none).  No other key is used.  Grid and workspace depend on the arguments,
  * never on the values in seqlens_k and k_start.  A NaN reaches the batch rows that see it and no
  * others.  B * Hq must be below 2^31.
  */

@@ -333,7 +333,9 @@ __global__ void __launch_bounds__(256) fa_bwd_convert(const BwdParams p, long lo
 
 // The scored modes hold weights times 2^15 (the factor leaves with the LSE's staging, D's staging and
 // dV's epilogue, at no cost): what dS is formed of is then kept in f16, which has 11 bits for every
-// weight above 2^-29 where bf16 has 8.  dS itself is rounded to bf16 for its two products.
+// weight above 2^-29 where bf16 has 8.  Smaller ones lose bits (the step is 2^-39), and below 2^-40 they are 0
+// there, where bf16 (the plain modes) would keep them: nothing beside a row's other weights in dQ, but dK of a key to
+// which no query gives more ends at that size.  dV keeps bf16's range.  dS itself is rounded to bf16 for its two products.
 constexpr float kWeightLog2 = 15.f;
 constexpr float kWeightInv = 1.f / 32768.f;
 

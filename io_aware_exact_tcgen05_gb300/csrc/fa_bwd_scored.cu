@@ -23,6 +23,7 @@ cudaError_t launch_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUtenso
 
 }  // namespace
 
+// (304: two for each of GB300's SMs.  A constant, since sizes of workspaces depend on the arguments alone.)
 // Units that are at most two per SM are split where they are long, into 16 parts at most: 16 query
 // heads on 2 of 2048 rows 299 -> 138 us, 4 on 1 of 8192 582 -> 201, 32 on 8 of 2048 166 -> 145.  (Up
 // to one per SM: 112, 324 and not; four per SM 148, 269 and 158, and two batch rows of the last one

@@ -88,6 +88,7 @@ cudaError_t launch_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUtenso
 
 }  // namespace
 
+// (152: GB300's SMs.  A constant, since sizes of workspaces depend on the arguments alone.)
 // Units that leave half of the SMs or more without work are split, into parts that still fit the
 // SMs at once: 8 heads of 128 rows and 32768 keys 440 -> 35 us, 8 of 512 and 8192 115 -> 30.  (Up to
 // twice the SMs: 128 units of 16 tiles 36 -> 48, 16 of 64 tiles 43 us.)

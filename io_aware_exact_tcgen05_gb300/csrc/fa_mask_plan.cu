@@ -89,7 +89,7 @@ __global__ void __launch_bounds__(128)
   const int last = before ? 31 - __clz(before) : lane;
   const int pl = __shfl_sync(0xffffffffu, l, last), ph = __shfl_sync(0xffffffffu, h, last);
   const bool breaks = __any_sync(0xffffffffu, live && before && (l > ph || pl > h));
-  const bool past = __any_sync(0xffffffffu, live && h > i + Sk - Sq + 1);
+  const bool past = __any_sync(0xffffffffu, live && h > i + (Sk - Sq) + 1);
   const int mn_l = __reduce_min_sync(0xffffffffu, live ? l : 0x7fffffff);
   const int mx_h = __reduce_max_sync(0xffffffffu, live ? h : 0);
   row[threadIdx.x] = make_int2(l, h);
