@@ -522,7 +522,7 @@ fa_status fa_row_bounds(const int32_t* cu_docs, const int32_t* prefix, int n_doc
                         int32_t* row_hi, int B, int Sq, int Sk, int causal, int window,
                         cudaStream_t stream);
 
-/* Bytes of a mask plan: 8 per row, some 30 per 128 rows and 50 per 128 keys. */
+/* Bytes of a mask plan: 8 per row, some 45 per 128 rows and 60 per 128 keys. */
 size_t fa_mask_plan_size(int B, int Sq, int Sk);
 
 /* The tile plan of row_lo, row_hi int32 [B,Sq] (clamped to [0, Sk]; hi <= lo: no keys) into plan

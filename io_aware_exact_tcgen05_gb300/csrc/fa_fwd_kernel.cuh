@@ -360,39 +360,51 @@ __device__ __forceinline__ int all_seen_until(const ScoredUnit& u, const ScoredF
   const int t = u.r0 / kTileM;
   const int4* qt = p.sc.plan.qt + static_cast<size_t>(u.b) * p.sc.plan.nq + t;
   int4 r = __ldg(qt);
+  if (p.causal) r.y = min(r.y, min(u.r0 + kTileM, u.sq) + u.off);
   if (!p.pack_heads && t + 1 < p.sc.plan.nq) {
-    const int4 r1 = __ldg(qt + 1);
-    r.z |= r1.z | (r.y > 0 && r1.y > 0 && (r.y < r1.x || r1.y < r.x));
-    r.w |= r1.w;
+    int4 r1 = __ldg(qt + 1);
+    if (p.causal) r1.y = min(r1.y, min(u.r1 + kTileM, u.sq) + u.off);
+    r.z |= r1.z | (r.y > r.x && r1.y > r1.x && (r.y < r1.x || r1.y < r.x));
+    r.w = max(r.w, r1.w);
   }
   if (r.z) return 0;
-  return p.causal && r.w ? min(u.kend, u.r0 + u.off + 1) : u.kend;  // the rule hides those from no row
+  // The rule hides those up to the first row's position from no row; where all rows see their own, the hull, which
+  // ends at the last row's, holds none that it hides from all.
+  return p.causal && r.w == 2 ? min(u.kend, u.r0 + u.off + 1) : u.kend;
 }
 
 // Which keys of the tile from key c0 any row of the unit sees: lane w (and w + 4, ..) has those of keys
-// [32 w, +32).
+// [32 w, +32).  From the extremes of the unit's rows where they tell all (hull), else from those of each tile of rows and
+// its gaps, and row by row where these are many or the causal rule cuts into the tile.
 __device__ __forceinline__ uint32_t keys_seen(const ScoredUnit& u, const ScoredFwdParams& p, bool hull, int c0,
                                               int lane) {
-  if (hull) {
-    const int at = c0 + 32 * (lane & 3);
-    return bits_below(u.kend - at) & ~bits_below(u.klo - at);
-  }
-  const int2* rows = p.sc.plan.rows + static_cast<size_t>(u.b) * p.Sq;
+  const int at = c0 + 32 * (lane & 3);
+  auto span = [&](int lo, int hi) { return bits_below(hi - at) & ~bits_below(lo - at); };
+  if (hull) return span(u.klo, u.kend);
+  const MaskPlan& m = p.sc.plan;
   uint32_t mine = 0u;
+  bool rows = false;
 #pragma unroll 1
+  for (int t = u.r0 / kTileM, end = min(m.nq, t + (p.pack_heads ? 1 : 2)); t < end; ++t) {
+    const size_t i = static_cast<size_t>(u.b) * m.nq + t;
+    const int4 r = __ldg(m.qt + i), g = __ldg(m.gaps + i);
+    const int hi = p.causal ? min(r.y, min((t + 1) * kTileM, u.sq) + u.off) : r.y;
+    mine |= span(r.x, max(r.x, hi)) & ~(span(g.x, g.y) | span(g.z, g.w));
+    rows = rows || r.z == 3 || (p.causal && r.w == 2 && c0 + kTileN > t * kTileM + u.off + 1);
+  }
+  if (!rows) return mine;
+  uint32_t seen[4] = {0u, 0u, 0u, 0u};
+#pragma unroll 2
+  for (int k = 0; k < (p.pack_heads ? 4 : 8); ++k) {  // (slots of packed heads have the same rows)
+    const int i = u.r0 + 32 * k + lane;
+    const int2 r = i < u.sq ? __ldg(m.rows + static_cast<size_t>(u.b) * p.Sq + i) : make_int2(0, 0);
+    const int hi = p.causal ? min(r.y, i + u.off + 1) : r.y;
+    if (hi > r.x) add_span(seen, r.x - c0, hi - c0);
+  }
+#pragma unroll
   for (int w = 0; w < 4; ++w) {
-    const int at = c0 + 32 * w;
-    uint32_t bits = 0u;
-#pragma unroll 1
-    for (int k = 0; k < (p.pack_heads ? 4 : 8); ++k) {  // (slots of packed heads have the same rows)
-      const int i = u.r0 + 32 * k + lane;
-      if (i >= u.sq) continue;
-      const int2 r = __ldg(rows + i);
-      const int hi = p.causal ? min(r.y, i + u.off + 1) : r.y;
-      if (hi > r.x) bits |= bits_below(hi - at) & ~bits_below(r.x - at);
-    }
-    bits = __reduce_or_sync(0xffffffffu, bits);
-    if ((lane & 3) == w) mine = bits;
+    seen[w] = __reduce_or_sync(0xffffffffu, seen[w]);
+    if ((lane & 3) == w) mine = seen[w];
   }
   return mine;
 }

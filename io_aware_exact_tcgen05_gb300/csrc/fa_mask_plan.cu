@@ -70,8 +70,9 @@ __device__ __forceinline__ int key_tiles(int4 r) {
 __global__ void __launch_bounds__(128)
     fa_plan_rows_kernel(const int32_t* lo, const int32_t* hi, int Sq, int Sk, const MaskPlan m) {
   __shared__ int2 row[128];
-  __shared__ int4 red[4];       // of a warp's rows: min lo, max hi, intervals apart, past their positions
+  __shared__ int4 red[4];       // of a warp's rows: min lo, max hi, 1 intervals apart | 2 past their positions, all see their own
   __shared__ int2 ends[4][2];   // the first and the last interval of a warp's rows
+  __shared__ int part[4];
   const int b = blockIdx.y, t = blockIdx.x;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int i = t * 128 + threadIdx.x;
@@ -89,40 +90,73 @@ __global__ void __launch_bounds__(128)
   const int last = before ? 31 - __clz(before) : lane;
   const int pl = __shfl_sync(0xffffffffu, l, last), ph = __shfl_sync(0xffffffffu, h, last);
   const bool breaks = __any_sync(0xffffffffu, live && before && (l > ph || pl > h));
-  const bool past = __any_sync(0xffffffffu, live && h > i + (Sk - Sq) + 1);
+  const int p = i + (Sk - Sq);
+  const bool past = __any_sync(0xffffffffu, live && h > p + 1);
+  const bool own = __all_sync(0xffffffffu, i >= Sq || (live && l <= p && h > p));
   const int mn_l = __reduce_min_sync(0xffffffffu, live ? l : 0x7fffffff);
   const int mx_h = __reduce_max_sync(0xffffffffu, live ? h : 0);
   row[threadIdx.x] = make_int2(l, h);
   if (live && !before) ends[w][0] = make_int2(l, h);
   if (live && !(alive >> lane >> 1)) ends[w][1] = make_int2(l, h);
-  if (lane == 0) red[w] = make_int4(mn_l, mx_h, breaks, past);
+  if (lane == 0) red[w] = make_int4(mn_l, mx_h, (breaks ? 1 : 0) | (past ? 2 : 0), own);
   __syncthreads();
   int first = 0x7fffffff, end = 0, prev = -1;
-  bool apart = false, beyond = false;
+  bool apart = false, beyond = false, all_own = true;
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
     const int4 r = red[k];
+    all_own = all_own && r.w;
     if (r.y == 0) continue;
     if (prev >= 0 && (ends[k][0].x > ends[prev][1].y || ends[prev][1].x > ends[k][0].y)) apart = true;
     prev = k;
     first = min(first, r.x);
     end = max(end, r.y);
-    apart = apart || r.z;
-    beyond = beyond || r.w;
+    apart = apart || (r.z & 1);
+    beyond = beyond || (r.z & 2);
   }
-  int gaps = 0;
+  int n_gaps = 0;
+  int4 gap = make_int4(0, 0, 0, 0);
   if (apart) {  // (CTA-uniform)
-    bool bare = live && h < end;  // key h, which this row does not see, is in no row's interval
-    if (bare) {
-#pragma unroll 8
-      for (int k = 0; k < 128; ++k) bare = bare && !(row[k].x <= h && row[k].y > h);
+    // Ends of intervals that the next row neither sees nor shares are looked for in every row's; a stretch starts at one
+    // that none sees and ends at the next interval's first.
+    const int2 next = row[(threadIdx.x + 1) & 127];
+    const uint32_t ask = __ballot_sync(0xffffffffu, live && h < end && next.y != h && !(next.x <= h && next.y > h));
+    if (lane == 0) part[w] = static_cast<int>(ask);
+    __syncthreads();
+    int start[2] = {-1, -1}, covered = -1;
+    for (int k = 0; k < 4 && n_gaps < 3; ++k)
+      for (uint32_t todo = static_cast<uint32_t>(part[k]); todo && n_gaps < 3; todo &= todo - 1) {
+        const int key = row[32 * k + __ffs(todo) - 1].y;
+        if (key == start[0] || key == start[1] || key == covered) continue;
+        if (__syncthreads_or(l <= key && h > key)) {
+          covered = key;
+          continue;
+        }
+        ++n_gaps;
+        if (n_gaps == 2) start[1] = max(start[0], key);
+        start[0] = n_gaps == 1 ? key : min(start[0], key);
+      }
+    auto first_behind = [&](int key) {  // of the intervals
+      const int x = __reduce_min_sync(0xffffffffu, live && l > key ? l : 0x7fffffff);
+      __syncthreads();  // what part held has been read
+      if (lane == 0) part[w] = x;
+      __syncthreads();
+      return min(min(part[0], part[1]), min(part[2], part[3]));
+    };
+    if (n_gaps == 1 || n_gaps == 2) {
+      gap.x = start[0];
+      gap.y = first_behind(start[0]);
     }
-    gaps = __syncthreads_or(bare);
+    if (n_gaps == 2) {
+      gap.z = start[1];
+      gap.w = first_behind(start[1]);
+    }
   }
   if (threadIdx.x == 0) {
-    const int4 r = end > 0 ? make_int4(first, end, gaps ? 1 : 0, beyond ? 1 : 0) : make_int4(0, 0, 0, 0);
+    const int4 r = end > 0 ? make_int4(first, end, n_gaps, !beyond ? 0 : all_own ? 1 : 2) : make_int4(0, 0, 0, 0);
     const size_t at = static_cast<size_t>(b) * m.nq + t;
     const_cast<int4*>(m.qt)[at] = r;
+    const_cast<int4*>(m.gaps)[at] = gap;
     const_cast<int*>(m.work)[at] = key_tiles(r);
     if (at == 0) *const_cast<int4*>(m.sizes) = make_int4(m.B, Sq, Sk, kPlanMark);
   }
@@ -142,8 +176,8 @@ __device__ __forceinline__ bool gather_bits(uint32_t (&bits)[4], const uint32_t 
 
 // First and end query tile whose hull of intervals meets each key tile, and which of its keys any row sees,
 // also under the causal rule; the work of key tiles and of pairs of query tiles.  A warp per key tile.  The
-// rows of a query tile are looked at one by one only where no hull holds the whole tile and its own does not
-// tell: where keys within it are in no row's interval, or where the causal rule cuts into it.
+// rows of a query tile are looked at one by one only where no hull holds the whole tile and its own and its gaps do not
+// tell: where it has more than two, or where the causal rule cuts into it.
 __global__ void __launch_bounds__(256) fa_plan_keys_kernel(const MaskPlan m, int Sq, int Sk) {
   const int b = blockIdx.y, lane = threadIdx.x & 31;
   const int kt = blockIdx.x * 8 + (threadIdx.x >> 5);
@@ -171,7 +205,9 @@ __global__ void __launch_bounds__(256) fa_plan_keys_kernel(const MaskPlan m, int
         end = t0 + 32 * u + 1;
         const bool holds = r[u].x <= c0 && r[u].y >= c1 && !r[u].z;
         whole = whole || holds;
-        whole_causal = whole_causal || (holds && (!r[u].w || (t0 + 32 * u) * 128 + off >= c1 - 1));
+        // (the position of a row of the tile from which on the rule cuts: the first, or where rows see their own the last)
+        const int p = min((t0 + 32 * u) * 128 + (r[u].w == 1 ? 127 : 0), Sq - 1) + off;
+        whole_causal = whole_causal || (holds && (!r[u].w || p >= c1 - 1));
       }
     }
     first = __reduce_min_sync(0xffffffffu, first);
@@ -195,12 +231,24 @@ __global__ void __launch_bounds__(256) fa_plan_keys_kernel(const MaskPlan m, int
       if (r.x < c1 && r.y > c0) {
         // positions of the tile's first and last row
         const int p0 = t * 128 + off, p1 = min(t * 128 + 127, Sq - 1) + off;
-        const bool cut = r.w && p0 < c1 - 1;
-        if (!r.z) {
-          add_span(any, r.x - c0, r.y - c0);
-          if (!cut) add_span(causal, r.x - c0, r.y - c0);
+        const bool cut = r.w == 2 && p0 < c1 - 1;
+        const int to = r.w == 1 ? min(r.y, p1 + 1) : r.y;  // under the rule
+        if (r.z < 3) {
+          uint32_t in[4] = {0u, 0u, 0u, 0u}, ruled[4] = {0u, 0u, 0u, 0u}, out[4] = {0u, 0u, 0u, 0u};
+          add_span(in, r.x - c0, r.y - c0);
+          if (!cut && to > r.x) add_span(ruled, r.x - c0, to - c0);
+          if (r.z > 0) {
+            const int4 gap = m.gaps[static_cast<size_t>(b) * m.nq + t];
+            add_span(out, gap.x - c0, gap.y - c0);
+            add_span(out, gap.z - c0, gap.w - c0);
+          }
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            any[w] |= in[w] & ~out[w];
+            causal[w] |= ruled[w] & ~out[w];
+          }
         }
-        rows = r.z || (cut && p1 >= c0);
+        rows = r.z == 3 || (cut && p1 >= c0);
       }
       uint32_t look = __ballot_sync(0xffffffffu, rows);
       do {

@@ -16,9 +16,11 @@ namespace fa {
 // rows == nullptr: no plan, every key is visible.
 struct MaskPlan {
   const int4* sizes; // B, Sq, Sk, kPlanMark: what the kernels know a plan of theirs by (plan_fits)
-  const int4* qt;    // [B][nq]  per 128-row tile, over its rows with keys: min lo, max hi, whether a key
-                     //          between them is in no row's interval, whether a row's interval goes
-                     //          past its own position (0, 0, 0, 0 where no row has keys)
+  const int4* qt;    // [B][nq]  per 128-row tile, over its rows with keys: min lo, max hi, how many stretches
+                     //          of keys between them are in no row's interval (3: more than two), whether an
+                     //          interval goes past its row's position (1: and every row of the tile sees
+                     //          its own; 2: not) (0, 0, 0, 0 where no row has keys)
+  const int4* gaps;  // [B][nq]  those stretches, first and end key each, where they are one or two (0, 0: none)
   const uint4* seen; // [B][nk]  which of the 128 keys of a tile any row of the batch row sees
   const uint4* seen_causal;  // the same under the causal rule
   const int4* kt;    // [B][nk]  first and end query tile that may see the 128-key tile; 0 where every key of
@@ -38,10 +40,10 @@ constexpr int kUnseen = 0x7fffffff;
 
 constexpr int kPlanMark = 0x6d61736b;
 
-// 32-bit words of a plan: sizes, qt, seen, seen_causal, kt, rows, by_q1, by_q2, by_k, by_k_row, work.
+// 32-bit words of a plan: sizes, qt, gaps, seen, seen_causal, kt, rows, by_q1, by_q2, by_k, by_k_row, work.
 inline size_t mask_plan_words(long long B, long long Sq, long long Sk) {
   const long long nq = (Sq + 127) / 128, np = (nq + 1) / 2, nk = (Sk + 127) / 128;
-  return static_cast<size_t>(4 + B * (4 * nq + 12 * nk + 2 * Sq + 2 * (nq + np + nk) + nk));
+  return static_cast<size_t>(4 + B * (8 * nq + 12 * nk + 2 * Sq + 2 * (nq + np + nk) + nk));
 }
 
 inline MaskPlan mask_plan_view(const void* base, long long B, long long Sq, long long Sk) {
@@ -55,6 +57,8 @@ inline MaskPlan mask_plan_view(const void* base, long long B, long long Sq, long
   m.sizes = reinterpret_cast<const int4*>(w);
   w += 4;
   m.qt = reinterpret_cast<const int4*>(w);
+  w += 4 * B * m.nq;
+  m.gaps = reinterpret_cast<const int4*>(w);
   w += 4 * B * m.nq;
   m.seen = reinterpret_cast<const uint4*>(w);
   w += 4 * B * m.nk;

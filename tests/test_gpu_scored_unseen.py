@@ -48,6 +48,11 @@ MASKS = {
     "scattered_rule": lambda: (1, 300, 420, True, _scattered(1, 300, 420, 2)),
     # a gap that only the two tiles of a pair together have, in both orders
     "pairs": lambda: (1, 512, 512, False, _rows(1, 512, lambda b, i: [(0, 100), (300, 400), (410, 500), (20, 99)][i // 128])),
+    # the first tile's rows see everything, the next ones' only keys in front of their own: a gap under the rule alone
+    "pairs_rule": lambda: (1, 512, 512, True, _rows(1, 512, lambda b, i: (0, 512) if i < 128 else
+                                                   (140, 145) if i < 256 else (0, 0) if i < 400 else (300, 512))),
+    "own": lambda: (1, 500, 500, True, _rows(1, 500, lambda b, i: (i // 100 * 100, i // 100 * 100 + 90)
+                                            if i % 100 < 90 else (0, 0))),
     # few rows with long keys, many heads on few keys: split over the GPU
     "long": lambda: (1, 60, 3000, False, _rows(1, 60, lambda b, i: (700, 1900) if i % 2 else (2000, 2900))),
     "long_rule": lambda: (1, 200, 2600, True, _rows(1, 200, lambda b, i: (100, 2600) if i < 90 else (0, 0))),
