@@ -872,7 +872,7 @@ def fa_mask_plan_size(B, Sq, Sk) -> int:
 
 def fa_mask_plan(row_lo, row_hi, Sk: int, plan=None, stream=None):
     """The tile plan of row intervals (fa_mask_plan): row_lo, row_hi int32 [B,Sq].  Returns the plan,
-    a uint8 tensor of fa_mask_plan_size(B, Sq, Sk) bytes for fa_fwd_scored and fa_bwd_scored."""
+    a uint8 tensor of fa_mask_plan_size(B, Sq, Sk) bytes for fa_fwd_scored and fa_bwd_scored of these sizes."""
     lib, dev = load_library(), _device()
     B, Sq = _dims(row_lo, "row_lo", 2)
     Sk = _int(Sk, "Sk")

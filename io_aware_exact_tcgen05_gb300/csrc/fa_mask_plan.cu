@@ -70,7 +70,8 @@ __device__ __forceinline__ int key_tiles(int4 r) {
 __global__ void __launch_bounds__(128)
     fa_plan_rows_kernel(const int32_t* lo, const int32_t* hi, int Sq, int Sk, const MaskPlan m) {
   __shared__ int2 row[128];
-  __shared__ int4 red[4];       // of a warp's rows: min lo, max hi, 1 intervals apart | 2 past their positions, all see their own
+  __shared__ int4 red[4];       // of a warp's rows: min lo, max hi, 1 where intervals are apart | 2 where they
+                                // go past their rows' positions, whether all rows see their own
   __shared__ int2 ends[4][2];   // the first and the last interval of a warp's rows
   __shared__ int part[4];
   const int b = blockIdx.y, t = blockIdx.x;
